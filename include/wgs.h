@@ -70,7 +70,9 @@ extern "C" {
 /* 1: the LayerNorm family, gathers and bias + GELU in fp16 / fp32.
  * 2: adds the bfloat16 forms, the GELU backward (with and without a
  *    workspace), the attention bias-mask add and the region-label builder;
- *    the backward's workspace query covers zero rows. */
+ *    the backward's workspace query covers zero rows.
+ * Entry points added since (position bias by buckets, group norm) change no
+ * call of version 2, so the number stays. */
 #define WGS_ABI_VERSION 2
 
 typedef enum {
@@ -89,6 +91,9 @@ typedef enum {
 } wgs_status;
 
 typedef enum { WGS_F32 = 0, WGS_F16 = 1, WGS_BF16 = 2 } wgs_dtype;
+
+/* Activations of group_norm_act. */
+typedef enum { WGS_ACT_NONE = 0, WGS_ACT_SILU = 1, WGS_ACT_GELU_TANH = 2 } wgs_act;
 
 /* Index-map construction order (wgs_build_window_index). */
 #define WGS_SHIFT_THEN_PAD 0
@@ -341,6 +346,154 @@ wgs_status window_bias_mask_add(const void *scores, const void *bias, const int3
                                 cudaStream_t stream);
 
 /* ------------------------------------------------------------------ */
+/* position_bias -- a learned position bias by buckets                  */
+/* ------------------------------------------------------------------ */
+/* What window_bias_mask_add reads as its `bias` is, in training, expanded
+ * from a table of learned values: a bucket map sends every (query, key)
+ * pair p = i * n_k + j of a window to a row of the table.
+ *     bias[t,h,p] = fp(table[t, bucket[p], h])   for 0 <= bucket[p] < n_buckets
+ *     bias[t,h,p] = 0                             for bucket[p] == -1
+ * fp() rounds once, to nearest even, to `dtype`.  A bucket outside
+ * [-1, n_buckets) gives 0 and sets the device error word (wgs_check_error);
+ * nothing faults.
+ *   table   [n_types, n_buckets, heads] of table_dtype: WGS_F32, or `dtype`.
+ *   bucket  int32 [n_pairs], device memory; usually from
+ *           wgs_build_window_buckets or wgs_build_distance_buckets.
+ *   bias    [n_types, heads, n_pairs] of dtype (any wgs_dtype); must not
+ *           overlap the inputs (WGS_ERR_ALIAS).
+ * n_pairs must be below 2^31 - 4096 (else WGS_ERR_SHAPE).  Pointers need
+ * their element's alignment; with n_pairs a multiple of 8 and bucket and
+ * bias 16-byte aligned the heads of a bucket are read together (same
+ * results). */
+wgs_status position_bias(const void *table, const int32_t *bucket, void *bias, int32_t n_types,
+                         int32_t heads, int64_t n_pairs, int32_t n_buckets, wgs_dtype table_dtype,
+                         wgs_dtype dtype, cudaStream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* position_bias_bwd -- the table's gradient                            */
+/* ------------------------------------------------------------------ */
+/* The bias addition passes the gradient of its output to the logits and to
+ * the bias unchanged, so with grad the gradient of the logits
+ *     grad_table[t,b,h] = fp(sum of grad[w,h,p] over the windows w with
+ *                            win_type[w] == t and pairs p with bucket[p] == b)
+ * summed in FP32 in an order that depends on the sizes and the map alone.
+ *   grad      [n_win, heads, n_pairs] of dtype (any wgs_dtype).
+ *   plan      device copy of the bucket map's plan (wgs_build_bucket_plan),
+ *             16-byte aligned, with its n_slots.  A plan of other sizes than
+ *             the call's gives a zero gradient and sets the device error word.
+ *   win_type  int32 [n_win] in [0, n_types), or NULL for type 0.  A window
+ *             of another type adds to no gradient and sets the error word.
+ *   grad_table  [n_types, n_buckets, heads] of table_dtype (WGS_F32, or
+ *             `dtype`); every entry is written, 0 where nothing is added.
+ *   workspace at least wgs_position_bias_bwd_workspace_bytes(...) bytes,
+ *             16-byte aligned, disjoint from the tensors; its contents on
+ *             entry do not matter.  Calls that overlap on the GPU need
+ *             workspaces of their own. */
+size_t wgs_position_bias_bwd_workspace_bytes(int64_t n_win, int32_t heads, int32_t n_types,
+                                             int64_t n_pairs, int64_t n_slots);
+wgs_status position_bias_bwd(const void *grad, const int32_t *plan, const int32_t *win_type,
+                             void *grad_table, void *workspace, size_t workspace_bytes,
+                             int64_t n_win, int32_t heads, int64_t n_pairs, int32_t n_buckets,
+                             int64_t n_slots, int32_t n_types, wgs_dtype dtype,
+                             wgs_dtype table_dtype, cudaStream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* Host-side bucket maps and plans                                      */
+/* ------------------------------------------------------------------ */
+/* Buckets of a window's cell pairs, cells numbered row-major as the window
+ * index map lays them out.  Axis k contributes q_k * window[k] + k_k of
+ * window[k]^2 values when bit k of absolute_axes is set (a bias that knows
+ * where in the window the axis stands), else q_k - k_k + window[k] - 1 of
+ * 2 window[k] - 1 values; the axes combine row-major.  The count is -1, and
+ * the builder returns WGS_ERR_SHAPE, for extents below 1, an axis bit above
+ * 7, more than 46340 cells or a count above INT32_MAX.  out_len must be at
+ * least the square of the cell count.  Host memory only. */
+int64_t wgs_window_bucket_count(const int32_t window[3], int32_t absolute_axes);
+wgs_status wgs_build_window_buckets(const int32_t window[3], int32_t absolute_axes,
+                                    int32_t *out_host, int64_t out_len);
+
+/* Buckets of the signed distance d = j - (i + q_start) between key j and
+ * query i of a sequence (q_start: the first query's position; n_q = 1 for
+ * one new token).  Of the buckets of one direction (n_buckets / 2 with
+ * bidirectional = 1, else n_buckets) the first half, E, hold the distances
+ * 0 ... E - 1 themselves; a larger |d| goes to
+ *     E + floor((buckets - E) log(|d| / E) / log(max_distance / E)),
+ * at most the last (a distance within 1e-9 of a border counts as on it).
+ * With bidirectional = 1 keys behind the query use the first half of the
+ * buckets and keys ahead (d > 0) the second; with 0 keys ahead have no
+ * bucket (-1).  WGS_ERR_SHAPE for negative sizes, fewer than two buckets a
+ * direction, an odd n_buckets with bidirectional = 1, max_distance <= E, or
+ * out_len < n_q * n_k.  Host memory only. */
+wgs_status wgs_build_distance_buckets(int64_t n_q, int64_t n_k, int64_t q_start,
+                                      int32_t n_buckets, int32_t max_distance,
+                                      int32_t bidirectional, int32_t *out_host, int64_t out_len);
+
+/* The plan of a bucket map (host int32 [n_pairs], values in [-1,
+ * n_buckets)): for tiles of 4096 pairs, the pairs of each bucket.  Built once
+ * per map and copied to the device.  wgs_bucket_plan_words returns its size
+ * in int32 words and its slot count (pairs of a tile and a bucket that occurs
+ * in it), or -1 for invalid sizes or a value outside [-1, n_buckets), for
+ * which the builder returns WGS_ERR_SHAPE or WGS_ERR_INDEX.  Host memory
+ * only. */
+int64_t wgs_bucket_plan_words(const int32_t *bucket_host, int64_t n_pairs, int32_t n_buckets,
+                              int64_t *n_slots);
+wgs_status wgs_build_bucket_plan(const int32_t *bucket_host, int64_t n_pairs, int32_t n_buckets,
+                                 int32_t *plan_host, int64_t plan_words);
+
+/* ------------------------------------------------------------------ */
+/* group_norm_act -- group norm with an activation, channels last       */
+/* ------------------------------------------------------------------ */
+/* x holds n samples of `spatial` rows of `channels` values; a group is
+ * channels / groups neighbouring channels over all rows of a sample:
+ *     mean, var   over the spatial * channels / groups values (biased, FP32)
+ *     rstd = 1 / sqrt(var + eps)
+ *     y    = fp(act((x - mean) * rstd * weight[c] + bias[c]))
+ * in FP32, rounded once to `dtype`.  act: WGS_ACT_NONE, WGS_ACT_SILU
+ * (z / (1 + exp(-z))) or WGS_ACT_GELU_TANH (as bias_gelu_tanh's); any other
+ * value returns WGS_ERR_DTYPE.
+ *   x, y    [n, spatial, channels] of dtype (any wgs_dtype); y == x allowed,
+ *           other overlaps return WGS_ERR_ALIAS.
+ *   weight, bias  [channels] of param_dtype (WGS_F32, or `dtype`), both or
+ *           neither (NULL: 1 and 0).
+ *   mean, rstd  float [n, groups], written for the backward; both or neither.
+ *   workspace  at least wgs_group_norm_act_workspace_bytes(...) bytes,
+ *           16-byte aligned, disjoint from the tensors; its contents on entry
+ *           do not matter.  Calls that overlap on the GPU need their own.
+ * channels: a multiple of groups, at most 4096 (else WGS_ERR_WIDTH); n at most
+ * 65535.  n == 0 or spatial == 0 launches nothing.  The 16-byte path needs
+ * channels a multiple of 4 (f32) or 8 (16-bit types) and 16-byte aligned x
+ * and y; otherwise rows are walked element by element.  Sums run in an order that depends on
+ * the sizes alone. */
+size_t wgs_group_norm_act_workspace_bytes(int64_t n, int64_t spatial, int32_t channels,
+                                          int32_t groups);
+wgs_status group_norm_act(const void *x, const void *weight, const void *bias, void *y, float *mean,
+                          float *rstd, void *workspace, size_t workspace_bytes, int64_t n,
+                          int64_t spatial, int32_t channels, int32_t groups, float eps, wgs_act act,
+                          wgs_dtype dtype, wgs_dtype param_dtype, cudaStream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* group_norm_act_bwd -- its gradients                                  */
+/* ------------------------------------------------------------------ */
+/* With h = (x - mean) rstd, z = h weight + bias, dz = grad_y act'(z) and M()
+ * the mean over a group:
+ *     grad_x      = fp(rstd (dz weight - M(dz weight) - h M(dz weight h)))
+ *     grad_weight = fp(sum of dz h),   grad_bias = fp(sum of dz)  (all rows)
+ * in FP32, each rounded once.
+ *   grad_y, x, grad_x  as x above; grad_x may equal grad_y or x.
+ *   mean, rstd  as the forward wrote them.
+ *   grad_weight, grad_bias  [channels] of param_dtype; NULL skips either
+ *           (both must be NULL where weight and bias are).
+ *   n == 0 or spatial == 0 writes zeros to grad_weight and grad_bias. */
+size_t wgs_group_norm_act_bwd_workspace_bytes(int64_t n, int64_t spatial, int32_t channels,
+                                              int32_t groups);
+wgs_status group_norm_act_bwd(const void *grad_y, const void *x, const void *weight,
+                              const void *bias, const float *mean, const float *rstd, void *grad_x,
+                              void *grad_weight, void *grad_bias, void *workspace,
+                              size_t workspace_bytes, int64_t n, int64_t spatial, int32_t channels,
+                              int32_t groups, wgs_act act, wgs_dtype dtype, wgs_dtype param_dtype,
+                              cudaStream_t stream);
+
+/* ------------------------------------------------------------------ */
 /* Host-side window index map                                 [P1 s5] */
 /* ------------------------------------------------------------------ */
 /* The page fixes the protocol (INT32 per destination row, >= 0 source
@@ -410,8 +563,9 @@ wgs_status wgs_build_shift_regions(const int32_t grid[3], const int32_t window[3
  * `stream`.  Returns WGS_ERR_INDEX if any gather since the last check met
  * an index outside [-1, n_src), any window reverse an inverse index outside
  * [0, n_windowed), or any window_bias_mask_add a window type outside
- * [0, n_types); WGS_OK otherwise.  The words are shared by every stream of
- * the device. */
+ * [0, n_types), or a position-bias call a bucket, window type or plan out of
+ * its range; WGS_OK otherwise.  The words are shared by every stream of the
+ * device. */
 wgs_status wgs_check_error(cudaStream_t stream);
 
 #ifdef __cplusplus

@@ -1,6 +1,7 @@
 """CPU oracle for the block-glue path (LN, residual add + LN, window index
 map, window gather, norm-gather, bias + tanh-GELU and its backward, the
-shifted-window attention bias-mask add).
+shifted-window attention bias-mask add, the learned position bias by buckets
+and group norm with an activation, each with its backward).
 
 TEST INFRASTRUCTURE ONLY.  Only the test suite, the smoke check and the
 benchmark's CPU-baseline leg import this package; the library in
@@ -59,6 +60,14 @@ def _load():
             "orc_bias_gelu_bwd": (None, [P, P, P, P, P, P, P, i64, i32, ctypes.c_int]),
             "orc_bias_gelu_f16": (None, [P, P, P, P, i64, i32]),
             "orc_build_shift_regions": (ctypes.c_int, [P, P, P, P, i32, i32, P]),
+            "orc_build_window_buckets": (None, [P, i32, P]),
+            "orc_distance_bucket": (i32, [i64, i32, i32, i32]),
+            "orc_position_bias": (i64, [P, P, P, i32, i32, i64, i32, ctypes.c_int, ctypes.c_int]),
+            "orc_position_bias_bwd": (None, [P, P, P, P, P, i64, i32, i64, i32, i32, ctypes.c_int]),
+            "orc_group_norm_act": (None, [P, P, P, P, P, P, i64, i64, i32, i32, ctypes.c_double,
+                                          ctypes.c_int, ctypes.c_int]),
+            "orc_group_norm_act_bwd": (None, [P] * 12 + [i64, i64, i32, i32, ctypes.c_int,
+                                                         ctypes.c_int]),
             "orc_window_bias_mask_add_fmt": (None, [P, P, P, P, P, i64, i32, i32, ctypes.c_double,
                                                     ctypes.c_int]),
         }
@@ -333,3 +342,83 @@ def window_bias_mask_add(scores, bias, win_type=None, region=None, mask_value: f
     _load().orc_window_bias_mask_add_fmt(_ptr(s), _ptr(b), _ptr(t), _ptr(r), _ptr(out), n_win,
                                          heads, n, float(mask_value), code)
     return out
+
+
+# -------------------------------------------------------- position bias ----
+
+_ANY = {"f32": (-1, np.float32), "f16": (0, np.float16), "bf16": (1, np.uint16)}
+
+
+def build_window_buckets(window, absolute_axes: int = 0):
+    """int32 [n, n] bucket of every cell pair of a window."""
+    w = _i3(window)
+    n = int(np.prod(w))
+    out = np.empty((n, n), dtype=np.int32)
+    _load().orc_build_window_buckets(_ptr(w), absolute_axes, _ptr(out))
+    return out
+
+
+def build_distance_buckets(n_q, n_k, n_buckets, max_distance, both=True, q_start=0):
+    """int32 [n_q, n_k] bucket of every key's distance from its query."""
+    lib = _load()
+    one = {d: lib.orc_distance_bucket(d, n_buckets, max_distance, int(both))
+           for d in range(-(n_q - 1 + q_start), n_k - q_start)}
+    return np.array([[one[j - i - q_start] for j in range(n_k)] for i in range(n_q)],
+                    dtype=np.int32).reshape(n_q, n_k)
+
+
+def position_bias(table, bucket, table_fmt: str, fmt: str):
+    """(bias [n_types, heads, n_q, n_k] in fmt, pairs with a bucket out of
+    range) of a table [n_types, n_buckets, heads]; bfloat16 as uint16 bits."""
+    (tc, tt), (code, dt) = _ANY[table_fmt], _ANY[fmt]
+    t, b = _c(table, tt), _c(bucket, np.int32)
+    n_types, n_buckets, heads = t.shape
+    out = np.empty((n_types, heads) + b.shape, dtype=dt)
+    bad = _load().orc_position_bias(_ptr(t), _ptr(b), _ptr(out), n_types, heads, b.size, n_buckets,
+                                    tc, code)
+    return out, bad
+
+
+def position_bias_bwd(grad, bucket, win_type, n_types, n_buckets, fmt: str):
+    """(grad_table, sums of magnitudes), float64 [n_types, n_buckets, heads]."""
+    code, dt = _ANY[fmt]
+    g, b = _c(grad, dt), _c(bucket, np.int32)
+    n_win, heads = g.shape[:2]
+    t = None if win_type is None else _c(win_type, np.int32)
+    out = np.empty((n_types, n_buckets, heads))
+    mag = np.empty_like(out)
+    _load().orc_position_bias_bwd(_ptr(g), _ptr(b), _ptr(t), _ptr(out), _ptr(mag), n_win, heads,
+                                  b.size, n_buckets, n_types, code)
+    return out, mag
+
+
+# ----------------------------------------------------------- group norm ----
+
+ACTS = {None: 0, "none": 0, "silu": 1, "gelu_tanh": 2}
+
+
+def group_norm_act(x, groups, weight, bias, eps, act, fmt: str):
+    """(y, mean, rstd) in float64, x [n, spatial, channels] in fmt."""
+    code, dt = _ANY[fmt]
+    xs, w, b = _c(x, dt), _c(weight, np.float64), _c(bias, np.float64)
+    n, spatial, channels = xs.shape
+    y = np.empty(xs.shape)
+    mean, rstd = np.empty((n, groups)), np.empty((n, groups))
+    _load().orc_group_norm_act(_ptr(xs), _ptr(w), _ptr(b), _ptr(y), _ptr(mean), _ptr(rstd), n,
+                               spatial, channels, groups, float(eps), ACTS[act], code)
+    return y, mean, rstd
+
+
+def group_norm_act_bwd(grad_y, x, groups, weight, bias, mean, rstd, act, fmt: str):
+    """((grad_x, grad_weight, grad_bias), their sums of magnitudes), float64."""
+    code, dt = _ANY[fmt]
+    gy, xs = _c(grad_y, dt), _c(x, dt)
+    w, b = _c(weight, np.float64), _c(bias, np.float64)
+    m, r = _c(mean, np.float64), _c(rstd, np.float64)
+    n, spatial, channels = xs.shape
+    gx, gxm = np.empty(xs.shape), np.empty(xs.shape)
+    gw, gb, gwm, gbm = (np.empty(channels) for _ in range(4))
+    _load().orc_group_norm_act_bwd(_ptr(gy), _ptr(xs), _ptr(w), _ptr(b), _ptr(m), _ptr(r), _ptr(gx),
+                                   _ptr(gw), _ptr(gb), _ptr(gxm), _ptr(gwm), _ptr(gbm), n, spatial,
+                                   channels, groups, ACTS[act], code)
+    return (gx, gw, gb), (gxm, gwm, gbm)

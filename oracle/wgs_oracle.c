@@ -689,3 +689,176 @@ void orc_window_bias_mask_add_fmt(const uint16_t *scores, const uint16_t *bias,
                 }
     }
 }
+
+/* ------------------------------------------------------------------ */
+/* Learned position bias by buckets                                    */
+/* ------------------------------------------------------------------ */
+/* Bucket of cells i, j of a window: a mixed-radix number whose digit along
+ * axis k is the pair of positions (absolute axes) or their difference.
+ * Walks the digits from the last axis up, with a running radix. */
+void orc_build_window_buckets(const int32_t win[3], int32_t absolute_axes, int32_t *out)
+{
+    int64_t n = (int64_t)win[0] * win[1] * win[2];
+    for (int64_t i = 0; i < n; ++i)
+        for (int64_t j = 0; j < n; ++j) {
+            int64_t a = i, b = j, radix = 1, value = 0;
+            for (int k = 2; k >= 0; --k) {
+                int64_t p = a % win[k], q = b % win[k];
+                a /= win[k];
+                b /= win[k];
+                if (absolute_axes & (1 << k)) {
+                    value += radix * (p * win[k] + q);
+                    radix *= (int64_t)win[k] * win[k];
+                } else {
+                    value += radix * (p - q + (win[k] - 1));
+                    radix *= 2 * win[k] - 1;
+                }
+            }
+            out[i * n + j] = (int32_t)value;
+        }
+}
+
+/* Bucket of the signed distance d between a key and its query: single
+ * distances below E, then the range whose lower border E (max / E)^(k / m),
+ * k = 0 ... m - 1, is the last at or below |d| (borders compared in
+ * logarithms, with the stated 1e-9 of a range). */
+int32_t orc_distance_bucket(int64_t d, int32_t n_buckets, int32_t max_distance, int32_t both)
+{
+    int32_t side = both ? n_buckets / 2 : n_buckets, first = 0;
+    if (d > 0) {
+        if (!both) return -1;
+        first = side;
+    }
+    int64_t away = d < 0 ? -d : d;
+    int32_t e = side / 2, m = side - e, k = 0;
+    if (away < e) return first + (int32_t)away;
+    double x = m * (log((double)away / e) / log((double)max_distance / e));
+    while (k + 1 < m && x >= (double)(k + 1) - 1e-9) ++k;
+    return first + e + k;
+}
+
+/* out[t,h,p] = round(table[t, bucket[p], h]), 0 without a bucket.  Returns
+ * the number of pairs whose bucket lies outside [-1, n_buckets). */
+int64_t orc_position_bias(const void *table, const int32_t *bucket, void *out, int32_t n_types,
+                          int32_t heads, int64_t n_pairs, int32_t n_buckets, int table_fmt, int fmt)
+{
+    int64_t bad = 0;
+    for (int32_t t = 0; t < n_types; ++t)
+        for (int32_t h = 0; h < heads; ++h)
+            for (int64_t p = 0; p < n_pairs; ++p) {
+                double v = 0.0;
+                int32_t b = bucket[p];
+                if (b >= 0 && b < n_buckets)
+                    v = dec_any(table, ((int64_t)t * n_buckets + b) * heads + h, table_fmt);
+                enc_any(out, ((int64_t)t * heads + h) * n_pairs + p, v, fmt);
+            }
+    for (int64_t p = 0; p < n_pairs; ++p) bad += bucket[p] < -1 || bucket[p] >= n_buckets;
+    return bad;
+}
+
+/* grad_table[t,b,h] = sum of grad[w,h,p], type[w] == t and bucket[p] == b;
+ * mag receives the sum of magnitudes. */
+void orc_position_bias_bwd(const void *grad, const int32_t *bucket, const int32_t *win_type,
+                           double *out, double *mag, int64_t n_win, int32_t heads, int64_t n_pairs,
+                           int32_t n_buckets, int32_t n_types, int fmt)
+{
+    int64_t total = (int64_t)n_types * n_buckets * heads;
+    for (int64_t i = 0; i < total; ++i) out[i] = mag[i] = 0.0;
+    for (int64_t w = 0; w < n_win; ++w) {
+        int32_t t = win_type ? win_type[w] : 0;
+        if (t < 0 || t >= n_types) continue;
+        for (int32_t h = 0; h < heads; ++h)
+            for (int64_t p = 0; p < n_pairs; ++p) {
+                if (bucket[p] < 0 || bucket[p] >= n_buckets) continue;
+                double g = dec_any(grad, (w * heads + h) * n_pairs + p, fmt);
+                int64_t i = ((int64_t)t * n_buckets + bucket[p]) * heads + h;
+                out[i] += g;
+                mag[i] += fabs(g);
+            }
+    }
+}
+
+/* ------------------------------------------------------------------ */
+/* Group norm with an activation, channels last                        */
+/* ------------------------------------------------------------------ */
+/* act: 0 none, 1 SiLU z sigma(z), 2 tanh-GELU. */
+static double act_value(double z, int act)
+{
+    return act == 1 ? z * sigmoid_exact(z) : act == 2 ? gelu_tanh(z) : z;
+}
+
+static double act_slope(double z, int act)
+{
+    if (act == 1) return sigmoid_exact(z) + z * sigmoid_exact(z) * sigmoid_exact(-z);
+    return act == 2 ? gelu_tanh_grad(z) : 1.0;
+}
+
+/* weight and bias as doubles; x in fmt.  y, mean and rstd unrounded. */
+void orc_group_norm_act(const void *x, const double *weight, const double *bias, double *y,
+                        double *mean, double *rstd, int64_t n, int64_t spatial, int32_t channels,
+                        int32_t groups, double eps, int act, int fmt)
+{
+    int32_t per = channels / groups;
+    double m = (double)spatial * per;
+    for (int64_t i = 0; i < n; ++i)
+        for (int32_t g = 0; g < groups; ++g) {
+            double s = 0.0, q = 0.0;
+            for (int64_t r = 0; r < spatial; ++r)
+                for (int32_t c = g * per; c < (g + 1) * per; ++c)
+                    s += dec_any(x, (i * spatial + r) * channels + c, fmt);
+            double mu = s / m;
+            for (int64_t r = 0; r < spatial; ++r)
+                for (int32_t c = g * per; c < (g + 1) * per; ++c) {
+                    double d = dec_any(x, (i * spatial + r) * channels + c, fmt) - mu;
+                    q += d * d;
+                }
+            double rs = 1.0 / sqrt(q / m + eps);
+            mean[i * groups + g] = mu;
+            rstd[i * groups + g] = rs;
+            for (int64_t r = 0; r < spatial; ++r)
+                for (int32_t c = g * per; c < (g + 1) * per; ++c) {
+                    int64_t at = (i * spatial + r) * channels + c;
+                    y[at] = act_value((dec_any(x, at, fmt) - mu) * rs * weight[c] + bias[c], act);
+                }
+        }
+}
+
+/* Gradients with the given statistics.  gw_mag and gb_mag receive the sums
+ * of magnitudes; gx_mag, per element, the size of the terms that grad_x is
+ * the difference of. */
+void orc_group_norm_act_bwd(const void *grad_y, const void *x, const double *weight,
+                            const double *bias, const double *mean, const double *rstd, double *gx,
+                            double *gw, double *gb, double *gx_mag, double *gw_mag, double *gb_mag,
+                            int64_t n, int64_t spatial, int32_t channels, int32_t groups, int act,
+                            int fmt)
+{
+    int32_t per = channels / groups;
+    double m = (double)spatial * per;
+    for (int32_t c = 0; c < channels; ++c) gw[c] = gb[c] = gw_mag[c] = gb_mag[c] = 0.0;
+    for (int64_t i = 0; i < n; ++i)
+        for (int32_t g = 0; g < groups; ++g) {
+            double mu = mean[i * groups + g], rs = rstd[i * groups + g];
+            double m1 = 0.0, m2 = 0.0, a1 = 0.0, a2 = 0.0;
+            for (int pass = 0; pass < 2; ++pass)
+                for (int64_t r = 0; r < spatial; ++r)
+                    for (int32_t c = g * per; c < (g + 1) * per; ++c) {
+                        int64_t at = (i * spatial + r) * channels + c;
+                        double h = (dec_any(x, at, fmt) - mu) * rs;
+                        double gy = dec_any(grad_y, at, fmt);
+                        double dz = gy * act_slope(h * weight[c] + bias[c], act);
+                        if (pass == 0) {
+                            gb[c] += dz;
+                            gw[c] += dz * h;
+                            gb_mag[c] += fabs(gy);
+                            gw_mag[c] += fabs(gy * h);
+                            m1 += dz * weight[c] / m;
+                            m2 += dz * weight[c] * h / m;
+                            a1 += fabs(gy * weight[c]) / m;
+                            a2 += fabs(gy * weight[c] * h) / m;
+                        } else {
+                            gx[at] = rs * (dz * weight[c] - m1 - h * m2);
+                            gx_mag[at] = rs * (fabs(gy * weight[c]) + a1 + fabs(h) * a2);
+                        }
+                    }
+        }
+}

@@ -17,6 +17,7 @@ STATUS_NAMES = {
     8: "WGS_ERR_INDEX", 9: "WGS_ERR_ALIAS", 10: "WGS_ERR_CUDA", 11: "WGS_ERR_TOO_LARGE",
 }
 WGS_F32, WGS_F16, WGS_BF16 = 0, 1, 2
+WGS_ACT_NONE, WGS_ACT_SILU, WGS_ACT_GELU_TANH = 0, 1, 2
 ABI_VERSION = 2  # WGS_ABI_VERSION of include/wgs.h that these signatures describe
 
 _P = ctypes.c_void_p
@@ -47,6 +48,21 @@ SIGNATURES = {
     "wgs_build_window_index": (_st, [_P, _P, _P, _P, _i32, _P, _i64]),
     "window_bias_mask_add": (_st, [_P, _P, _P, _P, _P, _i64, _i32, _i32, _i32, _f32, _i32, _P]),
     "wgs_build_shift_regions": (_st, [_P, _P, _P, _P, _i32, _i32, _P, _i64]),
+    "position_bias": (_st, [_P, _P, _P, _i32, _i32, _i64, _i32, _i32, _i32, _P]),
+    "wgs_position_bias_bwd_workspace_bytes": (ctypes.c_size_t, [_i64, _i32, _i32, _i64, _i64]),
+    "position_bias_bwd": (_st, [_P, _P, _P, _P, _P, ctypes.c_size_t, _i64, _i32, _i64, _i32, _i64,
+                                _i32, _i32, _i32, _P]),
+    "wgs_window_bucket_count": (_i64, [_P, _i32]),
+    "wgs_build_window_buckets": (_st, [_P, _i32, _P, _i64]),
+    "wgs_build_distance_buckets": (_st, [_i64, _i64, _i64, _i32, _i32, _i32, _P, _i64]),
+    "wgs_bucket_plan_words": (_i64, [_P, _i64, _i32, _P]),
+    "wgs_build_bucket_plan": (_st, [_P, _i64, _i32, _P, _i64]),
+    "wgs_group_norm_act_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i32, _i32]),
+    "group_norm_act": (_st, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _i64, _i64, _i32, _i32,
+                             _f32, _i32, _i32, _i32, _P]),
+    "wgs_group_norm_act_bwd_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i32, _i32]),
+    "group_norm_act_bwd": (_st, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _i64,
+                                 _i64, _i32, _i32, _i32, _i32, _i32, _P]),
     "wgs_check_error": (_st, [_P]),
 }
 

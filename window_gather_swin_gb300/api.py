@@ -9,6 +9,7 @@ CPU tensors are rejected.
 from __future__ import annotations
 
 import ctypes
+from dataclasses import dataclass
 from typing import Optional, Sequence
 
 import torch
@@ -295,6 +296,249 @@ def window_bias_mask_add(scores: torch.Tensor, bias: torch.Tensor,
     return y
 
 
+# ------------------------------------------------------- position bias ----
+
+def window_bucket_count(window: Sequence[int], absolute_axes: int = 0) -> int:
+    """Buckets of build_window_buckets: the rows of the learned table."""
+    n = _capi.load().wgs_window_bucket_count(_i3(window, "window"), int(absolute_axes))
+    _require(n >= 0, "invalid window extents or absolute_axes")
+    return int(n)
+
+
+def build_window_buckets(window: Sequence[int], absolute_axes: int = 0,
+                         device=None) -> torch.Tensor:
+    """int32 [n, n] bucket map of a window's n cells (host-built); on `device`
+    if given.  Axes whose bit is set in absolute_axes keep both positions, the
+    others their difference."""
+    window_bucket_count(window, absolute_axes)
+    n = int(window[0]) * int(window[1]) * int(window[2])
+    out = torch.empty(n, n, dtype=torch.int32)
+    _capi.check("wgs_build_window_buckets", _capi.load().wgs_build_window_buckets(
+        _i3(window, "window"), int(absolute_axes), ctypes.c_void_p(out.data_ptr()), n * n))
+    return out if device is None else out.to(device)
+
+
+def build_distance_buckets(n_q: int, n_k: int, n_buckets: int, max_distance: int,
+                           bidirectional: bool = True, q_start: int = 0,
+                           device=None) -> torch.Tensor:
+    """int32 [n_q, n_k] bucket map of a sequence: single distances, then
+    logarithmic ranges up to max_distance (host-built); on `device` if given.
+    Query i stands at position q_start + i; without `bidirectional` keys ahead
+    of their query have no bucket (-1)."""
+    _require(n_q >= 0 and n_k >= 0, "n_q and n_k must not be negative")
+    out = torch.empty(n_q, n_k, dtype=torch.int32)
+    _capi.check("wgs_build_distance_buckets", _capi.load().wgs_build_distance_buckets(
+        n_q, n_k, int(q_start), int(n_buckets), int(max_distance), int(bool(bidirectional)),
+        ctypes.c_void_p(out.data_ptr()), n_q * n_k))
+    return out if device is None else out.to(device)
+
+
+def position_bias(table: torch.Tensor, bucket: torch.Tensor, dtype=None,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """bias[t, h, i, j] = table[t, bucket[i, j], h] (0 for bucket -1): table
+    [n_types, n_buckets, heads] (or [n_buckets, heads]: one type), bucket
+    int32 [n_q, n_k].  `dtype` is the bias's format, by default out's or the
+    table's; the table is float32 or of that format."""
+    _cuda(table, "table")
+    _cuda(bucket, "bucket", torch.int32)
+    _require(table.dim() in (2, 3), "table must be [n_types, n_buckets, heads] or [n_buckets, heads]")
+    _require(bucket.dim() == 2, "bucket must be [n_q, n_k]")
+    n_types = table.shape[0] if table.dim() == 3 else 1
+    n_buckets, heads = table.shape[-2:]
+    if dtype is None:
+        dtype = table.dtype if out is None else out.dtype
+    _require(dtype in _DTYPE, f"dtype must be float32, float16 or bfloat16 (got {dtype})")
+    _require(table.dtype in (torch.float32, dtype),
+             f"table must be float32 or {dtype} (got {table.dtype})")
+    y = _out(out, (n_types, heads) + tuple(bucket.shape), dtype, table.device, "out")
+    _same_device(table, bucket, y)
+    _call("position_bias", _capi.load().position_bias, table.device, _ptr(table), _ptr(bucket),
+          _ptr(y), n_types, heads, bucket.numel(), n_buckets, _DTYPE[table.dtype], _DTYPE[dtype])
+    return y
+
+
+@dataclass(frozen=True)
+class BucketPlan:
+    """A bucket map's inverse on a device (build_bucket_plan)."""
+    words: torch.Tensor      # int32, the C ABI's plan
+    shape: tuple             # (n_q, n_k) of the map
+    n_buckets: int
+    n_slots: int
+
+    @property
+    def n_pairs(self) -> int:
+        return self.shape[0] * self.shape[1]
+
+
+def build_bucket_plan(bucket: torch.Tensor, n_buckets: int, device="cuda") -> BucketPlan:
+    """The plan that position_bias_bwd reads, from a bucket map int32
+    [n_q, n_k] with values in [-1, n_buckets) (host-built, once per map)."""
+    _require(isinstance(bucket, torch.Tensor) and bucket.dtype == torch.int32 and bucket.dim() == 2,
+             "bucket must be an int32 tensor [n_q, n_k]")
+    host = bucket.cpu().contiguous()
+    lib = _capi.load()
+    slots = ctypes.c_int64()
+    n = lib.wgs_bucket_plan_words(ctypes.c_void_p(host.data_ptr()), host.numel(), int(n_buckets),
+                                  ctypes.byref(slots))
+    _require(n >= 0, f"bucket values must lie in [-1, {n_buckets}) and n_buckets be positive")
+    words = torch.empty(n, dtype=torch.int32)
+    _capi.check("wgs_build_bucket_plan", lib.wgs_build_bucket_plan(
+        ctypes.c_void_p(host.data_ptr()), host.numel(), int(n_buckets),
+        ctypes.c_void_p(words.data_ptr()), n))
+    return BucketPlan(words.to(device), tuple(host.shape), int(n_buckets), int(slots.value))
+
+
+def position_bias_bwd_workspace_bytes(plan: BucketPlan, n_win: int, heads: int,
+                                      n_types: int = 1) -> int:
+    """Bytes of workspace position_bias_bwd needs."""
+    return int(_capi.load().wgs_position_bias_bwd_workspace_bytes(
+        int(n_win), int(heads), int(n_types), plan.n_pairs, plan.n_slots))
+
+
+def position_bias_bwd(grad: torch.Tensor, plan: BucketPlan,
+                      win_type: Optional[torch.Tensor] = None, n_types: int = 1,
+                      dtype=torch.float32, grad_table: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of position_bias's table, [n_types, n_buckets, heads], from
+    the gradient of the logits grad [n_win, heads, n_q, n_k]; win_type int32
+    [n_win] (None: type 0).  `dtype`, the gradient's format, is float32 or
+    grad's.  The fixed-order sums need a workspace of
+    position_bias_bwd_workspace_bytes(...) bytes; one is allocated here unless
+    the caller passes a uint8 CUDA tensor that large."""
+    _cuda(grad, "grad")
+    _require(grad.dtype in _DTYPE, f"grad must be float32, float16 or bfloat16 (got {grad.dtype})")
+    _require(isinstance(plan, BucketPlan), "plan must come from build_bucket_plan")
+    _cuda(plan.words, "plan", torch.int32)
+    _require(grad.dim() == 4 and tuple(grad.shape[2:]) == plan.shape,
+             f"grad must be [n_win, heads, {plan.shape[0]}, {plan.shape[1]}] (got {tuple(grad.shape)})")
+    n_win, heads = grad.shape[:2]
+    _require(int(n_types) >= 0, "n_types must not be negative")
+    _require(dtype in (torch.float32, grad.dtype), f"dtype must be float32 or {grad.dtype} (got {dtype})")
+    ts = [grad, plan.words]
+    if win_type is not None:
+        _cuda(win_type, "win_type", torch.int32)
+        _require(win_type.numel() == n_win, f"win_type must have {n_win} entries")
+        ts.append(win_type)
+    gt = _out(grad_table, (int(n_types), plan.n_buckets, heads), dtype, grad.device, "grad_table")
+    lib = _capi.load()
+    if workspace is None:
+        need = position_bias_bwd_workspace_bytes(plan, n_win, heads, n_types)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=grad.device)
+    _cuda(workspace, "workspace", torch.uint8)
+    _same_device(*ts, gt, workspace)
+    _call("position_bias_bwd", lib.position_bias_bwd, grad.device, _ptr(grad), _ptr(plan.words),
+          _ptr(win_type), _ptr(gt), _ptr(workspace), workspace.numel(), n_win, heads, plan.n_pairs,
+          plan.n_buckets, plan.n_slots, int(n_types), _DTYPE[grad.dtype], _DTYPE[dtype])
+    return gt
+
+
+# ---------------------------------------------------------- group norm ----
+
+_ACT = {None: _capi.WGS_ACT_NONE, "none": _capi.WGS_ACT_NONE, "silu": _capi.WGS_ACT_SILU,
+        "gelu_tanh": _capi.WGS_ACT_GELU_TANH}
+
+
+def _norm_args(x, groups, weight, bias, act):
+    """(n, spatial, channels, param dtype) of checked group-norm arguments."""
+    _cuda(x, "x")
+    _require(x.dtype in _DTYPE, f"x must be float32, float16 or bfloat16 (got {x.dtype})")
+    _require(x.dim() >= 2, "x must be [n, ..., channels]")
+    _require(act in _ACT, f"act must be one of {sorted(k for k in _ACT if k)} or None (got {act!r})")
+    n, channels = x.shape[0], x.shape[-1]
+    _require(channels > 0 and int(groups) > 0 and channels % int(groups) == 0,
+             f"channels ({channels}) must be a multiple of groups ({groups})")
+    spatial = 1
+    for d in x.shape[1:-1]:
+        spatial *= d
+    _require((weight is None) == (bias is None), "weight and bias go together")
+    pt = torch.float32
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _cuda(t, name)
+            _require(t.dtype in (torch.float32, x.dtype),
+                     f"{name} must be float32 or {x.dtype} (got {t.dtype})")
+            _require(tuple(t.shape) == (channels,), f"{name} must have {channels} elements")
+            pt = t.dtype
+    _require(weight is None or weight.dtype == bias.dtype, "weight and bias must have one dtype")
+    return n, spatial, channels, pt
+
+
+def group_norm_act_workspace_bytes(n: int, spatial: int, channels: int, groups: int) -> int:
+    """Bytes of workspace group_norm_act needs for [n, spatial, channels]."""
+    return int(_capi.load().wgs_group_norm_act_workspace_bytes(int(n), int(spatial), int(channels),
+                                                               int(groups)))
+
+
+def group_norm_act_bwd_workspace_bytes(n: int, spatial: int, channels: int, groups: int) -> int:
+    """Bytes of workspace group_norm_act_bwd needs for [n, spatial, channels]."""
+    return int(_capi.load().wgs_group_norm_act_bwd_workspace_bytes(int(n), int(spatial),
+                                                                   int(channels), int(groups)))
+
+
+def group_norm_act(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
+                   bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                   act: Optional[str] = "silu", out: Optional[torch.Tensor] = None,
+                   mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None):
+    """Group norm over channels-last x [n, ..., channels] with weight and bias
+    [channels] and an activation (None, "silu" or "gelu_tanh").  Returns
+    (y, mean, rstd); mean and rstd, float32 [n, groups], are what
+    group_norm_act_bwd takes (they are left as they are when x is empty).
+    A workspace of group_norm_act_workspace_bytes(...) bytes is allocated here
+    unless the caller passes a uint8 CUDA tensor that large."""
+    n, spatial, channels, pt = _norm_args(x, groups, weight, bias, act)
+    y = _out(out, x.shape, x.dtype, x.device, "out")
+    m = _out(mean, (n, groups), torch.float32, x.device, "mean")
+    r = _out(rstd, (n, groups), torch.float32, x.device, "rstd")
+    lib = _capi.load()
+    if workspace is None:
+        need = group_norm_act_workspace_bytes(n, spatial, channels, groups)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+    _cuda(workspace, "workspace", torch.uint8)
+    _same_device(x, *(t for t in (weight, bias) if t is not None), y, m, r, workspace)
+    _call("group_norm_act", lib.group_norm_act, x.device, _ptr(x), _ptr(weight), _ptr(bias),
+          _ptr(y), _ptr(m), _ptr(r), _ptr(workspace), workspace.numel(), n, spatial, channels,
+          int(groups), float(eps), _ACT[act], _DTYPE[x.dtype], _DTYPE[pt])
+    return y, m, r
+
+
+def group_norm_act_bwd(grad_y: torch.Tensor, x: torch.Tensor, groups: int, mean: torch.Tensor,
+                       rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                       bias: Optional[torch.Tensor] = None, act: Optional[str] = "silu",
+                       grad_x: Optional[torch.Tensor] = None,
+                       grad_weight: Optional[torch.Tensor] = None,
+                       grad_bias: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None):
+    """Gradients of group_norm_act.  Returns (grad_x, grad_weight, grad_bias),
+    the last two None without weight and bias.  grad_x may be grad_y or x."""
+    n, spatial, channels, pt = _norm_args(x, groups, weight, bias, act)
+    _cuda(grad_y, "grad_y", x.dtype)
+    _require(grad_y.shape == x.shape, "grad_y and x must have the same shape")
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _cuda(t, name, torch.float32)
+        _require(tuple(t.shape) == (n, groups), f"{name} must have shape {(n, groups)}")
+    gx = _out(grad_x, x.shape, x.dtype, x.device, "grad_x")
+    gw = gb = None
+    if weight is not None:
+        gw = _out(grad_weight, weight.shape, pt, x.device, "grad_weight")
+        gb = _out(grad_bias, bias.shape, pt, x.device, "grad_bias")
+    else:
+        _require(grad_weight is None and grad_bias is None,
+                 "grad_weight and grad_bias need weight and bias")
+    lib = _capi.load()
+    if workspace is None:
+        need = group_norm_act_bwd_workspace_bytes(n, spatial, channels, groups)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+    _cuda(workspace, "workspace", torch.uint8)
+    _same_device(x, grad_y, mean, rstd, *(t for t in (weight, bias, gw, gb) if t is not None), gx,
+                 workspace)
+    _call("group_norm_act_bwd", lib.group_norm_act_bwd, x.device, _ptr(grad_y), _ptr(x),
+          _ptr(weight), _ptr(bias), _ptr(mean), _ptr(rstd), _ptr(gx), _ptr(gw), _ptr(gb),
+          _ptr(workspace), workspace.numel(), n, spatial, channels, int(groups), _ACT[act],
+          _DTYPE[x.dtype], _DTYPE[pt])
+    return gx, gw, gb
+
+
 # ----------------------------------------------------------- index map ----
 
 SHIFT_THEN_PAD, PAD_THEN_SHIFT = 0, 1
@@ -358,8 +602,8 @@ def build_shift_regions(grid: Sequence[int], window: Sequence[int], shift: Seque
 
 def check_error(device=None) -> None:
     """Raise if any gather on `device` met an index outside [-1, n_src), or
-    any bias-mask add a window type outside [0, n_types), since the last
-    check.  Synchronises that device's current stream."""
+    any bias-mask add a window type outside [0, n_types), or any position-bias
+    call a bucket, window type or plan out of its range, since the last check.  Synchronises that device's current stream."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(dev):
         _capi.check("wgs_check_error", _capi.load().wgs_check_error(_stream_ptr(dev)))

@@ -586,7 +586,7 @@ extern "C" wgs_status residual_add_norm_gather_bf16(const void *residual, const 
 extern "C" wgs_status wgs_check_error(cudaStream_t stream) {
     // The error words are read and cleared by symbol, so each copy resolves
     // the word in the context current at this call.
-    unsigned int seen = 0, seen_mask = 0;
+    unsigned int seen = 0, seen_mask = 0, seen_bucket = 0;
     static const unsigned int cleared = 0;
     if (cudaMemcpyFromSymbolAsync(&seen, g_index_error, sizeof(seen), 0, cudaMemcpyDeviceToHost,
                                   stream) != cudaSuccess ||
@@ -595,10 +595,12 @@ extern "C" wgs_status wgs_check_error(cudaStream_t stream) {
         cudaGetLastError();  // clear this thread's error
         return WGS_ERR_CUDA;
     }
-    if (bias_mask_error_take(&seen_mask, stream) != WGS_OK) return WGS_ERR_CUDA;
+    if (bias_mask_error_take(&seen_mask, stream) != WGS_OK ||
+        position_bias_error_take(&seen_bucket, stream) != WGS_OK)
+        return WGS_ERR_CUDA;
     if (cudaStreamSynchronize(stream) != cudaSuccess) {
         cudaGetLastError();
         return WGS_ERR_CUDA;
     }
-    return (seen | seen_mask) ? WGS_ERR_INDEX : WGS_OK;
+    return (seen | seen_mask | seen_bucket) ? WGS_ERR_INDEX : WGS_OK;
 }
