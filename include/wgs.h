@@ -459,7 +459,8 @@ wgs_status wgs_build_bucket_plan(const int32_t *bucket_host, int64_t n_pairs, in
  *   workspace  at least wgs_group_norm_act_workspace_bytes(...) bytes,
  *           16-byte aligned, disjoint from the tensors; its contents on entry
  *           do not matter.  Calls that overlap on the GPU need their own.
- * channels: a multiple of groups, at most 4096 (else WGS_ERR_WIDTH); n at most
+ * channels: a multiple of groups, at most 4096, and groups at most 2048 (else
+ * WGS_ERR_WIDTH); n at most
  * 65535.  n == 0 or spatial == 0 launches nothing.  The 16-byte path needs
  * channels a multiple of 4 (f32) or 8 (16-bit types) and 16-byte aligned x
  * and y; otherwise rows are walked element by element.  Sums run in an order that depends on

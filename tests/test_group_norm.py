@@ -125,7 +125,7 @@ def test_group_norm_refusals():
                                   act, dtype, param, None)
 
     assert call(dtype=3) == DTYPE and call(param=2) == DTYPE and call(act=3) == DTYPE
-    assert call(channels=4104, groups=8) == WIDTH
+    assert call(channels=4104, groups=8) == WIDTH and call(channels=4096, groups=4096) == WIDTH
     assert call(groups=7) == SHAPE and call(groups=0) == SHAPE and call(channels=0) == SHAPE
     assert call(n=-1) == SHAPE and call(spatial=-1) == SHAPE and call(n=65536) == SHAPE
     assert call(n=60000, spatial=2 ** 40) == SHAPE

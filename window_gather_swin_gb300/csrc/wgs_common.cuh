@@ -60,6 +60,29 @@ wgs_status launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
     return WGS_OK;
 }
 
+// The same for a grid of clusters of `cluster` blocks along x.
+template <typename... Params, typename... Args>
+wgs_status launch_clusters(void (*kernel)(Params...), dim3 grid, dim3 block, int cluster,
+                           size_t smem, cudaStream_t stream, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = WGS_PDL ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) != cudaSuccess) {
+        cudaGetLastError();  // clear this thread's launch error
+        return WGS_ERR_LAUNCH;
+    }
+    return WGS_OK;
+}
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
