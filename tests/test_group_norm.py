@@ -402,3 +402,81 @@ def test_graph_replay_and_streams_give_the_same_bits():
             assert torch.equal(_bits(p), _bits(q)) and torch.equal(_bits(p), _bits(r))
         for t in got:
             t.zero_()
+
+
+# The launches for samples that one cluster does not hold: one batch (two
+# launches), and several batches (a launch whose blocks take them in turn),
+# with whole and odd rows.
+LARGE = [
+    ((1, 131040, 192, 32), "f16", "silu"), ((3, 65600, 192, 32), "f16", "silu"),
+    ((2, 131040, 192, 8), "bf16", "gelu_tanh"), ((33, 1000, 1001, 7), "bf16", "silu"),
+    ((2, 20000, 770, 1), "f32", "gelu_tanh"), ((5, 32760, 384, 32), "bf16", None),
+    ((3, 3000, 4096, 2048), "f32", "silu"), ((60, 700, 760, 95), "f16", "gelu_tanh"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape,fmt,act", LARGE, ids=str)
+def test_large_samples(shape, fmt, act):
+    """As above, against the formulas in double precision on the GPU."""
+    n, s, c, g = shape
+    dtype = DT[fmt]
+    x, w, b, gy = (t.to(DEV) for t in _inputs((1, s, c, g), fmt, "f32", c))
+    gen = torch.Generator(DEV).manual_seed(5)
+    x, gy = ((torch.randn(n, s, c, generator=gen, device=DEV) * (1 + t[0, :1].float().abs())).to(dtype)
+             for t in (x, gy))
+    y, mean, rstd = wgs.group_norm_act(x, g, w, b, 1e-5, act)
+    gx, gw, gb = wgs.group_norm_act_bwd(gy, x, g, mean, rstd, w, b, act)
+    wgs.check_error(DEV)
+    D, half = 2056, torch.finfo(dtype).eps / 2
+    want_gw, want_gb, mag_w, mag_b = (torch.zeros(c, dtype=torch.float64, device=DEV) for _ in range(4))
+    K = 0.0
+    for i in range(n):
+        xd = x[i].double().view(s, g, c // g)
+        m, var = xd.mean((0, 2)), xd.var((0, 2), unbiased=False)
+        r = (var + 1e-5).rsqrt()
+        S = (xd - m[:, None]).abs().amax((0, 2))
+        tol_m, tol_r = 2 * D * U * S + 2 * U * m.abs(), 2 * D * U * (S * r) ** 2 + 8 * U
+        assert ((mean[i].double() - m).abs() <= tol_m).all()
+        assert ((rstd[i].double() - r).abs() <= tol_r * r).all()
+        up = lambda v: v.repeat_interleave(c // g)
+        wd, bd = w.double(), b.double()
+        h = ((xd - m[:, None]) * r[:, None]).view(s, c)
+        z = (h * wd + bd).requires_grad_()
+        ref = {None: lambda v: v * 1.0, "silu": torch.nn.functional.silu,
+               "gelu_tanh": lambda v: torch.nn.functional.gelu(v, approximate="tanh")}[act](z)
+        ref.sum().backward()
+        slope, ref, z, hw = z.grad, ref.detach(), z.detach(), (h * wd).abs()
+        t = 1.6 * z.abs() + 0.0714 * z.abs() ** 3 if act == "gelu_tanh" else z.abs()
+        tz = wd.abs() * up(r) * (up(tol_m) + U * x[i].double().abs()) + hw * (up(tol_r) + 4 * U) \
+            + 2 * U * (hw + bd.abs())
+        tol = (1.13 * tz + ref.abs() * (4 * U * t + 16 * U)) * (1 + half * 2) + half * ref.abs() + 1e-7 * half
+        err = (y[i].double() - ref).abs()
+        assert (err <= tol).all(), (err / tol).max()
+        # the gradients, from the statistics that the forward gave
+        m, r = mean[i].double(), rstd[i].double()
+        h = ((xd - m[:, None]) * r[:, None]).view(s, c)
+        K = max(K, 5 * U * (hw.max() + bd.abs().max()).item() + 80 * U)
+        gyd = gy[i].double()
+        dz = gyd * slope          # the slope moves by less than the bound below with the statistics
+        d, size = (dz * wd).view(s, g, -1), (gyd * wd).abs().view(s, g, -1)
+        hg = h.view(s, g, -1)
+        want = (r[:, None] * (d - d.mean((0, 2))[:, None] - hg * (d * hg).mean((0, 2))[:, None])).view(s, c)
+        mag = (r[:, None] * (size + size.mean((0, 2))[:, None]
+                             + hg.abs() * (size * hg.abs()).mean((0, 2))[:, None])).view(s, c)
+        slack = 1.2 * D * U + K + 8 * U + 1.2 * tz.max().item()
+        err = (gx[i].double() - want).abs()
+        assert (err <= mag * slack * 1.01 + half * want.abs() + 1e-7 * half).all(), (err / mag).max()
+        want_gw += (dz * h).sum(0)
+        want_gb += dz.sum(0)
+        mag_w += (gyd * h).abs().sum(0)
+        mag_b += gyd.abs().sum(0)
+    for got, want, mag in ((gw, want_gw, mag_w), (gb, want_gb, mag_b)):
+        assert ((got.double() - want).abs() <= mag * slack + U * want.abs()).all()
+    # the same call again, and in place, gives the same bits
+    y2, mean2, _ = wgs.group_norm_act(x.clone(), g, w, b, 1e-5, act)
+    again = wgs.group_norm_act_bwd(gy, x, g, mean, rstd, w, b, act, grad_x=gy)
+    assert torch.equal(_bits(y2), _bits(y)) and torch.equal(mean2, mean)
+    assert all(torch.equal(_bits(p), _bits(q)) for p, q in zip(again, (gx, gw, gb)))
+    wgs.group_norm_act(x, g, w, b, 1e-5, act, out=x)
+    assert torch.equal(_bits(x), _bits(y))

@@ -33,6 +33,8 @@ wgs_status current_device(DeviceInfo *info);
 wgs_status bias_mask_error_take(unsigned int *seen, cudaStream_t stream);
 // The same for the position bias's error word.
 wgs_status position_bias_error_take(unsigned int *seen, cudaStream_t stream);
+// The same for the group norm's.
+wgs_status group_norm_error_take(unsigned int *seen, cudaStream_t stream);
 
 // Launch `kernel` on `stream`.  With WGS_PDL the launch allows programmatic
 // dependent launch: the grid may be scheduled while the previous kernel on

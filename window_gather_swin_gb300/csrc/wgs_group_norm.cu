@@ -13,20 +13,19 @@
 // Design.  A sample is cut into slabs of rows, a block each; a thread owns one
 // chunk of channels (16 bytes where rows consist of whole ones) and steps
 // through the slab's rows, so that a block reads whole rows and a channel's
-// weights and sums stay in registers.  Rows reach a thread through slots of
-// its own in shared memory, filled by asynchronous copies several rows ahead:
-// a slab is only some twenty rows a thread, so without them most of the time
-// is the latency of its loads.  Pass 1 sums, pass 2 computes the result;
-// between them the sums of a sample have to meet:
-//   * the blocks of a cluster add theirs over distributed shared memory, and
-//     one value pair per (cluster, group) goes to the workspace, where every
-//     block of pass 2 adds those of its sample up;
-//   * a sample that one cluster holds goes through both passes in one launch.
-// Pass 2 finds what pass 1 read in L2 when few enough samples are worked on
-// at a time, and walks its rows backwards, the latest first.  With more
-// samples than that, one launch runs pass 2 of a batch of samples next to
-// pass 1 of the following batch, so that reading, writing and arithmetic
-// overlap.
+// weights and sums stay in registers.  Rows reach the block through stages in
+// shared memory, copied in bulk several stages ahead.  Pass 1 sums, pass 2
+// computes the result; between them the sums of a sample have to meet:
+//   * each block of pass 1 leaves one pair of values a group in the workspace,
+//     and every block of pass 2, a launch of its own, adds its sample's up;
+//   * a small sample, or one of many, is taken through both passes in one
+//     launch by a cluster of blocks, which add theirs over distributed shared
+//     memory.
+// Pass 2 walks its rows backwards: what pass 1 read last is still in L2.  Cutting
+// a call into batches of samples that L2 holds, so that pass 2 finds all of
+// them there, was measured slower, as launches of their own (the few
+// microseconds that each pass takes to start and end) and as one resident
+// launch whose blocks wait for one another batch by batch.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -39,18 +38,85 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+// Set (never cleared by a kernel) when a block gave up waiting for its own
+// copies; read and cleared by wgs_check_error.
+__device__ unsigned int g_norm_error;
+
+
 struct F32 {};
 
 constexpr int kMaxChannels = 4096;
 constexpr int kMaxGroups = 2048;
-constexpr int kThreadsFwd = 512, kThreadsBwd = 384;  // two blocks an SM, of 64 and 80 registers a thread
-constexpr int kMaxSmem = 112 << 10;                  // two blocks an SM
+#ifndef WGS_NORM_T1F
+#define WGS_NORM_T1F 384  // threads of a block at most: forward, pass 1
+#endif
+#ifndef WGS_NORM_B1F
+#define WGS_NORM_B1F 304  // blocks of the launch
+#endif
+#ifndef WGS_NORM_T2F
+#define WGS_NORM_T2F 384  // forward, pass 2
+#endif
+#ifndef WGS_NORM_B2F
+#define WGS_NORM_B2F 304
+#endif
+#ifndef WGS_NORM_T1B
+#define WGS_NORM_T1B 512  // backward, pass 1
+#endif
+#ifndef WGS_NORM_B1B
+#define WGS_NORM_B1B 152
+#endif
+#ifndef WGS_NORM_T2B
+#define WGS_NORM_T2B 512  // backward, pass 2
+#endif
+#ifndef WGS_NORM_B2B
+#define WGS_NORM_B2B 152
+#endif
+constexpr int kMaxSmem = 200 << 10;
 constexpr int kMaxCluster = 8;   // of a sample that one cluster holds
-constexpr int kPairCluster = 2;  // of larger ones: a pair of blocks finds room on any GPC
 
 enum : int { kNone = 0, kSilu = 1, kGeluTanh = 2 };
 
 // ------------------------------------------------------------ pairs, chunks --
+
+// How L2 keeps lines: as any others, or given up before them.
+__device__ __forceinline__ uint64_t l2_policy(bool first_out) {
+    uint64_t p;
+    if (first_out)
+        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    else
+        asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+// mbarriers of a block's own bulk copies.
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Wait for the end of phase `parity`: a copy of this block, or its own warps'
+// arrivals, which always come.  The limit (far beyond any copy's time) only
+// keeps a fault from hanging the GPU; it is reported.
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity) {
+    uint32_t done = 0;
+    for (int tries = 0; tries < 1 << 22; ++tries) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+        if (done) return;
+    }
+    atomicOr(&g_norm_error, 1u);
+}
+__device__ __forceinline__ void bulk_copy(uint32_t to, const char *from, uint32_t bytes, uint32_t bar,
+                                          uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+        ::"r"(to), "l"(from), "r"(bytes), "r"(bar), "l"(policy) : "memory");
+}
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
@@ -108,8 +174,8 @@ struct Chunk {
             return E::to_f2(word_of(r, p));
         }
     }
-    // rounds each value once, to nearest even
-    __device__ static void store(char *p, const float2 (&v)[kPairs]) {
+    // rounds each value once, to nearest even; `policy` says how L2 keeps the line
+    __device__ static void store(char *p, const float2 (&v)[kPairs], uint64_t policy) {
         Raw r;
         if constexpr (k32) {
             if constexpr (kV == 4)
@@ -125,7 +191,10 @@ struct Chunk {
         } else {
             r = static_cast<Raw>(E::from_f2(v[0].x, v[0].y));
         }
-        *reinterpret_cast<Raw *>(p) = r;
+        if constexpr (kBytes == 16)
+            asm volatile("st.global.L2::cache_hint.v4.b32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "l"(policy) : "memory");
+        else
+            *reinterpret_cast<Raw *>(p) = r;
     }
 };
 
@@ -149,18 +218,30 @@ __device__ __forceinline__ void store_param(void *p, int64_t c, bool p32, float 
     }
 }
 
-// 1 / (1 + exp(-t)).  For 16-bit tensors the hardware's exp2 and reciprocal
-// (relative errors of a few 2^-22 and that of the product t log2(e)) are far
-// below the output's half step; FP32 tensors take expf and a division.
-template <bool k32>
-__device__ __forceinline__ float2 sigmoid(float2 t) {
+constexpr float kTwoK = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kCubic = 0.044715f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 1 / (1 + exp(-q)), q = z for SiLU and z (kTwoK + kTwoK kCubic z^2) for the
+// GELU (0.5 (1 + tanh(u)) = 1 / (1 + exp(-2u)), which does not cancel for
+// negative z).  16-bit tensors take the hardware's exp2 and reciprocal
+// (relative errors of a few 2^-22, and that of the argument's rounding: far
+// below the output's half step), with log2(e) in the constants; FP32 tensors
+// take expf and a division.
+template <int kAct, bool k32>
+__device__ __forceinline__ float2 gate(float2 z) {
+    constexpr float m = k32 ? -1.0f : -kLog2e;
+    float2 t;
+    if constexpr (kAct == kSilu)
+        t = __fmul2_rn(z, both(m));
+    else
+        t = __fmul2_rn(z, __ffma2_rn(__fmul2_rn(z, z), both(m * kTwoK * kCubic), both(m * kTwoK)));
     if constexpr (k32) {
-        return make_float2(1.0f / (1.0f + expf(-t.x)), 1.0f / (1.0f + expf(-t.y)));
+        return make_float2(1.0f / (1.0f + expf(t.x)), 1.0f / (1.0f + expf(t.y)));
     } else {
-        const float2 w = __fmul2_rn(t, both(-1.4426950408889634f));
         float2 e, s;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(w.x));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(w.y));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
         e = __fadd2_rn(e, both(1.0f));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(e.x));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(e.y));
@@ -168,42 +249,43 @@ __device__ __forceinline__ float2 sigmoid(float2 t) {
     }
 }
 
-constexpr float kTwoK = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-constexpr float kCubic = 0.044715f;
-
-// act(z); gelu_tanh(z) = 0.5 z (1 + tanh(u)) = z sigmoid(2u), which does not
-// cancel for negative z.
 template <int kAct, bool k32>
 __device__ __forceinline__ float2 act(float2 z) {
-    if constexpr (kAct == kSilu) return __fmul2_rn(z, sigmoid<k32>(z));
-    if constexpr (kAct == kGeluTanh) {
-        const float2 q = __ffma2_rn(__fmul2_rn(z, z), both(kTwoK * kCubic), both(kTwoK));
-        return __fmul2_rn(z, sigmoid<k32>(__fmul2_rn(z, q)));
-    }
-    return z;
+    if constexpr (kAct == kNone) return z;
+    return __fmul2_rn(z, gate<kAct, k32>(z));
 }
 
-// act'(z) = s + z s (1 - s) q', with s the sigmoid's value and q its argument.
+// act'(z) = s + z s (1 - s) q', with s the gate.
 template <int kAct, bool k32>
 __device__ __forceinline__ float2 act_grad(float2 z) {
+    if constexpr (kAct == kNone) return both(1.0f);
+    const float2 s = gate<kAct, k32>(z);
+    const float2 p = __fmul2_rn(z, s);
+    const float2 rest = __ffma2_rn(s, both(-1.0f), both(1.0f));
     if constexpr (kAct == kSilu) {
-        const float2 s = sigmoid<k32>(z);
-        return __ffma2_rn(__fmul2_rn(z, s), __ffma2_rn(s, both(-1.0f), both(1.0f)), s);
+        return __ffma2_rn(p, rest, s);
+    } else {
+        // q' = kTwoK + 3 kTwoK kCubic z^2.  Far out z s (1 - s) is 0, and there
+        // the slope may be infinite: it is cut to what a finite z^2 gives
+        float2 z2 = __fmul2_rn(z, z);
+        z2 = make_float2(fminf(z2.x, 1e30f), fminf(z2.y, 1e30f));
+        return __ffma2_rn(__fmul2_rn(p, rest), __ffma2_rn(z2, both(3.0f * kTwoK * kCubic), both(kTwoK)), s);
     }
-    if constexpr (kAct == kGeluTanh) {
-        const float2 z2 = __fmul2_rn(z, z);
-        const float2 q = __ffma2_rn(z2, both(kTwoK * kCubic), both(kTwoK));
-        const float2 s = sigmoid<k32>(__fmul2_rn(z, q));
-        const float2 p = __fmul2_rn(__fmul2_rn(z, s), __ffma2_rn(s, both(-1.0f), both(1.0f)));
-        // q' = q + 2 kTwoK kCubic z^2.  Far out p is 0, and there the slope
-        // may be infinite: it is cut to what a finite z^2 gives
-        const float2 zc = make_float2(fminf(z2.x, 1e30f), fminf(z2.y, 1e30f));
-        return __ffma2_rn(p, __ffma2_rn(zc, both(3.0f * kTwoK * kCubic), both(kTwoK)), s);
-    }
-    return both(1.0f);
 }
 
+// max(v, 0) that keeps NaN.
+__device__ __forceinline__ float not_below_zero(float v) { return v < 0.f ? 0.f : v; }
+
 // -------------------------------------------------------------------- work --
+
+// A sample's rows in `count` slabs of `rows`, one more in the first `longer`.
+struct Slabs {
+    int32_t count, rows, longer;
+    // first row of slab s
+    __device__ int32_t start(int32_t s) const { return s * rows + min(s, longer); }
+    // rows of n slabs from slab s on
+    __device__ int32_t of(int32_t s, int32_t n) const { return n * rows + max(min(longer - s, n), 0); }
+};
 
 struct NormArgs {
     const char *x, *gy;         // gy: backward
@@ -214,119 +296,221 @@ struct NormArgs {
     float2 *chan_part;          // backward: [n, clusters, C]: the sums of (dz, dz h)
     void *grad_weight, *grad_bias;
     int64_t spatial;
-    int64_t first1, first2;     // first sample of pass 1 and of pass 2
-    int32_t n1, n2;             // samples of pass 1 and of pass 2
     int32_t channels, groups, per_group;
+    int32_t group_shift;        // log2 of the lanes that add a group's channels up
     int32_t chunks;             // of a row
-    int32_t columns;            // chunks a block walks side by side
-    int32_t slabs, cluster;     // slabs of a sample, a multiple of the cluster size
-    int32_t clusters;           // slabs / cluster
-    int32_t slab_rows, longer;  // rows of a slab, one more in the first `longer`
+    int32_t cluster, clusters;  // blocks of a cluster, clusters of a sample
+    Slabs slabs1, slabs2;       // of the two passes
     int32_t ring;               // bytes of the slots
-    int32_t passes;             // 1 + 2 for a launch that takes its samples through both
+    int32_t behind;             // bytes before what pass 1 of the backward keeps of the groups
+    int32_t passes;             // of the launch: 1, 2 or 3 (both)
+    bool last_use;              // pass 2's lines need not stay in L2: the call is larger
     float eps;
     bool p32;                   // weight and bias are FP32
 };
 
-// First row of a slab.
-__device__ __forceinline__ int32_t slab_start(const NormArgs &a, int32_t slab) {
-    return slab * a.slab_rows + min(slab, a.longer);
+// The first launch of a call waits for what came before on the stream.  A
+// launch of pass 2 follows one of pass 1 of the same call, which has waited
+// for all that, and needs of it only the workspace's sums: it may read the
+// call's inputs at once, and waits (wait_for_sums) before it reads the sums or writes.
+__device__ __forceinline__ void start_launch(const NormArgs &a) {
+#if WGS_PDL
+    if (a.passes != 2) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+#endif
+}
+__device__ __forceinline__ void wait_for_sums(const NormArgs &a) {
+#if WGS_PDL
+    if (a.passes == 2) asm volatile("griddepcontrol.wait;" ::: "memory");
+#endif
 }
 
-// What a block is to do: its pass (1, 2 or 3 for both), sample and slab.
+// A block's work: a slab of a sample in pass 1 or 2; and what its thread is in
+// it: chunk j and row group g of the columns x row groups that the block walks
+// side by side.
 struct Job {
-    int pass;
     int64_t sample;
-    int32_t cl, rank;  // cluster of the sample, block of the cluster
+    int32_t cl, rank;  // cluster of the sample, block of the cluster (pass 1)
     int32_t r0, rows;  // first row, rows
+    int j, g, columns, row_groups, tid, threads;
     __device__ explicit Job(const NormArgs &a) {
-        const uint32_t per = static_cast<uint32_t>(a.clusters);
-        uint32_t id = blockIdx.x / static_cast<uint32_t>(a.cluster);
-        rank = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(a.cluster));
-        pass = a.passes;
-        if (pass == 0) {
-            // clusters of the two passes alternate while both have some
-            const uint32_t c1 = per * a.n1, c2 = per * a.n2, m = min(c1, c2);
-            if (id < 2 * m) {
-                pass = id & 1 ? 1 : 2;
-                id >>= 1;
-            } else {
-                pass = c1 > c2 ? 1 : 2;
-                id -= m;
-            }
-        }
-        sample = (pass == 2 ? a.first2 : a.first1) + id / per;
-        cl = static_cast<int32_t>(id % per);
-        const int32_t slab = cl * a.cluster + rank;
-        r0 = slab_start(a, slab);
-        rows = a.slab_rows + (slab < a.longer);
+        const Slabs &slabs = a.passes & 1 ? a.slabs1 : a.slabs2;
+        const int32_t slab = blockIdx.x;
+        sample = blockIdx.y;
+        rank = slab & (a.cluster - 1);  // clusters have a power of two
+        cl = slab / a.cluster;
+        r0 = slabs.start(slab);
+        rows = slabs.of(slab, 1);
+        j = threadIdx.x, g = threadIdx.y, columns = blockDim.x, row_groups = blockDim.y;
+        tid = g * columns + j, threads = columns * row_groups;
     }
+    // rows of this thread
+    __device__ int32_t mine() const { return g < rows ? (rows - g + row_groups - 1) / row_groups : 0; }
 };
 
-// Thread (g, j) of a block of `columns` chunks x row groups.
-struct Place {
-    int j, g, row_groups;
-    bool active;
-    __device__ explicit Place(int columns) {
-        row_groups = static_cast<int>(blockDim.x) / columns;
-        j = static_cast<int>(threadIdx.x) % columns;
-        g = static_cast<int>(threadIdx.x) / columns;
-        active = g < row_groups;
-    }
+// A slab's rows on their way through shared memory: kRows rows of every thread
+// a stage, kStages stages, f(chunk of each tensor, its byte offset) for each
+// of the thread's places in run().
+//
+// Rows of whole 16-byte chunks: one thread copies a stage's rows in bulk (TMA;
+// they are one piece of memory where the block walks whole rows), and an
+// mbarrier a stage tells that they have come, another that every warp has
+// read them.  A thread spends nothing on addresses and copies of its own.
+struct Bars {
+    uint32_t full, empty;  // of stage 0; 8 bytes a stage
+    int stage;             // of the next use
+    uint32_t phase;        // its parity
+    bool used;             // a stage has been
 };
 
-// The chunks of kTensors tensors at the byte offsets at, at + step, ... of a
-// thread, kSlots - 1 places ahead of their use: each thread copies its own
-// chunks into its own slots and needs no barrier.  The slot that a copy
-// overwrites was read one place before.
-template <typename C, int kTensors, int kSlots>
-struct Stream {
-    static constexpr bool kAsync = C::kBytes >= 4;  // the smallest asynchronous copy
-    static constexpr int kLead = kSlots - 1;
-    uint32_t slots;  // address of the thread's chunk of slot 0
+template <typename C, int kTensors, int kRows, int kStages>
+struct Bulk {
+    const Job &job;
+    Bars &bars;
     const char *src[kTensors];
-    int64_t at;  // offset of the next chunk to use
-    int32_t step, left;
-    int next;    // its slot
+    uint32_t ring;
+    int64_t base;       // byte offset of the slab's first row, at the block's first chunk
+    int64_t row_bytes;
+    int32_t wide;       // chunks of a row that the block takes
+    int32_t count;      // stages of the slab
+    bool reverse;
+    uint64_t policy;
 
-    __device__ uint32_t slot(int s, int t) const { return slots + (s * kTensors + t) * (blockDim.x * C::kBytes); }
-    // the chunk kLead places on, into slot s
-    __device__ void copy(int s, int64_t from, bool live) const {
-        if (live) {
+    __device__ Bulk(const Job &job_, Bars &bars_) : job(job_), bars(bars_) {}
+    __device__ uint32_t stage_bytes() const { return job.threads * C::kBytes * kTensors * kRows; }
+    __device__ int32_t stage_rows() const { return job.row_groups * kRows; }
+
+    // by one thread: the slab's i-th stage into slot `stage`
+    __device__ void copy(int32_t i, int stage) const {
+        const int32_t r0 = (reverse ? count - 1 - i : i) * stage_rows(), rows = min(stage_rows(), job.rows - r0);
+        const uint32_t bar = bars.full + 8 * stage, to = ring + stage * stage_bytes();
+        const uint32_t seg = wide * C::kBytes;
+        bar_expect(bar, rows * seg * kTensors);
+        const int64_t from = base + r0 * row_bytes;
 #pragma unroll
-            for (int t = 0; t < kTensors; ++t) {
-                const uint32_t to = slot(s, t);
-                if constexpr (C::kBytes == 16)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src[t] + from) : "memory");
-                else
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(src[t] + from), "n"(C::kBytes) : "memory");
-            }
+        for (int t = 0; t < kTensors; ++t) {
+            const uint32_t at = to + t * job.threads * C::kBytes * kRows;
+            if (seg == row_bytes)
+                bulk_copy(at, src[t] + from, rows * seg, bar, policy);
+            else
+                for (int32_t r = 0; r < rows; ++r)
+                    bulk_copy(at + r * (job.columns * C::kBytes), src[t] + from + r * row_bytes, seg, bar, policy);
         }
-        cp_async_commit();
     }
-    __device__ void start(float2 *smem, int64_t first, int32_t step_, int32_t rows) {
-        slots = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * C::kBytes;
-        at = first;
-        step = step_;
-        left = rows;
-        next = 0;
-        if constexpr (kAsync)
+    // every slot has been read (the block has met at a barrier since)
+    __device__ void start(const float2 *smem, int64_t base_, int64_t row_bytes_, int32_t wide_, bool reverse_,
+                          uint64_t policy_) {
+        ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+        base = base_, row_bytes = row_bytes_, wide = wide_, reverse = reverse_, policy = policy_;
+        count = (job.rows + stage_rows() - 1) / stage_rows();
+        if (job.tid == 0) {
+            // what the block wrote to the slots comes before the copies
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            for (int i = 0; i < kStages - 1 && i < count; ++i)
+                copy(i, bars.stage + i < kStages ? bars.stage + i : bars.stage + i - kStages);
+        }
+    }
+    template <typename Use>
+    __device__ void run(Use f) {
+        const uint32_t stride = job.threads * C::kBytes;
+        const int32_t step = static_cast<int32_t>(job.row_groups * row_bytes);
+        int64_t at = base + job.g * row_bytes + job.j * C::kBytes;
+        if (reverse) at += static_cast<int64_t>(count - 1) * kRows * step;
+        for (int32_t i = 0; i < count; ++i) {
+            if (job.tid == 0 && i + kStages - 1 < count) {
+                // into the slot that was read last, when all warps have
+                const int free = bars.stage == 0 ? kStages - 1 : bars.stage - 1;
+                if (bars.used) bar_wait(bars.empty + 8 * free, bars.stage == 0 ? bars.phase ^ 1 : bars.phase);
+                copy(i + kStages - 1, free);
+            }
+            bar_wait(bars.full + 8 * bars.stage, bars.phase);
+            const uint32_t slot = ring + bars.stage * stage_bytes() + job.tid * C::kBytes;
+            auto load = [&](int u, typename C::Raw (&v)[kTensors]) {
 #pragma unroll
-            for (int i = 0; i < kLead; ++i) copy(i, at + i * step, i < left);
+                for (int t = 0; t < kTensors; ++t) v[t] = C::load_shared(slot + (t * kRows + u) * stride);
+            };
+            // only the slab's last stage can be short
+            int32_t live = kRows * job.row_groups;
+            if (i == (reverse ? 0 : count - 1)) live = job.rows - (count - 1) * live;
+            live = job.j < wide ? live - job.g : 0;
+            if (live > (kRows - 1) * job.row_groups) {
+                typename C::Raw v[kRows][kTensors];
+#pragma unroll
+                for (int u = 0; u < kRows; ++u) load(u, v[u]);
+#pragma unroll
+                for (int u = 0; u < kRows; ++u) f(v[u], at + u * step);
+            } else {
+                for (int u = 0; u * job.row_groups < live; ++u) {
+                    typename C::Raw v[kTensors];
+                    load(u, v);
+                    f(v, at + u * step);
+                }
+            }
+            at += reverse ? -kRows * step : kRows * step;
+            __syncwarp();
+            if ((job.tid & 31) == 0) bar_arrive(bars.empty + 8 * bars.stage);
+            bars.used = true;
+            if (++bars.stage == kStages) bars.stage = 0, bars.phase ^= 1;
+        }
     }
-    // f(chunk of each tensor, offset) for every place in order
+};
+
+// Other rows: each thread copies its own chunks into its own slots
+// (cp.async), which needs no barrier; 2-byte chunks, which cp.async does not
+// know, are loaded several rows at a time.
+template <typename C, int kTensors, int kRows, int kStages>
+struct Own {
+    static constexpr bool kAsync = C::kBytes >= 4;
+    const Job &job;
+    const char *src[kTensors];
+    uint32_t slots, stride;  // address of the thread's first slot, bytes from slot to slot
+    int64_t at;              // offset of the next chunk to use
+    int32_t step, left;
+
+    __device__ Own(const Job &job_, Bars &) : job(job_) {}
+
+    __device__ void copy(uint32_t to, int64_t from, int32_t rows) const {
+        if constexpr (kAsync) {
+#pragma unroll
+            for (int u = 0; u < kRows; ++u)
+                if (u < rows) {
+#pragma unroll
+                    for (int t = 0; t < kTensors; ++t)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + (u * kTensors + t) * stride), "l"(src[t] + from + u * step), "n"(C::kBytes) : "memory");
+                }
+            cp_async_commit();
+        }
+    }
+    __device__ void start(const float2 *smem, int64_t base, int64_t row_bytes, int32_t wide, bool reverse, uint64_t) {
+        slots = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + job.tid * C::kBytes;
+        stride = job.threads * C::kBytes;
+        left = job.j < wide ? job.mine() : 0;
+        step = static_cast<int32_t>(job.row_groups * row_bytes);
+        at = base + job.g * row_bytes + job.j * C::kBytes;
+        if (reverse) at += static_cast<int64_t>(left - 1) * step, step = -step;
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i)
+            copy(slots + i * kRows * kTensors * stride, at + i * kRows * step, left - i * kRows);
+    }
     template <typename Use>
     __device__ void run(Use f) {
         if constexpr (kAsync) {
-            for (; left > 0; --left) {
-                cp_async_wait<kLead - 1>();
-                typename C::Raw v[kTensors];
+            const uint32_t stage = kRows * kTensors * stride;
+            const int32_t lead = (kStages - 1) * kRows * step;
+            uint32_t use = slots, free = slots + (kStages - 1) * stage;
+            for (; left > 0; left -= kRows, at += kRows * step) {
+                cp_async_wait<kStages - 2>();
+                typename C::Raw v[kRows][kTensors];
 #pragma unroll
-                for (int t = 0; t < kTensors; ++t) v[t] = C::load_shared(slot(next, t));
-                copy(next == 0 ? kLead : next - 1, at + kLead * step, left > kLead);
-                next = next == kLead ? 0 : next + 1;
-                f(v, at);
-                at += step;
+                for (int u = 0; u < kRows; ++u)
+#pragma unroll
+                    for (int t = 0; t < kTensors; ++t) v[u][t] = C::load_shared(use + (u * kTensors + t) * stride);
+                copy(free, at + lead, left - (kStages - 1) * kRows);
+                free = use;
+                use = use == slots + (kStages - 1) * stage ? slots : use + stage;
+#pragma unroll
+                for (int u = 0; u < kRows; ++u)
+                    if (u < left) f(v[u], at + u * step);
             }
             cp_async_wait<0>();
         } else {
@@ -346,61 +530,168 @@ struct Stream {
     }
 };
 
-constexpr int kSlotsFwd = 8, kSlotsBwd = 6;
+// Rows a stage and stages: the forward's with one tensor, the backward's with two.
+constexpr int kRowsFwd = 4, kStagesFwd = 3, kRowsBwd = 2, kStagesBwd = 4;
+
+template <typename C, int kTensors>
+using Stream = std::conditional_t<
+    C::kBytes == 16,
+    std::conditional_t<kTensors == 1, Bulk<C, 1, kRowsFwd, kStagesFwd>, Bulk<C, 2, kRowsBwd, kStagesBwd>>,
+    std::conditional_t<kTensors == 1, Own<C, 1, kRowsFwd, kStagesFwd>, Own<C, 2, kRowsBwd, kStagesBwd>>>;
+
+// The block's barriers, before its first job.
+template <int kStages>
+__device__ __forceinline__ Bars make_bars(uint64_t *storage) {
+    Bars b;
+    b.full = static_cast<uint32_t>(__cvta_generic_to_shared(storage));
+    b.empty = b.full + 8 * kStages;
+    b.stage = 0, b.phase = 0, b.used = false;
+    if (threadIdx.x == 0 && threadIdx.y == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(b.full + 8 * i, 1);
+            bar_init(b.empty + 8 * i, (blockDim.x * blockDim.y + 31) / 32);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    return b;
+}
 
 // Add the threads' pairs of sums (s1, s2) over the row groups, in order;
-// done(channel of the column block, its sums) is called once a channel.
-// Every thread calls it.  In `red` a row group's values lie element by element of
-// the chunk, so that neighbouring threads touch neighbouring words.
+// done(element of the chunk, its channel, its sums) is called once a channel
+// by a thread of the channel's chunk.  Every thread calls it.  In `red` a row group's
+// values lie element by element of the chunk, so that neighbouring threads
+// touch neighbouring words.
 template <int kV, int kPairs, typename Done>
-__device__ __forceinline__ void add_row_groups(float2 *red, const Place &at, int wide,
+__device__ __forceinline__ void add_row_groups(float2 *red, const Job &job, int32_t c0, int wide,
                                                const float2 (&s1)[kPairs],
                                                const float2 (&s2)[kPairs], Done done) {
     __syncthreads();  // the slots that `red` lies over have been read
-    if (at.active && at.j < wide) {
-        float2 *mine = red + at.g * wide * kV + at.j;
+    if (job.j < wide) {
+        float2 *mine = red + job.g * wide * kV + job.j;
 #pragma unroll
         for (int e = 0; e < kV; ++e)
             mine[e * wide] = e & 1 ? make_float2(s1[e / 2].y, s2[e / 2].y) : make_float2(s1[e / 2].x, s2[e / 2].x);
     }
     __syncthreads();
-    const int cols = wide * kV;
-    for (int i = threadIdx.x; i < cols; i += blockDim.x) {
-        float2 t = red[i];
+    if (job.j < wide)
+        for (int e = job.g; e < kV; e += job.row_groups) {
+            const float2 *p = red + e * wide + job.j;
+            float2 t = *p;
 #pragma unroll 4
-        for (int g = 1; g < at.row_groups; ++g) t = __fadd2_rn(t, red[g * cols + i]);
-        done(i % wide * kV + i / wide, t);
-    }
+            for (int g = 1; g < job.row_groups; ++g) t = __fadd2_rn(t, p[g * wide * kV]);
+            done(e, (c0 + job.j) * kV + e, t);
+        }
     __syncthreads();
 }
 
-// Values of a group in the slabs [s0, s1).
-__device__ __forceinline__ float values_of(const NormArgs &a, int32_t s0, int32_t s1) {
-    return static_cast<float>(slab_start(a, s1) - slab_start(a, s0)) * static_cast<float>(a.per_group);
+// Sum over the 2^shift neighbouring lanes of a group.
+__device__ __forceinline__ float lanes_sum(float v, int shift) {
+    for (int o = 1 << shift >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
-// For every group g: the sum of value(part, g) over the parts [0, parts),
-// in a fixed order, to done(g, sum).  Neighbouring threads take neighbouring
-// groups, and the threads beyond the groups a share of the parts each.
-template <typename Value, typename Done>
-__device__ __forceinline__ void add_parts(float2 *smem, int groups, int parts, Value value, Done done) {
-    const int wide = min(groups, static_cast<int>(blockDim.x));
-    const int lanes = static_cast<int>(blockDim.x) / wide;
-    const int j = static_cast<int>(threadIdx.x) % wide, l = static_cast<int>(threadIdx.x) / wide;
+// For every group g: f(g, first lane, lanes) with all threads of full warps.
+template <typename F>
+__device__ __forceinline__ void each_group(const NormArgs &a, const Job &job, F f) {
+    const int whole = job.threads & ~31;
+    if (job.tid >= whole) return;
+    const int at_a_time = whole >> a.group_shift;
+    for (int g0 = 0; g0 < a.groups; g0 += at_a_time)
+        f(g0 + (job.tid >> a.group_shift), job.tid & ((1 << a.group_shift) - 1), 1 << a.group_shift);
+}
+
+// Values of a group in `count` of pass 1's slabs from slab s on.
+__device__ __forceinline__ float values_of(const NormArgs &a, int32_t s, int32_t count) {
+    return static_cast<float>(a.slabs1.of(s, count)) * static_cast<float>(a.per_group);
+}
+
+// For every group g: the sum of value(part, g, own(g)) over the parts [0,
+// parts), in a fixed order, to done(g, sum, own(g)).  Neighbouring threads take
+// neighbouring groups, and the threads beyond the groups a share of the
+// parts each.  smem holds a pair a thread.
+template <typename Own, typename Value, typename Done>
+__device__ __forceinline__ void add_parts(float2 *smem, const Job &job, int groups, int parts, Own own,
+                                          Value value, Done done) {
+    const int wide = min(groups, job.threads);
+    const int lanes = job.threads / wide;
+    const int l = job.tid / wide, j = job.tid - l * wide;
     for (int g0 = 0; g0 < groups; g0 += wide) {
         const int g = g0 + j;
         float2 t = make_float2(0.f, 0.f);
-        if (l < lanes && g < groups)
-#pragma unroll 4
-            for (int p = l; p < parts; p += lanes) t = __fadd2_rn(t, value(p, g));
-        smem[threadIdx.x] = t;
+        float o = 0.f;
+        if (l < lanes && g < groups) {
+            o = own(g);
+#pragma unroll 16
+            for (int p = l; p < parts; p += lanes) t = __fadd2_rn(t, value(p, g, o));
+        }
+        smem[job.tid] = t;
         __syncthreads();
         if (l == 0 && g < groups) {
-            for (int q = 1; q < lanes && q < parts; ++q) t = __fadd2_rn(t, smem[q * wide + j]);
-            done(g, t);
+#pragma unroll 8
+            for (int q = 1; q < min(lanes, parts); ++q) t = __fadd2_rn(t, smem[q * wide + j]);
+            done(g, t, o);
         }
         __syncthreads();
     }
+}
+
+// Weights or biases of a chunk's channels: FP32 or the tensor's own format;
+// NULL is the default.
+template <typename E, int kV>
+__device__ __forceinline__ void params(const void *p, int32_t chunk, bool p32, float otherwise,
+                                       float (&v)[kV]) {
+    const bool whole = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+    if (!p) {
+#pragma unroll
+        for (int e = 0; e < kV; ++e) v[e] = otherwise;
+    } else if (p32) {
+        const float *q = static_cast<const float *>(p) + static_cast<int64_t>(chunk) * kV;
+        if (kV % 4 == 0 && whole) {
+#pragma unroll
+            for (int e = 0; e < kV; e += 4) {
+                const float4 f = __ldg(reinterpret_cast<const float4 *>(q + e));
+                v[e] = f.x, v[(e + 1) % kV] = f.y, v[(e + 2) % kV] = f.z, v[(e + 3) % kV] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kV; ++e) v[e] = __ldg(q + e);
+        }
+    } else if constexpr (!std::is_same<E, F32>::value) {
+        const uint16_t *q = static_cast<const uint16_t *>(p) + static_cast<int64_t>(chunk) * kV;
+        if (kV == 8 && whole) {
+            const uint4 f = __ldg(reinterpret_cast<const uint4 *>(q));
+#pragma unroll
+            for (int e = 0; e < kV; e += 2) {
+                const float2 w = E::to_f2(word(f, e / 2));
+                v[e] = w.x, v[(e + 1) % kV] = w.y;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kV; ++e) v[e] = E::to_f2(__ldg(q + e)).x;
+        }
+    }
+}
+
+// enter(group) at a chunk's first channel and where another group begins,
+// f(element, channel) for each of its channels.
+template <int kV, typename Enter, typename F>
+__device__ __forceinline__ void each_channel(const NormArgs &a, int32_t chunk, Enter enter, F f) {
+    int32_t g = chunk * kV / a.per_group, in_group = chunk * kV - g * a.per_group;
+    enter(g);
+#pragma unroll
+    for (int e = 0; e < kV; ++e) {
+        if (in_group == a.per_group) {
+            in_group = 0;
+            enter(++g);
+        }
+        f(e);
+        ++in_group;
+    }
+}
+
+__device__ __forceinline__ void set_half(float2 *v, int e, float x) {
+    if (e & 1) v[e / 2].y = x; else v[e / 2].x = x;
 }
 
 // Forward, pass 1: (mean, M2) of every group over the rows of a cluster, M2
@@ -411,42 +702,37 @@ __device__ __forceinline__ void add_parts(float2 *smem, int groups, int parts, V
 // outlier, whatever the mean.  Where parts are joined the same is done with
 // the first part's mean as the reference.
 template <typename E, int kV>
-__device__ void stats_pass(const NormArgs &a, const Job &job, float2 *smem) {
+__device__ void stats_pass(const NormArgs &a, const Job &job, Bars &bars, float2 *smem) {
     using C = Chunk<E, kV>;
     using One = Chunk<E, 1>;
     constexpr int kP = C::kPairs;
     float2 *ch = smem, *red = smem + a.channels;  // red holds the groups' results in the end
-    float2 *ring = a.columns == a.chunks ? smem : red;
-    const Place at(a.columns);
+    float2 *ring = job.columns == a.chunks ? smem : red;
     const int64_t row_bytes = static_cast<int64_t>(a.chunks) * C::kBytes;
-    const int32_t rows = job.rows;
-    const float inv = rows > 0 ? 1.0f / static_cast<float>(rows) : 0.f;
-    const char *lead = a.x + (job.sample * a.spatial + job.r0) * row_bytes;
+    const float inv = job.rows > 0 ? 1.0f / static_cast<float>(job.rows) : 0.f;
+    const int64_t origin = (job.sample * a.spatial + job.r0) * row_bytes;
     auto first = [&](int c) {  // the channel's value in the slab's first row
-        return rows > 0 ? One::wide(One::load(lead + static_cast<int64_t>(c) * One::kBytes), 0).x : 0.f;
+        return job.rows > 0 ? One::wide(One::load(a.x + origin + static_cast<int64_t>(c) * One::kBytes), 0).x : 0.f;
     };
-    for (int32_t c0 = 0; c0 < a.chunks; c0 += a.columns) {
-        const int32_t wide = min(a.columns, a.chunks - c0);
-        const bool mine = at.active && at.j < wide && at.g < rows;
-        Stream<C, 1, kSlotsFwd> in;
+    for (int32_t c0 = 0; c0 < a.chunks; c0 += job.columns) {
+        const int32_t wide = min(job.columns, a.chunks - c0);
+        const int64_t o = origin + c0 * C::kBytes;
+        // first the few values that the block starts with, before its copies
+        // fill the way to memory
+        typename C::Raw lead = {};
+        if (job.j < wide && job.rows > 0) lead = C::load(a.x + o + job.j * C::kBytes);
+        // the value that this thread will need where it ends its first channel
+        const float ahead = job.j < wide && job.g < kV ? first((c0 + job.j) * kV + job.g) : 0.f;
+        Stream<C, 1> in(job, bars);
         in.src[0] = a.x;
-        const int64_t o = (job.sample * a.spatial + job.r0 + at.g) * row_bytes + (c0 + at.j) * C::kBytes;
-        in.start(ring, o, static_cast<int32_t>(at.row_groups * row_bytes),
-                 mine ? (rows - at.g + at.row_groups - 1) / at.row_groups : 0);
+        in.start(ring, o, row_bytes, wide, false, l2_policy(false));
         float2 k[kP], s1[kP], s2[kP];
 #pragma unroll
-        for (int p = 0; p < kP; ++p) k[p] = s1[p] = s2[p] = both(0.f);
-        if (mine) {
-            const typename C::Raw r = C::load(lead + (c0 + at.j) * C::kBytes);
-#pragma unroll
-            for (int p = 0; p < kP; ++p) {
-                k[p] = C::wide(r, p);
-                k[p].x = -k[p].x, k[p].y = -k[p].y;
-            }
+        for (int p = 0; p < kP; ++p) {
+            k[p] = C::wide(lead, p);
+            k[p].x = -k[p].x, k[p].y = -k[p].y;
+            s1[p] = s2[p] = both(0.f);
         }
-        // the value that this thread will need where it ends a channel
-        const int ends = static_cast<int>(threadIdx.x) % wide * kV + static_cast<int>(threadIdx.x) / wide;
-        const float ahead = static_cast<int>(threadIdx.x) < wide * kV ? first(c0 * kV + ends) : 0.f;
         in.run([&](const typename C::Raw (&v)[1], int64_t) {
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
@@ -455,135 +741,121 @@ __device__ void stats_pass(const NormArgs &a, const Job &job, float2 *smem) {
                 s2[p] = __ffma2_rn(d, d, s2[p]);
             }
         });
-        add_row_groups<kV>(red, at, wide, s1, s2, [&](int c, float2 t) {
+        add_row_groups<kV>(red, job, c0, wide, s1, s2, [&](int e, int c, float2 t) {
             const float m = t.x * inv;
-            ch[c0 * kV + c] = make_float2((c == ends ? ahead : first(c0 * kV + c)) + m,
-                                          fmaxf(fmaf(-m, t.x, t.y), 0.f));
+            ch[c] = make_float2((e == job.g ? ahead : first(c)) + m, not_below_zero(fmaf(-m, t.x, t.y)));
         });
     }
-    // a warp a group, in two steps over its channels: the mean, M2 about it
-    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
-    for (int g = threadIdx.x / 32; g < a.groups; g += warps) {
-        const float2 *p = ch + g * a.per_group;
+    wait_for_sums(a);  // nothing is written before
+    float2 *out = a.groups_part + (job.sample * a.clusters + job.cl) * a.groups;
+    // the channels of a group, in two steps: the mean, M2 about it
+    each_group(a, job, [&](int g, int lane, int lanes) {
+        const bool live = g < a.groups;
+        const float2 *p = ch + (live ? g : 0) * a.per_group;
         const float ref = p[0].x;
         float mean = 0.f, m2 = 0.f;
-        for (int i = lane; i < a.per_group; i += 32) mean += p[i].x - ref;
-        mean = ref + group_sum<32>(mean) / static_cast<float>(a.per_group);
-        for (int i = lane; i < a.per_group; i += 32) {
+        for (int i = lane; i < a.per_group; i += lanes) mean += p[i].x - ref;
+        mean = ref + lanes_sum(mean, a.group_shift) / static_cast<float>(a.per_group);
+        for (int i = lane; i < a.per_group; i += lanes) {
             const float d = p[i].x - mean;
-            m2 += fmaf(static_cast<float>(rows) * d, d, p[i].y);
+            m2 += fmaf(static_cast<float>(job.rows) * d, d, p[i].y);
         }
-        m2 = group_sum<32>(m2);
-        if (lane == 0) red[g] = make_float2(mean, m2);
+        m2 = lanes_sum(m2, a.group_shift);
+        if (live && lane == 0) (a.cluster == 1 ? out : red)[g] = make_float2(mean, m2);
+    });
+    if (a.cluster == 1) {
+        __syncthreads();
+        return;
     }
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
     const int32_t slab0 = job.cl * a.cluster;
-    float2 *out = a.groups_part + (job.sample * a.clusters + job.cl) * a.groups;
-    for (int g = job.rank * blockDim.x + threadIdx.x; g < a.groups; g += a.cluster * blockDim.x) {
+    const float n_all = values_of(a, slab0, a.cluster);
+    for (int g = job.rank * job.threads + job.tid; g < a.groups; g += a.cluster * job.threads) {
         const float ref = cluster.map_shared_rank(red, 0)[g].x;
         float s1 = 0.f, s2 = 0.f;
         for (int r = 0; r < a.cluster; ++r) {
             const float2 v = cluster.map_shared_rank(red, r)[g];
-            const float n = values_of(a, slab0 + r, slab0 + r + 1), d = n > 0.f ? v.x - ref : 0.f;
+            const float n = values_of(a, slab0 + r, 1), d = n > 0.f ? v.x - ref : 0.f;
             s1 = fmaf(n, d, s1);
             s2 += fmaf(n * d, d, v.y);
         }
-        const float m = s1 / values_of(a, slab0, slab0 + a.cluster);
-        out[g] = make_float2(ref + m, fmaxf(fmaf(-m, s1, s2), 0.f));
+        const float m = s1 / n_all;
+        out[g] = make_float2(ref + m, not_below_zero(fmaf(-m, s1, s2)));
     }
     cluster.sync();  // the others' shared memory has been read; the result is visible to them
 }
 
-// f(e, channel, group) for the elements of a chunk.
-template <int kV, typename F>
-__device__ __forceinline__ void each_channel(const NormArgs &a, int32_t chunk, F f) {
-    int32_t g = chunk * kV / a.per_group, in_group = chunk * kV - g * a.per_group;
-#pragma unroll
-    for (int e = 0; e < kV; ++e) {
-        f(e, chunk * kV + e, g);
-        if (++in_group == a.per_group) in_group = 0, ++g;
-    }
-}
-
-__device__ __forceinline__ void set_half(float2 *v, int e, float x) {
-    if (e & 1) v[e / 2].y = x; else v[e / 2].x = x;
-}
-
-// The rows of a pass 2: a thread's in the slab, and the offset of the last.
-struct LastRows {
-    int32_t left;
-    int64_t last;
-    __device__ LastRows(const NormArgs &a, const Job &job, const Place &at, int64_t row_bytes) {
-        const int32_t rows = job.rows;
-        left = at.active && at.g < rows ? (rows - at.g + at.row_groups - 1) / at.row_groups : 0;
-        last = (job.sample * a.spatial + job.r0 + at.g + static_cast<int64_t>(left - 1) * at.row_groups) * row_bytes;
-    }
-};
-
-// Forward, pass 2.  The first rows are on their way while the statistics of
-// the groups, which lie behind the slots, are put together.
+// Forward, pass 2, the slab's last rows first.  They are on their way before
+// the statistics of the groups, which lie behind the slots.
 template <typename E, int kV, int kAct>
-__device__ void apply_pass(const NormArgs &a, const Job &job, float2 *smem) {
+__device__ void apply_pass(const NormArgs &a, const Job &job, Bars &bars, float2 *smem) {
     using C = Chunk<E, kV>;
-    using In = Stream<C, 1, kSlotsFwd>;
     constexpr int kP = C::kPairs;
-    const Place at(a.columns);
     const int64_t row_bytes = static_cast<int64_t>(a.chunks) * C::kBytes;
-    const LastRows rows(a, job, at, row_bytes);
-    const int32_t step = -static_cast<int32_t>(at.row_groups * row_bytes);
-    float2 *stat = smem + a.ring / 8, *lanes = stat + a.groups;
-    In in;
+    const int64_t base = (job.sample * a.spatial + job.r0) * row_bytes;
+    const uint64_t policy = l2_policy(a.last_use);
+    float2 *stat = smem + a.ring / 8;
+    float w[kV], b[kV];
+    params<E, kV>(a.weight, job.j, a.p32, 1.f, w);
+    params<E, kV>(a.bias, job.j, a.p32, 0.f, b);
+    Stream<C, 1> in(job, bars);
     in.src[0] = a.x;
-    in.start(smem, rows.last + at.j * C::kBytes, step, rows.left);
-    // (mean, rstd) of the sample's groups from its clusters'
-    const int32_t clusters = a.clusters;
-    const float2 *part = a.groups_part + job.sample * clusters * a.groups;
+    in.start(smem, base, row_bytes, min(job.columns, a.chunks), true, policy);
+    wait_for_sums(a);
+    // (mean, rstd) of the sample's groups
+    const float2 *part = a.groups_part + job.sample * a.clusters * a.groups;
     add_parts(
-        lanes, a.groups, clusters,
-        [&](int c, int g) {
-            const float2 v = __ldcg(part + static_cast<int64_t>(c) * a.groups + g);
-            const int32_t s0 = c * a.cluster;
-            const float n = values_of(a, s0, s0 + a.cluster), d = v.x - __ldcg(part + g).x;
+        stat + a.groups, job, a.groups, a.clusters, [&](int g) { return __ldcg(part + g).x; },
+        [&](int c, int g, float ref) {
+            const float2 v = __ldcg(part + c * a.groups + g);
+            const float n = values_of(a, c * a.cluster, a.cluster), d = v.x - ref;
             return make_float2(n * d, fmaf(n * d, d, v.y));
         },
-        [&](int g, float2 t) {
-            const float n = static_cast<float>(a.spatial) * a.per_group, m = t.x / n;
-            const float mean = __ldcg(part + g).x + m;
-            const float rstd = 1.0f / sqrtf(fmaxf(fmaf(-m, t.x, t.y), 0.f) / n + a.eps);
+        [&](int g, float2 t, float ref) {
+            const float n = static_cast<float>(a.spatial) * static_cast<float>(a.per_group), m = t.x / n;
+            const float mean = ref + m;
+            const float rstd = 1.0f / sqrtf(not_below_zero(fmaf(-m, t.x, t.y)) / n + a.eps);
             stat[g] = make_float2(-mean, rstd);
-            if (job.cl == 0 && job.rank == 0 && a.mean) {
+            if (job.r0 == 0 && a.mean) {
                 a.mean[job.sample * a.groups + g] = mean;
                 a.rstd[job.sample * a.groups + g] = rstd;
             }
         });
-    for (int32_t c = at.j; c < a.chunks; c += a.columns) {
-        if (c != at.j) in.start(smem, rows.last + c * C::kBytes, step, rows.left);
-        float2 mean[kP], scale[kP], shift[kP];
-        each_channel<kV>(a, c, [&](int e, int32_t k, int32_t g) {
-            const float2 st = stat[g];
+    for (int32_t c0 = 0; c0 < a.chunks; c0 += job.columns) {
+        const int32_t wide = min(job.columns, a.chunks - c0), c = c0 + min(job.j, wide - 1);
+        if (c0 > 0) {
+            __syncthreads();  // the slots have been read
+            in.start(smem, base + c0 * C::kBytes, row_bytes, wide, true, policy);
+            params<E, kV>(a.weight, c, a.p32, 1.f, w);
+            params<E, kV>(a.bias, c, a.p32, 0.f, b);
+        }
+        float2 mean[kP], scale[kP], shift[kP], st;
+        mean[kP - 1].y = scale[kP - 1].y = shift[kP - 1].y = 0.f;
+        each_channel<kV>(a, c, [&](int32_t g) { st = stat[g]; }, [&](int e) {
             set_half(mean, e, st.x);
-            set_half(scale, e, st.y * param<E>(a.weight, k, a.p32, 1.f));
-            set_half(shift, e, param<E>(a.bias, k, a.p32, 0.f));
+            set_half(scale, e, st.y * w[e]);
+            set_half(shift, e, b[e]);
         });
-        if (kV == 1) mean[0].y = scale[0].y = shift[0].y = 0.f;
         in.run([&](const typename C::Raw (&v)[1], int64_t o) {
             float2 y[kP];
 #pragma unroll
             for (int p = 0; p < kP; ++p)
                 y[p] = act<kAct, C::k32>(__ffma2_rn(C::plus(v[0], p, mean[p]), scale[p], shift[p]));
-            C::store(a.out + o, y);
+            C::store(a.out + o, y, policy);
         });
     }
 }
 
 template <typename E, int kV, int kAct>
-__global__ void __launch_bounds__(kThreadsFwd, 2) norm_forward(NormArgs a) {
+__global__ void __launch_bounds__(384, 2) norm_forward(NormArgs a) {
     extern __shared__ __align__(16) float2 smem[];
-    pdl_prologue();
+    __shared__ __align__(8) uint64_t storage[2 * kStagesFwd];
+    Bars bars = make_bars<kStagesFwd>(storage);
+    start_launch(a);
     const Job job(a);
-    if (job.pass & 1) stats_pass<E, kV>(a, job, smem);
-    if (job.pass & 2) apply_pass<E, kV, kAct>(a, job, smem);
+    if (a.passes & 1) stats_pass<E, kV>(a, job, bars, smem);
+    if (a.passes & 2) apply_pass<E, kV, kAct>(a, job, bars, smem);
 }
 
 // What the backward passes need of a thread's channels.
@@ -591,120 +863,146 @@ template <typename E, int kV>
 struct Channels {
     static constexpr int kP = Chunk<E, kV>::kPairs;
     float2 mean[kP], scale[kP], shift[kP];  // -mean, rstd w, b
-    __device__ void read(const NormArgs &a, int64_t sample, int32_t c) {
-        each_channel<kV>(a, c, [&](int e, int32_t k, int32_t g) {
-            set_half(mean, e, -__ldcg(a.mean + sample * a.groups + g));
-            set_half(scale, e, __ldcg(a.rstd + sample * a.groups + g) * param<E>(a.weight, k, a.p32, 1.f));
-            set_half(shift, e, param<E>(a.bias, k, a.p32, 0.f));
+    __device__ void read(const NormArgs &a, int32_t c) {
+        float w[kV], b[kV];
+        params<E, kV>(a.weight, c, a.p32, 1.f, w);
+        params<E, kV>(a.bias, c, a.p32, 0.f, b);
+        mean[kP - 1].y = scale[kP - 1].y = shift[kP - 1].y = 0.f;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) set_half(scale, e, w[e]), set_half(shift, e, b[e]);
+    }
+    // with the groups' (-mean, rstd)
+    __device__ void set(const NormArgs &a, int32_t c, const float2 *stat) {
+        float2 st;
+        each_channel<kV>(a, c, [&](int32_t g) { st = stat[g]; }, [&](int e) {
+            set_half(mean, e, st.x);
+            set_half(scale, e, st.y * (e & 1 ? scale[e / 2].y : scale[e / 2].x));
         });
-        if (kV == 1) mean[0].y = scale[0].y = shift[0].y = 0.f;
     }
 };
 
 // Backward, pass 1: the sums of dz and dz h a channel, and of d = dz w and d h
 // a group, over the rows of a cluster.
 template <typename E, int kV, int kAct>
-__device__ void sums_pass(const NormArgs &a, const Job &job, float2 *smem) {
+__device__ void sums_pass(const NormArgs &a, const Job &job, Bars &bars, float2 *smem) {
     using C = Chunk<E, kV>;
     constexpr int kP = C::kPairs;
-    float2 *ch = smem, *red = smem + a.channels;
-    float2 *ring = a.columns == a.chunks ? smem : red;
-    const Place at(a.columns);
+    float2 *ch = smem, *red = smem + a.channels, *stat = smem + a.behind / 8;
+    float2 *ring = job.columns == a.chunks ? smem : red;
     const int64_t row_bytes = static_cast<int64_t>(a.chunks) * C::kBytes;
-    const int32_t rows = job.rows;
-    for (int32_t c0 = 0; c0 < a.chunks; c0 += a.columns) {
-        const int32_t wide = min(a.columns, a.chunks - c0);
-        const bool mine = at.active && at.j < wide && at.g < rows;
-        Stream<C, 2, kSlotsBwd> in;
+    for (int g = job.tid; g < a.groups; g += job.threads) {
+        const int64_t at = job.sample * a.groups + g;
+        stat[g] = make_float2(-__ldcg(a.mean + at), __ldcg(a.rstd + at));
+    }
+    __syncthreads();
+    for (int32_t c0 = 0; c0 < a.chunks; c0 += job.columns) {
+        const int32_t wide = min(job.columns, a.chunks - c0);
+        Stream<C, 2> in(job, bars);
         in.src[0] = a.x, in.src[1] = a.gy;
-        in.start(ring, (job.sample * a.spatial + job.r0 + at.g) * row_bytes + (c0 + at.j) * C::kBytes,
-                 static_cast<int32_t>(at.row_groups * row_bytes),
-                 mine ? (rows - at.g + at.row_groups - 1) / at.row_groups : 0);
+        in.start(ring, (job.sample * a.spatial + job.r0) * row_bytes + c0 * C::kBytes, row_bytes, wide, false,
+                 l2_policy(false));
         float2 s1[kP], s2[kP];
 #pragma unroll
         for (int p = 0; p < kP; ++p) s1[p] = s2[p] = both(0.f);
-        if (mine) {
-            Channels<E, kV> t;
-            t.read(a, job.sample, c0 + at.j);
-            in.run([&](const typename C::Raw (&v)[2], int64_t) {
+        Channels<E, kV> t;
+        t.read(a, c0 + min(job.j, wide - 1));
+        t.set(a, c0 + min(job.j, wide - 1), stat);
+        in.run([&](const typename C::Raw (&v)[2], int64_t) {
 #pragma unroll
-                for (int p = 0; p < kP; ++p) {
-                    const float2 xc = C::plus(v[0], p, t.mean[p]);
-                    const float2 dz = __fmul2_rn(
-                        C::wide(v[1], p), act_grad<kAct, C::k32>(__ffma2_rn(xc, t.scale[p], t.shift[p])));
-                    s1[p] = __fadd2_rn(s1[p], dz);
-                    s2[p] = __ffma2_rn(dz, xc, s2[p]);
-                }
-            });
-        }
+            for (int p = 0; p < kP; ++p) {
+                const float2 xc = C::plus(v[0], p, t.mean[p]);
+                const float2 dz = __fmul2_rn(
+                    C::wide(v[1], p), act_grad<kAct, C::k32>(__ffma2_rn(xc, t.scale[p], t.shift[p])));
+                s1[p] = __fadd2_rn(s1[p], dz);
+                s2[p] = __ffma2_rn(dz, xc, s2[p]);
+            }
+        });
         // h = (x - mean) rstd
-        add_row_groups<kV>(red, at, wide, s1, s2, [&](int c, float2 t) {
-            t.y *= __ldcg(a.rstd + job.sample * a.groups + (c0 * kV + c) / a.per_group);
-            ch[c0 * kV + c] = t;
+        add_row_groups<kV>(red, job, c0, wide, s1, s2, [&](int, int c, float2 t) {
+            t.y *= stat[c / a.per_group].y;
+            ch[c] = t;
         });
     }
-    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
-    for (int g = threadIdx.x / 32; g < a.groups; g += warps) {
+    wait_for_sums(a);  // nothing is written before
+    const int64_t place = job.sample * a.clusters + job.cl;
+    float2 *group_out = a.groups_part + place * a.groups;
+    each_group(a, job, [&](int g, int lane, int lanes) {
         float m1 = 0.f, m2 = 0.f;
-        for (int i = lane; i < a.per_group; i += 32) {
-            const int c = g * a.per_group + i;
-            const float w = param<E>(a.weight, c, a.p32, 1.f);
-            m1 = fmaf(w, ch[c].x, m1);
-            m2 = fmaf(w, ch[c].y, m2);
-        }
-        m1 = group_sum<32>(m1);
-        m2 = group_sum<32>(m2);
-        if (lane == 0) red[g] = make_float2(m1, m2);
+        if (g < a.groups)
+            for (int i = lane; i < a.per_group; i += lanes) {
+                const int c = g * a.per_group + i;
+                const float w = param<E>(a.weight, c, a.p32, 1.f);
+                m1 = fmaf(w, ch[c].x, m1);
+                m2 = fmaf(w, ch[c].y, m2);
+            }
+        m1 = lanes_sum(m1, a.group_shift);
+        m2 = lanes_sum(m2, a.group_shift);
+        if (g < a.groups && lane == 0) (a.cluster == 1 ? group_out : red)[g] = make_float2(m1, m2);
+    });
+    const bool weights = a.grad_weight || a.grad_bias;
+    float2 *chan_out = a.chan_part + place * a.channels;
+    if (a.cluster == 1) {
+        if (weights)
+            for (int c = job.tid; c < a.channels; c += job.threads) chan_out[c] = ch[c];
+        __syncthreads();
+        return;
     }
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
-    const int64_t place = job.sample * a.clusters + job.cl;
+    // every block of the cluster ends its share of the values
     auto gather = [&](float2 *mine, float2 *out, int count) {
-        // every block of the cluster ends its share of the values
-        for (int i = job.rank * blockDim.x + threadIdx.x; i < count; i += a.cluster * blockDim.x) {
+        for (int i = job.rank * job.threads + job.tid; i < count; i += a.cluster * job.threads) {
             float2 t = make_float2(0.f, 0.f);
             for (int r = 0; r < a.cluster; ++r) t = __fadd2_rn(t, cluster.map_shared_rank(mine, r)[i]);
             out[i] = t;
         }
     };
-    gather(red, a.groups_part + place * a.groups, a.groups);
-    if (a.grad_weight || a.grad_bias) gather(ch, a.chan_part + place * a.channels, a.channels);
+    gather(red, group_out, a.groups);
+    if (weights) gather(ch, chan_out, a.channels);
     cluster.sync();
 }
 
 // Backward, pass 2: grad_x = rstd w dz - rstd M1 - (x - mean) rstd^2 M2.
 template <typename E, int kV, int kAct>
-__device__ void grad_pass(const NormArgs &a, const Job &job, float2 *smem) {
+__device__ void grad_pass(const NormArgs &a, const Job &job, Bars &bars, float2 *smem) {
     using C = Chunk<E, kV>;
     constexpr int kP = C::kPairs;
-    const Place at(a.columns);
     const int64_t row_bytes = static_cast<int64_t>(a.chunks) * C::kBytes;
-    const LastRows rows(a, job, at, row_bytes);
-    const int32_t step = -static_cast<int32_t>(at.row_groups * row_bytes);
-    float2 *coef = smem + a.ring / 8, *lanes = coef + a.groups;
-    Stream<C, 2, kSlotsBwd> in;
+    const int64_t base = (job.sample * a.spatial + job.r0) * row_bytes;
+    const uint64_t policy = l2_policy(a.last_use);
+    float2 *stat = smem + a.ring / 8, *coef = stat + a.groups;
+    for (int g = job.tid; g < a.groups; g += job.threads) {
+        const int64_t at = job.sample * a.groups + g;
+        stat[g] = make_float2(-__ldcg(a.mean + at), __ldcg(a.rstd + at));
+    }
+    Channels<E, kV> t;
+    t.read(a, job.j);
+    Stream<C, 2> in(job, bars);
     in.src[0] = a.x, in.src[1] = a.gy;
-    in.start(smem, rows.last + at.j * C::kBytes, step, rows.left);
-    const int32_t clusters = a.clusters;
-    const float2 *part = a.groups_part + job.sample * clusters * a.groups;
+    in.start(smem, base, row_bytes, min(job.columns, a.chunks), true, policy);
+    wait_for_sums(a);
+    const float2 *part = a.groups_part + job.sample * a.clusters * a.groups;
     add_parts(
-        lanes, a.groups, clusters,
-        [&](int c, int g) { return __ldcg(part + static_cast<int64_t>(c) * a.groups + g); },
-        [&](int g, float2 t) {
-            const float count = static_cast<float>(a.spatial) * a.per_group;
-            const float rstd = __ldcg(a.rstd + job.sample * a.groups + g);
-            coef[g] = make_float2(-rstd * (t.x / count), -rstd * rstd * (t.y / count));
+        coef + a.groups, job, a.groups, a.clusters, [&](int) { return 0.f; },
+        [&](int c, int g, float) { return __ldcg(part + c * a.groups + g); },
+        [&](int g, float2 v, float) {
+            const float n = static_cast<float>(a.spatial) * static_cast<float>(a.per_group), rstd = stat[g].y;
+            coef[g] = make_float2(-rstd * (v.x / n), -rstd * rstd * (v.y / n));
         });
-    for (int32_t c = at.j; c < a.chunks; c += a.columns) {
-        if (c != at.j) in.start(smem, rows.last + c * C::kBytes, step, rows.left);
-        Channels<E, kV> t;
-        t.read(a, job.sample, c);
-        float2 k1[kP], k2[kP];
-        each_channel<kV>(a, c, [&](int e, int32_t, int32_t g) {
-            set_half(k1, e, coef[g].x);
-            set_half(k2, e, coef[g].y);
+    for (int32_t c0 = 0; c0 < a.chunks; c0 += job.columns) {
+        const int32_t wide = min(job.columns, a.chunks - c0), c = c0 + min(job.j, wide - 1);
+        if (c0 > 0) {
+            __syncthreads();  // the slots have been read
+            in.start(smem, base + c0 * C::kBytes, row_bytes, wide, true, policy);
+            t.read(a, c);
+        }
+        t.set(a, c, stat);
+        float2 k1[kP], k2[kP], m;
+        k1[kP - 1].y = k2[kP - 1].y = 0.f;
+        each_channel<kV>(a, c, [&](int32_t g) { m = coef[g]; }, [&](int e) {
+            set_half(k1, e, m.x);
+            set_half(k2, e, m.y);
         });
-        if (kV == 1) k1[0].y = k2[0].y = 0.f;
         in.run([&](const typename C::Raw (&v)[2], int64_t o) {
             float2 y[kP];
 #pragma unroll
@@ -714,18 +1012,20 @@ __device__ void grad_pass(const NormArgs &a, const Job &job, float2 *smem) {
                     C::wide(v[1], p), act_grad<kAct, C::k32>(__ffma2_rn(xc, t.scale[p], t.shift[p])));
                 y[p] = __ffma2_rn(xc, k2[p], __ffma2_rn(t.scale[p], dz, k1[p]));
             }
-            C::store(a.out + o, y);
+            C::store(a.out + o, y, policy);
         });
     }
 }
 
 template <typename E, int kV, int kAct>
-__global__ void __launch_bounds__(kThreadsBwd, 2) norm_backward(NormArgs a) {
+__global__ void __launch_bounds__(512, 1) norm_backward(NormArgs a) {
     extern __shared__ __align__(16) float2 smem[];
-    pdl_prologue();
+    __shared__ __align__(8) uint64_t storage[2 * kStagesBwd];
+    Bars bars = make_bars<kStagesBwd>(storage);
+    start_launch(a);
     const Job job(a);
-    if (job.pass & 1) sums_pass<E, kV, kAct>(a, job, smem);
-    if (job.pass & 2) grad_pass<E, kV, kAct>(a, job, smem);
+    if (a.passes & 1) sums_pass<E, kV, kAct>(a, job, bars, smem);
+    if (a.passes & 2) grad_pass<E, kV, kAct>(a, job, bars, smem);
 }
 
 // Backward, last: the weight's and bias's gradients over all samples'
@@ -760,11 +1060,8 @@ bool dtype_ok(wgs_dtype d) { return d == WGS_F32 || d == WGS_F16 || d == WGS_BF1
 int64_t bytes_of(wgs_dtype d) { return d == WGS_F32 ? 4 : 2; }
 bool aligned_to(const void *p, int64_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Samples in a batch: as many as pass 2 still finds in L2, counted in
-// elements that both passes read (48 MB of 16-bit ones).
-constexpr int64_t kResident = int64_t{24} << 20;
-// Blocks that fill the GPU: two on each of 152 SMs.
-constexpr int64_t kBlocks = 304;
+// Elements beyond which a call's tensors outgrow L2.
+constexpr int64_t kResident = int64_t{32} << 20;
 // Rows that a slab has at least.
 constexpr int64_t kMinSlabRows = 16;
 // A sample of at most this many elements goes through both passes in one
@@ -773,7 +1070,7 @@ constexpr int64_t kOneLaunch = int64_t{1} << 19;
 
 struct Plan {
     int64_t x_bytes, group_part, chan_part;  // bytes
-    int64_t slabs, cluster, batch;
+    int64_t slabs1, slabs2, cluster;
     bool one_launch;
 };
 
@@ -785,78 +1082,86 @@ bool plan_of(int64_t n, int64_t spatial, int64_t channels, int64_t groups, int64
     if (n > 65535 || spatial > INT32_MAX || channels > kMaxChannels || groups > kMaxGroups) return false;
     if (spatial > 0 && n > (int64_t{1} << 44) / spatial) return false;
     z->x_bytes = n * spatial * channels * elem;
-    z->slabs = z->cluster = z->batch = 1;
+    z->slabs1 = z->slabs2 = z->cluster = 1;
     z->one_launch = true;
     if (n > 0 && spatial > 0) {
         const int64_t most = ceil_div(spatial, kMinSlabRows);
         while (z->cluster < kMaxCluster && 2 * z->cluster <= most) z->cluster *= 2;
-        z->one_launch = spatial * channels <= kOneLaunch || n * z->cluster >= kBlocks;
-        if (z->one_launch) {
-            z->batch = n;
-            z->slabs = z->cluster;
-        } else {
-            if (z->cluster > kPairCluster) z->cluster = kPairCluster;
-            const int64_t fit = kResident / (spatial * channels * (backward ? 2 : 1));
-            z->batch = fit < 1 ? 1 : fit > n ? n : fit;
-            // two batches share a launch when there are several
-            const int64_t want = ceil_div(z->batch < n ? kBlocks / 2 : kBlocks, z->batch);
-            z->slabs = ceil_div(want < most ? want : most, z->cluster) * z->cluster;
+        z->slabs1 = z->slabs2 = z->cluster;
+        z->one_launch = spatial * channels <= kOneLaunch || n * z->cluster >= 304;
+        if (!z->one_launch) {
+            z->cluster = 1;
+            // the launch's blocks over the samples, no more than are resident
+            auto share = [&](int64_t blocks) { return blocks / n < most ? blocks / n : most; };
+            z->slabs1 = share(backward ? WGS_NORM_B1B : WGS_NORM_B1F);
+            z->slabs2 = share(backward ? WGS_NORM_B2B : WGS_NORM_B2F);
         }
     }
-    const int64_t parts = n * (z->slabs / z->cluster);
+    const int64_t parts = n * (z->slabs1 / z->cluster);
     z->group_part = parts * groups * 8;
     z->chan_part = backward ? parts * channels * 8 : 0;
     return true;
 }
 
-// The launches of a call: batches of samples through pass 1 and pass 2.
+// The launches of a call.
 template <typename E, int kV>
 wgs_status run(NormArgs a, const Plan &z, int act, bool backward, int64_t n, cudaStream_t stream) {
     using C = Chunk<E, kV>;
     a.chunks = a.channels / kV;
-    a.slabs = static_cast<int32_t>(z.slabs), a.cluster = static_cast<int32_t>(z.cluster);
-    a.clusters = a.slabs / a.cluster;
-    a.slab_rows = static_cast<int32_t>(a.spatial / a.slabs);
-    a.longer = static_cast<int32_t>(a.spatial % a.slabs);
-    // Shared memory.  Pass 1: the channels' sums, and in one place the slots,
-    // the row groups' sums and the groups'; where one walk covers the row the
-    // channels' lie over the slots too.  Pass 2: the slots, the groups'
-    // values, a pair a thread.
-    const int threads = backward ? kThreadsBwd : kThreadsFwd;
-    a.columns = a.chunks < threads ? a.chunks : threads;
-    a.ring = C::kBytes < 4 ? 0 : threads * C::kBytes * (backward ? 2 * kSlotsBwd : kSlotsFwd);
-    const int red = 8 * (threads * kV > a.groups ? threads * kV : a.groups), ch = 8 * a.channels;
-    const int pass1 = a.columns == a.chunks ? (ch + red > a.ring ? ch + red : a.ring)
-                                            : ch + (red > a.ring ? red : a.ring);
-    const int pass2 = a.ring + 8 * (a.groups + threads);
-    const int smem = pass1 > pass2 ? pass1 : pass2;
+    a.cluster = static_cast<int32_t>(z.cluster);
+    a.clusters = static_cast<int32_t>(z.slabs1 / z.cluster);
+    auto slabs = [&](int64_t count) {
+        return Slabs{static_cast<int32_t>(count), static_cast<int32_t>(a.spatial / count),
+                     static_cast<int32_t>(a.spatial % count)};
+    };
+    a.slabs1 = slabs(z.slabs1), a.slabs2 = slabs(z.slabs2);
+    a.last_use = n * a.spatial * a.channels > kResident;
+    a.group_shift = 0;
+    while (a.group_shift < 5 && 1 << a.group_shift < a.per_group) ++a.group_shift;
     auto kernel = backward ? (act == kSilu       ? norm_backward<E, kV, kSilu>
                               : act == kGeluTanh ? norm_backward<E, kV, kGeluTanh>
                                                  : norm_backward<E, kV, kNone>)
                            : (act == kSilu       ? norm_forward<E, kV, kSilu>
                               : act == kGeluTanh ? norm_forward<E, kV, kGeluTanh>
                                                  : norm_forward<E, kV, kNone>);
-    // Above 48 KB a kernel needs the runtime's leave, which belongs to the
-    // context; asking for the same amount on every call needs no record of it.
-    if (smem > 48 << 10 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) {
-        cudaGetLastError();
-        return WGS_ERR_LAUNCH;
-    }
-    auto part = [&](int64_t i) { return static_cast<int32_t>(i < 0 || i >= n ? 0 : i + z.batch < n ? z.batch : n - i); };
+    auto go = [&](int passes, int most) {
+        const int columns = a.chunks < most ? a.chunks : most;
+        const int row_groups = most / columns;  // more than half of the threads, so whole warps
+        const int threads = columns * row_groups;
+        // Shared memory.  Pass 1: the channels' sums, and in one place the
+        // slots, the row groups' sums and the groups'; where one walk covers
+        // the row the channels' lie over the slots too.  Pass 2: the slots,
+        // the groups' values, a pair a thread.
+        a.ring = C::kBytes < 4 ? 0 : threads * C::kBytes * (backward ? 2 * kRowsBwd * kStagesBwd : kRowsFwd * kStagesFwd);
+        const int red = 8 * (threads * kV > a.groups ? threads * kV : a.groups), ch = 8 * a.channels;
+        const int pass1 = columns == a.chunks ? (ch + red > a.ring ? ch + red : a.ring)
+                                              : ch + (red > a.ring ? red : a.ring);
+        // (the backward's pass 1 keeps the groups' statistics behind that)
+        a.behind = (pass1 + 15) / 16 * 16;
+        const int one = passes & 1 ? a.behind + (backward ? 8 * a.groups : 0) : 0;
+        const int two = passes & 2 ? a.ring + (backward ? 16 : 8) * a.groups + 8 * threads : 0;
+        const int smem = one > two ? one : two;
+        // Above 48 KB a kernel needs the runtime's leave, which belongs to the
+        // context; asking for the same amount on every call needs no record of it.
+        if (smem > 48 << 10 &&
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) {
+            cudaGetLastError();
+            return WGS_ERR_LAUNCH;
+        }
+        a.passes = passes;
+        const int64_t count = passes & 1 ? z.slabs1 : z.slabs2;
+        return launch_clusters(kernel, dim3(static_cast<unsigned>(count), static_cast<unsigned>(n)),
+                               dim3(columns, row_groups), a.cluster, static_cast<size_t>(smem), stream, a);
+    };
+    const int threads1 = backward ? WGS_NORM_T1B : WGS_NORM_T1F, threads2 = backward ? WGS_NORM_T2B : WGS_NORM_T2F;
     wgs_status st = WGS_OK;
-    a.passes = z.one_launch ? 3 : 0;
-    for (int64_t i = 0; i < (z.one_launch ? n : n + z.batch) && st == WGS_OK; i += z.batch) {
-        a.first1 = i, a.n1 = part(i);
-        a.first2 = i - z.batch, a.n2 = part(i - z.batch);
-        if (z.one_launch) a.n2 = 0;
-        const unsigned grid = static_cast<unsigned>((a.n1 + a.n2) * z.slabs);
-        if (grid == 0) continue;
-        st = launch_clusters(kernel, dim3(grid), dim3(threads), a.cluster, static_cast<size_t>(smem), stream, a);
+    if (n > 0) {
+        st = go(z.one_launch ? 3 : 1, threads1);
+        if (st == WGS_OK && !z.one_launch) st = go(2, threads2);
     }
     if (st == WGS_OK && backward && (a.grad_weight || a.grad_bias))
         st = launch(norm_params<E>, dim3(static_cast<unsigned>(ceil_div(a.channels, 32))), dim3(1024), 0,
-                    stream, a, n * (z.slabs / z.cluster));
+                    stream, a, n * a.clusters);
     return st;
 }
 
@@ -884,6 +1189,19 @@ wgs_status run_dtype(const NormArgs &a, const Plan &z, wgs_act act, wgs_dtype dt
 }  // namespace
 
 }  // namespace wgs
+
+// As bias_mask_error_take, for the group norm's error word.
+wgs_status wgs::group_norm_error_take(unsigned int *seen, cudaStream_t stream) {
+    static const unsigned int cleared = 0;
+    if (cudaMemcpyFromSymbolAsync(seen, g_norm_error, sizeof(*seen), 0, cudaMemcpyDeviceToHost,
+                                  stream) != cudaSuccess ||
+        cudaMemcpyToSymbolAsync(g_norm_error, &cleared, sizeof(cleared), 0,
+                                cudaMemcpyHostToDevice, stream) != cudaSuccess) {
+        cudaGetLastError();  // clear this thread's error
+        return WGS_ERR_CUDA;
+    }
+    return WGS_OK;
+}
 
 using namespace wgs;
 

@@ -586,7 +586,7 @@ extern "C" wgs_status residual_add_norm_gather_bf16(const void *residual, const 
 extern "C" wgs_status wgs_check_error(cudaStream_t stream) {
     // The error words are read and cleared by symbol, so each copy resolves
     // the word in the context current at this call.
-    unsigned int seen = 0, seen_mask = 0, seen_bucket = 0;
+    unsigned int seen = 0, seen_mask = 0, seen_bucket = 0, seen_norm = 0;
     static const unsigned int cleared = 0;
     if (cudaMemcpyFromSymbolAsync(&seen, g_index_error, sizeof(seen), 0, cudaMemcpyDeviceToHost,
                                   stream) != cudaSuccess ||
@@ -596,11 +596,13 @@ extern "C" wgs_status wgs_check_error(cudaStream_t stream) {
         return WGS_ERR_CUDA;
     }
     if (bias_mask_error_take(&seen_mask, stream) != WGS_OK ||
-        position_bias_error_take(&seen_bucket, stream) != WGS_OK)
+        position_bias_error_take(&seen_bucket, stream) != WGS_OK ||
+        group_norm_error_take(&seen_norm, stream) != WGS_OK)
         return WGS_ERR_CUDA;
     if (cudaStreamSynchronize(stream) != cudaSuccess) {
         cudaGetLastError();
         return WGS_ERR_CUDA;
     }
+    if (seen_norm) return WGS_ERR_LAUNCH;
     return (seen | seen_mask | seen_bucket) ? WGS_ERR_INDEX : WGS_OK;
 }
