@@ -385,6 +385,7 @@ wgs_status position_bias(const void *table, const int32_t *bucket, void *bias, i
  *             of another type adds to no gradient and sets the error word.
  *   grad_table  [n_types, n_buckets, heads] of table_dtype (WGS_F32, or
  *             `dtype`); every entry is written, 0 where nothing is added.
+ * heads * n_buckets must be below 2^26 (else WGS_ERR_SHAPE).
  *   workspace at least wgs_position_bias_bwd_workspace_bytes(...) bytes,
  *             16-byte aligned, disjoint from the tensors; its contents on
  *             entry do not matter.  Calls that overlap on the GPU need

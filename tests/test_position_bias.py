@@ -121,12 +121,12 @@ def _plan_parts(plan):
     assert w[:5].tolist() == [0x57425031, plan.n_pairs, plan.n_buckets, tiles, plan.n_slots]
     at = 8
     parts = []
-    for n in (tiles + 1, plan.n_slots, plan.n_slots, plan.n_buckets + 1):
+    for n in (tiles + 1, 2 * plan.n_slots, plan.n_buckets + 1):
         parts.append(w[at:at + n])
         at += up(n)
     order = w[at:].view(np.uint16)
     assert order.size == tiles * TILE
-    return parts + [order]
+    return parts[0], parts[1][::2], parts[1][1::2], parts[2], order
 
 
 def _maps():

@@ -10,9 +10,8 @@
 // int32 words, every section starting on a multiple of four words:
 //   header[8]              kPlanMagic, n_pairs, n_buckets, n_tiles, n_slots, 0...
 //   tile_slot[n_tiles + 1] first slot of each tile
-//   slot_span[n_slots]     first entry of the slot in its tile's order, and
-//                          the number of entries << 16
-//   slot_dest[n_slots]     its destination
+//   slot[n_slots]          two words: the slot's first entry in its tile's
+//                          order and the number of entries << 16; its destination
 //   bucket_dest[n_buckets + 1]  first destination of each bucket
 //   order                  uint16 [n_tiles * kPlanTile]: per tile, the
 //                          tile's pairs grouped by bucket, as offsets into it
@@ -27,7 +26,7 @@ constexpr int32_t kPlanTile = 4096;
 constexpr int32_t kPlanHeader = 8;
 
 struct PlanLayout {
-    int64_t tile_slot, slot_span, slot_dest, bucket_dest, order, words;
+    int64_t tile_slot, slot, bucket_dest, order, words;
 };
 
 inline int64_t plan_round4(int64_t v) { return (v + 3) / 4 * 4; }
@@ -38,9 +37,8 @@ inline PlanLayout plan_layout(int64_t n_pairs, int64_t n_buckets, int64_t n_slot
     const int64_t n_tiles = ceil_tiles(n_pairs);
     PlanLayout p;
     p.tile_slot = kPlanHeader;
-    p.slot_span = p.tile_slot + plan_round4(n_tiles + 1);
-    p.slot_dest = p.slot_span + plan_round4(n_slots);
-    p.bucket_dest = p.slot_dest + plan_round4(n_slots);
+    p.slot = p.tile_slot + plan_round4(n_tiles + 1);
+    p.bucket_dest = p.slot + plan_round4(2 * n_slots);
     p.order = p.bucket_dest + plan_round4(n_buckets + 1);
     p.words = p.order + n_tiles * (kPlanTile / 2);
     return p;

@@ -169,8 +169,8 @@ extern "C" wgs_status wgs_build_bucket_plan(const int32_t *bucket_host, int64_t 
         const int32_t head[5] = {wgs::kPlanMagic, static_cast<int32_t>(n_pairs), n_buckets,
                                  static_cast<int32_t>(n_tiles), static_cast<int32_t>(slots)};
         std::memcpy(plan_host, head, sizeof(head));
-        int32_t *tile_slot = plan_host + at.tile_slot, *span = plan_host + at.slot_span;
-        int32_t *dest = plan_host + at.slot_dest, *bucket_dest = plan_host + at.bucket_dest;
+        int32_t *tile_slot = plan_host + at.tile_slot, *record = plan_host + at.slot;
+        int32_t *bucket_dest = plan_host + at.bucket_dest;
         uint16_t *order = reinterpret_cast<uint16_t *>(plan_host + at.order);
 
         int64_t slot = 0;
@@ -188,8 +188,8 @@ extern "C" wgs_status wgs_build_bucket_plan(const int32_t *bucket_host, int64_t 
             for (int32_t b : mine) {
                 const size_t k = static_cast<size_t>(b);
                 start[k] = at_entry;
-                span[slot] = at_entry | (count[k] << 16);
-                dest[slot] = b;  // its bucket for now
+                record[2 * slot] = at_entry | (count[k] << 16);
+                record[2 * slot + 1] = b;  // its bucket for now
                 ++bucket_dest[k + 1];
                 at_entry += count[k];
                 ++slot;
@@ -203,7 +203,7 @@ extern "C" wgs_status wgs_build_bucket_plan(const int32_t *bucket_host, int64_t 
         tile_slot[n_tiles] = static_cast<int32_t>(slot);
         for (size_t b = 0; b < nb; ++b) bucket_dest[b + 1] += bucket_dest[b];
         std::vector<int32_t> next(bucket_dest, bucket_dest + nb);
-        for (int64_t s = 0; s < slot; ++s) dest[s] = next[static_cast<size_t>(dest[s])]++;
+        for (int64_t s = 0; s < slot; ++s) record[2 * s + 1] = next[static_cast<size_t>(record[2 * s + 1])]++;
         return WGS_OK;
     } catch (const std::bad_alloc &) {
         return WGS_ERR_TOO_LARGE;

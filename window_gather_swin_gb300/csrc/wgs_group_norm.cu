@@ -78,46 +78,6 @@ enum : int { kNone = 0, kSilu = 1, kGeluTanh = 2 };
 
 // ------------------------------------------------------------ pairs, chunks --
 
-// How L2 keeps lines: as any others, or given up before them.
-__device__ __forceinline__ uint64_t l2_policy(bool first_out) {
-    uint64_t p;
-    if (first_out)
-        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-    else
-        asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-
-// mbarriers of a block's own bulk copies.
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-// Wait for the end of phase `parity`: a copy of this block, or its own warps'
-// arrivals, which always come.  The limit (far beyond any copy's time) only
-// keeps a fault from hanging the GPU; it is reported.
-__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity) {
-    uint32_t done = 0;
-    for (int tries = 0; tries < 1 << 22; ++tries) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-        if (done) return;
-    }
-    atomicOr(&g_norm_error, 1u);
-}
-__device__ __forceinline__ void bulk_copy(uint32_t to, const char *from, uint32_t bytes, uint32_t bar,
-                                          uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
-        ::"r"(to), "l"(from), "r"(bytes), "r"(bar), "l"(policy) : "memory");
-}
-
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // kV neighbouring elements in one register value, handled as pairs (a single
@@ -377,6 +337,9 @@ struct Bulk {
     uint64_t policy;
 
     __device__ Bulk(const Job &job_, Bars &bars_) : job(job_), bars(bars_) {}
+    __device__ static void wait(uint32_t bar, uint32_t parity) {
+        if (!bar_wait(bar, parity)) atomicOr(&g_norm_error, 1u);
+    }
     __device__ uint32_t stage_bytes() const { return job.threads * C::kBytes * kTensors * kRows; }
     __device__ int32_t stage_rows() const { return job.row_groups * kRows; }
 
@@ -420,10 +383,10 @@ struct Bulk {
             if (job.tid == 0 && i + kStages - 1 < count) {
                 // into the slot that was read last, when all warps have
                 const int free = bars.stage == 0 ? kStages - 1 : bars.stage - 1;
-                if (bars.used) bar_wait(bars.empty + 8 * free, bars.stage == 0 ? bars.phase ^ 1 : bars.phase);
+                if (bars.used) wait(bars.empty + 8 * free, bars.stage == 0 ? bars.phase ^ 1 : bars.phase);
                 copy(i + kStages - 1, free);
             }
-            bar_wait(bars.full + 8 * bars.stage, bars.phase);
+            wait(bars.full + 8 * bars.stage, bars.phase);
             const uint32_t slot = ring + bars.stage * stage_bytes() + job.tid * C::kBytes;
             auto load = [&](int u, typename C::Raw (&v)[kTensors]) {
 #pragma unroll

@@ -252,14 +252,16 @@ wgs_status launch_expand(ExpandArgs a, int32_t n_types, cudaStream_t stream) {
 // --------------------------------------------------------------- backward --
 
 struct GradArgs {
-    const void *grad;         // [n_win, heads, n_pairs]
+    const char *grad;         // [n_win, heads, n_pairs]
+    int64_t grad_bytes;
     const int32_t *plan;      // wgs_bucket_plan.h
     const int32_t *win_type;  // [n_win] or NULL
     float *partial;           // [slabs, n_types, heads, n_slots]
     void *table;              // grad_table [n_types, n_buckets, heads]
     PlanLayout at;
-    int64_t n_win, n_pairs;
-    int32_t heads, n_types, n_buckets, n_tiles, n_slots, slabs;
+    int64_t n_pairs;
+    int32_t n_win, heads, n_types, n_buckets, n_tiles, n_slots, slabs;
+    int32_t units;            // n_tiles * n_types * slabs * heads
 };
 
 // The plan's header against the sizes of the call (a plan of another map
@@ -269,220 +271,377 @@ __device__ __forceinline__ bool plan_matches(const GradArgs &a) {
            a.plan[3] == a.n_tiles && a.plan[4] == a.n_slots;
 }
 
-constexpr int kListed = 1024;  // windows looked over at a time
+// The first of `count` things of the i-th of `parts` equal shares.
+__device__ __forceinline__ int32_t share_start(int32_t count, int32_t parts, int32_t i) {
+    return count / parts * i + min(i, count % parts);
+}
 
-// Pass 1: a block takes one tile of pairs of one (slab of windows, type,
-// head).  It adds the windows' gradients pair by pair in FP32 registers,
-// puts the sums into shared memory and adds them there by slot, LANES
-// neighbouring lanes a slot.  Every gradient is read once, 16 bytes a load;
-// what leaves is one value per slot.  The order of all additions is fixed by
-// the sizes and the plan.
-template <typename E, bool kVec, int LANES>
-__global__ void __launch_bounds__(kThreads, 4) bias_grad_tiles(GradArgs a) {
-    constexpr bool k32 = std::is_same<E, F32>::value;
-    constexpr int kN = kVec ? (k32 ? 4 : 8) : 1;        // elements of a load
-    constexpr int kOwn = kPlanTile / (kThreads * kN);   // loads a window
-    constexpr int kAhead = kVec ? 8 / kOwn : 1;         // windows in flight
-    __shared__ __align__(16) float sums[kPlanTile];
-    __shared__ __align__(16) uint16_t order[kPlanTile];
-    __shared__ int32_t list[kListed];
-    __shared__ int32_t warp_count[kThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_prologue();
-    uint32_t blk = blockIdx.x;
-    const int32_t tile = static_cast<int32_t>(blk % a.n_tiles);
-    blk /= a.n_tiles;
-    const int32_t head = static_cast<int32_t>(blk % a.heads);
-    blk /= a.heads;
-    const int32_t type = static_cast<int32_t>(blk % a.n_types);
-    const int32_t slab = static_cast<int32_t>(blk / a.n_types);
-    if (!plan_matches(a)) {
-        if (tid == 0) atomicOr(&g_bucket_error, 1u);
-        return;
+// A unit of pass 1: a tile of pairs of one type, slab of windows and head,
+// heads first, so that neighbouring units read the same part of the plan and
+// list the same windows.
+struct Unit {
+    int32_t tile, type, slab, head;
+    __device__ Unit(const GradArgs &a, int32_t u) {
+        head = u % a.heads;
+        u /= a.heads;
+        slab = u % a.slabs;
+        u /= a.slabs;
+        type = u % a.n_types;
+        tile = u / a.n_types;
     }
-    const int64_t p0 = static_cast<int64_t>(tile) * kPlanTile;
-    const int32_t len = static_cast<int32_t>(min(a.n_pairs - p0, static_cast<int64_t>(kPlanTile)));
-    float acc[kOwn * kN];
-#pragma unroll
-    for (int i = 0; i < kOwn * kN; ++i) acc[i] = 0.f;
+};
 
-    const int64_t stride = a.heads * a.n_pairs;  // elements from window to window
-    const char *src = static_cast<const char *>(a.grad) + (head * a.n_pairs + p0) * kBytes<E>;
-    // the gradients of windows win(0) ... win(count - 1)
-    auto add = [&](int count, auto win) {
-        int i = 0;
-        if constexpr (kVec) {
-            for (; i + kAhead <= count; i += kAhead) {
-                uint4 v[kAhead][kOwn];
+constexpr int kAdders = 256;                  // threads that add
+constexpr int kGradThreads = kAdders + 32;    // and a warp that copies
+constexpr int kListed = 1024;                 // windows looked over at a time
+template <typename E>
+constexpr int kGradStages = std::is_same<E, F32>::value ? 4 : 6;
+template <typename E>
+constexpr int kStageBytes = kPlanTile * kBytes<E> + 16;  // a tile that starts between 16-byte borders
+
+// What the copying warp says of a stage.
+constexpr int kData = 8, kDirect = 16, kEnd = 32;  // | elements before the tile's first (0 ... 7)
+
+template <typename E>
+struct GradShared {
+    alignas(16) char stage[kGradStages<E>][kStageBytes<E>];
+    alignas(16) float sums[kPlanTile];
+    alignas(16) uint16_t order[kPlanTile];
+    int32_t list[kListed];
+    int32_t said[kGradStages<E>];    // of the stage's window, see kData
+    int32_t window[kGradStages<E>];
+    alignas(8) uint64_t full[kGradStages<E>], empty[kGradStages<E>];
+};
+
+// The slot of the ring that a side of it is at.
+template <int kStages>
+struct RingPlace {
+    int stage = 0;
+    uint32_t phase = 0;
+    bool wrapped = false;
+    __device__ void next() {
+        if (++stage == kStages) stage = 0, phase ^= 1, wrapped = true;
+    }
+};
+
+__device__ __forceinline__ void must_wait(const uint64_t *bar, uint32_t parity) {
+    if (!bar_wait(shared_address(bar), parity)) atomicOr(&g_bucket_error, 1u);
+}
+
+// The copying warp: the tiles of each unit's windows into the ring, in order.
+template <typename E>
+__device__ void copy_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int32_t u1, int lane) {
+    constexpr int kES = kBytes<E>;
+    RingPlace<kGradStages<E>> ring;
+    const uint64_t policy = l2_policy(true);
+    const char *end = a.grad + a.grad_bytes;
+    int32_t listed_type = -1, listed_slab = -1, listed = 0;
+    // by lane 0: the next stage, w < 0 for a unit without windows
+    auto say = [&](const Unit &u, int32_t w, bool last) {
+        if (ring.wrapped) must_wait(&sh.empty[ring.stage], ring.phase ^ 1);
+        const uint32_t bar = shared_address(&sh.full[ring.stage]);
+        int said = last ? kEnd : 0;
+        uint32_t bytes = 0;
+        const char *from = nullptr;
+        if (w >= 0) {
+            said |= kData;
+            const int64_t p0 = static_cast<int64_t>(u.tile) * kPlanTile;
+            const int64_t len = min(a.n_pairs - p0, static_cast<int64_t>(kPlanTile));
+            const char *first = a.grad + ((static_cast<int64_t>(w) * a.heads + u.head) * a.n_pairs + p0) * kES;
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(first) & ~uintptr_t{15};
+            const uintptr_t hi = (reinterpret_cast<uintptr_t>(first + len * kES) + 15) & ~uintptr_t{15};
+            // a tile at the tensor's ends, whose 16-byte lines hold other bytes too, is read directly
+            if (lo < reinterpret_cast<uintptr_t>(a.grad) || hi > reinterpret_cast<uintptr_t>(end)) {
+                said |= kDirect;
+            } else {
+                said |= static_cast<int>((reinterpret_cast<uintptr_t>(first) - lo) / kES);
+                from = reinterpret_cast<const char *>(lo);
+                bytes = static_cast<uint32_t>(hi - lo);
+            }
+        }
+        sh.said[ring.stage] = said;
+        sh.window[ring.stage] = w;
+        if (bytes) {
+            bar_expect(bar, bytes);
+            bulk_copy(shared_address(sh.stage[ring.stage]), from, bytes, bar, policy);
+        } else {
+            bar_arrive(bar);
+        }
+    };
+    for (int32_t i = u0; i < u1; ++i) {
+        const Unit u(a, i);
+        const int32_t w0 = share_start(a.n_win, a.slabs, u.slab), w1 = share_start(a.n_win, a.slabs, u.slab + 1);
+        int32_t pending = -1;  // the last window found so far
+        auto found = [&](int32_t w) {
+            if (pending >= 0) {
+                if (lane == 0) say(u, pending, false);
+                ring.next();
+            }
+            pending = w;
+        };
+        if (!a.win_type) {
+            if (u.type == 0)
+                for (int32_t w = w0; w < w1; ++w) found(w);
+        } else {
+            const bool kept = listed_type == u.type && listed_slab == u.slab && w1 - w0 <= kListed;
+            for (int32_t w = w0; w < w1; w += kListed) {
+                if (!kept) {
+                    // the windows of this type among the next kListed, in order
+                    constexpr int kBatch = 8;
+                    listed = 0;
+                    for (int32_t part = 0; part < min(kListed, w1 - w); part += 32 * kBatch) {
+                        int32_t t[kBatch];
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const uint4 *q = reinterpret_cast<const uint4 *>(src + win(i + u) * stride * kBytes<E>);
+                        for (int k = 0; k < kBatch; ++k) {
+                            const int32_t at = w + part + 32 * k + lane;
+                            t[k] = at < w1 ? __ldg(a.win_type + at) : u.type - 1;
+                            if (at < w1 && (t[k] < 0 || t[k] >= a.n_types)) atomicOr(&g_bucket_error, 1u);
+                        }
 #pragma unroll
-                    for (int k = 0; k < kOwn; ++k)
-                        if ((tid + k * kThreads) * kN < len) v[u][k] = ld_stream(q + tid + k * kThreads);
-                        else v[u][k] = make_uint4(0u, 0u, 0u, 0u);
+                        for (int k = 0; k < kBatch; ++k) {
+                            const int32_t at = w + part + 32 * k + lane;
+                            const bool hit = at < w1 && t[k] == u.type;
+                            const unsigned hits = __ballot_sync(0xffffffffu, hit);
+                            if (hit) sh.list[listed + __popc(hits & ((1u << lane) - 1u))] = at;
+                            listed += __popc(hits);
+                        }
+                    }
+                    __syncwarp();
+                    listed_type = u.type, listed_slab = u.slab;
                 }
+                for (int32_t k = 0; k < listed; ++k) found(sh.list[k]);
+                __syncwarp();
+            }
+        }
+        if (lane == 0) say(u, pending, true);
+        ring.next();
+    }
+}
+
+// The adding warps: a unit's windows pair by pair into FP32 registers, the
+// sums into shared memory, and there slot by slot, LANES neighbouring lanes a
+// slot.
+template <typename E, bool kVec, int LANES>
+__device__ void add_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int32_t u1) {
+    constexpr bool k32 = std::is_same<E, F32>::value;
+    constexpr int kN = kVec ? (k32 ? 4 : 8) : 1;       // neighbouring pairs of a thread
+    constexpr int kOwn = kPlanTile / (kAdders * kN);   // runs of them
+    const int tid = threadIdx.x;
+    auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kAdders) : "memory"); };
+    RingPlace<kGradStages<E>> ring;
+    int32_t tile = -1;
+    for (int32_t i = u0; i < u1; ++i) {
+        const Unit u(a, i);
+        const int64_t p0 = static_cast<int64_t>(u.tile) * kPlanTile;
+        const int32_t len = static_cast<int32_t>(min(a.n_pairs - p0, static_cast<int64_t>(kPlanTile)));
+        if (u.tile != tile) {
+            tile = u.tile;
+            const uint4 *oq = reinterpret_cast<const uint4 *>(a.plan + a.at.order) + tile * (kPlanTile / 8);
+            for (int k = tid; k < kPlanTile / 8; k += kAdders) reinterpret_cast<uint4 *>(sh.order)[k] = __ldg(oq + k);
+        }
+        float acc[kOwn * kN];
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u)
+        for (int k = 0; k < kOwn * kN; ++k) acc[k] = 0.f;
+        int said;
+        do {
+            must_wait(&sh.full[ring.stage], ring.phase);
+            said = sh.said[ring.stage];
+            const char *at = sh.stage[ring.stage];
+            if (said & kDirect) {
+                const int64_t first = (static_cast<int64_t>(sh.window[ring.stage]) * a.heads + u.head) * a.n_pairs + p0;
 #pragma unroll
-                    for (int k = 0; k < kOwn; ++k)
+                for (int k = 0; k < kOwn; ++k)
+#pragma unroll
+                    for (int j = 0; j < kN; ++j) {
+                        const int e = (tid + k * kAdders) * kN + j;
+                        if (e < len) acc[k * kN + j] += load1<E>(a.grad, first + e);
+                    }
+            } else if (said & kData) {
+                if constexpr (kVec) {
+#pragma unroll
+                    for (int k = 0; k < kOwn; ++k) {
+                        // a short tile's end adds what an earlier one left: no slot names it
+                        const uint4 v = reinterpret_cast<const uint4 *>(at)[tid + k * kAdders];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const uint32_t w = word(v[u][k], j);
                             if constexpr (k32) {
-                                acc[k * 4 + j] += __uint_as_float(w);
+                                acc[k * 4 + j] += __uint_as_float(word(v, j));
                             } else {
                                 float *s = acc + k * 8 + 2 * j;
-                                const float2 r = E::widen_add2(w, make_float2(s[0], s[1]));
+                                const float2 r = E::widen_add2(word(v, j), make_float2(s[0], s[1]));
                                 s[0] = r.x, s[1] = r.y;
                             }
                         }
-            }
-        }
-        for (; i < count; ++i) {
-            const char *q = src + win(i) * stride * kBytes<E>;
+                    }
+                } else {
+                    const char *q = at + ((said & 7) + tid) * kBytes<E>;
 #pragma unroll
-            for (int k = 0; k < kOwn; ++k) {
-                const int e = (tid + k * kThreads) * kN;
-                if (e < len)
-#pragma unroll
-                    for (int j = 0; j < kN; ++j) acc[k * kN + j] += load1<E>(q, e + j);
-            }
-        }
-    };
-    const int64_t w0 = a.n_win * slab / a.slabs, w1 = a.n_win * (slab + 1) / a.slabs;
-    if (!a.win_type) {
-        if (type == 0)
-            for (int64_t w = w0; w < w1; w += kListed)
-                add(static_cast<int>(min(w1 - w, static_cast<int64_t>(kListed))),
-                    [&](int i) { return w + i; });
-    } else {
-        for (int64_t w = w0; w < w1; w += kListed) {
-            // the windows of this type among the next kListed, in order
-            int found = 0;
-            for (int part = 0; part < kListed && w + part < w1; part += kThreads) {
-                const int64_t mine = w + part + tid;
-                const int32_t t = mine < w1 ? __ldg(a.win_type + mine) : type - 1;
-                const bool hit = mine < w1 && t == type;
-                if (mine < w1 && (t < 0 || t >= a.n_types)) atomicOr(&g_bucket_error, 1u);
-                const unsigned hits = __ballot_sync(0xffffffffu, hit);
-                if (lane == 0) warp_count[warp] = __popc(hits);
-                __syncthreads();
-                int before = found;
-#pragma unroll
-                for (int q = 0; q < kThreads / 32; ++q) {
-                    if (q < warp) before += warp_count[q];
-                    found += warp_count[q];
+                    for (int k = 0; k < kOwn; ++k) acc[k] += load1<E>(q, k * kAdders);
                 }
-                if (hit) list[before + __popc(hits & ((1u << lane) - 1u))] = part + tid;
-                __syncthreads();
             }
-            add(found, [&](int i) { return w + list[i]; });
-            __syncthreads();  // the list is free
-        }
-    }
-
-    // the tile's sums and its order into shared memory
+            __syncwarp();
+            if ((tid & 31) == 0) bar_arrive(shared_address(&sh.empty[ring.stage]));
+            ring.next();
+        } while (!(said & kEnd));
 #pragma unroll
-    for (int k = 0; k < kOwn; ++k)
+        for (int k = 0; k < kOwn; ++k) {
+            if constexpr (kN % 4 == 0) {
 #pragma unroll
-        for (int j = 0; j < kN; ++j) sums[(tid + k * kThreads) * kN + j] = acc[k * kN + j];
-    const uint4 *oq = reinterpret_cast<const uint4 *>(a.plan + a.at.order) + tile * (kPlanTile / 8);
-    for (int i = tid; i < kPlanTile / 8; i += kThreads)
-        reinterpret_cast<uint4 *>(order)[i] = __ldg(oq + i);
-    __syncthreads();
-    const int32_t s0 = max(a.plan[a.at.tile_slot + tile], 0);
-    const int32_t s1 = min(a.plan[a.at.tile_slot + tile + 1], a.n_slots);
-    float *out = a.partial + ((static_cast<int64_t>(slab) * a.n_types + type) * a.heads + head) * a.n_slots;
-    constexpr int kSlots = kThreads / LANES;  // at a time
-    for (int32_t s = s0; s < s1; s += kSlots) {
-        const int32_t mine = s + tid / LANES;
-        float v = 0.f;
-        if (mine < s1) {
-            const uint32_t span = static_cast<uint32_t>(__ldg(a.plan + a.at.slot_span + mine));
-            const int begin = span & 0xffffu, end = min(begin + static_cast<int>(span >> 16), kPlanTile);
-            for (int k = begin + tid % LANES; k < end; k += LANES)
-                v += sums[order[k] & (kPlanTile - 1)];
+                for (int j = 0; j < kN; j += 4)
+                    *reinterpret_cast<float4 *>(sh.sums + (tid + k * kAdders) * kN + j) =
+                        make_float4(acc[k * kN + j], acc[k * kN + j + 1], acc[k * kN + j + 2], acc[k * kN + j + 3]);
+            } else {
+                sh.sums[tid + k * kAdders] = acc[k];
+            }
         }
-        v = group_sum<LANES>(v);
-        if (mine < s1 && tid % LANES == 0) {
-            const int32_t d = __ldg(a.plan + a.at.slot_dest + mine);
-            if (d >= 0 && d < a.n_slots) out[d] = v;
+        meet();
+        const int32_t s0 = max(__ldg(a.plan + a.at.tile_slot + tile), 0);
+        const int32_t s1 = min(__ldg(a.plan + a.at.tile_slot + tile + 1), a.n_slots);
+        float *out = a.partial + ((static_cast<int64_t>(u.slab) * a.n_types + u.type) * a.heads + u.head) * a.n_slots;
+        constexpr int kSlots = kAdders / LANES;  // at a time
+        for (int32_t s = s0; s < s1; s += kSlots) {
+            const int32_t mine = s + tid / LANES;
+            float v = 0.f;
+            int2 slot = make_int2(0, -1);
+            if (mine < s1) {
+                slot = __ldg(reinterpret_cast<const int2 *>(a.plan + a.at.slot) + mine);
+                const int begin = slot.x & 0xffff, count = static_cast<int>(static_cast<uint32_t>(slot.x) >> 16);
+                const int last = min(begin + count, kPlanTile);
+#pragma unroll 4
+                for (int k = begin + tid % LANES; k < last; k += LANES) v += sh.sums[sh.order[k] & (kPlanTile - 1)];
+            }
+            v = group_sum<LANES>(v);
+            if (tid % LANES == 0 && slot.y >= 0 && slot.y < a.n_slots) out[slot.y] = v;
         }
+        meet();  // the sums and the order have been read
     }
 }
 
-// Pass 2: LANES lanes a (type, head, bucket) add the bucket's slots over the
-// slabs and round once to the table's format.
-template <typename T, int LANES>
-__global__ void __launch_bounds__(kThreads) bias_grad_table(GradArgs a) {
+// Pass 1.  Two resident blocks an SM share the units out; in each a warp copies
+// the tiles of the units' windows in bulk (TMA) into a ring of stages, ahead
+// across units, and eight warps add them up.  Every gradient is read once, a
+// few of them at the tensor's ends excepted in no 16-byte line of another; what
+// leaves is one value per slot.  The order of all additions is fixed by the
+// sizes and the plan.
+template <typename E, bool kVec, int LANES>
+__global__ void __launch_bounds__(kGradThreads, 2) bias_grad_tiles(GradArgs a) {
+    extern __shared__ __align__(16) char smem[];
+    GradShared<E> &sh = *reinterpret_cast<GradShared<E> *>(smem);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kGradStages<E>; ++i) {
+            bar_init(shared_address(&sh.full[i]), 1);
+            bar_init(shared_address(&sh.empty[i]), kAdders / 32);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
     pdl_prologue();
-    const int64_t total = static_cast<int64_t>(a.n_types) * a.heads * a.n_buckets;
+    if (!plan_matches(a)) {
+        if (threadIdx.x == 0) atomicOr(&g_bucket_error, 1u);
+        return;
+    }
+    const int32_t u0 = share_start(a.units, gridDim.x, blockIdx.x);
+    const int32_t u1 = share_start(a.units, gridDim.x, blockIdx.x + 1);
+    if (threadIdx.x < kAdders)
+        add_units<E, kVec, LANES>(a, sh, u0, u1);
+    else
+        copy_units<E>(a, sh, u0, u1, threadIdx.x - kAdders);
+}
+
+// Pass 2: LANES lanes a (type, bucket, head) add the bucket's slots over the
+// slabs (the lanes share the slabs where there are many, else the slots) and
+// round once to the table's format.  Heads are neighbours, as in the table.
+template <typename T, int LANES, bool kSlabs>
+__global__ void __launch_bounds__(kThreads) bias_grad_table(GradArgs a, int32_t blocks) {
+    pdl_prologue();
     const bool ok = plan_matches(a);
     if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_bucket_error, 1u);
-    const int64_t lane_of = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t i = lane_of / LANES;
-    const int32_t lane = static_cast<int32_t>(lane_of % LANES);
-    const int64_t th = i / a.n_buckets;
-    const int32_t b = static_cast<int32_t>(i - th * a.n_buckets);
+    const int32_t type = blockIdx.x / blocks;
+    const int32_t i = ((blockIdx.x - type * blocks) * kThreads + static_cast<int32_t>(threadIdx.x)) / LANES;
+    const int32_t lane = threadIdx.x % LANES;
+    const int32_t b = i / a.heads, head = i - b * a.heads;
     float v = 0.f;
-    if (ok && i < total) {
+    if (ok && b < a.n_buckets) {
         const int32_t d0 = max(__ldg(a.plan + a.at.bucket_dest + b), 0);
         const int32_t d1 = min(__ldg(a.plan + a.at.bucket_dest + b + 1), a.n_slots);
         const int64_t step = static_cast<int64_t>(a.n_types) * a.heads * a.n_slots;
-        for (int32_t d = d0 + lane; d < d1; d += LANES) {
-            const float *p = a.partial + th * a.n_slots + d;
-#pragma unroll 8
-            for (int32_t s = 0; s < a.slabs; ++s) v += __ldcg(p + s * step);
+        const float *p = a.partial + (static_cast<int64_t>(type) * a.heads + head) * a.n_slots;
+        if constexpr (kSlabs) {
+            for (int32_t d = d0; d < d1; ++d)
+#pragma unroll 4
+                for (int32_t s = lane; s < a.slabs; s += LANES) v += p[s * step + d];
+        } else {
+            for (int32_t s = 0; s < a.slabs; ++s)
+#pragma unroll 4
+                for (int32_t d = d0 + lane; d < d1; d += LANES) v += p[s * step + d];
         }
     }
     v = group_sum<LANES>(v);
-    if (i < total && lane == 0) {
-        const int64_t type = th / a.heads, head = th - type * a.heads;
-        store1<T>(a.table, (type * a.n_buckets + b) * a.heads + head, v);
-    }
+    if (b < a.n_buckets && lane == 0)
+        store1<T>(a.table, (static_cast<int64_t>(type) * a.n_buckets + b) * a.heads + head, v);
 }
 
-// Slabs of windows: enough blocks for five on each of 152 SMs, but about
-// four windows of a type in a slab (a block's slot sums cost about as much
-// as reading two).  Depends on the sizes alone, so results do not depend on
-// the device.
-constexpr int64_t kGradBlocks = 1520;
+// Blocks of pass 1 at most: two on each of 152 SMs.
+constexpr int64_t kGradBlocks = 304;
+// Windows of a type in a slab at least, on average.
 constexpr int64_t kSlabWindows = 4;
 
+// Slabs of windows: the fewest with which the blocks' shares of the units,
+// whole ones, leave at most a tenth of the blocks' time unused.  Depends on the
+// sizes alone, so results do not depend on the device.
 int64_t grad_slabs(int64_t n_win, int64_t heads, int64_t n_types, int64_t n_tiles) {
-    const int64_t units = heads * n_types * (n_tiles > 0 ? n_tiles : 1);
-    int64_t s = ceil_div(kGradBlocks, units);
+    const int64_t base = heads * n_types * (n_tiles > 0 ? n_tiles : 1);
     const int64_t most = n_win / (n_types * kSlabWindows);
-    if (s > most) s = most;
-    return s > 1 ? s : 1;
+    if (base >= 16 * kGradBlocks || most <= 1) return 1;
+    int64_t best = 1;
+    double best_use = 0;
+    for (int64_t s = 1; s <= most && s * base <= 16 * kGradBlocks; ++s) {
+        const int64_t units = s * base;
+        const double use = static_cast<double>(units) / (ceil_div(units, kGradBlocks) * kGradBlocks);
+        if (use > best_use) best_use = use, best = s;
+        if (use >= 0.9) break;
+    }
+    return best;
 }
 
 template <typename E, bool kVec>
-wgs_status launch_tiles(const GradArgs &a, unsigned grid, cudaStream_t stream) {
+wgs_status launch_tiles(const GradArgs &a, cudaStream_t stream) {
     // lanes a slot by the slots' average length
     const int64_t mean = a.n_slots > 0 ? a.n_pairs / a.n_slots : 0;
     auto kernel = mean < 8    ? bias_grad_tiles<E, kVec, 1>
                   : mean < 64 ? bias_grad_tiles<E, kVec, 8>
                               : bias_grad_tiles<E, kVec, 32>;
-    return launch(kernel, dim3(grid), dim3(kThreads), 0, stream, a);
+    // More than 48 KB needs the runtime's leave, which belongs to the context;
+    // asking on every call needs no record of it.
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(sizeof(GradShared<E>))) != cudaSuccess) {
+        cudaGetLastError();
+        return WGS_ERR_LAUNCH;
+    }
+    const unsigned grid = static_cast<unsigned>(a.units < kGradBlocks ? a.units : kGradBlocks);
+    return launch(kernel, dim3(grid), dim3(kGradThreads), sizeof(GradShared<E>), stream, a);
 }
 
 template <typename E>
-wgs_status launch_tiles_any(const GradArgs &a, unsigned grid, cudaStream_t stream) {
+wgs_status launch_tiles_any(const GradArgs &a, cudaStream_t stream) {
     constexpr int n = std::is_same<E, F32>::value ? 4 : 8;
-    return a.n_pairs % n == 0 && aligned16(a.grad) ? launch_tiles<E, true>(a, grid, stream)
-                                                    : launch_tiles<E, false>(a, grid, stream);
+    return a.n_pairs % n == 0 && aligned16(a.grad) ? launch_tiles<E, true>(a, stream)
+                                                    : launch_tiles<E, false>(a, stream);
 }
 
 template <typename T>
 wgs_status launch_table(const GradArgs &a, cudaStream_t stream) {
     const int64_t mean = a.n_slots / a.n_buckets;
-    const int lanes = mean < 8 ? 1 : mean < 64 ? 8 : 32;
-    const int64_t grid = ceil_div(static_cast<int64_t>(a.n_types) * a.heads * a.n_buckets * lanes, kThreads);
-    if (grid > INT32_MAX) return WGS_ERR_SHAPE;
-    auto kernel = lanes == 1 ? bias_grad_table<T, 1> : lanes == 8 ? bias_grad_table<T, 8> : bias_grad_table<T, 32>;
-    return launch(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, a);
+    const bool slabs = a.slabs >= mean;
+    const int64_t most = slabs ? a.slabs : mean;
+    const int lanes = most < 4 ? 1 : most < 64 ? 8 : 32;
+    const int64_t blocks = ceil_div(static_cast<int64_t>(a.heads) * a.n_buckets * lanes, kThreads);
+    if (blocks * a.n_types > INT32_MAX) return WGS_ERR_SHAPE;
+    auto kernel = lanes == 1 ? bias_grad_table<T, 1, true>
+                  : lanes == 8 ? (slabs ? bias_grad_table<T, 8, true> : bias_grad_table<T, 8, false>)
+                               : (slabs ? bias_grad_table<T, 32, true> : bias_grad_table<T, 32, false>);
+    return launch(kernel, dim3(static_cast<unsigned>(blocks * a.n_types)), dim3(kThreads), 0, stream, a,
+                  static_cast<int32_t>(blocks));
 }
 
 // a * b for non-negative a and b, or false past 2^62.
@@ -557,7 +716,8 @@ extern "C" wgs_status position_bias_bwd(const void *grad, const int32_t *plan,
     const int64_t n_tiles = ceil_tiles(n_pairs);
     const int64_t slabs = grad_slabs(n_win, heads, n_types, n_tiles);
     int64_t th, units, grad_bytes, table_bytes, part_bytes;
-    if (!times(n_types, heads, &th) || !times(th * slabs, n_tiles, &units) || units > INT32_MAX ||
+    if (!times(n_types, heads, &th) || !times(heads, n_buckets, &units) || units > INT32_MAX / 32 ||
+        !times(th * slabs, n_tiles, &units) || units > INT32_MAX ||
         !times(n_win * heads, n_pairs * bytes_of(dtype), &grad_bytes) ||
         !times(th, n_buckets * bytes_of(table_dtype), &table_bytes) ||
         !times(th * slabs, n_slots * 4, &part_bytes))
@@ -580,14 +740,15 @@ extern "C" wgs_status position_bias_bwd(const void *grad, const int32_t *plan,
     DeviceInfo dev;
     wgs_status st = current_device(&dev);
     if (st != WGS_OK) return st;
-    GradArgs a = {grad, plan, win_type, static_cast<float *>(workspace), grad_table, at,
-                  n_win, n_pairs, heads, n_types, n_buckets, static_cast<int32_t>(n_tiles),
-                  static_cast<int32_t>(n_slots), static_cast<int32_t>(slabs)};
+    GradArgs a = {static_cast<const char *>(grad), grad_bytes, plan, win_type,
+                  static_cast<float *>(workspace), grad_table, at, n_pairs,
+                  static_cast<int32_t>(n_win), heads, n_types, n_buckets,
+                  static_cast<int32_t>(n_tiles), static_cast<int32_t>(n_slots),
+                  static_cast<int32_t>(slabs), static_cast<int32_t>(units)};
     if (units > 0) {
-        const unsigned grid = static_cast<unsigned>(units);
-        st = dtype == WGS_F32   ? launch_tiles_any<F32>(a, grid, stream)
-             : dtype == WGS_F16 ? launch_tiles_any<Fp16>(a, grid, stream)
-                                : launch_tiles_any<Bf16>(a, grid, stream);
+        st = dtype == WGS_F32   ? launch_tiles_any<F32>(a, stream)
+             : dtype == WGS_F16 ? launch_tiles_any<Fp16>(a, stream)
+                                : launch_tiles_any<Bf16>(a, stream);
         if (st != WGS_OK) return st;
     }
     return table_dtype == WGS_F32   ? launch_table<F32>(a, stream)
