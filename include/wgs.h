@@ -361,7 +361,8 @@ wgs_status window_bias_mask_add(const void *scores, const void *bias, const int3
  *           wgs_build_window_buckets or wgs_build_distance_buckets.
  *   bias    [n_types, heads, n_pairs] of dtype (any wgs_dtype); must not
  *           overlap the inputs (WGS_ERR_ALIAS).
- * n_pairs must be below 2^31 - 4096 (else WGS_ERR_SHAPE).  Pointers need
+ * n_pairs must be below 2^31 - 4096 and heads * n_buckets below 2^26 (else
+ * WGS_ERR_SHAPE).  Pointers need
  * their element's alignment; with n_pairs a multiple of 8 and bucket and
  * bias 16-byte aligned the heads of a bucket are read together (same
  * results). */
@@ -432,8 +433,8 @@ wgs_status wgs_build_distance_buckets(int64_t n_q, int64_t n_k, int64_t q_start,
 /* The plan of a bucket map (host int32 [n_pairs], values in [-1,
  * n_buckets)): for tiles of 4096 pairs, the pairs of each bucket.  Built once
  * per map and copied to the device.  wgs_bucket_plan_words returns its size
- * in int32 words and its slot count (pairs of a tile and a bucket that occurs
- * in it), or -1 for invalid sizes or a value outside [-1, n_buckets), for
+ * in int32 words and its slot count (a bucket's pairs in a tile make a slot or
+ * more), or -1 for invalid sizes or a value outside [-1, n_buckets), for
  * which the builder returns WGS_ERR_SHAPE or WGS_ERR_INDEX.  Host memory
  * only. */
 int64_t wgs_bucket_plan_words(const int32_t *bucket_host, int64_t n_pairs, int32_t n_buckets,

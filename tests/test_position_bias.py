@@ -3,7 +3,7 @@
 
 Tolerance of the gradient.  It is an FP32 sum of gradients in a fixed order:
 windows of a slab one after another, then a slot's pairs, then slots and
-slabs.  With D additions on the longest path and u = 2^-24 its error is at
+slabs over some lanes.  With D additions on the longest path and u = 2^-24 its error is at
 most D u sum|g| (1 + small), and rounding to a 16-bit table adds half a step.
 D <= windows + 4096 (a tile's pairs) + tiles * slabs; 64 slabs bound every
 case here.
@@ -114,19 +114,21 @@ TILE = 4096
 
 
 def _plan_parts(plan):
-    """The sections of a plan by its documented layout."""
+    """The sections of a plan by its documented layout: the lanes' bits and
+    first slots, each bucket's slots, and the order, lane by lane."""
     w = plan.words.cpu().numpy()
     up = lambda v: (v + 3) // 4 * 4
     tiles = -(-plan.n_pairs // TILE)
-    assert w[:5].tolist() == [0x57425031, plan.n_pairs, plan.n_buckets, tiles, plan.n_slots]
+    assert w[:5].tolist() == [0x57425032, plan.n_pairs, plan.n_buckets, tiles, plan.n_slots]
     at = 8
     parts = []
-    for n in (tiles + 1, 2 * plan.n_slots, plan.n_buckets + 1):
+    for n in (tiles * 256, plan.n_buckets + 1, plan.n_slots):
         parts.append(w[at:at + n])
         at += up(n)
-    order = w[at:].view(np.uint16)
-    assert order.size == tiles * TILE
-    return parts[0], parts[1][::2], parts[1][1::2], parts[2], order
+    order = w[at:].view(np.uint16).reshape(tiles, 4, 128, 8).transpose(0, 2, 1, 3).reshape(tiles, TILE)
+    order = order ^ (order >> 5 & 31)      # places of the sums back to pairs
+    lane = parts[0].reshape(tiles, 128, 2)
+    return lane[..., 0].view(np.uint32), lane[..., 1], parts[1], parts[2], order
 
 
 def _maps():
@@ -145,25 +147,30 @@ def _maps():
 def test_plan_inverts_its_map(i):
     bucket, n_buckets = next(itertools.islice(_maps(), i, None))
     plan = wgs.build_bucket_plan(bucket, n_buckets, device="cpu")
-    tile_slot, span, dest, bucket_dest, order = _plan_parts(plan)
+    ends, first_slot, bucket_first, bucket_slot, order = _plan_parts(plan)
     flat = bucket.numpy().reshape(-1)
-    assert sorted(dest.tolist()) == list(range(plan.n_slots))
-    bucket_of = np.searchsorted(bucket_dest, np.arange(plan.n_slots), side="right") - 1
+    assert sorted(bucket_slot.tolist()) == list(range(plan.n_slots))
+    of_slot = np.full(plan.n_slots, -1)
+    for b in range(plan.n_buckets):
+        mine = bucket_slot[bucket_first[b]:bucket_first[b + 1]]
+        assert (np.diff(mine) > 0).all()
+        of_slot[mine] = b
+    # a slot is a run of a lane's entries up to a set bit: each pair once, in
+    # the slot of its bucket, slots numbered along the order
     seen = np.full(flat.size, -1)
-    last = {}
-    for t in range(len(tile_slot) - 1):
-        names = []
-        for s in range(tile_slot[t], tile_slot[t + 1]):
-            b = bucket_of[dest[s]]
-            names.append(b)
-            assert dest[s] > last.get(b, -1)   # a bucket's slots stay in tile order
-            last[b] = dest[s]
-            begin, n = span[s] & 0xffff, span[s] >> 16
-            pairs = t * TILE + order[t * TILE + begin:t * TILE + begin + n].astype(np.int64)
-            assert n > 0 and (np.diff(pairs) > 0).all()
-            assert (seen[pairs] == -1).all()
-            seen[pairs] = b
-        assert len(set(names)) == len(names)
+    expect = 0
+    for t in range(len(ends)):
+        for l in range(128):
+            slot, begin = first_slot[t, l], 0
+            for e in range(32):
+                if not ends[t, l] >> e & 1:
+                    continue
+                assert slot == expect
+                pairs = t * TILE + order[t, 32 * l + begin:32 * l + e + 1].astype(np.int64)
+                assert (np.diff(pairs) > 0).all() and (seen[pairs] == -1).all()
+                seen[pairs] = of_slot[slot]
+                slot, begin, expect = slot + 1, e + 1, expect + 1
+    assert expect == plan.n_slots
     assert np.array_equal(seen, flat)
 
 

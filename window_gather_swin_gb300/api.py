@@ -9,6 +9,7 @@ CPU tensors are rejected.
 from __future__ import annotations
 
 import ctypes
+import math
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -296,6 +297,47 @@ def window_bias_mask_add(scores: torch.Tensor, bias: torch.Tensor,
     return y
 
 
+# The calls below are short next to what Python spends on them, so their
+# checks look first and word a message only when something is wrong.
+
+def _fail(msg: str) -> None:
+    raise RuntimeError(msg)
+
+
+def _given(t: torch.Tensor, name: str, dtype, index: int) -> int:
+    """Device address of t (0 when empty), a contiguous tensor of `dtype` on
+    CUDA device `index`; raises otherwise."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index
+            or not t.is_contiguous()):
+        _cuda(t, name, dtype)
+        _fail(f"all tensors must be on cuda:{index} (got {name} on {t.device})")
+    return t.data_ptr()
+
+
+def _into(out: Optional[torch.Tensor], shape, dtype, device, name: str) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if out.shape != shape:
+        _fail(f"{name} must have shape {tuple(shape)} (got {tuple(out.shape)})")
+    return out
+
+
+def _space(workspace: Optional[torch.Tensor], need, device) -> torch.Tensor:
+    return workspace if workspace is not None else torch.empty(max(need(), 16), dtype=torch.uint8,
+                                                               device=device)
+
+
+def _run(name: str, fn, index: int, *args) -> None:
+    """fn(*args, stream) on device `index`'s current stream."""
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    else:
+        status = fn(*args, _raw_stream(index))
+    if status:
+        _capi.check(name, status)
+
+
 # ------------------------------------------------------- position bias ----
 
 def window_bucket_count(window: Sequence[int], absolute_axes: int = 0) -> int:
@@ -339,21 +381,28 @@ def position_bias(table: torch.Tensor, bucket: torch.Tensor, dtype=None,
     [n_types, n_buckets, heads] (or [n_buckets, heads]: one type), bucket
     int32 [n_q, n_k].  `dtype` is the bias's format, by default out's or the
     table's; the table is float32 or of that format."""
-    _cuda(table, "table")
-    _cuda(bucket, "bucket", torch.int32)
-    _require(table.dim() in (2, 3), "table must be [n_types, n_buckets, heads] or [n_buckets, heads]")
-    _require(bucket.dim() == 2, "bucket must be [n_q, n_k]")
-    n_types = table.shape[0] if table.dim() == 3 else 1
-    n_buckets, heads = table.shape[-2:]
+    if not isinstance(table, torch.Tensor) or not table.is_cuda or not table.is_contiguous():
+        _cuda(table, "table")
+    index = table.get_device()
+    where = _given(bucket, "bucket", torch.int32, index)
+    dims = table.shape
+    if len(dims) not in (2, 3):
+        _fail("table must be [n_types, n_buckets, heads] or [n_buckets, heads]")
+    if bucket.dim() != 2:
+        _fail("bucket must be [n_q, n_k]")
+    n_types = dims[0] if len(dims) == 3 else 1
+    n_buckets, heads = dims[-2:]
     if dtype is None:
         dtype = table.dtype if out is None else out.dtype
-    _require(dtype in _DTYPE, f"dtype must be float32, float16 or bfloat16 (got {dtype})")
-    _require(table.dtype in (torch.float32, dtype),
-             f"table must be float32 or {dtype} (got {table.dtype})")
-    y = _out(out, (n_types, heads) + tuple(bucket.shape), dtype, table.device, "out")
-    _same_device(table, bucket, y)
-    _call("position_bias", _capi.load().position_bias, table.device, _ptr(table), _ptr(bucket),
-          _ptr(y), n_types, heads, bucket.numel(), n_buckets, _DTYPE[table.dtype], _DTYPE[dtype])
+    if dtype not in _DTYPE:
+        _fail(f"dtype must be float32, float16 or bfloat16 (got {dtype})")
+    if table.dtype not in (torch.float32, dtype):
+        _fail(f"table must be float32 or {dtype} (got {table.dtype})")
+    n_q, n_k = bucket.shape
+    y = _into(out, (n_types, heads, n_q, n_k), dtype, table.device, "out")
+    _run("position_bias", _capi.load().position_bias, index, table.data_ptr(), where,
+         _given(y, "out", dtype, index), n_types, heads, n_q * n_k, n_buckets,
+         _DTYPE[table.dtype], _DTYPE[dtype])
     return y
 
 
@@ -405,30 +454,35 @@ def position_bias_bwd(grad: torch.Tensor, plan: BucketPlan,
     grad's.  The fixed-order sums need a workspace of
     position_bias_bwd_workspace_bytes(...) bytes; one is allocated here unless
     the caller passes a uint8 CUDA tensor that large."""
-    _cuda(grad, "grad")
-    _require(grad.dtype in _DTYPE, f"grad must be float32, float16 or bfloat16 (got {grad.dtype})")
-    _require(isinstance(plan, BucketPlan), "plan must come from build_bucket_plan")
-    _cuda(plan.words, "plan", torch.int32)
-    _require(grad.dim() == 4 and tuple(grad.shape[2:]) == plan.shape,
-             f"grad must be [n_win, heads, {plan.shape[0]}, {plan.shape[1]}] (got {tuple(grad.shape)})")
+    if not isinstance(grad, torch.Tensor) or not grad.is_cuda or not grad.is_contiguous():
+        _cuda(grad, "grad")
+    index, kind = grad.get_device(), grad.dtype
+    if kind not in _DTYPE:
+        _fail(f"grad must be float32, float16 or bfloat16 (got {kind})")
+    if not isinstance(plan, BucketPlan):
+        _fail("plan must come from build_bucket_plan")
+    if grad.dim() != 4 or grad.shape[2:] != plan.shape:
+        _fail(f"grad must be [n_win, heads, {plan.shape[0]}, {plan.shape[1]}] (got {tuple(grad.shape)})")
     n_win, heads = grad.shape[:2]
-    _require(int(n_types) >= 0, "n_types must not be negative")
-    _require(dtype in (torch.float32, grad.dtype), f"dtype must be float32 or {grad.dtype} (got {dtype})")
-    ts = [grad, plan.words]
+    if n_types < 0:
+        _fail("n_types must not be negative")
+    if dtype not in (torch.float32, kind):
+        _fail(f"dtype must be float32 or {kind} (got {dtype})")
+    types = 0
     if win_type is not None:
-        _cuda(win_type, "win_type", torch.int32)
-        _require(win_type.numel() == n_win, f"win_type must have {n_win} entries")
-        ts.append(win_type)
-    gt = _out(grad_table, (int(n_types), plan.n_buckets, heads), dtype, grad.device, "grad_table")
-    lib = _capi.load()
-    if workspace is None:
-        need = position_bias_bwd_workspace_bytes(plan, n_win, heads, n_types)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=grad.device)
-    _cuda(workspace, "workspace", torch.uint8)
-    _same_device(*ts, gt, workspace)
-    _call("position_bias_bwd", lib.position_bias_bwd, grad.device, _ptr(grad), _ptr(plan.words),
-          _ptr(win_type), _ptr(gt), _ptr(workspace), workspace.numel(), n_win, heads, plan.n_pairs,
-          plan.n_buckets, plan.n_slots, int(n_types), _DTYPE[grad.dtype], _DTYPE[dtype])
+        types = _given(win_type, "win_type", torch.int32, index)
+        if win_type.numel() != n_win:
+            _fail(f"win_type must have {n_win} entries")
+        if n_win == 0:
+            types = 0
+    gt = _into(grad_table, (n_types, plan.n_buckets, heads), dtype, grad.device, "grad_table")
+    ws = _space(workspace, lambda: position_bias_bwd_workspace_bytes(plan, n_win, heads, n_types),
+                grad.device)
+    _run("position_bias_bwd", _capi.load().position_bias_bwd, index, grad.data_ptr(),
+         _given(plan.words, "plan", torch.int32, index), types,
+         _given(gt, "grad_table", dtype, index), _given(ws, "workspace", torch.uint8, index),
+         ws.numel(), n_win, heads, plan.n_pairs, plan.n_buckets, plan.n_slots, n_types,
+         _DTYPE[kind], _DTYPE[dtype])
     return gt
 
 
@@ -439,28 +493,33 @@ _ACT = {None: _capi.WGS_ACT_NONE, "none": _capi.WGS_ACT_NONE, "silu": _capi.WGS_
 
 
 def _norm_args(x, groups, weight, bias, act):
-    """(n, spatial, channels, param dtype) of checked group-norm arguments."""
-    _cuda(x, "x")
-    _require(x.dtype in _DTYPE, f"x must be float32, float16 or bfloat16 (got {x.dtype})")
-    _require(x.dim() >= 2, "x must be [n, ..., channels]")
-    _require(act in _ACT, f"act must be one of {sorted(k for k in _ACT if k)} or None (got {act!r})")
-    n, channels = x.shape[0], x.shape[-1]
-    _require(channels > 0 and int(groups) > 0 and channels % int(groups) == 0,
-             f"channels ({channels}) must be a multiple of groups ({groups})")
-    spatial = 1
-    for d in x.shape[1:-1]:
-        spatial *= d
-    _require((weight is None) == (bias is None), "weight and bias go together")
-    pt = torch.float32
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _cuda(t, name)
-            _require(t.dtype in (torch.float32, x.dtype),
-                     f"{name} must be float32 or {x.dtype} (got {t.dtype})")
-            _require(tuple(t.shape) == (channels,), f"{name} must have {channels} elements")
-            pt = t.dtype
-    _require(weight is None or weight.dtype == bias.dtype, "weight and bias must have one dtype")
-    return n, spatial, channels, pt
+    """(device index, n, spatial, channels, weight's and bias's addresses,
+    their dtype) of checked group-norm arguments."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or not x.is_contiguous():
+        _cuda(x, "x")
+    if x.dtype not in _DTYPE:
+        _fail(f"x must be float32, float16 or bfloat16 (got {x.dtype})")
+    if act not in _ACT:
+        _fail(f"act must be one of {sorted(k for k in _ACT if k)} or None (got {act!r})")
+    dims = x.shape
+    if len(dims) < 2:
+        _fail("x must be [n, ..., channels]")
+    n, channels = dims[0], dims[-1]
+    if channels <= 0 or groups <= 0 or channels % groups != 0:
+        _fail(f"channels ({channels}) must be a multiple of groups ({groups})")
+    spatial = dims[1] if len(dims) == 3 else 1 if len(dims) == 2 else math.prod(dims[1:-1])
+    index = x.get_device()
+    if weight is None or bias is None:
+        if weight is not bias:
+            _fail("weight and bias go together")
+        return index, n, spatial, channels, 0, 0, torch.float32
+    pt = weight.dtype
+    if pt is not torch.float32 and pt is not x.dtype:
+        _fail(f"weight must be float32 or {x.dtype} (got {pt})")
+    w, b = _given(weight, "weight", pt, index), _given(bias, "bias", pt, index)
+    if weight.shape != (channels,) or bias.shape != (channels,):
+        _fail(f"weight and bias must have {channels} elements")
+    return index, n, spatial, channels, w, b, pt
 
 
 def group_norm_act_workspace_bytes(n: int, spatial: int, channels: int, groups: int) -> int:
@@ -486,19 +545,19 @@ def group_norm_act(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
     group_norm_act_bwd takes (they are left as they are when x is empty).
     A workspace of group_norm_act_workspace_bytes(...) bytes is allocated here
     unless the caller passes a uint8 CUDA tensor that large."""
-    n, spatial, channels, pt = _norm_args(x, groups, weight, bias, act)
-    y = _out(out, x.shape, x.dtype, x.device, "out")
-    m = _out(mean, (n, groups), torch.float32, x.device, "mean")
-    r = _out(rstd, (n, groups), torch.float32, x.device, "rstd")
-    lib = _capi.load()
-    if workspace is None:
-        need = group_norm_act_workspace_bytes(n, spatial, channels, groups)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
-    _cuda(workspace, "workspace", torch.uint8)
-    _same_device(x, *(t for t in (weight, bias) if t is not None), y, m, r, workspace)
-    _call("group_norm_act", lib.group_norm_act, x.device, _ptr(x), _ptr(weight), _ptr(bias),
-          _ptr(y), _ptr(m), _ptr(r), _ptr(workspace), workspace.numel(), n, spatial, channels,
-          int(groups), float(eps), _ACT[act], _DTYPE[x.dtype], _DTYPE[pt])
+    index, n, spatial, channels, w, b, pt = _norm_args(x, groups, weight, bias, act)
+    kind, device = x.dtype, x.device
+    y = torch.empty_like(x) if out is None else _into(out, x.shape, kind, device, "out")
+    if mean is None and rstd is None:
+        m, r = torch.empty((2, n, groups), dtype=torch.float32, device=device).unbind(0)
+    else:
+        m = _into(mean, (n, groups), torch.float32, device, "mean")
+        r = _into(rstd, (n, groups), torch.float32, device, "rstd")
+    ws = _space(workspace, lambda: group_norm_act_workspace_bytes(n, spatial, channels, groups), device)
+    _run("group_norm_act", _capi.load().group_norm_act, index, x.data_ptr(), w, b,
+         _given(y, "out", kind, index), _given(m, "mean", torch.float32, index),
+         _given(r, "rstd", torch.float32, index), _given(ws, "workspace", torch.uint8, index),
+         ws.numel(), n, spatial, channels, groups, eps, _ACT[act], _DTYPE[kind], _DTYPE[pt])
     return y, m, r
 
 
@@ -511,31 +570,31 @@ def group_norm_act_bwd(grad_y: torch.Tensor, x: torch.Tensor, groups: int, mean:
                        workspace: Optional[torch.Tensor] = None):
     """Gradients of group_norm_act.  Returns (grad_x, grad_weight, grad_bias),
     the last two None without weight and bias.  grad_x may be grad_y or x."""
-    n, spatial, channels, pt = _norm_args(x, groups, weight, bias, act)
-    _cuda(grad_y, "grad_y", x.dtype)
-    _require(grad_y.shape == x.shape, "grad_y and x must have the same shape")
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _cuda(t, name, torch.float32)
-        _require(tuple(t.shape) == (n, groups), f"{name} must have shape {(n, groups)}")
-    gx = _out(grad_x, x.shape, x.dtype, x.device, "grad_x")
+    index, n, spatial, channels, w, b, pt = _norm_args(x, groups, weight, bias, act)
+    kind, device = x.dtype, x.device
+    gy = _given(grad_y, "grad_y", kind, index)
+    if grad_y.shape != x.shape:
+        _fail("grad_y and x must have the same shape")
+    m, r = _given(mean, "mean", torch.float32, index), _given(rstd, "rstd", torch.float32, index)
+    if mean.shape != (n, groups) or rstd.shape != (n, groups):
+        _fail(f"mean and rstd must have shape {(n, groups)}")
+    gx = torch.empty_like(x) if grad_x is None else _into(grad_x, x.shape, kind, device, "grad_x")
     gw = gb = None
+    pw = pb = 0
     if weight is not None:
-        gw = _out(grad_weight, weight.shape, pt, x.device, "grad_weight")
-        gb = _out(grad_bias, bias.shape, pt, x.device, "grad_bias")
-    else:
-        _require(grad_weight is None and grad_bias is None,
-                 "grad_weight and grad_bias need weight and bias")
-    lib = _capi.load()
-    if workspace is None:
-        need = group_norm_act_bwd_workspace_bytes(n, spatial, channels, groups)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
-    _cuda(workspace, "workspace", torch.uint8)
-    _same_device(x, grad_y, mean, rstd, *(t for t in (weight, bias, gw, gb) if t is not None), gx,
-                 workspace)
-    _call("group_norm_act_bwd", lib.group_norm_act_bwd, x.device, _ptr(grad_y), _ptr(x),
-          _ptr(weight), _ptr(bias), _ptr(mean), _ptr(rstd), _ptr(gx), _ptr(gw), _ptr(gb),
-          _ptr(workspace), workspace.numel(), n, spatial, channels, int(groups), _ACT[act],
-          _DTYPE[x.dtype], _DTYPE[pt])
+        if grad_weight is None and grad_bias is None:
+            gw, gb = torch.empty((2, channels), dtype=pt, device=device).unbind(0)
+        else:
+            gw = _into(grad_weight, (channels,), pt, device, "grad_weight")
+            gb = _into(grad_bias, (channels,), pt, device, "grad_bias")
+        pw, pb = _given(gw, "grad_weight", pt, index), _given(gb, "grad_bias", pt, index)
+    elif grad_weight is not None or grad_bias is not None:
+        _fail("grad_weight and grad_bias need weight and bias")
+    ws = _space(workspace, lambda: group_norm_act_bwd_workspace_bytes(n, spatial, channels, groups),
+                device)
+    _run("group_norm_act_bwd", _capi.load().group_norm_act_bwd, index, gy, x.data_ptr(), w, b, m, r,
+         _given(gx, "grad_x", kind, index), pw, pb, _given(ws, "workspace", torch.uint8, index),
+         ws.numel(), n, spatial, channels, groups, _ACT[act], _DTYPE[kind], _DTYPE[pt])
     return gx, gw, gb
 
 

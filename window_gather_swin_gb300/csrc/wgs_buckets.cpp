@@ -35,21 +35,52 @@ bool window_counts(const int32_t window[3], int32_t absolute_axes, int64_t *cell
     return true;
 }
 
-// Pairs and slots of a map; false for a value outside [-1, n_buckets).
-// `seen` holds n_buckets entries.
-bool count_slots(const int32_t *bucket, int64_t n_pairs, int64_t n_buckets,
-                 std::vector<int64_t> &seen, int64_t *n_slots) {
-    int64_t slots = 0;
-    for (int64_t p = 0; p < n_pairs; ++p) {
-        const int32_t b = bucket[p];
-        if (b < -1 || b >= n_buckets) return false;
-        if (b < 0) continue;
-        const int64_t tile = p / wgs::kPlanTile;
-        if (seen[b] != tile) {
-            seen[b] = tile;
-            ++slots;
+// Groups of a tile: buckets in the order of their first pairs, and how many
+// pairs each has.  count holds n_buckets zeros before and after walk().
+struct Tile {
+    std::vector<int32_t> count, mine;
+
+    explicit Tile(int32_t n_buckets) : count(static_cast<size_t>(n_buckets), 0) {}
+
+    // group(bucket, first entry in the order, entries) for each group of the
+    // pairs [p0, p1); false for a value outside [-1, n_buckets)
+    template <typename Group>
+    bool walk(const int32_t *bucket, int64_t p0, int64_t p1, Group group) {
+        bool ok = true;
+        mine.clear();
+        for (int64_t p = p0; p < p1; ++p) {
+            const int32_t b = bucket[p];
+            if (b < -1 || b >= static_cast<int64_t>(count.size())) {
+                ok = false;
+                break;
+            }
+            if (b >= 0 && count[static_cast<size_t>(b)]++ == 0) mine.push_back(b);
         }
+        int32_t entry = 0;
+        for (int32_t b : mine) {
+            int32_t &n = count[static_cast<size_t>(b)];
+            if (ok) group(b, entry, n);
+            entry += n;
+            n = 0;
+        }
+        return ok;
     }
+};
+
+int64_t tile_end(int64_t tile, int64_t n_pairs) {
+    const int64_t p = (tile + 1) * wgs::kPlanTile;
+    return p < n_pairs ? p : n_pairs;
+}
+
+// Slots of a map; false for a value outside [-1, n_buckets).
+bool count_slots(const int32_t *bucket, int64_t n_pairs, int32_t n_buckets, int64_t *n_slots) {
+    Tile tile(n_buckets);
+    int64_t slots = 0;
+    for (int64_t t = 0; t < wgs::ceil_tiles(n_pairs); ++t)
+        if (!tile.walk(bucket, t * wgs::kPlanTile, tile_end(t, n_pairs), [&](int32_t, int32_t entry, int32_t n) {
+                slots += (entry + n - 1) / 32 - entry / 32 + 1;
+            }))
+            return false;
     *n_slots = slots;
     return true;
 }
@@ -139,9 +170,8 @@ extern "C" int64_t wgs_bucket_plan_words(const int32_t *bucket_host, int64_t n_p
                                          int32_t n_buckets, int64_t *n_slots) {
     if (!plan_sizes_ok(n_pairs, n_buckets) || (n_pairs > 0 && !bucket_host)) return -1;
     try {
-        std::vector<int64_t> seen(static_cast<size_t>(n_buckets), -1);
         int64_t slots;
-        if (!count_slots(bucket_host, n_pairs, n_buckets, seen, &slots)) return -1;
+        if (!count_slots(bucket_host, n_pairs, n_buckets, &slots)) return -1;
         if (n_slots) *n_slots = slots;
         return wgs::plan_layout(n_pairs, n_buckets, slots).words;
     } catch (const std::bad_alloc &) {
@@ -156,54 +186,48 @@ extern "C" wgs_status wgs_build_bucket_plan(const int32_t *bucket_host, int64_t 
     if (!plan_host || (n_pairs > 0 && !bucket_host)) return WGS_ERR_NULL;
     try {
         const size_t nb = static_cast<size_t>(n_buckets);
-        std::vector<int64_t> seen(nb, -1);
         int64_t slots;
-        if (!count_slots(bucket_host, n_pairs, n_buckets, seen, &slots)) return WGS_ERR_INDEX;
+        if (!count_slots(bucket_host, n_pairs, n_buckets, &slots)) return WGS_ERR_INDEX;
         const wgs::PlanLayout at = wgs::plan_layout(n_pairs, n_buckets, slots);
         if (plan_words < at.words) return WGS_ERR_SHAPE;
         const int64_t n_tiles = wgs::ceil_tiles(n_pairs);
-        std::vector<int32_t> count(nb, 0), start(nb, 0);  // of the current tile
-        std::vector<int32_t> mine;                        // buckets of the current tile
+        std::vector<int32_t> next(nb);  // entry of the next pair of each bucket
+        std::vector<int32_t> of_slot;   // the bucket of each slot
+        of_slot.reserve(static_cast<size_t>(slots));
 
         std::memset(plan_host, 0, static_cast<size_t>(at.words) * sizeof(int32_t));
         const int32_t head[5] = {wgs::kPlanMagic, static_cast<int32_t>(n_pairs), n_buckets,
                                  static_cast<int32_t>(n_tiles), static_cast<int32_t>(slots)};
         std::memcpy(plan_host, head, sizeof(head));
-        int32_t *tile_slot = plan_host + at.tile_slot, *record = plan_host + at.slot;
-        int32_t *bucket_dest = plan_host + at.bucket_dest;
-        uint16_t *order = reinterpret_cast<uint16_t *>(plan_host + at.order);
-
-        int64_t slot = 0;
+        int32_t *first = plan_host + at.bucket_first, *bucket_slot = plan_host + at.bucket_slot;
+        Tile tile(n_buckets);
         for (int64_t t = 0; t < n_tiles; ++t) {
-            const int64_t p0 = t * wgs::kPlanTile;
-            const int64_t p1 = p0 + wgs::kPlanTile < n_pairs ? p0 + wgs::kPlanTile : n_pairs;
-            mine.clear();
+            int32_t *lane = plan_host + at.lane + t * 2 * wgs::kPlanLanes;
+            uint16_t *order = reinterpret_cast<uint16_t *>(plan_host + at.order) + t * wgs::kPlanTile;
+            const int64_t p0 = t * wgs::kPlanTile, p1 = tile_end(t, n_pairs);
+            tile.walk(bucket_host, p0, p1, [&](int32_t b, int32_t entry, int32_t n) {
+                next[static_cast<size_t>(b)] = entry;
+                for (int32_t e = entry; e < entry + n;) {
+                    const int32_t l = e / 32, end = (l + 1) * 32 < entry + n ? (l + 1) * 32 : entry + n;
+                    if (e % 32 == 0) lane[2 * l + 1] = static_cast<int32_t>(of_slot.size());
+                    const uint32_t bit = uint32_t{1} << (end - 1) % 32;
+                    lane[2 * l] = static_cast<int32_t>(static_cast<uint32_t>(lane[2 * l]) | bit);
+                    of_slot.push_back(b);
+                    ++first[static_cast<size_t>(b) + 1];
+                    e = end;
+                }
+            });
             for (int64_t p = p0; p < p1; ++p) {
-                const int32_t b = bucket_host[p];
-                if (b >= 0 && count[static_cast<size_t>(b)]++ == 0) mine.push_back(b);
+                if (bucket_host[p] < 0) continue;
+                const int32_t e = next[static_cast<size_t>(bucket_host[p])]++;
+                order[(e % 32 / 8 * wgs::kPlanLanes + e / 32) * 8 + e % 8] =
+                    static_cast<uint16_t>(wgs::plan_place(static_cast<int>(p - p0)));
             }
-            // slots in the order in which their buckets first appear in the tile
-            tile_slot[t] = static_cast<int32_t>(slot);
-            int32_t at_entry = 0;
-            for (int32_t b : mine) {
-                const size_t k = static_cast<size_t>(b);
-                start[k] = at_entry;
-                record[2 * slot] = at_entry | (count[k] << 16);
-                record[2 * slot + 1] = b;  // its bucket for now
-                ++bucket_dest[k + 1];
-                at_entry += count[k];
-                ++slot;
-            }
-            for (int64_t p = p0; p < p1; ++p) {
-                const int32_t b = bucket_host[p];
-                if (b >= 0) order[p0 + start[static_cast<size_t>(b)]++] = static_cast<uint16_t>(p - p0);
-            }
-            for (int32_t b : mine) count[static_cast<size_t>(b)] = 0;
         }
-        tile_slot[n_tiles] = static_cast<int32_t>(slot);
-        for (size_t b = 0; b < nb; ++b) bucket_dest[b + 1] += bucket_dest[b];
-        std::vector<int32_t> next(bucket_dest, bucket_dest + nb);
-        for (int64_t s = 0; s < slot; ++s) record[2 * s + 1] = next[static_cast<size_t>(record[2 * s + 1])]++;
+        for (size_t b = 0; b < nb; ++b) first[b + 1] += first[b];
+        std::vector<int32_t> place(first, first + nb);
+        for (size_t s = 0; s < of_slot.size(); ++s)
+            bucket_slot[place[static_cast<size_t>(of_slot[s])]++] = static_cast<int32_t>(s);
         return WGS_OK;
     } catch (const std::bad_alloc &) {
         return WGS_ERR_TOO_LARGE;

@@ -65,46 +65,60 @@ __device__ __forceinline__ void store1(void *p, int64_t i, float v) {
         static_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(T::from_f2(v, 0.f));
 }
 
-// HC neighbouring table values in one load.
+// HC neighbouring table values in one load, as their words: FP32 values, or
+// 16-bit values in pairs (one alone in the low half).
 template <typename T, int HC>
-__device__ __forceinline__ void load_heads(const void *table, int64_t i, float (&v)[HC]) {
-    if constexpr (HC == 1) {
-        v[0] = load1<T>(table, i);
-    } else if constexpr (std::is_same<T, F32>::value) {
-        const float *p = static_cast<const float *>(table) + i;
-        if constexpr (HC == 4) {
-            const float4 q = *reinterpret_cast<const float4 *>(p);
-            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+struct Heads {
+    static constexpr int kWords = kBytes<T> == 4 ? HC : (HC + 1) / 2;
+    uint32_t w[kWords];
+
+    __device__ void zero() {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) w[k] = 0u;
+    }
+    __device__ void load(const char *p) {
+        if constexpr (HC * kBytes<T> == 16) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p));
+            w[0] = q.x, w[1] = q.y, w[kWords - 2] = q.z, w[kWords - 1] = q.w;
+        } else if constexpr (HC * kBytes<T> == 8) {
+            const uint2 q = __ldg(reinterpret_cast<const uint2 *>(p));
+            w[0] = q.x, w[kWords - 1] = q.y;
+        } else if constexpr (HC * kBytes<T> == 4) {
+            w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
         } else {
-            const float2 q = *reinterpret_cast<const float2 *>(p);
-            v[0] = q.x, v[1] = q.y;
-        }
-    } else {
-        const uint16_t *p = static_cast<const uint16_t *>(table) + i;
-        if constexpr (HC == 4) {
-            const uint2 q = *reinterpret_cast<const uint2 *>(p);
-            const float2 a = T::to_f2(q.x), b = T::to_f2(q.y);
-            v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
-        } else {
-            const float2 a = T::to_f2(*reinterpret_cast<const uint32_t *>(p));
-            v[0] = a.x, v[1] = a.y;
+            w[0] = __ldg(reinterpret_cast<const uint16_t *>(p));
         }
     }
-}
+    __device__ float value(int k) const {
+        if constexpr (kBytes<T> == 4) {
+            return __uint_as_float(w[k]);
+        } else {
+            const float2 f = T::to_f2(w[k / 2]);
+            return k & 1 ? f.y : f.x;
+        }
+    }
+};
 
-// Eight consecutive outputs at a 16-byte aligned address, each rounded once
-// (to nearest even) to the output's format.
-template <typename O>
-__device__ __forceinline__ void store8(void *p, const float (&v)[8]) {
+// Head k's values of eight pairs as outputs at a 16-byte aligned address:
+// copied where table and output have one format, else rounded once, to
+// nearest even.
+template <typename O, typename T, int HC>
+__device__ __forceinline__ void store8(void *p, const Heads<T, HC> (&v)[8], int k) {
     uint4 *q = static_cast<uint4 *>(p);
-    if constexpr (std::is_same<O, F32>::value) {
-        st_stream(q, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
-                                __float_as_uint(v[2]), __float_as_uint(v[3])));
-        st_stream(q + 1, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]),
-                                    __float_as_uint(v[6]), __float_as_uint(v[7])));
+    if constexpr (kBytes<O> == 4) {
+        st_stream(q, make_uint4(v[0].w[k], v[1].w[k], v[2].w[k], v[3].w[k]));
+        st_stream(q + 1, make_uint4(v[4].w[k], v[5].w[k], v[6].w[k], v[7].w[k]));
+    } else if constexpr (std::is_same<O, T>::value) {
+        const uint32_t pick = k & 1 ? 0x7632 : 0x5410;  // the halves of two words
+        uint4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) set_word(o, j, __byte_perm(v[2 * j].w[k / 2], v[2 * j + 1].w[k / 2], pick));
+        st_stream(q, o);
     } else {
-        st_stream(q, make_uint4(O::from_f2(v[0], v[1]), O::from_f2(v[2], v[3]),
-                                O::from_f2(v[4], v[5]), O::from_f2(v[6], v[7])));
+        uint4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) set_word(o, j, O::from_f2(v[2 * j].value(k), v[2 * j + 1].value(k)));
+        st_stream(q, o);
     }
 }
 
@@ -149,71 +163,92 @@ __global__ void __launch_bounds__(kThreads) bias_expand_eights(ExpandArgs a) {
         if (row[e] >= a.n_buckets) row[e] = -1;
     }
     if (bad) atomicOr(&g_bucket_error, 1u);
+    // byte offsets of the rows from the type's table
+    uint32_t at[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) at[e] = static_cast<uint32_t>(max(row[e], 0)) * a.heads * kBytes<T>;
+    const char *table = static_cast<const char *>(a.table) + type * a.n_buckets * a.heads * kBytes<T>;
     const int32_t h1 = min(a.heads, static_cast<int32_t>((hb + 1) * a.head_step));
     for (int32_t h = hb * a.head_step; h < h1; h += HC) {
-        float v[8][HC];
+        Heads<T, HC> v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-#pragma unroll
-            for (int k = 0; k < HC; ++k) v[e][k] = 0.f;
-            if (row[e] >= 0)
-                load_heads<T, HC>(a.table, (type * a.n_buckets + row[e]) * a.heads + h, v[e]);
+            v[e].zero();
+            if (row[e] >= 0) v[e].load(table + h * kBytes<T> + at[e]);
         }
 #pragma unroll
-        for (int k = 0; k < HC; ++k) {
-            const float o[8] = {v[0][k], v[1][k], v[2][k], v[3][k], v[4][k], v[5][k], v[6][k], v[7][k]};
-            store8<O>(static_cast<char *>(a.bias) +
-                          ((type * a.heads + h + k) * a.n_pairs + p) * kBytes<O>, o);
-        }
+        for (int k = 0; k < HC; ++k)
+            store8<O>(static_cast<char *>(a.bias) + ((type * a.heads + h + k) * a.n_pairs + p) * kBytes<O>, v, k);
     }
 }
 
-// Any pair count or alignment.  The outputs of a (type, head) slab are cut
-// where the address is a multiple of eight elements, so all but the slab's
-// two ends are stored 16 bytes at a time wherever the slab starts; the
-// block's buckets wait in shared memory (nine words for eight pairs, which
-// keeps the lanes' stride of eight off the same bank) because the cut moves
-// from head to head.
-template <typename O, typename T>
+// Any pair count or alignment.  As above up to the stores: the eight outputs of
+// a head go to shared memory, HC heads at a time, and from there to the slab
+// in words cut where the output's address is a multiple of four bytes, which
+// differs from head to head; neighbouring threads store neighbouring words.
+template <typename O, typename T, int HC>
 __global__ void __launch_bounds__(kThreads) bias_expand_any(ExpandArgs a) {
-    constexpr int kSpan = kThreads * 8;
-    __shared__ int32_t rows[(kSpan + 8) / 8 * 9];
+    constexpr int kSpan = kThreads * 8, kB = kBytes<O>;
+    // kept twice, so that one barrier a step does
+    __shared__ __align__(16) char rows[2][HC][kSpan * kB + 16];
     pdl_prologue();
     uint32_t blk = blockIdx.x;
     const uint32_t pb = blk % a.pair_blocks;
     blk /= a.pair_blocks;
     const uint32_t hb = blk % a.head_blocks;
     const int64_t type = blk / a.head_blocks;
-    const int64_t first = static_cast<int64_t>(pb) * kSpan - 8;
+    const int64_t p0 = static_cast<int64_t>(pb) * kSpan;
+    const int32_t count = static_cast<int32_t>(min(a.n_pairs - p0, static_cast<int64_t>(kSpan)));
+    const int32_t mine = static_cast<int32_t>(threadIdx.x) * 8;
+    int32_t row[8];
     bool bad = false;
-    for (int i = threadIdx.x; i < kSpan + 8; i += kThreads) {
-        const int64_t p = first + i;
-        int32_t r = p >= 0 && p < a.n_pairs ? __ldg(a.bucket + p) : -1;
-        bad |= r < -1 || r >= a.n_buckets;
-        if (r >= a.n_buckets) r = -1;
-        rows[i + i / 8] = r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        row[e] = mine + e < count ? __ldg(a.bucket + p0 + mine + e) : -1;
+        bad |= row[e] < -1 || row[e] >= a.n_buckets;
+        if (row[e] >= a.n_buckets) row[e] = -1;
     }
     if (bad) atomicOr(&g_bucket_error, 1u);
-    __syncthreads();
-    const uint64_t base = reinterpret_cast<uint64_t>(a.bias) / kBytes<O>;
+    uint32_t at[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) at[e] = static_cast<uint32_t>(max(row[e], 0)) * a.heads * kBytes<T>;
+    const char *table = static_cast<const char *>(a.table) + type * a.n_buckets * a.heads * kBytes<T>;
     const int32_t h1 = min(a.heads, static_cast<int32_t>((hb + 1) * a.head_step));
-    for (int32_t h = hb * a.head_step; h < h1; ++h) {
-        const int64_t slab = (type * a.heads + h) * a.n_pairs;
-        const int shift = static_cast<int>((base + static_cast<uint64_t>(slab)) & 7);
-        const int i0 = static_cast<int>(threadIdx.x) * 8 + 8 - shift;
-        const int64_t p = first + i0;
-        float v[8];
+    int turn = 0;
+    for (int32_t h = hb * a.head_step; h < h1; h += HC, turn ^= 1) {
+        Heads<T, HC> v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int32_t r = rows[i0 + e + (i0 + e) / 8];
-            v[e] = r >= 0 ? load1<T>(a.table, (type * a.n_buckets + r) * a.heads + h) : 0.f;
+            v[e].zero();
+            if (row[e] >= 0) v[e].load(table + h * kBytes<T> + at[e]);
         }
-        if (p >= 0 && p + 8 <= a.n_pairs) {
-            store8<O>(static_cast<char *>(a.bias) + (slab + p) * kBytes<O>, v);
-        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (p + e >= 0 && p + e < a.n_pairs) store1<O>(a.bias, slab + p + e, v[e]);
+        for (int k = 0; k < HC; ++k) store8<O>(rows[turn][k] + mine * kB, v, k);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < HC; ++k) {
+            const int64_t first = (type * a.heads + h + k) * a.n_pairs + p0;  // element of the output
+            const char *from = rows[turn][k];
+            if constexpr (kB == 4) {
+                for (int32_t i = threadIdx.x; i < count; i += kThreads)
+                    static_cast<uint32_t *>(a.bias)[first + i] = reinterpret_cast<const uint32_t *>(from)[i];
+            } else {
+                uint16_t *to = static_cast<uint16_t *>(a.bias) + first;
+                const uint16_t *q = reinterpret_cast<const uint16_t *>(from);
+                // odd: the slab's piece starts in the middle of a word
+                const int odd = static_cast<int>((reinterpret_cast<uintptr_t>(to) >> 1) & 1);
+                const int32_t words = (count - odd) / 2;
+                uint32_t *out = reinterpret_cast<uint32_t *>(to + odd);
+                if (odd) {
+                    for (int32_t i = threadIdx.x; i < words; i += kThreads)
+                        out[i] = q[2 * i + 1] | static_cast<uint32_t>(q[2 * i + 2]) << 16;
+                } else {
+                    for (int32_t i = threadIdx.x; i < words; i += kThreads)
+                        out[i] = reinterpret_cast<const uint32_t *>(q)[i];
+                }
+                if (threadIdx.x == 0 && odd && count > 0) to[0] = q[0];
+                if (threadIdx.x == 1 && odd + 2 * words < count) to[count - 1] = q[count - 1];
+            }
         }
     }
 }
@@ -226,14 +261,13 @@ template <typename O, typename T>
 wgs_status launch_expand(ExpandArgs a, int32_t n_types, cudaStream_t stream) {
     const bool eights = a.n_pairs % 8 == 0 && aligned16(a.bucket) && aligned16(a.bias);
     int hc = 1;
-    if (eights)
-        for (int c = 4; c > 1; c /= 2)
-            if (a.heads % c == 0 && reinterpret_cast<uintptr_t>(a.table) % (c * kBytes<T>) == 0) {
-                hc = c;
-                break;
-            }
-    // the slab's cut moves the pairs of a block by up to seven
-    const int64_t pair_blocks = ceil_div(a.n_pairs + (eights ? 0 : 7), kThreads * 8);
+    for (int c = 4; c > 1; c /= 2)
+        if (a.heads % c == 0 && reinterpret_cast<uintptr_t>(a.table) % (c * kBytes<T>) == 0) {
+            hc = c;
+            break;
+        }
+    if (!eights && kBytes<O> == 4 && hc > 2) hc = 2;  // FP32 rows in 48 KB of shared memory
+    const int64_t pair_blocks = ceil_div(a.n_pairs, kThreads * 8);
     // all heads in one block (the map is read once), unless that leaves the GPU idle
     const int64_t want = ceil_div(kExpandBlocks, pair_blocks * n_types);
     const int64_t steps = ceil_div(a.heads, hc);
@@ -242,10 +276,13 @@ wgs_status launch_expand(ExpandArgs a, int32_t n_types, cudaStream_t stream) {
     a.pair_blocks = static_cast<int32_t>(pair_blocks);
     const int64_t grid = pair_blocks * a.head_blocks * n_types;
     if (grid > INT32_MAX) return WGS_ERR_SHAPE;
-    auto kernel = !eights   ? bias_expand_any<O, T>
-                  : hc == 4 ? bias_expand_eights<O, T, 4>
-                  : hc == 2 ? bias_expand_eights<O, T, 2>
-                            : bias_expand_eights<O, T, 1>;
+    constexpr int kAny = kBytes<O> == 4 ? 2 : 4;
+    auto kernel = eights ? (hc == 4   ? bias_expand_eights<O, T, 4>
+                            : hc == 2 ? bias_expand_eights<O, T, 2>
+                                      : bias_expand_eights<O, T, 1>)
+                         : (hc == 4   ? bias_expand_any<O, T, kAny>
+                            : hc == 2 ? bias_expand_any<O, T, 2>
+                                      : bias_expand_any<O, T, 1>);
     return launch(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, a);
 }
 
@@ -291,11 +328,18 @@ struct Unit {
     }
 };
 
-constexpr int kAdders = 256;                  // threads that add
-constexpr int kGradThreads = kAdders + 32;    // and a warp that copies
+// Warps of a block: four add windows up, four add the sums up by slot, one copies.
+constexpr int kAdders = 128, kSlotters = kPlanLanes;
+constexpr int kGradThreads = kAdders + kSlotters + 32;
 constexpr int kListed = 1024;                 // windows looked over at a time
+#ifndef WGS_GRAD_STAGES
+#define WGS_GRAD_STAGES 6
+#endif
+#ifndef WGS_GRAD_CTAS
+#define WGS_GRAD_CTAS 2
+#endif
 template <typename E>
-constexpr int kGradStages = std::is_same<E, F32>::value ? 4 : 6;
+constexpr int kGradStages = std::is_same<E, F32>::value ? WGS_GRAD_STAGES * 2 / 3 : WGS_GRAD_STAGES;
 template <typename E>
 constexpr int kStageBytes = kPlanTile * kBytes<E> + 16;  // a tile that starts between 16-byte borders
 
@@ -305,12 +349,12 @@ constexpr int kData = 8, kDirect = 16, kEnd = 32;  // | elements before the tile
 template <typename E>
 struct GradShared {
     alignas(16) char stage[kGradStages<E>][kStageBytes<E>];
-    alignas(16) float sums[kPlanTile];
-    alignas(16) uint16_t order[kPlanTile];
+    alignas(16) float sums[2][kPlanTile];  // of a unit, and of the next
     int32_t list[kListed];
     int32_t said[kGradStages<E>];    // of the stage's window, see kData
     int32_t window[kGradStages<E>];
     alignas(8) uint64_t full[kGradStages<E>], empty[kGradStages<E>];
+    uint64_t summed[2], read[2];     // the sums are there, have been added up
 };
 
 // The slot of the ring that a side of it is at.
@@ -329,125 +373,132 @@ __device__ __forceinline__ void must_wait(const uint64_t *bar, uint32_t parity) 
 }
 
 // The copying warp: the tiles of each unit's windows into the ring, in order.
-template <typename E>
+// One lane does it, in as few steps a window as can be: a window's latency
+// here bounds what the block takes in.
+template <typename E, bool kVec>
 __device__ void copy_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int32_t u1, int lane) {
-    constexpr int kES = kBytes<E>;
-    RingPlace<kGradStages<E>> ring;
+    constexpr int kES = kBytes<E>, kRing = kGradStages<E>;
     const uint64_t policy = l2_policy(true);
+    const uint32_t full = shared_address(sh.full), empty = shared_address(sh.empty), slots = shared_address(sh.stage);
     const char *end = a.grad + a.grad_bytes;
+    int stage = 0;
+    uint32_t phase = 1;  // of the wait for an empty stage: a new barrier's counts as past
     int32_t listed_type = -1, listed_slab = -1, listed = 0;
-    // by lane 0: the next stage, w < 0 for a unit without windows
-    auto say = [&](const Unit &u, int32_t w, bool last) {
-        if (ring.wrapped) must_wait(&sh.empty[ring.stage], ring.phase ^ 1);
-        const uint32_t bar = shared_address(&sh.full[ring.stage]);
-        int said = last ? kEnd : 0;
-        uint32_t bytes = 0;
-        const char *from = nullptr;
-        if (w >= 0) {
-            said |= kData;
-            const int64_t p0 = static_cast<int64_t>(u.tile) * kPlanTile;
-            const int64_t len = min(a.n_pairs - p0, static_cast<int64_t>(kPlanTile));
-            const char *first = a.grad + ((static_cast<int64_t>(w) * a.heads + u.head) * a.n_pairs + p0) * kES;
-            const uintptr_t lo = reinterpret_cast<uintptr_t>(first) & ~uintptr_t{15};
-            const uintptr_t hi = (reinterpret_cast<uintptr_t>(first + len * kES) + 15) & ~uintptr_t{15};
-            // a tile at the tensor's ends, whose 16-byte lines hold other bytes too, is read directly
-            if (lo < reinterpret_cast<uintptr_t>(a.grad) || hi > reinterpret_cast<uintptr_t>(end)) {
-                said |= kDirect;
-            } else {
-                said |= static_cast<int>((reinterpret_cast<uintptr_t>(first) - lo) / kES);
-                from = reinterpret_cast<const char *>(lo);
-                bytes = static_cast<uint32_t>(hi - lo);
-            }
-        }
-        sh.said[ring.stage] = said;
-        sh.window[ring.stage] = w;
-        if (bytes) {
-            bar_expect(bar, bytes);
-            bulk_copy(shared_address(sh.stage[ring.stage]), from, bytes, bar, policy);
-        } else {
-            bar_arrive(bar);
-        }
-    };
     for (int32_t i = u0; i < u1; ++i) {
         const Unit u(a, i);
         const int32_t w0 = share_start(a.n_win, a.slabs, u.slab), w1 = share_start(a.n_win, a.slabs, u.slab + 1);
-        int32_t pending = -1;  // the last window found so far
-        auto found = [&](int32_t w) {
-            if (pending >= 0) {
-                if (lane == 0) say(u, pending, false);
-                ring.next();
+        const int64_t p0 = static_cast<int64_t>(u.tile) * kPlanTile;
+        const uint32_t bytes = static_cast<uint32_t>(min(a.n_pairs - p0, static_cast<int64_t>(kPlanTile))) * kES;
+        const char *tile0 = a.grad + (static_cast<int64_t>(u.head) * a.n_pairs + p0) * kES;
+        const int64_t stride = static_cast<int64_t>(a.heads) * a.n_pairs * kES;
+        auto advance = [&] {
+            if (++stage == kRing) stage = 0, phase ^= 1;
+        };
+        // `count` windows, the n-th window(n)
+        auto send = [&](int32_t count, bool ends, auto window) {
+            if (lane != 0) return;
+            for (int32_t n = 0; n < count; ++n) {
+                const int32_t w = window(n);
+                const char *from = tile0 + w * stride;
+                if (!bar_wait(empty + 8 * stage, phase)) atomicOr(&g_bucket_error, 1u);
+                const int last = ends && n + 1 == count ? kEnd : 0;
+                uint32_t size = bytes;
+                int said = kData | last;
+                if constexpr (!kVec) {
+                    // the 16-byte lines that hold the tile; at the tensor's ends they
+                    // hold other bytes too, and the tile is read directly
+                    const uintptr_t first = reinterpret_cast<uintptr_t>(from);
+                    const char *lo = reinterpret_cast<const char *>(first & ~uintptr_t{15});
+                    const char *hi = reinterpret_cast<const char *>((first + bytes + 15) & ~uintptr_t{15});
+                    said |= static_cast<int>(first & 15) / kES;
+                    size = static_cast<uint32_t>(hi - lo);
+                    from = lo;
+                    if (lo < a.grad || hi > end) {
+                        sh.window[stage] = w;
+                        size = 0;
+                        said |= kDirect;
+                    }
+                }
+                sh.said[stage] = said;
+                const uint32_t bar = full + 8 * stage;
+                if (size) {
+                    bar_expect(bar, size);
+                    bulk_copy(slots + stage * kStageBytes<E>, from, size, bar, policy);
+                } else {
+                    bar_arrive(bar);
+                }
+                advance();
             }
-            pending = w;
+            if (count == 0 && ends) {  // a stage without a window
+                if (!bar_wait(empty + 8 * stage, phase)) atomicOr(&g_bucket_error, 1u);
+                sh.said[stage] = kEnd;
+                bar_arrive(full + 8 * stage);
+                advance();
+            }
         };
         if (!a.win_type) {
-            if (u.type == 0)
-                for (int32_t w = w0; w < w1; ++w) found(w);
-        } else {
-            const bool kept = listed_type == u.type && listed_slab == u.slab && w1 - w0 <= kListed;
-            for (int32_t w = w0; w < w1; w += kListed) {
-                if (!kept) {
-                    // the windows of this type among the next kListed, in order
-                    constexpr int kBatch = 8;
-                    listed = 0;
-                    for (int32_t part = 0; part < min(kListed, w1 - w); part += 32 * kBatch) {
-                        int32_t t[kBatch];
-#pragma unroll
-                        for (int k = 0; k < kBatch; ++k) {
-                            const int32_t at = w + part + 32 * k + lane;
-                            t[k] = at < w1 ? __ldg(a.win_type + at) : u.type - 1;
-                            if (at < w1 && (t[k] < 0 || t[k] >= a.n_types)) atomicOr(&g_bucket_error, 1u);
-                        }
-#pragma unroll
-                        for (int k = 0; k < kBatch; ++k) {
-                            const int32_t at = w + part + 32 * k + lane;
-                            const bool hit = at < w1 && t[k] == u.type;
-                            const unsigned hits = __ballot_sync(0xffffffffu, hit);
-                            if (hit) sh.list[listed + __popc(hits & ((1u << lane) - 1u))] = at;
-                            listed += __popc(hits);
-                        }
-                    }
-                    __syncwarp();
-                    listed_type = u.type, listed_slab = u.slab;
-                }
-                for (int32_t k = 0; k < listed; ++k) found(sh.list[k]);
-                __syncwarp();
-            }
+            send(u.type == 0 ? w1 - w0 : 0, true, [&](int32_t n) { return w0 + n; });
+            continue;
         }
-        if (lane == 0) say(u, pending, true);
-        ring.next();
+        const bool one = w1 - w0 <= kListed;  // the list holds the slab's
+        const bool kept = one && listed_type == u.type && listed_slab == u.slab;
+        for (int32_t w = w0; w < w1; w += kListed) {
+            if (!kept) {
+                // the windows of this type among the next kListed, in order
+                constexpr int kBatch = 32;
+                const int32_t stop = min(w1, w + kListed);
+                listed = 0;
+                __syncwarp();  // the list has been read
+                for (int32_t part = w; part < stop; part += 32 * kBatch) {
+                    int32_t t[kBatch];
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const int32_t at = part + 32 * k + lane;
+                        t[k] = at < stop ? __ldg(a.win_type + at) : u.type - 1;
+                        if (at < stop && (t[k] < 0 || t[k] >= a.n_types)) atomicOr(&g_bucket_error, 1u);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const int32_t at = part + 32 * k + lane;
+                        const bool hit = at < stop && t[k] == u.type;
+                        const unsigned hits = __ballot_sync(0xffffffffu, hit);
+                        if (hit) sh.list[listed + __popc(hits & ((1u << lane) - 1u))] = at;
+                        listed += __popc(hits);
+                    }
+                }
+                __syncwarp();
+                listed_type = u.type, listed_slab = u.slab;
+            }
+            send(listed, one, [&](int32_t n) { return sh.list[n]; });
+        }
+        if (!one || w0 == w1) send(0, true, [](int32_t) { return 0; });
     }
 }
 
 // The adding warps: a unit's windows pair by pair into FP32 registers, the
-// sums into shared memory, and there slot by slot, LANES neighbouring lanes a
-// slot.
-template <typename E, bool kVec, int LANES>
+// sums into shared memory.
+template <typename E, bool kVec>
 __device__ void add_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int32_t u1) {
     constexpr bool k32 = std::is_same<E, F32>::value;
     constexpr int kN = kVec ? (k32 ? 4 : 8) : 1;       // neighbouring pairs of a thread
     constexpr int kOwn = kPlanTile / (kAdders * kN);   // runs of them
     const int tid = threadIdx.x;
-    auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kAdders) : "memory"); };
+    const uint32_t full = shared_address(sh.full), empty = shared_address(sh.empty);
     RingPlace<kGradStages<E>> ring;
-    int32_t tile = -1;
+    RingPlace<2> out;
     for (int32_t i = u0; i < u1; ++i) {
-        const Unit u(a, i);
-        const int64_t p0 = static_cast<int64_t>(u.tile) * kPlanTile;
-        const int32_t len = static_cast<int32_t>(min(a.n_pairs - p0, static_cast<int64_t>(kPlanTile)));
-        if (u.tile != tile) {
-            tile = u.tile;
-            const uint4 *oq = reinterpret_cast<const uint4 *>(a.plan + a.at.order) + tile * (kPlanTile / 8);
-            for (int k = tid; k < kPlanTile / 8; k += kAdders) reinterpret_cast<uint4 *>(sh.order)[k] = __ldg(oq + k);
-        }
         float acc[kOwn * kN];
 #pragma unroll
         for (int k = 0; k < kOwn * kN; ++k) acc[k] = 0.f;
         int said;
         do {
-            must_wait(&sh.full[ring.stage], ring.phase);
+            if (!bar_wait(full + 8 * ring.stage, ring.phase)) atomicOr(&g_bucket_error, 1u);
             said = sh.said[ring.stage];
             const char *at = sh.stage[ring.stage];
-            if (said & kDirect) {
+            if (!kVec && (said & kDirect)) {
+                const Unit u(a, i);
+                const int64_t p0 = static_cast<int64_t>(u.tile) * kPlanTile;
+                const int32_t len = static_cast<int32_t>(min(a.n_pairs - p0, static_cast<int64_t>(kPlanTile)));
                 const int64_t first = (static_cast<int64_t>(sh.window[ring.stage]) * a.heads + u.head) * a.n_pairs + p0;
 #pragma unroll
                 for (int k = 0; k < kOwn; ++k)
@@ -457,10 +508,10 @@ __device__ void add_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int3
                         if (e < len) acc[k * kN + j] += load1<E>(a.grad, first + e);
                     }
             } else if (said & kData) {
+                // (a short tile's end adds what an earlier one left: no slot names it)
                 if constexpr (kVec) {
 #pragma unroll
                     for (int k = 0; k < kOwn; ++k) {
-                        // a short tile's end adds what an earlier one left: no slot names it
                         const uint4 v = reinterpret_cast<const uint4 *>(at)[tid + k * kAdders];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -480,51 +531,70 @@ __device__ void add_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int3
                 }
             }
             __syncwarp();
-            if ((tid & 31) == 0) bar_arrive(shared_address(&sh.empty[ring.stage]));
+            if ((tid & 31) == 0) bar_arrive(empty + 8 * ring.stage);
             ring.next();
         } while (!(said & kEnd));
+        if (out.wrapped) must_wait(&sh.read[out.stage], out.phase ^ 1);
+        float *sums = sh.sums[out.stage];
 #pragma unroll
-        for (int k = 0; k < kOwn; ++k) {
-            if constexpr (kN % 4 == 0) {
+        for (int k = 0; k < kOwn; ++k)
 #pragma unroll
-                for (int j = 0; j < kN; j += 4)
-                    *reinterpret_cast<float4 *>(sh.sums + (tid + k * kAdders) * kN + j) =
-                        make_float4(acc[k * kN + j], acc[k * kN + j + 1], acc[k * kN + j + 2], acc[k * kN + j + 3]);
-            } else {
-                sh.sums[tid + k * kAdders] = acc[k];
-            }
+            for (int j = 0; j < kN; ++j) sums[plan_place((tid + k * kAdders) * kN + j)] = acc[k * kN + j];
+        __syncwarp();
+        if ((tid & 31) == 0) bar_arrive(shared_address(&sh.summed[out.stage]));
+        out.next();
+    }
+}
+
+// The slot warps: a unit's sums slot by slot, while the next unit's windows are
+// added up.  A thread is a lane of the plan: 32 entries of the tile's order,
+// whose sums it adds from slot end to slot end.  (A thread a slot took
+// several times as long: slots are short and long, and named by loads.)
+template <typename E>
+__device__ void slot_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int32_t u1, int tid) {
+    RingPlace<2> in;
+    int32_t tile = -1;
+    uint4 order[4];
+    int2 lane;
+    const bool ok = plan_matches(a);  // else nothing of it is followed
+    if (!ok && tid == 0) atomicOr(&g_bucket_error, 1u);
+    for (int32_t i = u0; i < u1; ++i) {
+        const Unit u(a, i);
+        if (u.tile != tile && ok) {
+            tile = u.tile;
+            const uint4 *oq = reinterpret_cast<const uint4 *>(a.plan + a.at.order) + tile * (kPlanTile / 8);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) order[k] = __ldg(oq + k * kPlanLanes + tid);
+            lane = __ldg(reinterpret_cast<const int2 *>(a.plan + a.at.lane) + tile * kPlanLanes + tid);
         }
-        meet();
-        const int32_t s0 = max(__ldg(a.plan + a.at.tile_slot + tile), 0);
-        const int32_t s1 = min(__ldg(a.plan + a.at.tile_slot + tile + 1), a.n_slots);
         float *out = a.partial + ((static_cast<int64_t>(u.slab) * a.n_types + u.type) * a.heads + u.head) * a.n_slots;
-        constexpr int kSlots = kAdders / LANES;  // at a time
-        for (int32_t s = s0; s < s1; s += kSlots) {
-            const int32_t mine = s + tid / LANES;
-            float v = 0.f;
-            int2 slot = make_int2(0, -1);
-            if (mine < s1) {
-                slot = __ldg(reinterpret_cast<const int2 *>(a.plan + a.at.slot) + mine);
-                const int begin = slot.x & 0xffff, count = static_cast<int>(static_cast<uint32_t>(slot.x) >> 16);
-                const int last = min(begin + count, kPlanTile);
-#pragma unroll 4
-                for (int k = begin + tid % LANES; k < last; k += LANES) v += sh.sums[sh.order[k] & (kPlanTile - 1)];
+        must_wait(&sh.summed[in.stage], in.phase);
+        const float *sums = sh.sums[in.stage];
+        uint32_t slot = static_cast<uint32_t>(lane.y);
+        float v = 0.f;
+        if (ok)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            v += sums[word(order[e / 8], e % 8 / 2) >> (e & 1 ? 16 : 0) & (kPlanTile - 1)];
+            if (lane.x >> e & 1) {
+                if (slot < static_cast<uint32_t>(a.n_slots)) out[slot] = v;
+                ++slot;
+                v = 0.f;
             }
-            v = group_sum<LANES>(v);
-            if (tid % LANES == 0 && slot.y >= 0 && slot.y < a.n_slots) out[slot.y] = v;
         }
-        meet();  // the sums and the order have been read
+        __syncwarp();
+        if ((tid & 31) == 0) bar_arrive(shared_address(&sh.read[in.stage]));
+        in.next();
     }
 }
 
 // Pass 1.  Two resident blocks an SM share the units out; in each a warp copies
 // the tiles of the units' windows in bulk (TMA) into a ring of stages, ahead
-// across units, and eight warps add them up.  Every gradient is read once, a
-// few of them at the tensor's ends excepted in no 16-byte line of another; what
-// leaves is one value per slot.  The order of all additions is fixed by the
-// sizes and the plan.
-template <typename E, bool kVec, int LANES>
-__global__ void __launch_bounds__(kGradThreads, 2) bias_grad_tiles(GradArgs a) {
+// across units, four warps add them up and four add the last unit's sums up by
+// slot.  Every gradient is read once; what leaves is one value per slot.  The
+// order of all additions is fixed by the sizes and the plan.
+template <typename E, bool kVec>
+__global__ void __launch_bounds__(kGradThreads, WGS_GRAD_CTAS) bias_grad_tiles(GradArgs a) {
     extern __shared__ __align__(16) char smem[];
     GradShared<E> &sh = *reinterpret_cast<GradShared<E> *>(smem);
     if (threadIdx.x == 0) {
@@ -532,20 +602,28 @@ __global__ void __launch_bounds__(kGradThreads, 2) bias_grad_tiles(GradArgs a) {
             bar_init(shared_address(&sh.full[i]), 1);
             bar_init(shared_address(&sh.empty[i]), kAdders / 32);
         }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(shared_address(&sh.summed[i]), kAdders / 32);
+            bar_init(shared_address(&sh.read[i]), kSlotters / 32);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
     pdl_prologue();
-    if (!plan_matches(a)) {
-        if (threadIdx.x == 0) atomicOr(&g_bucket_error, 1u);
-        return;
-    }
     const int32_t u0 = share_start(a.units, gridDim.x, blockIdx.x);
     const int32_t u1 = share_start(a.units, gridDim.x, blockIdx.x + 1);
-    if (threadIdx.x < kAdders)
-        add_units<E, kVec, LANES>(a, sh, u0, u1);
+    const int tid = threadIdx.x;
+    if (tid < kAdders)
+        add_units<E, kVec>(a, sh, u0, u1);
+    else if (tid < kAdders + kSlotters)
+        slot_units<E>(a, sh, u0, u1, tid - kAdders);
     else
-        copy_units<E>(a, sh, u0, u1, threadIdx.x - kAdders);
+        copy_units<E, kVec>(a, sh, u0, u1, tid - kAdders - kSlotters);
+}
+
+// The d-th slot of the buckets' lists.
+__device__ __forceinline__ int32_t slot_of(const GradArgs &a, int32_t d) {
+    return min(max(__ldg(a.plan + a.at.bucket_slot + d), 0), a.n_slots - 1);
 }
 
 // Pass 2: LANES lanes a (type, bucket, head) add the bucket's slots over the
@@ -562,18 +640,20 @@ __global__ void __launch_bounds__(kThreads) bias_grad_table(GradArgs a, int32_t 
     const int32_t b = i / a.heads, head = i - b * a.heads;
     float v = 0.f;
     if (ok && b < a.n_buckets) {
-        const int32_t d0 = max(__ldg(a.plan + a.at.bucket_dest + b), 0);
-        const int32_t d1 = min(__ldg(a.plan + a.at.bucket_dest + b + 1), a.n_slots);
+        const int32_t d0 = max(__ldg(a.plan + a.at.bucket_first + b), 0);
+        const int32_t d1 = min(__ldg(a.plan + a.at.bucket_first + b + 1), a.n_slots);
         const int64_t step = static_cast<int64_t>(a.n_types) * a.heads * a.n_slots;
         const float *p = a.partial + (static_cast<int64_t>(type) * a.heads + head) * a.n_slots;
         if constexpr (kSlabs) {
-            for (int32_t d = d0; d < d1; ++d)
+            for (int32_t d = d0; d < d1; ++d) {
+                const float *q = p + slot_of(a, d);
 #pragma unroll 4
-                for (int32_t s = lane; s < a.slabs; s += LANES) v += p[s * step + d];
+                for (int32_t s = lane; s < a.slabs; s += LANES) v += q[s * step];
+            }
         } else {
             for (int32_t s = 0; s < a.slabs; ++s)
 #pragma unroll 4
-                for (int32_t d = d0 + lane; d < d1; d += LANES) v += p[s * step + d];
+                for (int32_t d = d0 + lane; d < d1; d += LANES) v += p[s * step + slot_of(a, d)];
         }
     }
     v = group_sum<LANES>(v);
@@ -581,8 +661,71 @@ __global__ void __launch_bounds__(kThreads) bias_grad_table(GradArgs a, int32_t 
         store1<T>(a.table, (static_cast<int64_t>(type) * a.n_buckets + b) * a.heads + head, v);
 }
 
+// Pass 2 where buckets have many values: a block a (type, bucket, head).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) bias_grad_block(GradArgs a) {
+    __shared__ float part[kThreads / 32];
+    pdl_prologue();
+    const bool ok = plan_matches(a);
+    if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_bucket_error, 1u);
+    const int32_t head = blockIdx.x % a.heads, tb = blockIdx.x / a.heads;
+    const int32_t type = tb / a.n_buckets, b = tb - type * a.n_buckets;
+    float v = 0.f;
+    if (ok) {
+        const int32_t d0 = max(__ldg(a.plan + a.at.bucket_first + b), 0);
+        const int32_t d1 = min(__ldg(a.plan + a.at.bucket_first + b + 1), a.n_slots);
+        const int64_t step = static_cast<int64_t>(a.n_types) * a.heads * a.n_slots;
+        const float *p = a.partial + (static_cast<int64_t>(type) * a.heads + head) * a.n_slots;
+        for (int32_t s = 0; s < a.slabs; ++s)
+#pragma unroll 8
+            for (int32_t d = d0 + static_cast<int32_t>(threadIdx.x); d < d1; d += kThreads)
+                v += p[s * step + slot_of(a, d)];
+    }
+    v = group_sum<32>(v);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int k = 1; k < kThreads / 32; ++k) v += part[k];
+        store1<T>(a.table, blockIdx.x, v);
+    }
+}
+
+// Pass 2 where a bucket has few values: a thread a (type, bucket) for all
+// heads, whose slots it looks up once; the threads' slots are neighbours.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) bias_grad_rows(GradArgs a, int32_t blocks) {
+    pdl_prologue();
+    const bool ok = plan_matches(a);
+    if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_bucket_error, 1u);
+    const int32_t type = blockIdx.x / blocks;
+    const int32_t b = (blockIdx.x - type * blocks) * kThreads + static_cast<int32_t>(threadIdx.x);
+    if (b >= a.n_buckets) return;
+    const int32_t d0 = ok ? max(__ldg(a.plan + a.at.bucket_first + b), 0) : 0;
+    const int32_t d1 = ok ? min(__ldg(a.plan + a.at.bucket_first + b + 1), a.n_slots) : 0;
+    const int64_t step = static_cast<int64_t>(a.n_types) * a.heads * a.n_slots;
+    const float *p = a.partial + static_cast<int64_t>(type) * a.heads * a.n_slots;
+    const int64_t out = (static_cast<int64_t>(type) * a.n_buckets + b) * a.heads;
+    constexpr int kHeads = 8;  // at a time: loads in flight
+    for (int32_t h0 = 0; h0 < a.heads; h0 += kHeads) {
+        float v[kHeads];
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k) v[k] = 0.f;
+        for (int32_t d = d0; d < d1; ++d) {
+            const float *q = p + static_cast<int64_t>(h0) * a.n_slots + slot_of(a, d);
+            for (int32_t s = 0; s < a.slabs; ++s, q += step)
+#pragma unroll
+                for (int k = 0; k < kHeads; ++k)
+                    if (h0 + k < a.heads) v[k] += q[static_cast<int64_t>(k) * a.n_slots];
+        }
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k)
+            if (h0 + k < a.heads) store1<T>(a.table, out + h0 + k, v[k]);
+    }
+}
+
 // Blocks of pass 1 at most: two on each of 152 SMs.
-constexpr int64_t kGradBlocks = 304;
+constexpr int64_t kGradBlocks = 152 * WGS_GRAD_CTAS;
 // Windows of a type in a slab at least, on average.
 constexpr int64_t kSlabWindows = 4;
 
@@ -606,11 +749,7 @@ int64_t grad_slabs(int64_t n_win, int64_t heads, int64_t n_types, int64_t n_tile
 
 template <typename E, bool kVec>
 wgs_status launch_tiles(const GradArgs &a, cudaStream_t stream) {
-    // lanes a slot by the slots' average length
-    const int64_t mean = a.n_slots > 0 ? a.n_pairs / a.n_slots : 0;
-    auto kernel = mean < 8    ? bias_grad_tiles<E, kVec, 1>
-                  : mean < 64 ? bias_grad_tiles<E, kVec, 8>
-                              : bias_grad_tiles<E, kVec, 32>;
+    auto kernel = bias_grad_tiles<E, kVec>;
     // More than 48 KB needs the runtime's leave, which belongs to the context;
     // asking on every call needs no record of it.
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -634,6 +773,15 @@ wgs_status launch_table(const GradArgs &a, cudaStream_t stream) {
     const int64_t mean = a.n_slots / a.n_buckets;
     const bool slabs = a.slabs >= mean;
     const int64_t most = slabs ? a.slabs : mean;
+    if (most < 4 && static_cast<int64_t>(a.n_types) * a.n_buckets >= 32 * kThreads) {
+        const int64_t blocks = ceil_div(a.n_buckets, kThreads);
+        if (blocks * a.n_types > INT32_MAX) return WGS_ERR_SHAPE;
+        return launch(bias_grad_rows<T>, dim3(static_cast<unsigned>(blocks * a.n_types)), dim3(kThreads), 0,
+                      stream, a, static_cast<int32_t>(blocks));
+    }
+    if (mean >= 64 && static_cast<int64_t>(a.n_types) * a.heads * a.n_buckets <= INT32_MAX)
+        return launch(bias_grad_block<T>, dim3(static_cast<unsigned>(a.n_types) * a.heads * a.n_buckets),
+                      dim3(kThreads), 0, stream, a);
     const int lanes = most < 4 ? 1 : most < 64 ? 8 : 32;
     const int64_t blocks = ceil_div(static_cast<int64_t>(a.heads) * a.n_buckets * lanes, kThreads);
     if (blocks * a.n_types > INT32_MAX) return WGS_ERR_SHAPE;
@@ -672,7 +820,8 @@ extern "C" wgs_status position_bias(const void *table, const int32_t *bucket, vo
     if (n_buckets < 1 || n_pairs > INT32_MAX - kPlanTile) return WGS_ERR_SHAPE;
     int64_t slabs, out_n, table_n;
     if (!times(n_types, heads, &slabs) || !times(slabs, n_pairs * bytes_of(dtype), &out_n) ||
-        !times(slabs, n_buckets * bytes_of(table_dtype), &table_n))
+        !times(slabs, n_buckets * bytes_of(table_dtype), &table_n) ||
+        static_cast<int64_t>(heads) * n_buckets > INT32_MAX / 32)
         return WGS_ERR_SHAPE;
     if (!table || !bucket || !bias) return WGS_ERR_NULL;
     if (!aligned_to(table, bytes_of(table_dtype)) || !aligned4(bucket) ||
