@@ -548,11 +548,8 @@ def group_norm_act(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
     index, n, spatial, channels, w, b, pt = _norm_args(x, groups, weight, bias, act)
     kind, device = x.dtype, x.device
     y = torch.empty_like(x) if out is None else _into(out, x.shape, kind, device, "out")
-    if mean is None and rstd is None:
-        m, r = torch.empty((2, n, groups), dtype=torch.float32, device=device).unbind(0)
-    else:
-        m = _into(mean, (n, groups), torch.float32, device, "mean")
-        r = _into(rstd, (n, groups), torch.float32, device, "rstd")
+    m = _into(mean, (n, groups), torch.float32, device, "mean")
+    r = _into(rstd, (n, groups), torch.float32, device, "rstd")
     ws = _space(workspace, lambda: group_norm_act_workspace_bytes(n, spatial, channels, groups), device)
     _run("group_norm_act", _capi.load().group_norm_act, index, x.data_ptr(), w, b,
          _given(y, "out", kind, index), _given(m, "mean", torch.float32, index),
@@ -582,11 +579,8 @@ def group_norm_act_bwd(grad_y: torch.Tensor, x: torch.Tensor, groups: int, mean:
     gw = gb = None
     pw = pb = 0
     if weight is not None:
-        if grad_weight is None and grad_bias is None:
-            gw, gb = torch.empty((2, channels), dtype=pt, device=device).unbind(0)
-        else:
-            gw = _into(grad_weight, (channels,), pt, device, "grad_weight")
-            gb = _into(grad_bias, (channels,), pt, device, "grad_bias")
+        gw = _into(grad_weight, (channels,), pt, device, "grad_weight")
+        gb = _into(grad_bias, (channels,), pt, device, "grad_bias")
         pw, pb = _given(gw, "grad_weight", pt, index), _given(gb, "grad_bias", pt, index)
     elif grad_weight is not None or grad_bias is not None:
         _fail("grad_weight and grad_bias need weight and bias")

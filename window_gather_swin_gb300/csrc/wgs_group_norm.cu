@@ -80,6 +80,11 @@ enum : int { kNone = 0, kSilu = 1, kGeluTanh = 2 };
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// FP32 pairs on the packed pipe: each half the correctly rounded operation.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+
 // kV neighbouring elements in one register value, handled as pairs (a single
 // element is the first of a pair).
 template <typename E, int kV>
@@ -118,7 +123,7 @@ struct Chunk {
             if constexpr (kV == 1)
                 return make_float2(__uint_as_float(r) + c.x, 0.f);
             else
-                return __fadd2_rn(make_float2(__uint_as_float(word_of(r, 2 * p)),
+                return add2(make_float2(__uint_as_float(word_of(r, 2 * p)),
                                               __uint_as_float(word_of(r, 2 * p + 1))), c);
         } else {
             return E::widen_add2(word_of(r, p), c);
@@ -193,16 +198,16 @@ __device__ __forceinline__ float2 gate(float2 z) {
     constexpr float m = k32 ? -1.0f : -kLog2e;
     float2 t;
     if constexpr (kAct == kSilu)
-        t = __fmul2_rn(z, both(m));
+        t = mul2(z, both(m));
     else
-        t = __fmul2_rn(z, __ffma2_rn(__fmul2_rn(z, z), both(m * kTwoK * kCubic), both(m * kTwoK)));
+        t = mul2(z, fma2(mul2(z, z), both(m * kTwoK * kCubic), both(m * kTwoK)));
     if constexpr (k32) {
         return make_float2(1.0f / (1.0f + expf(t.x)), 1.0f / (1.0f + expf(t.y)));
     } else {
         float2 e, s;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-        e = __fadd2_rn(e, both(1.0f));
+        e = add2(e, both(1.0f));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(e.x));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(e.y));
         return s;
@@ -212,7 +217,7 @@ __device__ __forceinline__ float2 gate(float2 z) {
 template <int kAct, bool k32>
 __device__ __forceinline__ float2 act(float2 z) {
     if constexpr (kAct == kNone) return z;
-    return __fmul2_rn(z, gate<kAct, k32>(z));
+    return mul2(z, gate<kAct, k32>(z));
 }
 
 // act'(z) = s + z s (1 - s) q', with s the gate.
@@ -220,16 +225,16 @@ template <int kAct, bool k32>
 __device__ __forceinline__ float2 act_grad(float2 z) {
     if constexpr (kAct == kNone) return both(1.0f);
     const float2 s = gate<kAct, k32>(z);
-    const float2 p = __fmul2_rn(z, s);
-    const float2 rest = __ffma2_rn(s, both(-1.0f), both(1.0f));
+    const float2 p = mul2(z, s);
+    const float2 rest = fma2(s, both(-1.0f), both(1.0f));
     if constexpr (kAct == kSilu) {
-        return __ffma2_rn(p, rest, s);
+        return fma2(p, rest, s);
     } else {
         // q' = kTwoK + 3 kTwoK kCubic z^2.  Far out z s (1 - s) is 0, and there
         // the slope may be infinite: it is cut to what a finite z^2 gives
-        float2 z2 = __fmul2_rn(z, z);
+        float2 z2 = mul2(z, z);
         z2 = make_float2(fminf(z2.x, 1e30f), fminf(z2.y, 1e30f));
-        return __ffma2_rn(__fmul2_rn(p, rest), __ffma2_rn(z2, both(3.0f * kTwoK * kCubic), both(kTwoK)), s);
+        return fma2(mul2(p, rest), fma2(z2, both(3.0f * kTwoK * kCubic), both(kTwoK)), s);
     }
 }
 
@@ -542,7 +547,7 @@ __device__ __forceinline__ void add_row_groups(float2 *red, const Job &job, int3
             const float2 *p = red + e * wide + job.j;
             float2 t = *p;
 #pragma unroll 4
-            for (int g = 1; g < job.row_groups; ++g) t = __fadd2_rn(t, p[g * wide * kV]);
+            for (int g = 1; g < job.row_groups; ++g) t = add2(t, p[g * wide * kV]);
             done(e, (c0 + job.j) * kV + e, t);
         }
     __syncthreads();
@@ -569,31 +574,41 @@ __device__ __forceinline__ float values_of(const NormArgs &a, int32_t s, int32_t
     return static_cast<float>(a.slabs1.of(s, count)) * static_cast<float>(a.per_group);
 }
 
-// For every group g: the sum of value(part, g, own(g)) over the parts [0,
-// parts), in a fixed order, to done(g, sum, own(g)).  Neighbouring threads take
-// neighbouring groups, and the threads beyond the groups a share of the
-// parts each.  smem holds a pair a thread.
-template <typename Own, typename Value, typename Done>
-__device__ __forceinline__ void add_parts(float2 *smem, const Job &job, int groups, int parts, Own own,
-                                          Value value, Done done) {
+// For every group g: the sum of value(part, g's pair of the part, its pair of
+// part 0) over the parts, in a fixed order, to done(g, sum, pair of part 0).
+// part[parts][groups].  Neighbouring threads take neighbouring groups, and the
+// threads beyond the groups a share of the parts each.  smem holds a pair a
+// thread.  then() runs once the first loads are under way: what it starts
+// should not be ahead of them on the way to memory.
+template <typename Value, typename Then, typename Done>
+__device__ __forceinline__ void add_parts(float2 *smem, const Job &job, const float2 *part, int groups, int parts,
+                                          Value value, Then then, Done done) {
+    constexpr int kFirst = 16;
     const int wide = min(groups, job.threads);
     const int lanes = job.threads / wide;
     const int l = job.tid / wide, j = job.tid - l * wide;
     for (int g0 = 0; g0 < groups; g0 += wide) {
         const int g = g0 + j;
+        const bool live = l < lanes && g < groups;
+        const float2 *q = part + (live ? g : 0);
+        const float2 own = __ldcg(q);
+        float2 v[kFirst];
+#pragma unroll
+        for (int k = 0; k < kFirst; ++k)
+            if (live && l + k * lanes < parts) v[k] = __ldcg(q + (l + k * lanes) * groups);
+        if (g0 == 0) then();
         float2 t = make_float2(0.f, 0.f);
-        float o = 0.f;
-        if (l < lanes && g < groups) {
-            o = own(g);
-#pragma unroll 16
-            for (int p = l; p < parts; p += lanes) t = __fadd2_rn(t, value(p, g, o));
-        }
+#pragma unroll
+        for (int k = 0; k < kFirst; ++k)
+            if (live && l + k * lanes < parts) t = add2(t, value(l + k * lanes, v[k], own));
+        if (live)
+            for (int p = l + kFirst * lanes; p < parts; p += lanes) t = add2(t, value(p, __ldcg(q + p * groups), own));
         smem[job.tid] = t;
         __syncthreads();
-        if (l == 0 && g < groups) {
+        if (l == 0 && live) {
 #pragma unroll 8
-            for (int q = 1; q < min(lanes, parts); ++q) t = __fadd2_rn(t, smem[q * wide + j]);
-            done(g, t, o);
+            for (int k = 1; k < min(lanes, parts); ++k) t = add2(t, smem[k * wide + j]);
+            done(g, t, own);
         }
         __syncthreads();
     }
@@ -700,8 +715,8 @@ __device__ void stats_pass(const NormArgs &a, const Job &job, Bars &bars, float2
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
                 const float2 d = C::plus(v[0], p, k[p]);
-                s1[p] = __fadd2_rn(s1[p], d);
-                s2[p] = __ffma2_rn(d, d, s2[p]);
+                s1[p] = add2(s1[p], d);
+                s2[p] = fma2(d, d, s2[p]);
             }
         });
         add_row_groups<kV>(red, job, c0, wide, s1, s2, [&](int e, int c, float2 t) {
@@ -749,8 +764,8 @@ __device__ void stats_pass(const NormArgs &a, const Job &job, Bars &bars, float2
     cluster.sync();  // the others' shared memory has been read; the result is visible to them
 }
 
-// Forward, pass 2, the slab's last rows first.  They are on their way before
-// the statistics of the groups, which lie behind the slots.
+// Forward, pass 2, the slab's last rows first.  The statistics of the groups
+// lie behind the slots.
 template <typename E, int kV, int kAct>
 __device__ void apply_pass(const NormArgs &a, const Job &job, Bars &bars, float2 *smem) {
     using C = Chunk<E, kV>;
@@ -758,26 +773,25 @@ __device__ void apply_pass(const NormArgs &a, const Job &job, Bars &bars, float2
     const int64_t row_bytes = static_cast<int64_t>(a.chunks) * C::kBytes;
     const int64_t base = (job.sample * a.spatial + job.r0) * row_bytes;
     const uint64_t policy = l2_policy(a.last_use);
-    float2 *stat = smem + a.ring / 8;
-    float w[kV], b[kV];
-    params<E, kV>(a.weight, job.j, a.p32, 1.f, w);
-    params<E, kV>(a.bias, job.j, a.p32, 0.f, b);
+    // behind the slots: the groups' (-mean, rstd), the channels' (weight, bias),
+    // a pair a thread
+    float2 *stat = smem + a.ring / 8, *wb = stat + a.groups, *lanes = wb + a.channels;
+    for (int c = job.tid; c < a.channels; c += job.threads)
+        wb[c] = make_float2(param<E>(a.weight, c, a.p32, 1.f), param<E>(a.bias, c, a.p32, 0.f));
     Stream<C, 1> in(job, bars);
     in.src[0] = a.x;
-    in.start(smem, base, row_bytes, min(job.columns, a.chunks), true, policy);
     wait_for_sums(a);
     // (mean, rstd) of the sample's groups
-    const float2 *part = a.groups_part + job.sample * a.clusters * a.groups;
     add_parts(
-        stat + a.groups, job, a.groups, a.clusters, [&](int g) { return __ldcg(part + g).x; },
-        [&](int c, int g, float ref) {
-            const float2 v = __ldcg(part + c * a.groups + g);
-            const float n = values_of(a, c * a.cluster, a.cluster), d = v.x - ref;
+        lanes, job, a.groups_part + job.sample * a.clusters * a.groups, a.groups, a.clusters,
+        [&](int c, float2 v, float2 own) {
+            const float n = values_of(a, c * a.cluster, a.cluster), d = v.x - own.x;
             return make_float2(n * d, fmaf(n * d, d, v.y));
         },
-        [&](int g, float2 t, float ref) {
+        [&] { in.start(smem, base, row_bytes, min(job.columns, a.chunks), true, policy); },
+        [&](int g, float2 t, float2 own) {
             const float n = static_cast<float>(a.spatial) * static_cast<float>(a.per_group), m = t.x / n;
-            const float mean = ref + m;
+            const float mean = own.x + m;
             const float rstd = 1.0f / sqrtf(not_below_zero(fmaf(-m, t.x, t.y)) / n + a.eps);
             stat[g] = make_float2(-mean, rstd);
             if (job.r0 == 0 && a.mean) {
@@ -790,21 +804,20 @@ __device__ void apply_pass(const NormArgs &a, const Job &job, Bars &bars, float2
         if (c0 > 0) {
             __syncthreads();  // the slots have been read
             in.start(smem, base + c0 * C::kBytes, row_bytes, wide, true, policy);
-            params<E, kV>(a.weight, c, a.p32, 1.f, w);
-            params<E, kV>(a.bias, c, a.p32, 0.f, b);
         }
         float2 mean[kP], scale[kP], shift[kP], st;
         mean[kP - 1].y = scale[kP - 1].y = shift[kP - 1].y = 0.f;
         each_channel<kV>(a, c, [&](int32_t g) { st = stat[g]; }, [&](int e) {
+            const float2 f = wb[c * kV + e];
             set_half(mean, e, st.x);
-            set_half(scale, e, st.y * w[e]);
-            set_half(shift, e, b[e]);
+            set_half(scale, e, st.y * f.x);
+            set_half(shift, e, f.y);
         });
         in.run([&](const typename C::Raw (&v)[1], int64_t o) {
             float2 y[kP];
 #pragma unroll
             for (int p = 0; p < kP; ++p)
-                y[p] = act<kAct, C::k32>(__ffma2_rn(C::plus(v[0], p, mean[p]), scale[p], shift[p]));
+                y[p] = act<kAct, C::k32>(fma2(C::plus(v[0], p, mean[p]), scale[p], shift[p]));
             C::store(a.out + o, y, policy);
         });
     }
@@ -874,10 +887,10 @@ __device__ void sums_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
                 const float2 xc = C::plus(v[0], p, t.mean[p]);
-                const float2 dz = __fmul2_rn(
-                    C::wide(v[1], p), act_grad<kAct, C::k32>(__ffma2_rn(xc, t.scale[p], t.shift[p])));
-                s1[p] = __fadd2_rn(s1[p], dz);
-                s2[p] = __ffma2_rn(dz, xc, s2[p]);
+                const float2 dz = mul2(
+                    C::wide(v[1], p), act_grad<kAct, C::k32>(fma2(xc, t.scale[p], t.shift[p])));
+                s1[p] = add2(s1[p], dz);
+                s2[p] = fma2(dz, xc, s2[p]);
             }
         });
         // h = (x - mean) rstd
@@ -916,7 +929,7 @@ __device__ void sums_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
     auto gather = [&](float2 *mine, float2 *out, int count) {
         for (int i = job.rank * job.threads + job.tid; i < count; i += a.cluster * job.threads) {
             float2 t = make_float2(0.f, 0.f);
-            for (int r = 0; r < a.cluster; ++r) t = __fadd2_rn(t, cluster.map_shared_rank(mine, r)[i]);
+            for (int r = 0; r < a.cluster; ++r) t = add2(t, cluster.map_shared_rank(mine, r)[i]);
             out[i] = t;
         }
     };
@@ -942,13 +955,12 @@ __device__ void grad_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
     t.read(a, job.j);
     Stream<C, 2> in(job, bars);
     in.src[0] = a.x, in.src[1] = a.gy;
-    in.start(smem, base, row_bytes, min(job.columns, a.chunks), true, policy);
     wait_for_sums(a);
-    const float2 *part = a.groups_part + job.sample * a.clusters * a.groups;
     add_parts(
-        coef + a.groups, job, a.groups, a.clusters, [&](int) { return 0.f; },
-        [&](int c, int g, float) { return __ldcg(part + c * a.groups + g); },
-        [&](int g, float2 v, float) {
+        coef + a.groups, job, a.groups_part + job.sample * a.clusters * a.groups, a.groups, a.clusters,
+        [](int, float2 v, float2) { return v; },
+        [&] { in.start(smem, base, row_bytes, min(job.columns, a.chunks), true, policy); },
+        [&](int g, float2 v, float2) {
             const float n = static_cast<float>(a.spatial) * static_cast<float>(a.per_group), rstd = stat[g].y;
             coef[g] = make_float2(-rstd * (v.x / n), -rstd * rstd * (v.y / n));
         });
@@ -971,9 +983,9 @@ __device__ void grad_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
                 const float2 xc = C::plus(v[0], p, t.mean[p]);
-                const float2 dz = __fmul2_rn(
-                    C::wide(v[1], p), act_grad<kAct, C::k32>(__ffma2_rn(xc, t.scale[p], t.shift[p])));
-                y[p] = __ffma2_rn(xc, k2[p], __ffma2_rn(t.scale[p], dz, k1[p]));
+                const float2 dz = mul2(
+                    C::wide(v[1], p), act_grad<kAct, C::k32>(fma2(xc, t.scale[p], t.shift[p])));
+                y[p] = fma2(xc, k2[p], fma2(t.scale[p], dz, k1[p]));
             }
             C::store(a.out + o, y, policy);
         });
@@ -1002,7 +1014,7 @@ __global__ void __launch_bounds__(1024) norm_params(NormArgs a, int64_t parts) {
     float2 t = make_float2(0.f, 0.f);
     if (c < a.channels) {
 #pragma unroll 4
-        for (int64_t i = l; i < parts; i += 32) t = __fadd2_rn(t, __ldcg(a.chan_part + i * a.channels + c));
+        for (int64_t i = l; i < parts; i += 32) t = add2(t, __ldcg(a.chan_part + i * a.channels + c));
     }
     red[l][j] = t;
     __syncthreads();
@@ -1031,6 +1043,9 @@ constexpr int64_t kMinSlabRows = 16;
 // launch of a cluster.
 constexpr int64_t kOneLaunch = int64_t{1} << 19;
 
+// Slabs of a sample in pass 1 at most.
+constexpr int64_t kMaxParts = 152;
+
 struct Plan {
     int64_t x_bytes, group_part, chan_part;  // bytes
     int64_t slabs1, slabs2, cluster;
@@ -1057,6 +1072,9 @@ bool plan_of(int64_t n, int64_t spatial, int64_t channels, int64_t groups, int64
             // the launch's blocks over the samples, no more than are resident
             auto share = [&](int64_t blocks) { return blocks / n < most ? blocks / n : most; };
             z->slabs1 = share(backward ? WGS_NORM_B1B : WGS_NORM_B1F);
+            // what pass 2 joins: 152 pairs a group come in one round of loads
+            // ([131040,192] fp16: 32.4 us; with 304 33.5)
+            if (z->slabs1 > kMaxParts) z->slabs1 = kMaxParts;
             z->slabs2 = share(backward ? WGS_NORM_B2B : WGS_NORM_B2F);
         }
     }
@@ -1094,7 +1112,7 @@ wgs_status run(NormArgs a, const Plan &z, int act, bool backward, int64_t n, cud
         // Shared memory.  Pass 1: the channels' sums, and in one place the
         // slots, the row groups' sums and the groups'; where one walk covers
         // the row the channels' lie over the slots too.  Pass 2: the slots,
-        // the groups' values, a pair a thread.
+        // the groups' values, in the forward the channels', a pair a thread.
         a.ring = C::kBytes < 4 ? 0 : threads * C::kBytes * (backward ? 2 * kRowsBwd * kStagesBwd : kRowsFwd * kStagesFwd);
         const int red = 8 * (threads * kV > a.groups ? threads * kV : a.groups), ch = 8 * a.channels;
         const int pass1 = columns == a.chunks ? (ch + red > a.ring ? ch + red : a.ring)
@@ -1102,7 +1120,7 @@ wgs_status run(NormArgs a, const Plan &z, int act, bool backward, int64_t n, cud
         // (the backward's pass 1 keeps the groups' statistics behind that)
         a.behind = (pass1 + 15) / 16 * 16;
         const int one = passes & 1 ? a.behind + (backward ? 8 * a.groups : 0) : 0;
-        const int two = passes & 2 ? a.ring + (backward ? 16 : 8) * a.groups + 8 * threads : 0;
+        const int two = passes & 2 ? a.ring + (backward ? 16 * a.groups : 8 * (a.groups + a.channels)) + 8 * threads : 0;
         const int smem = one > two ? one : two;
         // Above 48 KB a kernel needs the runtime's leave, which belongs to the
         // context; asking for the same amount on every call needs no record of it.
