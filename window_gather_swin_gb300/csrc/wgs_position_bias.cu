@@ -326,6 +326,15 @@ struct Unit {
         type = u % a.n_types;
         tile = u / a.n_types;
     }
+    __device__ void next(const GradArgs &a) {
+        if (++head < a.heads) return;
+        head = 0;
+        if (++slab < a.slabs) return;
+        slab = 0;
+        if (++type < a.n_types) return;
+        type = 0;
+        ++tile;
+    }
 };
 
 // Warps of a block: four add windows up, four add the sums up by slot, one copies.
@@ -351,6 +360,7 @@ struct GradShared {
     alignas(16) char stage[kGradStages<E>][kStageBytes<E>];
     alignas(16) float sums[2][kPlanTile];  // of a unit, and of the next
     int32_t list[kListed];
+    int32_t counts[8];
     int32_t said[kGradStages<E>];    // of the stage's window, see kData
     int32_t window[kGradStages<E>];
     alignas(8) uint64_t full[kGradStages<E>], empty[kGradStages<E>];
@@ -376,17 +386,20 @@ __device__ __forceinline__ void must_wait(const uint64_t *bar, uint32_t parity) 
 // One lane does it, in as few steps a window as can be: a window's latency
 // here bounds what the block takes in.
 template <typename E, bool kVec>
-__device__ void copy_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int32_t u1, int lane) {
+__device__ void copy_units(const GradArgs &a, GradShared<E> &sh, Unit u, int32_t units, int32_t listed, int lane) {
     constexpr int kES = kBytes<E>, kRing = kGradStages<E>;
     const uint64_t policy = l2_policy(true);
     const uint32_t full = shared_address(sh.full), empty = shared_address(sh.empty), slots = shared_address(sh.stage);
     const char *end = a.grad + a.grad_bytes;
     int stage = 0;
     uint32_t phase = 1;  // of the wait for an empty stage: a new barrier's counts as past
-    int32_t listed_type = -1, listed_slab = -1, listed = 0;
-    for (int32_t i = u0; i < u1; ++i) {
-        const Unit u(a, i);
-        const int32_t w0 = share_start(a.n_win, a.slabs, u.slab), w1 = share_start(a.n_win, a.slabs, u.slab + 1);
+    int32_t listed_type = listed >= 0 ? u.type : -1, listed_slab = u.slab;  // of the list
+    int32_t slab = -1, w0 = 0, w1 = 0;
+    for (; units > 0; --units, u.next(a)) {
+        if (u.slab != slab) {
+            slab = u.slab;
+            w0 = share_start(a.n_win, a.slabs, slab), w1 = share_start(a.n_win, a.slabs, slab + 1);
+        }
         const int64_t p0 = static_cast<int64_t>(u.tile) * kPlanTile;
         const uint32_t bytes = static_cast<uint32_t>(min(a.n_pairs - p0, static_cast<int64_t>(kPlanTile))) * kES;
         const char *tile0 = a.grad + (static_cast<int64_t>(u.head) * a.n_pairs + p0) * kES;
@@ -478,7 +491,7 @@ __device__ void copy_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int
 // The adding warps: a unit's windows pair by pair into FP32 registers, the
 // sums into shared memory.
 template <typename E, bool kVec>
-__device__ void add_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int32_t u1) {
+__device__ void add_units(const GradArgs &a, GradShared<E> &sh, Unit u, int32_t units) {
     constexpr bool k32 = std::is_same<E, F32>::value;
     constexpr int kN = kVec ? (k32 ? 4 : 8) : 1;       // neighbouring pairs of a thread
     constexpr int kOwn = kPlanTile / (kAdders * kN);   // runs of them
@@ -486,19 +499,18 @@ __device__ void add_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int3
     const uint32_t full = shared_address(sh.full), empty = shared_address(sh.empty);
     RingPlace<kGradStages<E>> ring;
     RingPlace<2> out;
-    for (int32_t i = u0; i < u1; ++i) {
+    for (; units > 0; --units, u.next(a)) {
         float acc[kOwn * kN];
 #pragma unroll
         for (int k = 0; k < kOwn * kN; ++k) acc[k] = 0.f;
+        const int64_t p0 = static_cast<int64_t>(u.tile) * kPlanTile;
+        const int32_t len = static_cast<int32_t>(min(a.n_pairs - p0, static_cast<int64_t>(kPlanTile)));
         int said;
         do {
             if (!bar_wait(full + 8 * ring.stage, ring.phase)) atomicOr(&g_bucket_error, 1u);
             said = sh.said[ring.stage];
             const char *at = sh.stage[ring.stage];
             if (!kVec && (said & kDirect)) {
-                const Unit u(a, i);
-                const int64_t p0 = static_cast<int64_t>(u.tile) * kPlanTile;
-                const int32_t len = static_cast<int32_t>(min(a.n_pairs - p0, static_cast<int64_t>(kPlanTile)));
                 const int64_t first = (static_cast<int64_t>(sh.window[ring.stage]) * a.heads + u.head) * a.n_pairs + p0;
 #pragma unroll
                 for (int k = 0; k < kOwn; ++k)
@@ -508,7 +520,7 @@ __device__ void add_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int3
                         if (e < len) acc[k * kN + j] += load1<E>(a.grad, first + e);
                     }
             } else if (said & kData) {
-                // (a short tile's end adds what an earlier one left: no slot names it)
+                // (a short tile's last runs may add what an earlier one left: no slot names it)
                 if constexpr (kVec) {
 #pragma unroll
                     for (int k = 0; k < kOwn; ++k) {
@@ -525,9 +537,13 @@ __device__ void add_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int3
                         }
                     }
                 } else {
-                    const char *q = at + ((said & 7) + tid) * kBytes<E>;
+                    using Raw = std::conditional_t<k32, float, uint16_t>;
+                    const Raw *q = reinterpret_cast<const Raw *>(at) + (said & 7) + tid;
+                    Raw v[kOwn];  // all under way before the first is added
 #pragma unroll
-                    for (int k = 0; k < kOwn; ++k) acc[k] += load1<E>(q, k * kAdders);
+                    for (int k = 0; k < kOwn; ++k) v[k] = q[k * kAdders];
+#pragma unroll
+                    for (int k = 0; k < kOwn; ++k) acc[k] += load1<E>(&v[k], 0);
                 }
             }
             __syncwarp();
@@ -546,20 +562,23 @@ __device__ void add_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int3
     }
 }
 
+__device__ __forceinline__ void store_if(bool yes, float *p, float v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %0, 0;\n\t@p st.global.f32 [%1], %2;\n\t}" ::"r"(static_cast<int>(yes)), "l"(p), "f"(v) : "memory");
+}
+
 // The slot warps: a unit's sums slot by slot, while the next unit's windows are
 // added up.  A thread is a lane of the plan: 32 entries of the tile's order,
 // whose sums it adds from slot end to slot end.  (A thread a slot took
 // several times as long: slots are short and long, and named by loads.)
 template <typename E>
-__device__ void slot_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int32_t u1, int tid) {
+__device__ void slot_units(const GradArgs &a, GradShared<E> &sh, Unit u, int32_t units, int tid) {
     RingPlace<2> in;
     int32_t tile = -1;
     uint4 order[4];
     int2 lane;
     const bool ok = plan_matches(a);  // else nothing of it is followed
     if (!ok && tid == 0) atomicOr(&g_bucket_error, 1u);
-    for (int32_t i = u0; i < u1; ++i) {
-        const Unit u(a, i);
+    for (; units > 0; --units, u.next(a)) {
         if (u.tile != tile && ok) {
             tile = u.tile;
             const uint4 *oq = reinterpret_cast<const uint4 *>(a.plan + a.at.order) + tile * (kPlanTile / 8);
@@ -570,16 +589,21 @@ __device__ void slot_units(const GradArgs &a, GradShared<E> &sh, int32_t u0, int
         float *out = a.partial + ((static_cast<int64_t>(u.slab) * a.n_types + u.type) * a.heads + u.head) * a.n_slots;
         must_wait(&sh.summed[in.stage], in.phase);
         const float *sums = sh.sums[in.stage];
-        uint32_t slot = static_cast<uint32_t>(lane.y);
-        float v = 0.f;
-        if (ok)
+        if (ok) {
+            float v[32];  // all under way before the first is added
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            v += sums[word(order[e / 8], e % 8 / 2) >> (e & 1 ? 16 : 0) & (kPlanTile - 1)];
-            if (lane.x >> e & 1) {
-                if (slot < static_cast<uint32_t>(a.n_slots)) out[slot] = v;
-                ++slot;
-                v = 0.f;
+            for (int e = 0; e < 32; ++e)
+                v[e] = sums[word(order[e / 8], e % 8 / 2) >> (e & 1 ? 16 : 0) & (kPlanTile - 1)];
+            // without branches: lanes end their slots at different entries
+            float *to = out + lane.y, sum = 0.f;
+            const float *end = out + a.n_slots;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                sum += v[e];
+                const bool last = lane.x >> e & 1;
+                store_if(last && to >= out && to < end, to, sum);
+                to += last;
+                sum = last ? 0.f : sum;
             }
         }
         __syncwarp();
@@ -611,14 +635,57 @@ __global__ void __launch_bounds__(kGradThreads, WGS_GRAD_CTAS) bias_grad_tiles(G
     __syncthreads();
     pdl_prologue();
     const int32_t u0 = share_start(a.units, gridDim.x, blockIdx.x);
-    const int32_t u1 = share_start(a.units, gridDim.x, blockIdx.x + 1);
+    const int32_t units = share_start(a.units, gridDim.x, blockIdx.x + 1) - u0;
+    const Unit u(a, u0);
     const int tid = threadIdx.x;
+    int32_t listed = -1;
+    if (a.win_type) {
+        // the first unit's windows by eight warps at once: nothing is copied before
+        const int32_t w0 = share_start(a.n_win, a.slabs, u.slab), w1 = share_start(a.n_win, a.slabs, u.slab + 1);
+        if (w1 - w0 <= kListed) {
+            constexpr int kEach = kListed / 8;
+            const int warp = tid >> 5, lane = tid & 31;
+            unsigned hits[kEach / 32];
+            int32_t count = 0;
+            if (warp < 8) {
+                int32_t t[kEach / 32];
+#pragma unroll
+                for (int k = 0; k < kEach / 32; ++k) {
+                    const int32_t at = w0 + warp * kEach + 32 * k + lane;
+                    t[k] = at < w1 ? __ldg(a.win_type + at) : u.type - 1;
+                    if (at < w1 && (t[k] < 0 || t[k] >= a.n_types)) atomicOr(&g_bucket_error, 1u);
+                }
+#pragma unroll
+                for (int k = 0; k < kEach / 32; ++k) {
+                    const int32_t at = w0 + warp * kEach + 32 * k + lane;
+                    hits[k] = __ballot_sync(0xffffffffu, at < w1 && t[k] == u.type);
+                    count += __popc(hits[k]);
+                }
+                if (lane == 0) sh.counts[warp] = count;
+            }
+            __syncthreads();
+            listed = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (q == warp) count = listed;  // this warp's first place
+                listed += sh.counts[q];
+            }
+            if (warp < 8)
+#pragma unroll
+                for (int k = 0; k < kEach / 32; ++k) {
+                    if (hits[k] >> lane & 1)
+                        sh.list[count + __popc(hits[k] & ((1u << lane) - 1u))] = w0 + warp * kEach + 32 * k + lane;
+                    count += __popc(hits[k]);
+                }
+            __syncthreads();
+        }
+    }
     if (tid < kAdders)
-        add_units<E, kVec>(a, sh, u0, u1);
+        add_units<E, kVec>(a, sh, u, units);
     else if (tid < kAdders + kSlotters)
-        slot_units<E>(a, sh, u0, u1, tid - kAdders);
+        slot_units<E>(a, sh, u, units, tid - kAdders);
     else
-        copy_units<E, kVec>(a, sh, u0, u1, tid - kAdders - kSlotters);
+        copy_units<E, kVec>(a, sh, u, units, listed, tid - kAdders - kSlotters);
 }
 
 // The d-th slot of the buckets' lists.
@@ -662,9 +729,11 @@ __global__ void __launch_bounds__(kThreads) bias_grad_table(GradArgs a, int32_t 
 }
 
 // Pass 2 where buckets have many values: a block a (type, bucket, head).
+constexpr int kBlockThreads = 1024;
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) bias_grad_block(GradArgs a) {
-    __shared__ float part[kThreads / 32];
+__global__ void __launch_bounds__(kBlockThreads) bias_grad_block(GradArgs a) {
+    __shared__ float part[kBlockThreads / 32];
     pdl_prologue();
     const bool ok = plan_matches(a);
     if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_bucket_error, 1u);
@@ -678,7 +747,7 @@ __global__ void __launch_bounds__(kThreads) bias_grad_block(GradArgs a) {
         const float *p = a.partial + (static_cast<int64_t>(type) * a.heads + head) * a.n_slots;
         for (int32_t s = 0; s < a.slabs; ++s)
 #pragma unroll 8
-            for (int32_t d = d0 + static_cast<int32_t>(threadIdx.x); d < d1; d += kThreads)
+            for (int32_t d = d0 + static_cast<int32_t>(threadIdx.x); d < d1; d += kBlockThreads)
                 v += p[s * step + slot_of(a, d)];
     }
     v = group_sum<32>(v);
@@ -686,7 +755,7 @@ __global__ void __launch_bounds__(kThreads) bias_grad_block(GradArgs a) {
     __syncthreads();
     if (threadIdx.x == 0) {
 #pragma unroll
-        for (int k = 1; k < kThreads / 32; ++k) v += part[k];
+        for (int k = 1; k < kBlockThreads / 32; ++k) v += part[k];
         store1<T>(a.table, blockIdx.x, v);
     }
 }
@@ -781,7 +850,7 @@ wgs_status launch_table(const GradArgs &a, cudaStream_t stream) {
     }
     if (mean >= 64 && static_cast<int64_t>(a.n_types) * a.heads * a.n_buckets <= INT32_MAX)
         return launch(bias_grad_block<T>, dim3(static_cast<unsigned>(a.n_types) * a.heads * a.n_buckets),
-                      dim3(kThreads), 0, stream, a);
+                      dim3(kBlockThreads), 0, stream, a);
     const int lanes = most < 4 ? 1 : most < 64 ? 8 : 32;
     const int64_t blocks = ceil_div(static_cast<int64_t>(a.heads) * a.n_buckets * lanes, kThreads);
     if (blocks * a.n_types > INT32_MAX) return WGS_ERR_SHAPE;
