@@ -34,7 +34,10 @@
  *     (an index-driven kernel also reads its first index entries, L2 only,
  *     to steer those fetches).  No value read before the previous kernel
  *     has completed reaches a result: indices and rows are read again after
- *     the wait, so the usual stream order holds for every buffer.
+ *     the wait, so the usual stream order holds for every buffer.  (A call of
+ *     several kernels, group_norm_act and its backward, has its later ones
+ *     read the call's inputs while its first one runs, never before that one
+ *     has waited.)
  *   - Arguments are checked before anything is launched; a failed check
  *     returns a status and launches nothing.  A launch failure reported by
  *     the runtime returns WGS_ERR_LAUNCH.
@@ -55,7 +58,8 @@
  *     which belongs to the context: the first call on a device does it, and
  *     in a later context (after cudaDeviceReset, say) the first launch there
  *     is rejected by the runtime, the limit raised and the launch retried;
- *     make that call outside stream capture too.
+ *     make that call outside stream capture too.  (position_bias_bwd and the
+ *     group norms raise theirs on every call, which captures as well.)
  */
 #ifndef WGS_H
 #define WGS_H
@@ -461,12 +465,12 @@ wgs_status wgs_build_bucket_plan(const int32_t *bucket_host, int64_t n_pairs, in
  *   workspace  at least wgs_group_norm_act_workspace_bytes(...) bytes,
  *           16-byte aligned, disjoint from the tensors; its contents on entry
  *           do not matter.  Calls that overlap on the GPU need their own.
- * channels: a multiple of groups, at most 4096, and groups at most 2048 (else
- * WGS_ERR_WIDTH); n at most
- * 65535.  n == 0 or spatial == 0 launches nothing.  The 16-byte path needs
- * channels a multiple of 4 (f32) or 8 (16-bit types) and 16-byte aligned x
- * and y; otherwise rows are walked element by element.  Sums run in an order that depends on
- * the sizes alone. */
+ * channels: a multiple of groups, at most 4096, with groups at most 2048 (else
+ * WGS_ERR_WIDTH).  n at most 65535, spatial below 2^31 (else WGS_ERR_SHAPE);
+ * n == 0 or spatial == 0 launches nothing.  Rows are moved in 16-byte chunks
+ * when channels is a multiple of 4 (f32) or 8 (16-bit types) and x and y are
+ * 16-byte aligned, else in pairs of elements or single ones.  Sums run in an
+ * order that depends on the sizes alone. */
 size_t wgs_group_norm_act_workspace_bytes(int64_t n, int64_t spatial, int32_t channels,
                                           int32_t groups);
 wgs_status group_norm_act(const void *x, const void *weight, const void *bias, void *y, float *mean,
@@ -567,8 +571,9 @@ wgs_status wgs_build_shift_regions(const int32_t grid[3], const int32_t window[3
  * an index outside [-1, n_src), any window reverse an inverse index outside
  * [0, n_windowed), or any window_bias_mask_add a window type outside
  * [0, n_types), or a position-bias call a bucket, window type or plan out of
- * its range; WGS_OK otherwise.  The words are shared by every stream of the
- * device. */
+ * its range; WGS_ERR_LAUNCH if a kernel since then gave up waiting for its own
+ * copies to arrive (its outputs are not to be used); WGS_OK otherwise.  The
+ * words are shared by every stream of the device. */
 wgs_status wgs_check_error(cudaStream_t stream);
 
 #ifdef __cplusplus

@@ -480,3 +480,103 @@ def test_large_samples(shape, fmt, act):
     assert all(torch.equal(_bits(p), _bits(q)) for p, q in zip(again, (gx, gw, gb)))
     wgs.group_norm_act(x, g, w, b, 1e-5, act, out=x)
     assert torch.equal(_bits(x), _bits(y))
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """More than 2^31 elements in a call, checked in the last sample's first and
+    last groups and in its first and last rows."""
+    n, s, c, g = 2, 5_700_000, 192, 32
+    gen = torch.Generator(DEV).manual_seed(1)
+    x = torch.empty(n, s, c, dtype=torch.float16, device=DEV)
+    gy = torch.empty_like(x)
+    for i in range(n):
+        x[i].normal_(generator=gen)
+        gy[i].normal_(generator=gen)
+    assert x.numel() > 2 ** 31
+    w = torch.linspace(0.5, 1.5, c, device=DEV)
+    b = torch.linspace(-0.2, 0.2, c, device=DEV)
+    y, mean, rstd = wgs.group_norm_act(x, g, w, b, 1e-5, "silu")
+    gx, gw, gb = wgs.group_norm_act_bwd(gy, x, g, mean, rstd, w, b, "silu")
+    D, half = 2 ** 17, 2.0 ** -11      # a slab's 37500 rows of 6 channels, and the joins
+    for i, j in ((0, 0), (n - 1, 0), (n - 1, g - 1)):
+        at = slice(j * c // g, (j + 1) * c // g)
+        xd, gd = x[i, :, at].double(), gy[i, :, at].double()
+        m, r = xd.mean(), (xd.var(unbiased=False) + 1e-5).rsqrt()
+        S = (xd - m).abs().max()
+        assert (mean[i, j] - m).abs() <= 2 * D * U * S
+        assert (rstd[i, j] / r - 1).abs() <= 2 * D * U * (S * r) ** 2
+        m, r = mean[i, j].double(), rstd[i, j].double()
+        h = (xd - m) * r
+        z = h * w[at].double() + b[at].double()
+        sig = torch.sigmoid(z)
+        assert ((y[i, :, at].double() - z * sig).abs() <= half * (z * sig).abs() + 2e-6).all()
+        d = gd * (sig + z * sig * (1 - sig)) * w[at].double()
+        want = r * (d - d.mean() - h * (d * h).mean())
+        assert ((gx[i, :, at].double() - want).abs() <= half * want.abs() + 5e-6 * gd.abs() + 1e-5).all()
+    gwant = torch.zeros(c, dtype=torch.float64, device=DEV)
+    mag = torch.zeros_like(gwant)
+    for i in range(n):
+        for k in range(0, s, s // 20):
+            rows = slice(k, min(s, k + s // 20))
+            up = lambda v: v[i].double().repeat_interleave(c // g)
+            h = (x[i, rows].double() - up(mean)) * up(rstd)
+            z = h * w.double() + b.double()
+            sig = torch.sigmoid(z)
+            dz = gy[i, rows].double() * (sig + z * sig * (1 - sig))
+            gwant += dz.sum(0)
+            mag += dz.abs().sum(0)
+    assert ((gb.double() - gwant).abs() <= 40000 * U * mag).all()
+
+
+@pytest.mark.gpu
+def test_calls_with_given_outputs_allocate_nothing():
+    n, s, c, g = 3, 900, 192, 32
+    x, w, b, gy = (t.to(DEV) for t in _inputs((n, s, c, g), "bf16", "f32", 3))
+    y, gx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(n, g, device=DEV), torch.empty(n, g, device=DEV)
+    gw, gb = torch.empty_like(w), torch.empty_like(b)
+    ws = torch.empty(wgs.group_norm_act_bwd_workspace_bytes(n, s, c, g), dtype=torch.uint8, device=DEV)
+    assert ws.numel() >= wgs.group_norm_act_workspace_bytes(n, s, c, g)
+
+    def calls():
+        wgs.group_norm_act(x, g, w, b, out=y, mean=mean, rstd=rstd, workspace=ws)
+        wgs.group_norm_act_bwd(gy, x, g, mean, rstd, w, b, grad_x=gx, grad_weight=gw, grad_bias=gb,
+                               workspace=ws)
+
+    calls()
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    allocated, free = torch.cuda.memory_allocated(), torch.cuda.mem_get_info()[0]
+    for _ in range(3):
+        calls()
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() == allocated
+    assert torch.cuda.mem_get_info()[0] == free
+
+
+@pytest.mark.gpu
+def test_inputs_written_right_before_the_call():
+    """x, the weights and grad_y written by the kernels just before, again and
+    again with new values, with nothing between: no launch of a call may read
+    what was there earlier."""
+    for n, s, c, g in ((1, 30000, 192, 32), (2, 143, 90, 6)):
+        x = torch.zeros(n, s, c, dtype=torch.float16, device=DEV)
+        gy, w, b = torch.zeros_like(x), torch.zeros(c, device=DEV), torch.zeros(c, device=DEV)
+        src = [[t.to(DEV) for t in _inputs((n, s, c, g), "f16", "f32", k)] for k in range(4)]
+        got = []
+        for _ in range(5):
+            for sx, sw, sb, sg in src:
+                x.copy_(sx)
+                gy.copy_(sg)
+                w.copy_(sw)
+                b.copy_(sb)
+                y, mean, rstd = wgs.group_norm_act(x, g, w, b)
+                got.append((y,) + wgs.group_norm_act_bwd(gy, x, g, mean, rstd, w, b))
+        torch.cuda.synchronize()
+        for k, (sx, sw, sb, sg) in enumerate(src):
+            y, mean, rstd = wgs.group_norm_act(sx, g, sw, sb)
+            torch.cuda.synchronize()
+            want = (y,) + wgs.group_norm_act_bwd(sg, sx, g, mean, rstd, sw, sb)
+            for r in range(5):
+                assert all(torch.equal(_bits(p), _bits(q)) for p, q in zip(got[4 * r + k], want))

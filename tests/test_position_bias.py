@@ -553,3 +553,52 @@ def test_graph_replay_and_streams_give_the_same_bits():
         assert torch.equal(_bits(out[1]), _bits(want[1]))
         for o in out:
             o.zero_()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [7400, 7401])
+def test_offsets_past_32_bits(n):
+    """More than 2^31 logits, in whole 16-byte runs and in odd rows: the last
+    heads' bias and gradient."""
+    heads, buckets = 40, 64
+    bucket = wgs.build_distance_buckets(n, n, buckets, 4000, True)
+    dbucket = bucket.to(DEV)
+    assert heads * bucket.numel() > 2 ** 31
+    table = _table(1, buckets, heads, "bf16", 3).to(DEV)
+    bias = wgs.position_bias(table, dbucket)
+    for h in (0, 19, 38, 39):
+        assert torch.equal(_bits(bias[0, h]), _bits(table[0, :, h][dbucket.long()])), h
+    # the bias itself as the gradient of one window
+    plan = wgs.build_bucket_plan(bucket, buckets, device=DEV)
+    got = wgs.position_bias_bwd(bias, plan)
+    count = torch.bincount(dbucket.view(-1), minlength=buckets).double()
+    want = table[0].double() * count[:, None]
+    # a bucket's values are equal here, so its sum of magnitudes is |want|; pairs
+    # are added over at most 4096 + 13372 tiles' slots
+    assert ((got[0].double() - want).abs() <= 20000 * U * want.abs()).all()
+    wgs.check_error(DEV)
+
+
+@pytest.mark.gpu
+def test_calls_with_given_outputs_allocate_nothing():
+    bucket = wgs.build_window_buckets((1, 4, 6))
+    plan, dbucket = wgs.build_bucket_plan(bucket, 77, device=DEV), bucket.to(DEV)
+    table, grad = _table(2, 77, 4, "f32", 1).to(DEV), _grad((30, 4, 24, 24), "f16", 2).to(DEV)
+    types = (torch.arange(30) % 2).int().to(DEV)
+    out = torch.empty(2, 4, 24, 24, dtype=torch.float16, device=DEV)
+    gt = torch.empty(2, 77, 4, device=DEV)
+    ws = torch.empty(wgs.position_bias_bwd_workspace_bytes(plan, 30, 4, 2), dtype=torch.uint8, device=DEV)
+
+    def calls():
+        wgs.position_bias(table, dbucket, out=out)
+        wgs.position_bias_bwd(grad, plan, types, 2, grad_table=gt, workspace=ws)
+
+    calls()
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    allocated, free = torch.cuda.memory_allocated(), torch.cuda.mem_get_info()[0]
+    for _ in range(3):
+        calls()
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() == allocated
+    assert torch.cuda.mem_get_info()[0] == free

@@ -164,14 +164,16 @@ struct Chunk {
 };
 
 // A weight or bias: FP32 or the tensor's own format; NULL is the default.
+// Read from L2, as all that pass 2 reads before it waits: L1 may hold an older
+// line.
 template <typename E>
 __device__ __forceinline__ float param(const void *p, int64_t c, bool p32, float otherwise) {
     if (!p) return otherwise;
-    if (p32) return __ldg(static_cast<const float *>(p) + c);
+    if (p32) return __ldcg(static_cast<const float *>(p) + c);
     if constexpr (std::is_same<E, F32>::value)
         return otherwise;  // FP32 tensors have FP32 weights
     else
-        return E::to_f2(__ldg(static_cast<const uint16_t *>(p) + c)).x;
+        return E::to_f2(__ldcg(static_cast<const uint16_t *>(p) + c)).x;
 }
 
 template <typename E>
@@ -628,17 +630,17 @@ __device__ __forceinline__ void params(const void *p, int32_t chunk, bool p32, f
         if (kV % 4 == 0 && whole) {
 #pragma unroll
             for (int e = 0; e < kV; e += 4) {
-                const float4 f = __ldg(reinterpret_cast<const float4 *>(q + e));
+                const float4 f = __ldcg(reinterpret_cast<const float4 *>(q + e));
                 v[e] = f.x, v[(e + 1) % kV] = f.y, v[(e + 2) % kV] = f.z, v[(e + 3) % kV] = f.w;
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < kV; ++e) v[e] = __ldg(q + e);
+            for (int e = 0; e < kV; ++e) v[e] = __ldcg(q + e);
         }
     } else if constexpr (!std::is_same<E, F32>::value) {
         const uint16_t *q = static_cast<const uint16_t *>(p) + static_cast<int64_t>(chunk) * kV;
         if (kV == 8 && whole) {
-            const uint4 f = __ldg(reinterpret_cast<const uint4 *>(q));
+            const uint4 f = __ldcg(reinterpret_cast<const uint4 *>(q));
 #pragma unroll
             for (int e = 0; e < kV; e += 2) {
                 const float2 w = E::to_f2(word(f, e / 2));
@@ -646,7 +648,7 @@ __device__ __forceinline__ void params(const void *p, int32_t chunk, bool p32, f
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < kV; ++e) v[e] = E::to_f2(__ldg(q + e)).x;
+            for (int e = 0; e < kV; ++e) v[e] = E::to_f2(__ldcg(q + e)).x;
         }
     }
 }

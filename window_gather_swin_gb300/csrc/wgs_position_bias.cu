@@ -21,7 +21,8 @@ namespace {
 
 // Set (never cleared by a kernel) when a bucket lies outside [-1, n_buckets),
 // a window type outside [0, n_types), or a plan does not belong to the sizes
-// it came with; read and cleared by wgs_check_error.
+// it came with (bit 0), or a block gave up waiting for its own copies (bit 1);
+// read and cleared by wgs_check_error.
 __device__ unsigned int g_bucket_error;
 
 }  // namespace
@@ -379,7 +380,7 @@ struct RingPlace {
 };
 
 __device__ __forceinline__ void must_wait(const uint64_t *bar, uint32_t parity) {
-    if (!bar_wait(shared_address(bar), parity)) atomicOr(&g_bucket_error, 1u);
+    if (!bar_wait(shared_address(bar), parity)) atomicOr(&g_bucket_error, 2u);
 }
 
 // The copying warp: the tiles of each unit's windows into the ring, in order.
@@ -413,7 +414,7 @@ __device__ void copy_units(const GradArgs &a, GradShared<E> &sh, Unit u, int32_t
             for (int32_t n = 0; n < count; ++n) {
                 const int32_t w = window(n);
                 const char *from = tile0 + w * stride;
-                if (!bar_wait(empty + 8 * stage, phase)) atomicOr(&g_bucket_error, 1u);
+                if (!bar_wait(empty + 8 * stage, phase)) atomicOr(&g_bucket_error, 2u);
                 const int last = ends && n + 1 == count ? kEnd : 0;
                 uint32_t size = bytes;
                 int said = kData | last;
@@ -443,7 +444,7 @@ __device__ void copy_units(const GradArgs &a, GradShared<E> &sh, Unit u, int32_t
                 advance();
             }
             if (count == 0 && ends) {  // a stage without a window
-                if (!bar_wait(empty + 8 * stage, phase)) atomicOr(&g_bucket_error, 1u);
+                if (!bar_wait(empty + 8 * stage, phase)) atomicOr(&g_bucket_error, 2u);
                 sh.said[stage] = kEnd;
                 bar_arrive(full + 8 * stage);
                 advance();
@@ -507,7 +508,7 @@ __device__ void add_units(const GradArgs &a, GradShared<E> &sh, Unit u, int32_t 
         const int32_t len = static_cast<int32_t>(min(a.n_pairs - p0, static_cast<int64_t>(kPlanTile)));
         int said;
         do {
-            if (!bar_wait(full + 8 * ring.stage, ring.phase)) atomicOr(&g_bucket_error, 1u);
+            if (!bar_wait(full + 8 * ring.stage, ring.phase)) atomicOr(&g_bucket_error, 2u);
             said = sh.said[ring.stage];
             const char *at = sh.stage[ring.stage];
             if (!kVec && (said & kDirect)) {

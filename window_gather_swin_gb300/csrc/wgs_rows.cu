@@ -603,6 +603,6 @@ extern "C" wgs_status wgs_check_error(cudaStream_t stream) {
         cudaGetLastError();
         return WGS_ERR_CUDA;
     }
-    if (seen_norm) return WGS_ERR_LAUNCH;
+    if (seen_norm || (seen_bucket & 2u)) return WGS_ERR_LAUNCH;
     return (seen | seen_mask | seen_bucket) ? WGS_ERR_INDEX : WGS_OK;
 }
