@@ -42,36 +42,28 @@ namespace cg = cooperative_groups;
 // copies; read and cleared by wgs_check_error.
 __device__ unsigned int g_norm_error;
 
-
 struct F32 {};
 
 constexpr int kMaxChannels = 4096;
 constexpr int kMaxGroups = 2048;
-#ifndef WGS_NORM_T1F
-#define WGS_NORM_T1F 384  // threads of a block at most: forward, pass 1
-#endif
-#ifndef WGS_NORM_B1F
-#define WGS_NORM_B1F 304  // blocks of the launch
-#endif
-#ifndef WGS_NORM_T2F
-#define WGS_NORM_T2F 384  // forward, pass 2
-#endif
-#ifndef WGS_NORM_B2F
-#define WGS_NORM_B2F 304
-#endif
-#ifndef WGS_NORM_T1B
-#define WGS_NORM_T1B 512  // backward, pass 1
-#endif
-#ifndef WGS_NORM_B1B
-#define WGS_NORM_B1B 152
-#endif
-#ifndef WGS_NORM_T2B
-#define WGS_NORM_T2B 512  // backward, pass 2
-#endif
-#ifndef WGS_NORM_B2B
-#define WGS_NORM_B2B 152
-#endif
-constexpr int kMaxSmem = 200 << 10;
+// Threads of a block at most, and blocks of a launch that cuts few samples into
+// slabs: two blocks an SM for the forward, whose loops wait for the rows, one
+// for the backward, whose threads need twice the registers and whose ring takes
+// the shared memory of the SM.  Measured, in us: the forward at [1, 131040, 192]
+// fp16 with SiLU and at [8, 32760, 384] bf16 with GELU, the backward at the same
+// with 4 samples: 32, 102, 51, 97; with 608 blocks of half the threads 52, 104,
+// 95, 122; with those for the forward's pass 2 alone 34 for the first.
+constexpr int kThreadsFwd = 384, kBlocksFwd = 304;
+constexpr int kThreadsBwd = 512, kBlocksBwd = 152;
+// Rows of a thread a stage and stages of the ring: the forward's with one
+// tensor, the backward's with two.  Same sizes: the forward with 2 x 6 36 and
+// 108, with 1 x 10 46 and 127, with 8 x 2 32 and 102; the backward with 2 x 4
+// 52 and 103, with 1 x 8 65 and 125.
+constexpr int kRowsFwd = 4, kStagesFwd = 3;
+constexpr int kRowsBwd = 4, kStagesBwd = 2;
+// Of a block.  The most that a call asks for is 208 KB (backward, 4096
+// channels of FP32 in 2048 groups).
+constexpr int kMaxSmem = 220 << 10;
 constexpr int kMaxCluster = 8;   // of a sample that one cluster holds
 
 enum : int { kNone = 0, kSilu = 1, kGeluTanh = 2 };
@@ -500,9 +492,6 @@ struct Own {
     }
 };
 
-// Rows a stage and stages: the forward's with one tensor, the backward's with two.
-constexpr int kRowsFwd = 4, kStagesFwd = 3, kRowsBwd = 2, kStagesBwd = 4;
-
 template <typename C, int kTensors>
 using Stream = std::conditional_t<
     C::kBytes == 16,
@@ -616,43 +605,6 @@ __device__ __forceinline__ void add_parts(float2 *smem, const Job &job, const fl
     }
 }
 
-// Weights or biases of a chunk's channels: FP32 or the tensor's own format;
-// NULL is the default.
-template <typename E, int kV>
-__device__ __forceinline__ void params(const void *p, int32_t chunk, bool p32, float otherwise,
-                                       float (&v)[kV]) {
-    const bool whole = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
-    if (!p) {
-#pragma unroll
-        for (int e = 0; e < kV; ++e) v[e] = otherwise;
-    } else if (p32) {
-        const float *q = static_cast<const float *>(p) + static_cast<int64_t>(chunk) * kV;
-        if (kV % 4 == 0 && whole) {
-#pragma unroll
-            for (int e = 0; e < kV; e += 4) {
-                const float4 f = __ldcg(reinterpret_cast<const float4 *>(q + e));
-                v[e] = f.x, v[(e + 1) % kV] = f.y, v[(e + 2) % kV] = f.z, v[(e + 3) % kV] = f.w;
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < kV; ++e) v[e] = __ldcg(q + e);
-        }
-    } else if constexpr (!std::is_same<E, F32>::value) {
-        const uint16_t *q = static_cast<const uint16_t *>(p) + static_cast<int64_t>(chunk) * kV;
-        if (kV == 8 && whole) {
-            const uint4 f = __ldcg(reinterpret_cast<const uint4 *>(q));
-#pragma unroll
-            for (int e = 0; e < kV; e += 2) {
-                const float2 w = E::to_f2(word(f, e / 2));
-                v[e] = w.x, v[(e + 1) % kV] = w.y;
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < kV; ++e) v[e] = E::to_f2(__ldcg(q + e)).x;
-        }
-    }
-}
-
 // enter(group) at a chunk's first channel and where another group begins,
 // f(element, channel) for each of its channels.
 template <int kV, typename Enter, typename F>
@@ -674,7 +626,8 @@ __device__ __forceinline__ void set_half(float2 *v, int e, float x) {
     if (e & 1) v[e / 2].y = x; else v[e / 2].x = x;
 }
 
-// Forward, pass 1: (mean, M2) of every group over the rows of a cluster, M2
+// Forward, pass 1 (reads x once; bound by DRAM): (mean, M2) of every group over
+// the rows of a cluster, M2
 // the sum of the squared distances from the mean.  A thread sums x - k and
 // its square, k the channel's value in the slab's first row.  With k one of
 // the values, the cancellation in M2 = sum d^2 - (sum d)^2 / n costs at most
@@ -766,8 +719,12 @@ __device__ void stats_pass(const NormArgs &a, const Job &job, Bars &bars, float2
     cluster.sync();  // the others' shared memory has been read; the result is visible to them
 }
 
-// Forward, pass 2, the slab's last rows first.  The statistics of the groups
-// lie behind the slots.
+// Forward, pass 2 (reads x again, writes y), the slab's last rows first.  The
+// statistics of the groups lie behind the slots.  At [1, 131040, 192] fp16, 50
+// MB, pass 1 reads x from DRAM and pass 2 finds all but 4 MB in L2; the call's
+// 100 MB take 32 us, 3.1 TB/s, of which each pass spends a few us on its start
+// and its last blocks, and pass 2 on the join.  At [8, 32760, 384] bf16, 201 MB,
+// most of x comes from DRAM twice: 102 us for 403 MB (604 MB moved, 5.9 TB/s).
 template <typename E, int kV, int kAct>
 __device__ void apply_pass(const NormArgs &a, const Job &job, Bars &bars, float2 *smem) {
     using C = Chunk<E, kV>;
@@ -826,7 +783,7 @@ __device__ void apply_pass(const NormArgs &a, const Job &job, Bars &bars, float2
 }
 
 template <typename E, int kV, int kAct>
-__global__ void __launch_bounds__(384, 2) norm_forward(NormArgs a) {
+__global__ void __launch_bounds__(kThreadsFwd, 2) norm_forward(NormArgs a) {
     extern __shared__ __align__(16) float2 smem[];
     __shared__ __align__(8) uint64_t storage[2 * kStagesFwd];
     Bars bars = make_bars<kStagesFwd>(storage);
@@ -836,42 +793,45 @@ __global__ void __launch_bounds__(384, 2) norm_forward(NormArgs a) {
     if (a.passes & 2) apply_pass<E, kV, kAct>(a, job, bars, smem);
 }
 
-// What the backward passes need of a thread's channels.
+// What the backward passes need of a thread's channels, from the groups'
+// (-mean, rstd) and the channels' (weight, bias) in shared memory.
 template <typename E, int kV>
 struct Channels {
     static constexpr int kP = Chunk<E, kV>::kPairs;
     float2 mean[kP], scale[kP], shift[kP];  // -mean, rstd w, b
-    __device__ void read(const NormArgs &a, int32_t c) {
-        float w[kV], b[kV];
-        params<E, kV>(a.weight, c, a.p32, 1.f, w);
-        params<E, kV>(a.bias, c, a.p32, 0.f, b);
-        mean[kP - 1].y = scale[kP - 1].y = shift[kP - 1].y = 0.f;
-#pragma unroll
-        for (int e = 0; e < kV; ++e) set_half(scale, e, w[e]), set_half(shift, e, b[e]);
-    }
-    // with the groups' (-mean, rstd)
-    __device__ void set(const NormArgs &a, int32_t c, const float2 *stat) {
+    __device__ void set(const NormArgs &a, int32_t c, const float2 *stat, const float2 *wb) {
         float2 st;
+        mean[kP - 1].y = scale[kP - 1].y = shift[kP - 1].y = 0.f;
         each_channel<kV>(a, c, [&](int32_t g) { st = stat[g]; }, [&](int e) {
+            const float2 f = wb[c * kV + e];
             set_half(mean, e, st.x);
-            set_half(scale, e, st.y * (e & 1 ? scale[e / 2].y : scale[e / 2].x));
+            set_half(scale, e, st.y * f.x);
+            set_half(shift, e, f.y);
         });
     }
 };
 
-// Backward, pass 1: the sums of dz and dz h a channel, and of d = dz w and d h
+// The block's copy of both.
+template <typename E>
+__device__ __forceinline__ void keep_inputs(const NormArgs &a, const Job &job, float2 *stat, float2 *wb) {
+    for (int g = job.tid; g < a.groups; g += job.threads) {
+        const int64_t at = job.sample * a.groups + g;
+        stat[g] = make_float2(-__ldcg(a.mean + at), __ldcg(a.rstd + at));
+    }
+    for (int c = job.tid; c < a.channels; c += job.threads)
+        wb[c] = make_float2(param<E>(a.weight, c, a.p32, 1.f), param<E>(a.bias, c, a.p32, 0.f));
+}
+
+// Backward, pass 1 (reads x and gy): the sums of dz and dz h a channel, and of d = dz w and d h
 // a group, over the rows of a cluster.
 template <typename E, int kV, int kAct>
 __device__ void sums_pass(const NormArgs &a, const Job &job, Bars &bars, float2 *smem) {
     using C = Chunk<E, kV>;
     constexpr int kP = C::kPairs;
-    float2 *ch = smem, *red = smem + a.channels, *stat = smem + a.behind / 8;
+    float2 *ch = smem, *red = smem + a.channels, *stat = smem + a.behind / 8, *wb = stat + a.groups;
     float2 *ring = job.columns == a.chunks ? smem : red;
     const int64_t row_bytes = static_cast<int64_t>(a.chunks) * C::kBytes;
-    for (int g = job.tid; g < a.groups; g += job.threads) {
-        const int64_t at = job.sample * a.groups + g;
-        stat[g] = make_float2(-__ldcg(a.mean + at), __ldcg(a.rstd + at));
-    }
+    keep_inputs<E>(a, job, stat, wb);
     __syncthreads();
     for (int32_t c0 = 0; c0 < a.chunks; c0 += job.columns) {
         const int32_t wide = min(job.columns, a.chunks - c0);
@@ -883,8 +843,7 @@ __device__ void sums_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
 #pragma unroll
         for (int p = 0; p < kP; ++p) s1[p] = s2[p] = both(0.f);
         Channels<E, kV> t;
-        t.read(a, c0 + min(job.j, wide - 1));
-        t.set(a, c0 + min(job.j, wide - 1), stat);
+        t.set(a, c0 + min(job.j, wide - 1), stat, wb);
         in.run([&](const typename C::Raw (&v)[2], int64_t) {
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
@@ -909,7 +868,7 @@ __device__ void sums_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
         if (g < a.groups)
             for (int i = lane; i < a.per_group; i += lanes) {
                 const int c = g * a.per_group + i;
-                const float w = param<E>(a.weight, c, a.p32, 1.f);
+                const float w = wb[c].x;
                 m1 = fmaf(w, ch[c].x, m1);
                 m2 = fmaf(w, ch[c].y, m2);
             }
@@ -940,7 +899,12 @@ __device__ void sums_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
     cluster.sync();
 }
 
-// Backward, pass 2: grad_x = rstd w dz - rstd M1 - (x - mean) rstd^2 M2.
+// Backward, pass 2 (reads x and gy again): grad_x = rstd w dz - rstd M1 -
+// (x - mean) rstd^2 M2.  The gate is computed in both passes, two special
+// functions an element: 10 us a pass at [1, 131040, 192] on that unit alone,
+// beside 15 us for 100 MB from DRAM; keeping dz for pass 2 would be 50 MB to write
+// and to read.  That size takes 51 us for 151 MB (3.0 TB/s; pass 2 finds 60 of
+// its 100 MB in L2), [4, 32760, 384] bf16 97 us for 302 MB.
 template <typename E, int kV, int kAct>
 __device__ void grad_pass(const NormArgs &a, const Job &job, Bars &bars, float2 *smem) {
     using C = Chunk<E, kV>;
@@ -948,18 +912,16 @@ __device__ void grad_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
     const int64_t row_bytes = static_cast<int64_t>(a.chunks) * C::kBytes;
     const int64_t base = (job.sample * a.spatial + job.r0) * row_bytes;
     const uint64_t policy = l2_policy(a.last_use);
-    float2 *stat = smem + a.ring / 8, *coef = stat + a.groups;
-    for (int g = job.tid; g < a.groups; g += job.threads) {
-        const int64_t at = job.sample * a.groups + g;
-        stat[g] = make_float2(-__ldcg(a.mean + at), __ldcg(a.rstd + at));
-    }
+    // behind the slots: the groups' (-mean, rstd) and what grad_x takes off, the
+    // channels' (weight, bias), a pair a thread
+    float2 *stat = smem + a.ring / 8, *coef = stat + a.groups, *wb = coef + a.groups, *lanes = wb + a.channels;
+    keep_inputs<E>(a, job, stat, wb);
     Channels<E, kV> t;
-    t.read(a, job.j);
     Stream<C, 2> in(job, bars);
     in.src[0] = a.x, in.src[1] = a.gy;
     wait_for_sums(a);
     add_parts(
-        coef + a.groups, job, a.groups_part + job.sample * a.clusters * a.groups, a.groups, a.clusters,
+        lanes, job, a.groups_part + job.sample * a.clusters * a.groups, a.groups, a.clusters,
         [](int, float2 v, float2) { return v; },
         [&] { in.start(smem, base, row_bytes, min(job.columns, a.chunks), true, policy); },
         [&](int g, float2 v, float2) {
@@ -971,9 +933,8 @@ __device__ void grad_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
         if (c0 > 0) {
             __syncthreads();  // the slots have been read
             in.start(smem, base + c0 * C::kBytes, row_bytes, wide, true, policy);
-            t.read(a, c);
         }
-        t.set(a, c, stat);
+        t.set(a, c, stat, wb);
         float2 k1[kP], k2[kP], m;
         k1[kP - 1].y = k2[kP - 1].y = 0.f;
         each_channel<kV>(a, c, [&](int32_t g) { m = coef[g]; }, [&](int e) {
@@ -995,7 +956,7 @@ __device__ void grad_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
 }
 
 template <typename E, int kV, int kAct>
-__global__ void __launch_bounds__(512, 1) norm_backward(NormArgs a) {
+__global__ void __launch_bounds__(kThreadsBwd, 1) norm_backward(NormArgs a) {
     extern __shared__ __align__(16) float2 smem[];
     __shared__ __align__(8) uint64_t storage[2 * kStagesBwd];
     Bars bars = make_bars<kStagesBwd>(storage);
@@ -1006,7 +967,8 @@ __global__ void __launch_bounds__(512, 1) norm_backward(NormArgs a) {
 }
 
 // Backward, last: the weight's and bias's gradients over all samples'
-// clusters; 32 row lanes of 32 channels each.
+// clusters; 32 row lanes of 32 channels each, with 16 loads in flight a thread
+// (latency bounds it: a call leaves at least one pair a sample and channel).
 template <typename E>
 __global__ void __launch_bounds__(1024) norm_params(NormArgs a, int64_t parts) {
     __shared__ float2 red[32][33];
@@ -1015,8 +977,16 @@ __global__ void __launch_bounds__(1024) norm_params(NormArgs a, int64_t parts) {
     const int32_t c = blockIdx.x * 32 + j;
     float2 t = make_float2(0.f, 0.f);
     if (c < a.channels) {
-#pragma unroll 4
-        for (int64_t i = l; i < parts; i += 32) t = add2(t, __ldcg(a.chan_part + i * a.channels + c));
+        constexpr int kAhead = 16;
+        const float2 *q = a.chan_part + c;
+        for (int64_t i = l; i < parts; i += 32 * kAhead) {
+            float2 v[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                v[u] = i + 32 * u < parts ? __ldcg(q + (i + 32 * u) * a.channels) : both(0.f);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) t = add2(t, v[u]);
+        }
     }
     red[l][j] = t;
     __syncthreads();
@@ -1037,15 +1007,19 @@ bool dtype_ok(wgs_dtype d) { return d == WGS_F32 || d == WGS_F16 || d == WGS_BF1
 int64_t bytes_of(wgs_dtype d) { return d == WGS_F32 ? 4 : 2; }
 bool aligned_to(const void *p, int64_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Elements beyond which a call's tensors outgrow L2.
+// Elements beyond which a call's tensors outgrow L2: pass 2 then marks its
+// lines as the first to leave, so that rows not yet read stay.
 constexpr int64_t kResident = int64_t{32} << 20;
 // Rows that a slab has at least.
 constexpr int64_t kMinSlabRows = 16;
 // A sample of at most this many elements goes through both passes in one
-// launch of a cluster.
+// launch of a cluster, and so do samples that are many enough to fill the GPU
+// with clusters; the larger ones of fewer samples are cut into slabs over the
+// whole GPU ([8, 32760, 384] bf16 by clusters of 8 leaves SMs idle).
 constexpr int64_t kOneLaunch = int64_t{1} << 19;
 
-// Slabs of a sample in pass 1 at most.
+// Slabs of a sample in pass 1 at most: so many pairs a group come to pass 2 in
+// one round of loads ([1, 131040, 192] fp16 forward: 32.4 us; with 304 33.5).
 constexpr int64_t kMaxParts = 152;
 
 struct Plan {
@@ -1073,11 +1047,8 @@ bool plan_of(int64_t n, int64_t spatial, int64_t channels, int64_t groups, int64
             z->cluster = 1;
             // the launch's blocks over the samples, no more than are resident
             auto share = [&](int64_t blocks) { return blocks / n < most ? blocks / n : most; };
-            z->slabs1 = share(backward ? WGS_NORM_B1B : WGS_NORM_B1F);
-            // what pass 2 joins: 152 pairs a group come in one round of loads
-            // ([131040,192] fp16: 32.4 us; with 304 33.5)
-            if (z->slabs1 > kMaxParts) z->slabs1 = kMaxParts;
-            z->slabs2 = share(backward ? WGS_NORM_B2B : WGS_NORM_B2F);
+            z->slabs2 = share(backward ? kBlocksBwd : kBlocksFwd);
+            z->slabs1 = z->slabs2 < kMaxParts ? z->slabs2 : kMaxParts;
         }
     }
     const int64_t parts = n * (z->slabs1 / z->cluster);
@@ -1107,22 +1078,23 @@ wgs_status run(NormArgs a, const Plan &z, int act, bool backward, int64_t n, cud
                            : (act == kSilu       ? norm_forward<E, kV, kSilu>
                               : act == kGeluTanh ? norm_forward<E, kV, kGeluTanh>
                                                  : norm_forward<E, kV, kNone>);
-    auto go = [&](int passes, int most) {
+    const int most = backward ? kThreadsBwd : kThreadsFwd;
+    auto go = [&](int passes) {
         const int columns = a.chunks < most ? a.chunks : most;
         const int row_groups = most / columns;  // more than half of the threads, so whole warps
         const int threads = columns * row_groups;
         // Shared memory.  Pass 1: the channels' sums, and in one place the
         // slots, the row groups' sums and the groups'; where one walk covers
         // the row the channels' lie over the slots too.  Pass 2: the slots,
-        // the groups' values, in the forward the channels', a pair a thread.
+        // the groups' and channels' values, a pair a thread.
         a.ring = C::kBytes < 4 ? 0 : threads * C::kBytes * (backward ? 2 * kRowsBwd * kStagesBwd : kRowsFwd * kStagesFwd);
         const int red = 8 * (threads * kV > a.groups ? threads * kV : a.groups), ch = 8 * a.channels;
         const int pass1 = columns == a.chunks ? (ch + red > a.ring ? ch + red : a.ring)
                                               : ch + (red > a.ring ? red : a.ring);
-        // (the backward's pass 1 keeps the groups' statistics behind that)
+        // (the backward's pass 1 keeps the groups' and channels' values behind that)
         a.behind = (pass1 + 15) / 16 * 16;
-        const int one = passes & 1 ? a.behind + (backward ? 8 * a.groups : 0) : 0;
-        const int two = passes & 2 ? a.ring + (backward ? 16 * a.groups : 8 * (a.groups + a.channels)) + 8 * threads : 0;
+        const int one = passes & 1 ? a.behind + (backward ? 8 * (a.groups + a.channels) : 0) : 0;
+        const int two = passes & 2 ? a.ring + 8 * ((backward ? 2 : 1) * a.groups + a.channels + threads) : 0;
         const int smem = one > two ? one : two;
         // Above 48 KB a kernel needs the runtime's leave, which belongs to the
         // context; asking for the same amount on every call needs no record of it.
@@ -1136,11 +1108,10 @@ wgs_status run(NormArgs a, const Plan &z, int act, bool backward, int64_t n, cud
         return launch_clusters(kernel, dim3(static_cast<unsigned>(count), static_cast<unsigned>(n)),
                                dim3(columns, row_groups), a.cluster, static_cast<size_t>(smem), stream, a);
     };
-    const int threads1 = backward ? WGS_NORM_T1B : WGS_NORM_T1F, threads2 = backward ? WGS_NORM_T2B : WGS_NORM_T2F;
     wgs_status st = WGS_OK;
     if (n > 0) {
-        st = go(z.one_launch ? 3 : 1, threads1);
-        if (st == WGS_OK && !z.one_launch) st = go(2, threads2);
+        st = go(z.one_launch ? 3 : 1);
+        if (st == WGS_OK && !z.one_launch) st = go(2);
     }
     if (st == WGS_OK && backward && (a.grad_weight || a.grad_bias))
         st = launch(norm_params<E>, dim3(static_cast<unsigned>(ceil_div(a.channels, 32))), dim3(1024), 0,
