@@ -482,6 +482,25 @@ def test_large_samples(shape, fmt, act):
     assert torch.equal(_bits(x), _bits(y))
 
 
+# Samples that are many enough to fill the GPU: fewer blocks a sample and fewer
+# threads a block, more samples than blocks that are resident, one position each.
+MANY = [(1300, 49, 24, 3), (700, 20, 40, 8), (313, 70, 136, 17), (5000, 1, 64, 8), (2500, 3, 15, 5),
+        (90, 130, 64, 32), (13, 520, 90, 45)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,pfmt", [("f32", "f32"), ("f16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("shape", MANY, ids=str)
+def test_many_samples(shape, fmt, pfmt):
+    g = shape[3]
+    act = "gelu_tanh" if fmt == "f16" else "silu"
+    x, w, b, gy = (t.to(DEV) for t in _inputs(shape, fmt, pfmt, 11))
+    y, mean, rstd = _check_forward(x, w, b, g, 1e-5, act, fmt)
+    first = _check_backward(gy, x, w, b, g, mean, rstd, act, fmt, pfmt)
+    again = wgs.group_norm_act_bwd(gy, x, g, mean, rstd, w, b, act)
+    assert all(torch.equal(_bits(p), _bits(q)) for p, q in zip(first, again))
+
+
 @pytest.mark.gpu
 def test_offsets_past_32_bits():
     """More than 2^31 elements in a call, checked in the last sample's first and

@@ -967,35 +967,40 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) norm_backward(NormArgs a) {
 }
 
 // Backward, last: the weight's and bias's gradients over all samples'
-// clusters; 32 row lanes of 32 channels each, with 16 loads in flight a thread
+// clusters; 128 lanes a channel, 8 channels a block, 16 loads in flight a thread
 // (latency bounds it: a call leaves at least one pair a sample and channel).
 template <typename E>
 __global__ void __launch_bounds__(1024) norm_params(NormArgs a, int64_t parts) {
-    __shared__ float2 red[32][33];
+    constexpr int kChannels = 8, kLanes = 1024 / kChannels, kAhead = 16;
+    __shared__ float2 red[kChannels][32 + 1];
     pdl_prologue();
-    const int j = threadIdx.x & 31, l = threadIdx.x >> 5;
-    const int32_t c = blockIdx.x * 32 + j;
-    float2 t = make_float2(0.f, 0.f);
-    if (c < a.channels) {
-        constexpr int kAhead = 16;
-        const float2 *q = a.chan_part + c;
-        for (int64_t i = l; i < parts; i += 32 * kAhead) {
+    const int j = threadIdx.x % kChannels, l = threadIdx.x / kChannels, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int32_t c0 = blockIdx.x * kChannels;
+    float2 t = both(0.f);
+    if (c0 + j < a.channels) {
+        const float2 *q = a.chan_part + c0 + j;
+        for (int64_t i = l; i < parts; i += kLanes * kAhead) {
             float2 v[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
-                v[u] = i + 32 * u < parts ? __ldcg(q + (i + 32 * u) * a.channels) : both(0.f);
+                v[u] = i + kLanes * u < parts ? __ldcg(q + (i + kLanes * u) * a.channels) : both(0.f);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) t = add2(t, v[u]);
         }
     }
-    red[l][j] = t;
+    for (int o = 16; o >= kChannels; o /= 2) {
+        t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
+        t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
+    }
+    if (lane < kChannels) red[j][warp] = t;
     __syncthreads();
-    // warp l ends channel l of the block
-    t = red[j][l];
+    // warp w ends channel w of the block
+    if (warp >= kChannels) return;
+    t = red[warp][lane];
     t.x = group_sum<32>(t.x);
     t.y = group_sum<32>(t.y);
-    const int32_t mine = blockIdx.x * 32 + l;
-    if (j == 0 && mine < a.channels) {
+    const int32_t mine = c0 + warp;
+    if (lane == 0 && mine < a.channels) {
         if (a.grad_weight) store_param<E>(a.grad_weight, mine, a.p32, t.y);
         if (a.grad_bias) store_param<E>(a.grad_bias, mine, a.p32, t.x);
     }
@@ -1022,6 +1027,15 @@ constexpr int64_t kOneLaunch = int64_t{1} << 19;
 // one round of loads ([1, 131040, 192] fp16 forward: 32.4 us; with 304 33.5).
 constexpr int64_t kMaxParts = 152;
 
+// A sample's cluster grows to 8 blocks while the launch has fewer than
+// kEnoughBlocks or a block would keep kShare elements: [1024, 256, 128] fp16 forward
+// and backward by 1024 blocks 43 and 70 us, by 4096 62 and 95; [300, 1000, 512]
+// by 1200 154 and 276, by 2400 163 and 288.
+constexpr int64_t kEnoughBlocks = 608, kShare = 65536;
+// See run().
+constexpr int64_t kFewBlocksFwd = 304, kFewBlocksBwd = 100, kRowsMany = 32;
+constexpr int kThreadsMany = 256;
+
 struct Plan {
     int64_t x_bytes, group_part, chan_part;  // bytes
     int64_t slabs1, slabs2, cluster;
@@ -1040,7 +1054,9 @@ bool plan_of(int64_t n, int64_t spatial, int64_t channels, int64_t groups, int64
     z->one_launch = true;
     if (n > 0 && spatial > 0) {
         const int64_t most = ceil_div(spatial, kMinSlabRows);
-        while (z->cluster < kMaxCluster && 2 * z->cluster <= most) z->cluster *= 2;
+        while (z->cluster < kMaxCluster && 2 * z->cluster <= most &&
+               (n * z->cluster < kEnoughBlocks || spatial * channels >= 2 * z->cluster * kShare))
+            z->cluster *= 2;
         z->slabs1 = z->slabs2 = z->cluster;
         z->one_launch = spatial * channels <= kOneLaunch || n * z->cluster >= 304;
         if (!z->one_launch) {
@@ -1078,7 +1094,21 @@ wgs_status run(NormArgs a, const Plan &z, int act, bool backward, int64_t n, cud
                            : (act == kSilu       ? norm_forward<E, kV, kSilu>
                               : act == kGeluTanh ? norm_forward<E, kV, kGeluTanh>
                                                  : norm_forward<E, kV, kNone>);
-    const int most = backward ? kThreadsBwd : kThreadsFwd;
+    int most = backward ? kThreadsBwd : kThreadsFwd;
+    // Of the blocks that take a slab through both passes, more have to fit an SM
+    // where there are more than the GPU holds of the largest: a block's way from
+    // end to end is a chain of waits.  Threads halve to 64 as long as each has
+    // kRowsMany rows of the slab at most.  (The backward's blocks of 512 fill an SM,
+    // and clusters of 8 of those do not all find room beyond some 100 blocks.)
+    // [4096, 49, 96] fp16: 42 and 62 us forward and backward, with 256 threads 75 and
+    // 118; [1024, 256, 128] 40 and 62 (43 and 70); [16, 512, 320] backward 19, with
+    // 512 threads 28; [12, 512, 512] of 96 blocks 17, with 256 threads 22.
+    const int64_t blocks = n * z.cluster;
+    if (z.one_launch && blocks > (backward ? kFewBlocksBwd : kFewBlocksFwd)) most = kThreadsMany;
+    if (z.one_launch && blocks > kFewBlocksFwd) {
+        const int64_t rows = ceil_div(a.spatial, z.cluster), want = ceil_div(rows, kRowsMany) * a.chunks;
+        while (most > 64 && most / 2 >= want) most /= 2;
+    }
     auto go = [&](int passes) {
         const int columns = a.chunks < most ? a.chunks : most;
         const int row_groups = most / columns;  // more than half of the threads, so whole warps
@@ -1114,7 +1144,7 @@ wgs_status run(NormArgs a, const Plan &z, int act, bool backward, int64_t n, cud
         if (st == WGS_OK && !z.one_launch) st = go(2);
     }
     if (st == WGS_OK && backward && (a.grad_weight || a.grad_bias))
-        st = launch(norm_params<E>, dim3(static_cast<unsigned>(ceil_div(a.channels, 32))), dim3(1024), 0,
+        st = launch(norm_params<E>, dim3(static_cast<unsigned>(ceil_div(a.channels, 8))), dim3(1024), 0,
                     stream, a, n * a.clusters);
     return st;
 }
