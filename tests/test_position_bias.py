@@ -429,6 +429,42 @@ def test_position_bias_gradient(i, order, table_fmt, fmt):
     wgs.check_error(DEV)
 
 
+# Maps of few pairs: windows shared out over groups of threads, several heads a
+# block (the last with fewer), maps that just do and just do not belong here.
+FEW = [  # map, buckets, types, heads, windows
+    (lambda: wgs.build_window_buckets((1, 1, 1)), 1, 3, 32, 4096),
+    (lambda: wgs.build_window_buckets((1, 2, 2)), 9, 1, 5, 777),
+    (lambda: wgs.build_window_buckets((1, 3, 3)), 25, 4, 100, 90),
+    (lambda: wgs.build_distance_buckets(16, 16, 8, 10, False), 8, 2, 12, 333),
+    (lambda: wgs.build_window_buckets((1, 4, 8)), 105, 2, 7, 150),
+    (lambda: wgs.build_distance_buckets(31, 33, 32, 20), 32, 1, 9, 60),
+    (lambda: wgs.build_distance_buckets(25, 41, 32, 20), 32, 1, 9, 60),
+    (lambda: wgs.build_window_buckets((1, 1, 2)), 3, 70, 1, 5000),
+    (lambda: torch.full((3, 7), -1, dtype=torch.int32), 2, 1, 3, 40),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("table_fmt,fmt", [("f32", "f32"), ("f32", "f16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("i", range(len(FEW)))
+def test_gradient_of_small_maps(i, table_fmt, fmt):
+    make, n_buckets, n_types, heads, n_win = FEW[i]
+    bucket = make()
+    plan = wgs.build_bucket_plan(bucket, n_buckets, device=DEV)
+    buf = _grad((n_win * heads * bucket.numel() + 3,), fmt, i).to(DEV)
+    grad = buf[:-3].view((n_win, heads) + tuple(bucket.shape))
+    types = torch.randint(0, n_types, (n_win,), generator=torch.Generator().manual_seed(i)).int().to(DEV)
+    got = _check_backward(grad, bucket, plan, types if n_types > 1 else None, n_types, fmt, table_fmt)
+    # elsewhere in memory, the same bits
+    view = torch.cat([buf[:1], buf[:-3]])[1:].view(grad.shape)
+    again = wgs.position_bias_bwd(view, plan, types if n_types > 1 else None, n_types, dtype=DT[table_fmt])
+    assert torch.equal(_bits(got), _bits(again))
+    # without types every window counts for the first
+    first = _check_backward(grad, bucket, plan, None, n_types, fmt, table_fmt)
+    assert not first[1:].any()
+    wgs.check_error(DEV)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
 def test_gradient_of_unaligned_views_equals_the_aligned_one(fmt):

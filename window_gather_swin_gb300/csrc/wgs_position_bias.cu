@@ -342,14 +342,12 @@ struct Unit {
 constexpr int kAdders = 128, kSlotters = kPlanLanes;
 constexpr int kGradThreads = kAdders + kSlotters + 32;
 constexpr int kListed = 1024;                 // windows looked over at a time
-#ifndef WGS_GRAD_STAGES
-#define WGS_GRAD_STAGES 6
-#endif
-#ifndef WGS_GRAD_CTAS
-#define WGS_GRAD_CTAS 2
-#endif
+// Blocks of an SM, and stages of a block's ring (48 KB).  960 windows of 6 heads and
+// 144 x 144 pairs, fp16: two blocks of six stages 59 us, of four 60, one block 84
+// (51 since the slots are added by lanes).
+constexpr int kGradCtas = 2;
 template <typename E>
-constexpr int kGradStages = std::is_same<E, F32>::value ? WGS_GRAD_STAGES * 2 / 3 : WGS_GRAD_STAGES;
+constexpr int kGradStages = std::is_same<E, F32>::value ? 4 : 6;
 template <typename E>
 constexpr int kStageBytes = kPlanTile * kBytes<E> + 16;  // a tile that starts between 16-byte borders
 
@@ -563,8 +561,20 @@ __device__ void add_units(const GradArgs &a, GradShared<E> &sh, Unit u, int32_t 
     }
 }
 
-__device__ __forceinline__ void store_if(bool yes, float *p, float v) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %0, 0;\n\t@p st.global.f32 [%1], %2;\n\t}" ::"r"(static_cast<int>(yes)), "l"(p), "f"(v) : "memory");
+// Where bit e of `ends` says that a slot ends: its sum to *to, and on to the next.
+template <int e>
+__device__ __forceinline__ void end_slot(uint32_t ends, float *&to, float &sum) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 t;\n\tand.b32 t, %2, %3;\n\tsetp.ne.u32 p, t, 0;\n\t"
+                 "@p st.global.f32 [%0], %1;\n\t@p add.s64 %0, %0, 4;\n\t@p mov.f32 %1, 0f00000000;\n\t}"
+                 : "+l"(to), "+f"(sum) : "r"(ends), "n"(1u << e) : "memory");
+}
+template <int e>
+__device__ __forceinline__ void add_entries(const float (&v)[32], uint32_t ends, float *&to, float &sum) {
+    if constexpr (e < 32) {
+        sum += v[e];
+        end_slot<e>(ends, to, sum);
+        add_entries<e + 1>(v, ends, to, sum);
+    }
 }
 
 // The slot warps: a unit's sums slot by slot, while the next unit's windows are
@@ -575,7 +585,7 @@ template <typename E>
 __device__ void slot_units(const GradArgs &a, GradShared<E> &sh, Unit u, int32_t units, int tid) {
     RingPlace<2> in;
     int32_t tile = -1;
-    uint4 order[4];
+    uint32_t at[32];  // the entries' bytes among the sums
     int2 lane;
     const bool ok = plan_matches(a);  // else nothing of it is followed
     if (!ok && tid == 0) atomicOr(&g_bucket_error, 1u);
@@ -584,28 +594,26 @@ __device__ void slot_units(const GradArgs &a, GradShared<E> &sh, Unit u, int32_t
             tile = u.tile;
             const uint4 *oq = reinterpret_cast<const uint4 *>(a.plan + a.at.order) + tile * (kPlanTile / 8);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) order[k] = __ldg(oq + k * kPlanLanes + tid);
+            for (int k = 0; k < 4; ++k) {
+                const uint4 o = __ldg(oq + k * kPlanLanes + tid);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) at[8 * k + j] = (word(o, j / 2) >> (j & 1 ? 16 : 0) & (kPlanTile - 1)) * 4;
+            }
             lane = __ldg(reinterpret_cast<const int2 *>(a.plan + a.at.lane) + tile * kPlanLanes + tid);
+            // no slot but the map's
+            if (lane.y < 0 || lane.y > a.n_slots - __popc(lane.x)) lane.x = lane.y = 0;
         }
-        float *out = a.partial + ((static_cast<int64_t>(u.slab) * a.n_types + u.type) * a.heads + u.head) * a.n_slots;
+        float *to = a.partial + ((static_cast<int64_t>(u.slab) * a.n_types + u.type) * a.heads + u.head) * a.n_slots;
         must_wait(&sh.summed[in.stage], in.phase);
-        const float *sums = sh.sums[in.stage];
+        const char *sums = reinterpret_cast<const char *>(sh.sums[in.stage]);
         if (ok) {
             float v[32];  // all under way before the first is added
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-                v[e] = sums[word(order[e / 8], e % 8 / 2) >> (e & 1 ? 16 : 0) & (kPlanTile - 1)];
+            for (int e = 0; e < 32; ++e) v[e] = *reinterpret_cast<const float *>(sums + at[e]);
             // without branches: lanes end their slots at different entries
-            float *to = out + lane.y, sum = 0.f;
-            const float *end = out + a.n_slots;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                sum += v[e];
-                const bool last = lane.x >> e & 1;
-                store_if(last && to >= out && to < end, to, sum);
-                to += last;
-                sum = last ? 0.f : sum;
-            }
+            float sum = 0.f;
+            to += lane.y;
+            add_entries<0>(v, lane.x, to, sum);
         }
         __syncwarp();
         if ((tid & 31) == 0) bar_arrive(shared_address(&sh.read[in.stage]));
@@ -618,8 +626,12 @@ __device__ void slot_units(const GradArgs &a, GradShared<E> &sh, Unit u, int32_t
 // across units, four warps add them up and four add the last unit's sums up by
 // slot.  Every gradient is read once; what leaves is one value per slot.  The
 // order of all additions is fixed by the sizes and the plan.
+// 960 windows of 6 heads and 144 x 144 pairs in 5 types, fp16: 43 us of the call's
+// 51 for 239 MB (5.6 TB/s, bound by DRAM).  Where a unit has one window the way
+// of its sums through shared memory bounds it: 16 heads of 2047 x 2047 pairs, 134
+// MB, 58 us (1.1 us a unit and block).
 template <typename E, bool kVec>
-__global__ void __launch_bounds__(kGradThreads, WGS_GRAD_CTAS) bias_grad_tiles(GradArgs a) {
+__global__ void __launch_bounds__(kGradThreads, kGradCtas) bias_grad_tiles(GradArgs a) {
     extern __shared__ __align__(16) char smem[];
     GradShared<E> &sh = *reinterpret_cast<GradShared<E> *>(smem);
     if (threadIdx.x == 0) {
@@ -689,15 +701,190 @@ __global__ void __launch_bounds__(kGradThreads, WGS_GRAD_CTAS) bias_grad_tiles(G
         copy_units<E, kVec>(a, sh, u, units, listed, tid - kAdders - kSlotters);
 }
 
+// Pass 1 of small maps, where a tile of one head is too little to copy: a block
+// takes several heads of a slab's windows of one type, which lie side by side,
+// window by window, groups of threads the windows in turn.  A thread keeps the
+// sums of the same kOwn words (of kW pairs) of each of its windows; the groups'
+// are added in order in shared memory, and from there by slot, as above.  4096
+// windows, fp16, us of the call (by tiles): 1 pair of 32 heads 6 (134), 16 pairs of
+// 32 heads 9 (83), 256 pairs of 16 heads, 34 MB, 15 (45).  Latency bounds it.
+constexpr int kSmallThreads = 512, kSmallValues = 4096;
+
+template <typename E, int kW, int kOwn>
+__global__ void __launch_bounds__(kSmallThreads, 2) bias_grad_small(GradArgs a, int32_t head_step) {
+    constexpr bool k32 = std::is_same<E, F32>::value;
+    constexpr int kAhead = 8 / kOwn < 2 ? 2 : 8 / kOwn;  // windows in flight a thread
+    __shared__ int32_t list[kListed];
+    __shared__ int32_t counts[kSmallThreads / 32];
+    // by group, or (one group) by place
+    __shared__ float parts[kOwn == 1 ? kSmallThreads * kW : 1];
+    __shared__ float sums[kSmallValues];
+    pdl_prologue();
+    const bool ok = plan_matches(a);
+    if (!ok && threadIdx.x == 0) atomicOr(&g_bucket_error, 1u);
+    const int tid = threadIdx.x;
+    const int32_t chunks = (a.heads + head_step - 1) / head_step;
+    int32_t u = blockIdx.x;
+    const int32_t h0 = u % chunks * head_step, heads = min(head_step, a.heads - h0);
+    u /= chunks;
+    const int32_t slab = u % a.slabs, type = u / a.slabs;
+    const int32_t w0 = share_start(a.n_win, a.slabs, slab), w1 = share_start(a.n_win, a.slabs, slab + 1);
+    const int32_t pairs = static_cast<int32_t>(a.n_pairs), padded = (pairs + 31) / 32 * 32;
+    const int32_t words = heads * pairs / kW;
+    // groups of threads, of which each window has one: by the pairs, so that the order
+    // of additions does not depend on the alignment
+    const int32_t groups = kOwn == 1 ? max(kSmallThreads / (heads * pairs), 1) : 1;
+    const int32_t group = kOwn == 1 ? tid / words : 0, j = kOwn == 1 ? tid - group * words : tid;
+    const int64_t stride = static_cast<int64_t>(a.heads) * a.n_pairs;
+    const char *base = a.grad + (static_cast<int64_t>(h0) * a.n_pairs + static_cast<int64_t>(j) * kW) * kBytes<E>;
+    using Raw = std::conditional_t<k32 || kW == 2, uint32_t, uint16_t>;
+    float acc[kOwn * kW];
+#pragma unroll
+    for (int k = 0; k < kOwn * kW; ++k) acc[k] = 0.f;
+    // `count` windows, the n-th window(n)
+    auto add = [&](int32_t count, auto window) {
+        if (group >= groups) return;
+        for (int32_t n = group; n < count; n += kAhead * groups) {
+            Raw v[kAhead][kOwn];
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const bool live = n + q * groups < count;
+                const char *from = base + (live ? window(n + q * groups) * stride : 0) * kBytes<E>;
+#pragma unroll
+                for (int k = 0; k < kOwn; ++k)
+                    v[q][k] = live && j + k * kSmallThreads < words
+                        ? __ldcs(reinterpret_cast<const Raw *>(from + k * (kSmallThreads * kW * kBytes<E>))) : Raw(0);
+            }
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+                for (int k = 0; k < kOwn; ++k) {
+                    if constexpr (k32) {
+                        acc[k] += __uint_as_float(v[q][k]);
+                    } else {
+                        const float2 f = E::to_f2(v[q][k]);
+                        acc[k * kW] += f.x;
+                        if constexpr (kW == 2) acc[k * kW + 1] += f.y;
+                    }
+                }
+        }
+    };
+    if (!a.win_type) {
+        add(type == 0 ? w1 - w0 : 0, [&](int32_t n) { return w0 + n; });
+    } else {
+        constexpr int kWarps = kSmallThreads / 32, kEach = kListed / kSmallThreads;
+        const int warp = tid >> 5, lane = tid & 31;
+        for (int32_t w = w0; w < w1; w += kListed) {
+            // the windows of this type among the next kListed, in order
+            unsigned hits[kEach];
+            int32_t count = 0;
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int32_t at = w + (warp * kEach + k) * 32 + lane;
+                const int32_t t = at < w1 ? __ldg(a.win_type + at) : type - 1;
+                if (at < w1 && (t < 0 || t >= a.n_types)) atomicOr(&g_bucket_error, 1u);
+                hits[k] = __ballot_sync(0xffffffffu, at < w1 && t == type);
+                count += __popc(hits[k]);
+            }
+            if (lane == 0) counts[warp] = count;
+            __syncthreads();  // (the last list has been read, too)
+            int32_t before = 0, listed = 0;
+            for (int q = 0; q < kWarps; ++q) {
+                if (q == warp) before = listed;
+                listed += counts[q];
+            }
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                if (hits[k] >> lane & 1)
+                    list[before + __popc(hits[k] & ((1u << lane) - 1u))] = w + (warp * kEach + k) * 32 + lane;
+                before += __popc(hits[k]);
+            }
+            __syncthreads();
+            add(listed, [&](int32_t n) { return list[n]; });
+        }
+    }
+    // pair i of head h at h * padded + plan_place(i)
+    auto place = [&](int32_t e) {
+        const int32_t h = e / pairs;
+        return h * padded + plan_place(e - h * pairs);
+    };
+    if constexpr (kOwn == 1) {
+        if (group < groups)
+#pragma unroll
+            for (int q = 0; q < kW; ++q) parts[(group * words + j) * kW + q] = acc[q];
+        __syncthreads();
+        for (int32_t e = tid; e < words * kW; e += kSmallThreads) {
+            float t = parts[e];
+            for (int32_t g = 1; g < groups; ++g) t += parts[g * words * kW + e];
+            sums[place(e)] = t;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+            if (j + k * kSmallThreads < words)
+#pragma unroll
+                for (int q = 0; q < kW; ++q) sums[place((j + k * kSmallThreads) * kW + q)] = acc[k * kW + q];
+    }
+    __syncthreads();
+    if (!ok) return;
+    const int32_t lanes = padded / 32;  // of the plan that can have entries
+    for (int32_t i = tid; i < heads * lanes; i += kSmallThreads) {
+        const int32_t h = i / lanes, l = i - h * lanes;
+        int2 lane = __ldg(reinterpret_cast<const int2 *>(a.plan + a.at.lane) + l);
+        if (lane.y < 0 || lane.y > a.n_slots - __popc(lane.x)) lane.x = lane.y = 0;
+        float *to = a.partial + ((static_cast<int64_t>(slab) * a.n_types + type) * a.heads + h0 + h) * a.n_slots + lane.y;
+        const uint4 *oq = reinterpret_cast<const uint4 *>(a.plan + a.at.order) + l;
+        float v[32], sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint4 o = __ldg(oq + k * kPlanLanes);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                v[8 * k + q] = sums[h * padded + min(static_cast<int32_t>(word(o, q / 2) >> (q & 1 ? 16 : 0) & 0xffff), padded - 1)];
+        }
+        add_entries<0>(v, lane.x, to, sum);
+    }
+}
+
 // The d-th slot of the buckets' lists.
 __device__ __forceinline__ int32_t slot_of(const GradArgs &a, int32_t d) {
     return min(max(__ldg(a.plan + a.at.bucket_slot + d), 0), a.n_slots - 1);
 }
 
+// The sum of a bucket's values of one (type, head), n slots from d0 on in every
+// slab: those of lane `lane` of `lanes`, of the slabs one after another.
+__device__ __forceinline__ float add_bucket(const GradArgs &a, int32_t type, int32_t b, int32_t head, int32_t lane,
+                                            int32_t lanes) {
+    const int32_t d0 = max(__ldg(a.plan + a.at.bucket_first + b), 0);
+    const int32_t n = min(__ldg(a.plan + a.at.bucket_first + b + 1), a.n_slots) - d0;
+    if (n <= 0) return 0.f;
+    const int64_t step = static_cast<int64_t>(a.n_types) * a.heads * a.n_slots;
+    const float *p = a.partial + (static_cast<int64_t>(type) * a.heads + head) * a.n_slots;
+    const int32_t by_slabs = lanes / n, by_slots = lanes - by_slabs * n;
+    int32_t s = lane / n, d = lane - s * n;
+    float sum = 0.f;
+    constexpr int kAhead = 8;  // loads in flight
+    while (s < a.slabs) {
+        const float *q[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            q[k] = s < a.slabs ? p + s * step + slot_of(a, d0 + d) : nullptr;
+            s += by_slabs, d += by_slots;
+            if (d >= n) d -= n, ++s;
+        }
+        float v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) v[k] = q[k] ? *q[k] : 0.f;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) sum += v[k];
+    }
+    return sum;
+}
+
 // Pass 2: LANES lanes a (type, bucket, head) add the bucket's slots over the
-// slabs (the lanes share the slabs where there are many, else the slots) and
-// round once to the table's format.  Heads are neighbours, as in the table.
-template <typename T, int LANES, bool kSlabs>
+// slabs and round once to the table's format.  Heads are neighbours, as in the
+// table.
+template <typename T, int LANES>
 __global__ void __launch_bounds__(kThreads) bias_grad_table(GradArgs a, int32_t blocks) {
     pdl_prologue();
     const bool ok = plan_matches(a);
@@ -706,30 +893,15 @@ __global__ void __launch_bounds__(kThreads) bias_grad_table(GradArgs a, int32_t 
     const int32_t i = ((blockIdx.x - type * blocks) * kThreads + static_cast<int32_t>(threadIdx.x)) / LANES;
     const int32_t lane = threadIdx.x % LANES;
     const int32_t b = i / a.heads, head = i - b * a.heads;
-    float v = 0.f;
-    if (ok && b < a.n_buckets) {
-        const int32_t d0 = max(__ldg(a.plan + a.at.bucket_first + b), 0);
-        const int32_t d1 = min(__ldg(a.plan + a.at.bucket_first + b + 1), a.n_slots);
-        const int64_t step = static_cast<int64_t>(a.n_types) * a.heads * a.n_slots;
-        const float *p = a.partial + (static_cast<int64_t>(type) * a.heads + head) * a.n_slots;
-        if constexpr (kSlabs) {
-            for (int32_t d = d0; d < d1; ++d) {
-                const float *q = p + slot_of(a, d);
-#pragma unroll 4
-                for (int32_t s = lane; s < a.slabs; s += LANES) v += q[s * step];
-            }
-        } else {
-            for (int32_t s = 0; s < a.slabs; ++s)
-#pragma unroll 4
-                for (int32_t d = d0 + lane; d < d1; d += LANES) v += p[s * step + slot_of(a, d)];
-        }
-    }
+    float v = ok && b < a.n_buckets ? add_bucket(a, type, b, head, lane, LANES) : 0.f;
     v = group_sum<LANES>(v);
     if (b < a.n_buckets && lane == 0)
         store1<T>(a.table, (static_cast<int64_t>(type) * a.n_buckets + b) * a.heads + head, v);
 }
 
-// Pass 2 where buckets have many values: a block a (type, bucket, head).
+// Pass 2 where buckets have many slots: a block a (type, bucket, head).  The
+// largest bucket bounds it, two rounds to L2 for 16 values a thread: 512 outputs
+// of 158,323 slots 19 us.  (A cluster of blocks an output: 175.)
 constexpr int kBlockThreads = 1024;
 
 template <typename T>
@@ -746,18 +918,26 @@ __global__ void __launch_bounds__(kBlockThreads) bias_grad_block(GradArgs a) {
         const int32_t d1 = min(__ldg(a.plan + a.at.bucket_first + b + 1), a.n_slots);
         const int64_t step = static_cast<int64_t>(a.n_types) * a.heads * a.n_slots;
         const float *p = a.partial + (static_cast<int64_t>(type) * a.heads + head) * a.n_slots;
-        for (int32_t s = 0; s < a.slabs; ++s)
-#pragma unroll 8
-            for (int32_t d = d0 + static_cast<int32_t>(threadIdx.x); d < d1; d += kBlockThreads)
-                v += p[s * step + slot_of(a, d)];
+        constexpr int kAhead = 16;  // loads in flight
+        for (int32_t s = 0; s < a.slabs; ++s, p += step)
+            for (int32_t d = d0 + static_cast<int32_t>(threadIdx.x); d < d1; d += kAhead * kBlockThreads) {
+                int32_t slot[kAhead];
+                float q[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    slot[k] = d1 - d > k * kBlockThreads ? slot_of(a, d + k * kBlockThreads) : -1;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) q[k] = slot[k] >= 0 ? p[slot[k]] : 0.f;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) v += q[k];
+            }
     }
     v = group_sum<32>(v);
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
-    if (threadIdx.x == 0) {
-#pragma unroll
-        for (int k = 1; k < kBlockThreads / 32; ++k) v += part[k];
-        store1<T>(a.table, blockIdx.x, v);
+    if (threadIdx.x < 32) {
+        v = group_sum<32>(part[threadIdx.x]);
+        if (threadIdx.x == 0) store1<T>(a.table, blockIdx.x, v);
     }
 }
 
@@ -795,7 +975,7 @@ __global__ void __launch_bounds__(kThreads) bias_grad_rows(GradArgs a, int32_t b
 }
 
 // Blocks of pass 1 at most: two on each of 152 SMs.
-constexpr int64_t kGradBlocks = 152 * WGS_GRAD_CTAS;
+constexpr int64_t kGradBlocks = 152 * kGradCtas;
 // Windows of a type in a slab at least, on average.
 constexpr int64_t kSlabWindows = 4;
 
@@ -817,6 +997,44 @@ int64_t grad_slabs(int64_t n_win, int64_t heads, int64_t n_types, int64_t n_tile
     return best;
 }
 
+// Maps that bias_grad_small takes, and how it is cut: maps of 1024 pairs still
+// gain (900 pairs, 16 heads, 1024 windows of 4 types: 13 us, by tiles 30), tiles of
+// one head are as good from there on.  At most one wave of blocks, and 16 rounds of
+// windows each on average: with 4 rounds 15 and 22 us where these take 9 and 15
+// (16 pairs of 32 heads, 256 pairs of 16 heads; 4096 windows).
+constexpr int64_t kSmallPairs = 1024, kSmallRounds = 16;
+bool small_map(int64_t n_pairs) { return n_pairs > 0 && n_pairs <= kSmallPairs; }
+int64_t small_heads(int64_t heads, int64_t n_pairs) {
+    const int64_t most = kSmallValues / ((n_pairs + 31) / 32 * 32);
+    return heads < most ? heads : most;
+}
+int64_t small_slabs(int64_t n_win, int64_t heads, int64_t n_types, int64_t n_pairs) {
+    const int64_t step = small_heads(heads, n_pairs), base = ceil_div(heads, step) * n_types;
+    const int64_t groups = step * n_pairs < kSmallThreads ? kSmallThreads / (step * n_pairs) : 1;
+    const int64_t room = kGradBlocks / base, most = n_win / (n_types * groups * kSmallRounds);
+    const int64_t s = room < most ? room : most;
+    return s > 1 ? s : 1;
+}
+// Slabs of a call.
+int64_t slabs_of(int64_t n_win, int64_t heads, int64_t n_types, int64_t n_pairs) {
+    return small_map(n_pairs) ? small_slabs(n_win, heads, n_types, n_pairs)
+                              : grad_slabs(n_win, heads, n_types, ceil_tiles(n_pairs));
+}
+
+template <typename E>
+wgs_status launch_small(const GradArgs &a, cudaStream_t stream) {
+    const int32_t step = static_cast<int32_t>(small_heads(a.heads, a.n_pairs));
+    const int64_t blocks = ceil_div(a.heads, step) * a.n_types * a.slabs;
+    if (blocks > INT32_MAX) return WGS_ERR_SHAPE;
+    constexpr bool k32 = std::is_same<E, F32>::value;
+    const bool two = !k32 && a.heads * a.n_pairs % 2 == 0 && step * a.n_pairs % 2 == 0 && aligned4(a.grad);
+    const bool one = step * a.n_pairs / (two ? 2 : 1) <= kSmallThreads;
+    auto kernel = one ? bias_grad_small<E, 1, 1> : bias_grad_small<E, 1, 8>;
+    if constexpr (!k32)
+        if (two) kernel = one ? bias_grad_small<E, 2, 1> : bias_grad_small<E, 2, 4>;
+    return launch(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kSmallThreads), 0, stream, a, step);
+}
+
 template <typename E, bool kVec>
 wgs_status launch_tiles(const GradArgs &a, cudaStream_t stream) {
     auto kernel = bias_grad_tiles<E, kVec>;
@@ -833,6 +1051,7 @@ wgs_status launch_tiles(const GradArgs &a, cudaStream_t stream) {
 
 template <typename E>
 wgs_status launch_tiles_any(const GradArgs &a, cudaStream_t stream) {
+    if (small_map(a.n_pairs)) return launch_small<E>(a, stream);
     constexpr int n = std::is_same<E, F32>::value ? 4 : 8;
     return a.n_pairs % n == 0 && aligned16(a.grad) ? launch_tiles<E, true>(a, stream)
                                                     : launch_tiles<E, false>(a, stream);
@@ -840,24 +1059,22 @@ wgs_status launch_tiles_any(const GradArgs &a, cudaStream_t stream) {
 
 template <typename T>
 wgs_status launch_table(const GradArgs &a, cudaStream_t stream) {
-    const int64_t mean = a.n_slots / a.n_buckets;
-    const bool slabs = a.slabs >= mean;
-    const int64_t most = slabs ? a.slabs : mean;
-    if (most < 4 && static_cast<int64_t>(a.n_types) * a.n_buckets >= 32 * kThreads) {
+    const int64_t outputs = static_cast<int64_t>(a.n_types) * a.n_buckets * a.heads;
+    const int64_t mean = static_cast<int64_t>(a.n_slots) * a.slabs / a.n_buckets;  // values of a bucket
+    if (mean < 4 && outputs >= 32 * kThreads * a.heads) {
         const int64_t blocks = ceil_div(a.n_buckets, kThreads);
         if (blocks * a.n_types > INT32_MAX) return WGS_ERR_SHAPE;
         return launch(bias_grad_rows<T>, dim3(static_cast<unsigned>(blocks * a.n_types)), dim3(kThreads), 0,
                       stream, a, static_cast<int32_t>(blocks));
     }
-    if (mean >= 64 && static_cast<int64_t>(a.n_types) * a.heads * a.n_buckets <= INT32_MAX)
-        return launch(bias_grad_block<T>, dim3(static_cast<unsigned>(a.n_types) * a.heads * a.n_buckets),
-                      dim3(kBlockThreads), 0, stream, a);
-    const int lanes = most < 4 ? 1 : most < 64 ? 8 : 32;
+    if (a.n_slots / a.n_buckets >= 64 && outputs <= INT32_MAX)
+        return launch(bias_grad_block<T>, dim3(static_cast<unsigned>(outputs)), dim3(kBlockThreads), 0, stream, a);
+    // more lanes where outputs are few: a bucket can hold many times the mean (32
+    // buckets of 2047 pairs in 77 slots, 32 heads: 5 us, a lane each 30)
+    const int lanes = mean >= 64 || outputs <= 8192 ? 32 : mean >= 8 || outputs <= 32768 ? 8 : 1;
     const int64_t blocks = ceil_div(static_cast<int64_t>(a.heads) * a.n_buckets * lanes, kThreads);
     if (blocks * a.n_types > INT32_MAX) return WGS_ERR_SHAPE;
-    auto kernel = lanes == 1 ? bias_grad_table<T, 1, true>
-                  : lanes == 8 ? (slabs ? bias_grad_table<T, 8, true> : bias_grad_table<T, 8, false>)
-                               : (slabs ? bias_grad_table<T, 32, true> : bias_grad_table<T, 32, false>);
+    auto kernel = lanes == 1 ? bias_grad_table<T, 1> : lanes == 8 ? bias_grad_table<T, 8> : bias_grad_table<T, 32>;
     return launch(kernel, dim3(static_cast<unsigned>(blocks * a.n_types)), dim3(kThreads), 0, stream, a,
                   static_cast<int32_t>(blocks));
 }
@@ -915,7 +1132,7 @@ extern "C" size_t wgs_position_bias_bwd_workspace_bytes(int64_t n_win, int32_t h
                                                         int32_t n_types, int64_t n_pairs,
                                                         int64_t n_slots) {
     if (n_win < 0 || heads < 1 || n_types < 1 || n_pairs < 0 || n_slots < 0) return 0;
-    return static_cast<size_t>(grad_slabs(n_win, heads, n_types, ceil_tiles(n_pairs))) * n_types *
+    return static_cast<size_t>(slabs_of(n_win, heads, n_types, n_pairs)) * n_types *
            heads * static_cast<size_t>(n_slots) * sizeof(float);
 }
 
@@ -930,10 +1147,11 @@ extern "C" wgs_status position_bias_bwd(const void *grad, const int32_t *plan,
     if (n_win < 0 || heads < 0 || n_pairs < 0 || n_buckets < 0 || n_types < 0 || n_slots < 0)
         return WGS_ERR_SHAPE;
     if (n_types == 0 || heads == 0 || n_buckets == 0) return WGS_OK;
-    if (n_pairs > INT32_MAX - kPlanTile || n_slots > n_pairs || n_win > INT32_MAX)
+    // (the kernels step past the last window by less than 65536)
+    if (n_pairs > INT32_MAX - kPlanTile || n_slots > n_pairs || n_win > INT32_MAX - 65536)
         return WGS_ERR_SHAPE;
     const int64_t n_tiles = ceil_tiles(n_pairs);
-    const int64_t slabs = grad_slabs(n_win, heads, n_types, n_tiles);
+    const int64_t slabs = slabs_of(n_win, heads, n_types, n_pairs);
     int64_t th, units, grad_bytes, table_bytes, part_bytes;
     if (!times(n_types, heads, &th) || !times(heads, n_buckets, &units) || units > INT32_MAX / 32 ||
         !times(th * slabs, n_tiles, &units) || units > INT32_MAX ||
