@@ -366,8 +366,7 @@ wgs_status window_bias_mask_add(const void *scores, const void *bias, const int3
  *   bias    [n_types, heads, n_pairs] of dtype (any wgs_dtype); must not
  *           overlap the inputs (WGS_ERR_ALIAS).
  * n_pairs must be below 2^31 - 4096 and heads * n_buckets below 2^26 (else
- * WGS_ERR_SHAPE).  Pointers need
- * their element's alignment; with n_pairs a multiple of 8 and bucket and
+ * WGS_ERR_SHAPE).  Pointers need their element's alignment; with n_pairs a multiple of 8 and bucket and
  * bias 16-byte aligned the heads of a bucket are read together (same
  * results). */
 wgs_status position_bias(const void *table, const int32_t *bucket, void *bias, int32_t n_types,
@@ -390,7 +389,10 @@ wgs_status position_bias(const void *table, const int32_t *bucket, void *bias, i
  *             of another type adds to no gradient and sets the error word.
  *   grad_table  [n_types, n_buckets, heads] of table_dtype (WGS_F32, or
  *             `dtype`); every entry is written, 0 where nothing is added.
- * heads * n_buckets must be below 2^26 (else WGS_ERR_SHAPE).
+ * n_pairs must be below 2^31 - 4096, n_win at most 2^31 - 65537, heads * n_buckets
+ * below 2^26 and the tiles of 4096 pairs of all heads and types below 2^31 (else
+ * WGS_ERR_SHAPE).  A block looks at the types of all windows of its share:
+ * n_types is meant to be a few hundred at most.
  *   workspace at least wgs_position_bias_bwd_workspace_bytes(...) bytes,
  *             16-byte aligned, disjoint from the tensors; its contents on
  *             entry do not matter.  Calls that overlap on the GPU need
@@ -470,7 +472,7 @@ wgs_status wgs_build_bucket_plan(const int32_t *bucket_host, int64_t n_pairs, in
  * n == 0 or spatial == 0 launches nothing.  Rows are moved in 16-byte chunks
  * when channels is a multiple of 4 (f32) or 8 (16-bit types) and x and y are
  * 16-byte aligned, else in pairs of elements or single ones.  Sums run in an
- * order that depends on the sizes alone. */
+ * order that depends on the sizes and on which of these it is. */
 size_t wgs_group_norm_act_workspace_bytes(int64_t n, int64_t spatial, int32_t channels,
                                           int32_t groups);
 wgs_status group_norm_act(const void *x, const void *weight, const void *bias, void *y, float *mean,

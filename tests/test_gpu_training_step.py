@@ -103,3 +103,39 @@ def test_block_gradients(stage, dtype):
     for name, got, want in zip(("x", "w", "b", "table"), _library(p, m), _autograd(p, m)):
         err = (got.double() - want).norm() / want.norm()
         assert err < bound, (name, err.item(), bound)
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls that overlap on the GPU, each with its own inputs and workspace,
+    give the bits that they give alone."""
+    gen = torch.Generator(DEV).manual_seed(3)
+    rand = lambda *shape: torch.randn(*shape, generator=gen, device=DEV)
+    bucket = wgs.build_window_buckets((1, 7, 7), device=DEV)
+    small = wgs.build_window_buckets((1, 3, 3), device=DEV)
+    plan, plan3 = wgs.build_bucket_plan(bucket, 169, device=DEV), wgs.build_bucket_plan(small, 25, device=DEV)
+    work = []
+    for _ in range(2):
+        x, gy, w, b = rand(3, 5000, 96), rand(3, 5000, 96), rand(96), rand(96)
+        xs, table = rand(900, 30, 64).half(), rand(2, 169, 4)
+        grad, grad3 = rand(300, 4, 49, 49).half(), rand(700, 6, 9, 9)
+        types = torch.randint(0, 2, (300,), generator=gen, device=DEV, dtype=torch.int32)
+
+        def run(x=x, gy=gy, w=w, b=b, xs=xs, table=table, grad=grad, grad3=grad3, types=types):
+            y, mean, rstd = wgs.group_norm_act(x, 8, w, b, 1e-5, "silu")
+            return (y, mean, rstd, *wgs.group_norm_act_bwd(gy, x, 8, mean, rstd, w, b, "silu"),
+                    wgs.group_norm_act(xs, 16)[0], wgs.position_bias(table, bucket, torch.float16),
+                    wgs.position_bias_bwd(grad, plan, types, 2), wgs.position_bias_bwd(grad3, plan3))
+        work.append(run)
+    want = [run() for run in work]
+    streams = [torch.cuda.Stream(DEV) for _ in work]
+    torch.cuda.synchronize(DEV)
+    for _ in range(3):
+        got = []
+        for run, stream in zip(work, streams):
+            with torch.cuda.stream(stream):
+                got.append([run() for _ in range(4)])
+        torch.cuda.synchronize(DEV)
+        for each, alone in zip(got, want):
+            for outs in each:
+                assert all(torch.equal(p, q) for p, q in zip(outs, alone))
+    wgs.check_error(DEV)

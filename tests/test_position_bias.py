@@ -108,6 +108,14 @@ def test_map_builder_refusals():
     assert g(2 ** 31 - 1, 2 ** 31 - 1, 0, 32, 128, 1, out, 576) == SHAPE
 
 
+def test_distance_buckets_of_a_reach_beyond_all_pairs():
+    # (the table of single distances is as long as the pairs need)
+    got = wgs.build_distance_buckets(3, 5, 32, 2 ** 31 - 1, True, 2)
+    d = np.arange(5)[None] - (np.arange(3)[:, None] + 2)
+    assert np.array_equal(got.numpy(), np.abs(d) + 16 * (d > 0))      # all below 8
+    assert np.array_equal(got.numpy(), oracle.build_distance_buckets(3, 5, 32, 2 ** 31 - 1, True, 2))
+
+
 # ------------------------------------------------------- host: the plan ----
 
 TILE = 4096
@@ -251,6 +259,14 @@ def test_position_bias_bwd_refusals():
     assert call(grad=None, plan=None, out=None, ws=None, n_types=0) == OK
     assert call(grad=None, plan=None, out=None, ws=None, heads=0) == OK
     assert call(grad=None, plan=None, out=None, ws=None, buckets=0) == OK
+
+
+def test_position_bias_bwd_refuses_too_many_windows():
+    f = _capi.load().position_bias_bwd
+    # the workspace is said to be large enough; nothing is launched
+    args = (A, B, None, C, D, 2 ** 62)
+    assert f(*args, 2 ** 31 - 65536, 1, 1, 1, 1, 1, 0, 0, None) == SHAPE
+    assert f(*args, 2 ** 31 - 65536, 1, 144, 9, 20, 1, 1, 0, None) == SHAPE
 
 
 def test_python_refusals_on_the_cpu():

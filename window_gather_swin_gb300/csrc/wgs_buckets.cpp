@@ -135,15 +135,18 @@ extern "C" wgs_status wgs_build_distance_buckets(int64_t n_q, int64_t n_k, int64
     if (n_q == 0 || n_k == 0) return WGS_OK;
     if (!out_host) return WGS_ERR_NULL;
     if (n_k > INT64_MAX / n_q || out_len < n_q * n_k) return WGS_ERR_SHAPE;
-    // the bucket depends on the distance alone; beyond max_distance it is the last
+    // the bucket depends on the distance alone; beyond max_distance it is the last.
+    // No pair is farther apart than `far`
+    const int64_t behind = n_q - 1 + q_start, ahead = n_k - 1;
+    const int64_t most = behind > ahead ? behind : ahead, far = most < max_distance ? most : max_distance;
     std::vector<int32_t> of;
     try {
-        of.resize(static_cast<size_t>(max_distance) + 1);
+        of.resize(static_cast<size_t>(far) + 1);
     } catch (const std::bad_alloc &) {
         return WGS_ERR_TOO_LARGE;
     }
     const double scale = (half - exact) / std::log(static_cast<double>(max_distance) / exact);
-    for (int64_t d = 0; d <= max_distance; ++d) {
+    for (int64_t d = 0; d <= far; ++d) {
         int64_t b = d;
         if (d >= exact) {
             b = exact + static_cast<int64_t>(
@@ -158,7 +161,7 @@ extern "C" wgs_status wgs_build_distance_buckets(int64_t n_q, int64_t n_k, int64
             int32_t b = -1;
             if (d <= 0 || bidirectional) {
                 const int64_t away = d < 0 ? -d : d;
-                b = of[static_cast<size_t>(away < max_distance ? away : max_distance)] +
+                b = of[static_cast<size_t>(away < far ? away : far)] +
                     (d > 0 ? half : 0);
             }
             out_host[i * n_k + j] = b;
