@@ -141,7 +141,9 @@ struct ExpandArgs {
 // pairs in registers and, HC heads at a time, gathers the heads of each
 // bucket in one load (they are neighbours in the table) and stores eight
 // outputs a head.  Neighbouring pairs name neighbouring or equal table rows,
-// so the gather stays in L1; the stores, whole lines a warp, are the cost.
+// so the gather stays in L1; the stores, whole lines a warp, are the cost.  64
+// types of 6 heads and 144 x 144 pairs, FP32 tables to fp16: 9.6 us for 16 MB
+// written and the tables read.
 template <typename O, typename T, int HC>
 __global__ void __launch_bounds__(kThreads) bias_expand_eights(ExpandArgs a) {
     pdl_prologue();
@@ -187,6 +189,8 @@ __global__ void __launch_bounds__(kThreads) bias_expand_eights(ExpandArgs a) {
 // a head go to shared memory, HC heads at a time, and from there to the slab
 // in words cut where the output's address is a multiple of four bytes, which
 // differs from head to head; neighbouring threads store neighbouring words.
+// 16 heads of 2047 x 2047 pairs, bf16: 35 us for 151 MB (4.3 TB/s); issue bounds
+// it, 77 % of the slots.
 template <typename O, typename T, int HC>
 __global__ void __launch_bounds__(kThreads) bias_expand_any(ExpandArgs a) {
     constexpr int kSpan = kThreads * 8, kB = kBytes<O>;
@@ -626,7 +630,7 @@ __device__ void slot_units(const GradArgs &a, GradShared<E> &sh, Unit u, int32_t
 // across units, four warps add them up and four add the last unit's sums up by
 // slot.  Every gradient is read once; what leaves is one value per slot.  The
 // order of all additions is fixed by the sizes and the plan.
-// 960 windows of 6 heads and 144 x 144 pairs in 5 types, fp16: 43 us of the call's
+// 960 windows of 6 heads and 144 x 144 pairs in 64 types, fp16: 43 us of the call's
 // 51 for 239 MB (5.6 TB/s, bound by DRAM).  Where a unit has one window the way
 // of its sums through shared memory bounds it: 16 heads of 2047 x 2047 pairs, 134
 // MB, 58 us (1.1 us a unit and block).
