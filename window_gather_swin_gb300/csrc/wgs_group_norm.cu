@@ -51,18 +51,21 @@ constexpr int kMaxGroups = 2048;
 // for the backward, whose threads need twice the registers and whose ring takes
 // the shared memory of the SM.  Measured, in us: the forward at [1, 131040, 192]
 // fp16 with SiLU and at [8, 32760, 384] bf16 with GELU, the backward at the same
-// with 4 samples: 32, 102, 51, 97; with 608 blocks of half the threads 52, 104,
+// with 4 samples: 32, 102, 50, 94; with 608 blocks of half the threads 52, 104,
 // 95, 122; with those for the forward's pass 2 alone 34 for the first.
 constexpr int kThreadsFwd = 384, kBlocksFwd = 304;
 constexpr int kThreadsBwd = 512, kBlocksBwd = 152;
 // Rows of a thread a stage and stages of the ring: the forward's with one
 // tensor, the backward's with two.  Same sizes: the forward with 2 x 6 36 and
-// 108, with 1 x 10 46 and 127, with 8 x 2 32 and 102; the backward with 2 x 4
-// 52 and 103, with 1 x 8 65 and 125.
+// 108, with 1 x 10 46 and 127, with 8 x 2 32 and 102; the backward with 4 x 3
+// 50 and 94, with 4 x 2 51 and 97, with 2 x 4 52 and 103, with 1 x 8 65 and
+// 125.  The backward's third stage is left out where the values of many
+// channels and groups or more blocks an SM need its room, and where each thread
+// copies its own rows.
 constexpr int kRowsFwd = 4, kStagesFwd = 3;
-constexpr int kRowsBwd = 4, kStagesBwd = 2;
-// Of a block.  The most that a call asks for is 208 KB (backward, 4096
-// channels of FP32 in 2048 groups).
+constexpr int kRowsBwd = 4, kStagesBwd = 2, kMostStages = 3;
+// Of a block.  The most that a call needs is 208 KB (backward, 4096 channels
+// of FP32 in 2048 groups).
 constexpr int kMaxSmem = 220 << 10;
 constexpr int kMaxCluster = 8;   // of a sample that one cluster holds
 
@@ -261,6 +264,7 @@ struct NormArgs {
     int32_t cluster, clusters;  // blocks of a cluster, clusters of a sample
     Slabs slabs1, slabs2;       // of the two passes
     int32_t ring;               // bytes of the slots
+    int32_t stages;             // of rows copied in bulk
     int32_t behind;             // bytes before what pass 1 of the backward keeps of the groups
     int32_t passes;             // of the launch: 1, 2 or 3 (both)
     bool last_use;              // pass 2's lines need not stay in L2: the call is larger
@@ -317,12 +321,13 @@ struct Job {
 // read them.  A thread spends nothing on addresses and copies of its own.
 struct Bars {
     uint32_t full, empty;  // of stage 0; 8 bytes a stage
+    int stages;
     int stage;             // of the next use
     uint32_t phase;        // its parity
     bool used;             // a stage has been
 };
 
-template <typename C, int kTensors, int kRows, int kStages>
+template <typename C, int kTensors, int kRows, int kStages>  // stages, or 0: bars.stages
 struct Bulk {
     const Job &job;
     Bars &bars;
@@ -339,6 +344,7 @@ struct Bulk {
     __device__ static void wait(uint32_t bar, uint32_t parity) {
         if (!bar_wait(bar, parity)) atomicOr(&g_norm_error, 1u);
     }
+    __device__ int stages() const { return kStages ? kStages : bars.stages; }
     __device__ uint32_t stage_bytes() const { return job.threads * C::kBytes * kTensors * kRows; }
     __device__ int32_t stage_rows() const { return job.row_groups * kRows; }
 
@@ -368,8 +374,8 @@ struct Bulk {
         if (job.tid == 0) {
             // what the block wrote to the slots comes before the copies
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            for (int i = 0; i < kStages - 1 && i < count; ++i)
-                copy(i, bars.stage + i < kStages ? bars.stage + i : bars.stage + i - kStages);
+            for (int i = 0; i < stages() - 1 && i < count; ++i)
+                copy(i, bars.stage + i < stages() ? bars.stage + i : bars.stage + i - stages());
         }
     }
     template <typename Use>
@@ -379,11 +385,11 @@ struct Bulk {
         int64_t at = base + job.g * row_bytes + job.j * C::kBytes;
         if (reverse) at += static_cast<int64_t>(count - 1) * kRows * step;
         for (int32_t i = 0; i < count; ++i) {
-            if (job.tid == 0 && i + kStages - 1 < count) {
+            if (job.tid == 0 && i + stages() - 1 < count) {
                 // into the slot that was read last, when all warps have
-                const int free = bars.stage == 0 ? kStages - 1 : bars.stage - 1;
+                const int free = bars.stage == 0 ? stages() - 1 : bars.stage - 1;
                 if (bars.used) wait(bars.empty + 8 * free, bars.stage == 0 ? bars.phase ^ 1 : bars.phase);
-                copy(i + kStages - 1, free);
+                copy(i + stages() - 1, free);
             }
             wait(bars.full + 8 * bars.stage, bars.phase);
             const uint32_t slot = ring + bars.stage * stage_bytes() + job.tid * C::kBytes;
@@ -412,7 +418,7 @@ struct Bulk {
             __syncwarp();
             if ((job.tid & 31) == 0) bar_arrive(bars.empty + 8 * bars.stage);
             bars.used = true;
-            if (++bars.stage == kStages) bars.stage = 0, bars.phase ^= 1;
+            if (++bars.stage == stages()) bars.stage = 0, bars.phase ^= 1;
         }
     }
 };
@@ -495,18 +501,18 @@ struct Own {
 template <typename C, int kTensors>
 using Stream = std::conditional_t<
     C::kBytes == 16,
-    std::conditional_t<kTensors == 1, Bulk<C, 1, kRowsFwd, kStagesFwd>, Bulk<C, 2, kRowsBwd, kStagesBwd>>,
+    std::conditional_t<kTensors == 1, Bulk<C, 1, kRowsFwd, kStagesFwd>, Bulk<C, 2, kRowsBwd, 0>>,
     std::conditional_t<kTensors == 1, Own<C, 1, kRowsFwd, kStagesFwd>, Own<C, 2, kRowsBwd, kStagesBwd>>>;
 
 // The block's barriers, before its first job.
-template <int kStages>
-__device__ __forceinline__ Bars make_bars(uint64_t *storage) {
+__device__ __forceinline__ Bars make_bars(uint64_t *storage, int stages) {
     Bars b;
+    b.stages = stages;
     b.full = static_cast<uint32_t>(__cvta_generic_to_shared(storage));
-    b.empty = b.full + 8 * kStages;
+    b.empty = b.full + 8 * kMostStages;
     b.stage = 0, b.phase = 0, b.used = false;
     if (threadIdx.x == 0 && threadIdx.y == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < stages; ++i) {
             bar_init(b.full + 8 * i, 1);
             bar_init(b.empty + 8 * i, (blockDim.x * blockDim.y + 31) / 32);
         }
@@ -785,8 +791,8 @@ __device__ void apply_pass(const NormArgs &a, const Job &job, Bars &bars, float2
 template <typename E, int kV, int kAct>
 __global__ void __launch_bounds__(kThreadsFwd, 2) norm_forward(NormArgs a) {
     extern __shared__ __align__(16) float2 smem[];
-    __shared__ __align__(8) uint64_t storage[2 * kStagesFwd];
-    Bars bars = make_bars<kStagesFwd>(storage);
+    __shared__ __align__(8) uint64_t storage[2 * kMostStages];
+    Bars bars = make_bars(storage, a.stages);
     start_launch(a);
     const Job job(a);
     if (a.passes & 1) stats_pass<E, kV>(a, job, bars, smem);
@@ -903,8 +909,8 @@ __device__ void sums_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
 // (x - mean) rstd^2 M2.  The gate is computed in both passes, two special
 // functions an element: 10 us a pass at [1, 131040, 192] on that unit alone,
 // beside 15 us for 100 MB from DRAM; keeping dz for pass 2 would be 50 MB to write
-// and to read.  That size takes 51 us for 151 MB (3.0 TB/s; pass 2 finds 60 of
-// its 100 MB in L2), [4, 32760, 384] bf16 97 us for 302 MB.
+// and to read.  That size takes 50 us for 151 MB (3.0 TB/s; pass 2 finds 60 of
+// its 100 MB in L2), [4, 32760, 384] bf16 94 us for 302 MB.
 template <typename E, int kV, int kAct>
 __device__ void grad_pass(const NormArgs &a, const Job &job, Bars &bars, float2 *smem) {
     using C = Chunk<E, kV>;
@@ -958,8 +964,8 @@ __device__ void grad_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
 template <typename E, int kV, int kAct>
 __global__ void __launch_bounds__(kThreadsBwd, 1) norm_backward(NormArgs a) {
     extern __shared__ __align__(16) float2 smem[];
-    __shared__ __align__(8) uint64_t storage[2 * kStagesBwd];
-    Bars bars = make_bars<kStagesBwd>(storage);
+    __shared__ __align__(8) uint64_t storage[2 * kMostStages];
+    Bars bars = make_bars(storage, a.stages);
     start_launch(a);
     const Job job(a);
     if (a.passes & 1) sums_pass<E, kV, kAct>(a, job, bars, smem);
@@ -1117,15 +1123,23 @@ wgs_status run(NormArgs a, const Plan &z, int act, bool backward, int64_t n, cud
         // slots, the row groups' sums and the groups'; where one walk covers
         // the row the channels' lie over the slots too.  Pass 2: the slots,
         // the groups' and channels' values, a pair a thread.
-        a.ring = C::kBytes < 4 ? 0 : threads * C::kBytes * (backward ? 2 * kRowsBwd * kStagesBwd : kRowsFwd * kStagesFwd);
         const int red = 8 * (threads * kV > a.groups ? threads * kV : a.groups), ch = 8 * a.channels;
-        const int pass1 = columns == a.chunks ? (ch + red > a.ring ? ch + red : a.ring)
-                                              : ch + (red > a.ring ? red : a.ring);
-        // (the backward's pass 1 keeps the groups' and channels' values behind that)
-        a.behind = (pass1 + 15) / 16 * 16;
-        const int one = passes & 1 ? a.behind + (backward ? 8 * (a.groups + a.channels) : 0) : 0;
-        const int two = passes & 2 ? a.ring + 8 * ((backward ? 2 : 1) * a.groups + a.channels + threads) : 0;
-        const int smem = one > two ? one : two;
+        auto size = [&](int stages) {
+            a.stages = stages;
+            a.ring = C::kBytes < 4 ? 0 : threads * C::kBytes * (backward ? 2 * kRowsBwd : kRowsFwd) * stages;
+            const int pass1 = columns == a.chunks ? (ch + red > a.ring ? ch + red : a.ring)
+                                                  : ch + (red > a.ring ? red : a.ring);
+            // (the backward's pass 1 keeps the groups' and channels' values behind that)
+            a.behind = (pass1 + 15) / 16 * 16;
+            const int one = passes & 1 ? a.behind + (backward ? 8 * (a.groups + a.channels) : 0) : 0;
+            const int two = passes & 2 ? a.ring + 8 * ((backward ? 2 : 1) * a.groups + a.channels + threads) : 0;
+            return one > two ? one : two;
+        };
+        int smem = size(backward ? kStagesBwd : kStagesFwd);
+        if (backward && C::kBytes == 16 && most == kThreadsBwd) {
+            smem = size(kMostStages);
+            if (smem > kMaxSmem) smem = size(kStagesBwd);
+        }
         // Above 48 KB a kernel needs the runtime's leave, which belongs to the
         // context; asking for the same amount on every call needs no record of it.
         if (smem > 48 << 10 &&
