@@ -185,15 +185,37 @@ __global__ void __launch_bounds__(kThreads) bias_expand_eights(ExpandArgs a) {
     }
 }
 
+// 16 bytes of a row in shared memory, from `lead` elements past the aligned `p` on
+// (lead * kB below 16, the same for all threads).
+template <int kB>
+__device__ __forceinline__ uint4 shifted16(const char *p, int lead) {
+    const uint4 lo = reinterpret_cast<const uint4 *>(p)[0];
+    if (lead == 0) return lo;
+    const uint4 hi = reinterpret_cast<const uint4 *>(p)[1];
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const int words = lead * kB / 4;
+    uint32_t v[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) {
+        const uint32_t near = words & 1 ? w[j + 1] : w[j];
+        const uint32_t far = j + 3 > 7 ? 0u : words & 1 ? w[j + 3] : w[j + 2];
+        v[j] = words & 2 ? far : near;
+    }
+    if (kB == 2 && lead & 1)
+        return make_uint4(__byte_perm(v[0], v[1], 0x5432), __byte_perm(v[1], v[2], 0x5432),
+                          __byte_perm(v[2], v[3], 0x5432), __byte_perm(v[3], v[4], 0x5432));
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 // Any pair count or alignment.  As above up to the stores: the eight outputs of
 // a head go to shared memory, HC heads at a time, and from there to the slab
-// in words cut where the output's address is a multiple of four bytes, which
-// differs from head to head; neighbouring threads store neighbouring words.
-// 16 heads of 2047 x 2047 pairs, bf16: 35 us for 151 MB (4.3 TB/s); issue bounds
-// it, 77 % of the slots.
+// in 16 bytes cut where the output's address is a multiple of 16, which differs
+// from head to head; neighbouring threads store neighbours.
+// 16 heads of 2047 x 2047 pairs, bf16: 30 us for 151 MB (5.0 TB/s; in words instead
+// of 16 bytes 35, bound by issue).
 template <typename O, typename T, int HC>
 __global__ void __launch_bounds__(kThreads) bias_expand_any(ExpandArgs a) {
-    constexpr int kSpan = kThreads * 8, kB = kBytes<O>;
+    constexpr int kSpan = kThreads * 8, kB = kBytes<O>, kEach = 16 / kB;
     // kept twice, so that one barrier a step does
     __shared__ __align__(16) char rows[2][HC][kSpan * kB + 16];
     pdl_prologue();
@@ -232,27 +254,21 @@ __global__ void __launch_bounds__(kThreads) bias_expand_any(ExpandArgs a) {
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < HC; ++k) {
-            const int64_t first = (type * a.heads + h + k) * a.n_pairs + p0;  // element of the output
+            char *to = static_cast<char *>(a.bias) + ((type * a.heads + h + k) * a.n_pairs + p0) * kB;
             const char *from = rows[turn][k];
-            if constexpr (kB == 4) {
-                for (int32_t i = threadIdx.x; i < count; i += kThreads)
-                    static_cast<uint32_t *>(a.bias)[first + i] = reinterpret_cast<const uint32_t *>(from)[i];
-            } else {
-                uint16_t *to = static_cast<uint16_t *>(a.bias) + first;
-                const uint16_t *q = reinterpret_cast<const uint16_t *>(from);
-                // odd: the slab's piece starts in the middle of a word
-                const int odd = static_cast<int>((reinterpret_cast<uintptr_t>(to) >> 1) & 1);
-                const int32_t words = (count - odd) / 2;
-                uint32_t *out = reinterpret_cast<uint32_t *>(to + odd);
-                if (odd) {
-                    for (int32_t i = threadIdx.x; i < words; i += kThreads)
-                        out[i] = q[2 * i + 1] | static_cast<uint32_t>(q[2 * i + 2]) << 16;
-                } else {
-                    for (int32_t i = threadIdx.x; i < words; i += kThreads)
-                        out[i] = reinterpret_cast<const uint32_t *>(q)[i];
-                }
-                if (threadIdx.x == 0 && odd && count > 0) to[0] = q[0];
-                if (threadIdx.x == 1 && odd + 2 * words < count) to[count - 1] = q[count - 1];
+            // elements before the first whole 16 bytes, whole ones, elements behind
+            const int32_t lead = min(static_cast<int32_t>((16 - (reinterpret_cast<uintptr_t>(to) & 15)) & 15) / kB, count);
+            const int32_t whole = (count - lead) / kEach, behind = count - lead - whole * kEach;
+            for (int32_t i = threadIdx.x; i < whole; i += kThreads)
+                st_stream(reinterpret_cast<uint4 *>(to + lead * kB) + i, shifted16<kB>(from + i * 16, lead));
+            // the odd elements by threads of their own
+            const int32_t e = static_cast<int32_t>(threadIdx.x);
+            const int32_t odd = e < lead ? e : count - 1 - (e - lead);
+            if (e < lead + behind) {
+                if constexpr (kB == 4)
+                    reinterpret_cast<uint32_t *>(to)[odd] = reinterpret_cast<const uint32_t *>(from)[odd];
+                else
+                    reinterpret_cast<uint16_t *>(to)[odd] = reinterpret_cast<const uint16_t *>(from)[odd];
             }
         }
     }
