@@ -320,6 +320,7 @@ struct GradArgs {
     int64_t n_pairs;
     int32_t n_win, heads, n_types, n_buckets, n_tiles, n_slots, slabs;
     int32_t units;            // n_tiles * n_types * slabs * heads
+    bool follows;             // pass 2: pass 1 of the call is the launch before
 };
 
 // The plan's header against the sizes of the call (a plan of another map
@@ -364,7 +365,7 @@ constexpr int kGradThreads = kAdders + kSlotters + 32;
 constexpr int kListed = 1024;                 // windows looked over at a time
 // Blocks of an SM, and stages of a block's ring (48 KB).  960 windows of 6 heads and
 // 144 x 144 pairs, fp16: two blocks of six stages 59 us, of four 60, one block 84
-// (51 since the slots are added by lanes).
+// (49 now, with slots added by lanes).
 constexpr int kGradCtas = 2;
 template <typename E>
 constexpr int kGradStages = std::is_same<E, F32>::value ? 4 : 6;
@@ -726,8 +727,8 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas) bias_grad_tiles(GradA
 // window by window, groups of threads the windows in turn.  A thread keeps the
 // sums of the same kOwn words (of kW pairs) of each of its windows; the groups'
 // are added in order in shared memory, and from there by slot, as above.  4096
-// windows, fp16, us of the call (by tiles): 1 pair of 32 heads 6 (134), 16 pairs of
-// 32 heads 9 (83), 256 pairs of 16 heads, 34 MB, 15 (45).  Latency bounds it.
+// windows, fp16, us of the call (by tiles): 1 pair of 32 heads 5 (134), 16 pairs of
+// 32 heads 8 (83), 256 pairs of 16 heads, 34 MB, 12 (45).  Latency bounds it.
 constexpr int kSmallThreads = 512, kSmallValues = 4096;
 
 template <typename E, int kW, int kOwn>
@@ -866,6 +867,22 @@ __global__ void __launch_bounds__(kSmallThreads, 2) bias_grad_small(GradArgs a, 
     }
 }
 
+// Pass 2 after pass 1: all that came before on the stream is done when it starts
+// (pass 1 has waited for it), so the plan may be read at once; the sums are there
+// after wait_for_slots.  On its own it waits first.  (1 to 2 us of a call: 49 x 49
+// pairs of 12 heads, 1024 windows 18.1 us on the device, 20.1 waiting first.)
+__device__ __forceinline__ void start_table(const GradArgs &a) {
+#if WGS_PDL
+    if (!a.follows) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+#endif
+}
+__device__ __forceinline__ void wait_for_slots(const GradArgs &a) {
+#if WGS_PDL
+    if (a.follows) asm volatile("griddepcontrol.wait;" ::: "memory");
+#endif
+}
+
 // The d-th slot of the buckets' lists.
 __device__ __forceinline__ int32_t slot_of(const GradArgs &a, int32_t d) {
     return min(max(__ldg(a.plan + a.at.bucket_slot + d), 0), a.n_slots - 1);
@@ -877,14 +894,18 @@ __device__ __forceinline__ float add_bucket(const GradArgs &a, int32_t type, int
                                             int32_t lanes) {
     const int32_t d0 = max(__ldg(a.plan + a.at.bucket_first + b), 0);
     const int32_t n = min(__ldg(a.plan + a.at.bucket_first + b + 1), a.n_slots) - d0;
-    if (n <= 0) return 0.f;
+    if (n <= 0) {
+        wait_for_slots(a);
+        return 0.f;
+    }
     const int64_t step = static_cast<int64_t>(a.n_types) * a.heads * a.n_slots;
     const float *p = a.partial + (static_cast<int64_t>(type) * a.heads + head) * a.n_slots;
     const int32_t by_slabs = lanes / n, by_slots = lanes - by_slabs * n;
     int32_t s = lane / n, d = lane - s * n;
     float sum = 0.f;
     constexpr int kAhead = 8;  // loads in flight
-    while (s < a.slabs) {
+    bool first = true;
+    do {
         const float *q[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
@@ -892,12 +913,14 @@ __device__ __forceinline__ float add_bucket(const GradArgs &a, int32_t type, int
             s += by_slabs, d += by_slots;
             if (d >= n) d -= n, ++s;
         }
+        if (first) wait_for_slots(a);
+        first = false;
         float v[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) v[k] = q[k] ? *q[k] : 0.f;
+        for (int k = 0; k < kAhead; ++k) v[k] = q[k] ? __ldcg(q[k]) : 0.f;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) sum += v[k];
-    }
+    } while (s < a.slabs);
     return sum;
 }
 
@@ -906,14 +929,18 @@ __device__ __forceinline__ float add_bucket(const GradArgs &a, int32_t type, int
 // table.
 template <typename T, int LANES>
 __global__ void __launch_bounds__(kThreads) bias_grad_table(GradArgs a, int32_t blocks) {
-    pdl_prologue();
+    start_table(a);
     const bool ok = plan_matches(a);
     if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_bucket_error, 1u);
     const int32_t type = blockIdx.x / blocks;
     const int32_t i = ((blockIdx.x - type * blocks) * kThreads + static_cast<int32_t>(threadIdx.x)) / LANES;
     const int32_t lane = threadIdx.x % LANES;
     const int32_t b = i / a.heads, head = i - b * a.heads;
-    float v = ok && b < a.n_buckets ? add_bucket(a, type, b, head, lane, LANES) : 0.f;
+    float v = 0.f;
+    if (ok && b < a.n_buckets)
+        v = add_bucket(a, type, b, head, lane, LANES);
+    else
+        wait_for_slots(a);
     v = group_sum<LANES>(v);
     if (b < a.n_buckets && lane == 0)
         store1<T>(a.table, (static_cast<int64_t>(type) * a.n_buckets + b) * a.heads + head, v);
@@ -927,12 +954,13 @@ constexpr int kBlockThreads = 1024;
 template <typename T>
 __global__ void __launch_bounds__(kBlockThreads) bias_grad_block(GradArgs a) {
     __shared__ float part[kBlockThreads / 32];
-    pdl_prologue();
+    start_table(a);
     const bool ok = plan_matches(a);
     if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_bucket_error, 1u);
     const int32_t head = blockIdx.x % a.heads, tb = blockIdx.x / a.heads;
     const int32_t type = tb / a.n_buckets, b = tb - type * a.n_buckets;
     float v = 0.f;
+    bool waited = false;
     if (ok) {
         const int32_t d0 = max(__ldg(a.plan + a.at.bucket_first + b), 0);
         const int32_t d1 = min(__ldg(a.plan + a.at.bucket_first + b + 1), a.n_slots);
@@ -946,12 +974,15 @@ __global__ void __launch_bounds__(kBlockThreads) bias_grad_block(GradArgs a) {
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k)
                     slot[k] = d1 - d > k * kBlockThreads ? slot_of(a, d + k * kBlockThreads) : -1;
+                if (!waited) wait_for_slots(a);
+                waited = true;
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) q[k] = slot[k] >= 0 ? p[slot[k]] : 0.f;
+                for (int k = 0; k < kAhead; ++k) q[k] = slot[k] >= 0 ? __ldcg(p + slot[k]) : 0.f;
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) v += q[k];
             }
     }
+    if (!waited) wait_for_slots(a);
     v = group_sum<32>(v);
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
@@ -965,14 +996,17 @@ __global__ void __launch_bounds__(kBlockThreads) bias_grad_block(GradArgs a) {
 // heads, whose slots it looks up once; the threads' slots are neighbours.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) bias_grad_rows(GradArgs a, int32_t blocks) {
-    pdl_prologue();
+    start_table(a);
     const bool ok = plan_matches(a);
     if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_bucket_error, 1u);
     const int32_t type = blockIdx.x / blocks;
     const int32_t b = (blockIdx.x - type * blocks) * kThreads + static_cast<int32_t>(threadIdx.x);
+    const bool mine = ok && b < a.n_buckets;
+    const int32_t d0 = mine ? max(__ldg(a.plan + a.at.bucket_first + b), 0) : 0;
+    const int32_t d1 = mine ? min(__ldg(a.plan + a.at.bucket_first + b + 1), a.n_slots) : 0;
+    const int32_t slot0 = d0 < d1 ? slot_of(a, d0) : 0;
+    wait_for_slots(a);
     if (b >= a.n_buckets) return;
-    const int32_t d0 = ok ? max(__ldg(a.plan + a.at.bucket_first + b), 0) : 0;
-    const int32_t d1 = ok ? min(__ldg(a.plan + a.at.bucket_first + b + 1), a.n_slots) : 0;
     const int64_t step = static_cast<int64_t>(a.n_types) * a.heads * a.n_slots;
     const float *p = a.partial + static_cast<int64_t>(type) * a.heads * a.n_slots;
     const int64_t out = (static_cast<int64_t>(type) * a.n_buckets + b) * a.heads;
@@ -982,11 +1016,15 @@ __global__ void __launch_bounds__(kThreads) bias_grad_rows(GradArgs a, int32_t b
 #pragma unroll
         for (int k = 0; k < kHeads; ++k) v[k] = 0.f;
         for (int32_t d = d0; d < d1; ++d) {
-            const float *q = p + static_cast<int64_t>(h0) * a.n_slots + slot_of(a, d);
-            for (int32_t s = 0; s < a.slabs; ++s, q += step)
+            const float *q = p + static_cast<int64_t>(h0) * a.n_slots + (d == d0 ? slot0 : slot_of(a, d));
+            for (int32_t s = 0; s < a.slabs; ++s, q += step) {
+                float t[kHeads];
 #pragma unroll
                 for (int k = 0; k < kHeads; ++k)
-                    if (h0 + k < a.heads) v[k] += q[static_cast<int64_t>(k) * a.n_slots];
+                    t[k] = h0 + k < a.heads ? __ldcg(q + static_cast<int64_t>(k) * a.n_slots) : 0.f;
+#pragma unroll
+                for (int k = 0; k < kHeads; ++k) v[k] += t[k];
+            }
         }
 #pragma unroll
         for (int k = 0; k < kHeads; ++k)
@@ -1201,7 +1239,7 @@ extern "C" wgs_status position_bias_bwd(const void *grad, const int32_t *plan,
                   static_cast<float *>(workspace), grad_table, at, n_pairs,
                   static_cast<int32_t>(n_win), heads, n_types, n_buckets,
                   static_cast<int32_t>(n_tiles), static_cast<int32_t>(n_slots),
-                  static_cast<int32_t>(slabs), static_cast<int32_t>(units)};
+                  static_cast<int32_t>(slabs), static_cast<int32_t>(units), units > 0};
     if (units > 0) {
         st = dtype == WGS_F32   ? launch_tiles_any<F32>(a, stream)
              : dtype == WGS_F16 ? launch_tiles_any<Fp16>(a, stream)
