@@ -35,9 +35,9 @@
  *     to steer those fetches).  No value read before the previous kernel
  *     has completed reaches a result: indices and rows are read again after
  *     the wait, so the usual stream order holds for every buffer.  (A call of
- *     several kernels, group_norm_act and its backward, has its later ones
- *     read the call's inputs while its first one runs, never before that one
- *     has waited.)
+ *     several kernels, position_bias_bwd or group_norm_act and its backward,
+ *     may have its second one read the call's inputs while its first one
+ *     runs, never before that one has waited.)
  *   - Arguments are checked before anything is launched; a failed check
  *     returns a status and launches nothing.  A launch failure reported by
  *     the runtime returns WGS_ERR_LAUNCH.

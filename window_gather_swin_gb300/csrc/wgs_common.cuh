@@ -38,9 +38,10 @@ wgs_status group_norm_error_take(unsigned int *seen, cudaStream_t stream);
 
 // Launch `kernel` on `stream`.  With WGS_PDL the launch allows programmatic
 // dependent launch: the grid may be scheduled while the previous kernel on
-// the stream drains, and every kernel of this library starts with
-// pdl_prologue(), whose griddepcontrol.wait holds it until the previous
-// grid has completed and its writes are visible.  Kernels that do not use
+// the stream drains, and every kernel of this library that can be the first of
+// a call starts with pdl_prologue(), whose griddepcontrol.wait holds it until the
+// previous grid has completed and its writes are visible (a call's second kernel
+// may wait later, see start_launch and start_table).  Kernels that do not use
 // these controls (other libraries') keep the usual full serialisation.
 template <typename... Params, typename... Args>
 wgs_status launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
