@@ -67,6 +67,7 @@ constexpr int kRowsBwd = 4, kStagesBwd = 2, kMostStages = 3;
 // Of a block.  The most that a call needs is 208 KB (backward, 4096 channels
 // of FP32 in 2048 groups).
 constexpr int kMaxSmem = 220 << 10;
+constexpr int kBarBytes = 2 * kMostStages * static_cast<int>(sizeof(uint64_t));  // beside kMaxSmem
 constexpr int kMaxCluster = 8;   // of a sample that one cluster holds
 
 enum : int { kNone = 0, kSilu = 1, kGeluTanh = 2 };
@@ -791,7 +792,7 @@ __device__ void apply_pass(const NormArgs &a, const Job &job, Bars &bars, float2
 template <typename E, int kV, int kAct>
 __global__ void __launch_bounds__(kThreadsFwd, 2) norm_forward(NormArgs a) {
     extern __shared__ __align__(16) float2 smem[];
-    __shared__ __align__(8) uint64_t storage[2 * kMostStages];
+    __shared__ __align__(8) uint64_t storage[kBarBytes / sizeof(uint64_t)];
     Bars bars = make_bars(storage, a.stages);
     start_launch(a);
     const Job job(a);
@@ -964,7 +965,7 @@ __device__ void grad_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
 template <typename E, int kV, int kAct>
 __global__ void __launch_bounds__(kThreadsBwd, 1) norm_backward(NormArgs a) {
     extern __shared__ __align__(16) float2 smem[];
-    __shared__ __align__(8) uint64_t storage[2 * kMostStages];
+    __shared__ __align__(8) uint64_t storage[kBarBytes / sizeof(uint64_t)];
     Bars bars = make_bars(storage, a.stages);
     start_launch(a);
     const Job job(a);
@@ -1140,9 +1141,10 @@ wgs_status run(NormArgs a, const Plan &z, int act, bool backward, int64_t n, cud
             smem = size(kMostStages);
             if (smem > kMaxSmem) smem = size(kStagesBwd);
         }
-        // Above 48 KB a kernel needs the runtime's leave, which belongs to the
-        // context; asking for the same amount on every call needs no record of it.
-        if (smem > 48 << 10 &&
+        // Above 48 KB, its static barriers among them, a kernel needs the
+        // runtime's leave, which belongs to the context; asking for the same
+        // amount on every call needs no record of it.
+        if (smem + kBarBytes > 48 << 10 &&
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) {
             cudaGetLastError();
             return WGS_ERR_LAUNCH;
