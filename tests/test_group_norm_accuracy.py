@@ -1,0 +1,131 @@
+"""Group norm's statistics where sums lose most, against 64 bits with
+tolerances from the kernels' own depth.
+
+With u = 2^-24, and D the additions on a value's way: a thread's rows, the row
+groups of its block, a group's channels and the blocks' parts,
+
+* mean: each sum is of distances from a reference, which a thread moves to its
+  running mean after 8, 64, 512 ... rows.  A row that lies d from all others
+  can leave the next 7n rows, after n, at d / n each: at most (8n)^2 / 2 roundings
+  of u d / n, 32 n u d, in all no more than 37 u d times the thread's rows.  The
+  group's distances from its mean come to about 2d with it, so
+  |err| <= 20 D u mean|x - mean| + 2u |mean|.
+* rstd: likewise the squares take 36 u d^2 before the first move and
+  (8n)^2 / 2 (d / n)^2 u = 32 u d^2 after each, of which there are at most 5, where M2
+  is at least d^2 - d^2 / rows.  With D u for the rest and D u for the joins of the
+  blocks, var is off by (2D + 200) u and rstd by half: (D + 100) u + 8u.
+* y, from the mean and rstd that the kernel gave: z = h w + b is off by
+  3u (|h w| + |b|), an activation's slope is at most 1.13, and its own
+  evaluation costs |y| (4u |t| + 16u), t the sigmoid's argument.
+* rounding to the output's format adds half a step.
+"""
+import math
+
+import pytest
+import torch
+
+import window_gather_swin_gb300 as wgs
+
+DEV = "cuda:0"
+U = 2.0 ** -24
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+pytestmark = pytest.mark.gpu
+
+
+def _depth(shape, fmt, backward):
+    """D of a call: how many blocks share a sample, and a block's row
+    groups, as the library chooses them from the sizes."""
+    n, s, c, g = shape
+    size = 4 if fmt == "f32" else 2
+    chunks = c // (16 // size if c * size % 16 == 0 else 2 if c % 2 == 0 else 1)
+    most, threads, parts = -(-s // 16), 512 if backward else 384, 1
+    while parts < 8 and 2 * parts <= most and (n * parts < 608 or s * c >= 2 * parts * 65536):
+        parts *= 2
+    if s * c > 1 << 19 and n * parts < 304:
+        parts = min(152 // n, most)
+    elif n * parts > (100 if backward else 304):
+        threads = 256
+        want = -(-s // parts // 32) * chunks
+        while n * parts > 304 and threads > 64 and threads // 2 >= want:
+            threads //= 2
+    groups = threads // min(chunks, threads)
+    mine = -(-(-(-s // parts)) // groups)
+    return mine + groups + c // g + parts + 32
+
+
+def _slope(z, act):
+    """act(z) and act'(z) in double."""
+    if act is None:
+        return z, torch.ones_like(z)
+    if act == "silu":
+        s = torch.sigmoid(z)
+        return z * s, s + z * s * torch.sigmoid(-z)
+    k = 2 * math.sqrt(2 / math.pi)
+    t = k * (z + 0.044715 * z ** 3)
+    s = torch.sigmoid(t)
+    return z * s, s + z * s * torch.sigmoid(-t) * k * (1 + 3 * 0.044715 * z * z)
+
+
+def _half(want, dtype):
+    f = torch.finfo(dtype)
+    return want.abs().clamp(min=f.smallest_normal) * (f.eps / 2)
+
+
+def _check_statistics(x, mean, rstd, g, eps, D):
+    n, s, c = x.shape
+    for i in range(n):
+        xd = x[i].double().view(s, g, c // g)
+        m = xd.mean((0, 2))
+        away = (xd - m[:, None]).abs()
+        r = (away.square().mean((0, 2)) + eps).rsqrt()
+        err = (mean[i].double() - m).abs() / (20 * D * U * away.mean((0, 2)) + 2 * U * m.abs())
+        assert err.max() <= 1, ("mean", i, err.max().item())
+        err = (rstd[i].double() / r - 1).abs() / ((D + 108) * U)
+        assert err.max() <= 1, ("rstd", i, err.max().item())
+
+
+def _check_output(x, y, w, b, mean, rstd, g, act):
+    n, s, c = x.shape
+    up = lambda v: v.double().repeat_interleave(c // g)
+    for i in range(n):
+        hw = (x[i].double() - up(mean[i])) * up(rstd[i]) * w.double()
+        z = hw + b.double()
+        want, _ = _slope(z, act)
+        t = 1.6 * z.abs() + 0.0714 * z.abs() ** 3 if act == "gelu_tanh" else z.abs()
+        tol = 1.13 * 3 * U * (hw.abs() + b.double().abs())
+        if act is not None:
+            tol = tol + want.abs() * (4 * U * t + 16 * U)
+        err = (y[i].double() - want).abs() / (tol * (1 + torch.finfo(y.dtype).eps) + _half(want, y.dtype))
+        assert err.max() <= 1, ("y", i, err.max().item())
+
+
+def _weights(c, seed):
+    gen = torch.Generator(DEV).manual_seed(seed)
+    return (1 + 0.2 * torch.randn(c, generator=gen, device=DEV),
+            0.2 * torch.randn(c, generator=gen, device=DEV))
+
+
+# Short and long slabs, in two launches and in one by clusters.
+OUTLIERS = [
+    ((2, 3000, 32, 4), "f32"), ((1, 600_000, 16, 2), "f32"), ((4, 131040, 24, 4), "f32"),
+    ((320, 16384, 16, 2), "f32"), ((1, 2_000_000, 8, 1), "f16"), ((6, 32760, 90, 6), "bf16"),
+]
+
+
+@pytest.mark.parametrize("where", ["first row", "eight rows", "last row"])
+@pytest.mark.parametrize("shape,fmt", OUTLIERS, ids=str)
+def test_statistics_beside_far_rows(shape, fmt, where):
+    """Rows 5000 standard deviations from all others, where a sum starts and
+    where it ends."""
+    n, s, c, g = shape
+    gen = torch.Generator(DEV).manual_seed(s)
+    x = torch.randn(n, s, c, generator=gen, device=DEV) + torch.randn(c, generator=gen, device=DEV)
+    rows = {"first row": slice(0, 1), "eight rows": slice(0, 8), "last row": slice(s - 1, s)}[where]
+    x[:, rows] = 5000.0
+    x = x.to(DT[fmt])
+    w, b = _weights(c, 1)
+    y, mean, rstd = wgs.group_norm_act(x, g, w, b, 1e-5, "silu")
+    wgs.check_error(DEV)
+    _check_statistics(x, mean, rstd, g, 1e-5, _depth(shape, fmt, False))
+    _check_output(x, y, w, b, mean, rstd, g, "silu")

@@ -312,14 +312,22 @@ struct Job {
     __device__ int32_t mine() const { return g < rows ? (rows - g + row_groups - 1) / row_groups : 0; }
 };
 
+// Rows of a thread after which run() calls between() first; then 8 times as many.
+constexpr int32_t kMove = 8;
+static_assert(kMove % kRowsFwd == 0 && kMove % kRowsBwd == 0, "between whole stages");
+
 // A slab's rows on their way through shared memory: kRows rows of every thread
 // a stage, kStages stages, f(chunk of each tensor, its byte offset) for each
-// of the thread's places in run().
+// of the thread's places in run(), and once the thread has had 8, 64, 512 ... rows
+// between(their number), where it hides behind copies under way.
 //
 // Rows of whole 16-byte chunks: one thread copies a stage's rows in bulk (TMA;
 // they are one piece of memory where the block walks whole rows), and an
 // mbarrier a stage tells that they have come, another that every warp has
 // read them.  A thread spends nothing on addresses and copies of its own.
+struct Nothing {
+    __device__ void operator()(int32_t) const {}
+};
 struct Bars {
     uint32_t full, empty;  // of stage 0; 8 bytes a stage
     int stages;
@@ -375,12 +383,13 @@ struct Bulk {
         if (job.tid == 0) {
             // what the block wrote to the slots comes before the copies
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            for (int i = 0; i < stages() - 1 && i < count; ++i)
-                copy(i, bars.stage + i < stages() ? bars.stage + i : bars.stage + i - stages());
+            for (int u = 0; u < stages() - 1 && u < count; ++u)
+                copy(u, bars.stage + u < stages() ? bars.stage + u : bars.stage + u - stages());
         }
     }
-    template <typename Use>
-    __device__ void run(Use f) {
+    template <typename Use, typename Between = Nothing>
+    __device__ void run(Use f, Between between = {}) {
+        int32_t move = kMove / kRows;
         const uint32_t stride = job.threads * C::kBytes;
         const int32_t step = static_cast<int32_t>(job.row_groups * row_bytes);
         int64_t at = base + job.g * row_bytes + job.j * C::kBytes;
@@ -391,6 +400,10 @@ struct Bulk {
                 const int free = bars.stage == 0 ? stages() - 1 : bars.stage - 1;
                 if (bars.used) wait(bars.empty + 8 * free, bars.stage == 0 ? bars.phase ^ 1 : bars.phase);
                 copy(i + stages() - 1, free);
+            }
+            if (i == move) {
+                between(i * kRows);
+                move *= 8;
             }
             wait(bars.full + 8 * bars.stage, bars.phase);
             const uint32_t slot = ring + bars.stage * stage_bytes() + job.tid * C::kBytes;
@@ -461,8 +474,15 @@ struct Own {
         for (int i = 0; i < kStages - 1; ++i)
             copy(slots + i * kRows * kTensors * stride, at + i * kRows * step, left - i * kRows);
     }
-    template <typename Use>
-    __device__ void run(Use f) {
+    template <typename Use, typename Between = Nothing>
+    __device__ void run(Use f, Between between = {}) {
+        const int32_t all = left;
+        int32_t move = kMove;
+        auto moves = [&] {
+            if (all - left != move) return;
+            between(move);
+            move = move < INT32_MAX / 8 ? 8 * move : INT32_MAX;
+        };
         if constexpr (kAsync) {
             const uint32_t stage = kRows * kTensors * stride;
             const int32_t lead = (kStages - 1) * kRows * step;
@@ -477,6 +497,7 @@ struct Own {
                 copy(free, at + lead, left - (kStages - 1) * kRows);
                 free = use;
                 use = use == slots + (kStages - 1) * stage ? slots : use + stage;
+                moves();
 #pragma unroll
                 for (int u = 0; u < kRows; ++u)
                     if (u < left) f(v[u], at + u * step);
@@ -491,6 +512,7 @@ struct Own {
                     if (u < left)
 #pragma unroll
                         for (int t = 0; t < kTensors; ++t) v[u][t] = C::load(src[t] + at + u * step);
+                moves();
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u)
                     if (u < left) f(v[u], at + u * step);
@@ -634,57 +656,113 @@ __device__ __forceinline__ void set_half(float2 *v, int e, float x) {
 }
 
 // Forward, pass 1 (reads x once; bound by DRAM): (mean, M2) of every group over
-// the rows of a cluster, M2
-// the sum of the squared distances from the mean.  A thread sums x - k and
-// its square, k the channel's value in the slab's first row.  With k one of
-// the values, the cancellation in M2 = sum d^2 - (sum d)^2 / n costs at most
-// a factor of the slab's rows in relative error, and that only where k is an
-// outlier, whatever the mean.  Where parts are joined the same is done with
-// the first part's mean as the reference.
+// the rows of a cluster, M2 the sum of the squared distances from the mean.  A
+// thread sums x - k and its square, k first the channel's value in its first
+// row and after 8, 64, 512 ... rows their mean: M2 = sum d^2 - (sum d)^2 / n then
+// cancels by a small factor at most, whatever the mean and wherever a row lies
+// far from all others.  (With one k for a slab such a row in its first place cost
+// a factor of the slab's rows: rstd off by 1e-3 after 4096.)  Threads' parts are
+// joined one by one, blocks' about the first one's mean.
 template <typename E, int kV>
 __device__ void stats_pass(const NormArgs &a, const Job &job, Bars &bars, float2 *smem) {
     using C = Chunk<E, kV>;
-    using One = Chunk<E, 1>;
     constexpr int kP = C::kPairs;
     float2 *ch = smem, *red = smem + a.channels;  // red holds the groups' results in the end
     float2 *ring = job.columns == a.chunks ? smem : red;
     const int64_t row_bytes = static_cast<int64_t>(a.chunks) * C::kBytes;
-    const float inv = job.rows > 0 ? 1.0f / static_cast<float>(job.rows) : 0.f;
     const int64_t origin = (job.sample * a.spatial + job.r0) * row_bytes;
-    auto first = [&](int c) {  // the channel's value in the slab's first row
-        return job.rows > 0 ? One::wide(One::load(a.x + origin + static_cast<int64_t>(c) * One::kBytes), 0).x : 0.f;
-    };
     for (int32_t c0 = 0; c0 < a.chunks; c0 += job.columns) {
-        const int32_t wide = min(job.columns, a.chunks - c0);
+        const int32_t wide = min(job.columns, a.chunks - c0), count = wide * kV;
         const int64_t o = origin + c0 * C::kBytes;
         // first the few values that the block starts with, before its copies
         // fill the way to memory
         typename C::Raw lead = {};
-        if (job.j < wide && job.rows > 0) lead = C::load(a.x + o + job.j * C::kBytes);
-        // the value that this thread will need where it ends its first channel
-        const float ahead = job.j < wide && job.g < kV ? first((c0 + job.j) * kV + job.g) : 0.f;
+        if (job.j < wide && job.g < job.rows) lead = C::load(a.x + o + job.g * row_bytes + job.j * C::kBytes);
         Stream<C, 1> in(job, bars);
         in.src[0] = a.x;
         in.start(ring, o, row_bytes, wide, false, l2_policy(false));
-        float2 k[kP], s1[kP], s2[kP];
+        // row groups that have rows, and their rows: one more in the first `more`
+        const int live = min(job.row_groups, job.rows), each = job.rows / job.row_groups;
+        const int more = job.rows - each * job.row_groups;
+        const float few = static_cast<float>(each);
+        auto rows_of = [&](int g) { return g < more ? few + 1.f : few; };
+        // Narrow rows have many row groups, which are joined in two steps, kShares
+        // shares of them side by side: [1, 2000000, 8] fp16 25 us, in one step 30.
+        constexpr int kShares = 8;
+        const bool narrow = live >= max(kShares * kV, 64);
+        auto rows_of_share = [&](int l) {
+            const int with = max(more - l + kShares - 1, 0) / kShares;
+            return fmaf(static_cast<float>((live - l + kShares - 1) / kShares), few, static_cast<float>(with));
+        };
+        const float inv = 1.0f / rows_of(job.g);
+        float2 k[kP], s1[kP], s2[kP];  // -k
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
             k[p] = C::wide(lead, p);
             k[p].x = -k[p].x, k[p].y = -k[p].y;
             s1[p] = s2[p] = both(0.f);
         }
-        in.run([&](const typename C::Raw (&v)[1], int64_t) {
+        in.run(
+            [&](const typename C::Raw (&v)[1], int64_t) {
+#pragma unroll
+                for (int p = 0; p < kP; ++p) {
+                    const float2 d = C::plus(v[0], p, k[p]);
+                    s1[p] = add2(s1[p], d);
+                    s2[p] = fma2(d, d, s2[p]);
+                }
+            },
+            [&](int32_t rows) {
+                // k moves by c: sum (d - c) = s1 - n c, sum (d - c)^2 = s2 - c (s1 + (s1 - n c))
+                const float n = static_cast<float>(rows);
+#pragma unroll
+                for (int p = 0; p < kP; ++p) {
+                    const float2 to = fma2(s1[p], both(-1.0f / n), k[p]);
+                    const float2 c = add2(k[p], make_float2(-to.x, -to.y));
+                    const float2 t = fma2(c, both(-n), s1[p]);
+                    s2[p] = fma2(make_float2(-c.x, -c.y), add2(s1[p], t), s2[p]);
+                    s1[p] = t, k[p] = to;
+                }
+            });
+        // the row groups: the threads' (mean, M2) by chunk element, so that
+        // neighbouring threads touch neighbouring words
+        __syncthreads();  // the slots that `red` lies over have been read
+        if (job.j < wide) {
+            float2 *to = red + job.g * count + job.j;
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
-                const float2 d = C::plus(v[0], p, k[p]);
-                s1[p] = add2(s1[p], d);
-                s2[p] = fma2(d, d, s2[p]);
+                const float2 m = job.g < live ? mul2(s1[p], both(inv)) : both(0.f);
+                const float2 m2 = fma2(make_float2(-m.x, -m.y), s1[p], s2[p]);
+                to[2 * p * wide] = make_float2(m.x - k[p].x, not_below_zero(m2.x));
+                if constexpr (kV > 1) to[(2 * p + 1) * wide] = make_float2(m.y - k[p].y, not_below_zero(m2.y));
             }
-        });
-        add_row_groups<kV>(red, job, c0, wide, s1, s2, [&](int e, int c, float2 t) {
-            const float m = t.x * inv;
-            ch[c] = make_float2((e == job.g ? ahead : first(c)) + m, not_below_zero(fmaf(-m, t.x, t.y)));
-        });
+        }
+        __syncthreads();
+        // joined one by one: of n rows and then m more, whose mean is d further on, the
+        // mean is d m / (n + m) further on, and M2 grows by theirs and d^2 n m / (n + m)
+        auto join = [&](const float2 *q, int first, int step, int end, auto rows) {
+            const float2 own = q[first * count];
+            float mean = 0.f, m2 = own.y, n = rows(first);
+#pragma unroll 4
+            for (int g = first + step; g < end; g += step) {
+                const float2 v = q[g * count];
+                const float m = rows(g), share = __fdividef(m, n + m), d = v.x - own.x - mean;
+                m2 += fmaf(d * d, n * share, v.y);
+                mean = fmaf(d, share, mean);
+                n += m;
+            }
+            return make_float2(own.x + mean, m2);
+        };
+        if (__builtin_expect(narrow, 0)) {
+            const int e = job.g % kV, l = job.g / kV;
+            float2 *q = red + e * wide + job.j;
+            if (job.j < wide && l < kShares) q[l * count] = join(q, l, kShares, live, rows_of);
+            __syncthreads();
+            if (job.j < wide && l == 0) ch[(c0 + job.j) * kV + e] = join(q, 0, 1, kShares, rows_of_share);
+        } else if (job.j < wide) {
+            for (int e = job.g; e < kV; e += job.row_groups)
+                ch[(c0 + job.j) * kV + e] = join(red + e * wide + job.j, 0, 1, live, rows_of);
+        }
+        __syncthreads();
     }
     wait_for_sums(a);  // nothing is written before
     float2 *out = a.groups_part + (job.sample * a.clusters + job.cl) * a.groups;
