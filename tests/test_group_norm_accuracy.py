@@ -1,5 +1,5 @@
-"""Group norm's statistics where sums lose most, against 64 bits with
-tolerances from the kernels' own depth.
+"""Group norm's statistics where sums lose most, and its gradients over large
+samples, against 64 bits with tolerances from the kernels' own depth.
 
 With u = 2^-24, and D the additions on a value's way: a thread's rows, the row
 groups of its block, a group's channels and the blocks' parts,
@@ -17,6 +17,9 @@ groups of its block, a group's channels and the blocks' parts,
 * y, from the mean and rstd that the kernel gave: z = h w + b is off by
   3u (|h w| + |b|), an activation's slope is at most 1.13, and its own
   evaluation costs |y| (4u |t| + 16u), t the sigmoid's argument.
+* the gradients, from the same: a slope is off by K = 5u max(|h w| + |b|) + 80u,
+  so a sum by (D u + K + 4u) of its terms' magnitudes, and grad_x by
+  (D u + K + 8u) of the magnitudes of its three.
 * rounding to the output's format adds half a step.
 """
 import math
@@ -129,3 +132,69 @@ def test_statistics_beside_far_rows(shape, fmt, where):
     wgs.check_error(DEV)
     _check_statistics(x, mean, rstd, g, 1e-5, _depth(shape, fmt, False))
     _check_output(x, y, w, b, mean, rstd, g, "silu")
+
+
+LARGE = [
+    ((1, 131040, 192, 32), "f16", "silu"), ((3, 65600, 192, 32), "f16", "silu"),
+    ((2, 131040, 192, 8), "bf16", "gelu_tanh"), ((33, 1000, 1001, 7), "bf16", "silu"),
+    ((2, 20000, 770, 1), "f32", "gelu_tanh"), ((5, 32760, 384, 32), "bf16", None),
+    ((3, 3000, 4096, 2048), "f32", "silu"), ((60, 700, 760, 95), "f16", "gelu_tanh"),
+    ((400, 1000, 64, 8), "f32", "silu"), ((1, 40000, 99, 3), "f16", "gelu_tanh"),
+]
+
+
+@pytest.mark.parametrize("shape,fmt,act", LARGE, ids=str)
+def test_large_samples_and_their_gradients(shape, fmt, act):
+    """A gradient that is correlated with x and has a mean, so that the means
+    over the groups and the weights' gradients are a large share of their
+    terms: their absence would show, which is asserted too."""
+    n, s, c, g = shape
+    dtype = DT[fmt]
+    gen = torch.Generator(DEV).manual_seed(c)
+    noise = torch.randn(n, s, c, generator=gen, device=DEV)
+    x = (noise * (0.5 + torch.rand(c, generator=gen, device=DEV))
+         + torch.randn(c, generator=gen, device=DEV)).to(dtype)
+    gy = (0.5 + 0.5 * noise + 0.5 * torch.randn(n, s, c, generator=gen, device=DEV)).to(dtype)
+    del noise
+    w, b = _weights(c, 2)
+    y, mean, rstd = wgs.group_norm_act(x, g, w, b, 1e-5, act)
+    gx, gw, gb = wgs.group_norm_act_bwd(gy, x, g, mean, rstd, w, b, act)
+    wgs.check_error(DEV)
+    _check_statistics(x, mean, rstd, g, 1e-5, _depth(shape, fmt, False))
+    _check_output(x, y, w, b, mean, rstd, g, act)
+
+    D = _depth(shape, fmt, True)
+    up = lambda v: v.repeat_interleave(c // g)
+    wd, bd = w.double(), b.double()
+    want_w, want_b, mag_w, mag_b = (torch.zeros(c, dtype=torch.float64, device=DEV) for _ in range(4))
+    zmax, rows = 0.0, []
+    for i in range(n):
+        r = rstd[i].double()
+        h = (x[i].double() - up(mean[i].double())) * up(r)
+        zmax = max(zmax, ((h * wd).abs().max() + bd.abs().max()).item())
+        gyd = gy[i].double()
+        dz = gyd * _slope(h * wd + bd, act)[1]
+        want_w += (dz * h).sum(0)
+        want_b += dz.sum(0)
+        mag_w += (gyd * h).abs().sum(0)
+        mag_b += gyd.abs().sum(0)
+        d, size, hg = (v.view(s, g, -1) for v in (dz * wd, (gyd * wd).abs(), h))
+        means = d.mean((0, 2))[:, None] + hg * (d * hg).mean((0, 2))[:, None]
+        want = (r[:, None] * (d - means)).view(s, c)
+        means = (r[:, None] * means).view(s, c)
+        mag = (r[:, None] * (size + size.mean((0, 2))[:, None]
+                             + hg.abs() * (size * hg.abs()).mean((0, 2))[:, None])).view(s, c)
+        K = 5 * U * zmax + 80 * U
+        tol = mag * (D * U + K + 8 * U) * (1 + torch.finfo(dtype).eps) + _half(want, dtype)
+        err = (gx[i].double() - want).abs() / tol
+        assert err.max() <= 1, ("grad_x", i, err.max().item())
+        # a zero, or a grad_x without the group's means, would be outside
+        rows.append(((want.abs() > 4 * tol).double().mean().item(),
+                     (means.abs() > 4 * tol).double().mean().item()))
+    assert min(min(v) for v in rows) > 0.5, rows
+    K = 5 * U * zmax + 80 * U
+    for got, want, mag in ((gw, want_w, mag_w), (gb, want_b, mag_b)):
+        tol = mag * (D + n + K / U + 4) * U + U * want.abs()
+        err = (got.double() - want).abs() / tol
+        assert err.max() <= 1, err.max().item()
+        assert (want.abs() > 4 * tol).double().mean() > 0.9
