@@ -380,7 +380,9 @@ wgs_status position_bias(const void *table, const int32_t *bucket, void *bias, i
  * the bias unchanged, so with grad the gradient of the logits
  *     grad_table[t,b,h] = fp(sum of grad[w,h,p] over the windows w with
  *                            win_type[w] == t and pairs p with bucket[p] == b)
- * summed in FP32 in an order that depends on the sizes and the map alone.
+ * summed in FP32 in an order that depends on the sizes and the map alone: windows
+ * of a type in runs of at most 128, the runs, a bucket's pairs in 32s, and those
+ * sums, so that rounding errors grow with the longest of these, not with all.
  *   grad      [n_win, heads, n_pairs] of dtype (any wgs_dtype).
  *   plan      device copy of the bucket map's plan (wgs_build_bucket_plan),
  *             16-byte aligned, with its n_slots.  A plan of other sizes than
