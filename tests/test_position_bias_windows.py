@@ -10,6 +10,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import window_gather_swin_gb300 as wgs
 
 DEV = "cuda:0"
@@ -30,6 +31,35 @@ def _depth(plan, n_win, heads, n_types):
     slabs = wgs.position_bias_bwd_workspace_bytes(plan, n_win, heads, n_types) // (
         4 * n_types * heads * plan.n_slots)
     return 256 + n_win / 64 + _slots(plan) * slabs, slabs
+
+
+@pytest.mark.parametrize("fmt", ["f32", "f16"])
+@pytest.mark.parametrize("n_win", [1024, 1025, 1100, 2049])
+@pytest.mark.parametrize("order", ["mixed", "runs", "halves"])
+def test_types_of_more_windows_than_a_list_holds(n_win, order, fmt):
+    """One slab of more windows than are looked over at a time: types without
+    a window in a piece, in the last piece, or in any."""
+    heads, n_types = 6, 50
+    bucket = wgs.build_window_buckets((1, 7, 7))
+    plan = wgs.build_bucket_plan(bucket, 169, device=DEV)
+    gen = torch.Generator().manual_seed(n_win)
+    if order == "runs":
+        types = torch.arange(n_win) * n_types // n_win
+    else:
+        types = torch.randint(0, n_types, (n_win,), generator=gen)
+        types[types == 7] = 8                       # none of type 7 ...
+        if order == "halves":
+            types[:1024] -= types[:1024] % 2        # ... and odd ones behind the first piece alone
+    types = types.int()
+    grad = (0.25 + torch.randn(n_win, heads, 49, 49, generator=gen)).to(DT[fmt])
+    D, slabs = _depth(plan, n_win, heads, n_types)
+    assert slabs == 1
+    got = wgs.position_bias_bwd(grad.to(DEV), plan, types.to(DEV), n_types)
+    wgs.check_error(DEV)
+    want, mag = oracle.position_bias_bwd(grad.numpy(), bucket.numpy(), types.numpy(), n_types, 169, fmt)
+    err = np.abs(got.cpu().double().numpy() - want)
+    assert (err <= (D + 1) * U * mag).all(), (err / np.maximum(mag * D * U, 1e-300)).max()
+    assert order == "runs" or not got[7].any()
 
 
 MANY = [  # map, buckets, heads, types (all windows have one), windows; units of one slab fill the GPU
