@@ -120,3 +120,39 @@ def test_long_sums_elsewhere_in_memory_give_the_same_bits(shape, fmt):
         D, _ = _depth(plan, n_win, heads, 300)
         assert ((a[:3].double() - want).abs() <= D * U * size).all()
     wgs.check_error(DEV)
+
+
+def test_inputs_written_right_before_the_call():
+    """The plan, the types, the gradient and the table written in place by the
+    kernels and copies just before, again and again with other values: no
+    launch of a call may read what was there earlier."""
+    for n_q, n_k, heads, n_win, n_types in ((49, 49, 3, 200, 2), (12, 12, 4, 300, 3), (300, 300, 2, 2, 1),
+                                            (128, 128, 2, 40, 3)):
+        gen = torch.Generator().manual_seed(n_q)
+        n_buckets = 64
+        # the same pairs in other buckets: plans of one size
+        base = wgs.build_distance_buckets(n_q, n_k, n_buckets, 200)
+        maps = [((base.long() + 5 * k) % n_buckets).int() for k in range(4)]
+        plans = [wgs.build_bucket_plan(m, n_buckets, device=DEV) for m in maps]
+        assert len({p.n_slots for p in plans}) == 1
+        srcs = [(p.words, m.to(DEV), torch.randn(n_win, heads, n_q, n_k, generator=gen).half().to(DEV),
+                 torch.randint(0, n_types, (n_win,), generator=gen).int().to(DEV),
+                 torch.randn(n_types, n_buckets, heads, generator=gen).to(DEV)) for p, m in zip(plans, maps)]
+        now = [t.clone() for t in srcs[0]]
+        plan = wgs.BucketPlan(now[0], plans[0].shape, n_buckets, plans[0].n_slots)
+        torch.cuda.synchronize()
+        got = []
+        for _ in range(5):
+            for src in srcs:
+                for to, t in zip(now, src):
+                    to.copy_(t)
+                got.append((wgs.position_bias_bwd(now[2], plan, now[3], n_types),
+                            wgs.position_bias(now[4], now[1], torch.float16)))
+        torch.cuda.synchronize()
+        for k, src in enumerate(srcs):
+            want = (wgs.position_bias_bwd(src[2], plans[k], src[3], n_types),
+                    wgs.position_bias(src[4], src[1], torch.float16))
+            torch.cuda.synchronize()
+            for r in range(5):
+                assert all(torch.equal(p, q) for p, q in zip(got[4 * r + k], want)), (n_q, k, r)
+        wgs.check_error(DEV)

@@ -320,14 +320,15 @@ struct GradArgs {
     int64_t n_pairs;
     int32_t n_win, heads, n_types, n_buckets, n_tiles, n_slots, slabs;
     int32_t units;            // n_tiles * n_types * slabs * heads
-    bool follows;             // pass 2: pass 1 of the call is the launch before
+    bool early;               // pass 2: pass 1 of the call is the launch before, see start_table
 };
 
 // The plan's header against the sizes of the call (a plan of another map
 // would name other places).
-__device__ __forceinline__ bool plan_matches(const GradArgs &a) {
-    return a.plan[0] == kPlanMagic && a.plan[1] == a.n_pairs && a.plan[2] == a.n_buckets &&
-           a.plan[3] == a.n_tiles && a.plan[4] == a.n_slots;
+__device__ __forceinline__ bool plan_matches(const GradArgs &a, bool early = false) {  // early: see start_table
+    const int4 *head = reinterpret_cast<const int4 *>(a.plan);
+    const int4 v = early ? __ldcg(head) : __ldg(head), w = early ? __ldcg(head + 1) : __ldg(head + 1);
+    return v.x == kPlanMagic && v.y == a.n_pairs && v.z == a.n_buckets && v.w == a.n_tiles && w.x == a.n_slots;
 }
 
 // The first of `count` things of the i-th of `parts` equal shares.
@@ -902,31 +903,45 @@ __global__ void __launch_bounds__(kSmallThreads, 2) bias_grad_small(GradArgs a, 
 
 // Pass 2 after pass 1: all that came before on the stream is done when it starts
 // (pass 1 has waited for it), so the plan may be read at once; the sums are there
-// after wait_for_slots.  On its own it waits first.  (1 to 2 us of a call: 49 x 49
-// pairs of 12 heads, 1024 windows 18.1 us on the device, 20.1 waiting first.)
+// after wait_for_slots.  What is read before that comes from L2, as everywhere in
+// the library: L1 may hold an older line.  A large grid waits first, see
+// kEarlyBlocks.  (1 to 2 us of a call: 1024 x 1024 pairs of 8 heads, 2 windows 17.2 us
+// on the device, 18.1 waiting first.)
 __device__ __forceinline__ void start_table(const GradArgs &a) {
 #if WGS_PDL
-    if (!a.follows) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #endif
 }
 __device__ __forceinline__ void wait_for_slots(const GradArgs &a) {
 #if WGS_PDL
-    if (a.follows) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
 #endif
 }
 
+// A word of the plan, from L2 or through L1.
+__device__ __forceinline__ int32_t plan_word(const GradArgs &a, int64_t i, bool l2) {
+    return l2 ? __ldcg(a.plan + i) : __ldg(a.plan + i);
+}
+
+// The places of bucket b in the buckets' lists of slots, [x, y).
+__device__ __forceinline__ int2 places_of(const GradArgs &a, int32_t b) {
+    return make_int2(max(plan_word(a, a.at.bucket_first + b, a.early), 0),
+                     min(plan_word(a, a.at.bucket_first + b + 1, a.early), a.n_slots));
+}
+
 // The d-th slot of the buckets' lists.
+template <bool kL2>
 __device__ __forceinline__ int32_t slot_of(const GradArgs &a, int32_t d) {
-    return min(max(__ldg(a.plan + a.at.bucket_slot + d), 0), a.n_slots - 1);
+    return min(max(plan_word(a, a.at.bucket_slot + d, kL2), 0), a.n_slots - 1);
 }
 
 // The sum of a bucket's values of one (type, head), n slots from d0 on in every
 // slab: those of lane `lane` of `lanes`, of the slabs one after another.
 __device__ __forceinline__ float add_bucket(const GradArgs &a, int32_t type, int32_t b, int32_t head, int32_t lane,
                                             int32_t lanes) {
-    const int32_t d0 = max(__ldg(a.plan + a.at.bucket_first + b), 0);
-    const int32_t n = min(__ldg(a.plan + a.at.bucket_first + b + 1), a.n_slots) - d0;
+    const int2 places = places_of(a, b);
+    const int32_t d0 = places.x, n = places.y - d0;
     if (n <= 0) {
         wait_for_slots(a);
         return 0.f;
@@ -937,23 +952,23 @@ __device__ __forceinline__ float add_bucket(const GradArgs &a, int32_t type, int
     int32_t s = lane / n, d = lane - s * n;
     float sum = 0.f;
     constexpr int kAhead = 8;  // loads in flight
-    bool first = true;
-    do {
+    auto batch = [&](auto early) {
         const float *q[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            q[k] = s < a.slabs ? p + s * step + slot_of(a, d0 + d) : nullptr;
+            q[k] = s < a.slabs ? p + s * step + slot_of<decltype(early)::value>(a, d0 + d) : nullptr;
             s += by_slabs, d += by_slots;
             if (d >= n) d -= n, ++s;
         }
-        if (first) wait_for_slots(a);
-        first = false;
+        if (decltype(early)::value) wait_for_slots(a);
         float v[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) v[k] = q[k] ? __ldcg(q[k]) : 0.f;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) sum += v[k];
-    } while (s < a.slabs);
+    };
+    if (a.early) batch(std::true_type{});
+    while (s < a.slabs) batch(std::false_type{});
     return sum;
 }
 
@@ -963,7 +978,7 @@ __device__ __forceinline__ float add_bucket(const GradArgs &a, int32_t type, int
 template <typename T, int LANES>
 __global__ void __launch_bounds__(kThreads) bias_grad_table(GradArgs a, int32_t blocks) {
     start_table(a);
-    const bool ok = plan_matches(a);
+    const bool ok = plan_matches(a, a.early);
     if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_bucket_error, 1u);
     const int32_t type = blockIdx.x / blocks;
     const int32_t i = ((blockIdx.x - type * blocks) * kThreads + static_cast<int32_t>(threadIdx.x)) / LANES;
@@ -987,35 +1002,48 @@ constexpr int kBlockThreads = 1024;
 template <typename T>
 __global__ void __launch_bounds__(kBlockThreads) bias_grad_block(GradArgs a) {
     __shared__ float part[kBlockThreads / 32];
+    __shared__ int32_t known[3];  // the bucket's places and whether the plan is the call's
     start_table(a);
-    const bool ok = plan_matches(a);
-    if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_bucket_error, 1u);
     const int32_t head = blockIdx.x % a.heads, tb = blockIdx.x / a.heads;
     const int32_t type = tb / a.n_buckets, b = tb - type * a.n_buckets;
-    float v = 0.f;
-    bool waited = false;
-    if (ok) {
-        const int32_t d0 = max(__ldg(a.plan + a.at.bucket_first + b), 0);
-        const int32_t d1 = min(__ldg(a.plan + a.at.bucket_first + b + 1), a.n_slots);
-        const int64_t step = static_cast<int64_t>(a.n_types) * a.heads * a.n_slots;
-        const float *p = a.partial + (static_cast<int64_t>(type) * a.heads + head) * a.n_slots;
-        constexpr int kAhead = 16;  // loads in flight
-        for (int32_t s = 0; s < a.slabs; ++s, p += step)
-            for (int32_t d = d0 + static_cast<int32_t>(threadIdx.x); d < d1; d += kAhead * kBlockThreads) {
-                int32_t slot[kAhead];
-                float q[kAhead];
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    slot[k] = d1 - d > k * kBlockThreads ? slot_of(a, d + k * kBlockThreads) : -1;
-                if (!waited) wait_for_slots(a);
-                waited = true;
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) q[k] = slot[k] >= 0 ? __ldcg(p + slot[k]) : 0.f;
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) v += q[k];
-            }
+    bool ok;
+    int2 places;
+    auto look = [&] {
+        ok = plan_matches(a, a.early);
+        places = ok ? places_of(a, b) : make_int2(0, 0);
+    };
+    if (a.early) {  // by one thread: L2 would take these words thousands of times
+        if (threadIdx.x == 0) {
+            look();
+            known[0] = places.x, known[1] = places.y, known[2] = ok;
+        }
+        __syncthreads();
+        places = make_int2(known[0], known[1]), ok = known[2];
+    } else {
+        look();
     }
-    if (!waited) wait_for_slots(a);
+    if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_bucket_error, 1u);
+    float v = 0.f;
+    const int32_t first = places.x + static_cast<int32_t>(threadIdx.x), d1 = places.y;  // (none without a plan)
+    const int64_t step = static_cast<int64_t>(a.n_types) * a.heads * a.n_slots;
+    const float *p = a.partial + (static_cast<int64_t>(type) * a.heads + head) * a.n_slots;
+    constexpr int kAhead = 16, kStep = kAhead * kBlockThreads;  // loads in flight
+    auto batch = [&](int32_t d, auto early) {
+        int32_t slot[kAhead];
+        float q[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            slot[k] = d1 - d > k * kBlockThreads ? slot_of<decltype(early)::value>(a, d + k * kBlockThreads) : -1;
+        if (decltype(early)::value) wait_for_slots(a);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) q[k] = slot[k] >= 0 ? __ldcg(p + slot[k]) : 0.f;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) v += q[k];
+    };
+    int32_t d = first;
+    if (a.early) batch(d, std::true_type{}), d += kStep;
+    for (int32_t s = 0; s < a.slabs; ++s, p += step, d = first)
+        for (; d < d1; d += kStep) batch(d, std::false_type{});
     v = group_sum<32>(v);
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
@@ -1030,14 +1058,14 @@ __global__ void __launch_bounds__(kBlockThreads) bias_grad_block(GradArgs a) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) bias_grad_rows(GradArgs a, int32_t blocks) {
     start_table(a);
-    const bool ok = plan_matches(a);
+    const bool ok = plan_matches(a, a.early);
     if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_bucket_error, 1u);
     const int32_t type = blockIdx.x / blocks;
     const int32_t b = (blockIdx.x - type * blocks) * kThreads + static_cast<int32_t>(threadIdx.x);
     const bool mine = ok && b < a.n_buckets;
-    const int32_t d0 = mine ? max(__ldg(a.plan + a.at.bucket_first + b), 0) : 0;
-    const int32_t d1 = mine ? min(__ldg(a.plan + a.at.bucket_first + b + 1), a.n_slots) : 0;
-    const int32_t slot0 = d0 < d1 ? slot_of(a, d0) : 0;
+    const int2 places = mine ? places_of(a, b) : make_int2(0, 0);
+    const int32_t d0 = places.x, d1 = places.y;
+    const int32_t slot0 = d0 < d1 ? (a.early ? slot_of<true>(a, d0) : slot_of<false>(a, d0)) : 0;
     wait_for_slots(a);
     if (b >= a.n_buckets) return;
     const int64_t step = static_cast<int64_t>(a.n_types) * a.heads * a.n_slots;
@@ -1049,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads) bias_grad_rows(GradArgs a, int32_t b
 #pragma unroll
         for (int k = 0; k < kHeads; ++k) v[k] = 0.f;
         for (int32_t d = d0; d < d1; ++d) {
-            const float *q = p + static_cast<int64_t>(h0) * a.n_slots + (d == d0 ? slot0 : slot_of(a, d));
+            const float *q = p + static_cast<int64_t>(h0) * a.n_slots + (d == d0 ? slot0 : slot_of<false>(a, d));
             for (int32_t s = 0; s < a.slabs; ++s, q += step) {
                 float t[kHeads];
 #pragma unroll
@@ -1148,23 +1176,32 @@ wgs_status launch_tiles_any(const GradArgs &a, cudaStream_t stream) {
                                                     : launch_tiles<E, false>(a, stream);
 }
 
+// Blocks of pass 2 with which it starts early, of kThreads and of kBlockThreads.
+// Later ones have nothing to hide, and miss what L1 holds: 16 types of 32 buckets and
+// 32 heads, 16,384 blocks, 159 us, starting early 238; 512 blocks 69.7, waiting 71.3.
+constexpr int64_t kEarlyBlocks = 8 * 152, kEarlyLarge = 4 * 152;
+
 template <typename T>
-wgs_status launch_table(const GradArgs &a, cudaStream_t stream) {
+wgs_status launch_table(GradArgs a, cudaStream_t stream) {
     const int64_t outputs = static_cast<int64_t>(a.n_types) * a.n_buckets * a.heads;
     const int64_t mean = static_cast<int64_t>(a.n_slots) * a.slabs / a.n_buckets;  // values of a bucket
     if (mean < 4 && outputs >= 32 * kThreads * a.heads) {
         const int64_t blocks = ceil_div(a.n_buckets, kThreads);
         if (blocks * a.n_types > INT32_MAX) return WGS_ERR_SHAPE;
+        a.early = a.early && blocks * a.n_types <= kEarlyBlocks;
         return launch(bias_grad_rows<T>, dim3(static_cast<unsigned>(blocks * a.n_types)), dim3(kThreads), 0,
                       stream, a, static_cast<int32_t>(blocks));
     }
-    if (a.n_slots / a.n_buckets >= 64 && outputs <= INT32_MAX)
+    if (a.n_slots / a.n_buckets >= 64 && outputs <= INT32_MAX) {
+        a.early = a.early && outputs <= kEarlyLarge;
         return launch(bias_grad_block<T>, dim3(static_cast<unsigned>(outputs)), dim3(kBlockThreads), 0, stream, a);
+    }
     // more lanes where outputs are few: a bucket can hold many times the mean (32
     // buckets of 2047 pairs in 77 slots, 32 heads: 5 us, a lane each 30)
     const int lanes = mean >= 64 || outputs <= 8192 ? 32 : mean >= 8 || outputs <= 32768 ? 8 : 1;
     const int64_t blocks = ceil_div(static_cast<int64_t>(a.heads) * a.n_buckets * lanes, kThreads);
     if (blocks * a.n_types > INT32_MAX) return WGS_ERR_SHAPE;
+    a.early = a.early && blocks * a.n_types <= kEarlyBlocks;
     auto kernel = lanes == 1 ? bias_grad_table<T, 1> : lanes == 8 ? bias_grad_table<T, 8> : bias_grad_table<T, 32>;
     return launch(kernel, dim3(static_cast<unsigned>(blocks * a.n_types)), dim3(kThreads), 0, stream, a,
                   static_cast<int32_t>(blocks));
