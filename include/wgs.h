@@ -576,8 +576,9 @@ wgs_status wgs_build_shift_regions(const int32_t grid[3], const int32_t window[3
  * [0, n_windowed), or any window_bias_mask_add a window type outside
  * [0, n_types), or a position-bias call a bucket, window type or plan out of
  * its range; WGS_ERR_LAUNCH if a kernel since then gave up waiting for its own
- * copies to arrive (its outputs are not to be used); WGS_OK otherwise.  The
- * words are shared by every stream of the device. */
+ * copies to arrive (its outputs are not to be used), and then WGS_ERR_INDEX from
+ * the next check if there was a bad index too; WGS_OK otherwise.  The words are
+ * shared by every stream of the device. */
 wgs_status wgs_check_error(cudaStream_t stream);
 
 #ifdef __cplusplus

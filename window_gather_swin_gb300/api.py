@@ -654,9 +654,13 @@ def build_shift_regions(grid: Sequence[int], window: Sequence[int], shift: Seque
 
 
 def check_error(device=None) -> None:
-    """Raise if any gather on `device` met an index outside [-1, n_src), or
-    any bias-mask add a window type outside [0, n_types), or any position-bias
-    call a bucket, window type or plan out of its range, since the last check.  Synchronises that device's current stream."""
+    """Raise WgsError (WGS_ERR_INDEX) if any gather on `device` met an index
+    outside [-1, n_src), or any bias-mask add a window type outside
+    [0, n_types), or any position-bias call a bucket, window type or plan out
+    of its range, since the last check; WGS_ERR_LAUNCH if a kernel gave up
+    waiting for its own copies, whose outputs are not to be used (a bad index
+    seen too is raised by the next check).  Synchronises that device's current
+    stream."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(dev):
         _capi.check("wgs_check_error", _capi.load().wgs_check_error(_stream_ptr(dev)))

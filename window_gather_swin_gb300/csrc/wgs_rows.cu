@@ -587,7 +587,7 @@ extern "C" wgs_status wgs_check_error(cudaStream_t stream) {
     // The error words are read and cleared by symbol, so each copy resolves
     // the word in the context current at this call.
     unsigned int seen = 0, seen_mask = 0, seen_bucket = 0, seen_norm = 0;
-    static const unsigned int cleared = 0;
+    static const unsigned int cleared = 0, set = 1;
     if (cudaMemcpyFromSymbolAsync(&seen, g_index_error, sizeof(seen), 0, cudaMemcpyDeviceToHost,
                                   stream) != cudaSuccess ||
         cudaMemcpyToSymbolAsync(g_index_error, &cleared, sizeof(cleared), 0,
@@ -603,6 +603,13 @@ extern "C" wgs_status wgs_check_error(cudaStream_t stream) {
         cudaGetLastError();
         return WGS_ERR_CUDA;
     }
-    if (seen_norm || (seen_bucket & 2u)) return WGS_ERR_LAUNCH;
-    return (seen | seen_mask | seen_bucket) ? WGS_ERR_INDEX : WGS_OK;
+    const bool bad_index = seen || seen_mask || (seen_bucket & 1u);
+    if (!seen_norm && !(seen_bucket & 2u)) return bad_index ? WGS_ERR_INDEX : WGS_OK;
+    // one status a check: the bad index is left for the next
+    if (bad_index && cudaMemcpyToSymbolAsync(g_index_error, &set, sizeof(set), 0, cudaMemcpyHostToDevice,
+                                             stream) != cudaSuccess) {
+        cudaGetLastError();
+        return WGS_ERR_CUDA;
+    }
+    return WGS_ERR_LAUNCH;
 }
