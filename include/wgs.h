@@ -398,7 +398,7 @@ wgs_status position_bias(const void *table, const int32_t *bucket, void *bias, i
  *   workspace at least wgs_position_bias_bwd_workspace_bytes(...) bytes,
  *             16-byte aligned, disjoint from the tensors; its contents on
  *             entry do not matter.  Calls that overlap on the GPU need
- *             workspaces of their own. */
+ *             workspaces of their own.  (0 bytes for sizes that the call refuses.) */
 size_t wgs_position_bias_bwd_workspace_bytes(int64_t n_win, int32_t heads, int32_t n_types,
                                              int64_t n_pairs, int64_t n_slots);
 wgs_status position_bias_bwd(const void *grad, const int32_t *plan, const int32_t *win_type,

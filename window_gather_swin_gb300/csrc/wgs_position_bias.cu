@@ -1185,7 +1185,7 @@ template <typename T>
 wgs_status launch_table(GradArgs a, cudaStream_t stream) {
     const int64_t outputs = static_cast<int64_t>(a.n_types) * a.n_buckets * a.heads;
     const int64_t mean = static_cast<int64_t>(a.n_slots) * a.slabs / a.n_buckets;  // values of a bucket
-    if (mean < 4 && outputs >= 32 * kThreads * a.heads) {
+    if (mean < 4 && outputs >= int64_t{32} * kThreads * a.heads) {
         const int64_t blocks = ceil_div(a.n_buckets, kThreads);
         if (blocks * a.n_types > INT32_MAX) return WGS_ERR_SHAPE;
         a.early = a.early && blocks * a.n_types <= kEarlyBlocks;
@@ -1212,6 +1212,20 @@ bool times(int64_t a, int64_t b, int64_t *out) {
     if (b > 0 && a > (int64_t{1} << 62) / b) return false;
     *out = a * b;
     return true;
+}
+
+// Slabs, units and bytes of workspace of a gradient call, sizes not negative;
+// false where they pass what its kernels can count.
+bool grad_sizes(int64_t n_win, int64_t heads, int64_t n_types, int64_t n_pairs, int64_t n_slots, int64_t *slabs,
+                int64_t *units, int64_t *part_bytes) {
+    // (the kernels step past the last window by at most 65536)
+    if (n_pairs > INT32_MAX - kPlanTile || n_slots > n_pairs || n_win > INT32_MAX - 65536) return false;
+    const int64_t n_tiles = ceil_tiles(n_pairs);
+    int64_t th;
+    if (!times(n_types, heads, &th) || !times(th, n_tiles, units) || *units > INT32_MAX) return false;
+    *slabs = slabs_of(n_win, heads, n_types, n_pairs);
+    *units *= *slabs;
+    return *units <= INT32_MAX && times(th, *slabs, &th) && times(th, n_slots * 4, part_bytes);
 }
 
 bool dtype_ok(wgs_dtype d) { return d == WGS_F32 || d == WGS_F16 || d == WGS_BF16; }
@@ -1259,9 +1273,11 @@ extern "C" wgs_status position_bias(const void *table, const int32_t *bucket, vo
 extern "C" size_t wgs_position_bias_bwd_workspace_bytes(int64_t n_win, int32_t heads,
                                                         int32_t n_types, int64_t n_pairs,
                                                         int64_t n_slots) {
-    if (n_win < 0 || heads < 1 || n_types < 1 || n_pairs < 0 || n_slots < 0) return 0;
-    return static_cast<size_t>(slabs_of(n_win, heads, n_types, n_pairs)) * n_types *
-           heads * static_cast<size_t>(n_slots) * sizeof(float);
+    int64_t slabs, units, part_bytes;
+    if (n_win < 0 || heads < 1 || n_types < 1 || n_pairs < 0 || n_slots < 0 ||
+        !grad_sizes(n_win, heads, n_types, n_pairs, n_slots, &slabs, &units, &part_bytes))
+        return 0;
+    return static_cast<size_t>(part_bytes);
 }
 
 extern "C" wgs_status position_bias_bwd(const void *grad, const int32_t *plan,
@@ -1275,17 +1291,12 @@ extern "C" wgs_status position_bias_bwd(const void *grad, const int32_t *plan,
     if (n_win < 0 || heads < 0 || n_pairs < 0 || n_buckets < 0 || n_types < 0 || n_slots < 0)
         return WGS_ERR_SHAPE;
     if (n_types == 0 || heads == 0 || n_buckets == 0) return WGS_OK;
-    // (the kernels step past the last window by less than 65536)
-    if (n_pairs > INT32_MAX - kPlanTile || n_slots > n_pairs || n_win > INT32_MAX - 65536)
-        return WGS_ERR_SHAPE;
     const int64_t n_tiles = ceil_tiles(n_pairs);
-    const int64_t slabs = slabs_of(n_win, heads, n_types, n_pairs);
-    int64_t th, units, grad_bytes, table_bytes, part_bytes;
-    if (!times(n_types, heads, &th) || !times(heads, n_buckets, &units) || units > INT32_MAX / 32 ||
-        !times(th * slabs, n_tiles, &units) || units > INT32_MAX ||
+    int64_t slabs, units, grad_bytes, table_bytes, part_bytes;
+    if (static_cast<int64_t>(heads) * n_buckets > INT32_MAX / 32 ||
+        !grad_sizes(n_win, heads, n_types, n_pairs, n_slots, &slabs, &units, &part_bytes) ||
         !times(n_win * heads, n_pairs * bytes_of(dtype), &grad_bytes) ||
-        !times(th, n_buckets * bytes_of(table_dtype), &table_bytes) ||
-        !times(th * slabs, n_slots * 4, &part_bytes))
+        !times(static_cast<int64_t>(n_types) * heads, n_buckets * bytes_of(table_dtype), &table_bytes))
         return WGS_ERR_SHAPE;
     if (!plan || !grad_table || (grad_bytes > 0 && !grad) || (part_bytes > 0 && !workspace))
         return WGS_ERR_NULL;
