@@ -304,6 +304,21 @@ def _fail(msg: str) -> None:
     raise RuntimeError(msg)
 
 
+_MAX32, _MAX64 = 2 ** 31 - 1, 2 ** 63 - 1
+
+
+def _int32(v, name: str, most: int = _MAX32) -> int:
+    """v as the C ABI takes it: ctypes would cut a larger one silently."""
+    v = int(v)
+    if not -most - 1 <= v <= most:
+        _fail(f"{name} must be at most {most} (got {v})")
+    return v
+
+
+def _int64(v, name: str) -> int:
+    return _int32(v, name, _MAX64)
+
+
 def _given(t: torch.Tensor, name: str, dtype, index: int) -> int:
     """Device address of t (0 when empty), a contiguous tensor of `dtype` on
     CUDA device `index`; raises otherwise."""
@@ -342,7 +357,8 @@ def _run(name: str, fn, index: int, *args) -> None:
 
 def window_bucket_count(window: Sequence[int], absolute_axes: int = 0) -> int:
     """Buckets of build_window_buckets: the rows of the learned table."""
-    n = _capi.load().wgs_window_bucket_count(_i3(window, "window"), int(absolute_axes))
+    n = _capi.load().wgs_window_bucket_count(_i3(window, "window"),
+                                             _int32(absolute_axes, "absolute_axes"))
     _require(n >= 0, "invalid window extents or absolute_axes")
     return int(n)
 
@@ -368,10 +384,11 @@ def build_distance_buckets(n_q: int, n_k: int, n_buckets: int, max_distance: int
     Query i stands at position q_start + i; without `bidirectional` keys ahead
     of their query have no bucket (-1)."""
     _require(n_q >= 0 and n_k >= 0, "n_q and n_k must not be negative")
+    numbers = (_int64(q_start, "q_start"), _int32(n_buckets, "n_buckets"),
+               _int32(max_distance, "max_distance"))
     out = torch.empty(n_q, n_k, dtype=torch.int32)
     _capi.check("wgs_build_distance_buckets", _capi.load().wgs_build_distance_buckets(
-        n_q, n_k, int(q_start), int(n_buckets), int(max_distance), int(bool(bidirectional)),
-        ctypes.c_void_p(out.data_ptr()), n_q * n_k))
+        n_q, n_k, *numbers, int(bool(bidirectional)), ctypes.c_void_p(out.data_ptr()), n_q * n_k))
     return out if device is None else out.to(device)
 
 
@@ -392,6 +409,8 @@ def position_bias(table: torch.Tensor, bucket: torch.Tensor, dtype=None,
         _fail("bucket must be [n_q, n_k]")
     n_types = dims[0] if len(dims) == 3 else 1
     n_buckets, heads = dims[-2:]
+    if max(n_types, n_buckets, heads) > _MAX32:
+        _fail(f"n_types, n_buckets and heads must be at most {_MAX32} (got {tuple(dims)})")
     if dtype is None:
         dtype = table.dtype if out is None else out.dtype
     if dtype not in _DTYPE:
@@ -424,24 +443,26 @@ def build_bucket_plan(bucket: torch.Tensor, n_buckets: int, device="cuda") -> Bu
     [n_q, n_k] with values in [-1, n_buckets) (host-built, once per map)."""
     _require(isinstance(bucket, torch.Tensor) and bucket.dtype == torch.int32 and bucket.dim() == 2,
              "bucket must be an int32 tensor [n_q, n_k]")
+    n_buckets = _int32(n_buckets, "n_buckets")
     host = bucket.cpu().contiguous()
     lib = _capi.load()
     slots = ctypes.c_int64()
-    n = lib.wgs_bucket_plan_words(ctypes.c_void_p(host.data_ptr()), host.numel(), int(n_buckets),
+    n = lib.wgs_bucket_plan_words(ctypes.c_void_p(host.data_ptr()), host.numel(), n_buckets,
                                   ctypes.byref(slots))
     _require(n >= 0, f"bucket values must lie in [-1, {n_buckets}) and n_buckets be positive")
     words = torch.empty(n, dtype=torch.int32)
     _capi.check("wgs_build_bucket_plan", lib.wgs_build_bucket_plan(
-        ctypes.c_void_p(host.data_ptr()), host.numel(), int(n_buckets),
+        ctypes.c_void_p(host.data_ptr()), host.numel(), n_buckets,
         ctypes.c_void_p(words.data_ptr()), n))
-    return BucketPlan(words.to(device), tuple(host.shape), int(n_buckets), int(slots.value))
+    return BucketPlan(words.to(device), tuple(host.shape), n_buckets, int(slots.value))
 
 
 def position_bias_bwd_workspace_bytes(plan: BucketPlan, n_win: int, heads: int,
                                       n_types: int = 1) -> int:
     """Bytes of workspace position_bias_bwd needs."""
     return int(_capi.load().wgs_position_bias_bwd_workspace_bytes(
-        int(n_win), int(heads), int(n_types), plan.n_pairs, plan.n_slots))
+        _int64(n_win, "n_win"), _int32(heads, "heads"), _int32(n_types, "n_types"), plan.n_pairs,
+        plan.n_slots))
 
 
 def position_bias_bwd(grad: torch.Tensor, plan: BucketPlan,
@@ -466,6 +487,8 @@ def position_bias_bwd(grad: torch.Tensor, plan: BucketPlan,
     n_win, heads = grad.shape[:2]
     if n_types < 0:
         _fail("n_types must not be negative")
+    if max(n_types, heads) > _MAX32:
+        _fail(f"n_types and heads must be at most {_MAX32} (got {n_types}, {heads})")
     if dtype not in (torch.float32, kind):
         _fail(f"dtype must be float32 or {kind} (got {dtype})")
     types = 0
@@ -507,6 +530,8 @@ def _norm_args(x, groups, weight, bias, act):
     n, channels = dims[0], dims[-1]
     if channels <= 0 or groups <= 0 or channels % groups != 0:
         _fail(f"channels ({channels}) must be a multiple of groups ({groups})")
+    if channels > _MAX32:
+        _fail(f"channels must be at most {_MAX32} (got {channels})")
     spatial = dims[1] if len(dims) == 3 else 1 if len(dims) == 2 else math.prod(dims[1:-1])
     index = x.get_device()
     if weight is None or bias is None:
@@ -522,16 +547,19 @@ def _norm_args(x, groups, weight, bias, act):
     return index, n, spatial, channels, w, b, pt
 
 
+def _norm_sizes(n, spatial, channels, groups):
+    return (_int64(n, "n"), _int64(spatial, "spatial"), _int32(channels, "channels"),
+            _int32(groups, "groups"))
+
+
 def group_norm_act_workspace_bytes(n: int, spatial: int, channels: int, groups: int) -> int:
     """Bytes of workspace group_norm_act needs for [n, spatial, channels]."""
-    return int(_capi.load().wgs_group_norm_act_workspace_bytes(int(n), int(spatial), int(channels),
-                                                               int(groups)))
+    return int(_capi.load().wgs_group_norm_act_workspace_bytes(*_norm_sizes(n, spatial, channels, groups)))
 
 
 def group_norm_act_bwd_workspace_bytes(n: int, spatial: int, channels: int, groups: int) -> int:
     """Bytes of workspace group_norm_act_bwd needs for [n, spatial, channels]."""
-    return int(_capi.load().wgs_group_norm_act_bwd_workspace_bytes(int(n), int(spatial),
-                                                                   int(channels), int(groups)))
+    return int(_capi.load().wgs_group_norm_act_bwd_workspace_bytes(*_norm_sizes(n, spatial, channels, groups)))
 
 
 def group_norm_act(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
@@ -554,7 +582,7 @@ def group_norm_act(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
     _run("group_norm_act", _capi.load().group_norm_act, index, x.data_ptr(), w, b,
          _given(y, "out", kind, index), _given(m, "mean", torch.float32, index),
          _given(r, "rstd", torch.float32, index), _given(ws, "workspace", torch.uint8, index),
-         ws.numel(), n, spatial, channels, groups, eps, _ACT[act], _DTYPE[kind], _DTYPE[pt])
+         ws.numel(), n, spatial, channels, groups, float(eps), _ACT[act], _DTYPE[kind], _DTYPE[pt])
     return y, m, r
 
 
@@ -598,7 +626,7 @@ SHIFT_THEN_PAD, PAD_THEN_SHIFT = 0, 1
 
 
 def _i3(v, name):
-    vals = [int(a) for a in v]
+    vals = [_int32(a, name) for a in v]
     _require(len(vals) == 3, f"{name} must have 3 entries")
     return (ctypes.c_int32 * 3)(*vals)
 
