@@ -472,7 +472,8 @@ def position_bias_bwd(grad: torch.Tensor, plan: BucketPlan,
     """The gradient of position_bias's table, [n_types, n_buckets, heads], from
     the gradient of the logits grad [n_win, heads, n_q, n_k]; win_type int32
     [n_win] (None: type 0).  `dtype`, the gradient's format, is float32 or
-    grad's.  The fixed-order sums need a workspace of
+    grad's.  With one type, grad_table may be [n_buckets, heads], as the table
+    may, and is returned so.  The fixed-order sums need a workspace of
     position_bias_bwd_workspace_bytes(...) bytes; one is allocated here unless
     the caller passes a uint8 CUDA tensor that large."""
     if not isinstance(grad, torch.Tensor) or not grad.is_cuda or not grad.is_contiguous():
@@ -498,7 +499,10 @@ def position_bias_bwd(grad: torch.Tensor, plan: BucketPlan,
             _fail(f"win_type must have {n_win} entries")
         if n_win == 0:
             types = 0
-    gt = _into(grad_table, (n_types, plan.n_buckets, heads), dtype, grad.device, "grad_table")
+    shape = (n_types, plan.n_buckets, heads)
+    if grad_table is not None and n_types == 1 and grad_table.dim() == 2:
+        shape = shape[1:]
+    gt = _into(grad_table, shape, dtype, grad.device, "grad_table")
     ws = _space(workspace, lambda: position_bias_bwd_workspace_bytes(plan, n_win, heads, n_types),
                 grad.device)
     _run("position_bias_bwd", _capi.load().position_bias_bwd, index, grad.data_ptr(),
