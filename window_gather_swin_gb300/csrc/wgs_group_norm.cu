@@ -276,7 +276,8 @@ struct NormArgs {
 // The first launch of a call waits for what came before on the stream.  A
 // launch of pass 2 follows one of pass 1 of the same call, which has waited
 // for all that, and needs of it only the workspace's sums: it may read the
-// call's inputs at once, and waits (wait_for_sums) before it reads the sums or writes.
+// call's inputs at once, and waits (wait_for_sums) before it reads the sums or
+// writes.
 __device__ __forceinline__ void start_launch(const NormArgs &a) {
 #if WGS_PDL
     if (a.passes != 2) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -764,7 +765,6 @@ __device__ void stats_pass(const NormArgs &a, const Job &job, Bars &bars, float2
         }
         __syncthreads();
     }
-    wait_for_sums(a);  // nothing is written before
     float2 *out = a.groups_part + (job.sample * a.clusters + job.cl) * a.groups;
     // the channels of a group, in two steps: the mean, M2 about it
     each_group(a, job, [&](int g, int lane, int lanes) {
@@ -945,7 +945,6 @@ __device__ void sums_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
             ch[c] = t;
         });
     }
-    wait_for_sums(a);  // nothing is written before
     const int64_t place = job.sample * a.clusters + job.cl;
     float2 *group_out = a.groups_part + place * a.groups;
     each_group(a, job, [&](int g, int lane, int lanes) {

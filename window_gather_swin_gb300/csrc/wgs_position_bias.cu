@@ -1098,9 +1098,11 @@ constexpr int64_t kGradBlocks = 152 * kGradCtas;
 // Windows of a type in a slab at least, on average.
 constexpr int64_t kSlabWindows = 4;
 
-// Slabs of windows: the fewest with which the blocks' shares of the units,
-// whole ones, leave at most a tenth of the blocks' time unused.  Depends on the
-// sizes alone, so results do not depend on the device.
+// Slabs of windows: the fewest with which the blocks' shares of the units, whole
+// ones, leave at most a tenth of them out, where the units are as many as the
+// blocks' shares could hold.  (A map's last tile counts as a full one, so with a
+// short one blocks that hold more full tiles take longer.)  Depends on the sizes
+// alone, so results do not depend on the device.
 int64_t grad_slabs(int64_t n_win, int64_t heads, int64_t n_types, int64_t n_tiles) {
     const int64_t base = heads * n_types * (n_tiles > 0 ? n_tiles : 1);
     const int64_t most = n_win / (n_types * kSlabWindows);
