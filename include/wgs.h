@@ -440,7 +440,9 @@ wgs_status wgs_build_distance_buckets(int64_t n_q, int64_t n_k, int64_t q_start,
 
 /* The plan of a bucket map (host int32 [n_pairs], values in [-1,
  * n_buckets)): for tiles of 4096 pairs, the pairs of each bucket.  Built once
- * per map and copied to the device.  wgs_bucket_plan_words returns its size
+ * per map, on one host thread (about 13 ms for 1024 x 1024 pairs and 50 ms for
+ * 2047 x 2047: a map that changes with a sequence's length costs that each
+ * time), and copied to the device, which a captured graph cannot do anew.  wgs_bucket_plan_words returns its size
  * in int32 words and its slot count (a bucket's pairs in a tile make a slot or
  * more), or -1 for invalid sizes or a value outside [-1, n_buckets), for
  * which the builder returns WGS_ERR_SHAPE or WGS_ERR_INDEX.  Host memory
@@ -458,7 +460,10 @@ wgs_status wgs_build_bucket_plan(const int32_t *bucket_host, int64_t n_pairs, in
  *     mean, var   over the spatial * channels / groups values (biased, FP32)
  *     rstd = 1 / sqrt(var + eps)
  *     y    = fp(act((x - mean) * rstd * weight[c] + bias[c]))
- * in FP32, rounded once to `dtype`.  act: WGS_ACT_NONE, WGS_ACT_SILU
+ * in FP32, rounded once to `dtype`.  The statistics are sums of distances from
+ * references near the mean, so neither the mean's size nor rows far from all
+ * others cost accuracy; distances whose squares pass FP32's range (beyond about
+ * 1e18) are not covered.  act: WGS_ACT_NONE, WGS_ACT_SILU
  * (z / (1 + exp(-z))) or WGS_ACT_GELU_TANH (as bias_gelu_tanh's); any other
  * value returns WGS_ERR_DTYPE.
  *   x, y    [n, spatial, channels] of dtype (any wgs_dtype); y == x allowed,

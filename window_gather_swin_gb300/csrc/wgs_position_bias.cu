@@ -672,9 +672,9 @@ __device__ void slot_units(const GradArgs &a, GradShared<E> &sh, Unit u, int32_t
 // slot.  Every gradient is read once; what leaves is one value per slot.  The
 // order of all additions is fixed by the sizes and the plan.
 // 960 windows of 6 heads and 144 x 144 pairs in 64 types, fp16: 43 us of the call's
-// 51 for 239 MB (5.6 TB/s, bound by DRAM).  Where a unit has one window the way
+// 50 for 239 MB (5.6 TB/s, bound by DRAM).  Where a unit has one window the way
 // of its sums through shared memory bounds it: 16 heads of 2047 x 2047 pairs, 134
-// MB, 58 us (1.1 us a unit and block).
+// MB, 60 us (1.1 us a unit and block).
 template <typename E, bool kVec>
 __global__ void __launch_bounds__(kGradThreads, kGradCtas) bias_grad_tiles(GradArgs a) {
     extern __shared__ __align__(16) char smem[];
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradCtas) bias_grad_tiles(GradA
 // sums of the same kOwn words (of kW pairs) of each of its windows; the groups'
 // are added in order in shared memory, and from there by slot, as above.  4096
 // windows, fp16, us of the call (by tiles): 1 pair of 32 heads 5 (134), 16 pairs of
-// 32 heads 8 (83), 256 pairs of 16 heads, 34 MB, 12 (45).  Latency bounds it.
+// 32 heads 7 (83), 256 pairs of 16 heads, 34 MB, 14 (45).  Latency bounds it.
 constexpr int kSmallThreads = 512, kSmallValues = 4096;
 
 template <typename E, int kW, int kOwn>
@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) bias_grad_small(GradArgs a, 
         int32_t n = group;
         for (int32_t stop; n < count; end_run()) {
             stop = min(count, n + kRun * groups);
-#pragma unroll 2  // (4096 windows of 16 pairs and 32 heads 19.5 us, without 21.6)
+#pragma unroll 2  // (4096 windows of 256 pairs and 32 heads 19.5 us, without 21.6)
             for (; n < stop; n += kAhead * groups) {
                 Raw v[kAhead][kOwn];
 #pragma unroll
@@ -996,7 +996,7 @@ __global__ void __launch_bounds__(kThreads) bias_grad_table(GradArgs a, int32_t 
 
 // Pass 2 where buckets have many slots: a block a (type, bucket, head).  The
 // largest bucket bounds it, two rounds to L2 for 16 values a thread: 512 outputs
-// of 158,323 slots 19 us.  (A cluster of blocks an output: 175.)
+// of 158,323 slots 17 us.  (A cluster of blocks an output: 175.)
 constexpr int kBlockThreads = 1024;
 
 template <typename T>
