@@ -65,7 +65,7 @@ constexpr int kThreadsBwd = 512, kBlocksBwd = 152;
 constexpr int kRowsFwd = 4, kStagesFwd = 3;
 constexpr int kRowsBwd = 4, kStagesBwd = 2, kMostStages = 3;
 // Of a block.  The most that a call needs is 208 KB (backward, 4096 channels
-// of FP32 in 2048 groups).
+// of FP32 in 2048 groups); a third stage of the backward's fills what is left.
 constexpr int kMaxSmem = 220 << 10;
 constexpr int kBarBytes = 2 * kMostStages * static_cast<int>(sizeof(uint64_t));  // beside kMaxSmem
 constexpr int kMaxCluster = 8;   // of a sample that one cluster holds
@@ -316,6 +316,9 @@ struct Job {
 // Rows of a thread after which run() calls between() first; then 8 times as many.
 constexpr int32_t kMove = 8;
 static_assert(kMove % kRowsFwd == 0 && kMove % kRowsBwd == 0, "between whole stages");
+struct Nothing {
+    __device__ void operator()(int32_t) const {}
+};
 
 // A slab's rows on their way through shared memory: kRows rows of every thread
 // a stage, kStages stages, f(chunk of each tensor, its byte offset) for each
@@ -326,9 +329,6 @@ static_assert(kMove % kRowsFwd == 0 && kMove % kRowsBwd == 0, "between whole sta
 // they are one piece of memory where the block walks whole rows), and an
 // mbarrier a stage tells that they have come, another that every warp has
 // read them.  A thread spends nothing on addresses and copies of its own.
-struct Nothing {
-    __device__ void operator()(int32_t) const {}
-};
 struct Bars {
     uint32_t full, empty;  // of stage 0; 8 bytes a stage
     int stages;
@@ -384,8 +384,8 @@ struct Bulk {
         if (job.tid == 0) {
             // what the block wrote to the slots comes before the copies
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            for (int u = 0; u < stages() - 1 && u < count; ++u)
-                copy(u, bars.stage + u < stages() ? bars.stage + u : bars.stage + u - stages());
+            for (int i = 0; i < stages() - 1 && i < count; ++i)
+                copy(i, bars.stage + i < stages() ? bars.stage + i : bars.stage + i - stages());
         }
     }
     template <typename Use, typename Between = Nothing>
@@ -404,7 +404,7 @@ struct Bulk {
             }
             if (i == move) {
                 between(i * kRows);
-                move *= 8;
+                move = move < INT32_MAX / 8 ? 8 * move : INT32_MAX;
             }
             wait(bars.full + 8 * bars.stage, bars.phase);
             const uint32_t slot = ring + bars.stage * stage_bytes() + job.tid * C::kBytes;

@@ -1040,10 +1040,11 @@ __global__ void __launch_bounds__(kBlockThreads) bias_grad_block(GradArgs a) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) v += q[k];
     };
+    auto next = [&](int32_t d) { return d1 - d > kStep ? d + kStep : d1; };  // (no step past 2^31 - 1)
     int32_t d = first;
-    if (a.early) batch(d, std::true_type{}), d += kStep;
+    if (a.early) batch(d, std::true_type{}), d = next(d);
     for (int32_t s = 0; s < a.slabs; ++s, p += step, d = first)
-        for (; d < d1; d += kStep) batch(d, std::false_type{});
+        for (; d < d1; d = next(d)) batch(d, std::false_type{});
     v = group_sum<32>(v);
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
