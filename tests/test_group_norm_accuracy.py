@@ -134,6 +134,26 @@ def test_statistics_beside_far_rows(shape, fmt, where):
     _check_output(x, y, w, b, mean, rstd, g, "silu")
 
 
+@pytest.mark.parametrize("where", ["first", "last"])
+@pytest.mark.parametrize("shape,fmt", [((1, 131040, 192, 32), "f32"), ((1, 1_000_000, 8, 1), "f32"),
+                                       ((2, 20000, 48, 4), "f32"), ((2, 4000, 1024, 1), "f16"),
+                                       ((400, 300, 32, 4), "bf16")], ids=str)
+def test_statistics_beside_a_far_slab(shape, fmt, where):
+    """As many rows as a block takes, or an eighth of a sample where one cluster
+    does, 100 deviations from all others: padding in front or behind."""
+    n, s, c, g = shape
+    gen = torch.Generator(DEV).manual_seed(s)
+    x = 100 + torch.randn(n, s, c, generator=gen, device=DEV)
+    rows = s // 8 if n * s < 200_000 else s * n // 152
+    x[:, :rows] = 0
+    x = (x if where == "first" else x.flip(1)).to(DT[fmt])
+    w, b = _weights(c, 3)
+    y, mean, rstd = wgs.group_norm_act(x, g, w, b, 1e-5, None)
+    wgs.check_error(DEV)
+    _check_statistics(x, mean, rstd, g, 1e-5, _depth(shape, fmt, False))
+    _check_output(x, y, w, b, mean, rstd, g, None)
+
+
 LARGE = [
     ((1, 131040, 192, 32), "f16", "silu"), ((3, 65600, 192, 32), "f16", "silu"),
     ((2, 131040, 192, 8), "bf16", "gelu_tanh"), ((33, 1000, 1001, 7), "bf16", "silu"),

@@ -595,15 +595,14 @@ __device__ __forceinline__ float values_of(const NormArgs &a, int32_t s, int32_t
     return static_cast<float>(a.slabs1.of(s, count)) * static_cast<float>(a.per_group);
 }
 
-// For every group g: the sum of value(part, g's pair of the part, its pair of
-// part 0) over the parts, in a fixed order, to done(g, sum, pair of part 0).
-// part[parts][groups].  Neighbouring threads take neighbouring groups, and the
+// For every group g: the sum of its pairs over the parts, in a fixed order, to
+// done(g, sum).  part[parts][groups].  Neighbouring threads take neighbouring groups, and the
 // threads beyond the groups a share of the parts each.  smem holds a pair a
 // thread.  then() runs once the first loads are under way: what it starts
 // should not be ahead of them on the way to memory.
-template <typename Value, typename Then, typename Done>
+template <typename Then, typename Done>
 __device__ __forceinline__ void add_parts(float2 *smem, const Job &job, const float2 *part, int groups, int parts,
-                                          Value value, Then then, Done done) {
+                                          Then then, Done done) {
     constexpr int kFirst = 16;
     const int wide = min(groups, job.threads);
     const int lanes = job.threads / wide;
@@ -612,7 +611,6 @@ __device__ __forceinline__ void add_parts(float2 *smem, const Job &job, const fl
         const int g = g0 + j;
         const bool live = l < lanes && g < groups;
         const float2 *q = part + (live ? g : 0);
-        const float2 own = __ldcg(q);
         float2 v[kFirst];
 #pragma unroll
         for (int k = 0; k < kFirst; ++k)
@@ -621,15 +619,89 @@ __device__ __forceinline__ void add_parts(float2 *smem, const Job &job, const fl
         float2 t = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < kFirst; ++k)
-            if (live && l + k * lanes < parts) t = add2(t, value(l + k * lanes, v[k], own));
+            if (live && l + k * lanes < parts) t = add2(t, v[k]);
         if (live)
-            for (int p = l + kFirst * lanes; p < parts; p += lanes) t = add2(t, value(p, __ldcg(q + p * groups), own));
+            for (int p = l + kFirst * lanes; p < parts; p += lanes) t = add2(t, __ldcg(q + p * groups));
         smem[job.tid] = t;
         __syncthreads();
         if (l == 0 && live) {
 #pragma unroll 8
             for (int k = 1; k < min(lanes, parts); ++k) t = add2(t, smem[k * wide + j]);
-            done(g, t, own);
+            done(g, t);
+        }
+        __syncthreads();
+    }
+}
+
+// A set of values: how many, their mean (here from some origin) and M2.
+struct Stats {
+    float n = 0.f, mean = 0.f, m2 = 0.f;
+    // m > 0 more, whose mean is d further on: the joint mean is d m / (n + m)
+    // further on, and M2 grows by theirs and d^2 n m / (n + m)
+    __device__ void join(float m, float at, float more) {
+        const float share = __fdividef(m, n + m), d = at - mean;
+        m2 += fmaf(d * d, n * share, more);
+        mean = fmaf(d, share, mean);
+        n += m;
+    }
+};
+
+// For every group the statistics of all parts, each a (mean, M2), as add_parts
+// adds, joined one by one: a sum about one part's mean would cancel by a factor of
+// the parts where that one lies far from all others (a slab of zeros before values
+// 100 deviations off left rstd 6e-5 off, of 152 parts).  smem holds a pair and a
+// count a thread.
+template <typename Count, typename Then, typename Done>
+__device__ __forceinline__ void join_parts(float2 *smem, const Job &job, const float2 *part, int groups, int parts,
+                                            Count count, Then then, Done done) {
+    if (parts == 1) {  // a sample of one cluster
+        float2 v = __ldcg(part + min(job.tid, groups - 1));
+        then();
+        for (int g = job.tid; g < groups; g += job.threads) {
+            if (g != job.tid) v = __ldcg(part + g);
+            Stats t;
+            t.mean = v.x, t.m2 = v.y;
+            done(g, t);
+        }
+        __syncthreads();
+        return;
+    }
+    constexpr int kAhead = 16, kMostLanes = 16;
+    float *counts = reinterpret_cast<float *>(smem + job.threads);
+    const int wide = min(groups, job.threads);
+    const int lanes = min(min(job.threads / wide, kMostLanes), parts);
+    const int l = job.tid / wide, j = job.tid - l * wide;
+    for (int g0 = 0; g0 < groups; g0 += wide) {
+        const int g = g0 + j;
+        const bool live = l < lanes && g < groups;
+        const float2 *q = part + (live ? g : 0);
+        const float own = __ldcg(q).x;  // the origin
+        Stats t;
+        auto batch = [&](int first, auto started) {
+            float2 v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                v[k] = live && first + k * lanes < parts ? __ldcg(q + (first + k * lanes) * groups) : make_float2(own, 0.f);
+            started();
+            // a part that is not there counts nothing (each lane has its first)
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int p = first + k * lanes;
+                t.join(p < parts ? count(p) : 0.f, v[k].x - own, v[k].y);
+            }
+        };
+        batch(l, [&] { if (g0 == 0) then(); });
+        for (int p = l + kAhead * lanes; p < parts; p += kAhead * lanes) batch(p, [] {});
+        smem[job.tid] = make_float2(t.mean, t.m2), counts[job.tid] = t.n;
+        __syncthreads();
+        if (l == 0 && live) {
+#pragma unroll 4
+            for (int k = 1; k < lanes; ++k) {
+                const float2 more = smem[k * wide + j];
+                t.join(counts[k * wide + j], more.x, more.y);
+            }
+            t.mean += own;
+            done(g, t);
         }
         __syncthreads();
     }
@@ -663,7 +735,8 @@ __device__ __forceinline__ void set_half(float2 *v, int e, float x) {
 // cancels by a small factor at most, whatever the mean and wherever a row lies
 // far from all others.  (With one k for a slab such a row in its first place cost
 // a factor of the slab's rows: rstd off by 1e-3 after 4096.)  Threads' parts are
-// joined one by one, blocks' about the first one's mean.
+// joined one by one, those of a cluster's blocks, 8 at most, about the first one's
+// mean.
 template <typename E, int kV>
 __device__ void stats_pass(const NormArgs &a, const Job &job, Bars &bars, float2 *smem) {
     using C = Chunk<E, kV>;
@@ -738,20 +811,16 @@ __device__ void stats_pass(const NormArgs &a, const Job &job, Bars &bars, float2
             }
         }
         __syncthreads();
-        // joined one by one: of n rows and then m more, whose mean is d further on, the
-        // mean is d m / (n + m) further on, and M2 grows by theirs and d^2 n m / (n + m)
         auto join = [&](const float2 *q, int first, int step, int end, auto rows) {
             const float2 own = q[first * count];
-            float mean = 0.f, m2 = own.y, n = rows(first);
+            Stats t;
+            t.n = rows(first), t.m2 = own.y;
 #pragma unroll 4
             for (int g = first + step; g < end; g += step) {
                 const float2 v = q[g * count];
-                const float m = rows(g), share = __fdividef(m, n + m), d = v.x - own.x - mean;
-                m2 += fmaf(d * d, n * share, v.y);
-                mean = fmaf(d, share, mean);
-                n += m;
+                t.join(rows(g), v.x - own.x, v.y);
             }
-            return make_float2(own.x + mean, m2);
+            return make_float2(own.x + t.mean, t.m2);
         };
         if (__builtin_expect(narrow, 0)) {
             const int e = job.g % kV, l = job.g / kV;
@@ -818,7 +887,7 @@ __device__ void apply_pass(const NormArgs &a, const Job &job, Bars &bars, float2
     const int64_t base = (job.sample * a.spatial + job.r0) * row_bytes;
     const uint64_t policy = l2_policy(a.last_use);
     // behind the slots: the groups' (-mean, rstd), the channels' (weight, bias),
-    // a pair a thread
+    // a pair and a count a thread
     float2 *stat = smem + a.ring / 8, *wb = stat + a.groups, *lanes = wb + a.channels;
     for (int c = job.tid; c < a.channels; c += job.threads)
         wb[c] = make_float2(param<E>(a.weight, c, a.p32, 1.f), param<E>(a.bias, c, a.p32, 0.f));
@@ -826,17 +895,13 @@ __device__ void apply_pass(const NormArgs &a, const Job &job, Bars &bars, float2
     in.src[0] = a.x;
     wait_for_sums(a);
     // (mean, rstd) of the sample's groups
-    add_parts(
+    join_parts(
         lanes, job, a.groups_part + job.sample * a.clusters * a.groups, a.groups, a.clusters,
-        [&](int c, float2 v, float2 own) {
-            const float n = values_of(a, c * a.cluster, a.cluster), d = v.x - own.x;
-            return make_float2(n * d, fmaf(n * d, d, v.y));
-        },
+        [&](int c) { return values_of(a, c * a.cluster, a.cluster); },
         [&] { in.start(smem, base, row_bytes, min(job.columns, a.chunks), true, policy); },
-        [&](int g, float2 t, float2 own) {
-            const float n = static_cast<float>(a.spatial) * static_cast<float>(a.per_group), m = t.x / n;
-            const float mean = own.x + m;
-            const float rstd = 1.0f / sqrtf(not_below_zero(fmaf(-m, t.x, t.y)) / n + a.eps);
+        [&](int g, const Stats &t) {
+            const float n = static_cast<float>(a.spatial) * static_cast<float>(a.per_group), mean = t.mean;
+            const float rstd = 1.0f / sqrtf(not_below_zero(t.m2) / n + a.eps);
             stat[g] = make_float2(-mean, rstd);
             if (job.r0 == 0 && a.mean) {
                 a.mean[job.sample * a.groups + g] = mean;
@@ -1006,9 +1071,8 @@ __device__ void grad_pass(const NormArgs &a, const Job &job, Bars &bars, float2 
     wait_for_sums(a);
     add_parts(
         lanes, job, a.groups_part + job.sample * a.clusters * a.groups, a.groups, a.clusters,
-        [](int, float2 v, float2) { return v; },
         [&] { in.start(smem, base, row_bytes, min(job.columns, a.chunks), true, policy); },
-        [&](int g, float2 v, float2) {
+        [&](int g, float2 v) {
             const float n = static_cast<float>(a.spatial) * static_cast<float>(a.per_group), rstd = stat[g].y;
             coef[g] = make_float2(-rstd * (v.x / n), -rstd * rstd * (v.y / n));
         });
@@ -1200,7 +1264,7 @@ wgs_status run(NormArgs a, const Plan &z, int act, bool backward, int64_t n, cud
         // Shared memory.  Pass 1: the channels' sums, and in one place the
         // slots, the row groups' sums and the groups'; where one walk covers
         // the row the channels' lie over the slots too.  Pass 2: the slots,
-        // the groups' and channels' values, a pair a thread.
+        // the groups' and channels' values, a pair a thread (and a count, forward).
         const int red = 8 * (threads * kV > a.groups ? threads * kV : a.groups), ch = 8 * a.channels;
         auto size = [&](int stages) {
             a.stages = stages;
@@ -1210,7 +1274,8 @@ wgs_status run(NormArgs a, const Plan &z, int act, bool backward, int64_t n, cud
             // (the backward's pass 1 keeps the groups' and channels' values behind that)
             a.behind = (pass1 + 15) / 16 * 16;
             const int one = passes & 1 ? a.behind + (backward ? 8 * (a.groups + a.channels) : 0) : 0;
-            const int two = passes & 2 ? a.ring + 8 * ((backward ? 2 : 1) * a.groups + a.channels + threads) : 0;
+            const int two = passes & 2 ? a.ring + 8 * ((backward ? 2 : 1) * a.groups + a.channels + threads) +
+                                             (backward ? 0 : 4 * threads) : 0;
             return one > two ? one : two;
         };
         int smem = size(backward ? kStagesBwd : kStagesFwd);
