@@ -1248,9 +1248,9 @@ wgs_status run(NormArgs a, const Plan &z, int act, bool backward, int64_t n, cud
     // end to end is a chain of waits.  Threads halve to 64 as long as each has
     // kRowsMany rows of the slab at most.  (The backward's blocks of 512 fill an SM,
     // and clusters of 8 of those do not all find room beyond some 100 blocks.)
-    // [4096, 49, 96] fp16: 42 and 62 us forward and backward, with 256 threads 75 and
-    // 118; [1024, 256, 128] 40 and 62 (43 and 70); [16, 512, 320] backward 19, with
-    // 512 threads 28; [12, 512, 512] of 96 blocks 17, with 256 threads 22.
+    // [4096, 49, 96] fp16: 42 and 63 us forward and backward, with 256 threads 75 and
+    // 118; [1024, 256, 128] 41 and 63 (43 and 70); [16, 512, 320] backward 20, with
+    // 512 threads 28; [12, 512, 512] of 96 blocks 18.6, with 256 threads 22.
     const int64_t blocks = n * z.cluster;
     if (z.one_launch && blocks > (backward ? kFewBlocksBwd : kFewBlocksFwd)) most = kThreadsMany;
     if (z.one_launch && blocks > kFewBlocksFwd) {
