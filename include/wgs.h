@@ -494,7 +494,10 @@ wgs_status group_norm_act(const void *x, const void *weight, const void *bias, v
  * the mean over a group:
  *     grad_x      = fp(rstd (dz weight - M(dz weight) - h M(dz weight h)))
  *     grad_weight = fp(sum of dz h),   grad_bias = fp(sum of dz)  (all rows)
- * in FP32, each rounded once.
+ * in FP32, each rounded once.  A thread adds its rows one after another, of which
+ * there are about rows / 152 over its block's row groups: terms of one sign leave
+ * the sums off by a few 1e-7 at 131040 rows of 192 FP32 values, by 5e-5 at 11
+ * million.
  *   grad_y, x, grad_x  as x above; grad_x may equal grad_y or x.
  *   mean, rstd  as the forward wrote them.
  *   grad_weight, grad_bias  [channels] of param_dtype; NULL skips either
