@@ -75,8 +75,8 @@ extern "C" {
  * 2: adds the bfloat16 forms, the GELU backward (with and without a
  *    workspace), the attention bias-mask add and the region-label builder;
  *    the backward's workspace query covers zero rows.
- * Entry points added since (position bias by buckets, group norm) change no
- * call of version 2, so the number stays. */
+ * Entry points added since (position bias by buckets, group norm, layer norm
+ * with weights, embedding) change no call of version 2, so the number stays. */
 #define WGS_ABI_VERSION 2
 
 typedef enum {
@@ -513,6 +513,109 @@ wgs_status group_norm_act_bwd(const void *grad_y, const void *x, const void *wei
                               cudaStream_t stream);
 
 /* ------------------------------------------------------------------ */
+/* layer_norm -- layer norm with weight and bias, any width             */
+/* ------------------------------------------------------------------ */
+/* ln_fwd folds the affine part into the following Linear; a block in training
+ * keeps it, and reads the statistics again on its way back.  For each row:
+ *     mean = sum(x) / width,  var = sum((x - mean)^2) / width
+ *     rstd = 1 / sqrt(var + eps)
+ *     y    = fp((x - mean) * rstd * weight[c] + bias[c])
+ * in FP32, rounded once to `dtype`.  The variance and y are formed from the
+ * distances to the row's rounded mean and corrected for its rounding, so the
+ * mean's size costs no accuracy; sums of values, or of their distances'
+ * squares, that pass FP32's range are not covered.
+ *   x, y    [rows, width] of dtype (any wgs_dtype); y == x allowed, other
+ *           overlaps return WGS_ERR_ALIAS.
+ *   weight, bias  [width] of param_dtype (WGS_F32, or `dtype`); NULL: 1 and 0
+ *           (a bias needs a weight).
+ *   mean, rstd  float [rows], written for the backward; both or neither.
+ * width: 1 to 8192 (else WGS_ERR_WIDTH).  Pointers need their element's
+ * alignment; with width a multiple of 4 and rows that start on four elements
+ * the values are moved in fours (the sums' order differs). */
+wgs_status layer_norm(const void *x, const void *weight, const void *bias, void *y, float *mean,
+                      float *rstd, int64_t rows, int32_t width, float eps, wgs_dtype dtype,
+                      wgs_dtype param_dtype, cudaStream_t stream);
+
+/* residual_add_layer_norm -- the residual add and the norm in one pass:
+ *     residual_out = fp(residual + branch)   (written out)
+ *     y            = layer_norm(residual_out)
+ * with the rounding point of residual_add_ln_fwd.  residual_out and y may each
+ * equal residual or branch, must differ from each other; other overlaps return
+ * WGS_ERR_ALIAS. */
+wgs_status residual_add_layer_norm(const void *residual, const void *branch, const void *weight,
+                                   const void *bias, void *residual_out, void *y, float *mean,
+                                   float *rstd, int64_t rows, int32_t width, float eps,
+                                   wgs_dtype dtype, wgs_dtype param_dtype, cudaStream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* layer_norm_bwd -- the gradients of both                              */
+/* ------------------------------------------------------------------ */
+/* With h = (x - mean) rstd, g = grad_y weight and M() the mean over a row:
+ *     grad_x      = fp(rstd (g - M(g) - h M(g h)) + grad_residual)
+ *     grad_weight = fp(sum of grad_y h),  grad_bias = fp(sum of grad_y)  (all rows)
+ * in FP32, each rounded once.  x is the forward's x, or residual_out;
+ * grad_residual is the gradient that reaches residual_out past the norm (NULL:
+ * none), and grad_x then is the gradient of residual and of branch.  A thread
+ * adds its rows one after another, of which there are about rows / 152 over its
+ * block's units: the sums' order depends on the sizes alone.
+ *   grad_y, x, grad_residual, grad_x  as x above; grad_x may equal any of
+ *           the others.
+ *   mean, rstd  as the forward wrote them.
+ *   grad_weight, grad_bias  [width] of param_dtype; NULL skips either.
+ *   workspace  at least wgs_layer_norm_bwd_workspace_bytes(...) bytes, 16-byte
+ *           aligned, disjoint from the tensors; its contents on entry do not
+ *           matter, and it may be NULL where both gradients are.  Calls that
+ *           overlap on the GPU need their own.
+ *   rows == 0 writes zeros to grad_weight and grad_bias. */
+size_t wgs_layer_norm_bwd_workspace_bytes(int64_t rows, int32_t width);
+wgs_status layer_norm_bwd(const void *grad_y, const void *x, const float *mean, const float *rstd,
+                          const void *weight, const void *grad_residual, void *grad_x,
+                          void *grad_weight, void *grad_bias, void *workspace,
+                          size_t workspace_bytes, int64_t rows, int32_t width, wgs_dtype dtype,
+                          wgs_dtype param_dtype, cudaStream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* embedding -- rows of a table by index, scaled                        */
+/* ------------------------------------------------------------------ */
+/*     out[i] = fp(scale * table[idx[i]])   for 0 <= idx[i] < n_rows
+ *     out[i] = 0                            for idx[i] == -1 (a pad)
+ * fp() rounds once, to nearest even, to `dtype`.  window_gather's rule for
+ * indices: one outside [-1, n_rows) gives a zero row and sets the device error
+ * word (wgs_check_error); nothing faults.
+ *   table   [n_rows, width] of table_dtype: WGS_F32, or `dtype`.
+ *   idx     int32 [n_idx].
+ *   out     [n_idx, width] of dtype (any wgs_dtype); must not overlap the
+ *           inputs (WGS_ERR_ALIAS).
+ * width: 1 to 32768 (else WGS_ERR_WIDTH).  n_idx and n_rows below 2^31 - 1
+ * (else WGS_ERR_SHAPE).  Pointers need their element's alignment; 16 bytes of
+ * out are moved at a time where all rows start on as many. */
+wgs_status embedding(const void *table, const int32_t *idx, void *out, int64_t n_idx,
+                     int64_t n_rows, int32_t width, float scale, wgs_dtype table_dtype,
+                     wgs_dtype dtype, cudaStream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* embedding_bwd -- the table's gradient                                */
+/* ------------------------------------------------------------------ */
+/*     grad_table[r] = fp(scale * sum of grad[i] over the i with idx[i] == r)
+ * summed in FP32 over the indices sorted by row, in an order that depends on
+ * idx and the sizes alone.  With scale 1 it is also the gradient of
+ * window_gather through a map that may name a row more than once.  An index of
+ * -1 adds to no row, one outside [-1, n_rows) to none and sets the device error
+ * word.
+ *   grad        [n_idx, width] of dtype (any wgs_dtype).
+ *   grad_table  [n_rows, width] of table_dtype (WGS_F32, or `dtype`); every
+ *               row is written, zeros where no index names it.
+ *   workspace at least wgs_embedding_bwd_workspace_bytes(...) bytes, 16-byte
+ *             aligned, disjoint from the tensors; its contents on entry do not
+ *             matter.  Calls that overlap on the GPU need their own.  (0 bytes
+ *             for sizes that the call refuses.)
+ * Sizes as above. */
+size_t wgs_embedding_bwd_workspace_bytes(int64_t n_idx, int64_t n_rows, int32_t width);
+wgs_status embedding_bwd(const void *grad, const int32_t *idx, void *grad_table, void *workspace,
+                         size_t workspace_bytes, int64_t n_idx, int64_t n_rows, int32_t width,
+                         float scale, wgs_dtype dtype, wgs_dtype table_dtype, cudaStream_t stream);
+
+/* ------------------------------------------------------------------ */
 /* Host-side window index map                                 [P1 s5] */
 /* ------------------------------------------------------------------ */
 /* The page fixes the protocol (INT32 per destination row, >= 0 source
@@ -583,7 +686,7 @@ wgs_status wgs_build_shift_regions(const int32_t grid[3], const int32_t window[3
  * an index outside [-1, n_src), any window reverse an inverse index outside
  * [0, n_windowed), or any window_bias_mask_add a window type outside
  * [0, n_types), or a position-bias call a bucket, window type or plan out of
- * its range; WGS_ERR_LAUNCH if a kernel since then gave up waiting for its own
+ * its range, or an embedding call an index outside [-1, n_rows); WGS_ERR_LAUNCH if a kernel since then gave up waiting for its own
  * copies to arrive (its outputs are not to be used), and then WGS_ERR_INDEX from
  * the next check if there was a bad index too; WGS_OK otherwise.  The words are
  * shared by every stream of the device. */

@@ -63,6 +63,16 @@ SIGNATURES = {
     "wgs_group_norm_act_bwd_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i32, _i32]),
     "group_norm_act_bwd": (_st, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _i64,
                                  _i64, _i32, _i32, _i32, _i32, _i32, _P]),
+    "layer_norm": (_st, [_P, _P, _P, _P, _P, _P, _i64, _i32, _f32, _i32, _i32, _P]),
+    "residual_add_layer_norm": (_st, [_P, _P, _P, _P, _P, _P, _P, _P, _i64, _i32, _f32, _i32, _i32,
+                                      _P]),
+    "wgs_layer_norm_bwd_workspace_bytes": (ctypes.c_size_t, [_i64, _i32]),
+    "layer_norm_bwd": (_st, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _i64, _i32,
+                             _i32, _i32, _P]),
+    "embedding": (_st, [_P, _P, _P, _i64, _i64, _i32, _f32, _i32, _i32, _P]),
+    "wgs_embedding_bwd_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i32]),
+    "embedding_bwd": (_st, [_P, _P, _P, _P, ctypes.c_size_t, _i64, _i64, _i32, _f32, _i32, _i32,
+                            _P]),
     "wgs_check_error": (_st, [_P]),
 }
 

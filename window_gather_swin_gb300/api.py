@@ -626,6 +626,200 @@ def group_norm_act_bwd(grad_y: torch.Tensor, x: torch.Tensor, groups: int, mean:
     return gx, gw, gb
 
 
+# ---------------------------------------------------------- layer norm ----
+
+def _layer_norm_args(x, weight, bias, name):
+    """(device index, rows, width, weight's and bias's addresses, their dtype)
+    of checked layer-norm arguments."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or not x.is_contiguous():
+        _cuda(x, name)
+    kind, dims = x.dtype, x.shape
+    if kind not in _DTYPE:
+        _fail(f"{name} must be float32, float16 or bfloat16 (got {kind})")
+    if not dims:
+        _fail(f"{name} must be [..., width]")
+    width = dims[-1]
+    if width > _MAX32:
+        _fail(f"the width must be at most {_MAX32} (got {width})")
+    rows = dims[0] if len(dims) == 2 else math.prod(dims[:-1])
+    index = x.get_device()
+    if weight is None:
+        if bias is not None:
+            _fail("a bias needs a weight")
+        return index, rows, width, 0, 0, torch.float32
+    pt = weight.dtype if isinstance(weight, torch.Tensor) else None
+    if pt is not torch.float32 and pt is not kind:
+        _fail(f"weight must be float32 or {kind} (got {pt})")
+    w = _given(weight, "weight", pt, index)
+    b = _given(bias, "bias", pt, index) if bias is not None else 0
+    if weight.shape != (width,) or (b and bias.shape != (width,)):
+        _fail(f"weight and bias must have {width} elements")
+    return index, rows, width, w, b, pt
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+               out: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+               rstd: Optional[torch.Tensor] = None):
+    """Layer norm over the last dim (1 to 8192) of a float32, float16 or
+    bfloat16 tensor, with weight and bias [width] (float32 or x's format; None:
+    1 and 0).  Returns (y, mean, rstd); mean and rstd, float32 and shaped as x
+    without its last dim, are what layer_norm_bwd takes."""
+    index, rows, width, w, b, pt = _layer_norm_args(x, weight, bias, "x")
+    kind, device, lead = x.dtype, x.device, x.shape[:-1]
+    y = torch.empty_like(x) if out is None else _into(out, x.shape, kind, device, "out")
+    m = _into(mean, lead, torch.float32, device, "mean")
+    r = _into(rstd, lead, torch.float32, device, "rstd")
+    _run("layer_norm", _capi.load().layer_norm, index, x.data_ptr(), w, b,
+         _given(y, "out", kind, index), _given(m, "mean", torch.float32, index),
+         _given(r, "rstd", torch.float32, index), rows, width, float(eps), _DTYPE[kind], _DTYPE[pt])
+    return y, m, r
+
+
+def residual_add_layer_norm(residual: torch.Tensor, branch: torch.Tensor,
+                            weight: Optional[torch.Tensor] = None,
+                            bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                            residual_out: Optional[torch.Tensor] = None,
+                            out: Optional[torch.Tensor] = None,
+                            mean: Optional[torch.Tensor] = None,
+                            rstd: Optional[torch.Tensor] = None):
+    """Returns (residual_out, y, mean, rstd): residual_out = round(residual +
+    branch) in the tensors' format, the others layer_norm's of residual_out."""
+    index, rows, width, w, b, pt = _layer_norm_args(residual, weight, bias, "residual")
+    kind, device, shape = residual.dtype, residual.device, residual.shape
+    second = _given(branch, "branch", kind, index)
+    if branch.shape != shape:
+        _fail("residual and branch must have the same shape")
+    t = (torch.empty_like(residual) if residual_out is None
+         else _into(residual_out, shape, kind, device, "residual_out"))
+    y = torch.empty_like(residual) if out is None else _into(out, shape, kind, device, "out")
+    m = _into(mean, shape[:-1], torch.float32, device, "mean")
+    r = _into(rstd, shape[:-1], torch.float32, device, "rstd")
+    _run("residual_add_layer_norm", _capi.load().residual_add_layer_norm, index, residual.data_ptr(),
+         second, w, b, _given(t, "residual_out", kind, index), _given(y, "out", kind, index),
+         _given(m, "mean", torch.float32, index), _given(r, "rstd", torch.float32, index), rows, width,
+         float(eps), _DTYPE[kind], _DTYPE[pt])
+    return t, y, m, r
+
+
+def layer_norm_bwd_workspace_bytes(rows: int, width: int) -> int:
+    """Bytes of workspace layer_norm_bwd needs for [rows, width]."""
+    return int(_capi.load().wgs_layer_norm_bwd_workspace_bytes(_int64(rows, "rows"),
+                                                               _int32(width, "width")))
+
+
+def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                   weight: Optional[torch.Tensor] = None,
+                   grad_residual: Optional[torch.Tensor] = None,
+                   grad_x: Optional[torch.Tensor] = None,
+                   grad_weight: Optional[torch.Tensor] = None,
+                   grad_bias: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None):
+    """Gradients of layer_norm, or of residual_add_layer_norm with x its
+    residual_out and grad_residual the gradient that reaches residual_out past
+    the norm: grad_x is then that of residual and of branch.  Returns (grad_x,
+    grad_weight, grad_bias), the last two in the weight's format, None without
+    one.  grad_x may be grad_y, x or grad_residual.  The fixed-order sums need a
+    workspace of layer_norm_bwd_workspace_bytes(rows, width) bytes; one is
+    allocated here unless the caller passes a uint8 CUDA tensor that large."""
+    index, rows, width, w, _, pt = _layer_norm_args(x, weight, None, "x")
+    kind, device, shape = x.dtype, x.device, x.shape
+    gy = _given(grad_y, "grad_y", kind, index)
+    if grad_y.shape != shape:
+        _fail("grad_y and x must have the same shape")
+    m, r = _given(mean, "mean", torch.float32, index), _given(rstd, "rstd", torch.float32, index)
+    if mean.shape != shape[:-1] or rstd.shape != shape[:-1]:
+        _fail(f"mean and rstd must have shape {tuple(shape[:-1])}")
+    past = 0
+    if grad_residual is not None:
+        past = _given(grad_residual, "grad_residual", kind, index)
+        if grad_residual.shape != shape:
+            _fail("grad_residual and x must have the same shape")
+    gx = torch.empty_like(x) if grad_x is None else _into(grad_x, shape, kind, device, "grad_x")
+    gw = gb = None
+    pw = pb = ws = size = 0
+    if weight is not None:
+        gw = _into(grad_weight, (width,), pt, device, "grad_weight")
+        gb = _into(grad_bias, (width,), pt, device, "grad_bias")
+        pw, pb = _given(gw, "grad_weight", pt, index), _given(gb, "grad_bias", pt, index)
+        space = _space(workspace, lambda: layer_norm_bwd_workspace_bytes(rows, width), device)
+        ws, size = _given(space, "workspace", torch.uint8, index), space.numel()
+    elif grad_weight is not None or grad_bias is not None:
+        _fail("grad_weight and grad_bias need a weight")
+    _run("layer_norm_bwd", _capi.load().layer_norm_bwd, index, gy, x.data_ptr(), m, r, w, past,
+         _given(gx, "grad_x", kind, index), pw, pb, ws, size, rows, width, _DTYPE[kind], _DTYPE[pt])
+    return gx, gw, gb
+
+
+# ----------------------------------------------------------- embedding ----
+
+def embedding(table: torch.Tensor, idx: torch.Tensor, scale: float = 1.0, dtype=None,
+              out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[i] = round(scale * table[idx[i]]) for every entry of idx, int32 of any
+    shape (-1: a zero row); table [n_rows, width].  `dtype` is out's format, by
+    default out's or the table's; the table is float32 or of that format."""
+    if not isinstance(table, torch.Tensor) or not table.is_cuda or not table.is_contiguous():
+        _cuda(table, "table")
+    index = table.get_device()
+    where = _given(idx, "idx", torch.int32, index)
+    if table.dim() != 2:
+        _fail(f"table must be [n_rows, width] (got {tuple(table.shape)})")
+    n_rows, width = table.shape
+    if width > _MAX32:
+        _fail(f"the width must be at most {_MAX32} (got {width})")
+    if dtype is None:
+        dtype = table.dtype if out is None else out.dtype
+    if dtype not in _DTYPE:
+        _fail(f"dtype must be float32, float16 or bfloat16 (got {dtype})")
+    if table.dtype not in (torch.float32, dtype):
+        _fail(f"table must be float32 or {dtype} (got {table.dtype})")
+    y = _into(out, (*idx.shape, width), dtype, table.device, "out")
+    _run("embedding", _capi.load().embedding, index, table.data_ptr(), where,
+         _given(y, "out", dtype, index), idx.numel(), n_rows, width, float(scale),
+         _DTYPE[table.dtype], _DTYPE[dtype])
+    return y
+
+
+def embedding_bwd_workspace_bytes(n_idx: int, n_rows: int, width: int) -> int:
+    """Bytes of workspace embedding_bwd needs."""
+    return int(_capi.load().wgs_embedding_bwd_workspace_bytes(
+        _int64(n_idx, "n_idx"), _int64(n_rows, "n_rows"), _int32(width, "width")))
+
+
+def embedding_bwd(grad: torch.Tensor, idx: torch.Tensor, n_rows: int, scale: float = 1.0,
+                  dtype=torch.float32, grad_table: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of embedding's table, [n_rows, width], from that of its
+    output, grad [*idx.shape, width]: scale times the sum of the rows that idx
+    gives to each.  With scale 1 it is window_gather's too.  `dtype`, the
+    gradient's format, is float32 or grad's.  Sorting idx and the fixed-order
+    sums need a workspace of embedding_bwd_workspace_bytes(...) bytes; one is
+    allocated here unless the caller passes a uint8 CUDA tensor that large."""
+    if not isinstance(grad, torch.Tensor) or not grad.is_cuda or not grad.is_contiguous():
+        _cuda(grad, "grad")
+    index, kind = grad.get_device(), grad.dtype
+    if kind not in _DTYPE:
+        _fail(f"grad must be float32, float16 or bfloat16 (got {kind})")
+    where = _given(idx, "idx", torch.int32, index)
+    width = grad.shape[-1] if grad.dim() else 0
+    if grad.dim() != idx.dim() + 1 or grad.shape[:-1] != idx.shape:
+        _fail(f"grad must be {(*idx.shape, 'width')} (got {tuple(grad.shape)})")
+    if width > _MAX32:
+        _fail(f"the width must be at most {_MAX32} (got {width})")
+    n_rows = _int64(n_rows, "n_rows")
+    if n_rows < 0:
+        _fail("n_rows must not be negative")
+    if dtype not in (torch.float32, kind):
+        _fail(f"dtype must be float32 or {kind} (got {dtype})")
+    n = idx.numel()
+    gt = _into(grad_table, (n_rows, width), dtype, grad.device, "grad_table")
+    ws = _space(workspace, lambda: embedding_bwd_workspace_bytes(n, n_rows, width), grad.device)
+    _run("embedding_bwd", _capi.load().embedding_bwd, index, grad.data_ptr(), where,
+         _given(gt, "grad_table", dtype, index), _given(ws, "workspace", torch.uint8, index),
+         ws.numel(), n, n_rows, width, float(scale), _DTYPE[kind], _DTYPE[dtype])
+    return gt
+
+
 # ----------------------------------------------------------- index map ----
 
 SHIFT_THEN_PAD, PAD_THEN_SHIFT = 0, 1
@@ -691,7 +885,8 @@ def check_error(device=None) -> None:
     """Raise WgsError (WGS_ERR_INDEX) if any gather on `device` met an index
     outside [-1, n_src), or any bias-mask add a window type outside
     [0, n_types), or any position-bias call a bucket, window type or plan out
-    of its range, since the last check; WGS_ERR_LAUNCH if a kernel gave up
+    of its range, or any embedding call an index outside [-1, n_rows), since
+    the last check; WGS_ERR_LAUNCH if a kernel gave up
     waiting for its own copies, whose outputs are not to be used (a bad index
     seen too is raised by the next check).  Synchronises that device's current
     stream."""
