@@ -35,8 +35,6 @@ wgs_status bias_mask_error_take(unsigned int *seen, cudaStream_t stream);
 wgs_status position_bias_error_take(unsigned int *seen, cudaStream_t stream);
 // The same for the group norm's.
 wgs_status group_norm_error_take(unsigned int *seen, cudaStream_t stream);
-// The same for the layer norm's.
-wgs_status layer_norm_error_take(unsigned int *seen, cudaStream_t stream);
 // The same for the embedding's (a bad index).
 wgs_status embedding_error_take(unsigned int *seen, cudaStream_t stream);
 

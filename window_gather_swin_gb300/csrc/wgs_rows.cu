@@ -586,7 +586,7 @@ extern "C" wgs_status residual_add_norm_gather_bf16(const void *residual, const 
 extern "C" wgs_status wgs_check_error(cudaStream_t stream) {
     // The error words are read and cleared by symbol, so each copy resolves
     // the word in the context current at this call.
-    unsigned int seen = 0, seen_mask = 0, seen_bucket = 0, seen_norm = 0, seen_layer = 0, seen_row = 0;
+    unsigned int seen = 0, seen_mask = 0, seen_bucket = 0, seen_norm = 0, seen_row = 0;
     static const unsigned int cleared = 0, set = 1;
     if (cudaMemcpyFromSymbolAsync(&seen, g_index_error, sizeof(seen), 0, cudaMemcpyDeviceToHost,
                                   stream) != cudaSuccess ||
@@ -598,7 +598,6 @@ extern "C" wgs_status wgs_check_error(cudaStream_t stream) {
     if (bias_mask_error_take(&seen_mask, stream) != WGS_OK ||
         position_bias_error_take(&seen_bucket, stream) != WGS_OK ||
         group_norm_error_take(&seen_norm, stream) != WGS_OK ||
-        layer_norm_error_take(&seen_layer, stream) != WGS_OK ||
         embedding_error_take(&seen_row, stream) != WGS_OK)
         return WGS_ERR_CUDA;
     if (cudaStreamSynchronize(stream) != cudaSuccess) {
@@ -606,7 +605,7 @@ extern "C" wgs_status wgs_check_error(cudaStream_t stream) {
         return WGS_ERR_CUDA;
     }
     const bool bad_index = seen || seen_mask || seen_row || (seen_bucket & 1u);
-    if (!seen_norm && !seen_layer && !(seen_bucket & 2u)) return bad_index ? WGS_ERR_INDEX : WGS_OK;
+    if (!seen_norm && !(seen_bucket & 2u)) return bad_index ? WGS_ERR_INDEX : WGS_OK;
     // one status a check: the bad index is left for the next
     if (bad_index && cudaMemcpyToSymbolAsync(g_index_error, &set, sizeof(set), 0, cudaMemcpyHostToDevice,
                                              stream) != cudaSuccess) {
