@@ -19,6 +19,13 @@ template <typename E, int kC>
 constexpr int kBlocksPerSm = kC * 16 / kBytes<E> > 24 ? 1 : 2;
 constexpr int kHalfOfSm = 112 << 10, kMostOfSm = 216 << 10;   // shared memory
 
+// 1 / sqrt(v): the hardware's approximation and one step of Newton's method, which
+// would make NaN of an infinite one.
+__device__ __forceinline__ float reciprocal_root(float v) {
+    const float r = rsqrtf(v), better = fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
+    return v > 0.f && r > 0.f ? better : r;
+}
+
 // The row's statistics: with m = round(sum x / width) the distances d = x - m are
 // small whatever the mean's size, and their own mean, which m's rounding leaves,
 // comes off the variance and the result.
@@ -26,6 +33,7 @@ template <typename E, int kC, int kTeam, bool kWhole>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm<E, kC>) layer_norm_forward(const LayerNormArgs a) {
     extern __shared__ __align__(16) char shared[];
     __shared__ float2 exchange[2][kWarps];
+    __shared__ __align__(16) char edge_bytes[kWhole ? 16 : kEdgeBytes];
     using P = Place<E, kC, kTeam, kWhole>;
     constexpr int kPairs = P::kPairs, kHalf = P::kHalf;
     P p(a, exchange, shared_address(shared + a.kept_bytes));
@@ -33,6 +41,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<E, kC>) layer_norm_forw
     float *weight = reinterpret_cast<float *>(shared), *bias = weight + all, *inside = bias + all;
     char *mask_words = reinterpret_cast<char *>(inside + all);
     const uint32_t masks = shared_address(mask_words);
+    const uint32_t edges = shared_address(edge_bytes);
+    p.clear_slots();
     pdl_prologue();
     for (int s = 0; s < a.stages; ++s) p.fetch();
     p.keep_param(weight, a.weight, 1.f);
@@ -56,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<E, kC>) layer_norm_forw
 #pragma unroll
                 for (int i = 0; i < kPairs; ++i) x[i] = E::to_f2(E::from_f2(x[i].x, x[i].y));
             }
-            p.store(a.total, x);
+            p.store(a.total, edges, x);
         }
         p.fetch();
         float2 s = x[0];
@@ -81,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<E, kC>) layer_norm_forw
         const float m1 = t.x * a.inv;
         float var = fmaf(t.y, a.inv, -m1 * m1);
         if (var < 0.f) var = 0.f;   // (NaN stays)
-        const float rstd = __frsqrt_rn(var + a.eps);
+        const float rstd = reciprocal_root(var + a.eps), less = -m1 * rstd;
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             float2 w[kHalf], b[kHalf];
@@ -90,10 +100,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<E, kC>) layer_norm_forw
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) {
                 float2 &v = x[c * kHalf + i];
-                v = fma2(mul2(add2(v, both(-m1)), both(rstd)), w[i], b[i]);
+                v = fma2(fma2(v, both(rstd), both(less)), w[i], b[i]);
             }
         }
-        p.store(a.out, x);
+        p.store(a.out, edges, x);
         if (a.mean && p.there() && p.column_thread() == 0) {
             a.mean[p.row] = m + m1;
             a.rstd[p.row] = rstd;
@@ -120,7 +130,7 @@ wgs_status run_unit(LayerNormArgs a, cudaStream_t stream) {
     // Above 48 KB, its static memory included, a kernel needs the runtime's leave,
     // which belongs to the context; asking for the same amount on every call needs
     // no record of it.  (At most 118 KB beside a stage, and 72 KB of that.)
-    if (smem > 47 << 10 &&
+    if (smem > 45 << 10 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostOfSm) != cudaSuccess) {
         cudaGetLastError();
         return WGS_ERR_LAUNCH;

@@ -31,6 +31,7 @@ constexpr int kMaxWidth = 8192;
 constexpr int kWarps = 12;          // of a block, at most
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxStages = 4;
+constexpr int kEdgeBytes = kWarps * 4 * 32;   // of ragged rows' ends
 
 struct LayerNormArgs {
     const char *in[3];   // forward: x, branch; backward: x, grad_y, grad_residual
@@ -68,13 +69,13 @@ __device__ __forceinline__ float widen(const char *p) {
         return E::to_f2(*reinterpret_cast<const uint16_t *>(p)).x;
 }
 
-__device__ __forceinline__ void copy_chunk(uint32_t slot, const char *gmem) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot), "l"(gmem) : "memory");
-}
 __device__ __forceinline__ uint4 load_shared(uint32_t at) {
     uint4 q;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at) : "memory");
     return q;
+}
+__device__ __forceinline__ void store_shared(uint32_t at, const uint4 &q) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
 }
 // 16-byte asynchronous copy of the first `bytes` bytes at gmem, zeros behind.
 __device__ __forceinline__ void copy_part(uint32_t slot, const char *gmem, int bytes) {
@@ -171,39 +172,39 @@ struct Place {
         return v;
     }
 
-    // Copy the coming row of every tensor into the coming stage.  A row's first chunk
-    // may begin before the row, and before the tensor where that begins inside a chunk:
-    // in the same 16 bytes of memory as the tensor's first element.  Behind the tensor
-    // nothing is read.
+    // Copy the coming row of every tensor into the coming stage; zeros where there is
+    // none.  A row's first chunk may begin before the row, and before the tensor where
+    // that begins inside a chunk: in the same 16 bytes of memory as the tensor's first
+    // element.  Behind the tensor nothing is read.
     __device__ void fetch() {
         const uint32_t to = slots + coming;
-        if (next_row < a.rows) {
+        const bool is_there = next_row < a.rows;
+        const int64_t from_at = is_there ? next_at : 0;
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                if (k >= a.tensors) break;
-                const char *from = a.in[k] + next_at;
+        for (int k = 0; k < 3; ++k) {
+            if (k >= a.tensors) break;
+            const char *from = a.in[k] + from_at;
 #pragma unroll
-                for (int c = 0; c < kC; ++c) {
-                    if (!held(c)) continue;
-                    const char *p = from + c * column_threads() * 16;
-                    const uint32_t slot = to + (k * kC + c) * 512;
-                    if constexpr (kWhole) {
-                        copy_chunk(slot, p);
-                    } else if (a.together) {
-                        const int left = (a.width - column(c)) * kBytes<E>;
-                        copy_part(slot, p, left >= 16 || next_row + 1 < a.rows ? 16 : left);
-                    } else {
-                        uint32_t w[4] = {0u, 0u, 0u, 0u};
+            for (int c = 0; c < kC; ++c) {
+                if (!held(c)) continue;
+                const char *p = from + c * column_threads() * 16;
+                const uint32_t slot = to + (k * kC + c) * 512;
+                if constexpr (kWhole) {
+                    copy_part(slot, p, is_there ? 16 : 0);
+                } else if (a.together) {
+                    const int left = (a.width - column(c)) * kBytes<E>;
+                    copy_part(slot, p, !is_there ? 0 : left >= 16 || next_row + 1 < a.rows ? 16 : left);
+                } else {
+                    uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-                        for (int j = 0; j < kV; ++j) {
-                            if (column(c) + j >= a.width) continue;
-                            if constexpr (kV == 4)
-                                w[j] = *reinterpret_cast<const uint32_t *>(p + 4 * j);
-                            else
-                                w[j / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(p + 2 * j)) << (j & 1) * 16;
-                        }
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+                    for (int j = 0; j < kV; ++j) {
+                        if (!is_there || column(c) + j >= a.width) continue;
+                        if constexpr (kV == 4)
+                            w[j] = *reinterpret_cast<const uint32_t *>(p + 4 * j);
+                        else
+                            w[j / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(p + 2 * j)) << (j & 1) * 16;
                     }
+                    store_shared(slot, make_uint4(w[0], w[1], w[2], w[3]));
                 }
             }
         }
@@ -211,6 +212,14 @@ struct Place {
         next_row += row_step, next_at += step;
         coming += stage_bytes;
         if (coming == a.stages * stage_bytes) coming = 0;
+    }
+    // Before the first fetch: the slots of chunks past the row's end hold zeros for good.
+    __device__ void clear_slots() const {
+        for (uint32_t s = 0; s < a.stages * stage_bytes; s += stage_bytes)
+            for (int k = 0; k < a.tensors; ++k)
+#pragma unroll
+                for (int c = 0; c < kC; ++c)
+                    if (!held(c)) store_shared(slots + s + (k * kC + c) * 512, make_uint4(0u, 0u, 0u, 0u));
     }
     // Until the present stage has arrived.
     __device__ void arrived() const {
@@ -222,11 +231,9 @@ struct Place {
     // The thread's part of the present row of tensor k, widened; zeros outside the row
     // (`masks`: keep_masks').
     __device__ void load(int k, uint32_t masks, float2 (&v)[kPairs]) const {
-        const bool is_there = there();
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
-            uint4 q = make_uint4(0u, 0u, 0u, 0u);
-            if (is_there && held(c)) q = load_shared(slots + present + (k * kC + c) * 512);
+            uint4 q = load_shared(slots + present + (k * kC + c) * 512);
             if constexpr (!kWhole) {
                 const uint4 m = load_shared(masks + chunk(c) * 16);
                 q.x &= m.x, q.y &= m.y, q.z &= m.z, q.w &= m.w;
@@ -240,9 +247,15 @@ struct Place {
             }
         }
     }
-    // Rounds each value once, to nearest even, into the present row.
-    __device__ void store(char *base, const float2 (&v)[kPairs]) const {
-        if (!there()) return;
+    // Rounds each value once, to nearest even, into the present row.  A ragged row's
+    // first and last chunk go to shared memory (`edges`: two chunks a row of a warp), from
+    // where the row's lanes write an element each.
+    __device__ void store(char *base, uint32_t edges, const float2 (&v)[kPairs]) const {
+        const int lane = threadIdx.x & 31, team = kMulti ? 0 : lane / kTeam;
+        const uint32_t edge = edges + ((threadIdx.x >> 5) * 4 + team) * 32;
+        const bool is_there = there();
+        bool has_first = false, has_last = false;
+        if (!kWhole) __syncwarp();   // the edges' last readers
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             char *p = base + at + c * column_threads() * 16;
@@ -254,20 +267,46 @@ struct Place {
                 else
                     set_word(q, i, E::from_f2(v[c * 4 + i].x, v[c * 4 + i].y));
             }
-            if (kWhole ? held(c) : full(c) && a.together) {
-                st_stream(p, q);
-            } else if (!kWhole && held(c)) {
-                const int first = -column(c), end = a.width - column(c);
+            if constexpr (kWhole) {
+                if (is_there && held(c)) st_stream(p, q);
+            } else if (!a.together) {
 #pragma unroll
-                for (int j = 0; j < kV; ++j) {
-                    if (j < first || j >= end) continue;
-                    if constexpr (kV == 4)
-                        *reinterpret_cast<uint32_t *>(p + 4 * j) = word(q, j);
-                    else
-                        *reinterpret_cast<uint16_t *>(p + 2 * j) = static_cast<uint16_t>(word(q, j / 2) >> (j & 1) * 16);
-                }
+                for (int j = 0; j < kV; ++j)
+                    if (is_there && column(c) + j < a.width) put(p, j, word(q, j * kBytes<E> / 4));
+            } else if (full(c)) {
+                if (is_there) st_stream(p, q);
+            } else if (held(c)) {
+                const bool is_first = column(c) < 0;
+                store_shared(edge + (is_first ? 0 : 16), q);
+                (is_first ? has_first : has_last) = true;
             }
         }
+        if (kWhole || !a.together) return;
+        const unsigned firsts = __ballot_sync(0xffffffffu, has_first), lasts = __ballot_sync(0xffffffffu, has_last);
+        __syncwarp();
+        const unsigned team_lanes = kMulti || kTeam == 32 ? 0xffffffffu : ((1u << (kTeam & 31)) - 1) << (team * kTeam & 31);
+        const int j = kMulti ? lane : lane & (kTeam - 1);
+        if (j >= kV || !is_there) return;
+        char *row_at = base + at - column_thread() * 16;     // the row's first chunk
+        if (firsts & team_lanes) {
+            const int col = j - lead;
+            if (col >= 0 && col < a.width) put(row_at, j, element(edge, j));
+        }
+        if (lasts & team_lanes) {
+            const int first = (lead + a.width) / kV * kV;     // of the last chunk
+            if (first + j - lead < a.width) put(row_at + first * kBytes<E>, j, element(edge + 16, j));
+        }
+    }
+    __device__ static void put(char *p, int j, uint32_t w) {
+        if constexpr (kV == 4)
+            *reinterpret_cast<uint32_t *>(p + 4 * j) = w;
+        else
+            *reinterpret_cast<uint16_t *>(p + 2 * j) = static_cast<uint16_t>(w >> (j & 1) * 16);
+    }
+    __device__ static uint32_t element(uint32_t chunk_at, int j) {
+        uint32_t w;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(chunk_at + j * kBytes<E> / 4 * 4) : "memory");
+        return w;
     }
 
     // A value of every column in shared memory as the threads hold columns, zeros

@@ -21,12 +21,15 @@ template <typename E, int kC, int kTeam, bool kWhole>
 __global__ void __launch_bounds__(kThreads, 1) layer_norm_backward(const LayerNormArgs a) {
     extern __shared__ __align__(16) char shared[];
     __shared__ float2 exchange[2][kWarps];
+    __shared__ __align__(16) char edge_bytes[kWhole ? 16 : kEdgeBytes];
     using P = Place<E, kC, kTeam, kWhole>;
     constexpr int kPairs = P::kPairs, kHalf = P::kHalf;
     P p(a, exchange, shared_address(shared + a.kept_bytes));
     float *weight = reinterpret_cast<float *>(shared);
     char *mask_words = reinterpret_cast<char *>(weight + p.capacity() * P::kV);
     const uint32_t masks = shared_address(mask_words);
+    const uint32_t edges = shared_address(edge_bytes);
+    p.clear_slots();
     pdl_prologue();
     for (int s = 0; s < a.stages; ++s) p.fetch();
     // the statistics of two passes ahead
@@ -74,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_norm_backward(const LayerNo
             for (int i = 0; i < kPairs; ++i) g[i] = add2(g[i], h[i]);
         }
         p.fetch();
-        p.store(a.out, g);
+        p.store(a.out, edges, g);
         now = next, next = later;
     }
     if (!a.part) return;
@@ -158,7 +161,7 @@ wgs_status run_unit(LayerNormArgs a, cudaStream_t stream, int *blocks) {
     auto kernel = layer_norm_backward<E, kC, kTeam, kWhole>;
     // As the forward's.  (At most 66 KB beside a stage of six chunks from three
     // tensors, 108 KB, and 48 KB beside 168 KB of others.)
-    if (smem > 47 << 10 &&
+    if (smem > 45 << 10 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 216 << 10) != cudaSuccess) {
         cudaGetLastError();
         return WGS_ERR_LAUNCH;
