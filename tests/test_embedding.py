@@ -187,7 +187,8 @@ def test_gradient(shape, fmt, tfmt, kind):
                                         ((131040, 32768, 64), "one"), ((300001, 77777, 33), "skew"),
                                         ((262145, 1, 8), "one"), ((700000, 500, 4), "uniform"),
                                         ((3000000, 2 ** 21, 2), "uniform"), ((262144, 2 ** 18, 16), "once"),
-                                        ((131072, 2 ** 17 - 1, 24), "runs")], ids=str)
+                                        ((131072, 2 ** 17 - 1, 24), "runs"), ((9000000, 2 ** 28, 1), "skew"),
+                                        ((8500000, 3000, 2), "uniform")], ids=str)
 @pytest.mark.parametrize("fmt,tfmt", [("f32", "f32"), ("f16", "f16"), ("bf16", "f32")])
 def test_gradient_of_many_indices(shape, kind, fmt, tfmt):
     n, rows, width = shape
@@ -197,7 +198,7 @@ def test_gradient_of_many_indices(shape, kind, fmt, tfmt):
     got = wgs.embedding_bwd(grad, idx, rows, 0.5, DT[tfmt])
     _check_gradient(grad, idx, rows, 0.5, got)
     assert torch.equal(_bits(got), _bits(wgs.embedding_bwd(grad, idx, rows, 0.5, DT[tfmt])))
-    # |sum| <= 2 * 3000000 < 2^24
+    # a row gets at most half a million terms of at most 2: sums below 2^24
     whole = torch.randint(-2, 3, (n, width), generator=gen, device=DEV).to(DT[fmt])
     want = torch.zeros(rows, width, dtype=torch.float64, device=DEV)
     want.index_add_(0, idx[idx >= 0].long(), whole[idx >= 0].double())

@@ -14,8 +14,6 @@
 // rows, writes those that end inside it, and leaves what reaches over its ends to
 // a last launch, which adds a run's pieces up.  So the work is even if one row has
 // most of the indices, and the order of additions is fixed.
-#include <cooperative_groups.h>
-
 #include <type_traits>
 
 #include "wgs_common.cuh"
@@ -23,8 +21,6 @@
 namespace wgs {
 
 namespace {
-
-namespace cg = cooperative_groups;
 
 // Set (never cleared by a kernel) when an index lies outside [-1, n_rows); read
 // and cleared by wgs_check_error.
@@ -126,25 +122,62 @@ __global__ void __launch_bounds__(kLookupThreads) embedding_lookup(const char *t
     }
 }
 
+// Zeros over n bytes at p; `unit` bytes of an element divide both.
+__device__ void write_zeros(char *p, int64_t n, int unit, int64_t thread, int64_t threads) {
+    int64_t lead = (16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15;
+    if (lead > n) lead = n;
+    const int64_t whole = (n - lead) / 16, rest = n - lead - whole * 16;
+    for (int64_t i = thread; i < whole; i += threads) st_stream(p + lead + 16 * i, make_uint4(0u, 0u, 0u, 0u));
+    if (thread < 16) {
+        const int64_t i = thread * unit;
+        char *end = p + lead + whole * 16;
+        for (int side = 0; side < 2; ++side) {
+            char *q = side ? end : p;
+            if (i >= (side ? rest : lead)) continue;
+            if (unit == 4)
+                *reinterpret_cast<uint32_t *>(q + i) = 0u;
+            else
+                *reinterpret_cast<uint16_t *>(q + i) = 0;
+        }
+    }
+}
+
 // -------------------------------------------------------------------- sort --
 
-// A stable counting sort by digits of at most 8 bits, from the lowest.  A block
-// counts the digits of its own range, the counts are summed up over the blocks
-// before it, and it places its range's indices behind those.
-constexpr int kBins = 256;
-constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32;
-constexpr int kSortTile = 4096;        // indices a block ranks at a time
-constexpr int kSortBlocks = 608;       // at most
+// A stable counting sort by digits of up to 9 bits, from the lowest, a launch a
+// pass and one before the first: each is bound by the time that a launch and a few
+// dependent reads take, so the fewer the better.  A block has a range of the order
+// so far; it adds up all blocks' counts of every digit, to know where its own
+// indices of each go, ranks them, and lays them into shared memory in their order,
+// from where runs of a digit leave side by side.  As it knows where an index goes, it
+// counts it there for the next pass too (whole numbers, so the order of these
+// atomics does not matter).  Each launch has blocks besides that write a share of
+// the table's gradient's zeros.
+//
+// A warp ranks 32 indices at a time: lanes set their bits in a word of their digit
+// and read it back.  (Measured for 8190 indices an SM: 3.0 to 4.0 thousand cycles, 10
+// with a ballot for every bit of the digit, 16 with match.any.)  One cluster of 16
+// blocks with its barriers in place of launches was slower, 35 us for two passes
+// over 131040 indices: 16 SMs rank and place longer than launches take.
+constexpr int kBins = 512;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+constexpr int kRounds = 4;             // indices of a thread at a time
+constexpr int kSortTile = kSortThreads * kRounds;
+constexpr int kSortBlocks = 128;       // at most
 
 struct SortArgs {
     const int32_t *idx;          // first pass: the call's indices
     const int32_t *keys, *at;    // later passes: sorted by the lower digits
     int32_t *keys_out, *at_out;
-    int32_t *counts;             // [bins][blocks]
-    int32_t *totals;             // [bins]
+    void *counts, *next;         // [bins][stride], of this pass and the next
     int64_t n, range;            // indices; of a block
+    int64_t clear_words;         // from next on, cleared by the first launch
     int32_t n_rows;
-    int shift, bits, blocks;
+    int shift, bits, blocks, stride;
+    bool last;
+    char *zeros;                 // to be written as such by the blocks behind `blocks`
+    int64_t zero_bytes;
+    int zero_unit;
 };
 
 // The row that index i names; n_rows, sorted behind all, for none.
@@ -154,257 +187,157 @@ __device__ __forceinline__ int32_t key_of(const SortArgs &a, int64_t i) {
     return k >= 0 && k < a.n_rows ? k : a.n_rows;
 }
 
+__device__ __forceinline__ bool zeros_instead(const SortArgs &a) {
+    const int block = static_cast<int>(blockIdx.x) - a.blocks;
+    if (block < 0) return false;
+    write_zeros(a.zeros, a.zero_bytes, a.zero_unit, static_cast<int64_t>(block) * kSortThreads + threadIdx.x,
+                static_cast<int64_t>(gridDim.x - a.blocks) * kSortThreads);
+    return true;
+}
+
+// The first pass's counts, zeros in the others', and the indices' check.  C: of a
+// count, 16 bits where a block's range allows.
+template <typename C>
 __global__ void __launch_bounds__(kSortThreads) sort_count(const SortArgs a) {
     __shared__ int32_t count[kBins];
     pdl_prologue();
+    if (zeros_instead(a)) return;
     count[threadIdx.x] = 0;
     __syncthreads();
     const int64_t first = blockIdx.x * a.range, end = first + a.range < a.n ? first + a.range : a.n;
     const uint32_t mask = (1u << a.bits) - 1;
+    bool bad = false;
+#pragma unroll 4
     for (int64_t i = first + threadIdx.x; i < end; i += kSortThreads) {
-        if (a.idx) {
-            const int32_t k = __ldg(a.idx + i);
-            if (k < -1 || k >= a.n_rows) atomicOr(&g_embedding_error, 1u);
-        }
-        atomicAdd(&count[static_cast<uint32_t>(key_of(a, i)) >> a.shift & mask], 1);
+        const int32_t k = __ldg(a.idx + i);
+        bad |= k < -1 || k >= a.n_rows;
+        atomicAdd(&count[static_cast<uint32_t>(k >= 0 && k < a.n_rows ? k : a.n_rows) & mask], 1);
     }
+    if (bad) atomicOr(&g_embedding_error, 1u);
     __syncthreads();
-    if (threadIdx.x <= mask) a.counts[static_cast<int64_t>(threadIdx.x) * a.blocks + blockIdx.x] = count[threadIdx.x];
+    static_cast<C *>(a.counts)[threadIdx.x * a.stride + blockIdx.x] = static_cast<C>(count[threadIdx.x]);
+    for (int64_t i = blockIdx.x * kSortThreads + threadIdx.x; i < a.clear_words; i += a.blocks * kSortThreads)
+        static_cast<uint32_t *>(a.next)[i] = 0u;
 }
 
-// Sum of v over the threads before this one, of a block of kSortThreads; *total
-// of all.
-__device__ __forceinline__ int32_t scan_before(int32_t v, int32_t *warp_sums, int32_t *total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int32_t s = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int32_t u = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += u;
-    }
-    __syncthreads();   // warp_sums' last readers
-    if (lane == 31) warp_sums[warp] = s;
-    __syncthreads();
-    int32_t before = 0, all = 0;
-    for (int w = 0; w < kSortWarps; ++w) {
-        if (w < warp) before += warp_sums[w];
-        all += warp_sums[w];
-    }
-    *total = all;
-    return before + s - v;
-}
-
-// A digit's counts become the sums over the blocks before.
-__global__ void __launch_bounds__(kSortThreads) sort_scan(int32_t *counts, int32_t *totals, int blocks) {
-    __shared__ int32_t warp_sums[kSortWarps];
-    pdl_prologue();
-    int32_t *mine = counts + static_cast<int64_t>(blockIdx.x) * blocks;
-    int32_t run = 0;
-    for (int b0 = 0; b0 < blocks; b0 += kSortThreads) {
-        const int b = b0 + threadIdx.x;
-        int32_t total;
-        const int32_t before = scan_before(b < blocks ? mine[b] : 0, warp_sums, &total);
-        if (b < blocks) mine[b] = run + before;
-        run += total;
-    }
-    if (threadIdx.x == 0) totals[blockIdx.x] = run;
-}
-
+template <typename C>
 __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs a) {
-    __shared__ int32_t base[kBins], warp_base[kSortWarps][kBins], warp_sums[kSortWarps];
-    pdl_prologue();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t mask = (1u << a.bits) - 1;
-    const bool digit = threadIdx.x <= mask;
-    int32_t total;
-    const int32_t lower = scan_before(digit ? a.totals[threadIdx.x] : 0, warp_sums, &total);
-    base[threadIdx.x] = lower + (digit ? a.counts[static_cast<int64_t>(threadIdx.x) * a.blocks + blockIdx.x] : 0);
-    const int64_t first = blockIdx.x * a.range, end = first + a.range < a.n ? first + a.range : a.n;
-    constexpr int kEach = kSortTile / kSortThreads;   // of a lane
-    for (int64_t tile = first; tile < end; tile += kSortTile) {
-        for (int w = 0; w < kSortWarps; ++w) warp_base[w][threadIdx.x] = 0;
-        __syncthreads();
-        const int64_t mine = tile + warp * (kSortTile / kSortWarps) + lane;
-        int32_t key[kEach];
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-            const int64_t i = mine + 32 * j;
-            key[j] = i < end ? key_of(a, i) : 0;
-            if (i < end) atomicAdd(&warp_base[warp][static_cast<uint32_t>(key[j]) >> a.shift & mask], 1);
-        }
-        __syncthreads();
-        int32_t run = base[threadIdx.x];
-        for (int w = 0; w < kSortWarps; ++w) {
-            const int32_t c = warp_base[w][threadIdx.x];
-            warp_base[w][threadIdx.x] = run;
-            run += c;
-        }
-        base[threadIdx.x] = run;
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-            const int64_t i = mine + 32 * j;
-            const uint32_t d = static_cast<uint32_t>(key[j]) >> a.shift & mask;
-            const unsigned same = __match_any_sync(0xffffffffu, i < end ? d : 0xffffffffu);
-            const int rank = __popc(same & ((1u << lane) - 1));
-            const int32_t to = warp_base[warp][d] + rank;
-            __syncwarp();
-            if (i < end) {
-                if (rank == 0) warp_base[warp][d] += __popc(same);
-                a.keys_out[to] = key[j];
-                a.at_out[to] = a.idx ? static_cast<int32_t>(i) : __ldcg(a.at + i);
-            }
-            __syncwarp();
-        }
-        __syncthreads();
-    }
-}
-
-// The same sort in one cluster of blocks, for as many indices as its registers and
-// shared memory hold: a pass counts, exchanges the blocks' counts over distributed
-// shared memory and places the indices there, behind cluster barriers instead of
-// launches.  Digits have up to 9 bits, so two passes sort 2^18 rows.  Measured at
-// 131040 indices into 32768 rows: 152 us for the whole gradient with six launches
-// that sort, see below for what is left.  The grid's other clusters write the
-// table's gradient's zeros meanwhile, which the sort leaves the memory idle for.
-constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
-constexpr int kRounds = 12;            // indices of a thread, at most
-constexpr int kMostCluster = 16;
-constexpr int kMostClustered = kMostCluster * kRounds * kClusterThreads;
-constexpr int kClusterBins = 512;
-
-struct ClusterArgs {
-    SortArgs s;
-    int passes, tile, cluster;   // tile: indices of a block
-    uint32_t magic;              // 2^32 / tile, rounded up
-    char *zeros;                 // to be written as such
-    int64_t zero_bytes;
-    int zero_unit;               // bytes that its start and length are multiples of
-};
-
-__device__ void write_zeros(char *p, int64_t n, int bytes, int64_t thread, int64_t threads) {
-    int64_t lead = (16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15;
-    if (lead > n) lead = n;
-    const int64_t whole = (n - lead) / 16, rest = n - lead - whole * 16;
-    for (int64_t i = thread; i < whole; i += threads) st_stream(p + lead + 16 * i, make_uint4(0u, 0u, 0u, 0u));
-    if (thread < 16) {
-        const int64_t i = thread * bytes;
-        char *end = p + lead + whole * 16;
-        for (int side = 0; side < 2; ++side) {
-            char *q = side ? end : p;
-            if (i >= (side ? rest : lead)) continue;
-            if (bytes == 4)
-                *reinterpret_cast<uint32_t *>(q + i) = 0u;
-            else
-                *reinterpret_cast<uint16_t *>(q + i) = 0;
-        }
-    }
-}
-
-__global__ void __launch_bounds__(kClusterThreads, 1) sort_in_cluster(const ClusterArgs a) {
     extern __shared__ __align__(16) char shared[];
-    __shared__ int32_t total[kClusterBins], base[kClusterBins], warp_sums[kClusterWarps];
-    const SortArgs &s = a.s;
-    uint2 *pairs = reinterpret_cast<uint2 *>(shared);                       // [tile]: row, position
-    uint16_t *counts = reinterpret_cast<uint16_t *>(pairs + a.tile);        // [warps][bins]
+    uint2 *pairs = reinterpret_cast<uint2 *>(shared);                          // [tile]: row, position
+    uint32_t *same_digit = reinterpret_cast<uint32_t *>(pairs + kSortTile);    // [warps][bins]: lanes
+    uint32_t *warp_count = same_digit + kSortWarps * kBins;                    // [warps][bins]
+    __shared__ int32_t to_base[kBins], warp_sums[kSortWarps];
+    __shared__ uint32_t local_base[kBins];
     pdl_prologue();
-    if (static_cast<int>(blockIdx.x) >= a.cluster) {
-        const int64_t blocks = gridDim.x - a.cluster, block = blockIdx.x - a.cluster;
-        write_zeros(a.zeros, a.zero_bytes, a.zero_unit, block * kClusterThreads + threadIdx.x, blocks * kClusterThreads);
-        return;
-    }
-    cg::cluster_group cluster = cg::this_cluster();
-    const int me = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int bins = 1 << s.bits, rounds = a.tile / kClusterThreads;
-    const uint32_t mask = bins - 1, lower = (1u << lane) - 1;
-    uint16_t *mine = counts + warp * bins;
-    const int here = warp * rounds * 32 + lane, n_here = static_cast<int>(s.n) - me * a.tile;   // valid below n_here
-    uint32_t key[kRounds], at[kRounds], rank[kRounds];
+    if (zeros_instead(a)) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = blockIdx.x, bin = threadIdx.x;
+    const uint32_t mask = (1u << a.bits) - 1, lower = (1u << lane) - 1;
+    uint32_t *lanes = same_digit + warp * kBins, *mine = warp_count + warp * kBins;
+    for (int i = lane; i < kBins; i += 32) lanes[i] = 0u;
+
+    // Exclusive sums over the threads' values, in the threads' order.
+    auto scan = [&](int32_t v) {
+        int32_t s = v;
 #pragma unroll
-    for (int j = 0; j < kRounds; ++j) {
-        const int i = here + 32 * j;
-        key[j] = 0;
-        if (j < rounds && i < n_here) {
-            at[j] = static_cast<uint32_t>(me * a.tile + i);
-            const int32_t k = __ldg(s.idx + at[j]);
-            key[j] = static_cast<uint32_t>(k >= 0 && k < s.n_rows ? k : s.n_rows);
-            if (k < -1 || k >= s.n_rows) atomicOr(&g_embedding_error, 1u);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t u = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += u;
         }
+        __syncthreads();   // warp_sums' last readers
+        if (lane == 31) warp_sums[warp] = s;
+        __syncthreads();
+        int32_t before = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) before += w < warp ? warp_sums[w] : 0;
+        return before + s - v;
+    };
+
+    // Where this block's indices of digit `bin` go: behind all of lower digits and
+    // those of the blocks before.
+    {
+        int32_t all = 0, before = 0;
+        if (bin <= static_cast<int>(mask)) {
+            constexpr int kEach = 16 / sizeof(C);
+            const uint4 *row = reinterpret_cast<const uint4 *>(static_cast<const C *>(a.counts) + bin * a.stride);
+#pragma unroll
+            for (int g = 0; g < kSortBlocks / kEach; ++g) {
+                if (kEach * g >= a.blocks) break;
+                const uint4 q = __ldcg(row + g);
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) {
+                    const int b = kEach * g + j;
+                    const int32_t c = sizeof(C) == 4 ? word(q, j) : word(q, j / 2) >> 16 * (j & 1) & 0xffff;
+                    all += b < a.blocks ? c : 0;
+                    before += b < me ? c : 0;
+                }
+            }
+        }
+        to_base[bin] = scan(all) + before;
     }
-    for (int pass = 0; pass < a.passes; ++pass) {
-        const int shift = pass * s.bits;
-        for (int i = lane; i < bins / 2; i += 32) reinterpret_cast<uint32_t *>(mine)[i] = 0u;
+    const int64_t first = me * a.range, end = first + a.range < a.n ? first + a.range : a.n;
+    for (int64_t tile = first; tile < end; tile += kSortTile) {
+        for (int i = lane; i < kBins; i += 32) mine[i] = 0u;
         __syncwarp();
+        const int here = warp * 32 * kRounds + lane;
+        const int n_here = static_cast<int>(end - tile < kSortTile ? end - tile : kSortTile);
+        uint32_t key[kRounds], at[kRounds], rank[kRounds];
 #pragma unroll
         for (int j = 0; j < kRounds; ++j) {
-            if (j >= rounds) break;
+            const int64_t i = tile + here + 32 * j;
+            key[j] = at[j] = 0u;
+            if (here + 32 * j < n_here) {
+                key[j] = static_cast<uint32_t>(key_of(a, i));
+                at[j] = a.idx ? static_cast<uint32_t>(i) : static_cast<uint32_t>(__ldcg(a.at + i));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kRounds; ++j) {
             const bool valid = here + 32 * j < n_here;
-            const uint32_t d = key[j] >> shift & mask;
-            const unsigned same = __match_any_sync(0xffffffffu, valid ? d : 0xffffffffu);
-            const uint32_t before = __popc(same & lower), had = mine[d];
+            const uint32_t d = key[j] >> a.shift & mask;
+            if (valid) atomicOr(&lanes[d], 1u << lane);
             __syncwarp();
-            if (valid && before == 0) mine[d] = static_cast<uint16_t>(had + __popc(same));
+            const uint32_t same = lanes[d], had = mine[d], before = __popc(same & lower);
+            __syncwarp();
+            if (valid && before == 0) lanes[d] = 0u, mine[d] = had + __popc(same);
             __syncwarp();
             rank[j] = had + before;
         }
         __syncthreads();
-        const int d = threadIdx.x;
-        if (d < bins) {
-            uint32_t run = 0;
-#pragma unroll 8
-            for (int w = 0; w < kClusterWarps; ++w) {
-                const uint32_t c = counts[w * bins + d];
-                counts[w * bins + d] = static_cast<uint16_t>(run);
-                run += c;
-            }
-            total[d] = static_cast<int32_t>(run);
-        }
-        cluster.sync();
-        // all blocks hold their indices in registers from here on
-        int32_t all = 0, before = 0;
-        if (d < bins) {
-#pragma unroll 4
-            for (int b = 0; b < a.cluster; ++b) {
-                const int32_t c = *cluster.map_shared_rank(&total[d], b);
-                all += c;
-                if (b < me) before += c;
-            }
-        }
-        int32_t sum = all;
+        // counts of the warps before, and of the digits before: places in the tile
+        uint32_t run = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t u = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += u;
+        for (int w = 0; w < kSortWarps; ++w) {
+            const uint32_t c = warp_count[w * kBins + bin];
+            warp_count[w * kBins + bin] = run;
+            run += c;
         }
-        if (lane == 31) warp_sums[warp] = sum;
-        __syncthreads();
-        if (d < bins) {
-            for (int w = 0; w < warp; ++w) before += warp_sums[w];
-            base[d] = before + sum - all;
-        }
+        local_base[bin] = static_cast<uint32_t>(scan(static_cast<int32_t>(run)));
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kRounds; ++j) {
-            if (j >= rounds) break;
             if (here + 32 * j >= n_here) continue;
-            const uint32_t digit = key[j] >> shift & mask;
-            const uint32_t to = base[digit] + mine[digit] + rank[j];
-            if (pass + 1 == a.passes) {
-                s.keys_out[to] = static_cast<int32_t>(key[j]);
-                s.at_out[to] = static_cast<int32_t>(at[j]);
-            } else {
-                const uint32_t block = a.cluster == 1 ? 0 : __umulhi(to, a.magic);
-                *cluster.map_shared_rank(&pairs[to - block * a.tile], block) = make_uint2(key[j], at[j]);
+            const uint32_t d = key[j] >> a.shift & mask;
+            pairs[local_base[d] + mine[d] + rank[j]] = make_uint2(key[j], at[j]);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < n_here; i += kSortThreads) {
+            const uint2 v = pairs[i];
+            const uint32_t d = v.x >> a.shift & mask;
+            const int64_t to = to_base[d] + (i - static_cast<int>(local_base[d]));
+            a.keys_out[to] = static_cast<int32_t>(v.x);
+            a.at_out[to] = static_cast<int32_t>(v.y);
+            if (!a.last) {
+                const uint32_t place = (v.x >> (a.shift + a.bits) & mask) * a.stride +
+                                       static_cast<uint32_t>(to) / static_cast<uint32_t>(a.range);
+                if constexpr (sizeof(C) == 4)
+                    atomicAdd(static_cast<uint32_t *>(a.next) + place, 1u);
+                else
+                    atomicAdd(static_cast<uint32_t *>(a.next) + place / 2, 1u << 16 * (place & 1));
             }
         }
-        cluster.sync();
-        if (pass + 1 == a.passes) break;
-#pragma unroll
-        for (int j = 0; j < kRounds; ++j) {
-            const int i = here + 32 * j;
-            if (j >= rounds) break;
-            if (i < n_here) key[j] = pairs[i].x, at[j] = pairs[i].y;
-        }
+        __syncthreads();
+        to_base[bin] += static_cast<int32_t>(run);
+        __syncthreads();
     }
 }
 
@@ -608,17 +541,18 @@ __global__ void __launch_bounds__(kSumThreads) sum_runs(const SumArgs a) {
 }
 
 // Runs that go over the end of the piece they began in: the sums of the pieces that
-// each reaches into.  A block looks through some of the pieces for such beginnings
-// and takes their runs one after another; its groups of blockDim.x threads add every
-// groups-th piece's sums, and then the groups'.
-constexpr int kJoinThreads = 1024;
+// each reaches into.  A block looks through some of the pieces for such beginnings.
+// A run of a few pieces is a warp's, 128 columns at a time; a long one the block's,
+// whose groups of threads add every groups-th piece's sums, and then the groups'.
+constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
+constexpr int kLongRun = 24;           // pieces behind the first
 
 template <typename P>
 __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a) {
     __shared__ float sums[kJoinThreads];
-    __shared__ int found[kJoinThreads], n_found;
+    __shared__ int found[kJoinThreads], pieces[kJoinThreads], n_found;
     pdl_prologue();
-    const int thread = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
+    const int thread = threadIdx.x, lane = thread & 31, warp = thread >> 5;
     // does the run of piece c's last index go on into the next, having begun in c?
     auto begins = [&](int64_t c) {
         const int64_t end = (c + 1) * a.piece;
@@ -627,35 +561,70 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a) {
         const int32_t before = c > 0 ? __ldcg(a.keys + c * a.piece - 1) : a.n_rows;
         return k < a.n_rows && last == k && before != k;
     };
-    for (int64_t round = 0; round * threads * gridDim.x < a.pieces; ++round) {
+    for (int64_t round = 0; round * kJoinThreads * gridDim.x < a.pieces; ++round) {
         if (thread == 0) n_found = 0;
         __syncthreads();
-        const int64_t c = (round * threads + thread) * gridDim.x + blockIdx.x;
+        const int64_t c = (round * kJoinThreads + thread) * gridDim.x + blockIdx.x;
         if (begins(c)) found[atomicAdd(&n_found, 1)] = static_cast<int>(c);
         __syncthreads();
         const int runs = n_found;
-        for (int f = 0; f < runs; ++f) {
+        // pieces behind the first that each run reaches into
+        for (int f = warp; f < runs; f += kJoinWarps) {
             const int64_t c0 = found[f];
             const int32_t k = __ldcg(a.keys + (c0 + 1) * a.piece);
-            int64_t more = 1;       // pieces behind c0 that the run reaches into
+            int more = 1;
             for (;;) {
-                const int64_t next = (c0 + more + 1 + thread) * a.piece;
-                const int on = __syncthreads_count(next < a.n && __ldcg(a.keys + (next < a.n ? next : 0)) == k);
+                const int64_t next = (c0 + more + 1 + lane) * a.piece;
+                const int on = __popc(__ballot_sync(0xffffffffu, next < a.n && __ldcg(a.keys + (next < a.n ? next : 0)) == k));
                 more += on;
-                if (on < threads) break;
+                if (on < 32) break;
             }
-            for (int col = threadIdx.x; col - static_cast<int>(threadIdx.x) < a.width; col += blockDim.x) {
+            if (lane == 0) pieces[f] = more;
+        }
+        __syncthreads();
+        const int blocks = (a.width + 127) / 128;
+        for (int t = warp; t < runs * blocks; t += kJoinWarps) {
+            const int f = t / blocks, more = pieces[f];
+            if (more > kLongRun) continue;
+            const int64_t c0 = found[f];
+            const int32_t k = __ldcg(a.keys + (c0 + 1) * a.piece);
+            const int col = (t - f * blocks) * 128 + lane;
+            const float *part = a.part + c0 * 2 * a.width + col;
+            float s[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] = col + 32 * i < a.width ? __ldcg(part + a.width + 32 * i) : 0.f;
+#pragma unroll 4
+            for (int p = 1; p <= more; ++p) {
+                part += 2 * a.width;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (col + 32 * i < a.width) s[i] += __ldcg(part + 32 * i);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (col + 32 * i < a.width) write_one<P>(a.out, k * static_cast<int64_t>(a.width) + col + 32 * i, s[i] * a.scale);
+        }
+        // a group: as many warps as a row's columns take, at most a quarter of the block
+        const int wide = a.width >= 256 ? 256 : (a.width + 31) / 32 * 32, groups = kJoinThreads / wide;
+        const int group = thread / wide, lead = thread - group * wide;
+        for (int f = 0; f < runs; ++f) {
+            const int more = pieces[f];
+            if (more <= kLongRun) continue;
+            const int64_t c0 = found[f];
+            const int32_t k = __ldcg(a.keys + (c0 + 1) * a.piece);
+            for (int at = 0; at < a.width; at += wide) {
+                const int col = at + lead;
                 float s = 0.f;
-                if (col < a.width) {
+                if (col < a.width && group < groups) {
                     const float *part = a.part + c0 * 2 * a.width + col;
-                    if (threadIdx.y == 0) s = __ldcg(part + a.width);
+                    if (group == 0) s = __ldcg(part + a.width);
 #pragma unroll 8
-                    for (int64_t p = 1 + threadIdx.y; p <= more; p += blockDim.y) s += __ldcg(part + p * 2 * a.width);
+                    for (int p = 1 + group; p <= more; p += groups) s += __ldcg(part + p * 2ll * a.width);
                 }
                 sums[thread] = s;
                 __syncthreads();
-                if (threadIdx.y == 0 && col < a.width) {
-                    for (int g = 1; g < static_cast<int>(blockDim.y); ++g) s += sums[g * blockDim.x + threadIdx.x];
+                if (group == 0 && col < a.width) {
+                    for (int g = 1; g < groups; ++g) s += sums[g * wide + lead];
                     write_one<P>(a.out, k * static_cast<int64_t>(a.width) + col, s * a.scale);
                 }
                 __syncthreads();
@@ -664,7 +633,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a) {
     }
 }
 
-// Zeros over n bytes at p; `bytes` of an element divide both.
 __global__ void __launch_bounds__(256) fill_zeros(char *p, int64_t n, int bytes) {
     pdl_prologue();
     write_zeros(p, n, bytes, static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, gridDim.x * 256ll);
@@ -681,14 +649,12 @@ bool sizes_ok(int64_t n_idx, int64_t n_rows) {
 
 // How a gradient is cut, and where its parts lie in the workspace.
 struct Plan {
-    bool clustered;
-    int passes, bits;             // of the sort
-    int sort_blocks;              // of one in launches
+    int passes, bits, sort_blocks;   // of the sort
     int64_t range;
-    int cluster, tile;            // of one in a cluster
     int slices, cols, slots, each, piece;
     int64_t pieces;
-    int64_t keys[2], at[2], counts, totals, part, bytes;
+    int count_bytes, stride;         // of a count; blocks' counts of a digit
+    int64_t keys[2], at[2], counts, part, bytes;
 };
 
 // v: values of a thread
@@ -696,15 +662,13 @@ Plan plan_of(int64_t n, int64_t n_rows, int32_t width, int v) {
     Plan z = {};
     int bits = 1;
     while (bits < 31 && n_rows >> bits) ++bits;     // keys are 0 ... n_rows
-    z.clustered = n <= kMostClustered;
-    z.passes = static_cast<int>(ceil_div(bits, z.clustered ? 9 : 8));
+    z.passes = static_cast<int>(ceil_div(bits, 9));
     z.bits = static_cast<int>(ceil_div(bits, z.passes));
-    const int64_t tiles = ceil_div(n, kSortTile);
-    z.range = ceil_div(tiles, kSortBlocks) * kSortTile;
+    // whole rounds of a block's threads
+    z.range = ceil_div(ceil_div(n, kSortThreads), kSortBlocks) * kSortThreads;
     z.sort_blocks = n ? static_cast<int>(ceil_div(n, z.range)) : 0;
-    z.cluster = 1;
-    while (z.cluster < kMostCluster && z.cluster * kClusterThreads < n) z.cluster *= 2;
-    z.tile = static_cast<int>(ceil_div(ceil_div(n, z.cluster), kClusterThreads)) * kClusterThreads;
+    z.count_bytes = z.range < 65536 ? 2 : 4;
+    z.stride = (z.sort_blocks + 7) / 8 * 8;
     const int parts = static_cast<int>(ceil_div(width, v));
     z.slices = static_cast<int>(ceil_div(parts, kSumThreads));
     z.cols = static_cast<int>(ceil_div(parts, z.slices));
@@ -721,11 +685,10 @@ Plan plan_of(int64_t n, int64_t n_rows, int32_t width, int v) {
         at += (bytes + 15) / 16 * 16;
         return here;
     };
-    for (int i = 0; i < (z.clustered ? 1 : 2); ++i) z.keys[i] = place(4 * n), z.at[i] = place(4 * n);
-    if (!z.clustered) {
-        z.counts = place(4ll * kBins * z.sort_blocks);
-        z.totals = place(4 * kBins);
+    for (int i = 0; i < 2; ++i) {
+        if (i < z.passes) z.keys[i] = place(4 * n), z.at[i] = place(4 * n);
     }
+    z.counts = place(1ll * z.passes * kBins * z.stride * z.count_bytes);
     z.part = place(z.pieces * 8 * width);
     z.bytes = at;
     return z;
@@ -754,10 +717,8 @@ wgs_status run_sums(const SumArgs &a, const Plan &z, int sms, cudaStream_t strea
     const wgs_status st = launch(kernel, dim3(static_cast<unsigned>(z.pieces), z.slices), dim3(z.cols, z.slots),
                                  static_cast<size_t>(smem), stream, a);
     if (st != WGS_OK || z.pieces == 1) return st;
-    // threads for all columns, at least four groups of them where the rows are many
-    int cols = a.width < 256 ? static_cast<int>(ceil_div(a.width, 32)) * 32 : 256;
-    const int64_t blocks = z.pieces < 2 * sms ? z.pieces : 2 * sms;
-    return launch(join_runs<P>, dim3(static_cast<unsigned>(blocks)), dim3(cols, kJoinThreads / cols), 0, stream, a);
+    const int64_t blocks = z.pieces < sms ? z.pieces : sms;
+    return launch(join_runs<P>, dim3(static_cast<unsigned>(blocks)), dim3(kJoinThreads), 0, stream, a);
 }
 
 // 16 bytes of gradient at a time where all rows, and those of the output, start
@@ -772,50 +733,45 @@ wgs_status run_format(const SumArgs &a, const Plan &z, bool chunks, bool p32, in
     return p32 ? run_sums<E, F32, false>(a, z, sms, stream) : run_sums<E, E, false>(a, z, sms, stream);
 }
 
-// The sort in launches: three a pass.
-wgs_status sort_in_launches(SortArgs &s, const Plan &z, char *ws, cudaStream_t stream) {
-    s.range = z.range, s.blocks = z.sort_blocks, s.bits = z.bits;
-    s.counts = reinterpret_cast<int32_t *>(ws + z.counts), s.totals = reinterpret_cast<int32_t *>(ws + z.totals);
-    for (int p = 0; p < z.passes; ++p) {
-        wgs_status st;
-        s.shift = p * z.bits;
-        s.keys_out = reinterpret_cast<int32_t *>(ws + z.keys[p & 1]);
-        s.at_out = reinterpret_cast<int32_t *>(ws + z.at[p & 1]);
-        if ((st = launch(sort_count, dim3(s.blocks), dim3(kSortThreads), 0, stream, s)) != WGS_OK) return st;
-        if ((st = launch(sort_scan, dim3(1u << z.bits), dim3(kSortThreads), 0, stream, s.counts, s.totals,
-                         s.blocks)) != WGS_OK)
-            return st;
-        if ((st = launch(sort_place, dim3(s.blocks), dim3(kSortThreads), 0, stream, s)) != WGS_OK) return st;
-        s.idx = nullptr, s.keys = s.keys_out, s.at = s.at_out;
-    }
-    return WGS_OK;
-}
-
-// The sort in one cluster, with the zeros of `bytes` bytes at `out`.
-wgs_status sort_in_one_cluster(SortArgs &s, const Plan &z, char *ws, char *out, int64_t bytes, int unit,
-                               cudaStream_t stream) {
-    s.bits = z.bits;
-    s.keys_out = reinterpret_cast<int32_t *>(ws + z.keys[0]), s.at_out = reinterpret_cast<int32_t *>(ws + z.at[0]);
-    ClusterArgs c = {};
-    c.s = s, c.passes = z.passes, c.tile = z.tile, c.cluster = z.cluster;
-    c.magic = static_cast<uint32_t>(((1ull << 32) + z.tile - 1) / z.tile);
-    c.zeros = out, c.zero_bytes = bytes, c.zero_unit = unit;
-    // 64 bytes of zeros a thread, in whole clusters and up to 112 blocks
-    int64_t more = ceil_div(ceil_div(bytes, 64 * kClusterThreads), z.cluster);
-    if (more > 112 / z.cluster) more = 112 / z.cluster;
-    const int smem = z.tile * 8 + kClusterWarps * (2 << z.bits);
-    // As the layer norm's, and clusters beyond eight blocks need it too.
-    if ((smem > 43 << 10 &&
-         cudaFuncSetAttribute(sort_in_cluster, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kRounds * kClusterThreads * 8 + kClusterWarps * 2 * kClusterBins) != cudaSuccess) ||
-        (z.cluster > 8 && cudaFuncSetAttribute(sort_in_cluster, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-                              cudaSuccess)) {
+// Sorts s.idx; s.keys and s.at are the order.  Zeros go to `bytes` bytes at `out`.
+wgs_status sort_indices(SortArgs &s, const Plan &z, char *ws, char *out, int64_t bytes, int unit, int sms,
+                        cudaStream_t stream) {
+    s.range = z.range, s.blocks = z.sort_blocks, s.bits = z.bits, s.zero_unit = unit, s.stride = z.stride;
+    const int64_t counts = 1ll * kBins * z.stride * z.count_bytes;   // of a pass
+    auto count = z.count_bytes == 2 ? sort_count<uint16_t> : sort_count<uint32_t>;
+    auto order = z.count_bytes == 2 ? sort_place<uint16_t> : sort_place<uint32_t>;
+    // a share of the zeros in each launch, 64 bytes a thread or more
+    const int64_t share = ceil_div(ceil_div(bytes, 1 + z.passes), 16) * 16, most = 4 * sms - z.sort_blocks;
+    const int smem = kSortTile * 8 + kSortWarps * kBins * 8;
+    // (as the layer norm's)
+    if (cudaFuncSetAttribute(order, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         cudaGetLastError();
         return WGS_ERR_LAUNCH;
     }
-    s.keys = s.keys_out, s.at = s.at_out;
-    return launch_clusters(sort_in_cluster, dim3(static_cast<unsigned>(z.cluster * (1 + more))), dim3(kClusterThreads),
-                           z.cluster, static_cast<size_t>(smem), stream, c);
+    for (int p = -1; p < z.passes; ++p) {
+        s.zeros = out + (p + 1) * share;
+        s.zero_bytes = bytes - (p + 1) * share < share ? bytes - (p + 1) * share : share;
+        if (s.zero_bytes < 0) s.zero_bytes = 0;
+        int64_t more = ceil_div(s.zero_bytes, 64 * kSortThreads);
+        if (more > most) more = most;
+        const dim3 grid(static_cast<unsigned>(s.blocks + more));
+        const int q = p < 0 ? 0 : p;
+        s.shift = q * z.bits, s.last = q + 1 == z.passes;
+        s.counts = ws + z.counts + q * counts;
+        s.next = ws + z.counts + (q + 1) * counts;
+        s.clear_words = (z.passes - 1) * counts / 4;
+        wgs_status st;
+        if (p < 0) {
+            st = launch(count, grid, dim3(kSortThreads), 0, stream, s);
+        } else {
+            s.keys_out = reinterpret_cast<int32_t *>(ws + z.keys[p & 1]);
+            s.at_out = reinterpret_cast<int32_t *>(ws + z.at[p & 1]);
+            st = launch(order, grid, dim3(kSortThreads), static_cast<size_t>(smem), stream, s);
+            s.idx = nullptr, s.keys = s.keys_out, s.at = s.at_out;
+        }
+        if (st != WGS_OK) return st;
+    }
+    return WGS_OK;
 }
 
 template <typename T, typename E>
@@ -901,7 +857,7 @@ extern "C" wgs_status embedding_bwd(const void *grad, const int32_t *idx, void *
     if (st != WGS_OK) return st;
     const bool chunks = in_chunks(grad, grad_table, width, eb, tb);
     const Plan z = plan_of(n_idx, n_rows, width, static_cast<int>(16 / eb));
-    if (tbytes > 0 && (n_idx == 0 || !z.clustered)) {
+    if (tbytes > 0 && n_idx == 0) {
         const int64_t blocks = ceil_div(ceil_div(tbytes, 16), 256 * 8);
         const int64_t most = 8ll * dev.sm_count;
         st = launch(fill_zeros, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, stream,
@@ -911,8 +867,7 @@ extern "C" wgs_status embedding_bwd(const void *grad, const int32_t *idx, void *
     char *ws = static_cast<char *>(workspace);
     SortArgs s = {};
     s.idx = idx, s.n = n_idx, s.n_rows = static_cast<int32_t>(n_rows);
-    st = z.clustered ? sort_in_one_cluster(s, z, ws, static_cast<char *>(grad_table), tbytes, static_cast<int>(tb), stream)
-                     : sort_in_launches(s, z, ws, stream);
+    st = sort_indices(s, z, ws, static_cast<char *>(grad_table), tbytes, static_cast<int>(tb), dev.sm_count, stream);
     if (st != WGS_OK || n_rows == 0) return st;
     SumArgs a = {};
     a.grad = static_cast<const char *>(grad), a.keys = s.keys, a.at = s.at;
