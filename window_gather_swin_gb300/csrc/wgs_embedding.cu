@@ -163,17 +163,19 @@ constexpr int kBins = 512;
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 constexpr int kRounds = 4;             // indices of a thread at a time
 constexpr int kSortTile = kSortThreads * kRounds;
-constexpr int kSortBlocks = 128;       // at most
+// At most: every block reads all blocks' counts, so these cost the square.  131040
+// indices: KSORT
+constexpr int kSortBlocks = 64;
 
 struct SortArgs {
     const int32_t *idx;          // first pass: the call's indices
     const int32_t *keys, *at;    // later passes: sorted by the lower digits
     int32_t *keys_out, *at_out;
-    void *counts, *next;         // [bins][stride], of this pass and the next
+    void *counts, *next;         // [blocks][bins], of this pass and the next
     int64_t n, range;            // indices; of a block
     int64_t clear_words;         // from next on, cleared by the first launch
     int32_t n_rows;
-    int shift, bits, blocks, stride;
+    int shift, bits, blocks;
     bool last;
     char *zeros;                 // to be written as such by the blocks behind `blocks`
     int64_t zero_bytes;
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count(const SortArgs a) {
     }
     if (bad) atomicOr(&g_embedding_error, 1u);
     __syncthreads();
-    static_cast<C *>(a.counts)[threadIdx.x * a.stride + blockIdx.x] = static_cast<C>(count[threadIdx.x]);
+    if (threadIdx.x <= mask) static_cast<C *>(a.counts)[(blockIdx.x << a.bits) + threadIdx.x] = static_cast<C>(count[threadIdx.x]);
     for (int64_t i = blockIdx.x * kSortThreads + threadIdx.x; i < a.clear_words; i += a.blocks * kSortThreads)
         static_cast<uint32_t *>(a.next)[i] = 0u;
 }
@@ -231,9 +233,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs a) {
     pdl_prologue();
     if (zeros_instead(a)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = blockIdx.x, bin = threadIdx.x;
-    const uint32_t mask = (1u << a.bits) - 1, lower = (1u << lane) - 1;
+    const int bins = 1 << a.bits;
+    const uint32_t mask = bins - 1, lower = (1u << lane) - 1;
     uint32_t *lanes = same_digit + warp * kBins, *mine = warp_count + warp * kBins;
-    for (int i = lane; i < kBins; i += 32) lanes[i] = 0u;
+    for (int i = lane; i < bins; i += 32) lanes[i] = 0u;
 
     // Exclusive sums over the threads' values, in the threads' order.
     auto scan = [&](int32_t v) {
@@ -252,44 +255,76 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs a) {
         return before + s - v;
     };
 
-    // Where this block's indices of digit `bin` go: behind all of lower digits and
-    // those of the blocks before.
-    {
-        int32_t all = 0, before = 0;
-        if (bin <= static_cast<int>(mask)) {
-            constexpr int kEach = 16 / sizeof(C);
-            const uint4 *row = reinterpret_cast<const uint4 *>(static_cast<const C *>(a.counts) + bin * a.stride);
-#pragma unroll
-            for (int g = 0; g < kSortBlocks / kEach; ++g) {
-                if (kEach * g >= a.blocks) break;
-                const uint4 q = __ldcg(row + g);
-#pragma unroll
-                for (int j = 0; j < kEach; ++j) {
-                    const int b = kEach * g + j;
-                    const int32_t c = sizeof(C) == 4 ? word(q, j) : word(q, j / 2) >> 16 * (j & 1) & 0xffff;
-                    all += b < a.blocks ? c : 0;
-                    before += b < me ? c : 0;
-                }
-            }
-        }
-        to_base[bin] = scan(all) + before;
-    }
     const int64_t first = me * a.range, end = first + a.range < a.n ? first + a.range : a.n;
-    for (int64_t tile = first; tile < end; tile += kSortTile) {
-        for (int i = lane; i < kBins; i += 32) mine[i] = 0u;
-        __syncwarp();
-        const int here = warp * 32 * kRounds + lane;
-        const int n_here = static_cast<int>(end - tile < kSortTile ? end - tile : kSortTile);
-        uint32_t key[kRounds], at[kRounds], rank[kRounds];
+    const int here = warp * 32 * kRounds + lane;
+    uint32_t key[kRounds], at[kRounds];
+    auto load = [&](int64_t tile) {
 #pragma unroll
         for (int j = 0; j < kRounds; ++j) {
             const int64_t i = tile + here + 32 * j;
             key[j] = at[j] = 0u;
-            if (here + 32 * j < n_here) {
+            if (i < end) {
                 key[j] = static_cast<uint32_t>(key_of(a, i));
                 at[j] = a.idx ? static_cast<uint32_t>(i) : static_cast<uint32_t>(__ldcg(a.at + i));
             }
         }
+    };
+    load(first);
+
+    // Where this block's indices of digit `bin` go: behind all of lower digits and
+    // those of the blocks before.  Groups of threads each read some blocks' counts, 16
+    // bytes of digits a thread; the groups' sums meet in the ranks' tables.
+    {
+        constexpr int kEach = 16 / sizeof(C), kMostGroups = 16;
+        const int across = bins / kEach, groups = kSortThreads / across < kMostGroups ? kSortThreads / across : kMostGroups;
+        const int group = threadIdx.x / across, part = threadIdx.x - group * across;
+        const C *counts = static_cast<const C *>(a.counts) + part * kEach;
+        int32_t *sums = reinterpret_cast<int32_t *>(warp_count);       // [groups][2][bins]: at most the ranks' table
+        if (group < groups) {
+            int32_t all[kEach] = {}, before[kEach] = {};
+#pragma unroll 1
+            for (int from = group; from < a.blocks; from += 8 * groups) {
+                uint4 q[8];
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    const int b = from + g * groups;
+                    q[g] = b < a.blocks ? __ldcg(reinterpret_cast<const uint4 *>(counts + b * bins)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+#pragma unroll
+                    for (int j = 0; j < kEach; ++j) {
+                        const int32_t c = sizeof(C) == 4 ? word(q[g], j) : word(q[g], j / 2) >> 16 * (j & 1) & 0xffff;
+                        all[j] += c;
+                        before[j] += from + g * groups < me ? c : 0;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kEach; j += 4) {
+                *reinterpret_cast<int4 *>(sums + group * 2 * bins + part * kEach + j) =
+                    make_int4(all[j], all[j + 1], all[j + 2], all[j + 3]);
+                *reinterpret_cast<int4 *>(sums + (group * 2 + 1) * bins + part * kEach + j) =
+                    make_int4(before[j], before[j + 1], before[j + 2], before[j + 3]);
+            }
+        }
+        __syncthreads();
+        int32_t total = 0, mine_before = 0;
+        if (bin < bins) {
+#pragma unroll 8
+            for (int g = 0; g < groups; ++g) {
+                total += sums[g * 2 * bins + bin];
+                mine_before += sums[(g * 2 + 1) * bins + bin];
+            }
+        }
+        to_base[bin] = scan(total) + mine_before;      // (with a barrier, after which the table is free)
+    }
+    for (int64_t tile = first; tile < end; tile += kSortTile) {
+        for (int i = lane; i < bins; i += 32) mine[i] = 0u;
+        __syncwarp();
+        const int n_here = static_cast<int>(end - tile < kSortTile ? end - tile : kSortTile);
+        if (tile > first) load(tile);
+        uint32_t rank[kRounds];
 #pragma unroll
         for (int j = 0; j < kRounds; ++j) {
             const bool valid = here + 32 * j < n_here;
@@ -305,11 +340,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs a) {
         __syncthreads();
         // counts of the warps before, and of the digits before: places in the tile
         uint32_t run = 0;
+        if (bin < bins) {
 #pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) {
-            const uint32_t c = warp_count[w * kBins + bin];
-            warp_count[w * kBins + bin] = run;
-            run += c;
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t c = warp_count[w * kBins + bin];
+                warp_count[w * kBins + bin] = run;
+                run += c;
+            }
         }
         local_base[bin] = static_cast<uint32_t>(scan(static_cast<int32_t>(run)));
         __syncthreads();
@@ -327,8 +364,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs a) {
             a.keys_out[to] = static_cast<int32_t>(v.x);
             a.at_out[to] = static_cast<int32_t>(v.y);
             if (!a.last) {
-                const uint32_t place = (v.x >> (a.shift + a.bits) & mask) * a.stride +
-                                       static_cast<uint32_t>(to) / static_cast<uint32_t>(a.range);
+                const uint32_t place = static_cast<uint32_t>(to) / static_cast<uint32_t>(a.range) * bins +
+                                       (v.x >> (a.shift + a.bits) & mask);
                 if constexpr (sizeof(C) == 4)
                     atomicAdd(static_cast<uint32_t *>(a.next) + place, 1u);
                 else
@@ -345,6 +382,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs a) {
 
 constexpr int kSumThreads = 256;
 constexpr int kAhead = 6;              // rows that a thread has in flight
+// Of a block: the slots' ends are joined one after another.
+constexpr int kMostSlots = 32;
 constexpr int kMostPiece = 2048;       // indices of a block
 
 struct SumArgs {
@@ -544,12 +583,31 @@ __global__ void __launch_bounds__(kSumThreads) sum_runs(const SumArgs a) {
 // each reaches into.  A block looks through some of the pieces for such beginnings.
 // A run of a few pieces is a warp's, 128 columns at a time; a long one the block's,
 // whose groups of threads add every groups-th piece's sums, and then the groups'.
+__device__ __forceinline__ float4 plus(float4 a, float4 b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+// Four columns of row `row` of the pieces' sums.
+__device__ __forceinline__ float4 part_of(const SumArgs &a, int64_t row, int quad) {
+    const float *p = a.part + row * a.width + quad * 4;
+    if ((a.width & 3) == 0) return __ldcg(reinterpret_cast<const float4 *>(p));
+    const int left = a.width - quad * 4;
+    return make_float4(__ldcg(p), left > 1 ? __ldcg(p + 1) : 0.f, left > 2 ? __ldcg(p + 2) : 0.f, left > 3 ? __ldcg(p + 3) : 0.f);
+}
+template <typename P>
+__device__ __forceinline__ void write_quad(const SumArgs &a, int32_t k, int quad, float4 s) {
+    const int64_t at = k * static_cast<int64_t>(a.width) + quad * 4;
+    const int left = a.width - quad * 4;
+    write_one<P>(a.out, at, s.x * a.scale);
+    if (left > 1) write_one<P>(a.out, at + 1, s.y * a.scale);
+    if (left > 2) write_one<P>(a.out, at + 2, s.z * a.scale);
+    if (left > 3) write_one<P>(a.out, at + 3, s.w * a.scale);
+}
 constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
 constexpr int kLongRun = 24;           // pieces behind the first
 
 template <typename P>
 __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a) {
-    __shared__ float sums[kJoinThreads];
+    __shared__ float4 sums[kJoinThreads];
     __shared__ int found[kJoinThreads], pieces[kJoinThreads], n_found;
     pdl_prologue();
     const int thread = threadIdx.x, lane = thread & 31, warp = thread >> 5;
@@ -582,51 +640,42 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a) {
             if (lane == 0) pieces[f] = more;
         }
         __syncthreads();
-        const int blocks = (a.width + 127) / 128;
+        const int quads = (a.width + 3) / 4;     // four columns each
+        const int blocks = (quads + 31) / 32;
         for (int t = warp; t < runs * blocks; t += kJoinWarps) {
-            const int f = t / blocks, more = pieces[f];
-            if (more > kLongRun) continue;
+            const int f = t / blocks, more = pieces[f], quad = (t - f * blocks) * 32 + lane;
+            if (more > kLongRun || quad >= quads) continue;
             const int64_t c0 = found[f];
             const int32_t k = __ldcg(a.keys + (c0 + 1) * a.piece);
-            const int col = (t - f * blocks) * 128 + lane;
-            const float *part = a.part + c0 * 2 * a.width + col;
-            float s[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] = col + 32 * i < a.width ? __ldcg(part + a.width + 32 * i) : 0.f;
+            float4 s = part_of(a, 2 * c0 + 1, quad);
 #pragma unroll 4
-            for (int p = 1; p <= more; ++p) {
-                part += 2 * a.width;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (col + 32 * i < a.width) s[i] += __ldcg(part + 32 * i);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (col + 32 * i < a.width) write_one<P>(a.out, k * static_cast<int64_t>(a.width) + col + 32 * i, s[i] * a.scale);
+            for (int p = 1; p <= more; ++p) s = plus(s, part_of(a, 2 * (c0 + p), quad));
+            write_quad<P>(a, k, quad, s);
         }
-        // a group: as many warps as a row's columns take, at most a quarter of the block
-        const int wide = a.width >= 256 ? 256 : (a.width + 31) / 32 * 32, groups = kJoinThreads / wide;
+        const int wide = quads < 512 ? quads : 512, groups = kJoinThreads / wide;
         const int group = thread / wide, lead = thread - group * wide;
         for (int f = 0; f < runs; ++f) {
             const int more = pieces[f];
             if (more <= kLongRun) continue;
             const int64_t c0 = found[f];
             const int32_t k = __ldcg(a.keys + (c0 + 1) * a.piece);
-            for (int at = 0; at < a.width; at += wide) {
-                const int col = at + lead;
-                float s = 0.f;
-                if (col < a.width && group < groups) {
-                    const float *part = a.part + c0 * 2 * a.width + col;
-                    if (group == 0) s = __ldcg(part + a.width);
+            for (int from = 0; from < quads; from += wide) {
+                const int quad = from + lead;
+                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (quad < quads && group < groups) {
+                    if (group == 0) s = part_of(a, 2 * c0 + 1, quad);
 #pragma unroll 8
-                    for (int p = 1 + group; p <= more; p += groups) s += __ldcg(part + p * 2ll * a.width);
+                    for (int p = 1 + group; p <= more; p += groups) s = plus(s, part_of(a, 2 * (c0 + p), quad));
                 }
                 sums[thread] = s;
                 __syncthreads();
-                if (group == 0 && col < a.width) {
-                    for (int g = 1; g < groups; ++g) s += sums[g * wide + lead];
-                    write_one<P>(a.out, k * static_cast<int64_t>(a.width) + col, s * a.scale);
+                // the groups' sums, halved as often as it takes
+                for (int g = groups; g > 1; g = (g + 1) / 2) {
+                    const int half = (g + 1) / 2;
+                    if (group + half < g) sums[thread] = plus(sums[thread], sums[thread + half * wide]);
+                    __syncthreads();
                 }
+                if (group == 0 && quad < quads) write_quad<P>(a, k, quad, sums[thread]);
                 __syncthreads();
             }
         }
@@ -653,7 +702,7 @@ struct Plan {
     int64_t range;
     int slices, cols, slots, each, piece;
     int64_t pieces;
-    int count_bytes, stride;         // of a count; blocks' counts of a digit
+    int count_bytes;
     int64_t keys[2], at[2], counts, part, bytes;
 };
 
@@ -664,19 +713,18 @@ Plan plan_of(int64_t n, int64_t n_rows, int32_t width, int v) {
     while (bits < 31 && n_rows >> bits) ++bits;     // keys are 0 ... n_rows
     z.passes = static_cast<int>(ceil_div(bits, 9));
     z.bits = static_cast<int>(ceil_div(bits, z.passes));
+    if (z.bits < 4) z.bits = 4;      // whole 16 bytes of a block's counts
     // whole rounds of a block's threads
     z.range = ceil_div(ceil_div(n, kSortThreads), kSortBlocks) * kSortThreads;
     z.sort_blocks = n ? static_cast<int>(ceil_div(n, z.range)) : 0;
     z.count_bytes = z.range < 65536 ? 2 : 4;
-    z.stride = (z.sort_blocks + 7) / 8 * 8;
     const int parts = static_cast<int>(ceil_div(width, v));
     z.slices = static_cast<int>(ceil_div(parts, kSumThreads));
     z.cols = static_cast<int>(ceil_div(parts, z.slices));
-    z.slots = kSumThreads / z.cols;
+    z.slots = kSumThreads / z.cols < kMostSlots ? kSumThreads / z.cols : kMostSlots;
     // some six blocks an SM, of slots of 8 to 64 indices
     const int64_t want = ceil_div(n, static_cast<int64_t>(z.slots) * 912);
     z.each = want < 8 ? 8 : want > 64 ? 64 : static_cast<int>(want);
-    if (z.each * z.slots > kMostPiece) z.each = kMostPiece / z.slots;
     z.piece = z.slots * z.each;
     z.pieces = ceil_div(n, z.piece);
     int64_t at = 0;
@@ -688,7 +736,7 @@ Plan plan_of(int64_t n, int64_t n_rows, int32_t width, int v) {
     for (int i = 0; i < 2; ++i) {
         if (i < z.passes) z.keys[i] = place(4 * n), z.at[i] = place(4 * n);
     }
-    z.counts = place(1ll * z.passes * kBins * z.stride * z.count_bytes);
+    z.counts = place(1ll * z.passes * z.sort_blocks * z.count_bytes << z.bits);
     z.part = place(z.pieces * 8 * width);
     z.bytes = at;
     return z;
@@ -705,7 +753,8 @@ template <typename E, typename P, bool kChunks>
 wgs_status run_sums(const SumArgs &a, const Plan &z, int sms, cudaStream_t stream) {
     const int wide = z.cols * (16 / kBytes<E>);
     const int smem = (kChunks ? kAhead * z.cols * z.slots * 16 : 0) + 4 * (2 * z.piece + 2) + 8 * z.slots * wide;
-    static_assert(kAhead * kSumThreads * 16 + 4 * (2 * kMostPiece + 2) + 8 * kSumThreads * 8 <= 60 << 10,
+    static_assert(kMostPiece == 64 * kMostSlots &&
+                      kAhead * kSumThreads * 16 + 4 * (2 * kMostPiece + 2) + 8 * kSumThreads * 8 <= 60 << 10,
                   "shared memory of a block");
     auto kernel = sum_runs<E, P, kChunks>;
     // (as the layer norm's)
@@ -736,8 +785,8 @@ wgs_status run_format(const SumArgs &a, const Plan &z, bool chunks, bool p32, in
 // Sorts s.idx; s.keys and s.at are the order.  Zeros go to `bytes` bytes at `out`.
 wgs_status sort_indices(SortArgs &s, const Plan &z, char *ws, char *out, int64_t bytes, int unit, int sms,
                         cudaStream_t stream) {
-    s.range = z.range, s.blocks = z.sort_blocks, s.bits = z.bits, s.zero_unit = unit, s.stride = z.stride;
-    const int64_t counts = 1ll * kBins * z.stride * z.count_bytes;   // of a pass
+    s.range = z.range, s.blocks = z.sort_blocks, s.bits = z.bits, s.zero_unit = unit;
+    const int64_t counts = 1ll * z.sort_blocks * z.count_bytes << z.bits;   // of a pass
     auto count = z.count_bytes == 2 ? sort_count<uint16_t> : sort_count<uint32_t>;
     auto order = z.count_bytes == 2 ? sort_place<uint16_t> : sort_place<uint32_t>;
     // a share of the zeros in each launch, 64 bytes a thread or more
