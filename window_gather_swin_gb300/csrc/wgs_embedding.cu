@@ -80,45 +80,139 @@ __device__ __forceinline__ void store_values(char *p, const float (&v)[kV]) {
 
 // ------------------------------------------------------------------ lookup --
 
-constexpr int kLookupThreads = 256, kLookupChunks = 4;   // chunks of a thread
+// Chunks of the output, those of a block's threads side by side, are taken in steps
+// of the whole grid; a thread has the table's chunks of its next step on their way
+// into slots of its own in shared memory, and the indices of the one after that in
+// registers, so that neither the index nor the row that it names is waited for at
+// full length.  Rows that are not whole chunks are taken in parts of as many single
+// elements, every row_chunks-th of the row.
+constexpr int kLookupThreads = 256;
+constexpr int kLookupChunks = 2;       // of a thread in a step
+constexpr int kLookupBlocksPerSm = 5;
 
-// A block takes neighbouring chunks of the output.  T: the table's format, E: the
-// output's.  magic: 2^32 / chunks of a row, rounded up (exact quotients for
-// numbers below 2^16: those of a row and of a block's chunks).
-template <typename T, typename E, int kV>
-__global__ void __launch_bounds__(kLookupThreads) embedding_lookup(const char *table, const int32_t *idx, char *out,
-                                                                   int64_t n, int64_t n_rows, int row_chunks,
-                                                                   uint32_t magic, float scale) {
+struct LookupArgs {
+    const char *table;
+    const int32_t *idx;
+    char *out;
+    int64_t n, n_rows;
+    int row_chunks, width;
+    float scale;
+};
+
+// T: the table's format, E: the output's.
+template <typename T, typename E, bool kChunks>
+__global__ void __launch_bounds__(kLookupThreads, kLookupBlocksPerSm) embedding_lookup(const LookupArgs a) {
+    constexpr int kV = 16 / kBytes<E>, kIn = kV * kBytes<T>, kOut = 16;    // values, bytes of a chunk
+    constexpr int kSlots = kIn / 16;
+    __shared__ uint4 slots[kChunks ? 2 : 1][kChunks ? kLookupChunks * kSlots : 1][kChunks ? kLookupThreads : 1];
     pdl_prologue();
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kLookupThreads * kLookupChunks);
-    const int64_t row0 = first / row_chunks;
-    const uint32_t over = static_cast<uint32_t>(first - row0 * row_chunks);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kLookupThreads * kLookupChunks;
+    const int64_t row_step = step / a.row_chunks;
+    const int col_step = static_cast<int>(step - row_step * a.row_chunks);
     int64_t row[kLookupChunks];
-    int32_t from[kLookupChunks], col[kLookupChunks];
+    int col[kLookupChunks];
 #pragma unroll
     for (int j = 0; j < kLookupChunks; ++j) {
-        const uint32_t at = over + threadIdx.x + j * kLookupThreads;
-        const uint32_t r = row_chunks == 1 ? at : __umulhi(at, magic);
-        row[j] = row0 + r;
-        col[j] = static_cast<int32_t>(at - r * row_chunks);
-        from[j] = row[j] < n ? __ldg(idx + row[j]) : -1;
+        const int64_t at = (static_cast<int64_t>(blockIdx.x) * kLookupChunks + j) * kLookupThreads + threadIdx.x;
+        row[j] = at / a.row_chunks;
+        col[j] = static_cast<int>(at - row[j] * a.row_chunks);
     }
-    float v[kLookupChunks][kV];
+    auto advance = [&](int64_t &r, int &c) {
+        r += row_step, c += col_step;
+        if (c >= a.row_chunks) c -= a.row_chunks, ++r;
+    };
+    // the table row of a chunk's index: -1 for none
+    auto index = [&](int64_t r, int c) {
+        if (r >= a.n) return -1;
+        const int32_t k = __ldg(a.idx + r);
+        if (k >= 0 && k < a.n_rows) return k;
+        if (k != -1 && c == 0) atomicOr(&g_embedding_error, 1u);
+        return -1;
+    };
+    auto fetch = [&](int s, const int32_t (&from)[kLookupChunks], const int (&c)[kLookupChunks]) {
+        if constexpr (kChunks) {
 #pragma unroll
-    for (int j = 0; j < kLookupChunks; ++j) {
-        if (from[j] >= 0 && from[j] < n_rows) {
-            load_values<T, kV>(table + (static_cast<int64_t>(from[j]) * row_chunks + col[j]) * (kV * kBytes<T>), v[j]);
-        } else {
-            if (from[j] != -1 && col[j] == 0) atomicOr(&g_embedding_error, 1u);
-            from[j] = -1;
+            for (int j = 0; j < kLookupChunks; ++j)
+                if (from[j] >= 0) {
+                    const char *p = a.table + (static_cast<int64_t>(from[j]) * a.row_chunks + c[j]) * kIn;
+#pragma unroll
+                    for (int i = 0; i < kSlots; ++i) cp_async16_ca(&slots[s][j * kSlots + i][threadIdx.x], p + 16 * i);
+                }
+            cp_async_commit();
         }
-    }
+    };
+    int64_t next_row[kLookupChunks];
+    int next_col[kLookupChunks];
+    int32_t now[kLookupChunks], next[kLookupChunks];
 #pragma unroll
     for (int j = 0; j < kLookupChunks; ++j) {
-        if (row[j] >= n) continue;
+        now[j] = index(row[j], col[j]);
+        next_row[j] = row[j], next_col[j] = col[j];
+        advance(next_row[j], next_col[j]);
+        next[j] = index(next_row[j], next_col[j]);
+    }
+    fetch(0, now, col);
+    for (int s = 0; row[0] < a.n; s ^= 1) {
+        fetch(s ^ 1, next, next_col);
+        int32_t later[kLookupChunks];
+        int64_t later_row[kLookupChunks];
+        int later_col[kLookupChunks];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) v[j][i] = from[j] < 0 ? 0.f : v[j][i] * scale;
-        store_values<E, kV>(out + (row[j] * row_chunks + col[j]) * (kV * kBytes<E>), v[j]);
+        for (int j = 0; j < kLookupChunks; ++j) {
+            later_row[j] = next_row[j], later_col[j] = next_col[j];
+            advance(later_row[j], later_col[j]);
+            later[j] = index(later_row[j], later_col[j]);
+        }
+        if constexpr (kChunks) cp_async_wait<1>();
+#pragma unroll
+        for (int j = 0; j < kLookupChunks; ++j) {
+            if (row[j] >= a.n) continue;
+            float v[kV];
+#pragma unroll
+            for (int i = 0; i < kV; ++i) v[i] = 0.f;
+            if (now[j] >= 0) {
+                if constexpr (kChunks) {
+#pragma unroll
+                    for (int i = 0; i < kSlots; ++i) {
+                        const uint4 q = slots[s][j * kSlots + i][threadIdx.x];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if constexpr (std::is_same<T, F32>::value) {
+                                v[4 * i + k] = __uint_as_float(word(q, k));
+                            } else {
+                                const float2 f = T::to_f2(word(q, k));
+                                v[2 * k] = f.x, v[2 * k + 1] = f.y;
+                            }
+                        }
+                    }
+                } else {
+                    const char *p = a.table + static_cast<int64_t>(now[j]) * a.width * kBytes<T>;
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) {
+                        float one[1] = {0.f};
+                        if (col[j] + i * a.row_chunks < a.width) load_values<T, 1>(p + (col[j] + i * a.row_chunks) * kBytes<T>, one);
+                        v[i] = one[0];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kV; ++i) v[i] *= a.scale;
+            }
+            if constexpr (kChunks) {
+                store_values<E, kV>(a.out + (row[j] * a.row_chunks + col[j]) * kOut, v);
+            } else {
+                char *p = a.out + row[j] * a.width * kBytes<E>;
+#pragma unroll
+                for (int i = 0; i < kV; ++i) {
+                    const float one[1] = {v[i]};
+                    if (col[j] + i * a.row_chunks < a.width) store_values<E, 1>(p + (col[j] + i * a.row_chunks) * kBytes<E>, one);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kLookupChunks; ++j) {
+            row[j] = next_row[j], col[j] = next_col[j], now[j] = next[j];
+            next_row[j] = later_row[j], next_col[j] = later_col[j], next[j] = later[j];
+        }
     }
 }
 
@@ -381,7 +475,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs a) {
 // -------------------------------------------------------------------- sums --
 
 constexpr int kSumThreads = 256;
-constexpr int kAhead = 6;              // rows that a thread has in flight
+constexpr int kAhead = 8;              // rows that a thread has in flight
 // Of a block: the slots' ends are joined one after another.
 constexpr int kMostSlots = 32;
 constexpr int kMostPiece = 2048;       // indices of a block
@@ -453,99 +547,120 @@ __global__ void __launch_bounds__(kSumThreads) sum_runs(const SumArgs a) {
     const int slots = blockDim.y, wide = a.cols * kV;            // values of a row here
     const int thread = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
     // slots of rows on their way: [ahead][threads], 16 bytes each (kChunks alone)
+    constexpr int kRingStep = kSumThreads * 16;
     const uint32_t ring = shared_address(memory) + thread * 16;
-    const int ring_bytes = kChunks ? kAhead * threads * 16 : 0;
-    int32_t *keys = reinterpret_cast<int32_t *>(memory + ring_bytes) + 1;       // keys[-1] ... keys[piece]
-    int32_t *at = keys + a.piece + 1;
-    float *head = reinterpret_cast<float *>(at + a.piece);       // [slots][wide]
+    constexpr int kRingBytes = kChunks ? kAhead * kRingStep : 0;
+    int2 *tokens = reinterpret_cast<int2 *>(memory + kRingBytes) + 1;    // [-1] ... [piece]: row, position
+    float *head = reinterpret_cast<float *>(tokens + a.piece + 1);       // [slots][wide]
     float *tail = head + slots * wide;
     pdl_prologue();
     const int64_t first = static_cast<int64_t>(blockIdx.x) * a.piece;
     for (int i = thread - 1; i <= a.piece; i += threads) {
         const int64_t t = first + i;
         // no row: before the first index, and from the first that names none
-        keys[i] = t >= 0 && t < a.n ? __ldcg(a.keys + t) : a.n_rows;
-        if (i >= 0 && i < a.piece && t < a.n) at[i] = __ldcg(a.at + t);
+        const bool some = t >= 0 && t < a.n;
+        tokens[i] = some ? make_int2(__ldcg(a.keys + t), __ldcg(a.at + t)) : make_int2(a.n_rows, 0);
     }
     __syncthreads();
-    if (keys[0] >= a.n_rows) return;
+    if (tokens[0].x >= a.n_rows) return;
     const Part part(threadIdx.x, a.cols, blockIdx.y, a.width);
-    const int64_t row_bytes = static_cast<int64_t>(a.width) * kBytes<E>;
-    const int t0 = threadIdx.y * a.each, t1 = t0 + a.each;
-    if (keys[t0] < a.n_rows && part.any()) {
-        const int64_t out_bytes = static_cast<int64_t>(a.width) * kBytes<P>;
-        float acc[kV] = {};
-        int32_t cur = keys[t0];
-        bool open = keys[t0 - 1] == cur;    // the run began before this slot
+    const uint32_t row_bytes = static_cast<uint32_t>(a.width) * kBytes<E>;
+    const int t0 = threadIdx.y * a.each;
+    if (tokens[t0].x < a.n_rows && part.any()) {
+        const uint32_t out_bytes = static_cast<uint32_t>(a.width) * kBytes<P>;
+        const int2 *mine = tokens + t0;
+        float2 acc[kV / 2];
+#pragma unroll
+        for (int i = 0; i < kV / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+        int32_t cur = mine[0].x;
+        bool open = mine[-1].x == cur;    // the run began before this slot
         auto flush = [&](float *place) {
             if (place) {
 #pragma unroll
-                for (int i = 0; i < kV; ++i) place[threadIdx.y * wide + (kChunks ? threadIdx.x * kV + i : threadIdx.x + i * a.cols)] = acc[i];
+                for (int i = 0; i < kV; ++i)
+                    place[threadIdx.y * wide + (kChunks ? threadIdx.x * kV + i : threadIdx.x + i * a.cols)] =
+                        i & 1 ? acc[i / 2].y : acc[i / 2].x;
             } else {
+                float v[kV];
 #pragma unroll
-                for (int i = 0; i < kV; ++i) acc[i] *= a.scale;
-                part.store(a.out + cur * out_bytes, acc);
+                for (int i = 0; i < kV; ++i) v[i] = (i & 1 ? acc[i / 2].y : acc[i / 2].x) * a.scale;
+                part.store(a.out + static_cast<int64_t>(cur) * out_bytes, v);
             }
-#pragma unroll
-            for (int i = 0; i < kV; ++i) acc[i] = 0.f;
         };
-        auto take = [&](int32_t k, const float (&v)[kV]) {
+        // the run of row k takes v, after the one before is ended
+        auto take = [&](int32_t k, const float2 (&v)[kV / 2]) {
             if (k != cur) {
                 flush(open ? head : nullptr);
                 open = false;
                 cur = k;
+#pragma unroll
+                for (int i = 0; i < kV / 2; ++i) acc[i] = v[i];
+                return;
             }
 #pragma unroll
-            for (int i = 0; i < kV; ++i) acc[i] += v[i];
+            for (int i = 0; i < kV / 2; ++i) acc[i] = __fadd2_rn(acc[i], v[i]);
         };
         if constexpr (kChunks) {
             const char *from = a.grad + part.first * kBytes<E>;
-            const uint32_t around = kAhead * threads * 16;
-            auto fetch = [&](int t, uint32_t slot) {
-                if (t < t1 && keys[t] < a.n_rows)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + slot), "l"(from + at[t] * row_bytes) : "memory");
+            int32_t key[kAhead];         // of the rows on their way; n_rows: none
+            auto fetch = [&](int t, int j) {
+                key[j] = a.n_rows;
+                if (t < a.each) {
+                    const int2 token = mine[t];
+                    key[j] = token.x;
+                    if (token.x < a.n_rows)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + j * kRingStep),
+                                     "l"(from + static_cast<uint64_t>(static_cast<uint32_t>(token.y)) * row_bytes) : "memory");
+                }
                 cp_async_commit();
             };
-            uint32_t slot = 0;
-            for (int j = 0; j < kAhead; ++j) fetch(t0 + j, j * threads * 16);
-            for (int t = t0; t < t1; ++t) {
-                const int32_t k = keys[t];
-                if (k >= a.n_rows) break;
-                cp_async_wait<kAhead - 1>();
-                uint4 q;
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(ring + slot) : "memory");
-                float v[kV];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (kV == 4) {
-                        v[i] = __uint_as_float(word(q, i));
-                    } else {
-                        const float2 f = E::to_f2(word(q, i));
-                        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+            for (int j = 0; j < kAhead; ++j) fetch(j, j);
+            for (int t = 0; t < a.each; t += kAhead) {
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    cp_async_wait<kAhead - 1>();
+                    if (key[j] < a.n_rows) {
+                        uint4 q;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(ring + j * kRingStep) : "memory");
+                        float2 v[kV / 2];
+#pragma unroll
+                        for (int i = 0; i < kV / 2; ++i) {
+                            if constexpr (kV == 4)
+                                v[i] = make_float2(__uint_as_float(word(q, 2 * i)), __uint_as_float(word(q, 2 * i + 1)));
+                            else
+                                v[i] = E::to_f2(word(q, i));
+                        }
+                        take(key[j], v);
                     }
+                    fetch(t + j + kAhead, j);
                 }
-                take(k, v);
-                fetch(t + kAhead, slot);
-                slot += threads * 16;
-                if (slot == around) slot = 0;
             }
             cp_async_wait<0>();
         } else {
             constexpr int kBatch = 4;
-            for (int t = t0; t < t1; t += kBatch) {
+            for (int t = 0; t < a.each; t += kBatch) {
                 float v[kBatch][kV];
                 int32_t k[kBatch];
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) {
-                    k[j] = t + j < t1 ? keys[t + j] : a.n_rows;
-                    if (k[j] < a.n_rows) part.load(a.grad + at[t + j] * row_bytes, v[j]);
+                    const int2 token = t + j < a.each ? mine[t + j] : make_int2(a.n_rows, 0);
+                    k[j] = token.x;
+                    if (k[j] < a.n_rows)
+                        part.load(a.grad + static_cast<uint64_t>(static_cast<uint32_t>(token.y)) * row_bytes, v[j]);
                 }
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j)
-                    if (k[j] < a.n_rows) take(k[j], v[j]);
+                for (int j = 0; j < kBatch; ++j) {
+                    if (k[j] >= a.n_rows) continue;
+                    float2 pairs[kV / 2];
+#pragma unroll
+                    for (int i = 0; i < kV / 2; ++i) pairs[i] = make_float2(v[j][2 * i], v[j][2 * i + 1]);
+                    take(k[j], pairs);
+                }
             }
         }
-        flush(open ? head : keys[t1] == cur ? tail : nullptr);
+        flush(open ? head : mine[a.each].x == cur ? tail : nullptr);
     }
     __syncthreads();
     // The slots' ends, in their order.  A run that began before this piece, or
@@ -555,27 +670,27 @@ __global__ void __launch_bounds__(kSumThreads) sum_runs(const SumArgs a) {
         const int c = blockIdx.y * wide + f;
         if (c >= a.width) break;
         float run = 0.f;
-        bool before = keys[-1] == keys[0];      // the open run began before the piece
+        bool before = tokens[-1].x == tokens[0].x;      // the open run began before the piece
         for (int s = 0; s < slots; ++s) {
             const int b = s * a.each, e = b + a.each;
-            if (keys[b] >= a.n_rows) break;
-            const int32_t last = keys[e - 1];
-            if (keys[b - 1] == keys[b]) {
+            if (tokens[b].x >= a.n_rows) break;
+            const int32_t last = tokens[e - 1].x;
+            if (tokens[b - 1].x == tokens[b].x) {
                 run += head[s * wide + f];
                 // does it end here?
-                if (!(last == keys[b] && keys[e] == last)) {
+                if (!(last == tokens[b].x && tokens[e].x == last)) {
                     if (before) left[c] = run;
-                    else write_one<P>(a.out, keys[b] * static_cast<int64_t>(a.width) + c, run * a.scale);
+                    else write_one<P>(a.out, tokens[b].x * static_cast<int64_t>(a.width) + c, run * a.scale);
                     before = false;
                     run = 0.f;
                 } else {
                     continue;
                 }
             }
-            if (last < a.n_rows && keys[e] == last) run = tail[s * wide + f];
+            if (last < a.n_rows && tokens[e].x == last) run = tail[s * wide + f];
         }
-        const int32_t last = keys[a.piece - 1];
-        if (last < a.n_rows && keys[a.piece] == last) left[(before ? 0 : a.width) + c] = run;
+        const int32_t last = tokens[a.piece - 1].x;
+        if (last < a.n_rows && tokens[a.piece].x == last) left[(before ? 0 : a.width) + c] = run;
     }
 }
 
@@ -752,14 +867,14 @@ int64_t workspace_of(int64_t n, int64_t n_rows, int32_t width) {
 template <typename E, typename P, bool kChunks>
 wgs_status run_sums(const SumArgs &a, const Plan &z, int sms, cudaStream_t stream) {
     const int wide = z.cols * (16 / kBytes<E>);
-    const int smem = (kChunks ? kAhead * z.cols * z.slots * 16 : 0) + 4 * (2 * z.piece + 2) + 8 * z.slots * wide;
+    const int smem = (kChunks ? kAhead * kSumThreads * 16 : 0) + 8 * (z.piece + 2) + 8 * z.slots * wide;
     static_assert(kMostPiece == 64 * kMostSlots &&
-                      kAhead * kSumThreads * 16 + 4 * (2 * kMostPiece + 2) + 8 * kSumThreads * 8 <= 60 << 10,
+                      kAhead * kSumThreads * 16 + 8 * (kMostPiece + 2) + 8 * kSumThreads * 8 <= 66 << 10,
                   "shared memory of a block");
     auto kernel = sum_runs<E, P, kChunks>;
     // (as the layer norm's)
     if (smem > 47 << 10 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 60 << 10) != cudaSuccess) {
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 66 << 10) != cudaSuccess) {
         cudaGetLastError();
         return WGS_ERR_LAUNCH;
     }
@@ -824,16 +939,14 @@ wgs_status sort_indices(SortArgs &s, const Plan &z, char *ws, char *out, int64_t
 }
 
 template <typename T, typename E>
-wgs_status run_lookup(const char *table, const int32_t *idx, char *out, int64_t n, int64_t n_rows, int32_t width,
-                      float scale, cudaStream_t stream) {
+wgs_status run_lookup(LookupArgs a, int32_t width, int sms, cudaStream_t stream) {
     constexpr int kV = 16 / kBytes<E>;
-    const bool chunks = in_chunks(table, out, width, kBytes<T>, kBytes<E>);
-    const int row_chunks = chunks ? width / kV : width;
-    const int64_t blocks = ceil_div(n * row_chunks, kLookupThreads * kLookupChunks);
-    if (blocks > INT32_MAX) return WGS_ERR_SHAPE;
-    const uint32_t magic = static_cast<uint32_t>(((1ull << 32) + row_chunks - 1) / row_chunks);
-    return launch(chunks ? embedding_lookup<T, E, kV> : embedding_lookup<T, E, 1>, dim3(static_cast<unsigned>(blocks)),
-                  dim3(kLookupThreads), 0, stream, table, idx, out, n, n_rows, row_chunks, magic, scale);
+    const bool chunks = in_chunks(a.table, a.out, width, kBytes<T>, kBytes<E>);
+    a.row_chunks = static_cast<int>(ceil_div(width, kV)), a.width = width;
+    const int64_t blocks = ceil_div(a.n * a.row_chunks, kLookupThreads * kLookupChunks);
+    const int64_t most = static_cast<int64_t>(sms) * kLookupBlocksPerSm;
+    return launch(chunks ? embedding_lookup<T, E, true> : embedding_lookup<T, E, false>,
+                  dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(kLookupThreads), 0, stream, a);
 }
 
 }  // namespace
@@ -870,12 +983,13 @@ extern "C" wgs_status embedding(const void *table, const int32_t *idx, void *out
     DeviceInfo dev;
     const wgs_status st = current_device(&dev);
     if (st != WGS_OK) return st;
-    const char *t = static_cast<const char *>(table);
-    char *o = static_cast<char *>(out);
-    auto go = dtype == WGS_F32    ? run_lookup<F32, F32>
+    LookupArgs a = {};
+    a.table = static_cast<const char *>(table), a.idx = idx, a.out = static_cast<char *>(out);
+    a.n = n_idx, a.n_rows = n_rows, a.scale = scale;
+    auto go = dtype == WGS_F32   ? run_lookup<F32, F32>
               : dtype == WGS_F16 ? (table_dtype == WGS_F32 ? run_lookup<F32, Fp16> : run_lookup<Fp16, Fp16>)
                                  : (table_dtype == WGS_F32 ? run_lookup<F32, Bf16> : run_lookup<Bf16, Bf16>);
-    return go(t, idx, o, n_idx, n_rows, width, scale, stream);
+    return go(a, width, dev.sm_count, stream);
 }
 
 extern "C" size_t wgs_embedding_bwd_workspace_bytes(int64_t n_idx, int64_t n_rows, int32_t width) {
