@@ -6,9 +6,10 @@ torch's elementwise operations do as well: the bits are equal.
 
 The gradient's sums: a slot's indices (at most 64), the slots of a piece (at most
 256), every fourth or fewer of the pieces that a run reaches into (of which there
-are at most 913, or indices / 64) and those sums (at most 32), so with D = 64 + 256
-+ 229 + indices / 256 + 32 additions and u = 2^-24 the sum is off by D u of its
-terms' magnitudes, the product with scale by u, and rounding to the
+are at most 913, or indices / 64) and those sums (at most 32); of at most 2048
+indices no more than all, one after another.  So with D = 64 + 256 + 229 + indices
+/ 256 + 32, or 2048, additions and u = 2^-24 the sum is off by D u of its terms'
+magnitudes, the product with scale by u, and rounding to the
 output's format by half a step.  Where all values are small whole numbers every
 sum is exact, and the result has to be.
 """
@@ -148,7 +149,7 @@ def _check_gradient(grad, idx, rows, scale, got):
         mag[:, lo:lo + 256].index_add_(0, idx[keep].long(), g.abs())
     s = torch.tensor(scale, dtype=torch.float32).double().item()
     want *= s
-    most = 64 + 256 + 229 + n / 256 + 32
+    most = 64 + 256 + 229 + n / 256 + 32 if n > 2048 else n
     tol = (most * U * abs(s) * mag + U * want.abs()) * (1 + torch.finfo(got.dtype).eps) + _half_step(want, got.dtype)
     err = (got.double() - want).abs()
     assert (err <= tol).all(), (err / tol).max()

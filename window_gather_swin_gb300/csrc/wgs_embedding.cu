@@ -80,15 +80,16 @@ __device__ __forceinline__ void store_values(char *p, const float (&v)[kV]) {
 
 // ------------------------------------------------------------------ lookup --
 
-// Chunks of the output, those of a block's threads side by side, are taken in steps
-// of the whole grid; a thread has the table's chunks of its next step on their way
-// into slots of its own in shared memory, and the indices of the one after that in
-// registers, so that neither the index nor the row that it names is waited for at
-// full length.  Rows that are not whole chunks are taken in parts of as many single
+// Chunks of 16 bytes of the table's rows, those of a block's threads side by side,
+// are taken in steps of the whole grid; a thread has its next step's chunk on its way
+// into a slot of its own in shared memory, and the index of the one after that in a
+// register, so that neither the index nor the row that it names is waited for at
+// full length.  The copies go through L1, which keeps the rows that many indices
+// name: past it, a skewed sequence's rows were asked of the same L2 lines by all SMs
+// at once (131040 of 384, FP32 to bf16: 128 us, through L1 33).  Rows that are not whole chunks are taken in parts of as many single
 // elements, every row_chunks-th of the row.
 constexpr int kLookupThreads = 256;
-constexpr int kLookupChunks = 2;       // of a thread in a step
-constexpr int kLookupBlocksPerSm = 5;
+constexpr int kLookupBlocksPerSm = 8;
 
 struct LookupArgs {
     const char *table;
@@ -102,21 +103,14 @@ struct LookupArgs {
 // T: the table's format, E: the output's.
 template <typename T, typename E, bool kChunks>
 __global__ void __launch_bounds__(kLookupThreads, kLookupBlocksPerSm) embedding_lookup(const LookupArgs a) {
-    constexpr int kV = 16 / kBytes<E>, kIn = kV * kBytes<T>, kOut = 16;    // values, bytes of a chunk
-    constexpr int kSlots = kIn / 16;
-    __shared__ uint4 slots[kChunks ? 2 : 1][kChunks ? kLookupChunks * kSlots : 1][kChunks ? kLookupThreads : 1];
+    constexpr int kIn = 16, kV = kIn / kBytes<T>, kOut = kV * kBytes<E>;    // of a chunk
+    __shared__ uint4 slots[kChunks ? 2 : 1][kChunks ? kLookupThreads : 1];
     pdl_prologue();
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kLookupThreads * kLookupChunks;
-    const int64_t row_step = step / a.row_chunks;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kLookupThreads, row_step = step / a.row_chunks;
     const int col_step = static_cast<int>(step - row_step * a.row_chunks);
-    int64_t row[kLookupChunks];
-    int col[kLookupChunks];
-#pragma unroll
-    for (int j = 0; j < kLookupChunks; ++j) {
-        const int64_t at = (static_cast<int64_t>(blockIdx.x) * kLookupChunks + j) * kLookupThreads + threadIdx.x;
-        row[j] = at / a.row_chunks;
-        col[j] = static_cast<int>(at - row[j] * a.row_chunks);
-    }
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kLookupThreads + threadIdx.x;
+    int64_t row = first / a.row_chunks;
+    int col = static_cast<int>(first - row * a.row_chunks);
     auto advance = [&](int64_t &r, int &c) {
         r += row_step, c += col_step;
         if (c >= a.row_chunks) c -= a.row_chunks, ++r;
@@ -129,90 +123,63 @@ __global__ void __launch_bounds__(kLookupThreads, kLookupBlocksPerSm) embedding_
         if (k != -1 && c == 0) atomicOr(&g_embedding_error, 1u);
         return -1;
     };
-    auto fetch = [&](int s, const int32_t (&from)[kLookupChunks], const int (&c)[kLookupChunks]) {
+    auto fetch = [&](int s, int32_t from, int c) {
         if constexpr (kChunks) {
-#pragma unroll
-            for (int j = 0; j < kLookupChunks; ++j)
-                if (from[j] >= 0) {
-                    const char *p = a.table + (static_cast<int64_t>(from[j]) * a.row_chunks + c[j]) * kIn;
-#pragma unroll
-                    for (int i = 0; i < kSlots; ++i) cp_async16_ca(&slots[s][j * kSlots + i][threadIdx.x], p + 16 * i);
-                }
+            if (from >= 0) cp_async16_ca(&slots[s][threadIdx.x], a.table + (static_cast<int64_t>(from) * a.row_chunks + c) * kIn);
             cp_async_commit();
         }
     };
-    int64_t next_row[kLookupChunks];
-    int next_col[kLookupChunks];
-    int32_t now[kLookupChunks], next[kLookupChunks];
-#pragma unroll
-    for (int j = 0; j < kLookupChunks; ++j) {
-        now[j] = index(row[j], col[j]);
-        next_row[j] = row[j], next_col[j] = col[j];
-        advance(next_row[j], next_col[j]);
-        next[j] = index(next_row[j], next_col[j]);
-    }
+    int64_t next_row = row;
+    int next_col = col;
+    int32_t now = index(row, col);
+    advance(next_row, next_col);
     fetch(0, now, col);
-    for (int s = 0; row[0] < a.n; s ^= 1) {
+    int32_t next = index(next_row, next_col);
+    for (int s = 0; row < a.n; s ^= 1) {
         fetch(s ^ 1, next, next_col);
-        int32_t later[kLookupChunks];
-        int64_t later_row[kLookupChunks];
-        int later_col[kLookupChunks];
+        int64_t later_row = next_row;
+        int later_col = next_col;
+        advance(later_row, later_col);
+        const int32_t later = index(later_row, later_col);
+        float v[kV];
 #pragma unroll
-        for (int j = 0; j < kLookupChunks; ++j) {
-            later_row[j] = next_row[j], later_col[j] = next_col[j];
-            advance(later_row[j], later_col[j]);
-            later[j] = index(later_row[j], later_col[j]);
-        }
-        if constexpr (kChunks) cp_async_wait<1>();
+        for (int i = 0; i < kV; ++i) v[i] = 0.f;
+        if constexpr (kChunks) {
+            cp_async_wait<1>();
+            if (now >= 0) {
+                const uint4 q = slots[s][threadIdx.x];
 #pragma unroll
-        for (int j = 0; j < kLookupChunks; ++j) {
-            if (row[j] >= a.n) continue;
-            float v[kV];
-#pragma unroll
-            for (int i = 0; i < kV; ++i) v[i] = 0.f;
-            if (now[j] >= 0) {
-                if constexpr (kChunks) {
-#pragma unroll
-                    for (int i = 0; i < kSlots; ++i) {
-                        const uint4 q = slots[s][j * kSlots + i][threadIdx.x];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if constexpr (std::is_same<T, F32>::value) {
-                                v[4 * i + k] = __uint_as_float(word(q, k));
-                            } else {
-                                const float2 f = T::to_f2(word(q, k));
-                                v[2 * k] = f.x, v[2 * k + 1] = f.y;
-                            }
-                        }
-                    }
-                } else {
-                    const char *p = a.table + static_cast<int64_t>(now[j]) * a.width * kBytes<T>;
-#pragma unroll
-                    for (int i = 0; i < kV; ++i) {
-                        float one[1] = {0.f};
-                        if (col[j] + i * a.row_chunks < a.width) load_values<T, 1>(p + (col[j] + i * a.row_chunks) * kBytes<T>, one);
-                        v[i] = one[0];
+                for (int k = 0; k < 4; ++k) {
+                    if constexpr (kV == 4) {
+                        v[k] = __uint_as_float(word(q, k)) * a.scale;
+                    } else {
+                        const float2 f = T::to_f2(word(q, k));
+                        v[2 * k] = f.x * a.scale, v[2 * k + 1] = f.y * a.scale;
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < kV; ++i) v[i] *= a.scale;
             }
-            if constexpr (kChunks) {
-                store_values<E, kV>(a.out + (row[j] * a.row_chunks + col[j]) * kOut, v);
-            } else {
-                char *p = a.out + row[j] * a.width * kBytes<E>;
+            char *p = a.out + (row * a.row_chunks + col) * kOut;
+            if constexpr (kOut == 8)
+                *reinterpret_cast<uint2 *>(p) = make_uint2(E::from_f2(v[0], v[1]), E::from_f2(v[2], v[3]));
+            else
+                store_values<E, kV>(p, v);
+        } else {
+            const char *from = a.table + (now < 0 ? 0 : static_cast<int64_t>(now) * a.width * kBytes<T>);
+            char *p = a.out + row * a.width * kBytes<E>;
 #pragma unroll
-                for (int i = 0; i < kV; ++i) {
-                    const float one[1] = {v[i]};
-                    if (col[j] + i * a.row_chunks < a.width) store_values<E, 1>(p + (col[j] + i * a.row_chunks) * kBytes<E>, one);
-                }
+            for (int i = 0; i < kV; ++i) {
+                float one[1] = {0.f};
+                if (now >= 0 && col + i * a.row_chunks < a.width) load_values<T, 1>(from + (col + i * a.row_chunks) * kBytes<T>, one);
+                v[i] = one[0] * a.scale;
+            }
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const float one[1] = {now < 0 ? 0.f : v[i]};
+                if (col + i * a.row_chunks < a.width) store_values<E, 1>(p + (col + i * a.row_chunks) * kBytes<E>, one);
             }
         }
-#pragma unroll
-        for (int j = 0; j < kLookupChunks; ++j) {
-            row[j] = next_row[j], col[j] = next_col[j], now[j] = next[j];
-            next_row[j] = later_row[j], next_col[j] = later_col[j], next[j] = later[j];
-        }
+        row = next_row, col = next_col, now = next;
+        next_row = later_row, next_col = later_col, next = later;
     }
 }
 
@@ -316,24 +283,23 @@ __global__ void __launch_bounds__(kSortThreads) sort_count(const SortArgs a) {
         static_cast<uint32_t *>(a.next)[i] = 0u;
 }
 
-template <typename C>
-__global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs a) {
-    extern __shared__ __align__(16) char shared[];
-    uint2 *pairs = reinterpret_cast<uint2 *>(shared);                          // [tile]: row, position
-    uint32_t *same_digit = reinterpret_cast<uint32_t *>(pairs + kSortTile);    // [warps][bins]: lanes
-    uint32_t *warp_count = same_digit + kSortWarps * kBins;                    // [warps][bins]
-    __shared__ int32_t to_base[kBins], warp_sums[kSortWarps];
-    __shared__ uint32_t local_base[kBins];
-    pdl_prologue();
-    if (zeros_instead(a)) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = blockIdx.x, bin = threadIdx.x;
-    const int bins = 1 << a.bits;
-    const uint32_t mask = bins - 1, lower = (1u << lane) - 1;
-    uint32_t *lanes = same_digit + warp * kBins, *mine = warp_count + warp * kBins;
-    for (int i = lane; i < bins; i += 32) lanes[i] = 0u;
+// What a block of kSortThreads needs to sort a tile by a digit.
+struct Ranker {
+    uint32_t *lanes, *counts;       // [warps][bins]: lanes of a digit; counts of the warps
+    int32_t *warp_sums;             // [warps]
+    uint32_t *base;                 // [bins]: where a digit begins in the tile
+    static constexpr int kTableBytes = kSortWarps * kBins * 8;
 
+    __device__ Ranker(char *tables, int32_t *sums, uint32_t *bases)
+        : lanes(reinterpret_cast<uint32_t *>(tables)), counts(lanes + kSortWarps * kBins), warp_sums(sums), base(bases) {}
+    // the first use of the tables for digits of so many bins
+    __device__ void clear(int bins) const {
+        for (int i = threadIdx.x & 31; i < bins; i += 32) lanes[(threadIdx.x >> 5) * kBins + i] = 0u;
+        __syncwarp();
+    }
     // Exclusive sums over the threads' values, in the threads' order.
-    auto scan = [&](int32_t v) {
+    __device__ int32_t scan(int32_t v) const {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         int32_t s = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -347,15 +313,72 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs a) {
 #pragma unroll
         for (int w = 0; w < kSortWarps; ++w) before += w < warp ? warp_sums[w] : 0;
         return before + s - v;
-    };
+    }
+    __device__ static int first() { return (threadIdx.x >> 5) * 32 * kRounds + (threadIdx.x & 31); }
+    // The n values at first() + 32 j, round j, go to `pairs` in the order of the digit
+    // above `shift`, equal ones in theirs.  Returns the count of digit threadIdx.x.
+    __device__ uint32_t place(const uint32_t (&key)[kRounds], const uint32_t (&at)[kRounds], int n, int shift, int bits,
+                              uint2 *pairs) const {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << bits, bin = threadIdx.x;
+        const uint32_t mask = bins - 1, lower = (1u << lane) - 1;
+        uint32_t *lane_bits = lanes + warp * kBins, *mine = counts + warp * kBins;
+        for (int i = lane; i < bins; i += 32) mine[i] = 0u;
+        __syncwarp();
+        uint32_t rank[kRounds];
+#pragma unroll
+        for (int j = 0; j < kRounds; ++j) {
+            const bool valid = first() + 32 * j < n;
+            const uint32_t d = key[j] >> shift & mask;
+            if (valid) atomicOr(&lane_bits[d], 1u << lane);
+            __syncwarp();
+            const uint32_t same = lane_bits[d], had = mine[d], before = __popc(same & lower);
+            __syncwarp();
+            if (valid && before == 0) lane_bits[d] = 0u, mine[d] = had + __popc(same);
+            __syncwarp();
+            rank[j] = had + before;
+        }
+        __syncthreads();
+        // counts of the warps before, and of the digits before: places in the tile
+        uint32_t run = 0;
+        if (bin < bins) {
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t c = counts[w * kBins + bin];
+                counts[w * kBins + bin] = run;
+                run += c;
+            }
+        }
+        base[bin] = static_cast<uint32_t>(scan(static_cast<int32_t>(run)));
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kRounds; ++j) {
+            if (first() + 32 * j >= n) continue;
+            const uint32_t d = key[j] >> shift & mask;
+            pairs[base[d] + mine[d] + rank[j]] = make_uint2(key[j], at[j]);
+        }
+        __syncthreads();
+        return run;
+    }
+};
 
+template <typename C>
+__global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs a) {
+    extern __shared__ __align__(16) char shared[];
+    uint2 *pairs = reinterpret_cast<uint2 *>(shared);                          // [tile]: row, position
+    __shared__ int32_t to_base[kBins], warp_sums[kSortWarps];
+    __shared__ uint32_t local_base[kBins];
+    const Ranker ranker(shared + kSortTile * 8, warp_sums, local_base);
+    pdl_prologue();
+    if (zeros_instead(a)) return;
+    const int me = blockIdx.x, bin = threadIdx.x, bins = 1 << a.bits;
+    const uint32_t mask = bins - 1;
+    ranker.clear(bins);
     const int64_t first = me * a.range, end = first + a.range < a.n ? first + a.range : a.n;
-    const int here = warp * 32 * kRounds + lane;
     uint32_t key[kRounds], at[kRounds];
     auto load = [&](int64_t tile) {
 #pragma unroll
         for (int j = 0; j < kRounds; ++j) {
-            const int64_t i = tile + here + 32 * j;
+            const int64_t i = tile + Ranker::first() + 32 * j;
             key[j] = at[j] = 0u;
             if (i < end) {
                 key[j] = static_cast<uint32_t>(key_of(a, i));
@@ -373,7 +396,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs a) {
         const int across = bins / kEach, groups = kSortThreads / across < kMostGroups ? kSortThreads / across : kMostGroups;
         const int group = threadIdx.x / across, part = threadIdx.x - group * across;
         const C *counts = static_cast<const C *>(a.counts) + part * kEach;
-        int32_t *sums = reinterpret_cast<int32_t *>(warp_count);       // [groups][2][bins]: at most the ranks' table
+        int32_t *sums = reinterpret_cast<int32_t *>(ranker.counts);    // [groups][2][bins]: no more than that holds
         if (group < groups) {
             int32_t all[kEach] = {}, before[kEach] = {};
 #pragma unroll 1
@@ -411,46 +434,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs a) {
                 mine_before += sums[(g * 2 + 1) * bins + bin];
             }
         }
-        to_base[bin] = scan(total) + mine_before;      // (with a barrier, after which the table is free)
+        to_base[bin] = ranker.scan(total) + mine_before;      // (with a barrier, after which the table is free)
     }
     for (int64_t tile = first; tile < end; tile += kSortTile) {
-        for (int i = lane; i < bins; i += 32) mine[i] = 0u;
-        __syncwarp();
         const int n_here = static_cast<int>(end - tile < kSortTile ? end - tile : kSortTile);
         if (tile > first) load(tile);
-        uint32_t rank[kRounds];
-#pragma unroll
-        for (int j = 0; j < kRounds; ++j) {
-            const bool valid = here + 32 * j < n_here;
-            const uint32_t d = key[j] >> a.shift & mask;
-            if (valid) atomicOr(&lanes[d], 1u << lane);
-            __syncwarp();
-            const uint32_t same = lanes[d], had = mine[d], before = __popc(same & lower);
-            __syncwarp();
-            if (valid && before == 0) lanes[d] = 0u, mine[d] = had + __popc(same);
-            __syncwarp();
-            rank[j] = had + before;
-        }
-        __syncthreads();
-        // counts of the warps before, and of the digits before: places in the tile
-        uint32_t run = 0;
-        if (bin < bins) {
-#pragma unroll
-            for (int w = 0; w < kSortWarps; ++w) {
-                const uint32_t c = warp_count[w * kBins + bin];
-                warp_count[w * kBins + bin] = run;
-                run += c;
-            }
-        }
-        local_base[bin] = static_cast<uint32_t>(scan(static_cast<int32_t>(run)));
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kRounds; ++j) {
-            if (here + 32 * j >= n_here) continue;
-            const uint32_t d = key[j] >> a.shift & mask;
-            pairs[local_base[d] + mine[d] + rank[j]] = make_uint2(key[j], at[j]);
-        }
-        __syncthreads();
+        const uint32_t run = ranker.place(key, at, n_here, a.shift, a.bits, pairs);
         for (int i = threadIdx.x; i < n_here; i += kSortThreads) {
             const uint2 v = pairs[i];
             const uint32_t d = v.x >> a.shift & mask;
@@ -501,34 +490,82 @@ __device__ __forceinline__ void write_one(char *out, int64_t at, float v) {
 }
 
 // A thread's columns of a row's part that a block takes, kV of them: neighbouring
-// ones where rows are whole 16-byte chunks, else every cols-th, so that a warp's
-// single elements are neighbours.
+// ones where rows are whole 16-byte chunks; else every cols-th of single FP32 values or
+// pairs of 16-bit ones, so that neighbouring threads' copies of 4 bytes lie side by
+// side.  Pairs of a row that starts between two words are cut from two words each.
 template <typename E, typename P, bool kChunks>
 struct RowPart {
     static constexpr int kV = 16 / kBytes<E>;
-    int first, step, width;
+    static constexpr int kWords = kChunks || kV == 4 ? 4 : 8;    // of a slot
+    int thread, cols, start, width;    // start: of the block's part
 
-    __device__ RowPart(int thread, int cols, int slice, int w) : width(w) {
-        first = slice * cols * kV + (kChunks ? thread * kV : thread);
-        step = kChunks ? 1 : cols;
+    __device__ RowPart(int t, int c, int slice, int w) : thread(t), cols(c), start(slice * c * kV), width(w) {}
+    // from the part's start, of value i
+    __device__ int offset(int i) const {
+        return kChunks ? thread * kV + i : kV == 4 ? thread + i * cols : 2 * (thread + i / 2 * cols) + (i & 1);
     }
-    __device__ int col(int i) const { return first + i * step; }
-    __device__ bool any() const { return first < width; }
-    __device__ void load(const char *row, float (&v)[kV]) const {
+    __device__ int col(int i) const { return start + offset(i); }
+    __device__ bool any() const { return col(0) < width; }
+
+    // Copies of the thread's part of the row at `row` into its slot: words `step` bytes
+    // apart, from ring on.  end: of the tensor.
+    __device__ void fetch(const char *row, const char *end, uint32_t ring, uint32_t step) const {
         if constexpr (kChunks) {
-            load_values<E, kV>(row + first * kBytes<E>, v);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring), "l"(row + col(0) * kBytes<E>) : "memory");
         } else {
 #pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                float one[1] = {0.f};
-                if (col(i) < width) load_values<E, 1>(row + col(i) * kBytes<E>, one);
-                v[i] = one[0];
+            for (int i = 0; i < 4; ++i) {
+                const int at = col(kV == 4 ? i : 2 * i);
+                if (at >= width) break;
+                const char *p = row + at * kBytes<E>;
+                if constexpr (kV == 4) {
+                    copy_word(ring + i * step, p, 4);
+                } else if ((reinterpret_cast<uintptr_t>(p) & 2) == 0) {
+                    copy_word(ring + 2 * i * step, p, end - p < 4 ? 2 : 4);
+                } else {
+                    copy_word(ring + 2 * i * step, p - 2, 4);
+                    if (at + 1 < width) copy_word(ring + (2 * i + 1) * step, p + 2, end - p < 6 ? 2 : 4);
+                }
             }
         }
     }
+    __device__ static void copy_word(uint32_t to, const char *from, int bytes) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    }
+    // What fetch() copied of that row, widened.
+    __device__ void take(const char *row, uint32_t ring, uint32_t step, float2 (&v)[kV / 2]) const {
+        if constexpr (kChunks) {
+            uint4 q;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(ring) : "memory");
+#pragma unroll
+            for (int i = 0; i < kV / 2; ++i) {
+                if constexpr (kV == 4)
+                    v[i] = make_float2(__uint_as_float(word(q, 2 * i)), __uint_as_float(word(q, 2 * i + 1)));
+                else
+                    v[i] = E::to_f2(word(q, i));
+            }
+        } else if constexpr (kV == 4) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                v[i] = make_float2(__uint_as_float(load_word(ring + 2 * i * step)), __uint_as_float(load_word(ring + (2 * i + 1) * step)));
+        } else {
+            // columns are even, so all pairs of a row lie alike
+            const bool between = (reinterpret_cast<uintptr_t>(row) & 2) != 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t low = load_word(ring + 2 * i * step);
+                v[i] = E::to_f2(between ? __funnelshift_r(low, load_word(ring + (2 * i + 1) * step), 16) : low);
+            }
+        }
+    }
+    __device__ static uint32_t load_word(uint32_t at) {
+        uint32_t w;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+        return w;
+    }
     __device__ void store(char *row, const float (&v)[kV]) const {
         if constexpr (kChunks) {
-            store_values<P, kV>(row + first * kBytes<P>, v);
+            store_values<P, kV>(row + col(0) * kBytes<P>, v);
         } else {
 #pragma unroll
             for (int i = 0; i < kV; ++i)
@@ -537,160 +574,150 @@ struct RowPart {
     }
 };
 
-// A block of cols x slots threads: a slot takes neighbouring indices of the piece, a
-// thread a part of their rows' columns.  E: grad's format, P: the table's gradient's.
+// The first of [from, to) that is so, where all behind it are; `to` for none.
+template <typename F>
+__device__ __forceinline__ int first_of(int from, int to, F so) {
+    while (from < to) {
+        const int middle = (from + to) / 2;
+        if (so(middle)) to = middle; else from = middle + 1;
+    }
+    return from;
+}
+
+// How a block lays out its shared memory for sums: slots of rows on their way, 16 or
+// 32 bytes a thread, kAhead or half as many; then [slots][2][wide] sums of the slots' ends.
+template <typename E, bool kChunks>
+struct SumLayout {
+    static constexpr int kWords = RowPart<E, E, kChunks>::kWords;
+    static constexpr int kDeep = kWords == 8 ? kAhead / 2 : kAhead;
+    __host__ __device__ static constexpr int ring_bytes(int threads) { return kDeep * threads * kWords * 4; }
+};
+
+// The sums of `count` tokens (row, position) in their rows' order, `each` by each to
+// the block's slots: runs that end inside a slot are written, the others' parts left in
+// head (of a run that began before the slot) and tail (of one that began in it).
+// tokens[-1] and tokens[count] are not of the same row as a run that is to end there.
+template <typename E, typename P, bool kChunks, int kThreads>
+__device__ void sum_slots(const SumArgs &a, const RowPart<E, P, kChunks> &part, const int2 *tokens, int count, int slot,
+                          int each, uint32_t ring, float *head, float *tail) {
+    using Part = RowPart<E, P, kChunks>;
+    constexpr int kV = Part::kV, kDeep = SumLayout<E, kChunks>::kDeep;
+    // slots: [deep][words][threads], or 16 bytes a thread
+    constexpr uint32_t kStep = kThreads * 4, kRingStep = kThreads * Part::kWords * 4;
+    const int t0 = slot * each, mine_count = count - t0 < each ? count - t0 : each;
+    if (mine_count <= 0 || !part.any()) return;
+    const uint32_t row_bytes = static_cast<uint32_t>(a.width) * kBytes<E>, out_bytes = static_cast<uint32_t>(a.width) * kBytes<P>;
+    const char *end = a.grad + a.n * row_bytes;
+    const int2 *mine = tokens + t0;
+    const int wide = a.cols * kV;
+    float2 acc[kV / 2];
+#pragma unroll
+    for (int i = 0; i < kV / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+    int32_t cur = mine[0].x;
+    bool open = mine[-1].x == cur;    // the run began before this slot
+    auto flush = [&](float *place) {
+        if (place) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i) place[slot * wide + part.offset(i)] = i & 1 ? acc[i / 2].y : acc[i / 2].x;
+        } else {
+            float v[kV];
+#pragma unroll
+            for (int i = 0; i < kV; ++i) v[i] = (i & 1 ? acc[i / 2].y : acc[i / 2].x) * a.scale;
+            part.store(a.out + static_cast<int64_t>(cur) * out_bytes, v);
+        }
+    };
+    int2 coming[kDeep];         // rows on their way
+    auto row_at = [&](int32_t at) { return a.grad + static_cast<uint64_t>(static_cast<uint32_t>(at)) * row_bytes; };
+    auto fetch = [&](int t, int j) {
+        if (t < mine_count) {
+            coming[j] = mine[t];
+            part.fetch(row_at(coming[j].y), end, ring + j * kRingStep, kStep);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int j = 0; j < kDeep; ++j) fetch(j, j);
+    for (int t = 0; t < mine_count; t += kDeep) {
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) {
+            cp_async_wait<kDeep - 1>();
+            if (t + j < mine_count) {
+                float2 v[kV / 2];
+                part.take(row_at(coming[j].y), ring + j * kRingStep, kStep, v);
+                if (coming[j].x != cur) {
+                    flush(open ? head : nullptr);
+                    open = false;
+                    cur = coming[j].x;
+#pragma unroll
+                    for (int i = 0; i < kV / 2; ++i) acc[i] = v[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kV / 2; ++i) acc[i] = __fadd2_rn(acc[i], v[i]);
+                }
+            }
+            fetch(t + j + kDeep, j);
+        }
+    }
+    cp_async_wait<0>();
+    flush(open ? head : mine[mine_count].x == cur ? tail : nullptr);
+}
+
+// The slots' ends, in their order, value f of the block's part of a row.  A run that
+// began before the tokens, or goes on behind them, is left in `left` ([2][width]).
+template <typename P>
+__device__ void join_slots(const SumArgs &a, const int2 *tokens, int count, int slots, int each, const float *head,
+                           const float *tail, int wide, int f, int c, float *left) {
+    float run = 0.f;
+    bool before = tokens[-1].x == tokens[0].x;      // the open run began before them
+    for (int s = 0; s * each < count; ++s) {
+        const int b = s * each, e = count - b < each ? count : b + each;
+        const int32_t key = tokens[b].x, last = tokens[e - 1].x;
+        const bool on = tokens[e].x == last;        // the slot's last run goes on behind it
+        if (tokens[b - 1].x == key) {
+            run += head[s * wide + f];
+            if (on && last == key) continue;
+            if (before) left[c] = run;
+            else write_one<P>(a.out, key * static_cast<int64_t>(a.width) + c, run * a.scale);
+            before = false;
+            run = 0.f;
+        }
+        if (on) run = tail[s * wide + f];
+    }
+    if (tokens[count].x == tokens[count - 1].x) left[(before ? 0 : a.width) + c] = run;
+}
+
+// A block takes a piece of the sorted order.  E: grad's format, P: the table's
+// gradient's.
 template <typename E, typename P, bool kChunks>
 __global__ void __launch_bounds__(kSumThreads) sum_runs(const SumArgs a) {
     extern __shared__ __align__(16) char memory[];
-    using Part = RowPart<E, P, kChunks>;
-    constexpr int kV = Part::kV;
-    const int slots = blockDim.y, wide = a.cols * kV;            // values of a row here
-    const int thread = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
-    // slots of rows on their way: [ahead][threads], 16 bytes each (kChunks alone)
-    constexpr int kRingStep = kSumThreads * 16;
-    const uint32_t ring = shared_address(memory) + thread * 16;
-    constexpr int kRingBytes = kChunks ? kAhead * kRingStep : 0;
-    int2 *tokens = reinterpret_cast<int2 *>(memory + kRingBytes) + 1;    // [-1] ... [piece]: row, position
-    float *head = reinterpret_cast<float *>(tokens + a.piece + 1);       // [slots][wide]
-    float *tail = head + slots * wide;
+    using Layout = SumLayout<E, kChunks>;
+    constexpr int kV = 16 / kBytes<E>;
+    const int thread = threadIdx.x, slot = thread / a.cols, col_thread = thread - slot * a.cols;
+    const int slots = a.piece / a.each, wide = a.cols * kV;
+    const uint32_t ring = shared_address(memory) + thread * (kChunks ? 16 : 4);
+    int2 *tokens = reinterpret_cast<int2 *>(memory + Layout::ring_bytes(kSumThreads)) + 1;    // [-1] ... [piece]
+    float *head = reinterpret_cast<float *>(tokens + a.piece + 1), *tail = head + slots * wide;
     pdl_prologue();
     const int64_t first = static_cast<int64_t>(blockIdx.x) * a.piece;
-    for (int i = thread - 1; i <= a.piece; i += threads) {
+    // no row: before the first index, and behind the last that names one
+    for (int i = thread - 1; i <= a.piece; i += blockDim.x) {
         const int64_t t = first + i;
-        // no row: before the first index, and from the first that names none
-        const bool some = t >= 0 && t < a.n;
-        tokens[i] = some ? make_int2(__ldcg(a.keys + t), __ldcg(a.at + t)) : make_int2(a.n_rows, 0);
+        const int2 token = t >= 0 && t < a.n ? make_int2(__ldcg(a.keys + t), __ldcg(a.at + t)) : make_int2(a.n_rows, 0);
+        tokens[i] = token.x < a.n_rows ? token : make_int2(-1, 0);
     }
     __syncthreads();
-    if (tokens[0].x >= a.n_rows) return;
-    const Part part(threadIdx.x, a.cols, blockIdx.y, a.width);
-    const uint32_t row_bytes = static_cast<uint32_t>(a.width) * kBytes<E>;
-    const int t0 = threadIdx.y * a.each;
-    if (tokens[t0].x < a.n_rows && part.any()) {
-        const uint32_t out_bytes = static_cast<uint32_t>(a.width) * kBytes<P>;
-        const int2 *mine = tokens + t0;
-        float2 acc[kV / 2];
-#pragma unroll
-        for (int i = 0; i < kV / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-        int32_t cur = mine[0].x;
-        bool open = mine[-1].x == cur;    // the run began before this slot
-        auto flush = [&](float *place) {
-            if (place) {
-#pragma unroll
-                for (int i = 0; i < kV; ++i)
-                    place[threadIdx.y * wide + (kChunks ? threadIdx.x * kV + i : threadIdx.x + i * a.cols)] =
-                        i & 1 ? acc[i / 2].y : acc[i / 2].x;
-            } else {
-                float v[kV];
-#pragma unroll
-                for (int i = 0; i < kV; ++i) v[i] = (i & 1 ? acc[i / 2].y : acc[i / 2].x) * a.scale;
-                part.store(a.out + static_cast<int64_t>(cur) * out_bytes, v);
-            }
-        };
-        // the run of row k takes v, after the one before is ended
-        auto take = [&](int32_t k, const float2 (&v)[kV / 2]) {
-            if (k != cur) {
-                flush(open ? head : nullptr);
-                open = false;
-                cur = k;
-#pragma unroll
-                for (int i = 0; i < kV / 2; ++i) acc[i] = v[i];
-                return;
-            }
-#pragma unroll
-            for (int i = 0; i < kV / 2; ++i) acc[i] = __fadd2_rn(acc[i], v[i]);
-        };
-        if constexpr (kChunks) {
-            const char *from = a.grad + part.first * kBytes<E>;
-            int32_t key[kAhead];         // of the rows on their way; n_rows: none
-            auto fetch = [&](int t, int j) {
-                key[j] = a.n_rows;
-                if (t < a.each) {
-                    const int2 token = mine[t];
-                    key[j] = token.x;
-                    if (token.x < a.n_rows)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + j * kRingStep),
-                                     "l"(from + static_cast<uint64_t>(static_cast<uint32_t>(token.y)) * row_bytes) : "memory");
-                }
-                cp_async_commit();
-            };
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) fetch(j, j);
-            for (int t = 0; t < a.each; t += kAhead) {
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    cp_async_wait<kAhead - 1>();
-                    if (key[j] < a.n_rows) {
-                        uint4 q;
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(ring + j * kRingStep) : "memory");
-                        float2 v[kV / 2];
-#pragma unroll
-                        for (int i = 0; i < kV / 2; ++i) {
-                            if constexpr (kV == 4)
-                                v[i] = make_float2(__uint_as_float(word(q, 2 * i)), __uint_as_float(word(q, 2 * i + 1)));
-                            else
-                                v[i] = E::to_f2(word(q, i));
-                        }
-                        take(key[j], v);
-                    }
-                    fetch(t + j + kAhead, j);
-                }
-            }
-            cp_async_wait<0>();
-        } else {
-            constexpr int kBatch = 4;
-            for (int t = 0; t < a.each; t += kBatch) {
-                float v[kBatch][kV];
-                int32_t k[kBatch];
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    const int2 token = t + j < a.each ? mine[t + j] : make_int2(a.n_rows, 0);
-                    k[j] = token.x;
-                    if (k[j] < a.n_rows)
-                        part.load(a.grad + static_cast<uint64_t>(static_cast<uint32_t>(token.y)) * row_bytes, v[j]);
-                }
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    if (k[j] >= a.n_rows) continue;
-                    float2 pairs[kV / 2];
-#pragma unroll
-                    for (int i = 0; i < kV / 2; ++i) pairs[i] = make_float2(v[j][2 * i], v[j][2 * i + 1]);
-                    take(k[j], pairs);
-                }
-            }
-        }
-        flush(open ? head : mine[a.each].x == cur ? tail : nullptr);
-    }
+    // sorted, so those that name a row come first
+    const int count = first_of(0, a.piece, [&](int i) { return tokens[i].x < 0; });
+    if (count == 0) return;
+    const RowPart<E, P, kChunks> part(col_thread, a.cols, blockIdx.y, a.width);
+    if (slot < slots) sum_slots<E, P, kChunks, kSumThreads>(a, part, tokens, count, slot, a.each, ring, head, tail);
     __syncthreads();
-    // The slots' ends, in their order.  A run that began before this piece, or
-    // goes on after it, is left for the last launch.
-    float *left = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.width;
-    for (int f = thread; f < wide; f += threads) {
+    // what reaches over the piece's ends is for the last launch
+    for (int f = thread; f < wide; f += blockDim.x) {
         const int c = blockIdx.y * wide + f;
         if (c >= a.width) break;
-        float run = 0.f;
-        bool before = tokens[-1].x == tokens[0].x;      // the open run began before the piece
-        for (int s = 0; s < slots; ++s) {
-            const int b = s * a.each, e = b + a.each;
-            if (tokens[b].x >= a.n_rows) break;
-            const int32_t last = tokens[e - 1].x;
-            if (tokens[b - 1].x == tokens[b].x) {
-                run += head[s * wide + f];
-                // does it end here?
-                if (!(last == tokens[b].x && tokens[e].x == last)) {
-                    if (before) left[c] = run;
-                    else write_one<P>(a.out, tokens[b].x * static_cast<int64_t>(a.width) + c, run * a.scale);
-                    before = false;
-                    run = 0.f;
-                } else {
-                    continue;
-                }
-            }
-            if (last < a.n_rows && tokens[e].x == last) run = tail[s * wide + f];
-        }
-        const int32_t last = tokens[a.piece - 1].x;
-        if (last < a.n_rows && tokens[a.piece].x == last) left[(before ? 0 : a.width) + c] = run;
+        join_slots<P>(a, tokens, count, slots, a.each, head, tail, wide, f, c, a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.width);
     }
 }
 
@@ -797,6 +824,115 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a) {
     }
 }
 
+// ---------------------------------------------------------------- few indices --
+
+// Where a block can sort all indices, every block does, and takes the runs that begin
+// in its share of the order, whole ones, so that nothing is left for another launch:
+// one in place of five.  The rows that no index names are a share of the table's rows,
+// found with a bit for each in shared memory.  180 indices into 366 rows of 192 take
+// 7.1 us so, 12.4 in five launches; 2048 into 300 rows 10.4 and 13.3, but all of them
+// into one row, which is one block's, 21 and 13: half as many are even there.
+constexpr int kFew = 1024;
+static_assert(kFew <= kSortTile, "a tile of the sort");
+
+template <typename E, typename P, bool kChunks>
+__global__ void __launch_bounds__(kSortThreads) sum_few(const SumArgs a, const int32_t *idx, int passes, int bits) {
+    extern __shared__ __align__(16) char memory[];
+    __shared__ int32_t warp_sums[kSortWarps];
+    __shared__ uint32_t base[kBins];
+    using Layout = SumLayout<E, kChunks>;
+    constexpr int kV = 16 / kBytes<E>;
+    static_assert(Layout::ring_bytes(kSortThreads) <= Ranker::kTableBytes, "the ring takes the sort's tables' place");
+    int2 *tokens = reinterpret_cast<int2 *>(memory) + 2;      // [-1] ... [n]
+    char *tables = memory + (kFew + 4) * 8;
+    uint2 *pairs = reinterpret_cast<uint2 *>(tokens);
+    const Ranker ranker(tables, warp_sums, base);
+    const int n = static_cast<int>(a.n), thread = threadIdx.x;
+    ranker.clear(1 << bits);
+    pdl_prologue();
+    uint32_t key[kRounds], at[kRounds];
+#pragma unroll
+    for (int j = 0; j < kRounds; ++j) {
+        const int i = Ranker::first() + 32 * j;
+        key[j] = at[j] = 0u;
+        if (i < n) {
+            const int32_t k = __ldg(idx + i);
+            key[j] = static_cast<uint32_t>(k >= 0 && k < a.n_rows ? k : a.n_rows), at[j] = i;
+            if ((k < -1 || k >= a.n_rows) && blockIdx.x == 0) atomicOr(&g_embedding_error, 1u);
+        }
+    }
+    for (int pass = 0;;) {
+        ranker.place(key, at, n, pass * bits, bits, pairs);
+        if (++pass == passes) break;
+#pragma unroll
+        for (int j = 0; j < kRounds; ++j) {
+            const int i = Ranker::first() + 32 * j;
+            if (i < n) key[j] = pairs[i].x, at[j] = pairs[i].y;
+        }
+    }
+    const int named = first_of(0, n, [&](int i) { return tokens[i].x >= a.n_rows; });
+    __syncthreads();
+    if (thread == 0) tokens[-1].x = tokens[named].x = -1;
+    __syncthreads();
+
+    // the runs that begin in this block's share of the order
+    const int blocks = gridDim.x, block = blockIdx.x;
+    auto begin = [&](int64_t b) {
+        const int i = static_cast<int>(b * named / blocks);
+        if (i == 0 || i >= named || tokens[i].x != tokens[i - 1].x) return i;
+        const int32_t k = tokens[i].x;
+        return first_of(i, named, [&](int t) { return tokens[t].x > k; });
+    };
+    const int from = begin(block), count = begin(block + 1) - from;
+    if (count > 0) {
+        const int slots = kSortThreads / a.cols < kMostSlots ? kSortThreads / a.cols : kMostSlots;
+        const int slot = thread / a.cols, wide = a.cols * kV;
+        const int each = (count + slots - 1) / slots;
+        const uint32_t ring = shared_address(tables) + thread * (kChunks ? 16 : 4);
+        float *head = reinterpret_cast<float *>(tables + Ranker::kTableBytes), *tail = head + slots * wide;
+        for (int slice = 0; slice * wide < a.width; ++slice) {
+            const RowPart<E, P, kChunks> part(thread - slot * a.cols, a.cols, slice, a.width);
+            if (slot < slots)
+                sum_slots<E, P, kChunks, kSortThreads>(a, part, tokens + from, count, slot, each, ring, head, tail);
+            __syncthreads();
+            for (int f = thread; f < wide; f += kSortThreads) {
+                const int c = slice * wide + f;
+                if (c >= a.width) break;
+                join_slots<P>(a, tokens + from, count, slots, each, head, tail, wide, f, c, nullptr);
+            }
+            __syncthreads();
+        }
+    }
+
+    // the zeros: a bit for each of some rows, set where an index names it
+    constexpr int64_t kBits = kBins * 32;
+    const int64_t row0 = static_cast<int64_t>(a.n_rows) * block / blocks, row1 = static_cast<int64_t>(a.n_rows) * (block + 1) / blocks;
+    const int lane = thread & 31, warp = thread >> 5;
+    for (int64_t r0 = row0; r0 < row1; r0 += kBits) {
+        const int64_t r1 = r0 + kBits < row1 ? r0 + kBits : row1;
+        __syncthreads();
+        base[thread] = 0u;
+        __syncthreads();
+        const int lo = first_of(0, named, [&](int i) { return tokens[i].x >= r0; });
+        const int hi = first_of(lo, named, [&](int i) { return tokens[i].x >= r1; });
+        for (int i = lo + thread; i < hi; i += kSortThreads) {
+            const int bit = static_cast<int>(tokens[i].x - r0);
+            atomicOr(&base[bit / 32], 1u << bit % 32);
+        }
+        __syncthreads();
+        for (int64_t r = r0 + warp; r < r1; r += kSortWarps) {
+            const int bit = static_cast<int>(r - r0);
+            if (base[bit / 32] >> bit % 32 & 1u) continue;
+            char *row = a.out + r * a.width * kBytes<P>;
+            if constexpr (kChunks) {
+                for (int i = lane; i < a.width * kBytes<P> / 16; i += 32) st_stream(row + 16 * i, make_uint4(0u, 0u, 0u, 0u));
+            } else {
+                for (int i = lane; i < a.width; i += 32) write_one<P>(row, i, 0.f);
+            }
+        }
+    }
+}
+
 __global__ void __launch_bounds__(256) fill_zeros(char *p, int64_t n, int bytes) {
     pdl_prologue();
     write_zeros(p, n, bytes, static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, gridDim.x * 256ll);
@@ -813,6 +949,7 @@ bool sizes_ok(int64_t n_idx, int64_t n_rows) {
 
 // How a gradient is cut, and where its parts lie in the workspace.
 struct Plan {
+    bool few;
     int passes, bits, sort_blocks;   // of the sort
     int64_t range;
     int slices, cols, slots, each, piece;
@@ -834,8 +971,13 @@ Plan plan_of(int64_t n, int64_t n_rows, int32_t width, int v) {
     z.sort_blocks = n ? static_cast<int>(ceil_div(n, z.range)) : 0;
     z.count_bytes = z.range < 65536 ? 2 : 4;
     const int parts = static_cast<int>(ceil_div(width, v));
-    z.slices = static_cast<int>(ceil_div(parts, kSumThreads));
+    z.few = n <= kFew;
+    z.slices = static_cast<int>(ceil_div(parts, z.few ? kSortThreads : kSumThreads));
     z.cols = static_cast<int>(ceil_div(parts, z.slices));
+    if (z.few) {
+        z.bytes = n ? 16 : 0;
+        return z;
+    }
     z.slots = kSumThreads / z.cols < kMostSlots ? kSumThreads / z.cols : kMostSlots;
     // some six blocks an SM, of slots of 8 to 64 indices
     const int64_t want = ceil_div(n, static_cast<int64_t>(z.slots) * 912);
@@ -866,10 +1008,11 @@ int64_t workspace_of(int64_t n, int64_t n_rows, int32_t width) {
 
 template <typename E, typename P, bool kChunks>
 wgs_status run_sums(const SumArgs &a, const Plan &z, int sms, cudaStream_t stream) {
-    const int wide = z.cols * (16 / kBytes<E>);
-    const int smem = (kChunks ? kAhead * kSumThreads * 16 : 0) + 8 * (z.piece + 2) + 8 * z.slots * wide;
+    constexpr int kV = 16 / kBytes<E>;
+    using Layout = SumLayout<E, kChunks>;
+    const int smem = Layout::ring_bytes(kSumThreads) + 8 * (z.piece + 2) + 8 * z.slots * z.cols * kV;
     static_assert(kMostPiece == 64 * kMostSlots &&
-                      kAhead * kSumThreads * 16 + 8 * (kMostPiece + 2) + 8 * kSumThreads * 8 <= 66 << 10,
+                      Layout::ring_bytes(kSumThreads) + 8 * (kMostPiece + 2) + 8 * kSumThreads * kV <= 66 << 10,
                   "shared memory of a block");
     auto kernel = sum_runs<E, P, kChunks>;
     // (as the layer norm's)
@@ -878,11 +1021,32 @@ wgs_status run_sums(const SumArgs &a, const Plan &z, int sms, cudaStream_t strea
         cudaGetLastError();
         return WGS_ERR_LAUNCH;
     }
-    const wgs_status st = launch(kernel, dim3(static_cast<unsigned>(z.pieces), z.slices), dim3(z.cols, z.slots),
+    const wgs_status st = launch(kernel, dim3(static_cast<unsigned>(z.pieces), z.slices), dim3(z.cols * z.slots),
                                  static_cast<size_t>(smem), stream, a);
     if (st != WGS_OK || z.pieces == 1) return st;
     const int64_t blocks = z.pieces < sms ? z.pieces : sms;
     return launch(join_runs<P>, dim3(static_cast<unsigned>(blocks)), dim3(kJoinThreads), 0, stream, a);
+}
+
+template <typename E, typename P, bool kChunks>
+wgs_status run_few(const SumArgs &a, const int32_t *idx, const Plan &z, int sms, cudaStream_t stream) {
+    constexpr int kV = 16 / kBytes<E>;
+    const int slots = kSortThreads / z.cols < kMostSlots ? kSortThreads / z.cols : kMostSlots;
+    const int smem = (kFew + 4) * 8 + Ranker::kTableBytes + 8 * slots * z.cols * kV;
+    auto kernel = sum_few<E, P, kChunks>;
+    // (as the layer norm's)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (kFew + 4) * 8 + Ranker::kTableBytes + 8 * kSortThreads * kV) != cudaSuccess) {
+        cudaGetLastError();
+        return WGS_ERR_LAUNCH;
+    }
+    // an index a slot, or 8 KB of zeros a block
+    const int64_t bytes = static_cast<int64_t>(a.n_rows) * a.width * kBytes<P>;
+    int64_t blocks = ceil_div(a.n, slots);
+    if (blocks < ceil_div(bytes, 8192)) blocks = ceil_div(bytes, 8192);
+    if (blocks > sms) blocks = sms;
+    return launch(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kSortThreads), static_cast<size_t>(smem), stream, a, idx,
+                  z.passes, z.bits);
 }
 
 // 16 bytes of gradient at a time where all rows, and those of the output, start
@@ -892,7 +1056,12 @@ bool in_chunks(const void *grad, const void *out, int32_t width, int64_t eb, int
 }
 
 template <typename E>
-wgs_status run_format(const SumArgs &a, const Plan &z, bool chunks, bool p32, int sms, cudaStream_t stream) {
+wgs_status run_format(const SumArgs &a, const int32_t *idx, const Plan &z, bool chunks, bool p32, int sms,
+                      cudaStream_t stream) {
+    if (z.few && chunks)
+        return p32 ? run_few<E, F32, true>(a, idx, z, sms, stream) : run_few<E, E, true>(a, idx, z, sms, stream);
+    if (z.few)
+        return p32 ? run_few<E, F32, false>(a, idx, z, sms, stream) : run_few<E, E, false>(a, idx, z, sms, stream);
     if (chunks) return p32 ? run_sums<E, F32, true>(a, z, sms, stream) : run_sums<E, E, true>(a, z, sms, stream);
     return p32 ? run_sums<E, F32, false>(a, z, sms, stream) : run_sums<E, E, false>(a, z, sms, stream);
 }
@@ -906,7 +1075,7 @@ wgs_status sort_indices(SortArgs &s, const Plan &z, char *ws, char *out, int64_t
     auto order = z.count_bytes == 2 ? sort_place<uint16_t> : sort_place<uint32_t>;
     // a share of the zeros in each launch, 64 bytes a thread or more
     const int64_t share = ceil_div(ceil_div(bytes, 1 + z.passes), 16) * 16, most = 4 * sms - z.sort_blocks;
-    const int smem = kSortTile * 8 + kSortWarps * kBins * 8;
+    const int smem = kSortTile * 8 + Ranker::kTableBytes;
     // (as the layer norm's)
     if (cudaFuncSetAttribute(order, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         cudaGetLastError();
@@ -940,10 +1109,10 @@ wgs_status sort_indices(SortArgs &s, const Plan &z, char *ws, char *out, int64_t
 
 template <typename T, typename E>
 wgs_status run_lookup(LookupArgs a, int32_t width, int sms, cudaStream_t stream) {
-    constexpr int kV = 16 / kBytes<E>;
-    const bool chunks = in_chunks(a.table, a.out, width, kBytes<T>, kBytes<E>);
+    constexpr int kV = 16 / kBytes<T>;
+    const bool chunks = width % kV == 0 && aligned16(a.table) && aligned_to(a.out, kV * kBytes<E>);
     a.row_chunks = static_cast<int>(ceil_div(width, kV)), a.width = width;
-    const int64_t blocks = ceil_div(a.n * a.row_chunks, kLookupThreads * kLookupChunks);
+    const int64_t blocks = ceil_div(a.n * a.row_chunks, kLookupThreads);
     const int64_t most = static_cast<int64_t>(sms) * kLookupBlocksPerSm;
     return launch(chunks ? embedding_lookup<T, E, true> : embedding_lookup<T, E, false>,
                   dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(kLookupThreads), 0, stream, a);
@@ -1030,15 +1199,16 @@ extern "C" wgs_status embedding_bwd(const void *grad, const int32_t *idx, void *
     char *ws = static_cast<char *>(workspace);
     SortArgs s = {};
     s.idx = idx, s.n = n_idx, s.n_rows = static_cast<int32_t>(n_rows);
-    st = sort_indices(s, z, ws, static_cast<char *>(grad_table), tbytes, static_cast<int>(tb), dev.sm_count, stream);
-    if (st != WGS_OK || n_rows == 0) return st;
+    if (!z.few)
+        st = sort_indices(s, z, ws, static_cast<char *>(grad_table), tbytes, static_cast<int>(tb), dev.sm_count, stream);
+    if (st != WGS_OK || (n_rows == 0 && !z.few)) return st;
     SumArgs a = {};
     a.grad = static_cast<const char *>(grad), a.keys = s.keys, a.at = s.at;
     a.out = static_cast<char *>(grad_table), a.part = reinterpret_cast<float *>(ws + z.part);
     a.n = n_idx, a.pieces = z.pieces, a.n_rows = static_cast<int32_t>(n_rows), a.width = width, a.cols = z.cols;
     a.each = z.each, a.piece = z.piece, a.scale = scale;
     const bool p32 = table_dtype == WGS_F32;
-    if (dtype == WGS_F32) return run_format<F32>(a, z, chunks, true, dev.sm_count, stream);
-    if (dtype == WGS_F16) return run_format<Fp16>(a, z, chunks, p32, dev.sm_count, stream);
-    return run_format<Bf16>(a, z, chunks, p32, dev.sm_count, stream);
+    if (dtype == WGS_F32) return run_format<F32>(a, idx, z, chunks, true, dev.sm_count, stream);
+    if (dtype == WGS_F16) return run_format<Fp16>(a, idx, z, chunks, p32, dev.sm_count, stream);
+    return run_format<Bf16>(a, idx, z, chunks, p32, dev.sm_count, stream);
 }
