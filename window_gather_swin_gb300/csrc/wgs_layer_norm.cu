@@ -13,10 +13,10 @@ namespace wgs {
 
 namespace {
 
-// Blocks an SM: two, whose waits fall at different times, where the registers of
-// both fit and two stages beside the weights do.
+// Two blocks an SM, whose waits fall at different times, where two stages beside the
+// weights fit twice; of fewer warps where a thread's 32 columns need the registers.
 template <typename E, int kC>
-constexpr int kBlocksPerSm = kC * 16 / kBytes<E> > 24 ? 1 : 2;
+constexpr int kBlockWarps = kC * 16 / kBytes<E> > 24 ? 8 : kWarps;
 constexpr int kHalfOfSm = 112 << 10, kMostOfSm = 216 << 10;   // shared memory
 
 // 1 / sqrt(v): the hardware's approximation and one step of Newton's method, which
@@ -30,7 +30,7 @@ __device__ __forceinline__ float reciprocal_root(float v) {
 // small whatever the mean's size, and their own mean, which m's rounding leaves,
 // comes off the variance and the result.
 template <typename E, int kC, int kTeam, bool kWhole>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm<E, kC>) layer_norm_forward(const LayerNormArgs a) {
+__global__ void __launch_bounds__(kBlockWarps<E, kC> * 32, 2) layer_norm_forward(const LayerNormArgs a) {
     extern __shared__ __align__(16) char shared[];
     __shared__ float2 exchange[2][kWarps];
     __shared__ __align__(16) char edge_bytes[kWhole ? 16 : kEdgeBytes];
@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<E, kC>) layer_norm_forw
     char *mask_words = reinterpret_cast<char *>(inside + all);
     const uint32_t masks = shared_address(mask_words);
     const uint32_t edges = shared_address(edge_bytes);
+    p.look_ahead();
     p.clear_slots();
     pdl_prologue();
     for (int s = 0; s < a.stages; ++s) p.fetch();
@@ -69,9 +70,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<E, kC>) layer_norm_forw
             p.store(a.total, edges, x);
         }
         p.fetch();
-        float2 s = x[0];
+        // a chain of additions a chunk
+        float2 s = both(0.f);
 #pragma unroll
-        for (int i = 1; i < kPairs; ++i) s = add2(s, x[i]);
+        for (int c = 0; c < kC; ++c) {
+            float2 t = x[c * kHalf];
+#pragma unroll
+            for (int i = 1; i < kHalf; ++i) t = add2(t, x[c * kHalf + i]);
+            s = c ? add2(s, t) : t;
+        }
         const float m = p.sum(s.x + s.y) * a.inv;
         float2 d = both(0.f), q = both(0.f);
 #pragma unroll
@@ -79,13 +86,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<E, kC>) layer_norm_forw
             float2 in[kHalf];
             if (!kWhole) p.kept(inside, c, in);
             const bool held = !kWhole || p.held(c);
+            float2 dc = both(0.f), qc = both(0.f);
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) {
                 float2 &v = x[c * kHalf + j];
                 // outside the row the distance is 0
                 v = kWhole ? add2(v, both(held ? -m : 0.f)) : fma2(in[j], both(-m), v);
-                d = add2(d, v), q = fma2(v, v, q);
+                dc = j ? add2(dc, v) : v, qc = j ? fma2(v, v, qc) : mul2(v, v);
             }
+            d = c ? add2(d, dc) : dc, q = c ? add2(q, qc) : qc;
         }
         const float2 t = p.sum(make_float2(d.x + d.y, q.x + q.y));
         const float m1 = t.x * a.inv;
@@ -120,9 +129,10 @@ wgs_status run_unit(LayerNormArgs a, cudaStream_t stream) {
     a.team_warps = kTeam == 0 ? static_cast<int>(ceil_div(a.chunks, 32 * kC)) : 1;
     // weight and bias, and what tells a ragged row's own
     a.kept_bytes = kC * (kTeam == 0 ? 32 * a.team_warps : kTeam) * (kWhole ? 8 * P::kV : 12 * P::kV + 16);
-    const int most = kWarps / a.team_warps * a.team_warps * a.tensors * kC * 512;
-    const bool two = kBlocksPerSm<E, kC> == 2 && a.kept_bytes + 2 * most <= kHalfOfSm;
-    const Cut cut = cut_rows(a, P::kRowsPerPass, (two ? 2 : 1) * dev.sm_count);
+    constexpr int kMost = kBlockWarps<E, kC>;
+    const int most = kMost / a.team_warps * a.team_warps * a.tensors * kC * 512;
+    const bool two = a.kept_bytes + 2 * most <= kHalfOfSm;
+    const Cut cut = cut_rows(a, P::kRowsPerPass, kMost, (two ? 2 : 1) * dev.sm_count);
     const int stage = cut.threads * a.tensors * kC * 16, fit = ((two ? kHalfOfSm : kMostOfSm) - a.kept_bytes) / stage;
     a.stages = fit < kMaxStages ? fit : kMaxStages;
     const int smem = a.kept_bytes + a.stages * stage;

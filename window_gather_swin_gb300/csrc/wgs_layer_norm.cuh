@@ -101,6 +101,8 @@ struct Place {
     int64_t pass, passes, pass_step;
     uint32_t slots, stage_bytes, present, coming;   // this thread's; stages read and filled next
     int64_t next_row, next_at;  // to be fetched
+    uint32_t held_bits = 0, full_bits = 0;      // of a ragged row's chunks, see held() and full()
+    bool first_here, last_here; // a ragged row's partial first and last chunk are this warp's (team's)
     float2 (*meet)[kWarps];     // [2][warps]: sums of the unit's warps
     int turn = 0;
 
@@ -127,17 +129,35 @@ struct Place {
         stage_bytes = a.tensors * kC * 512;
         slots = ring + warp * a.stages * stage_bytes + (threadIdx.x & 31) * 16;
         present = coming = 0;
+        if constexpr (!kWhole) {
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const int col = column(c);
+                held_bits |= static_cast<uint32_t>(col < a.width) << c;
+                full_bits |= static_cast<uint32_t>(col >= 0 && col + kV <= a.width) << c;
+            }
+            const unsigned firsts = __ballot_sync(0xffffffffu, column(0) < 0);
+            const unsigned lasts = __ballot_sync(0xffffffffu, last_chunk() < kC);
+            const unsigned mine = kMulti || kTeam == 32 ? 0xffffffffu : ((1u << (kTeam & 31)) - 1) << ((threadIdx.x & 31) / kTeam_or_32() * kTeam);
+            first_here = (firsts & mine) != 0, last_here = (lasts & mine) != 0;
+        }
+    }
+    __device__ static constexpr int kTeam_or_32() { return kMulti ? 32 : kTeam; }
+    // This thread's chunk that ends behind the row but begins in it (kC: none).
+    __device__ int last_chunk() const {
+        int which = kC;
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+            if (column(c) >= 0 && column(c) < a.width && column(c) + kV > a.width) which = c;
+        return which;
     }
     __device__ int column_thread() const { return kMulti ? thread : thread & (kTeam - 1); }
     __device__ int column_threads() const { return kMulti ? warps * 32 : kTeam; }
     __device__ int capacity() const { return kC * column_threads(); }     // chunks of a unit
     __device__ int chunk(int c) const { return c * column_threads() + column_thread(); }
     __device__ int column(int c) const { return chunk(c) * kV - lead; }   // of its first element
-    __device__ bool held(int c) const { return column(c) < a.width; }
-    __device__ bool full(int c) const {
-        const int col = column(c);
-        return col >= 0 && col + kV <= a.width;
-    }
+    __device__ bool held(int c) const { return kWhole ? column(c) < a.width : (held_bits >> c & 1u) != 0; }
+    __device__ bool full(int c) const { return (full_bits >> c & 1u) != 0; }
     __device__ bool there() const { return row < a.rows; }
     __device__ void advance() {
         pass += pass_step, row += row_step, at += step;
@@ -192,8 +212,9 @@ struct Place {
                 if constexpr (kWhole) {
                     copy_part(slot, p, is_there ? 16 : 0);
                 } else if (a.together) {
-                    const int left = (a.width - column(c)) * kBytes<E>;
-                    copy_part(slot, p, !is_there ? 0 : left >= 16 || next_row + 1 < a.rows ? 16 : left);
+                    int bytes = is_there ? 16 : 0;
+                    if (next_row + 1 == a.rows && !full(c) && column(c) + kV > a.width) bytes = (a.width - column(c)) * kBytes<E>;
+                    copy_part(slot, p, bytes);
                 } else {
                     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -212,6 +233,16 @@ struct Place {
         next_row += row_step, next_at += step;
         coming += stage_bytes;
         if (coming == a.stages * stage_bytes) coming = 0;
+    }
+    // Before the wait for the previous grid: L2 may look for the first rows' lines.
+    __device__ void look_ahead() const {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            if (k >= a.tensors) break;
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+                if (there() && held(c) && column(c) >= 0) prefetch_l2(a.in[k] + at + c * column_threads() * 16);
+        }
     }
     // Before the first fetch: the slots of chunks past the row's end hold zeros for good.
     __device__ void clear_slots() const {
@@ -251,10 +282,9 @@ struct Place {
     // first and last chunk go to shared memory (`edges`: two chunks a row of a warp), from
     // where the row's lanes write an element each.
     __device__ void store(char *base, uint32_t edges, const float2 (&v)[kPairs]) const {
-        const int lane = threadIdx.x & 31, team = kMulti ? 0 : lane / kTeam;
+        const int lane = threadIdx.x & 31, team = kMulti ? 0 : lane / kTeam_or_32();
         const uint32_t edge = edges + ((threadIdx.x >> 5) * 4 + team) * 32;
         const bool is_there = there();
-        bool has_first = false, has_last = false;
         if (!kWhole) __syncwarp();   // the edges' last readers
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
@@ -276,23 +306,19 @@ struct Place {
             } else if (full(c)) {
                 if (is_there) st_stream(p, q);
             } else if (held(c)) {
-                const bool is_first = column(c) < 0;
-                store_shared(edge + (is_first ? 0 : 16), q);
-                (is_first ? has_first : has_last) = true;
+                store_shared(edge + (column(c) < 0 ? 0 : 16), q);
             }
         }
         if (kWhole || !a.together) return;
-        const unsigned firsts = __ballot_sync(0xffffffffu, has_first), lasts = __ballot_sync(0xffffffffu, has_last);
         __syncwarp();
-        const unsigned team_lanes = kMulti || kTeam == 32 ? 0xffffffffu : ((1u << (kTeam & 31)) - 1) << (team * kTeam & 31);
-        const int j = kMulti ? lane : lane & (kTeam - 1);
+        const int j = kMulti ? lane : lane & (kTeam_or_32() - 1);
         if (j >= kV || !is_there) return;
         char *row_at = base + at - column_thread() * 16;     // the row's first chunk
-        if (firsts & team_lanes) {
+        if (first_here) {
             const int col = j - lead;
             if (col >= 0 && col < a.width) put(row_at, j, element(edge, j));
         }
-        if (lasts & team_lanes) {
+        if (last_here) {
             const int first = (lead + a.width) / kV * kV;     // of the last chunk
             if (first + j - lead < a.width) put(row_at + first * kBytes<E>, j, element(edge + 16, j));
         }
@@ -386,9 +412,9 @@ struct Cut {
     int blocks, units, threads;
 };
 
-inline Cut cut_rows(const LayerNormArgs &a, int rows_per_pass, int most_blocks) {
+inline Cut cut_rows(const LayerNormArgs &a, int rows_per_pass, int most_warps, int most_blocks) {
     const int64_t passes = ceil_div(a.rows, rows_per_pass);
-    int64_t units = kWarps / a.team_warps;
+    int64_t units = most_warps / a.team_warps;
     if (units > ceil_div(passes, most_blocks)) units = ceil_div(passes, most_blocks);
     int64_t blocks = ceil_div(passes, units);
     if (blocks > most_blocks) blocks = most_blocks;

@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_norm_backward(const LayerNo
     char *mask_words = reinterpret_cast<char *>(weight + p.capacity() * P::kV);
     const uint32_t masks = shared_address(mask_words);
     const uint32_t edges = shared_address(edge_bytes);
+    p.look_ahead();
     p.clear_slots();
     pdl_prologue();
     for (int s = 0; s < a.stages; ++s) p.fetch();
@@ -54,7 +55,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_norm_backward(const LayerNo
         float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
-            float2 w[kHalf];
+            float2 w[kHalf], a1, a2;      // a chain of additions a chunk
             p.kept(weight, c, w);
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) {
@@ -63,9 +64,10 @@ __global__ void __launch_bounds__(kThreads, 1) layer_norm_backward(const LayerNo
                 gb[i] = add2(gb[i], g[i]);
                 gw[i] = fma2(g[i], h[i], gw[i]);
                 g[i] = mul2(g[i], w[j]);
-                s1 = add2(s1, g[i]);
-                s2 = fma2(g[i], h[i], s2);
+                a1 = j ? add2(a1, g[i]) : g[i];
+                a2 = j ? fma2(g[i], h[i], a2) : mul2(g[i], h[i]);
             }
+            s1 = c ? add2(s1, a1) : a1, s2 = c ? add2(s2, a2) : a2;
         }
         const float2 t = p.sum(make_float2(s1.x + s1.y, s2.x + s2.y));
         const float2 c1 = both(-t.x * a.inv), c2 = both(-t.y * a.inv);
@@ -116,30 +118,37 @@ __global__ void __launch_bounds__(kThreads, 1) layer_norm_backward(const LayerNo
     }
 }
 
-// grad_weight (blockIdx.y 0) and grad_bias (1): the blocks' sums, 32 columns a
-// block, 32 threads a column.
+// grad_weight (blockIdx.y 0) and grad_bias (1): the blocks' sums, eight columns a
+// block, 16 threads a column.  So few threads find room beside the first launch's
+// blocks and are there when those end.
+constexpr int kParamCols = 8, kParamGroups = 16;
+
 template <typename E>
-__global__ void __launch_bounds__(1024) layer_norm_params(const float *part, int blocks, int width, void *grad_weight,
-                                                          void *grad_bias, bool p32) {
-    __shared__ float sums[32][33];
+__global__ void __launch_bounds__(kParamCols * kParamGroups) layer_norm_params(const float *part, int blocks, int width,
+                                                                               void *grad_weight, void *grad_bias,
+                                                                               bool p32) {
+    __shared__ float sums[kParamGroups / 4][kParamCols];
     pdl_prologue();
-    const int col = blockIdx.x * 32 + threadIdx.x;
-    const int64_t at = static_cast<int64_t>(blockIdx.y) * width + col;
+    const int group = threadIdx.x / kParamCols, lane = threadIdx.x & 31, col = blockIdx.x * kParamCols + (threadIdx.x & 7);
+    const float *p = part + static_cast<int64_t>(blockIdx.y) * width + col;
     float s = 0.f;
     if (col < width) {
-#pragma unroll 8
-        for (int b = threadIdx.y; b < blocks; b += 32) s += __ldcg(part + b * 2ll * width + at);
+#pragma unroll
+        for (int b = group; b < kMostBlocks; b += kParamGroups)
+            if (b < blocks) s += __ldcg(p + b * 2ll * width);
     }
-    sums[threadIdx.y][threadIdx.x] = s;
+    // the four groups of a warp, then the warps
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if (lane < kParamCols) sums[threadIdx.x >> 5][lane] = s;
     __syncthreads();
-    const float t = group_sum<32>(sums[threadIdx.x][threadIdx.y]);
-    const int out_col = blockIdx.x * 32 + threadIdx.y;
     void *out = blockIdx.y ? grad_bias : grad_weight;
-    if (threadIdx.x != 0 || out_col >= width || !out) return;
+    if (threadIdx.x >= kParamCols || col >= width || !out) return;
+    const float t = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
     if (p32)
-        static_cast<float *>(out)[out_col] = t;
+        static_cast<float *>(out)[col] = t;
     else if constexpr (!std::is_same<E, F32>::value)
-        static_cast<uint16_t *>(out)[out_col] = static_cast<uint16_t>(E::from_f2(t, 0.f));
+        static_cast<uint16_t *>(out)[col] = static_cast<uint16_t>(E::from_f2(t, 0.f));
 }
 
 template <typename E, int kC, int kTeam, bool kWhole>
@@ -149,7 +158,7 @@ wgs_status run_unit(LayerNormArgs a, cudaStream_t stream, int *blocks) {
     if (st != WGS_OK) return st;
     using P = Place<E, kC, kTeam, kWhole>;
     a.team_warps = kTeam == 0 ? static_cast<int>(ceil_div(a.chunks, 32 * kC)) : 1;
-    const Cut cut = cut_rows(a, P::kRowsPerPass, dev.sm_count < kMostBlocks ? dev.sm_count : kMostBlocks);
+    const Cut cut = cut_rows(a, P::kRowsPerPass, kWarps, dev.sm_count < kMostBlocks ? dev.sm_count : kMostBlocks);
     *blocks = cut.blocks;
     const int stage = cut.threads * a.tensors * kC * 16;
     a.stages = kRing / stage < 1 ? 1 : kRing / stage < kMaxStages ? kRing / stage : kMaxStages;
@@ -247,6 +256,6 @@ extern "C" wgs_status layer_norm_bwd(const void *grad_y, const void *x, const fl
     auto kernel = dtype == WGS_F16    ? layer_norm_params<Fp16>
                   : dtype == WGS_BF16 ? layer_norm_params<Bf16>
                                       : layer_norm_params<F32>;
-    return launch(kernel, dim3(static_cast<unsigned>(ceil_div(width, 32)), 2), dim3(32, 32), 0, stream,
+    return launch(kernel, dim3(static_cast<unsigned>(ceil_div(width, kParamCols)), 2), dim3(kParamCols * kParamGroups), 0, stream,
                   static_cast<const float *>(a.part), blocks, width, grad_weight, grad_bias, a.p32);
 }
