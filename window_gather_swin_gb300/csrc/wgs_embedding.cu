@@ -224,8 +224,9 @@ constexpr int kBins = 512;
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 constexpr int kRounds = 4;             // indices of a thread at a time
 constexpr int kSortTile = kSortThreads * kRounds;
-// At most: every block reads all blocks' counts, so these cost the square.  131040
-// indices: KSORT
+// At most: every block reads all blocks' counts.  131040 indices into 24 and 32768 rows,
+// whole calls: 22.2 and 57.9 us, with 32 blocks 24.8 and 65.9, with 128 22.3 and 56.3,
+// but the windows' map 52.1, 56.8 and 55.0.
 constexpr int kSortBlocks = 64;
 
 struct SortArgs {
@@ -744,15 +745,28 @@ __device__ __forceinline__ void write_quad(const SumArgs &a, int32_t k, int quad
     if (left > 2) write_one<P>(a.out, at + 2, s.z * a.scale);
     if (left > 3) write_one<P>(a.out, at + 3, s.w * a.scale);
 }
-constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
 constexpr int kLongRun = 24;           // pieces behind the first
+
+// The first of [from, to) that is so, where all behind it are, by a warp; `to` for none.
+template <typename F>
+__device__ __forceinline__ int64_t first_piece(int64_t from, int64_t to, F so) {
+    const int lane = threadIdx.x & 31;
+    while (from < to) {
+        const int64_t part = (to - from + 31) / 32, i = from + (lane + 1) * part - 1;
+        const int below = 32 - __popc(__ballot_sync(0xffffffffu, i >= to || so(i < to ? i : to - 1)));
+        from += below * part;
+        to = from + part - 1 < to ? from + part - 1 : to;
+    }
+    return from;
+}
 
 template <typename P>
 __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a) {
     __shared__ float4 sums[kJoinThreads];
     __shared__ int found[kJoinThreads], pieces[kJoinThreads], n_found;
-    pdl_prologue();
     const int thread = threadIdx.x, lane = thread & 31, warp = thread >> 5;
+    bool waited = false;
     // does the run of piece c's last index go on into the next, having begun in c?
     auto begins = [&](int64_t c) {
         const int64_t end = (c + 1) * a.piece;
@@ -772,15 +786,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a) {
         for (int f = warp; f < runs; f += kJoinWarps) {
             const int64_t c0 = found[f];
             const int32_t k = __ldcg(a.keys + (c0 + 1) * a.piece);
-            int more = 1;
-            for (;;) {
-                const int64_t next = (c0 + more + 1 + lane) * a.piece;
-                const int on = __popc(__ballot_sync(0xffffffffu, next < a.n && __ldcg(a.keys + (next < a.n ? next : 0)) == k));
-                more += on;
-                if (on < 32) break;
-            }
+            // up to before the first piece that begins behind it
+            const int64_t behind = first_piece(c0 + 2, a.pieces, [&](int64_t p) { return __ldcg(a.keys + p * a.piece) > k; });
+            const int more = static_cast<int>(behind - 1 - c0);
             if (lane == 0) pieces[f] = more;
         }
+        // This launch may start while the sums' blocks end; those have waited for the
+        // sort, so its order is there to be read, and only their parts are waited for.
+        if (!waited) pdl_prologue();
+        waited = true;
         __syncthreads();
         const int quads = (a.width + 3) / 4;     // four columns each
         const int blocks = (quads + 31) / 32;
@@ -790,7 +804,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a) {
             const int64_t c0 = found[f];
             const int32_t k = __ldcg(a.keys + (c0 + 1) * a.piece);
             float4 s = part_of(a, 2 * c0 + 1, quad);
-#pragma unroll 4
+#pragma unroll 8
             for (int p = 1; p <= more; ++p) s = plus(s, part_of(a, 2 * (c0 + p), quad));
             write_quad<P>(a, k, quad, s);
         }
@@ -979,7 +993,8 @@ Plan plan_of(int64_t n, int64_t n_rows, int32_t width, int v) {
         return z;
     }
     z.slots = kSumThreads / z.cols < kMostSlots ? kSumThreads / z.cols : kMostSlots;
-    // some six blocks an SM, of slots of 8 to 64 indices
+    // some six blocks an SM, of slots of 8 to 64 indices (131040 indices into 24 rows of
+    // 192: 22.2 us a call, with four 25.1, with eight 23.8, with twelve 26.1)
     const int64_t want = ceil_div(n, static_cast<int64_t>(z.slots) * 912);
     z.each = want < 8 ? 8 : want > 64 ? 64 : static_cast<int>(want);
     z.piece = z.slots * z.each;
