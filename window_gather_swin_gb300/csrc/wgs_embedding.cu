@@ -33,30 +33,13 @@ constexpr int kMaxWidth = 32768;
 template <typename E>
 constexpr int kBytes = std::is_same<E, F32>::value ? 4 : 2;
 
-// kV neighbouring values at p, widened, and rounded back.
-template <typename E, int kV>
-__device__ __forceinline__ void load_values(const char *p, float (&v)[kV]) {
-    if constexpr (kV == 1) {
-        if constexpr (std::is_same<E, F32>::value)
-            v[0] = __ldcg(reinterpret_cast<const float *>(p));
-        else
-            v[0] = E::to_f2(__ldcg(reinterpret_cast<const uint16_t *>(p))).x;
-    } else if constexpr (std::is_same<E, F32>::value) {
-#pragma unroll
-        for (int i = 0; i < kV / 4; ++i) {
-            const uint4 q = ld_stream(p + 16 * i);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[4 * i + j] = __uint_as_float(word(q, j));
-        }
-    } else {
-        static_assert(kV == 8, "16 bytes of 16-bit values");
-        const uint4 q = ld_stream(p);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = E::to_f2(word(q, j));
-            v[2 * j] = f.x, v[2 * j + 1] = f.y;
-        }
-    }
+// One value through L1.
+template <typename E>
+__device__ __forceinline__ float load_kept(const char *p) {
+    if constexpr (std::is_same<E, F32>::value)
+        return __ldg(reinterpret_cast<const float *>(p));
+    else
+        return E::to_f2(__ldg(reinterpret_cast<const uint16_t *>(p))).x;
 }
 
 template <typename E, int kV>
@@ -86,8 +69,9 @@ __device__ __forceinline__ void store_values(char *p, const float (&v)[kV]) {
 // register, so that neither the index nor the row that it names is waited for at
 // full length.  The copies go through L1, which keeps the rows that many indices
 // name: past it, a skewed sequence's rows were asked of the same L2 lines by all SMs
-// at once (131040 of 384, FP32 to bf16: 128 us, through L1 33).  Rows that are not whole chunks are taken in parts of as many single
-// elements, every row_chunks-th of the row.
+// at once (131040 of 384, FP32 to bf16: 128 us, through L1 33).  What bounds it is L2,
+// which moves 8.5 to 9.1 TB/s: 33 us for those, of which the named rows are 201 MB and
+// the output 101; 22 us from and to fp16; 47 us in FP32.
 constexpr int kLookupThreads = 256;
 constexpr int kLookupBlocksPerSm = 8;
 
@@ -100,11 +84,20 @@ struct LookupArgs {
     float scale;
 };
 
+// The table row of index r, seen by its row's first element as `first`: -1 for none.
+__device__ __forceinline__ int32_t row_of_index(const LookupArgs &a, int64_t r, bool first) {
+    if (r >= a.n) return -1;
+    const int32_t k = __ldg(a.idx + r);
+    if (k >= 0 && k < a.n_rows) return k;
+    if (k != -1 && first) atomicOr(&g_embedding_error, 1u);
+    return -1;
+}
+
 // T: the table's format, E: the output's.
-template <typename T, typename E, bool kChunks>
+template <typename T, typename E>
 __global__ void __launch_bounds__(kLookupThreads, kLookupBlocksPerSm) embedding_lookup(const LookupArgs a) {
     constexpr int kIn = 16, kV = kIn / kBytes<T>, kOut = kV * kBytes<E>;    // of a chunk
-    __shared__ uint4 slots[kChunks ? 2 : 1][kChunks ? kLookupThreads : 1];
+    __shared__ uint4 slots[2][kLookupThreads];
     pdl_prologue();
     const int64_t step = static_cast<int64_t>(gridDim.x) * kLookupThreads, row_step = step / a.row_chunks;
     const int col_step = static_cast<int>(step - row_step * a.row_chunks);
@@ -115,71 +108,88 @@ __global__ void __launch_bounds__(kLookupThreads, kLookupBlocksPerSm) embedding_
         r += row_step, c += col_step;
         if (c >= a.row_chunks) c -= a.row_chunks, ++r;
     };
-    // the table row of a chunk's index: -1 for none
-    auto index = [&](int64_t r, int c) {
-        if (r >= a.n) return -1;
-        const int32_t k = __ldg(a.idx + r);
-        if (k >= 0 && k < a.n_rows) return k;
-        if (k != -1 && c == 0) atomicOr(&g_embedding_error, 1u);
-        return -1;
-    };
     auto fetch = [&](int s, int32_t from, int c) {
-        if constexpr (kChunks) {
-            if (from >= 0) cp_async16_ca(&slots[s][threadIdx.x], a.table + (static_cast<int64_t>(from) * a.row_chunks + c) * kIn);
-            cp_async_commit();
-        }
+        if (from >= 0) cp_async16_ca(&slots[s][threadIdx.x], a.table + (static_cast<int64_t>(from) * a.row_chunks + c) * kIn);
+        cp_async_commit();
     };
     int64_t next_row = row;
     int next_col = col;
-    int32_t now = index(row, col);
+    int32_t now = row_of_index(a, row, col == 0);
     advance(next_row, next_col);
     fetch(0, now, col);
-    int32_t next = index(next_row, next_col);
+    int32_t next = row_of_index(a, next_row, next_col == 0);
     for (int s = 0; row < a.n; s ^= 1) {
         fetch(s ^ 1, next, next_col);
         int64_t later_row = next_row;
         int later_col = next_col;
         advance(later_row, later_col);
-        const int32_t later = index(later_row, later_col);
+        const int32_t later = row_of_index(a, later_row, later_col == 0);
         float v[kV];
 #pragma unroll
         for (int i = 0; i < kV; ++i) v[i] = 0.f;
-        if constexpr (kChunks) {
-            cp_async_wait<1>();
-            if (now >= 0) {
-                const uint4 q = slots[s][threadIdx.x];
+        cp_async_wait<1>();
+        if (now >= 0) {
+            const uint4 q = slots[s][threadIdx.x];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if constexpr (kV == 4) {
-                        v[k] = __uint_as_float(word(q, k)) * a.scale;
-                    } else {
-                        const float2 f = T::to_f2(word(q, k));
-                        v[2 * k] = f.x * a.scale, v[2 * k + 1] = f.y * a.scale;
-                    }
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (kV == 4) {
+                    v[k] = __uint_as_float(word(q, k)) * a.scale;
+                } else {
+                    const float2 f = T::to_f2(word(q, k));
+                    v[2 * k] = f.x * a.scale, v[2 * k + 1] = f.y * a.scale;
                 }
             }
-            char *p = a.out + (row * a.row_chunks + col) * kOut;
-            if constexpr (kOut == 8)
-                *reinterpret_cast<uint2 *>(p) = make_uint2(E::from_f2(v[0], v[1]), E::from_f2(v[2], v[3]));
-            else
-                store_values<E, kV>(p, v);
-        } else {
-            const char *from = a.table + (now < 0 ? 0 : static_cast<int64_t>(now) * a.width * kBytes<T>);
-            char *p = a.out + row * a.width * kBytes<E>;
-#pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                float one[1] = {0.f};
-                if (now >= 0 && col + i * a.row_chunks < a.width) load_values<T, 1>(from + (col + i * a.row_chunks) * kBytes<T>, one);
-                v[i] = one[0] * a.scale;
-            }
-#pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                const float one[1] = {now < 0 ? 0.f : v[i]};
-                if (col + i * a.row_chunks < a.width) store_values<E, 1>(p + (col + i * a.row_chunks) * kBytes<E>, one);
-            }
         }
+        char *p = a.out + (row * a.row_chunks + col) * kOut;
+        if constexpr (kOut == 8)
+            *reinterpret_cast<uint2 *>(p) = make_uint2(E::from_f2(v[0], v[1]), E::from_f2(v[2], v[3]));
+        else
+            store_values<E, kV>(p, v);
         row = next_row, col = next_col, now = next;
         next_row = later_row, next_col = later_col, next = later;
+    }
+}
+
+// Rows of other widths, or at other places: the output as one run of elements, 16 bytes
+// of it a thread (single elements where it does not start on 16), which may span rows;
+// the table's elements one by one, through L1.
+template <typename T, typename E>
+__global__ void __launch_bounds__(kLookupThreads, kLookupBlocksPerSm) embedding_lookup_ragged(const LookupArgs a) {
+    constexpr int kV = 16 / kBytes<E>;
+    pdl_prologue();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kLookupThreads * kV, row_step = step / a.width;
+    const int col_step = static_cast<int>(step - row_step * a.width);
+    const int64_t all = a.n * a.width;
+    int64_t at = (static_cast<int64_t>(blockIdx.x) * kLookupThreads + threadIdx.x) * kV, row = at / a.width;
+    int col = static_cast<int>(at - row * a.width);
+    int32_t now = row_of_index(a, row, col == 0);
+    while (at < all) {
+        int64_t next_row = row + row_step;
+        int next_col = col + col_step;
+        if (next_col >= a.width) next_col -= a.width, ++next_row;
+        const int32_t next = row_of_index(a, next_row, next_col == 0);
+        float v[kV];
+        const char *from = a.table + static_cast<int64_t>(now) * a.width * kBytes<T>;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            if (col == a.width) {
+                col = 0, now = row_of_index(a, ++row, true);
+                from = a.table + static_cast<int64_t>(now) * a.width * kBytes<T>;
+            }
+            v[j] = now >= 0 ? load_kept<T>(from + col * kBytes<T>) * a.scale : 0.f;     // (a pad is +0)
+            ++col;
+        }
+        char *p = a.out + at * kBytes<E>;
+        if (at + kV <= all && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+            store_values<E, kV>(p, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kV; ++j) {
+                const float one[1] = {v[j]};
+                if (at + j < all) store_values<E, 1>(p + j * kBytes<E>, one);
+            }
+        }
+        at += step, row = next_row, col = next_col, now = next;
     }
 }
 
@@ -1127,9 +1137,10 @@ wgs_status run_lookup(LookupArgs a, int32_t width, int sms, cudaStream_t stream)
     constexpr int kV = 16 / kBytes<T>;
     const bool chunks = width % kV == 0 && aligned16(a.table) && aligned_to(a.out, kV * kBytes<E>);
     a.row_chunks = static_cast<int>(ceil_div(width, kV)), a.width = width;
-    const int64_t blocks = ceil_div(a.n * a.row_chunks, kLookupThreads);
+    const int64_t blocks = chunks ? ceil_div(a.n * a.row_chunks, kLookupThreads)
+                                  : ceil_div(a.n * width, kLookupThreads * (16 / kBytes<E>));
     const int64_t most = static_cast<int64_t>(sms) * kLookupBlocksPerSm;
-    return launch(chunks ? embedding_lookup<T, E, true> : embedding_lookup<T, E, false>,
+    return launch(chunks ? embedding_lookup<T, E> : embedding_lookup_ragged<T, E>,
                   dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(kLookupThreads), 0, stream, a);
 }
 
