@@ -32,7 +32,7 @@ __device__ __forceinline__ float reciprocal_root(float v) {
 template <typename E, int kC, int kTeam, bool kWhole>
 __global__ void __launch_bounds__(kBlockWarps<E, kC> * 32, 2) layer_norm_forward(const LayerNormArgs a) {
     extern __shared__ __align__(16) char shared[];
-    __shared__ float2 exchange[2][kWarps];
+    __shared__ __align__(16) float2 exchange[2][kMeet];
     __shared__ __align__(16) char edge_bytes[kWhole ? 16 : kEdgeBytes];
     using P = Place<E, kC, kTeam, kWhole>;
     constexpr int kPairs = P::kPairs, kHalf = P::kHalf;
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kBlockWarps<E, kC> * 32, 2) layer_norm_forward
     p.keep_param(weight, a.weight, 1.f);
     p.keep_param(bias, a.bias, 0.f);
     if (!kWhole) {
-        p.keep(inside, [](int) { return 1.f; });
+        p.keep_ones(inside);
         p.keep_masks(mask_words);
     }
     __syncthreads();
@@ -150,10 +150,11 @@ wgs_status run_unit(LayerNormArgs a, cudaStream_t stream) {
 
 // The narrowest unit that holds a row in three chunks a thread (four for a whole
 // warp, which spares rows just above its 96 chunks a second one), and the fewest
-// chunks that do; six where twelve warps are too few for three (FP32).
+// chunks that do.
 template <typename E, bool kWhole>
 wgs_status run_width(const LayerNormArgs &a, cudaStream_t stream) {
     const int n = a.chunks;
+    if (n <= 4) return run_unit<E, 1, 4, kWhole>(a, stream);
     if (n <= 8) return run_unit<E, 1, 8, kWhole>(a, stream);
     if (n <= 16) return run_unit<E, 2, 8, kWhole>(a, stream);
     if (n <= 24) return run_unit<E, 3, 8, kWhole>(a, stream);
@@ -162,8 +163,9 @@ wgs_status run_width(const LayerNormArgs &a, cudaStream_t stream) {
     if (n <= 64) return run_unit<E, 2, 32, kWhole>(a, stream);
     if (n <= 96) return run_unit<E, 3, 32, kWhole>(a, stream);
     if (n <= 128) return run_unit<E, 4, 32, kWhole>(a, stream);
-    if (ceil_div(n, 64) * 2 < ceil_div(n, 96) * 3 && n <= 64 * kWarps) return run_unit<E, 2, 0, kWhole>(a, stream);
-    if (n <= 96 * kWarps) return run_unit<E, 3, 0, kWhole>(a, stream);
+    const int each = chunks_of_units(n, std::is_same<E, F32>::value);
+    if (each == 2) return run_unit<E, 2, 0, kWhole>(a, stream);
+    if (each == 3) return run_unit<E, 3, 0, kWhole>(a, stream);
     if constexpr (std::is_same<E, F32>::value) return run_unit<E, 6, 0, kWhole>(a, stream);
     return WGS_ERR_WIDTH;
 }

@@ -30,8 +30,9 @@ struct F32 {};
 constexpr int kMaxWidth = 8192;
 constexpr int kWarps = 12;          // of a block, at most
 constexpr int kThreads = kWarps * 32;
+constexpr int kMeet = kWarps / 3 * 4;   // places of their sums: units of three warps have four each
 constexpr int kMaxStages = 4;
-constexpr int kEdgeBytes = kWarps * 4 * 32;   // of ragged rows' ends
+constexpr int kEdgeBytes = kWarps * 8 * 32;   // of ragged rows' ends
 
 struct LayerNormArgs {
     const char *in[3];   // forward: x, branch; backward: x, grad_y, grad_residual
@@ -103,10 +104,10 @@ struct Place {
     int64_t next_row, next_at;  // to be fetched
     uint32_t held_bits = 0, full_bits = 0;      // of a ragged row's chunks, see held() and full()
     bool first_here, last_here; // a ragged row's partial first and last chunk are this warp's (team's)
-    float2 (*meet)[kWarps];     // [2][warps]: sums of the unit's warps
+    float2 (*meet)[kMeet];      // [2][places]: sums of the units' warps
     int turn = 0;
 
-    __device__ Place(const LayerNormArgs &args, float2 (*exchange)[kWarps], uint32_t ring) : a(args), meet(exchange) {
+    __device__ Place(const LayerNormArgs &args, float2 (*exchange)[kMeet], uint32_t ring) : a(args), meet(exchange) {
         warps = kMulti ? a.team_warps : 1;
         const int warp = threadIdx.x >> 5;
         index = kMulti ? warp / warps : warp;
@@ -181,13 +182,23 @@ struct Place {
     }
     __device__ float2 across(float2 v) {
         if constexpr (kMulti) {
-            // two places in turn: a warp that is here again has passed the other's barrier
-            float2 *place = meet[turn] + index * warps;
+            // two places in turn: a warp that is here again has passed the other's barrier.
+            // Two warps' sums a read; a unit of an odd number has a place of zeros behind.
+            const int even = (warps + 1) / 2 * 2;
+            float2 *place = meet[turn] + index * even;
             turn ^= 1;
-            if ((threadIdx.x & 31) == 0) place[thread >> 5] = v;
+            if ((threadIdx.x & 31) == 0) {
+                place[thread >> 5] = v;
+                if (thread == 0 && even > warps) place[warps] = both(0.f);
+            }
             asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(warps * 32) : "memory");
-            v = place[0];
-            for (int w = 1; w < warps; ++w) v = add2(v, place[w]);
+            v = both(0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; w += 2) {
+                if (w >= warps) break;
+                const float4 q = *reinterpret_cast<const float4 *>(place + w);
+                v = add2(v, add2(make_float2(q.x, q.y), make_float2(q.z, q.w)));
+            }
         }
         return v;
     }
@@ -283,7 +294,7 @@ struct Place {
     // where the row's lanes write an element each.
     __device__ void store(char *base, uint32_t edges, const float2 (&v)[kPairs]) const {
         const int lane = threadIdx.x & 31, team = kMulti ? 0 : lane / kTeam_or_32();
-        const uint32_t edge = edges + ((threadIdx.x >> 5) * 4 + team) * 32;
+        const uint32_t edge = edges + ((threadIdx.x >> 5) * 8 + team) * 32;
         const bool is_there = there();
         if (!kWhole) __syncwarp();   // the edges' last readers
 #pragma unroll
@@ -311,16 +322,20 @@ struct Place {
         }
         if (kWhole || !a.together) return;
         __syncwarp();
-        const int j = kMulti ? lane : lane & (kTeam_or_32() - 1);
-        if (j >= kV || !is_there) return;
+        if (!is_there) return;
         char *row_at = base + at - column_thread() * 16;     // the row's first chunk
-        if (first_here) {
-            const int col = j - lead;
-            if (col >= 0 && col < a.width) put(row_at, j, element(edge, j));
-        }
-        if (last_here) {
-            const int first = (lead + a.width) / kV * kV;     // of the last chunk
-            if (first + j - lead < a.width) put(row_at + first * kBytes<E>, j, element(edge + 16, j));
+#pragma unroll
+        for (int j0 = 0; j0 < kV; j0 += kTeam_or_32()) {
+            const int j = j0 + (kMulti ? lane : lane & (kTeam_or_32() - 1));
+            if (j >= kV) break;
+            if (first_here) {
+                const int col = j - lead;
+                if (col >= 0 && col < a.width) put(row_at, j, element(edge, j));
+            }
+            if (last_here) {
+                const int first = (lead + a.width) / kV * kV;     // of the last chunk
+                if (first + j - lead < a.width) put(row_at + first * kBytes<E>, j, element(edge + 16, j));
+            }
         }
     }
     __device__ static void put(char *p, int j, uint32_t w) {
@@ -335,23 +350,46 @@ struct Place {
         return w;
     }
 
-    // A value of every column in shared memory as the threads hold columns, zeros
-    // outside the row: the first four elements of all chunks, then the other four (so
-    // that neighbouring threads' 16 bytes lie side by side).
-    template <typename F>
-    __device__ void keep(float *to, F value) const {
+    // Values of all columns in shared memory as the threads hold columns, zeros outside
+    // the row: the first four elements of all chunks, then the other four (so that
+    // neighbouring threads' 16 bytes lie side by side).  value(col): of a column in the
+    // row; four(col, v): of four from col on, false where they cannot be had at once.
+    template <typename Value, typename Four>
+    __device__ void keep(float *to, Value value, Four four) const {
+        constexpr int kQuads = kV / 4;       // of a chunk
         const int all = capacity();
-        for (int i = threadIdx.x; i < all * kV; i += blockDim.x) {
-            const int col = i - lead;
-            to[(i % kV / 4 * all + i / kV) * 4 + (i & 3)] = col >= 0 && col < a.width ? value(col) : 0.f;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < all * kQuads; i += blockDim.x) {
+            const int col = i * 4 - lead;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!(col >= 0 && col + 4 <= a.width && four(col, v))) {
+                if (col >= 0 && col < a.width) v.x = value(col);
+                if (col + 1 >= 0 && col + 1 < a.width) v.y = value(col + 1);
+                if (col + 2 >= 0 && col + 2 < a.width) v.z = value(col + 2);
+                if (col + 3 >= 0 && col + 3 < a.width) v.w = value(col + 3);
+            }
+            *reinterpret_cast<float4 *>(to + (i % kQuads * all + i / kQuads) * 4) = v;
         }
     }
+    __device__ void keep_ones(float *to) const {
+        keep(to, [](int) { return 1.f; }, [](int, float4 &v) { return v = make_float4(1.f, 1.f, 1.f, 1.f), true; });
+    }
+    // weight or bias, widened
     __device__ void keep_param(float *to, const void *from, float other) const {
-        keep(to, [&](int col) {
-            return !from   ? other
-                   : a.p32 ? static_cast<const float *>(from)[col]
-                           : widen<E>(static_cast<const char *>(from) + static_cast<size_t>(col) * kBytes<E>);
-        });
+        const char *p = static_cast<const char *>(from);
+        if (!from) {
+            keep(to, [&](int) { return other; }, [&](int, float4 &v) { return v = make_float4(other, other, other, other), true; });
+        } else if (a.p32) {
+            const bool whole = (reinterpret_cast<uintptr_t>(p) + 16 - lead * 4) % 16 == 0;     // at columns of whole quads
+            keep(to, [&](int col) { return __ldg(reinterpret_cast<const float *>(p) + col); },
+                 [&](int col, float4 &v) {
+                     if (whole) v = __ldg(reinterpret_cast<const float4 *>(p + col * 4));
+                     return whole;
+                 });
+        } else {
+            keep(to, [&](int col) { return widen<E>(p + static_cast<size_t>(col) * kBytes<E>); },
+                 [](int, float4 &) { return false; });
+        }
     }
     __device__ void kept(const float *from, int c, float2 (&w)[kHalf]) const {
 #pragma unroll
@@ -421,6 +459,19 @@ inline Cut cut_rows(const LayerNormArgs &a, int rows_per_pass, int most_warps, i
     const int64_t kinds = a.rows < a.period ? a.rows : a.period;
     if (blocks < kinds) blocks = kinds;
     return {static_cast<int>(blocks), static_cast<int>(units), static_cast<int>(units) * a.team_warps * 32};
+}
+
+// Chunks a thread for units of several warps: those that leave the fewest of a block's
+// threads without a part of a row.
+inline int chunks_of_units(int chunks, bool six) {
+    int best = 0, best_score = 0;
+    for (int c : {3, 2, 6}) {
+        const int warps = static_cast<int>(ceil_div(chunks, 32 * c));
+        if ((c == 6 && !six) || warps < 2 || warps > kWarps) continue;
+        const int score = chunks * 1000 / (warps * 32 * c) * (kWarps / warps * warps) / kWarps;
+        if (score > best_score) best = c, best_score = score;
+    }
+    return best;
 }
 
 // No output may share a byte with another or with an input, but for those that may

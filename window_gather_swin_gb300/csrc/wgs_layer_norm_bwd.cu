@@ -20,7 +20,7 @@ constexpr int kRing = 168 << 10;   // shared memory of a block's slots, at most 
 template <typename E, int kC, int kTeam, bool kWhole>
 __global__ void __launch_bounds__(kThreads, 1) layer_norm_backward(const LayerNormArgs a) {
     extern __shared__ __align__(16) char shared[];
-    __shared__ float2 exchange[2][kWarps];
+    __shared__ __align__(16) float2 exchange[2][kMeet];
     __shared__ __align__(16) char edge_bytes[kWhole ? 16 : kEdgeBytes];
     using P = Place<E, kC, kTeam, kWhole>;
     constexpr int kPairs = P::kPairs, kHalf = P::kHalf;
@@ -182,6 +182,7 @@ wgs_status run_unit(LayerNormArgs a, cudaStream_t stream, int *blocks) {
 template <typename E, bool kWhole>
 wgs_status run_width(const LayerNormArgs &a, cudaStream_t stream, int *blocks) {
     const int n = a.chunks;
+    if (n <= 4) return run_unit<E, 1, 4, kWhole>(a, stream, blocks);
     if (n <= 8) return run_unit<E, 1, 8, kWhole>(a, stream, blocks);
     if (n <= 16) return run_unit<E, 2, 8, kWhole>(a, stream, blocks);
     if (n <= 24) return run_unit<E, 3, 8, kWhole>(a, stream, blocks);
@@ -189,8 +190,9 @@ wgs_status run_width(const LayerNormArgs &a, cudaStream_t stream, int *blocks) {
     if (n <= 48) return run_unit<E, 3, 16, kWhole>(a, stream, blocks);
     if (n <= 64) return run_unit<E, 2, 32, kWhole>(a, stream, blocks);
     if (n <= 96) return run_unit<E, 3, 32, kWhole>(a, stream, blocks);
-    if (ceil_div(n, 64) * 2 < ceil_div(n, 96) * 3 && n <= 64 * kWarps) return run_unit<E, 2, 0, kWhole>(a, stream, blocks);
-    if (n <= 96 * kWarps) return run_unit<E, 3, 0, kWhole>(a, stream, blocks);
+    const int each = chunks_of_units(n, std::is_same<E, F32>::value);
+    if (each == 2) return run_unit<E, 2, 0, kWhole>(a, stream, blocks);
+    if (each == 3) return run_unit<E, 3, 0, kWhole>(a, stream, blocks);
     if constexpr (std::is_same<E, F32>::value) return run_unit<E, 6, 0, kWhole>(a, stream, blocks);
     return WGS_ERR_WIDTH;
 }
