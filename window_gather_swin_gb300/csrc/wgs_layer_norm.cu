@@ -17,6 +17,9 @@ namespace {
 // weights fit twice; of fewer warps where a thread's 32 columns need the registers.
 template <typename E, int kC>
 constexpr int kBlockWarps = kC * 16 / kBytes<E> > 24 ? 8 : kWarps;
+// (Six chunks a thread are for rows whose weights leave no room for a second block.)
+template <int kC>
+constexpr int kBlocksPerSm = kC == 6 ? 1 : 2;
 constexpr int kHalfOfSm = 112 << 10, kMostOfSm = 216 << 10;   // shared memory
 
 // 1 / sqrt(v): the hardware's approximation and one step of Newton's method, which
@@ -30,7 +33,7 @@ __device__ __forceinline__ float reciprocal_root(float v) {
 // small whatever the mean's size, and their own mean, which m's rounding leaves,
 // comes off the variance and the result.
 template <typename E, int kC, int kTeam, bool kWhole>
-__global__ void __launch_bounds__(kBlockWarps<E, kC> * 32, 2) layer_norm_forward(const LayerNormArgs a) {
+__global__ void __launch_bounds__(kBlockWarps<E, kC> * 32, kBlocksPerSm<kC>) layer_norm_forward(const LayerNormArgs a) {
     extern __shared__ __align__(16) char shared[];
     __shared__ __align__(16) float2 exchange[2][kMeet];
     __shared__ __align__(16) char edge_bytes[kWhole ? 16 : kEdgeBytes];
@@ -38,9 +41,9 @@ __global__ void __launch_bounds__(kBlockWarps<E, kC> * 32, 2) layer_norm_forward
     constexpr int kPairs = P::kPairs, kHalf = P::kHalf;
     P p(a, exchange, shared_address(shared + a.kept_bytes));
     const int all = p.capacity() * P::kV;
-    float *weight = reinterpret_cast<float *>(shared), *bias = weight + all, *inside = bias + all;
-    char *mask_words = reinterpret_cast<char *>(inside + all);
-    const uint32_t masks = shared_address(mask_words);
+    float *weight = reinterpret_cast<float *>(shared), *bias = weight + all;
+    __shared__ __align__(16) char ends[kWhole ? 16 : P::kKeptEdges];
+    const uint32_t masks = shared_address(ends);
     const uint32_t edges = shared_address(edge_bytes);
     p.look_ahead();
     p.clear_slots();
@@ -48,19 +51,16 @@ __global__ void __launch_bounds__(kBlockWarps<E, kC> * 32, 2) layer_norm_forward
     for (int s = 0; s < a.stages; ++s) p.fetch();
     p.keep_param(weight, a.weight, 1.f);
     p.keep_param(bias, a.bias, 0.f);
-    if (!kWhole) {
-        p.keep_ones(inside);
-        p.keep_masks(mask_words);
-    }
+    if constexpr (!kWhole) p.keep_edges(ends);
     __syncthreads();
 
     for (; p.pass < p.passes; p.advance()) {
         p.arrived();
         float2 x[kPairs];
-        p.load(0, masks, x);
+        p.template load<false>(0, masks, x);
         if (a.tensors == 2) {
             float2 add[kPairs];
-            p.load(1, masks, add);
+            p.template load<false>(1, masks, add);
 #pragma unroll
             for (int i = 0; i < kPairs; ++i) x[i] = add2(x[i], add[i]);
             if constexpr (!std::is_same<E, F32>::value) {   // as the residual stream holds them
@@ -83,15 +83,21 @@ __global__ void __launch_bounds__(kBlockWarps<E, kC> * 32, 2) layer_norm_forward
         float2 d = both(0.f), q = both(0.f);
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
-            float2 in[kHalf];
-            if (!kWhole) p.kept(inside, c, in);
-            const bool held = !kWhole || p.held(c);
+            // outside the row the distance is 0
+            if (kWhole || p.full(c)) {
+                const float2 less = both(kWhole && !p.held(c) ? 0.f : -m);
+#pragma unroll
+                for (int j = 0; j < kHalf; ++j) x[c * kHalf + j] = add2(x[c * kHalf + j], less);
+            } else {
+                float2 in[kHalf];
+                p.inside(ends, c, in);
+#pragma unroll
+                for (int j = 0; j < kHalf; ++j) x[c * kHalf + j] = fma2(in[j], both(-m), x[c * kHalf + j]);
+            }
             float2 dc = both(0.f), qc = both(0.f);
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) {
-                float2 &v = x[c * kHalf + j];
-                // outside the row the distance is 0
-                v = kWhole ? add2(v, both(held ? -m : 0.f)) : fma2(in[j], both(-m), v);
+                const float2 v = x[c * kHalf + j];
                 dc = j ? add2(dc, v) : v, qc = j ? fma2(v, v, qc) : mul2(v, v);
             }
             d = c ? add2(d, dc) : dc, q = c ? add2(q, qc) : qc;
@@ -127,11 +133,10 @@ wgs_status run_unit(LayerNormArgs a, cudaStream_t stream) {
     if (st != WGS_OK) return st;
     using P = Place<E, kC, kTeam, kWhole>;
     a.team_warps = kTeam == 0 ? static_cast<int>(ceil_div(a.chunks, 32 * kC)) : 1;
-    // weight and bias, and what tells a ragged row's own
-    a.kept_bytes = kC * (kTeam == 0 ? 32 * a.team_warps : kTeam) * (kWhole ? 8 * P::kV : 12 * P::kV + 16);
+    a.kept_bytes = kC * (kTeam == 0 ? 32 * a.team_warps : kTeam) * 8 * P::kV;     // weight and bias
     constexpr int kMost = kBlockWarps<E, kC>;
     const int most = kMost / a.team_warps * a.team_warps * a.tensors * kC * 512;
-    const bool two = a.kept_bytes + 2 * most <= kHalfOfSm;
+    const bool two = kBlocksPerSm<kC> == 2 && a.kept_bytes + 2 * most <= kHalfOfSm;
     const Cut cut = cut_rows(a, P::kRowsPerPass, kMost, (two ? 2 : 1) * dev.sm_count);
     const int stage = cut.threads * a.tensors * kC * 16, fit = ((two ? kHalfOfSm : kMostOfSm) - a.kept_bytes) / stage;
     a.stages = fit < kMaxStages ? fit : kMaxStages;
@@ -139,8 +144,8 @@ wgs_status run_unit(LayerNormArgs a, cudaStream_t stream) {
     auto kernel = layer_norm_forward<E, kC, kTeam, kWhole>;
     // Above 48 KB, its static memory included, a kernel needs the runtime's leave,
     // which belongs to the context; asking for the same amount on every call needs
-    // no record of it.  (At most 118 KB beside a stage, and 72 KB of that.)
-    if (smem > 45 << 10 &&
+    // no record of it.  (At most 67 KB beside a stage, and 72 KB of that.)
+    if (smem > 40 << 10 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostOfSm) != cudaSuccess) {
         cudaGetLastError();
         return WGS_ERR_LAUNCH;
@@ -163,7 +168,7 @@ wgs_status run_width(const LayerNormArgs &a, cudaStream_t stream) {
     if (n <= 64) return run_unit<E, 2, 32, kWhole>(a, stream);
     if (n <= 96) return run_unit<E, 3, 32, kWhole>(a, stream);
     if (n <= 128) return run_unit<E, 4, 32, kWhole>(a, stream);
-    const int each = chunks_of_units(n, std::is_same<E, F32>::value);
+    const int each = chunks_of_units(n, std::is_same<E, F32>::value && n > 96 * kWarps);
     if (each == 2) return run_unit<E, 2, 0, kWhole>(a, stream);
     if (each == 3) return run_unit<E, 3, 0, kWhole>(a, stream);
     if constexpr (std::is_same<E, F32>::value) return run_unit<E, 6, 0, kWhole>(a, stream);

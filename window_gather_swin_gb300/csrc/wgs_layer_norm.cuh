@@ -270,14 +270,18 @@ struct Place {
         else if (a.stages == 2) cp_async_wait<1>();
         else cp_async_wait<0>();
     }
-    // The thread's part of the present row of tensor k, widened; zeros outside the row
-    // (`masks`: keep_masks').
+    // The thread's part of the present row of tensor k, widened; zeros outside the row:
+    // `masks` are keep_edges', looked up by the chunks that are not full, or with kAll
+    // keep_masks', for all chunks alike.  (The backward has no registers for the former:
+    // [5000, 8191] bf16 85 us, so 78; the forward no shared memory to spare for the latter:
+    // 51, so 87.)
+    template <bool kAll>
     __device__ void load(int k, uint32_t masks, float2 (&v)[kPairs]) const {
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             uint4 q = load_shared(slots + present + (k * kC + c) * 512);
-            if constexpr (!kWhole) {
-                const uint4 m = load_shared(masks + chunk(c) * 16);
+            if (!kWhole && (kAll || !full(c))) {
+                const uint4 m = load_shared(masks + (kAll ? chunk(c) : kind(c)) * 16);
                 q.x &= m.x, q.y &= m.y, q.z &= m.z, q.w &= m.w;
             }
 #pragma unroll
@@ -371,9 +375,6 @@ struct Place {
             *reinterpret_cast<float4 *>(to + (i % kQuads * all + i / kQuads) * 4) = v;
         }
     }
-    __device__ void keep_ones(float *to) const {
-        keep(to, [](int) { return 1.f; }, [](int, float4 &v) { return v = make_float4(1.f, 1.f, 1.f, 1.f), true; });
-    }
     // weight or bias, widened
     __device__ void keep_param(float *to, const void *from, float other) const {
         const char *p = static_cast<const char *>(from);
@@ -398,18 +399,41 @@ struct Place {
             w[2 * h] = make_float2(q.x, q.y), w[2 * h + 1] = make_float2(q.z, q.w);
         }
     }
+    // What of a chunk that is not full is the row's: of the first one, the last one and one
+    // behind the row, as bits and as a factor for every element.
+    static constexpr int kEdgeKinds = 3;
+    static constexpr int kKeptEdges = kEdgeKinds * (16 + kV * 4);     // bytes
+    __device__ int kind(int c) const { return column(c) < 0 ? 0 : held(c) ? 1 : 2; }
+    __device__ void keep_edges(char *to) const {
+        const int i = threadIdx.x;
+        if (i >= kEdgeKinds * kV) return;
+        const int k = i / kV, j = i % kV;
+        const int at = k == 0 ? -lead : k == 1 ? (lead + a.width) / kV * kV - lead : a.width, col = at + j;
+        const bool in = col >= 0 && col < a.width;
+        if constexpr (kV == 4)
+            reinterpret_cast<uint32_t *>(to)[i] = in ? 0xffffffffu : 0u;
+        else
+            reinterpret_cast<uint16_t *>(to)[i] = in ? 0xffffu : 0u;
+        reinterpret_cast<float *>(to + kEdgeKinds * 16)[i] = in ? 1.f : 0.f;
+    }
     // The bits of each chunk that are the row's.
     __device__ void keep_masks(char *to) const {
-        if constexpr (!kWhole) {
-            for (int i = threadIdx.x; i < capacity() * 4; i += blockDim.x) {
-                uint32_t m = 0;
+        for (int i = threadIdx.x; i < capacity() * 4; i += blockDim.x) {
+            uint32_t m = 0;
 #pragma unroll
-                for (int j = 0; j < kV / 4; ++j) {
-                    const int col = i * (kV / 4) + j - lead;
-                    if (col >= 0 && col < a.width) m |= kV == 4 ? 0xffffffffu : 0xffffu << 16 * j;
-                }
-                reinterpret_cast<uint32_t *>(to)[i] = m;
+            for (int j = 0; j < kV / 4; ++j) {
+                const int col = i * (kV / 4) + j - lead;
+                if (col >= 0 && col < a.width) m |= kV == 4 ? 0xffffffffu : 0xffffu << 16 * j;
             }
+            reinterpret_cast<uint32_t *>(to)[i] = m;
+        }
+    }
+    __device__ void inside(const char *edges, int c, float2 (&in)[kHalf]) const {
+        const float *from = reinterpret_cast<const float *>(edges + kEdgeKinds * 16) + kind(c) * kV;
+#pragma unroll
+        for (int h = 0; h < kV / 4; ++h) {
+            const float4 q = *reinterpret_cast<const float4 *>(from + 4 * h);
+            in[2 * h] = make_float2(q.x, q.y), in[2 * h + 1] = make_float2(q.z, q.w);
         }
     }
 };

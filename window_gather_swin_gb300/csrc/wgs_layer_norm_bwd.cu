@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_norm_backward(const LayerNo
     };
     float2 now = stats(p.row), next = stats(p.row + p.row_step);
     p.keep_param(weight, a.weight, 1.f);
-    p.keep_masks(mask_words);
+    if constexpr (!kWhole) p.keep_masks(mask_words);
     __syncthreads();
     float2 gw[kPairs], gb[kPairs];
 #pragma unroll
@@ -50,8 +50,8 @@ __global__ void __launch_bounds__(kThreads, 1) layer_norm_backward(const LayerNo
         const float2 less = both(-now.x), rstd = both(now.y);
         p.arrived();
         float2 h[kPairs], g[kPairs];
-        p.load(0, masks, h);
-        p.load(1, masks, g);
+        p.template load<true>(0, masks, h);
+        p.template load<true>(1, masks, g);
         float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_norm_backward(const LayerNo
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) g[i] = mul2(fma2(h[i], c2, add2(g[i], c1)), rstd);
         if (a.tensors == 3) {
-            p.load(2, masks, h);
+            p.template load<true>(2, masks, h);
 #pragma unroll
             for (int i = 0; i < kPairs; ++i) g[i] = add2(g[i], h[i]);
         }
@@ -162,15 +162,15 @@ wgs_status run_unit(LayerNormArgs a, cudaStream_t stream, int *blocks) {
     *blocks = cut.blocks;
     const int stage = cut.threads * a.tensors * kC * 16;
     a.stages = kRing / stage < 1 ? 1 : kRing / stage < kMaxStages ? kRing / stage : kMaxStages;
-    // the weight, and what tells a ragged row's own
+    // the weight, and what of a ragged row's chunks is its own
     a.kept_bytes = kC * (kTeam == 0 ? 32 * a.team_warps : kTeam) * (kWhole ? 4 * P::kV : 4 * P::kV + 16);
     int smem = a.kept_bytes + a.stages * stage;
     const int sums = 8 * a.width * cut.units;
     if (smem < sums) smem = sums;
     auto kernel = layer_norm_backward<E, kC, kTeam, kWhole>;
-    // As the forward's.  (At most 66 KB beside a stage of six chunks from three
-    // tensors, 108 KB, and 48 KB beside 168 KB of others.)
-    if (smem > 45 << 10 &&
+    // As the forward's.  (At most 68 KB beside a stage of six chunks from three
+    // tensors, 99 KB, and 51 KB beside 168 KB of others.)
+    if (smem > 40 << 10 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 216 << 10) != cudaSuccess) {
         cudaGetLastError();
         return WGS_ERR_LAUNCH;
