@@ -37,7 +37,8 @@
  *     the wait, so the usual stream order holds for every buffer.  (A call of
  *     several kernels, position_bias_bwd or group_norm_act and its backward,
  *     may have its second one read the call's inputs while its first one
- *     runs, never before that one has waited.)
+ *     runs, never before that one has waited; embedding_bwd's last one reads the
+ *     workspace so.)
  *   - Arguments are checked before anything is launched; a failed check
  *     returns a status and launches nothing.  A launch failure reported by
  *     the runtime returns WGS_ERR_LAUNCH.
@@ -58,8 +59,9 @@
  *     which belongs to the context: the first call on a device does it, and
  *     in a later context (after cudaDeviceReset, say) the first launch there
  *     is rejected by the runtime, the limit raised and the launch retried;
- *     make that call outside stream capture too.  (position_bias_bwd and the
- *     group norms raise theirs on every call, which captures as well.)
+ *     make that call outside stream capture too.  (position_bias_bwd, the
+ *     group and layer norms and embedding_bwd raise theirs on every call, which
+ *     captures as well.)
  */
 #ifndef WGS_H
 #define WGS_H
@@ -530,8 +532,11 @@ wgs_status group_norm_act_bwd(const void *grad_y, const void *x, const void *wei
  *           (a bias needs a weight).
  *   mean, rstd  float [rows], written for the backward; both or neither.
  * width: 1 to 8192 (else WGS_ERR_WIDTH).  Pointers need their element's
- * alignment; with width a multiple of 4 and rows that start on four elements
- * the values are moved in fours (the sums' order differs). */
+ * alignment.  Rows are moved in 16-byte chunks whatever the width, so the first
+ * one's 16 bytes in memory may be read from their start where x does not begin on
+ * 16; tensors whose rows start at different places in a chunk are moved element by
+ * element.  Sums run in an order that depends on the sizes, the format and where
+ * rows start. */
 wgs_status layer_norm(const void *x, const void *weight, const void *bias, void *y, float *mean,
                       float *rstd, int64_t rows, int32_t width, float eps, wgs_dtype dtype,
                       wgs_dtype param_dtype, cudaStream_t stream);
@@ -557,7 +562,7 @@ wgs_status residual_add_layer_norm(const void *residual, const void *branch, con
  * grad_residual is the gradient that reaches residual_out past the norm (NULL:
  * none), and grad_x then is the gradient of residual and of branch.  A thread
  * adds its rows one after another, of which there are about rows / 152 over its
- * block's units: the sums' order depends on the sizes alone.
+ * block's units; the sums' order depends on what the forward's does.
  *   grad_y, x, grad_residual, grad_x  as x above; grad_x may equal any of
  *           the others.
  *   mean, rstd  as the forward wrote them.
@@ -579,7 +584,7 @@ wgs_status layer_norm_bwd(const void *grad_y, const void *x, const float *mean, 
 /* ------------------------------------------------------------------ */
 /*     out[i] = fp(scale * table[idx[i]])   for 0 <= idx[i] < n_rows
  *     out[i] = 0                            for idx[i] == -1 (a pad)
- * fp() rounds once, to nearest even, to `dtype`.  window_gather's rule for
+ * The product is one in FP32, which fp() rounds to nearest even in `dtype`.  window_gather's rule for
  * indices: one outside [-1, n_rows) gives a zero row and sets the device error
  * word (wgs_check_error); nothing faults.
  *   table   [n_rows, width] of table_dtype: WGS_F32, or `dtype`.
@@ -587,8 +592,8 @@ wgs_status layer_norm_bwd(const void *grad_y, const void *x, const float *mean, 
  *   out     [n_idx, width] of dtype (any wgs_dtype); must not overlap the
  *           inputs (WGS_ERR_ALIAS).
  * width: 1 to 32768 (else WGS_ERR_WIDTH).  n_idx and n_rows below 2^31 - 1
- * (else WGS_ERR_SHAPE).  Pointers need their element's alignment; 16 bytes of
- * out are moved at a time where all rows start on as many. */
+ * (else WGS_ERR_SHAPE).  Pointers need their element's alignment; 16 bytes of the
+ * table are moved at a time where all rows start on as many (same results). */
 wgs_status embedding(const void *table, const int32_t *idx, void *out, int64_t n_idx,
                      int64_t n_rows, int32_t width, float scale, wgs_dtype table_dtype,
                      wgs_dtype dtype, cudaStream_t stream);
@@ -597,8 +602,8 @@ wgs_status embedding(const void *table, const int32_t *idx, void *out, int64_t n
 /* embedding_bwd -- the table's gradient                                */
 /* ------------------------------------------------------------------ */
 /*     grad_table[r] = fp(scale * sum of grad[i] over the i with idx[i] == r)
- * summed in FP32 over the indices sorted by row, in an order that depends on
- * idx and the sizes alone.  With scale 1 it is also the gradient of
+ * summed in FP32 over the indices sorted by row, positions in order, cut into pieces
+ * of equal size: an order that depends on idx, the sizes and the format alone.  With scale 1 it is also the gradient of
  * window_gather through a map that may name a row more than once.  An index of
  * -1 adds to no row, one outside [-1, n_rows) to none and sets the device error
  * word.

@@ -337,6 +337,15 @@ def _into(out: Optional[torch.Tensor], shape, dtype, device, name: str) -> torch
     return out
 
 
+def _output(out: Optional[torch.Tensor], shape, dtype, device, name: str, index: int):
+    """(the tensor that takes an output, its address): `out` after its checks, or
+    a new one, which needs none."""
+    if out is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return _into(out, shape, dtype, device, name), _given(out, name, dtype, index)
+
+
 def _space(workspace: Optional[torch.Tensor], need, device) -> torch.Tensor:
     return workspace if workspace is not None else torch.empty(max(need(), 16), dtype=torch.uint8,
                                                                device=device)
@@ -666,13 +675,13 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     1 and 0).  Returns (y, mean, rstd); mean and rstd, float32 and shaped as x
     without its last dim, are what layer_norm_bwd takes."""
     index, rows, width, w, b, pt = _layer_norm_args(x, weight, bias, "x")
-    kind, device, lead = x.dtype, x.device, x.shape[:-1]
-    y = torch.empty_like(x) if out is None else _into(out, x.shape, kind, device, "out")
-    m = _into(mean, lead, torch.float32, device, "mean")
-    r = _into(rstd, lead, torch.float32, device, "rstd")
-    _run("layer_norm", _capi.load().layer_norm, index, x.data_ptr(), w, b,
-         _given(y, "out", kind, index), _given(m, "mean", torch.float32, index),
-         _given(r, "rstd", torch.float32, index), rows, width, float(eps), _DTYPE[kind], _DTYPE[pt])
+    kind, device, shape = x.dtype, x.device, x.shape
+    lead = shape[:-1]
+    y, py = _output(out, shape, kind, device, "out", index)
+    m, pm = _output(mean, lead, torch.float32, device, "mean", index)
+    r, pr = _output(rstd, lead, torch.float32, device, "rstd", index)
+    _run("layer_norm", _capi.load().layer_norm, index, x.data_ptr(), w, b, py, pm, pr, rows, width,
+         float(eps), _DTYPE[kind], _DTYPE[pt])
     return y, m, r
 
 
@@ -690,15 +699,13 @@ def residual_add_layer_norm(residual: torch.Tensor, branch: torch.Tensor,
     second = _given(branch, "branch", kind, index)
     if branch.shape != shape:
         _fail("residual and branch must have the same shape")
-    t = (torch.empty_like(residual) if residual_out is None
-         else _into(residual_out, shape, kind, device, "residual_out"))
-    y = torch.empty_like(residual) if out is None else _into(out, shape, kind, device, "out")
-    m = _into(mean, shape[:-1], torch.float32, device, "mean")
-    r = _into(rstd, shape[:-1], torch.float32, device, "rstd")
+    lead = shape[:-1]
+    t, to = _output(residual_out, shape, kind, device, "residual_out", index)
+    y, py = _output(out, shape, kind, device, "out", index)
+    m, pm = _output(mean, lead, torch.float32, device, "mean", index)
+    r, pr = _output(rstd, lead, torch.float32, device, "rstd", index)
     _run("residual_add_layer_norm", _capi.load().residual_add_layer_norm, index, residual.data_ptr(),
-         second, w, b, _given(t, "residual_out", kind, index), _given(y, "out", kind, index),
-         _given(m, "mean", torch.float32, index), _given(r, "rstd", torch.float32, index), rows, width,
-         float(eps), _DTYPE[kind], _DTYPE[pt])
+         second, w, b, to, py, pm, pr, rows, width, float(eps), _DTYPE[kind], _DTYPE[pt])
     return t, y, m, r
 
 
@@ -735,19 +742,18 @@ def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rs
         past = _given(grad_residual, "grad_residual", kind, index)
         if grad_residual.shape != shape:
             _fail("grad_residual and x must have the same shape")
-    gx = torch.empty_like(x) if grad_x is None else _into(grad_x, shape, kind, device, "grad_x")
+    gx, px = _output(grad_x, shape, kind, device, "grad_x", index)
     gw = gb = None
     pw = pb = ws = size = 0
     if weight is not None:
-        gw = _into(grad_weight, (width,), pt, device, "grad_weight")
-        gb = _into(grad_bias, (width,), pt, device, "grad_bias")
-        pw, pb = _given(gw, "grad_weight", pt, index), _given(gb, "grad_bias", pt, index)
+        gw, pw = _output(grad_weight, (width,), pt, device, "grad_weight", index)
+        gb, pb = _output(grad_bias, (width,), pt, device, "grad_bias", index)
         space = _space(workspace, lambda: layer_norm_bwd_workspace_bytes(rows, width), device)
         ws, size = _given(space, "workspace", torch.uint8, index), space.numel()
     elif grad_weight is not None or grad_bias is not None:
         _fail("grad_weight and grad_bias need a weight")
-    _run("layer_norm_bwd", _capi.load().layer_norm_bwd, index, gy, x.data_ptr(), m, r, w, past,
-         _given(gx, "grad_x", kind, index), pw, pb, ws, size, rows, width, _DTYPE[kind], _DTYPE[pt])
+    _run("layer_norm_bwd", _capi.load().layer_norm_bwd, index, gy, x.data_ptr(), m, r, w, past, px, pw, pb,
+         ws, size, rows, width, _DTYPE[kind], _DTYPE[pt])
     return gx, gw, gb
 
 
@@ -773,10 +779,9 @@ def embedding(table: torch.Tensor, idx: torch.Tensor, scale: float = 1.0, dtype=
         _fail(f"dtype must be float32, float16 or bfloat16 (got {dtype})")
     if table.dtype not in (torch.float32, dtype):
         _fail(f"table must be float32 or {dtype} (got {table.dtype})")
-    y = _into(out, (*idx.shape, width), dtype, table.device, "out")
-    _run("embedding", _capi.load().embedding, index, table.data_ptr(), where,
-         _given(y, "out", dtype, index), idx.numel(), n_rows, width, float(scale),
-         _DTYPE[table.dtype], _DTYPE[dtype])
+    y, py = _output(out, (*idx.shape, width), dtype, table.device, "out", index)
+    _run("embedding", _capi.load().embedding, index, table.data_ptr(), where, py, idx.numel(), n_rows,
+         width, float(scale), _DTYPE[table.dtype], _DTYPE[dtype])
     return y
 
 
@@ -812,11 +817,10 @@ def embedding_bwd(grad: torch.Tensor, idx: torch.Tensor, n_rows: int, scale: flo
     if dtype not in (torch.float32, kind):
         _fail(f"dtype must be float32 or {kind} (got {dtype})")
     n = idx.numel()
-    gt = _into(grad_table, (n_rows, width), dtype, grad.device, "grad_table")
+    gt, pt = _output(grad_table, (n_rows, width), dtype, grad.device, "grad_table", index)
     ws = _space(workspace, lambda: embedding_bwd_workspace_bytes(n, n_rows, width), grad.device)
     _run("embedding_bwd", _capi.load().embedding_bwd, index, grad.data_ptr(), where,
-         _given(gt, "grad_table", dtype, index), _given(ws, "workspace", torch.uint8, index),
-         ws.numel(), n, n_rows, width, float(scale), _DTYPE[kind], _DTYPE[dtype])
+         pt, _given(ws, "workspace", torch.uint8, index), ws.numel(), n, n_rows, width, float(scale), _DTYPE[kind], _DTYPE[dtype])
     return gt
 
 

@@ -932,6 +932,9 @@ __global__ void __launch_bounds__(kSortThreads) sum_few(const SumArgs a, const i
     constexpr int64_t kBits = kBins * 32;
     const int64_t row0 = static_cast<int64_t>(a.n_rows) * block / blocks, row1 = static_cast<int64_t>(a.n_rows) * (block + 1) / blocks;
     const int lane = thread & 31, warp = thread >> 5;
+    int lanes = 1;      // of a row
+    while (lanes < 32 && lanes < (kChunks ? a.width * kBytes<P> / 16 : a.width)) lanes *= 2;
+    const int rows_at_once = 32 / lanes;
     for (int64_t r0 = row0; r0 < row1; r0 += kBits) {
         const int64_t r1 = r0 + kBits < row1 ? r0 + kBits : row1;
         __syncthreads();
@@ -944,14 +947,14 @@ __global__ void __launch_bounds__(kSortThreads) sum_few(const SumArgs a, const i
             atomicOr(&base[bit / 32], 1u << bit % 32);
         }
         __syncthreads();
-        for (int64_t r = r0 + warp; r < r1; r += kSortWarps) {
+        for (int64_t r = r0 + warp * rows_at_once + lane / lanes; r < r1; r += kSortWarps * rows_at_once) {
             const int bit = static_cast<int>(r - r0);
             if (base[bit / 32] >> bit % 32 & 1u) continue;
             char *row = a.out + r * a.width * kBytes<P>;
             if constexpr (kChunks) {
-                for (int i = lane; i < a.width * kBytes<P> / 16; i += 32) st_stream(row + 16 * i, make_uint4(0u, 0u, 0u, 0u));
+                for (int i = lane % lanes; i < a.width * kBytes<P> / 16; i += lanes) st_stream(row + 16 * i, make_uint4(0u, 0u, 0u, 0u));
             } else {
-                for (int i = lane; i < a.width; i += 32) write_one<P>(row, i, 0.f);
+                for (int i = lane % lanes; i < a.width; i += lanes) write_one<P>(row, i, 0.f);
             }
         }
     }
