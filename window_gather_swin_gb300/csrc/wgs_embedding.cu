@@ -474,6 +474,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs a) {
 
 // -------------------------------------------------------------------- sums --
 
+// A slot's rows are copied eight ahead of its sums (rows scattered over memory, bound
+// by how many are in flight and by the instructions a row takes), a thread each 16
+// bytes of columns.  131040 rows of 384 bf16 into 32768 rows: 27 to 29 us of 58 for the
+// call, 4.3 TB/s read and written (floor of the call 22.3); of 192 fp16 into 24 rows 12.5
+// of 20.7 (7.5); rows of 383 take 87 us.  Four rows ahead with five blocks an SM in place
+// of four 60 and 21.4 us; six 64 and 22.1.
 constexpr int kSumThreads = 256;
 constexpr int kAhead = 8;              // rows that a thread has in flight
 // Of a block: the slots' ends are joined one after another.
@@ -735,7 +741,9 @@ __global__ void __launch_bounds__(kSumThreads) sum_runs(const SumArgs a) {
 // Runs that go over the end of the piece they began in: the sums of the pieces that
 // each reaches into.  A block looks through some of the pieces for such beginnings.
 // A run of a few pieces is a warp's, 128 columns at a time; a long one the block's,
-// whose groups of threads add every groups-th piece's sums, and then the groups'.
+// whose groups of threads add every groups-th piece's sums, and then the groups'.  (Run
+// by the last of a run's blocks inside the sums' launch, told by counters, it cost more
+// than this launch does: 22 us in place of 12.5 + 6.4 for 24 rows of 192.)
 __device__ __forceinline__ float4 plus(float4 a, float4 b) {
     return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
@@ -1101,8 +1109,11 @@ wgs_status sort_indices(SortArgs &s, const Plan &z, char *ws, char *out, int64_t
     const int64_t counts = 1ll * z.sort_blocks * z.count_bytes << z.bits;   // of a pass
     auto count = z.count_bytes == 2 ? sort_count<uint16_t> : sort_count<uint32_t>;
     auto order = z.count_bytes == 2 ? sort_place<uint16_t> : sort_place<uint32_t>;
-    // a share of the zeros in each launch, 64 bytes a thread or more
-    const int64_t share = ceil_div(ceil_div(bytes, 1 + z.passes), 16) * 16, most = 4 * sms - z.sort_blocks;
+    // A share of the zeros in each launch, 64 bytes a thread or more, by as many blocks as
+    // are resident beside the sort's (with 88 blocks 57 us in place of 53 for 32768 rows of
+    // 384 FP32).  Zeros in the rows alone that no index names, written by blocks of the sums'
+    // launch, took those 6 us longer and spared the sort 5.
+    const int64_t share = ceil_div(ceil_div(bytes, 1 + z.passes), 16) * 16, most = 2 * sms - z.sort_blocks;
     const int smem = kSortTile * 8 + Ranker::kTableBytes;
     // (as the layer norm's)
     if (cudaFuncSetAttribute(order, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {

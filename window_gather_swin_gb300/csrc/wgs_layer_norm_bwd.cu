@@ -8,6 +8,13 @@
 // same in all its rows, so their sums stay in registers while rows stream past; a
 // block's units add theirs up in shared memory, and a second launch the blocks', all
 // in a fixed order.  One block an SM, which walks the rows with all others.
+//
+// Measured, us a call in a row of calls, and of the copy rate: [131040, 192] fp16 29.7
+// (75 %), FP32 49.6 (90 %); [32760, 1536] bf16 with the residual stream's gradient 66
+// (90 %); [32761, 771] bf16 54 (41 %).  A thread's 24 columns take 48 registers of sums
+// beside 48 of values, so twelve warps an SM: they issue in half of their cycles and
+// wait for their own results (shuffles, shared memory) in most others.  The second
+// launch shows 2 to 3 us at the end of a call.
 #include "wgs_layer_norm.cuh"
 
 namespace wgs {
