@@ -4,12 +4,14 @@ the definitions in double precision.
 The lookup is one FP32 product and one rounding to the output's format, which
 torch's elementwise operations do as well: the bits are equal.
 
-The gradient's sums: a slot's indices (at most 64), the slots of a piece (at most
-256), every fourth or fewer of the pieces that a run reaches into (of which there
-are at most 913, or indices / 64) and those sums (at most 32); of at most 2048
-indices no more than all, one after another.  So with D = 64 + 256 + 229 + indices
-/ 256 + 32, or 2048, additions and u = 2^-24 the sum is off by D u of its terms'
-magnitudes, the product with scale by u, and rounding to the
+The gradient's sums.  Indices of a sorted piece: a slot's (at most 64), the slots of
+a piece (at most 256), every fourth or fewer of the pieces that a run reaches into (of
+which there are at most 913, or indices / 64) and those sums (at most 32).  Of a tile,
+where the table has few rows or the call few indices: all of the tile's, at most 2048,
+one after another, and the tiles, of which there are at most 152, or indices / 2048.  So
+with D = 2048 + 152 + 64 + 256 + 229 + indices / 256 + 32 additions, which covers both,
+and u = 2^-24 the sum is off by D u of its terms' magnitudes, the product with scale by
+u, and rounding to the
 output's format by half a step.  Where all values are small whole numbers every
 sum is exact, and the result has to be.
 """
@@ -149,7 +151,7 @@ def _check_gradient(grad, idx, rows, scale, got):
         mag[:, lo:lo + 256].index_add_(0, idx[keep].long(), g.abs())
     s = torch.tensor(scale, dtype=torch.float32).double().item()
     want *= s
-    most = 64 + 256 + 229 + n / 256 + 32 if n > 2048 else n
+    most = min(n, 2048) + 152 + 64 + 256 + 229 + n / 256 + 32
     tol = (most * U * abs(s) * mag + U * want.abs()) * (1 + torch.finfo(got.dtype).eps) + _half_step(want, got.dtype)
     err = (got.double() - want).abs()
     assert (err <= tol).all(), (err / tol).max()
@@ -189,7 +191,11 @@ def test_gradient(shape, fmt, tfmt, kind):
                                         ((262145, 1, 8), "one"), ((700000, 500, 4), "uniform"),
                                         ((3000000, 2 ** 21, 2), "uniform"), ((262144, 2 ** 18, 16), "once"),
                                         ((131072, 2 ** 17 - 1, 24), "runs"), ((9000000, 2 ** 28, 1), "skew"),
-                                        ((8500000, 3000, 2), "uniform")], ids=str)
+                                        ((8500000, 3000, 2), "uniform"), ((131040, 27, 40), "skew"), ((131040, 26, 40), "skew"),
+                                        ((131040, 53, 20), "uniform"), ((131040, 54, 20), "uniform"),
+                                        ((5000, 1, 4100), "one"), ((311297, 3, 1027), "uniform"),
+                                        ((20000, 2, 1), "none"), ((400000, 100, 33), "skew"), ((400000, 64, 72), "skew"),
+                                        ((30001, 6, 8), "runs")], ids=str)
 @pytest.mark.parametrize("fmt,tfmt", [("f32", "f32"), ("f16", "f16"), ("bf16", "f32")])
 def test_gradient_of_many_indices(shape, kind, fmt, tfmt):
     n, rows, width = shape

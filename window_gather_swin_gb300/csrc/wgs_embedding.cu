@@ -495,6 +495,7 @@ struct SumArgs {
     int32_t n_rows;
     int width, cols;             // cols: threads of a row
     int each, piece;             // indices of a slot and of a block
+    int64_t out_step;            // bytes from a tile's table to the next one's
     float scale;
 };
 
@@ -856,7 +857,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a) {
     }
 }
 
-// ---------------------------------------------------------------- few indices --
+// ------------------------------------------------- few indices, few table rows --
 
 // Where a block can sort all indices, every block does, and takes the runs that begin
 // in its share of the order, whole ones, so that nothing is left for another launch:
@@ -867,19 +868,30 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a) {
 constexpr int kFew = 1024;
 static_assert(kFew <= kSortTile, "a tile of the sort");
 
+// Where the table has few rows, a block does the same with a tile of neighbouring
+// indices, whose gradients are one run of bytes (which L2 is asked for while the block
+// sorts), into a table of its own; a second launch adds the blocks' tables.  TILED
+constexpr int kTileBlocks = 152;       // one an SM
+
 template <typename E, typename P, bool kChunks>
-__global__ void __launch_bounds__(kSortThreads) sum_few(const SumArgs a, const int32_t *idx, int passes, int bits) {
+__global__ void __launch_bounds__(kSortThreads) sum_tile(const SumArgs args, const int32_t *idx, int passes, int bits,
+                                                         int range) {
     extern __shared__ __align__(16) char memory[];
     __shared__ int32_t warp_sums[kSortWarps];
     __shared__ uint32_t base[kBins];
     using Layout = SumLayout<E, kChunks>;
     constexpr int kV = 16 / kBytes<E>;
     static_assert(Layout::ring_bytes(kSortThreads) <= Ranker::kTableBytes, "the ring takes the sort's tables' place");
+    // range: of a block's tile; 0 where every block takes all indices
+    const bool tiled = range > 0;
+    SumArgs a = args;
+    a.out += blockIdx.x * args.out_step;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * range;
+    const int n = static_cast<int>(tiled && a.n - first > range ? range : a.n - first), thread = threadIdx.x;
     int2 *tokens = reinterpret_cast<int2 *>(memory) + 2;      // [-1] ... [n]
-    char *tables = memory + (kFew + 4) * 8;
+    char *tables = memory + ((tiled ? range : static_cast<int>(a.n)) + 5) / 2 * 16;
     uint2 *pairs = reinterpret_cast<uint2 *>(tokens);
     const Ranker ranker(tables, warp_sums, base);
-    const int n = static_cast<int>(a.n), thread = threadIdx.x;
     ranker.clear(1 << bits);
     pdl_prologue();
     uint32_t key[kRounds], at[kRounds];
@@ -888,9 +900,20 @@ __global__ void __launch_bounds__(kSortThreads) sum_few(const SumArgs a, const i
         const int i = Ranker::first() + 32 * j;
         key[j] = at[j] = 0u;
         if (i < n) {
-            const int32_t k = __ldg(idx + i);
-            key[j] = static_cast<uint32_t>(k >= 0 && k < a.n_rows ? k : a.n_rows), at[j] = i;
-            if ((k < -1 || k >= a.n_rows) && blockIdx.x == 0) atomicOr(&g_embedding_error, 1u);
+            const int32_t k = __ldg(idx + first + i);
+            key[j] = static_cast<uint32_t>(k >= 0 && k < a.n_rows ? k : a.n_rows), at[j] = static_cast<uint32_t>(first + i);
+            if ((k < -1 || k >= a.n_rows) && (tiled || blockIdx.x == 0)) atomicOr(&g_embedding_error, 1u);
+        }
+    }
+    if (tiled) {
+        // the tile's gradients, a piece a thread
+        constexpr int kPiece = 16 << 10;
+        const int64_t row_bytes = static_cast<int64_t>(a.width) * kBytes<E>;
+        const uintptr_t from = (reinterpret_cast<uintptr_t>(a.grad) + first * row_bytes + 15) & ~uintptr_t(15);
+        const uintptr_t to = (reinterpret_cast<uintptr_t>(a.grad) + (first + n) * row_bytes) & ~uintptr_t(15);
+        for (uintptr_t p = from + static_cast<uintptr_t>(thread) * kPiece; p < to; p += static_cast<uintptr_t>(kSortThreads) * kPiece) {
+            const uint32_t bytes = to - p < kPiece ? static_cast<uint32_t>(to - p) : kPiece;
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
         }
     }
     for (int pass = 0;;) {
@@ -908,7 +931,7 @@ __global__ void __launch_bounds__(kSortThreads) sum_few(const SumArgs a, const i
     __syncthreads();
 
     // the runs that begin in this block's share of the order
-    const int blocks = gridDim.x, block = blockIdx.x;
+    const int blocks = tiled ? 1 : gridDim.x, block = tiled ? 0 : blockIdx.x;
     auto begin = [&](int64_t b) {
         const int i = static_cast<int>(b * named / blocks);
         if (i == 0 || i >= named || tokens[i].x != tokens[i - 1].x) return i;
@@ -968,6 +991,26 @@ __global__ void __launch_bounds__(kSortThreads) sum_few(const SumArgs a, const i
     }
 }
 
+// The blocks' tables added up: 32 values a block, 16 threads a value.
+template <typename P>
+__global__ void __launch_bounds__(512) add_tables(const float *part, int blocks, int64_t values, float scale, char *out) {
+    __shared__ float sums[16][33];
+    pdl_prologue();
+    const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+    const int64_t v = blockIdx.x * 32ll + lane;
+    float s = 0.f;
+    if (v < values) {
+#pragma unroll 10
+        for (int b = group; b < blocks; b += 16) s += __ldcg(part + b * values + v);
+    }
+    sums[group][lane] = s;
+    __syncthreads();
+    if (group > 0 || v >= values) return;
+#pragma unroll
+    for (int g = 1; g < 16; ++g) s += sums[g][lane];
+    write_one<P>(out, v, s * scale);
+}
+
 __global__ void __launch_bounds__(256) fill_zeros(char *p, int64_t n, int bytes) {
     pdl_prologue();
     write_zeros(p, n, bytes, static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, gridDim.x * 256ll);
@@ -984,7 +1027,8 @@ bool sizes_ok(int64_t n_idx, int64_t n_rows) {
 
 // How a gradient is cut, and where its parts lie in the workspace.
 struct Plan {
-    bool few;
+    bool few;                        // one launch
+    int tile, tile_blocks;           // or two, in tiles of so many indices (0: not so)
     int passes, bits, sort_blocks;   // of the sort
     int64_t range;
     int slices, cols, slots, each, piece;
@@ -1007,10 +1051,18 @@ Plan plan_of(int64_t n, int64_t n_rows, int32_t width, int v) {
     z.count_bytes = z.range < 65536 ? 2 : 4;
     const int parts = static_cast<int>(ceil_div(width, v));
     z.few = n <= kFew;
-    z.slices = static_cast<int>(ceil_div(parts, z.few ? kSortThreads : kSumThreads));
+    // a tile an SM (or the largest ones), of four indices for each 16 bytes of a column of
+    // the table at least, so that the blocks' tables, written and read, are an eighth of
+    // the gradients' bytes at most
+    const int64_t tile = ceil_div(n, kTileBlocks) < kSortTile ? ceil_div(n, kTileBlocks) : kSortTile;
+    if (!z.few && n_rows > 0 && 4 * n_rows * v <= tile) {
+        z.tile = static_cast<int>(tile);
+        z.tile_blocks = static_cast<int>(ceil_div(n, tile));
+    }
+    z.slices = static_cast<int>(ceil_div(parts, z.few || z.tile ? kSortThreads : kSumThreads));
     z.cols = static_cast<int>(ceil_div(parts, z.slices));
-    if (z.few) {
-        z.bytes = n ? 16 : 0;
+    if (z.few || z.tile) {
+        z.bytes = z.tile ? 4ll * z.tile_blocks * n_rows * width : n ? 16 : 0;
         return z;
     }
     z.slots = kSumThreads / z.cols < kMostSlots ? kSumThreads / z.cols : kMostSlots;
@@ -1064,25 +1116,42 @@ wgs_status run_sums(const SumArgs &a, const Plan &z, int sms, cudaStream_t strea
     return launch(join_runs<P>, dim3(static_cast<unsigned>(blocks)), dim3(kJoinThreads), 0, stream, a);
 }
 
+// Few indices, P the table's gradient's format; or a tile a block, P FP32.
 template <typename E, typename P, bool kChunks>
-wgs_status run_few(const SumArgs &a, const int32_t *idx, const Plan &z, int sms, cudaStream_t stream) {
+wgs_status run_tile(const SumArgs &a, const int32_t *idx, const Plan &z, int sms, cudaStream_t stream) {
     constexpr int kV = 16 / kBytes<E>;
     const int slots = kSortThreads / z.cols < kMostSlots ? kSortThreads / z.cols : kMostSlots;
-    const int smem = (kFew + 4) * 8 + Ranker::kTableBytes + 8 * slots * z.cols * kV;
-    auto kernel = sum_few<E, P, kChunks>;
+    const int tokens = ((z.tile ? z.tile : static_cast<int>(a.n)) + 5) / 2 * 16;
+    const int smem = tokens + Ranker::kTableBytes + 8 * slots * z.cols * kV;
+    auto kernel = sum_tile<E, P, kChunks>;
     // (as the layer norm's)
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (kFew + 4) * 8 + Ranker::kTableBytes + 8 * kSortThreads * kV) != cudaSuccess) {
+                             (kSortTile + 5) / 2 * 16 + Ranker::kTableBytes + 8 * kSortThreads * kV) != cudaSuccess) {
         cudaGetLastError();
         return WGS_ERR_LAUNCH;
     }
-    // an index a slot, or 8 KB of zeros a block
-    const int64_t bytes = static_cast<int64_t>(a.n_rows) * a.width * kBytes<P>;
-    int64_t blocks = ceil_div(a.n, slots);
-    if (blocks < ceil_div(bytes, 8192)) blocks = ceil_div(bytes, 8192);
-    if (blocks > sms) blocks = sms;
+    int64_t blocks = z.tile_blocks;
+    if (z.few) {
+        // an index a slot, or 8 KB of zeros a block
+        const int64_t bytes = static_cast<int64_t>(a.n_rows) * a.width * kBytes<P>;
+        blocks = ceil_div(a.n, slots);
+        if (blocks < ceil_div(bytes, 8192)) blocks = ceil_div(bytes, 8192);
+        if (blocks > sms) blocks = sms;
+    }
     return launch(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kSortThreads), static_cast<size_t>(smem), stream, a, idx,
-                  z.passes, z.bits);
+                  z.passes, z.bits, z.tile);
+}
+
+template <typename E, typename P, bool kChunks>
+wgs_status run_tiles(SumArgs a, const int32_t *idx, const Plan &z, int sms, cudaStream_t stream) {
+    const int64_t values = static_cast<int64_t>(a.n_rows) * a.width;
+    const float scale = a.scale;
+    char *out = a.out;
+    a.out = reinterpret_cast<char *>(a.part), a.out_step = 4 * values, a.scale = 1.f;
+    const wgs_status st = run_tile<E, F32, kChunks>(a, idx, z, sms, stream);
+    if (st != WGS_OK) return st;
+    return launch(add_tables<P>, dim3(static_cast<unsigned>(ceil_div(values, 32))), dim3(512), 0, stream,
+                  static_cast<const float *>(a.part), z.tile_blocks, values, scale, out);
 }
 
 // 16 bytes of gradient at a time where all rows, and those of the output, start
@@ -1095,9 +1164,13 @@ template <typename E>
 wgs_status run_format(const SumArgs &a, const int32_t *idx, const Plan &z, bool chunks, bool p32, int sms,
                       cudaStream_t stream) {
     if (z.few && chunks)
-        return p32 ? run_few<E, F32, true>(a, idx, z, sms, stream) : run_few<E, E, true>(a, idx, z, sms, stream);
+        return p32 ? run_tile<E, F32, true>(a, idx, z, sms, stream) : run_tile<E, E, true>(a, idx, z, sms, stream);
     if (z.few)
-        return p32 ? run_few<E, F32, false>(a, idx, z, sms, stream) : run_few<E, E, false>(a, idx, z, sms, stream);
+        return p32 ? run_tile<E, F32, false>(a, idx, z, sms, stream) : run_tile<E, E, false>(a, idx, z, sms, stream);
+    if (z.tile && chunks)
+        return p32 ? run_tiles<E, F32, true>(a, idx, z, sms, stream) : run_tiles<E, E, true>(a, idx, z, sms, stream);
+    if (z.tile)
+        return p32 ? run_tiles<E, F32, false>(a, idx, z, sms, stream) : run_tiles<E, E, false>(a, idx, z, sms, stream);
     if (chunks) return p32 ? run_sums<E, F32, true>(a, z, sms, stream) : run_sums<E, E, true>(a, z, sms, stream);
     return p32 ? run_sums<E, F32, false>(a, z, sms, stream) : run_sums<E, E, false>(a, z, sms, stream);
 }
@@ -1239,7 +1312,7 @@ extern "C" wgs_status embedding_bwd(const void *grad, const int32_t *idx, void *
     char *ws = static_cast<char *>(workspace);
     SortArgs s = {};
     s.idx = idx, s.n = n_idx, s.n_rows = static_cast<int32_t>(n_rows);
-    if (!z.few)
+    if (!z.few && !z.tile)
         st = sort_indices(s, z, ws, static_cast<char *>(grad_table), tbytes, static_cast<int>(tb), dev.sm_count, stream);
     if (st != WGS_OK || (n_rows == 0 && !z.few)) return st;
     SumArgs a = {};
