@@ -234,7 +234,7 @@ constexpr int kBins = 512;
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 constexpr int kRounds = 4;             // indices of a thread at a time
 constexpr int kSortTile = kSortThreads * kRounds;
-// At most: every block reads all blocks' counts.  131040 indices into 24 and 32768 rows,
+// Of blocks with a tile or less each: every block reads all blocks' counts.  131040 indices into 24 and 32768 rows,
 // whole calls: 22.2 and 57.9 us, with 32 blocks 24.8 and 65.9, with 128 22.3 and 56.3,
 // but the windows' map 52.1, 56.8 and 55.0.
 constexpr int kSortBlocks = 64;
@@ -1045,8 +1045,13 @@ Plan plan_of(int64_t n, int64_t n_rows, int32_t width, int v) {
     z.passes = static_cast<int>(ceil_div(bits, 9));
     z.bits = static_cast<int>(ceil_div(bits, z.passes));
     if (z.bits < 4) z.bits = 4;      // whole 16 bytes of a block's counts
-    // whole rounds of a block's threads
-    z.range = ceil_div(ceil_div(n, kSortThreads), kSortBlocks) * kSortThreads;
+    // whole rounds of a block's threads; twice the blocks where a tile each is too little
+    int64_t rounds = ceil_div(ceil_div(n, kSortThreads), kSortBlocks);
+    if (rounds > kRounds) {
+        rounds = ceil_div(ceil_div(n, kSortThreads), 2 * kSortBlocks);
+        if (rounds < kRounds) rounds = kRounds;
+    }
+    z.range = rounds * kSortThreads;
     z.sort_blocks = n ? static_cast<int>(ceil_div(n, z.range)) : 0;
     z.count_bytes = z.range < 65536 ? 2 : 4;
     const int parts = static_cast<int>(ceil_div(width, v));
