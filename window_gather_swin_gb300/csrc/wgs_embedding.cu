@@ -13,7 +13,8 @@
 // sorted order, whatever rows they fall on: a block sums its piece's runs of equal
 // rows, writes those that end inside it, and leaves what reaches over its ends to
 // a last launch, which adds a run's pieces up.  So the work is even if one row has
-// most of the indices, and the order of additions is fixed.
+// most of the indices, and the order of additions is fixed.  Few indices, or few rows
+// of the table, take one or two launches in which blocks sort for themselves.
 #include <type_traits>
 
 #include "wgs_common.cuh"
@@ -234,9 +235,10 @@ constexpr int kBins = 512;
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 constexpr int kRounds = 4;             // indices of a thread at a time
 constexpr int kSortTile = kSortThreads * kRounds;
-// Of blocks with a tile or less each: every block reads all blocks' counts.  131040 indices into 24 and 32768 rows,
-// whole calls: 22.2 and 57.9 us, with 32 blocks 24.8 and 65.9, with 128 22.3 and 56.3,
-// but the windows' map 52.1, 56.8 and 55.0.
+// Blocks of a tile or less each, twice as many before a block takes more: every block
+// reads all blocks' counts.  131040 indices into 24 and 32768 rows and 131040 rows once
+// each, whole calls: 22.2, 57.9 and 52.1 us, with 32 blocks 24.8, 65.9 and 56.8, with 128
+// 22.3, 56.3 and 55.0.
 constexpr int kSortBlocks = 64;
 
 struct SortArgs {
@@ -870,7 +872,9 @@ static_assert(kFew <= kSortTile, "a tile of the sort");
 
 // Where the table has few rows, a block does the same with a tile of neighbouring
 // indices, whose gradients are one run of bytes (which L2 is asked for while the block
-// sorts), into a table of its own; a second launch adds the blocks' tables.  TILED
+// sorts), into a table of its own; a second launch adds the blocks' tables.  131040
+// indices into 24 rows of 192 fp16 take 18.8 us so, 20.6 by pieces of a sorted order,
+// into one row 17 and 44; into 48 rows, with fewer and larger tiles, 24 and 23.
 constexpr int kTileBlocks = 152;       // one an SM
 
 template <typename E, typename P, bool kChunks>
