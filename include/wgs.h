@@ -609,7 +609,8 @@ wgs_status embedding(const void *table, const int32_t *idx, void *out, int64_t n
  * word.
  *   grad        [n_idx, width] of dtype (any wgs_dtype).
  *   grad_table  [n_rows, width] of table_dtype (WGS_F32, or `dtype`); every
- *               row is written, zeros where no index names it.
+ *               row is written, zeros where no index names it (all of them with
+ *               n_idx == 0).
  *   workspace at least wgs_embedding_bwd_workspace_bytes(...) bytes, 16-byte
  *             aligned, disjoint from the tensors; its contents on entry do not
  *             matter.  Calls that overlap on the GPU need their own.  (0 bytes

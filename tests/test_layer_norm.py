@@ -312,6 +312,34 @@ def test_views_that_start_anywhere(shape, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 1), (1, 7), (2, 3), (5, 8), (9, 20), (257, 64), (13, 771), (2000, 96), (30, 2050),
+                                   (5, 1536), (3, 8190)], ids=str)
+def test_views_that_all_start_at_the_same_place(shape, fmt):
+    """All tensors the same number of elements into 16 bytes: rows are read in chunks
+    that begin before the first one.  With fewer rows than lanes and units take, and
+    with more."""
+    rows, width = shape
+    x, w, b, gy, add = _inputs(rows, width, fmt, "f32", 7)
+    size, pad = x.numel(), 40
+    want = wgs.residual_add_layer_norm(x, add, w, b)
+    for shift in range(1, 8):
+        buf = torch.full((6, (size + 2 * pad) // 8 * 8), 3.0, dtype=x.dtype, device=DEV)
+        at = 8 + shift
+        xv, gv, av, yv, tv, gxv = (buf[i, at:at + size].view(x.shape) for i in range(6))
+        xv.copy_(x), gv.copy_(gy), av.copy_(add)
+        y, mean, rstd = wgs.layer_norm(xv, w, b, 1e-5, out=yv)
+        _check_forward(x, w, b, 1e-5, y, mean, rstd)
+        total, y, mean, rstd = wgs.residual_add_layer_norm(xv, av, w, b, residual_out=tv, out=yv)
+        assert _same((total,), want[:1])
+        _check_forward(total, w, b, 1e-5, y, mean, rstd)
+        got = wgs.layer_norm_bwd(gv, tv, mean, rstd, w, av, grad_x=gxv)
+        _check_backward(gy, total, mean, rstd, w, add, got)
+        for i in range(6):
+            assert (buf[i, :at] == 3.0).all() and (buf[i, at + size:] == 3.0).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("width", [96, 771, 1536])
 def test_far_from_zero_outliers_and_constant_rows(width):
     x, w, b, gy, _ = _inputs(500, width, "f32", "f32", 11, offset=0.0)

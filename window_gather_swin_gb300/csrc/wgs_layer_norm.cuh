@@ -210,7 +210,8 @@ struct Place {
     __device__ void fetch() {
         const uint32_t to = slots + coming;
         const bool is_there = next_row < a.rows;
-        const int64_t from_at = is_there ? next_at : 0;
+        // (a copy of no bytes names 16 bytes' boundary all the same)
+        const int64_t from_at = is_there ? next_at : kWhole || !a.together ? 0 : -a.lead * kBytes<E>;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             if (k >= a.tensors) break;
