@@ -340,6 +340,29 @@ def test_views_that_all_start_at_the_same_place(shape, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", [(10, 1), (9, 2), (11, 3), (6, 5), (5, 7), (8, 9)], ids=str)
+def test_narrow_rows_between_nans(shape, fmt):
+    """Rows narrower than 16 bytes, several of which end in the tensor's last 16:
+    what follows and precedes the tensor is neither used nor written."""
+    rows, width = shape
+    x, w, b, gy, add = _inputs(rows, width, fmt, "f32", 11)
+    size = x.numel()
+    for shift in range(8):
+        buf = torch.full((6, (size + 40) // 8 * 8), float("nan"), dtype=x.dtype, device=DEV)
+        xv, gv, av, yv, tv, gxv = (buf[i, 8 + shift:8 + shift + size].view(x.shape) for i in range(6))
+        xv.copy_(x), gv.copy_(gy), av.copy_(add)
+        y, mean, rstd = wgs.layer_norm(xv, w, b, 1e-3, out=yv)
+        _check_forward(x, w, b, 1e-3, y, mean, rstd)
+        total, y, mean, rstd = wgs.residual_add_layer_norm(xv, av, w, b, 1e-3, residual_out=tv, out=yv)
+        _check_forward(total, w, b, 1e-3, y, mean, rstd)
+        got = wgs.layer_norm_bwd(gv, tv, mean, rstd, w, av, grad_x=gxv)
+        _check_backward(gy, total, mean, rstd, w, add, got)
+        for i in range(6):
+            assert buf[i, :8 + shift].isnan().all() and buf[i, 8 + shift + size:].isnan().all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("width", [96, 771, 1536])
 def test_far_from_zero_outliers_and_constant_rows(width):
     x, w, b, gy, _ = _inputs(500, width, "f32", "f32", 11, offset=0.0)

@@ -1,7 +1,7 @@
 // What layer norm's forward and backward kernels share: how rows belong to
 // threads, how they reach them, and how a call is cut.
 //
-// A row belongs to a unit: 8, 16 or 32 lanes of a warp, or several warps.  It is
+// A row belongs to a unit: 4, 8, 16 or 32 lanes of a warp, or several warps.  It is
 // read in chunks of 16 bytes on 16-byte boundaries of memory, chunk c of a unit's
 // thread t being the row's (c threads + t)-th.  A width that is no whole number of
 // chunks makes rows start anywhere in a chunk (`lead` elements after its boundary),
@@ -41,7 +41,7 @@ struct LayerNormArgs {
     const void *weight, *bias;
     float *mean, *rstd;
     float *part;         // backward: [blocks][2][width]
-    int64_t rows;
+    int64_t rows, closing;   // closing: the first row whose chunks may end behind the tensor
     int tensors;         // of in
     int width, chunks;   // chunks: of a row, at most
     int lead, period;    // of row 0, in elements; rows that start at the same place
@@ -225,7 +225,10 @@ struct Place {
                     copy_part(slot, p, is_there ? 16 : 0);
                 } else if (a.together) {
                     int bytes = is_there ? 16 : 0;
-                    if (next_row + 1 == a.rows && !full(c) && column(c) + kV > a.width) bytes = (a.width - column(c)) * kBytes<E>;
+                    if (next_row >= a.closing && is_there && !full(c)) {
+                        const int left = (static_cast<int>(a.rows - next_row) * a.width - column(c)) * kBytes<E>;
+                        if (left < bytes) bytes = left;
+                    }
                     copy_part(slot, p, bytes);
                 } else {
                     uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -464,6 +467,7 @@ bool place_rows(LayerNormArgs *a) {
     while (a->together && a->period < kV && a->width * a->period % kV != 0) a->period *= 2;
     const bool whole = a->together && a->period == 1 && a->lead == 0;
     a->chunks = static_cast<int>(ceil_div(a->width + (whole || !a->together ? 0 : kV - 1), kV));
+    a->closing = a->rows - ceil_div(kV - 1, a->width);
     a->inv = 1.0f / static_cast<float>(a->width);
     return whole;
 }
