@@ -584,9 +584,9 @@ wgs_status layer_norm_bwd(const void *grad_y, const void *x, const float *mean, 
 /* ------------------------------------------------------------------ */
 /*     out[i] = fp(scale * table[idx[i]])   for 0 <= idx[i] < n_rows
  *     out[i] = 0                            for idx[i] == -1 (a pad)
- * The product is one in FP32, which fp() rounds to nearest even in `dtype`.  window_gather's rule for
- * indices: one outside [-1, n_rows) gives a zero row and sets the device error
- * word (wgs_check_error); nothing faults.
+ * The product is one in FP32, which fp() rounds to nearest even in `dtype`.
+ * window_gather's rule for indices: one outside [-1, n_rows) gives a zero row
+ * and sets the device error word (wgs_check_error); nothing faults.
  *   table   [n_rows, width] of table_dtype: WGS_F32, or `dtype`.
  *   idx     int32 [n_idx].
  *   out     [n_idx, width] of dtype (any wgs_dtype); must not overlap the
@@ -603,10 +603,10 @@ wgs_status embedding(const void *table, const int32_t *idx, void *out, int64_t n
 /* ------------------------------------------------------------------ */
 /*     grad_table[r] = fp(scale * sum of grad[i] over the i with idx[i] == r)
  * summed in FP32 over the indices sorted by row, positions in order, cut into pieces
- * of equal size: an order that depends on idx, the sizes and the format alone.  With scale 1 it is also the gradient of
- * window_gather through a map that may name a row more than once.  An index of
- * -1 adds to no row, one outside [-1, n_rows) to none and sets the device error
- * word.
+ * of equal size: an order that depends on idx, the sizes and the format alone.
+ * With scale 1 it is also the gradient of window_gather through a map that may
+ * name a row more than once.  An index of -1 adds to no row, one outside [-1,
+ * n_rows) to none and sets the device error word.
  *   grad        [n_idx, width] of dtype (any wgs_dtype).
  *   grad_table  [n_rows, width] of table_dtype (WGS_F32, or `dtype`); every
  *               row is written, zeros where no index names it (all of them with
@@ -692,7 +692,8 @@ wgs_status wgs_build_shift_regions(const int32_t grid[3], const int32_t window[3
  * an index outside [-1, n_src), any window reverse an inverse index outside
  * [0, n_windowed), or any window_bias_mask_add a window type outside
  * [0, n_types), or a position-bias call a bucket, window type or plan out of
- * its range, or an embedding call an index outside [-1, n_rows); WGS_ERR_LAUNCH if a kernel since then gave up waiting for its own
+ * its range, or an embedding call an index outside [-1, n_rows);
+ * WGS_ERR_LAUNCH if a kernel since then gave up waiting for its own
  * copies to arrive (its outputs are not to be used), and then WGS_ERR_INDEX from
  * the next check if there was a bad index too; WGS_OK otherwise.  The words are
  * shared by every stream of the device. */
