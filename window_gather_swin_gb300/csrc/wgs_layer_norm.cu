@@ -181,6 +181,13 @@ wgs_status run_width(const LayerNormArgs &a, cudaStream_t stream) {
     if (n <= 96) return run_unit<E, 3, 32, kWhole>(a, stream);
     if (n <= 128) return run_unit<E, 4, 32, kWhole>(a, stream);
     const int each = chunks_of_units(n, std::is_same<E, F32>::value && n > 96 * kWarps);
+    // Four where that takes fewer than three quarters of the warps ([32768, 4096] bf16 90
+    // us, with three chunks 104; [16384, 8192] 103, so 116; but [29127, 4608] 126, so 96),
+    // and not for ragged rows ([32760, 4097] 206, so 143), whose ends want more warps.
+    if constexpr (kWhole && !std::is_same<E, F32>::value) {
+        const int warps = static_cast<int>(ceil_div(n, 32 * each)), fewer = static_cast<int>(ceil_div(n, 128));
+        if (fewer <= kBlockWarps<E, 4> && 4 * fewer < 3 * warps) return run_unit<E, 4, 0, kWhole>(a, stream);
+    }
     if (each == 2) return run_unit<E, 2, 0, kWhole>(a, stream);
     if (each == 3) return run_unit<E, 3, 0, kWhole>(a, stream);
     if constexpr (std::is_same<E, F32>::value) return run_unit<E, 6, 0, kWhole>(a, stream);
