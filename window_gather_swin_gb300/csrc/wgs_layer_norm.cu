@@ -10,10 +10,10 @@
 //
 // Measured, us a call in a row of calls, and of the copy rate: [131040, 192] fp16 16.9
 // (6.0 TB/s, 88 %), FP32 33 (89 %); [32761, 768] bf16 with residual 33.5 (89 %), [32761,
-// 771] 45 (66 %); [5000, 8192] FP32 63 (76 %).  24 warps an SM issue in half of their
-// cycles, some 290 instructions for four rows of 192: the start (weights, first rows)
-// and the last rows' way through are the rest.  Ragged rows take 890 instructions a
-// row of 771 where 482 do for 768, most of them for the ends.
+// 771] 45 (66 %); [5000, 8192] FP32 63 (76 %), bf16 37 (65 %).  24 warps an SM issue in
+// half of their cycles, some 290 instructions for four rows of 192: the start (weights,
+// first rows) and the last rows' way through are the rest.  Ragged rows take 890
+// instructions a row of 771 where 482 do for 768, most of them for the ends.
 //
 // Rows in tiles copied in bulk (TMA) into a ring of each warp, with two sums a row
 // from shared memory, took 31 us for the first: a tile's addresses, barriers and
