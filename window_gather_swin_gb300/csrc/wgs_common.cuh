@@ -10,6 +10,7 @@
 #include <utility>
 
 #include "wgs.h"
+#include "wgs_sizes.h"
 
 #ifndef WGS_PDL
 #define WGS_PDL 1  // launch with programmatic dependent launch
@@ -102,8 +103,6 @@ inline bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
 inline bool same_or_disjoint(const void *a, const void *b, int64_t n) {
     return a == b || !overlap(a, n, b, n);
 }
-
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ---------------------------------------------------------- device side --
 

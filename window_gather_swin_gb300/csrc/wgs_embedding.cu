@@ -18,6 +18,7 @@
 #include <type_traits>
 
 #include "wgs_common.cuh"
+#include "wgs_embedding_plan.h"
 
 namespace wgs {
 
@@ -232,14 +233,7 @@ __device__ void write_zeros(char *p, int64_t n, int unit, int64_t thread, int64_
 // blocks with its barriers in place of launches was slower, 35 us for two passes
 // over 131040 indices: 16 SMs rank and place longer than launches take.
 constexpr int kBins = 512;
-constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
-constexpr int kRounds = 4;             // indices of a thread at a time
-constexpr int kSortTile = kSortThreads * kRounds;
-// Blocks of a tile or less each, twice as many before a block takes more: every block
-// reads all blocks' counts.  131040 indices into 24 and 32768 rows and 131040 rows once
-// each, whole calls: 22.2, 57.9 and 52.1 us, with 32 blocks 24.8, 65.9 and 56.8, with 128
-// 22.3, 56.3 and 55.0.
-constexpr int kSortBlocks = 64;
+constexpr int kSortWarps = kSortThreads / 32;
 
 struct SortArgs {
     const int32_t *idx;          // first pass: the call's indices
@@ -482,11 +476,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs a) {
 // call, 4.3 TB/s read and written (floor of the call 22.3); of 192 fp16 into 24 rows 12.5
 // of 20.7 (7.5); rows of 383 take 87 us.  Four rows ahead with five blocks an SM in place
 // of four 60 and 21.4 us; six 64 and 22.1.
-constexpr int kSumThreads = 256;
 constexpr int kAhead = 8;              // rows that a thread has in flight
-// Of a block: the slots' ends are joined one after another.
-constexpr int kMostSlots = 32;
-constexpr int kMostPiece = 2048;       // indices of a block
 
 struct SumArgs {
     const char *grad;
@@ -867,16 +857,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a) {
 // found with a bit for each in shared memory.  180 indices into 366 rows of 192 take
 // 7.1 us so, 12.4 in five launches; 2048 into 300 rows 10.4 and 13.3, but all of them
 // into one row, which is one block's, 21 and 13: half as many are even there.
-constexpr int kFew = 1024;
-static_assert(kFew <= kSortTile, "a tile of the sort");
-
+//
 // Where the table has few rows, a block does the same with a tile of neighbouring
 // indices, whose gradients are one run of bytes (which L2 is asked for while the block
 // sorts), into a table of its own; a second launch adds the blocks' tables.  131040
 // indices into 24 rows of 192 fp16 take 18.8 us so, 20.6 by pieces of a sorted order,
 // into one row 17 and 44; into 48 rows, with fewer and larger tiles, 24 and 23.
-constexpr int kTileBlocks = 152;       // one an SM
-
 template <typename E, typename P, bool kChunks>
 __global__ void __launch_bounds__(kSortThreads) sum_tile(const SumArgs args, const int32_t *idx, int passes, int bits,
                                                          int range) {
@@ -1029,80 +1015,6 @@ bool sizes_ok(int64_t n_idx, int64_t n_rows) {
     return n_idx >= 0 && n_rows >= 0 && n_idx < INT32_MAX && n_rows < INT32_MAX;
 }
 
-// How a gradient is cut, and where its parts lie in the workspace.
-struct Plan {
-    bool few;                        // one launch
-    int tile, tile_blocks;           // or two, in tiles of so many indices (0: not so)
-    int passes, bits, sort_blocks;   // of the sort
-    int64_t range;
-    int slices, cols, slots, each, piece;
-    int64_t pieces;
-    int count_bytes;
-    int64_t keys[2], at[2], counts, part, bytes;
-};
-
-// v: values of a thread
-Plan plan_of(int64_t n, int64_t n_rows, int32_t width, int v) {
-    Plan z = {};
-    int bits = 1;
-    while (bits < 31 && n_rows >> bits) ++bits;     // keys are 0 ... n_rows
-    z.passes = static_cast<int>(ceil_div(bits, 9));
-    z.bits = static_cast<int>(ceil_div(bits, z.passes));
-    if (z.bits < 4) z.bits = 4;      // whole 16 bytes of a block's counts
-    // whole rounds of a block's threads; twice the blocks where a tile each is too little
-    int64_t rounds = ceil_div(ceil_div(n, kSortThreads), kSortBlocks);
-    if (rounds > kRounds) {
-        rounds = ceil_div(ceil_div(n, kSortThreads), 2 * kSortBlocks);
-        if (rounds < kRounds) rounds = kRounds;
-    }
-    z.range = rounds * kSortThreads;
-    z.sort_blocks = n ? static_cast<int>(ceil_div(n, z.range)) : 0;
-    z.count_bytes = z.range < 65536 ? 2 : 4;
-    const int parts = static_cast<int>(ceil_div(width, v));
-    z.few = n <= kFew;
-    // a tile an SM (or the largest ones), of four indices for each 16 bytes of a column of
-    // the table at least, so that the blocks' tables, written and read, are an eighth of
-    // the gradients' bytes at most
-    const int64_t tile = ceil_div(n, kTileBlocks) < kSortTile ? ceil_div(n, kTileBlocks) : kSortTile;
-    if (!z.few && n_rows > 0 && 4 * n_rows * v <= tile) {
-        z.tile = static_cast<int>(tile);
-        z.tile_blocks = static_cast<int>(ceil_div(n, tile));
-    }
-    z.slices = static_cast<int>(ceil_div(parts, z.few || z.tile ? kSortThreads : kSumThreads));
-    z.cols = static_cast<int>(ceil_div(parts, z.slices));
-    if (z.few || z.tile) {
-        z.bytes = z.tile ? 4ll * z.tile_blocks * n_rows * width : n ? 16 : 0;
-        return z;
-    }
-    z.slots = kSumThreads / z.cols < kMostSlots ? kSumThreads / z.cols : kMostSlots;
-    // some six blocks an SM, of slots of 8 to 64 indices (131040 indices into 24 rows of
-    // 192: 22.2 us a call, with four 25.1, with eight 23.8, with twelve 26.1)
-    const int64_t want = ceil_div(n, static_cast<int64_t>(z.slots) * 912);
-    z.each = want < 8 ? 8 : want > 64 ? 64 : static_cast<int>(want);
-    z.piece = z.slots * z.each;
-    z.pieces = ceil_div(n, z.piece);
-    int64_t at = 0;
-    auto place = [&](int64_t bytes) {
-        const int64_t here = at;
-        at += (bytes + 15) / 16 * 16;
-        return here;
-    };
-    for (int i = 0; i < 2; ++i) {
-        if (i < z.passes) z.keys[i] = place(4 * n), z.at[i] = place(4 * n);
-    }
-    z.counts = place(1ll * z.passes * z.sort_blocks * z.count_bytes << z.bits);
-    z.part = place(z.pieces * 8 * width);
-    z.bytes = at;
-    return z;
-}
-
-// A thread's values are four or eight with grad's format, which cuts more or fewer
-// pieces.
-int64_t workspace_of(int64_t n, int64_t n_rows, int32_t width) {
-    const int64_t four = plan_of(n, n_rows, width, 4).bytes, eight = plan_of(n, n_rows, width, 8).bytes;
-    return four > eight ? four : eight;
-}
-
 template <typename E, typename P, bool kChunks>
 wgs_status run_sums(const SumArgs &a, const Plan &z, int sms, cudaStream_t stream) {
     constexpr int kV = 16 / kBytes<E>;
@@ -1191,11 +1103,6 @@ wgs_status sort_indices(SortArgs &s, const Plan &z, char *ws, char *out, int64_t
     const int64_t counts = 1ll * z.sort_blocks * z.count_bytes << z.bits;   // of a pass
     auto count = z.count_bytes == 2 ? sort_count<uint16_t> : sort_count<uint32_t>;
     auto order = z.count_bytes == 2 ? sort_place<uint16_t> : sort_place<uint32_t>;
-    // A share of the zeros in each launch, 64 bytes a thread or more, by as many blocks as
-    // are resident beside the sort's (with 88 blocks 57 us in place of 53 for 32768 rows of
-    // 384 FP32).  Zeros in the rows alone that no index names, written by blocks of the sums'
-    // launch, took those 6 us longer and spared the sort 5.
-    const int64_t share = ceil_div(ceil_div(bytes, 1 + z.passes), 16) * 16, most = 2 * sms - z.sort_blocks;
     const int smem = kSortTile * 8 + Ranker::kTableBytes;
     // (as the layer norm's)
     if (cudaFuncSetAttribute(order, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
@@ -1203,12 +1110,9 @@ wgs_status sort_indices(SortArgs &s, const Plan &z, char *ws, char *out, int64_t
         return WGS_ERR_LAUNCH;
     }
     for (int p = -1; p < z.passes; ++p) {
-        s.zeros = out + (p + 1) * share;
-        s.zero_bytes = bytes - (p + 1) * share < share ? bytes - (p + 1) * share : share;
-        if (s.zero_bytes < 0) s.zero_bytes = 0;
-        int64_t more = ceil_div(s.zero_bytes, 64 * kSortThreads);
-        if (more > most) more = most;
-        const dim3 grid(static_cast<unsigned>(s.blocks + more));
+        const ZeroShare share = zero_share(z, p, bytes, sms);
+        s.zeros = out + share.first, s.zero_bytes = share.bytes;
+        const dim3 grid(static_cast<unsigned>(s.blocks + share.blocks));
         const int q = p < 0 ? 0 : p;
         s.shift = q * z.bits, s.last = q + 1 == z.passes;
         s.counts = ws + z.counts + q * counts;
