@@ -3,6 +3,9 @@
 // The zeros of the table's gradient belong to blocks behind the sort's own: every byte
 // to one launch, a block at least in each that has any, and never fewer blocks in a
 // launch than the sort needs.
+//
+// Where one block may have all of a call's few indices in one row of the table, it has 1 KB
+// of their columns at most, and all columns belong to a block.
 #include <cstdio>
 #include <initializer_list>
 
@@ -21,6 +24,11 @@ int main() {
             for (int w : widths)
                 for (int v : {4, 8}) {
                     const Plan z = plan_of(n, r, w, v);
+                    if (z.few && (z.cols * 16 > 1024 || z.slices < 1 || static_cast<int64_t>(z.slices) * z.cols * v < w ||
+                                  static_cast<int64_t>(z.slices - 1) * z.cols * v >= w))
+                        return std::printf("%lld indices of width %d: %d slices of %d threads\n", static_cast<long long>(n), w,
+                                           z.slices, z.cols),
+                               1;
                     if (z.few || z.tile) continue;
                     for (int sms = 1; sms <= 160; ++sms) {
                         for (int64_t bytes : {r * w * 2, r * w * 4}) {

@@ -856,7 +856,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_runs(const SumArgs a) {
 // one in place of five.  The rows that no index names are a share of the table's rows,
 // found with a bit for each in shared memory.  180 indices into 366 rows of 192 take
 // 7.1 us so, 12.4 in five launches; 2048 into 300 rows 10.4 and 13.3, but all of them
-// into one row, which is one block's, 21 and 13: half as many are even there.
+// into one row, which is one block's, 21 and 13: half as many are even there.  A block
+// takes 1 KB of a row's columns, so that wide rows are several blocks' whatever rows are
+// named: 1024 indices into one row of 2048 and 32768 FP32 take 19 and 32 us so, 108 and 1660
+// where a block takes all columns, 43 and 740 in five launches; into 300 rows, evenly, 9
+// and 38, so 9 and 60, so 13 and 64.
 //
 // Where the table has few rows, a block does the same with a tile of neighbouring
 // indices, whose gradients are one run of bytes (which L2 is asked for while the block
@@ -892,7 +896,7 @@ __global__ void __launch_bounds__(kSortThreads) sum_tile(const SumArgs args, con
         if (i < n) {
             const int32_t k = __ldg(idx + first + i);
             key[j] = static_cast<uint32_t>(k >= 0 && k < a.n_rows ? k : a.n_rows), at[j] = static_cast<uint32_t>(first + i);
-            if ((k < -1 || k >= a.n_rows) && (tiled || blockIdx.x == 0)) atomicOr(&g_embedding_error, 1u);
+            if ((k < -1 || k >= a.n_rows) && (tiled || blockIdx.x + blockIdx.y == 0)) atomicOr(&g_embedding_error, 1u);
         }
     }
     if (tiled) {
@@ -935,7 +939,7 @@ __global__ void __launch_bounds__(kSortThreads) sum_tile(const SumArgs args, con
         const int each = (count + slots - 1) / slots;
         const uint32_t ring = shared_address(tables) + thread * (kChunks ? 16 : 4);
         float *head = reinterpret_cast<float *>(tables + Ranker::kTableBytes), *tail = head + slots * wide;
-        for (int slice = 0; slice * wide < a.width; ++slice) {
+        for (int slice = blockIdx.y; slice * wide < a.width; slice += gridDim.y) {
             const RowPart<E, P, kChunks> part(thread - slot * a.cols, a.cols, slice, a.width);
             if (slot < slots)
                 sum_slots<E, P, kChunks, kSortThreads>(a, part, tokens + from, count, slot, each, ring, head, tail);
@@ -951,7 +955,8 @@ __global__ void __launch_bounds__(kSortThreads) sum_tile(const SumArgs args, con
 
     // the zeros: a bit for each of some rows, set where an index names it
     constexpr int64_t kBits = kBins * 32;
-    const int64_t row0 = static_cast<int64_t>(a.n_rows) * block / blocks, row1 = static_cast<int64_t>(a.n_rows) * (block + 1) / blocks;
+    const int shares = blocks * gridDim.y, share = block + blocks * blockIdx.y;
+    const int64_t row0 = static_cast<int64_t>(a.n_rows) * share / shares, row1 = static_cast<int64_t>(a.n_rows) * (share + 1) / shares;
     const int lane = thread & 31, warp = thread >> 5;
     int lanes = 1;      // of a row
     while (lanes < 32 && lanes < (kChunks ? a.width * kBytes<P> / 16 : a.width)) lanes *= 2;
@@ -1053,13 +1058,13 @@ wgs_status run_tile(const SumArgs &a, const int32_t *idx, const Plan &z, int sms
     }
     int64_t blocks = z.tile_blocks;
     if (z.few) {
-        // an index a slot, or 8 KB of zeros a block
-        const int64_t bytes = static_cast<int64_t>(a.n_rows) * a.width * kBytes<P>;
+        // an index a slot, or 8 KB of zeros a block, and an SM for each at most
+        const int64_t bytes = static_cast<int64_t>(a.n_rows) * a.width * kBytes<P>, most = sms < z.slices ? 1 : sms / z.slices;
         blocks = ceil_div(a.n, slots);
-        if (blocks < ceil_div(bytes, 8192)) blocks = ceil_div(bytes, 8192);
-        if (blocks > sms) blocks = sms;
+        if (blocks < ceil_div(bytes, 8192 * z.slices)) blocks = ceil_div(bytes, 8192 * z.slices);
+        if (blocks > most) blocks = most;
     }
-    return launch(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kSortThreads), static_cast<size_t>(smem), stream, a, idx,
+    return launch(kernel, dim3(static_cast<unsigned>(blocks), z.few ? z.slices : 1), dim3(kSortThreads), static_cast<size_t>(smem), stream, a, idx,
                   z.passes, z.bits, z.tile);
 }
 

@@ -25,6 +25,7 @@ constexpr int kMostPiece = 2048;       // indices of a block
 
 constexpr int kFew = 1024;             // indices that every block sorts
 static_assert(kFew <= kSortTile, "a tile of the sort");
+constexpr int kFewCols = 64;           // threads of a row there, 16 bytes each: a block's part of it
 constexpr int kTileBlocks = 152;       // of tiles: one an SM
 
 // -------------------------------------------------------------------- plan --
@@ -68,7 +69,7 @@ inline Plan plan_of(int64_t n, int64_t n_rows, int32_t width, int v) {
         z.tile = static_cast<int>(tile);
         z.tile_blocks = static_cast<int>(ceil_div(n, tile));
     }
-    z.slices = static_cast<int>(ceil_div(parts, z.few || z.tile ? kSortThreads : kSumThreads));
+    z.slices = static_cast<int>(ceil_div(parts, z.few ? kFewCols : z.tile ? kSortThreads : kSumThreads));
     z.cols = static_cast<int>(ceil_div(parts, z.slices));
     if (z.few || z.tile) {
         z.bytes = z.tile ? 4ll * z.tile_blocks * n_rows * width : n ? 16 : 0;
