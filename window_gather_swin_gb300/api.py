@@ -792,14 +792,15 @@ def embedding_bwd_workspace_bytes(n_idx: int, n_rows: int, width: int) -> int:
 
 
 def embedding_bwd(grad: torch.Tensor, idx: torch.Tensor, n_rows: int, scale: float = 1.0,
-                  dtype=torch.float32, grad_table: Optional[torch.Tensor] = None,
+                  dtype=None, grad_table: Optional[torch.Tensor] = None,
                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gradient of embedding's table, [n_rows, width], from that of its
     output, grad [*idx.shape, width]: scale times the sum of the rows that idx
     gives to each.  With scale 1 it is window_gather's too.  `dtype`, the
-    gradient's format, is float32 or grad's.  Sorting idx and the fixed-order
-    sums need a workspace of embedding_bwd_workspace_bytes(...) bytes; one is
-    allocated here unless the caller passes a uint8 CUDA tensor that large."""
+    gradient's format, is float32 or grad's; by default grad_table's, or
+    float32.  Sorting idx and the fixed-order sums need a workspace of
+    embedding_bwd_workspace_bytes(...) bytes; one is allocated here unless the
+    caller passes a uint8 CUDA tensor that large."""
     if not isinstance(grad, torch.Tensor) or not grad.is_cuda or not grad.is_contiguous():
         _cuda(grad, "grad")
     index, kind = grad.get_device(), grad.dtype
@@ -814,6 +815,8 @@ def embedding_bwd(grad: torch.Tensor, idx: torch.Tensor, n_rows: int, scale: flo
     n_rows = _int64(n_rows, "n_rows")
     if n_rows < 0:
         _fail("n_rows must not be negative")
+    if dtype is None:
+        dtype = torch.float32 if grad_table is None else grad_table.dtype
     if dtype not in (torch.float32, kind):
         _fail(f"dtype must be float32 or {kind} (got {dtype})")
     n = idx.numel()
