@@ -297,6 +297,15 @@ struct Place {
             }
         }
     }
+    // `value` in the places outside the row.
+    __device__ void fill_outside(float2 (&v)[kPairs], float value) const {
+#pragma unroll
+        for (int i = 0; i < kC * kV; ++i) {
+            const int col = column(i / kV) + i % kV;
+            if (col >= 0 && col < a.width) continue;
+            if (i & 1) v[i / 2].y = value; else v[i / 2].x = value;
+        }
+    }
     // Rounds each value once, to nearest even, into the present row.  A ragged row's
     // first and last chunk go to shared memory (`edges`: two chunks a row of a warp), from
     // where the row's lanes write an element each.

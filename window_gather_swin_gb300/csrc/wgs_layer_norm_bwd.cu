@@ -54,16 +54,21 @@ __global__ void __launch_bounds__(kThreads, 1) layer_norm_backward(const LayerNo
 
     for (; p.pass < p.passes; p.advance()) {
         const float2 later = stats(p.row + 2 * p.row_step);
-        const float2 less = both(-now.x), rstd = both(now.y);
+        const float2 rstd = both(now.y);
         p.arrived();
         float2 h[kPairs], g[kPairs];
         p.template load<true>(0, masks, h);
+        // Outside the row the distance is 0 too: 0 times h = -mean rstd would be no number where
+        // that passes FP32's range, as in rows of one large value.  (A select in ragged rows
+        // is a table's read an element; asked by each thread alone, [131040, 193] 53.6 us.)
+        if (!kWhole && __any_sync(0xffffffffu, isinf(now.x * now.y))) p.fill_outside(h, now.x);
         p.template load<true>(1, masks, g);
         float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             float2 w[kHalf], a1, a2;      // a chain of additions a chunk
             p.kept(weight, c, w);
+            const float2 less = both(kWhole && !p.held(c) ? 0.f : -now.x);
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) {
                 const int i = c * kHalf + j;
