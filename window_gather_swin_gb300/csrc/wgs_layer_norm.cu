@@ -24,15 +24,6 @@ namespace wgs {
 
 namespace {
 
-// Two blocks an SM, whose waits fall at different times, where two stages beside the
-// weights fit twice; of fewer warps where a thread's 32 columns need the registers.
-template <typename E, int kC>
-constexpr int kBlockWarps = kC * 16 / kBytes<E> > 24 ? 8 : kWarps;
-// (Six chunks a thread are for rows whose weights leave no room for a second block.)
-template <int kC>
-constexpr int kBlocksPerSm = kC == 6 ? 1 : 2;
-constexpr int kHalfOfSm = 112 << 10, kMostOfSm = 216 << 10;   // shared memory
-
 // 1 / sqrt(v): the hardware's approximation and one step of Newton's method, which
 // would make NaN of an infinite one.
 __device__ __forceinline__ float reciprocal_root(float v) {
@@ -44,7 +35,7 @@ __device__ __forceinline__ float reciprocal_root(float v) {
 // small whatever the mean's size, and their own mean, which m's rounding leaves,
 // comes off the variance and the result.
 template <typename E, int kC, int kTeam, bool kWhole>
-__global__ void __launch_bounds__(kBlockWarps<E, kC> * 32, kBlocksPerSm<kC>) layer_norm_forward(const LayerNormArgs a) {
+__global__ void __launch_bounds__(forward_warps(kC, kBytes<E>) * 32, forward_blocks_per_sm(kC)) layer_norm_forward(const LayerNormArgs a) {
     extern __shared__ __align__(16) char shared[];
     __shared__ __align__(16) float2 exchange[2][kMeet];
     __shared__ __align__(16) char edge_bytes[kWhole ? 16 : kEdgeBytes];
@@ -142,54 +133,37 @@ wgs_status run_unit(LayerNormArgs a, cudaStream_t stream) {
     DeviceInfo dev;
     const wgs_status st = current_device(&dev);
     if (st != WGS_OK) return st;
-    using P = Place<E, kC, kTeam, kWhole>;
-    a.team_warps = kTeam == 0 ? static_cast<int>(ceil_div(a.chunks, 32 * kC)) : 1;
-    a.kept_bytes = kC * (kTeam == 0 ? 32 * a.team_warps : kTeam) * 8 * P::kV;     // weight and bias
-    constexpr int kMost = kBlockWarps<E, kC>;
-    const int most = kMost / a.team_warps * a.team_warps * a.tensors * kC * 512;
-    const bool two = kBlocksPerSm<kC> == 2 && a.kept_bytes + 2 * most <= kHalfOfSm;
-    const Cut cut = cut_rows(a, P::kRowsPerPass, kMost, (two ? 2 : 1) * dev.sm_count);
-    const int stage = cut.threads * a.tensors * kC * 16, fit = ((two ? kHalfOfSm : kMostOfSm) - a.kept_bytes) / stage;
-    a.stages = fit < kMaxStages ? fit : kMaxStages;
-    const int smem = a.kept_bytes + a.stages * stage;
+    const ForwardCut f = forward_cut({kC, kTeam}, a.chunks, a.tensors, kBytes<E>, kWhole, a.rows, a.period, dev.sm_count);
+    a.team_warps = f.team_warps, a.kept_bytes = f.kept_bytes, a.stages = f.stages;
     auto kernel = layer_norm_forward<E, kC, kTeam, kWhole>;
     // Above 48 KB, its static memory included, a kernel needs the runtime's leave,
     // which belongs to the context; asking for the same amount on every call needs
     // no record of it.  (At most 67 KB beside a stage, and 72 KB of that.)
-    if (smem > 40 << 10 &&
+    if (f.smem > 40 << 10 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostOfSm) != cudaSuccess) {
         cudaGetLastError();
         return WGS_ERR_LAUNCH;
     }
-    return launch(kernel, dim3(cut.blocks), dim3(cut.threads), static_cast<size_t>(smem), stream, a);
+    return launch(kernel, dim3(f.cut.blocks), dim3(f.cut.threads), static_cast<size_t>(f.smem), stream, a);
 }
 
-// The narrowest unit that holds a row in three chunks a thread, and the fewest chunks
-// that do; four for a whole warp: rows just above its 96 chunks would take a second one
-// ([32761, 771] bf16 with residual 45 us, with two warps of two chunks 56).  Four lanes
-// for the narrowest ([600000, 24] bf16 15 us, with eight 28).
 template <typename E, bool kWhole>
 wgs_status run_width(const LayerNormArgs &a, cudaStream_t stream) {
-    const int n = a.chunks;
-    if (n <= 4) return run_unit<E, 1, 4, kWhole>(a, stream);
-    if (n <= 8) return run_unit<E, 1, 8, kWhole>(a, stream);
-    if (n <= 16) return run_unit<E, 2, 8, kWhole>(a, stream);
-    if (n <= 24) return run_unit<E, 3, 8, kWhole>(a, stream);
-    if (n <= 32) return run_unit<E, 2, 16, kWhole>(a, stream);
-    if (n <= 48) return run_unit<E, 3, 16, kWhole>(a, stream);
-    if (n <= 64) return run_unit<E, 2, 32, kWhole>(a, stream);
-    if (n <= 96) return run_unit<E, 3, 32, kWhole>(a, stream);
-    if (n <= 128) return run_unit<E, 4, 32, kWhole>(a, stream);
-    const int each = chunks_of_units(n, std::is_same<E, F32>::value && n > 96 * kWarps);
-    // Four where that takes fewer than three quarters of the warps ([32768, 4096] bf16 90
-    // us, with three chunks 104; [16384, 8192] 103, so 116; but [29127, 4608] 126, so 96),
-    // and not for ragged rows ([32760, 4097] 206, so 143), whose ends want more warps.
+    const Unit u = forward_unit(a.chunks, kBytes<E>, kWhole);
+    if (u.team == 4) return run_unit<E, 1, 4, kWhole>(a, stream);
+    if (u.team == 8 && u.each == 1) return run_unit<E, 1, 8, kWhole>(a, stream);
+    if (u.team == 8 && u.each == 2) return run_unit<E, 2, 8, kWhole>(a, stream);
+    if (u.team == 8) return run_unit<E, 3, 8, kWhole>(a, stream);
+    if (u.team == 16 && u.each == 2) return run_unit<E, 2, 16, kWhole>(a, stream);
+    if (u.team == 16) return run_unit<E, 3, 16, kWhole>(a, stream);
+    if (u.team == 32 && u.each == 2) return run_unit<E, 2, 32, kWhole>(a, stream);
+    if (u.team == 32 && u.each == 3) return run_unit<E, 3, 32, kWhole>(a, stream);
+    if (u.team == 32) return run_unit<E, 4, 32, kWhole>(a, stream);
     if constexpr (kWhole && !std::is_same<E, F32>::value) {
-        const int warps = static_cast<int>(ceil_div(n, 32 * each)), fewer = static_cast<int>(ceil_div(n, 128));
-        if (fewer <= kBlockWarps<E, 4> && 4 * fewer < 3 * warps) return run_unit<E, 4, 0, kWhole>(a, stream);
+        if (u.each == 4) return run_unit<E, 4, 0, kWhole>(a, stream);
     }
-    if (each == 2) return run_unit<E, 2, 0, kWhole>(a, stream);
-    if (each == 3) return run_unit<E, 3, 0, kWhole>(a, stream);
+    if (u.each == 2) return run_unit<E, 2, 0, kWhole>(a, stream);
+    if (u.each == 3) return run_unit<E, 3, 0, kWhole>(a, stream);
     if constexpr (std::is_same<E, F32>::value) return run_unit<E, 6, 0, kWhole>(a, stream);
     return WGS_ERR_WIDTH;
 }

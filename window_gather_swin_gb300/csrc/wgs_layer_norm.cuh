@@ -20,6 +20,7 @@
 #include <type_traits>
 
 #include "wgs_common.cuh"
+#include "wgs_layer_norm_plan.h"
 
 namespace wgs {
 
@@ -27,12 +28,7 @@ namespace {
 
 struct F32 {};
 
-constexpr int kMaxWidth = 8192;
-constexpr int kWarps = 12;          // of a block, at most
-constexpr int kThreads = kWarps * 32;
-constexpr int kMeet = kWarps / 3 * 4;   // places of their sums: units of three warps have four each
-constexpr int kMaxStages = 4;
-constexpr int kEdgeBytes = kWarps * 8 * 32;   // of ragged rows' ends
+static_assert(kExchangeBytes == 2 * kMeet * sizeof(float2), "two places of the units' sums");
 
 struct LayerNormArgs {
     const char *in[3];   // forward: x, branch; backward: x, grad_y, grad_residual
@@ -414,8 +410,7 @@ struct Place {
     }
     // What of a chunk that is not full is the row's: of the first one, the last one and one
     // behind the row, as bits and as a factor for every element.
-    static constexpr int kEdgeKinds = 3;
-    static constexpr int kKeptEdges = kEdgeKinds * (16 + kV * 4);     // bytes
+    static constexpr int kKeptEdges = kept_edges(kBytes<E>);
     __device__ int kind(int c) const { return column(c) < 0 ? 0 : held(c) ? 1 : 2; }
     __device__ void keep_edges(char *to) const {
         const int i = threadIdx.x;
@@ -479,37 +474,6 @@ bool place_rows(LayerNormArgs *a) {
     a->closing = a->rows - ceil_div(kV - 1, a->width);
     a->inv = 1.0f / static_cast<float>(a->width);
     return whole;
-}
-
-// A call's blocks and units: as many units a block as its warps hold, or so few
-// that every SM gets some where the rows are few, and at least a block for each
-// class of rows.
-struct Cut {
-    int blocks, units, threads;
-};
-
-inline Cut cut_rows(const LayerNormArgs &a, int rows_per_pass, int most_warps, int most_blocks) {
-    const int64_t passes = ceil_div(a.rows, rows_per_pass);
-    int64_t units = most_warps / a.team_warps;
-    if (units > ceil_div(passes, most_blocks)) units = ceil_div(passes, most_blocks);
-    int64_t blocks = ceil_div(passes, units);
-    if (blocks > most_blocks) blocks = most_blocks;
-    const int64_t kinds = a.rows < a.period ? a.rows : a.period;
-    if (blocks < kinds) blocks = kinds;
-    return {static_cast<int>(blocks), static_cast<int>(units), static_cast<int>(units) * a.team_warps * 32};
-}
-
-// Chunks a thread for units of several warps: those that leave the fewest of a block's
-// threads without a part of a row.
-inline int chunks_of_units(int chunks, bool six) {
-    int best = 0, best_score = 0;
-    for (int c : {3, 2, 6}) {
-        const int warps = static_cast<int>(ceil_div(chunks, 32 * c));
-        if ((c == 6 && !six) || warps < 2 || warps > kWarps) continue;
-        const int score = chunks * 1000 / (warps * 32 * c) * (kWarps / warps * warps) / kWarps;
-        if (score > best_score) best = c, best_score = score;
-    }
-    return best;
 }
 
 // No output may share a byte with another or with an input, but for those that may

@@ -170,7 +170,7 @@ wgs_status run_unit(LayerNormArgs a, cudaStream_t stream, int *blocks) {
     if (st != WGS_OK) return st;
     using P = Place<E, kC, kTeam, kWhole>;
     a.team_warps = kTeam == 0 ? static_cast<int>(ceil_div(a.chunks, 32 * kC)) : 1;
-    const Cut cut = cut_rows(a, P::kRowsPerPass, kWarps, dev.sm_count < kMostBlocks ? dev.sm_count : kMostBlocks);
+    const Cut cut = cut_rows(a.rows, a.period, a.team_warps, P::kRowsPerPass, kWarps, dev.sm_count < kMostBlocks ? dev.sm_count : kMostBlocks);
     *blocks = cut.blocks;
     const int stage = cut.threads * a.tensors * kC * 16;
     a.stages = kRing / stage < 1 ? 1 : kRing / stage < kMaxStages ? kRing / stage : kMaxStages;
