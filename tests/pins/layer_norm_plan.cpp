@@ -2,7 +2,8 @@
 //
 // Where a call is cut for two blocks an SM, both fit there: their shared memory, static
 // and dynamic, and what the device keeps for each.  All of a row's chunks belong to a
-// thread, and every class of rows to a block.
+// thread, and every class of rows to a block.  Each kernel that is compiled for units of
+// several warps is some width's.
 #include <cstdio>
 #include <initializer_list>
 
@@ -12,6 +13,7 @@ using namespace wgs;
 
 int main() {
     long long cuts = 0;
+    bool seen[2][2][8] = {};        // [bytes][whole][chunks a thread]
     for (int bytes : {4, 2})
         for (int place = 0; place < 3; ++place)         // whole chunks; ragged, alike; ragged, apart
             for (int width = 1; width <= kMaxWidth; ++width) {
@@ -22,6 +24,7 @@ int main() {
                 while (place == 1 && period < v && width * period % v) period *= 2;
                 const int chunks = static_cast<int>(ceil_div(width + (place == 1 ? v - 1 : 0), v));
                 const Unit u = forward_unit(chunks, bytes, whole);
+                if (u.team == 0) seen[bytes == 4][whole][u.each] = true;
                 for (int tensors : {1, 2})
                     for (int sms : {152, 20})
                         for (int64_t rows : {1, 7, 300, 5000, 131040}) {
@@ -42,6 +45,13 @@ int main() {
                             ++cuts;
                         }
             }
+    for (int bytes : {4, 2})
+        for (bool whole : {false, true})
+            for (int each = 0; each < 8; ++each)
+                if (forward_has_warps(each, bytes, whole) != seen[bytes == 4][whole][each])
+                    return std::printf("%d chunks a thread of %d bytes, whole %d: compiled %d, called %d\n", each, bytes,
+                                       whole, forward_has_warps(each, bytes, whole), seen[bytes == 4][whole][each]),
+                           1;
     std::printf("cuts %lld\n", cuts);
     return 0;
 }

@@ -147,6 +147,12 @@ wgs_status run_unit(LayerNormArgs a, cudaStream_t stream) {
     return launch(kernel, dim3(f.cut.blocks), dim3(f.cut.threads), static_cast<size_t>(f.smem), stream, a);
 }
 
+template <typename E, int kC, bool kWhole>
+wgs_status run_warps(const LayerNormArgs &a, cudaStream_t stream) {
+    if constexpr (forward_has_warps(kC, kBytes<E>, kWhole)) return run_unit<E, kC, 0, kWhole>(a, stream);
+    return WGS_ERR_WIDTH;
+}
+
 template <typename E, bool kWhole>
 wgs_status run_width(const LayerNormArgs &a, cudaStream_t stream) {
     const Unit u = forward_unit(a.chunks, kBytes<E>, kWhole);
@@ -159,13 +165,10 @@ wgs_status run_width(const LayerNormArgs &a, cudaStream_t stream) {
     if (u.team == 32 && u.each == 2) return run_unit<E, 2, 32, kWhole>(a, stream);
     if (u.team == 32 && u.each == 3) return run_unit<E, 3, 32, kWhole>(a, stream);
     if (u.team == 32) return run_unit<E, 4, 32, kWhole>(a, stream);
-    if constexpr (kWhole && !std::is_same<E, F32>::value) {
-        if (u.each == 4) return run_unit<E, 4, 0, kWhole>(a, stream);
-    }
-    if (u.each == 2) return run_unit<E, 2, 0, kWhole>(a, stream);
-    if (u.each == 3) return run_unit<E, 3, 0, kWhole>(a, stream);
-    if constexpr (std::is_same<E, F32>::value) return run_unit<E, 6, 0, kWhole>(a, stream);
-    return WGS_ERR_WIDTH;
+    if (u.each == 2) return run_warps<E, 2, kWhole>(a, stream);
+    if (u.each == 3) return run_warps<E, 3, kWhole>(a, stream);
+    if (u.each == 4) return run_warps<E, 4, kWhole>(a, stream);
+    return run_warps<E, 6, kWhole>(a, stream);
 }
 
 template <typename E>

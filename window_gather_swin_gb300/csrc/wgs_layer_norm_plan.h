@@ -74,6 +74,13 @@ inline Unit forward_unit(int chunks, int value_bytes, bool whole) {
     return {each, 0};
 }
 
+// Units of several warps that forward_unit names: where it has four chunks a thread for
+// whole rows of 16 bits, it never has two.
+constexpr bool forward_has_warps(int each, int value_bytes, bool whole) {
+    if (value_bytes == 4) return each == 2 || each == 3 || each == 6;
+    return each == 3 || each == (whole ? 4 : 2);
+}
+
 // --------------------------------------------------------------- rows, memory --
 
 // A call's blocks and units: as many units a block as its warps hold, or so few
