@@ -605,9 +605,12 @@ wgs_status embedding(const void *table, const int32_t *idx, void *out, int64_t n
  * summed in FP32 over the indices sorted by row, positions in order, cut into pieces
  * of equal size: an order that depends on idx, the sizes and the format alone.
  * With scale 1 it is also the gradient of window_gather through a map that may
- * name a row more than once.  An index of -1 adds to no row, one outside [-1,
+ * name a row more than once.  scale is finite (else rows that no index names may be
+ * no numbers).  An index of -1 adds to no row, one outside [-1,
  * n_rows) to none and sets the device error word.
- *   grad        [n_idx, width] of dtype (any wgs_dtype).
+ *   grad        [n_idx, width] of dtype (any wgs_dtype).  Where 16-bit rows are no
+ *               whole 16-byte chunks they are read by words of 4 bytes, and so the 2
+ *               bytes before the first row where it does not begin on 4.
  *   grad_table  [n_rows, width] of table_dtype (WGS_F32, or `dtype`); every
  *               row is written, zeros where no index names it (all of them with
  *               n_idx == 0).

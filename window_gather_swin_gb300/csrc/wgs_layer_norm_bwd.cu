@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(kThreads, 1) layer_norm_backward(const LayerNo
 
 // grad_weight (blockIdx.y 0) and grad_bias (1): the blocks' sums, eight columns a
 // block, 16 threads a column.  So few threads find room beside the first launch's
-// blocks and are there when those end.
+// blocks of up to 160 registers a thread and are there when those end; beside the others
+// (some of three chunks a thread, those of six) they start behind them.
 constexpr int kParamCols = 8, kParamGroups = 16;
 
 template <typename E>
