@@ -270,19 +270,21 @@ struct Place {
         else if (a.stages == 2) cp_async_wait<1>();
         else cp_async_wait<0>();
     }
-    // The thread's part of the present row of tensor k, widened; zeros outside the row:
+    // The thread's part of the present row of tensor k, widened; outside the row zeros, or
+    // the bits `fill`:
     // `masks` are keep_edges', looked up by the chunks that are not full, or with kAll
     // keep_masks', for all chunks alike.  (The backward has no registers for the former:
     // [5000, 8191] bf16 85 us, so 78; the forward no shared memory to spare for the latter:
     // 51, so 87.)
     template <bool kAll>
-    __device__ void load(int k, uint32_t masks, float2 (&v)[kPairs]) const {
+    __device__ void load(int k, uint32_t masks, float2 (&v)[kPairs], uint32_t fill = 0u) const {
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             uint4 q = load_shared(slots + present + (k * kC + c) * 512);
             if (!kWhole && (kAll || !full(c))) {
                 const uint4 m = load_shared(masks + (kAll ? chunk(c) : kind(c)) * 16);
-                q.x &= m.x, q.y &= m.y, q.z &= m.z, q.w &= m.w;
+                q.x = (q.x & m.x) | (fill & ~m.x), q.y = (q.y & m.y) | (fill & ~m.y);
+                q.z = (q.z & m.z) | (fill & ~m.z), q.w = (q.w & m.w) | (fill & ~m.w);
             }
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) {
@@ -293,14 +295,12 @@ struct Place {
             }
         }
     }
-    // `value` in the places outside the row.
-    __device__ void fill_outside(float2 (&v)[kPairs], float value) const {
-#pragma unroll
-        for (int i = 0; i < kC * kV; ++i) {
-            const int col = column(i / kV) + i % kV;
-            if (col >= 0 && col < a.width) continue;
-            if (i & 1) v[i / 2].y = value; else v[i / 2].x = value;
-        }
+    // A word of load()'s that holds `value` in every place, rounded to the tensors' format.
+    __device__ static uint32_t filled(float value) {
+        if constexpr (kV == 4)
+            return __float_as_uint(value);
+        else
+            return E::from_f2(value, value);
     }
     // Rounds each value once, to nearest even, into the present row.  A ragged row's
     // first and last chunk go to shared memory (`edges`: two chunks a row of a warp), from

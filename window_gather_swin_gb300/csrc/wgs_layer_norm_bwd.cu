@@ -57,11 +57,11 @@ __global__ void __launch_bounds__(kThreads, 1) layer_norm_backward(const LayerNo
         const float2 rstd = both(now.y);
         p.arrived();
         float2 h[kPairs], g[kPairs];
-        p.template load<true>(0, masks, h);
-        // Outside the row the distance is 0 too: 0 times h = -mean rstd would be no number where
-        // that passes FP32's range, as in rows of one large value.  (A select in ragged rows
-        // is a table's read an element; asked by each thread alone, [131040, 193] 53.6 us.)
-        if (!kWhole && __any_sync(0xffffffffu, isinf(now.x * now.y))) p.fill_outside(h, now.x);
+        // Outside the row h is not -mean rstd, which may pass FP32's range, and then 0 h is no
+        // number, as in rows of one large value.  In ragged rows the mean stands there, as near
+        // as the format holds it: that is the value itself in rows of one value, and in all others
+        // mean rstd is no more than 2^24 sqrt(2 width).
+        p.template load<true>(0, masks, h, P::filled(now.x));
         p.template load<true>(1, masks, g);
         float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
