@@ -13,8 +13,9 @@
 // (75 %), FP32 49.6 (90 %); [32760, 1536] bf16 with the residual stream's gradient 66
 // (90 %); [32761, 771] bf16 55 (40 %).  A thread's 24 columns take 48 registers of sums
 // beside 48 of values, so twelve warps an SM: they issue in half of their cycles and
-// wait for their own results (shuffles, shared memory) in most others.  The second
-// launch shows 2 to 3 us at the end of a call.
+// wait for their own results (shuffles, shared memory) in most others.  Units of fewer
+// columns a thread need fewer registers and have the same twelve warps.  The second launch
+// shows 2 to 3 us at the end of a call.
 #include "wgs_layer_norm.cuh"
 
 namespace wgs {
